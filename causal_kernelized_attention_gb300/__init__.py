@@ -14,7 +14,10 @@ Tensors are PyTorch CUDA tensors (PyTorch supplies device memory and streams):
   gated forms: alpha fp32 shaped like k, one gate per (token, key feature);
   *_ex forms: feature_map "elu1" | "relu" (max(x, 0) + shift) | "identity" (x + shift),
   normalize True | False, and an optional gamma;
-  FAVOR+ forms: projections w [m, d] of the inputs' dtype, features [B, H, N, m].
+  FAVOR+ forms: projections w [m, d] of the inputs' dtype, features [B, H, N, m];
+  hybrid layers: rotary positions (int32 [B, N] or an offset), the gated recurrence
+  x [B, N, D] with gates alpha fp32, and softmax attention over a sliding window with
+  sinks (q [B, Hq, N, d], k, v [B, Hk, N, d]; ring caches [B, Hk, sinks + window, d]).
 """
 from __future__ import annotations
 
@@ -25,6 +28,8 @@ from ._binding import (LA_BF16, LA_F32, LA_PHI_ELU1, LA_PHI_IDENTITY, LA_PHI_REL
                        la_prefill_state_ex, la_forward_noncausal_noalloc, la_get_device_status, la_kernel_launches, la_last_cuda_error,
                        la_prefill_state, la_prefill_state_decay, la_status_string, la_version, load_library,
                        la_forward_causal_gated, la_prefill_state_gated, la_decode_step_gated)
+from ._hybrid import (la_recurrence_backward, la_recurrence_forward, la_recurrence_step, la_rotary_backward,
+                      la_rotary_forward, la_window_backward, la_window_cache, la_window_decode_step, la_window_forward)
 
 __all__ = [
     "LA_BF16", "LA_F32", "LA_PHI_ELU1", "LA_PHI_IDENTITY", "LA_PHI_RELU", "LAError", "Variant", "lib_path",
@@ -34,5 +39,7 @@ __all__ = [
     "la_forward_causal_ex", "la_forward_noncausal_ex", "la_prefill_state_ex",
     "la_forward_noncausal", "la_forward_noncausal_noalloc", "la_get_device_status", "la_kernel_launches", "la_last_cuda_error", "la_prefill_state",
     "la_prefill_state_decay", "la_forward_causal_gated", "la_prefill_state_gated", "la_decode_step_gated",
+    "la_rotary_forward", "la_rotary_backward", "la_recurrence_forward", "la_recurrence_backward", "la_recurrence_step",
+    "la_window_forward", "la_window_backward", "la_window_cache", "la_window_decode_step",
     "la_status_string", "la_version", "load_library",
 ]

@@ -33,6 +33,13 @@ class Variant(ctypes.Structure):
     _fields_ = [("feature_map", ctypes.c_int), ("shift", ctypes.c_float), ("normalize", ctypes.c_int)]
 
 
+class RotarySpec(ctypes.Structure):
+    """la_rotary_spec: which features of a head turn, in which pairs, at which frequencies."""
+    _fields_ = [("rot", ctypes.c_int), ("layout", ctypes.c_int), ("scaling", ctypes.c_int), ("original", ctypes.c_int),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double), ("ramp_lo", ctypes.c_double),
+                ("ramp_hi", ctypes.c_double), ("amplitude", ctypes.c_float)]
+
+
 LA_PHI_ELU1, LA_PHI_RELU, LA_PHI_IDENTITY = 0, 1, 2
 _FMAPS = {"elu1": LA_PHI_ELU1, "relu": LA_PHI_RELU, "identity": LA_PHI_IDENTITY}
 
@@ -75,6 +82,7 @@ def _declare(lib):
         "la_decode_step_gated": [P, P, P, P, P, P, P, I, I, I, I, F, I, P],
         "la_get_device_status": [P],
     }
+    sigs.update(_hybrid_signatures(P, I, F))
     for name, args in sigs.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -92,6 +100,22 @@ def _declare(lib):
     lib.la_test_drop_publication.argtypes = [ctypes.c_longlong]
     lib.la_test_drop_publication.restype = None
     return lib
+
+
+def _hybrid_signatures(P, I, F):
+    L = ctypes.c_longlong
+    S = ctypes.POINTER(RotarySpec)
+    return {
+        "la_rotary_forward": [P, P, P, P, P, L, S, I, I, I, I, I, I, P],
+        "la_rotary_backward": [P, P, P, P, P, L, S, I, I, I, I, I, I, P],
+        "la_recurrence_forward": [P, P, P, P, P, I, I, I, I, P],
+        "la_recurrence_backward": [P, P, P, P, P, P, P, P, I, I, I, I, P],
+        "la_recurrence_step": [P, P, P, P, I, I, I, P],
+        "la_window_forward": [P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, P],
+        "la_window_backward": [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, P],
+        "la_window_cache": [P, P, P, P, P, I, I, I, I, I, I, I, P],
+        "la_window_decode_step": [P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, P],
+    }
 
 
 def load_library(path: str = None):

@@ -1,0 +1,264 @@
+"""Hybrid-layer operators: rotary positions, the gated recurrence, window attention with sinks.
+
+Marshalling only, as in ``_binding``: each function checks shapes and types, allocates the
+outputs that were not given and calls the C entry point of the same name on the tensors'
+device (on ``stream``, or that device's current stream).
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+
+from ._binding import RotarySpec, _check, _dtype_code, _need_cuda, _same_dtype, load_library
+
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "ramp": 3}
+
+
+def _place(*ts):
+    """Checks that the tensors given are contiguous and on one CUDA device; returns it."""
+    ts = [t for t in ts if t is not None]
+    _need_cuda(*ts)
+    dev = ts[0].device
+    for t in ts[1:]:
+        if t.device != dev:
+            raise ValueError("tensors must be on one device")
+    return dev
+
+
+def _call(name, dev, stream, *args):
+    """The C entry point with its device current, on `stream` or the device's current stream."""
+    import torch
+    fn = getattr(load_library(), name)
+    with contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev):
+        s = torch.cuda.current_stream(dev) if stream is None else stream
+        if s.device != dev:
+            raise ValueError("stream must be on the tensors' device")
+        _check(name, fn(*args, ctypes.c_void_p(s.cuda_stream)))
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _shaped(what, t, shape, dtype=None):
+    if t is not None and (tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype)):
+        raise ValueError("%s must be %s%s" % (what, "" if dtype is None else "%s " % dtype, list(shape)))
+
+
+# ---------------------------------------------------------------- rotary positions
+def _rotary(name, q, k, oq, ok, positions, offset, rot, layout, base, scaling, factor, original, ramp, amplitude, stream):
+    import torch
+    if q.dim() not in (3, 4) or (k is not None and k.dim() != q.dim()):
+        raise ValueError("q and k must be [B, H, N, d], or [B, H, d] for one token")
+    if k is None and ok is not None:
+        raise ValueError("an output for k without k")
+    oq = torch.empty_like(q) if oq is None else oq
+    ok = torch.empty_like(k) if ok is None and k is not None else ok
+    dev = _place(q, k, oq, ok, positions)
+    _same_dtype(*[t for t in (q, k, oq, ok) if t is not None])
+    B, Hq, N, d = q.shape if q.dim() == 4 else (q.shape[0], q.shape[1], 1, q.shape[2])
+    Hk = 0 if k is None else k.shape[1]
+    _shaped("k", k, (B, Hk) + tuple(q.shape[2:]))
+    _shaped("the output for q", oq, q.shape)
+    _shaped("the output for k", ok, () if k is None else k.shape)
+    if positions is not None and (positions.dtype != torch.int32 or tuple(positions.shape) != (B, N)
+                                  and not (q.dim() == 3 and tuple(positions.shape) == (B,))):
+        raise ValueError("positions must be int32 [B, N]")
+    if layout not in _LAYOUTS or scaling not in _SCALINGS:
+        raise ValueError("layout is one of %s, scaling one of %s" % (sorted(_LAYOUTS), sorted(_SCALINGS)))
+    spec = RotarySpec(d if rot is None else int(rot), _LAYOUTS[layout], _SCALINGS[scaling], int(original), float(base),
+                      float(factor), float(ramp[0]), float(ramp[1]), float(amplitude))
+    _call(name, dev, stream, q.data_ptr(), _ptr(k), oq.data_ptr(), _ptr(ok), _ptr(positions), int(offset),
+          ctypes.byref(spec), B, Hq, Hk, N, d, _dtype_code(q))
+    return oq if k is None else (oq, ok)
+
+
+def la_rotary_forward(q, k=None, oq=None, ok=None, positions=None, offset: int = 0, rot: int = None, layout="half",
+                      base: float = 10000.0, scaling="none", factor: float = 1.0, original: int = 0,
+                      ramp=(1.0, 32.0), amplitude: float = 1.0, stream=None):
+    """Turns q [B,Hq,N,d] and k [B,Hk,N,d] (or [B,H,d], one token) by their positions: int32 [B,N],
+    or offset + n.  The first `rot` features (all by default) turn in pairs, layout "half" or
+    "interleaved", at base^(-2i/rot), scaled "none", "linear", "ntk" or "ramp" by `factor`
+    (ramp: by parts between `ramp` turns over `original` tokens).  oq = q and ok = k turn in
+    place.  Returns (oq, ok), or oq when k is None."""
+    return _rotary("la_rotary_forward", q, k, oq, ok, positions, offset, rot, layout, base, scaling, factor, original,
+                   ramp, amplitude, stream)
+
+
+def la_rotary_backward(doq, dok=None, dq=None, dk=None, positions=None, offset: int = 0, rot: int = None, layout="half",
+                       base: float = 10000.0, scaling="none", factor: float = 1.0, original: int = 0,
+                       ramp=(1.0, 32.0), amplitude: float = 1.0, stream=None):
+    """Gradients (dq, dk) of la_rotary_forward from its outputs' (same options)."""
+    return _rotary("la_rotary_backward", doq, dok, dq, dk, positions, offset, rot, layout, base, scaling, factor,
+                   original, ramp, amplitude, stream)
+
+
+# ---------------------------------------------------------------- gated recurrence
+def _gates(alpha, shape):
+    import torch
+    if alpha.dtype != torch.float32 or tuple(alpha.shape) != tuple(shape):
+        raise ValueError("alpha must be float32 %s" % list(shape))
+
+
+def la_recurrence_forward(x, alpha, h0=None, h=None, hN=None, stream=None):
+    """h_t = alpha_t h_{t-1} + x_t per channel; x [B,N,D], alpha fp32 [B,N,D], h0 fp32 [B,D] (None: zeros).
+    Returns (h in the dtype of x, the last state hN fp32 [B,D])."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x must be [B, N, D]")
+    B, N, D = x.shape
+    h = torch.empty_like(x) if h is None else h
+    hN = torch.empty((B, D), dtype=torch.float32, device=x.device) if hN is None else hN
+    dev = _place(x, alpha, h0, h, hN)
+    _same_dtype(x, h)
+    _gates(alpha, x.shape)
+    _shaped("h", h, x.shape)
+    _shaped("h0", h0, (B, D), torch.float32)
+    _shaped("hN", hN, (B, D), torch.float32)
+    _call("la_recurrence_forward", dev, stream, x.data_ptr(), alpha.data_ptr(), _ptr(h0), h.data_ptr(), hN.data_ptr(),
+          B, N, D, _dtype_code(x))
+    return h, hN
+
+
+def la_recurrence_backward(alpha, h, dh, h0=None, dhN=None, dx=None, dalpha=None, dh0=None, stream=None):
+    """Gradients of la_recurrence_forward from its output h, dh and dhN (None: zeros).  Returns
+    (dx, dalpha fp32, dh0 fp32 -- None when neither h0 nor dh0 was given)."""
+    import torch
+    if h.dim() != 3:
+        raise ValueError("h must be [B, N, D]")
+    B, N, D = h.shape
+    dx = torch.empty_like(h) if dx is None else dx
+    dalpha = torch.empty_like(alpha) if dalpha is None else dalpha
+    if dh0 is None and h0 is not None:
+        dh0 = torch.empty_like(h0)
+    dev = _place(alpha, h, dh, h0, dhN, dx, dalpha, dh0)
+    _same_dtype(h, dh, dx)
+    _gates(alpha, h.shape)
+    _shaped("dh", dh, h.shape)
+    _shaped("dx", dx, h.shape)
+    _shaped("dalpha", dalpha, h.shape, torch.float32)
+    for what, t in (("h0", h0), ("dhN", dhN), ("dh0", dh0)):
+        _shaped(what, t, (B, D), torch.float32)
+    _call("la_recurrence_backward", dev, stream, alpha.data_ptr(), h.data_ptr(), dh.data_ptr(), _ptr(h0), _ptr(dhN),
+          dx.data_ptr(), dalpha.data_ptr(), _ptr(dh0), B, N, D, _dtype_code(h))
+    return dx, dalpha, dh0
+
+
+def la_recurrence_step(state, x, alpha, h=None, stream=None):
+    """One token of la_recurrence_forward: state fp32 [B,D] in place, x, alpha [B,D]; returns h [B,D]."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [B, D]")
+    h = torch.empty_like(x) if h is None else h
+    dev = _place(state, x, alpha, h)
+    _same_dtype(x, h)
+    _gates(alpha, x.shape)
+    _shaped("state", state, x.shape, torch.float32)
+    _shaped("h", h, x.shape)
+    _call("la_recurrence_step", dev, stream, state.data_ptr(), x.data_ptr(), alpha.data_ptr(), h.data_ptr(),
+          x.shape[0], x.shape[1], _dtype_code(x))
+    return h
+
+
+# ---------------------------------------------------------------- window attention
+def _window_shapes(q, k, v, lens):
+    import torch
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, Hq, Nq, d], k and v [B, Hk, Nk, d]")
+    B, Hq, Nq, d = q.shape
+    Hk, Nk = k.shape[1], k.shape[2]
+    _shaped("k", k, (B, Hk, Nk, d))
+    _shaped("v", v, k.shape)
+    _shaped("lens", lens, (B,), torch.int32)
+    return B, Hq, Hk, Nq, Nk, d
+
+
+def _scale(scale, d):
+    return 1.0 / math.sqrt(max(d, 1)) if scale is None else float(scale)
+
+
+def la_window_forward(q, k, v, window: int, sinks: int = 0, lens=None, scale: float = None, o=None, lse=None,
+                      stream=None):
+    """Causal softmax attention over the last `window` keys and the first `sinks`; q [B,Hq,Nq,d] (the
+    last Nq tokens), k, v [B,Hk,Nk,d], lens int32 [B] valid tokens per entry (None: all), scale
+    1/sqrt(d) by default.  Returns (o, lse fp32 [B,Hq,Nq]); padding rows give 0 and -inf."""
+    import torch
+    B, Hq, Hk, Nq, Nk, d = _window_shapes(q, k, v, lens)
+    o = torch.empty_like(q) if o is None else o
+    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
+    dev = _place(q, k, v, lens, o, lse)
+    _same_dtype(q, k, v, o)
+    _shaped("o", o, q.shape)
+    _shaped("lse", lse, (B, Hq, Nq), torch.float32)
+    _call("la_window_forward", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+          _ptr(lens), B, Hq, Hk, Nq, Nk, d, int(window), int(sinks), _scale(scale, d), _dtype_code(q))
+    return o, lse
+
+
+def la_window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0, lens=None, scale: float = None, dq=None,
+                       dk=None, dv=None, stream=None):
+    """Gradients (dq, dk, dv) of sum(dout * o) for la_window_forward, from its o and lse."""
+    import torch
+    B, Hq, Hk, Nq, Nk, d = _window_shapes(q, k, v, lens)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    dev = _place(q, k, v, o, lse, dout, lens, dq, dk, dv)
+    _same_dtype(q, k, v, o, dout, dq, dk, dv)
+    for what, t, like in (("o", o, q), ("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _shaped(what, t, like.shape)
+    _shaped("lse", lse, (B, Hq, Nq), torch.float32)
+    _call("la_window_backward", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+          dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(lens), B, Hq, Hk, Nq, Nk, d, int(window),
+          int(sinks), _scale(scale, d), _dtype_code(q))
+    return dq, dk, dv
+
+
+def la_window_cache(k, v, window: int, sinks: int = 0, lens=None, kc=None, vc=None, stream=None):
+    """Ring caches (kc, vc) [B,Hk,sinks+window,d] of a prefill k, v [B,Hk,N,d]: token j in slot j while
+    j < sinks, else in sinks + (j - sinks) % window.  Slots without a token are left as they
+    were (zeros in caches made here)."""
+    import torch
+    if k.dim() != 4:
+        raise ValueError("k and v must be [B, Hk, N, d]")
+    B, Hk, N, d = k.shape
+    window, sinks = int(window), int(sinks)
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be at least 1, sinks at least 0")
+    shape = (B, Hk, sinks + window, d)
+    kc = torch.zeros(shape, dtype=k.dtype, device=k.device) if kc is None else kc
+    vc = torch.zeros(shape, dtype=k.dtype, device=k.device) if vc is None else vc
+    dev = _place(k, v, lens, kc, vc)
+    _same_dtype(k, v, kc, vc)
+    _shaped("v", v, k.shape)
+    _shaped("kc", kc, shape)
+    _shaped("vc", vc, shape)
+    _shaped("lens", lens, (B,), torch.int32)
+    _call("la_window_cache", dev, stream, k.data_ptr(), v.data_ptr(), kc.data_ptr(), vc.data_ptr(), _ptr(lens), B, Hk,
+          N, d, window, sinks, _dtype_code(k))
+    return kc, vc
+
+
+def la_window_decode_step(kc, vc, q, k, v, pos, window: int, sinks: int = 0, scale: float = None, o=None, stream=None):
+    """One decode step on ring caches kc, vc [B,Hk,sinks+window,d] (updated in place): q [B,Hq,d], k, v
+    [B,Hk,d], pos int32 [B] the new token's position per entry (negative: idle).  Returns o [B,Hq,d]."""
+    import torch
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [B, Hq, d], k and v [B, Hk, d]")
+    B, Hq, d = q.shape
+    Hk = k.shape[1]
+    window, sinks = int(window), int(sinks)
+    o = torch.empty_like(q) if o is None else o
+    dev = _place(kc, vc, q, k, v, pos, o)
+    _same_dtype(q, k, v, kc, vc, o)
+    _shaped("k", k, (B, Hk, d))
+    _shaped("v", v, (B, Hk, d))
+    _shaped("kc", kc, (B, Hk, sinks + window, d))
+    _shaped("vc", vc, (B, Hk, sinks + window, d))
+    _shaped("pos", pos, (B,), torch.int32)
+    _shaped("o", o, q.shape)
+    _call("la_window_decode_step", dev, stream, kc.data_ptr(), vc.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          o.data_ptr(), pos.data_ptr(), B, Hq, Hk, d, window, sinks, _scale(scale, d), _dtype_code(q))
+    return o

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stdint.h>
 
 #include "la.h"
 
@@ -137,6 +138,70 @@ long long test_drop_ticket();
 // cores in fp32.
 la_status favor_features(const void *xq, const void *xk, const void *W, void *oq, void *ok, int BH, int N, int d,
                          int m, la_dtype dtype, cudaStream_t stream);
+
+// Rotary positions (la_rotary.cu).  turns[i]: the frequency of pair i in turns per
+// position, times 2^64.  k and ok null when Hk = 0.
+constexpr int kRotaryMaxPairs = 128;
+struct RotaryProblem {
+    const void *q, *k;
+    void *oq, *ok;
+    const int *positions;
+    long long offset;
+    la_rotary_spec spec;
+    uint64_t turns[kRotaryMaxPairs];
+    int B, Hq, Hk, N, d;
+    bool backward;
+    la_dtype dtype;
+    cudaStream_t stream;
+};
+la_status rotary(const RotaryProblem &p);
+
+// Gated recurrence per channel (la_recurrence.cu): forward x, h0 -> h, hN; backward h_in
+// (the forward's h), dh, dhN, h0 -> dx, dalpha, dh0.
+struct RecurrenceProblem {
+    const void *x, *h_in, *dh;
+    const float *alpha, *h0, *dhN;
+    void *h, *dx;
+    float *hN, *dalpha, *dh0;
+    int B, N, D;
+    bool backward;
+    la_dtype dtype;
+    cudaStream_t stream;
+};
+la_status recurrence(const RecurrenceProblem &p);
+la_status recurrence_step(float *state, const void *x, const float *alpha, void *h, int B, int D, la_dtype dtype,
+                          cudaStream_t stream);
+
+// Window attention with sinks (la_window.cu: CUDA cores, fp32 arithmetic).  forward: out, lse;
+// backward: o, lse, dout -> dq, dk, dv, with delta (fp32, [B, Hq, Nq]) as scratch.  window
+// and sinks are at most Nk.
+struct WindowProblem {
+    const void *q, *k, *v, *o, *dout;
+    void *out, *dq, *dk, *dv;
+    float *lse, *delta;
+    const int *lens;
+    int B, Hq, Hk, Nq, Nk, d, window, sinks;
+    float scale;
+    la_dtype dtype;
+    cudaStream_t stream;
+};
+la_status window_forward_simt(const WindowProblem &p);
+la_status window_backward_simt(const WindowProblem &p);
+
+// The ring cache and the decode step (la_window_decode.cu).
+struct WindowDecodeProblem {
+    void *kc, *vc;
+    const void *q, *k, *v;
+    void *o;
+    const int *pos;
+    int B, Hq, Hk, d, window, sinks;
+    float scale;
+    la_dtype dtype;
+    cudaStream_t stream;
+};
+la_status window_decode(const WindowDecodeProblem &p);
+la_status window_cache(const void *k, const void *v, void *kc, void *vc, const int *lens, int B, int Hk, int N, int d,
+                       int window, int sinks, la_dtype dtype, cudaStream_t stream);
 
 bool supported_dim(int d);
 

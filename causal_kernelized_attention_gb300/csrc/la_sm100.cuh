@@ -313,6 +313,13 @@ __device__ __forceinline__ uint32_t cluster_ctarank()
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+// Number of CTAs in this CTA's cluster (1 for a launch without clusters).
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
 // The shared::cluster address of this CTA's shared-memory address `a` in CTA `rank`.
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t a, uint32_t rank)
 {
@@ -333,6 +340,11 @@ __device__ __forceinline__ float ld_dsmem_f32(uint32_t a)
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
+}
+// Stores to another CTA's shared memory.
+__device__ __forceinline__ void st_dsmem_f32(uint32_t a, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 // Arrive on an mbarrier of another CTA of the cluster (shared::cluster address),
 // releasing this thread's prior writes at cluster scope.

@@ -1,0 +1,411 @@
+// Softmax attention over a sliding window with sinks, on the CUDA cores in fp32.
+//
+//   forward   s_pj = scale q_p . k_j over the visible j,  lse_p = log sum_j exp(s_pj),
+//             o_p = sum_j exp(s_pj - lse_p) v_j           (no visible j: o = 0, lse = -inf)
+//   backward  P_pj = exp(s_pj - lse_p),  D_p = dO_p . o_p,
+//             dS_pj = P_pj (dO_p . v_j - D_p) scale,
+//             dq_p = sum_j dS_pj k_j,  dk_j = sum_p dS_pj q_p,  dv_j = sum_p P_pj dO_p
+//             (key and value heads: summed over the query heads that share them)
+//
+// The forward and the dq kernel give a CTA 64 query rows and pass over the key tiles their
+// window and the sinks reach (running maximum and sum of the softmax, the output rescaled as
+// the maximum grows); the dk, dv kernel gives a CTA 64 keys and passes over the query tiles
+// that see them, of every head of the group, so each gradient is written once, by one CTA,
+// in a fixed order.  All products are fp32 fused multiply-adds on 4 x 4 register tiles fed
+// by 16-byte shared-memory loads (8 loads for 64 multiply-adds), rows padded by 4 floats so
+// that the 8 threads of a quarter-warp meet 8 different bank groups: bound by the CUDA
+// cores' fp32 rate.  fp32 calls run here; bf16 calls run on the tensor cores.
+#include <math.h>
+
+#include "la_window.cuh"
+
+namespace la {
+namespace {
+
+using namespace window;
+
+constexpr int kT = 64;         // rows and keys of a tile
+constexpr int kThreads = 256;  // 16 x 16: thread (ty, tx) owns rows ty + 16 i, keys tx + 16 j
+constexpr int kPS = kT + 4;    // row stride of the probability tiles
+
+template <int D> constexpr int stride() { return D + 4; }
+
+// Rows [t0, t0 + 64) of x [N, D] into shared memory; rows at or past `rows` become zero.
+template <typename T, int D>
+__device__ __forceinline__ void load_tile(float *dst, const T *x, int t0, int rows)
+{
+    for (int u = threadIdx.x; u < kT * (D / 4); u += kThreads) {
+        const int r = u / (D / 4), c = (u % (D / 4)) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t0 + r < rows) {
+            const T *p = x + (size_t)(t0 + r) * D + c;
+            v = make_float4(Elem<T>::to_f32(p[0]), Elem<T>::to_f32(p[1]), Elem<T>::to_f32(p[2]), Elem<T>::to_f32(p[3]));
+        }
+        *reinterpret_cast<float4 *>(dst + r * stride<D>() + c) = v;
+    }
+}
+
+__device__ __forceinline__ float dot4(const float4 &a, const float4 &b, float c)
+{
+    return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, c))));
+}
+
+// acc[i][j] = A[ty + 16 i] . B[tx + 16 j] over D columns.
+template <int D>
+__device__ __forceinline__ void mul_nt(float (&acc)[4][4], const float *A, const float *B, int ty, int tx)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = *reinterpret_cast<const float4 *>(A + (ty + 16 * i) * stride<D>() + c);
+            b[i] = *reinterpret_cast<const float4 *>(B + (tx + 16 * i) * stride<D>() + c);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = dot4(a[i], b[j], acc[i][j]);
+    }
+}
+
+// acc[i][c] += sum_j P[ty + 16 i][j] X[j][col(c)] over the tile's 64 j; thread columns are
+// 2 tx, 2 tx + 1 and the same 32 further on.
+template <int D>
+__device__ __forceinline__ void mul_nn(float (&acc)[4][D / 16], const float *P, const float *X, int ty, int tx)
+{
+#pragma unroll 2
+    for (int j = 0; j < kT; j += 4) {
+        float4 p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(P + (ty + 16 * i) * kPS + j);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            float2 x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[e] = *reinterpret_cast<const float2 *>(X + (j + e) * stride<D>() + 32 * c + 2 * tx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[i][2 * c] = fmaf(p[i].w, x[3].x, fmaf(p[i].z, x[2].x, fmaf(p[i].y, x[1].x, fmaf(p[i].x, x[0].x, acc[i][2 * c]))));
+                acc[i][2 * c + 1] =
+                    fmaf(p[i].w, x[3].y, fmaf(p[i].z, x[2].y, fmaf(p[i].y, x[1].y, fmaf(p[i].x, x[0].y, acc[i][2 * c + 1]))));
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ float max16(float v)
+{
+#pragma unroll
+    for (int m = 8; m > 0; m /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
+    return v;
+}
+__device__ __forceinline__ float sum16(float v)
+{
+#pragma unroll
+    for (int m = 8; m > 0; m /= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+}
+
+struct Args {
+    const void *q, *k, *v, *o, *dout;
+    void *out, *dq, *dk, *dv;
+    float *lse, *delta;
+    const int *lens;
+    int Hq, Hk, Nq, Nk, window, sinks;
+    float scale;
+};
+
+// ---------------------------------------------------------------- forward
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) window_forward_kernel(const Args a)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *q = sm, *k = q + kT * stride<D>(), *v = k + kT * stride<D>(), *pr = v + kT * stride<D>();
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tiles = (a.Nq + kT - 1) / kT;
+    const int bh = (int)(blockIdx.x / tiles), t0 = (int)(blockIdx.x % tiles) * kT;
+    const int b = bh / a.Hq, h = bh % a.Hq, off = a.Nk - a.Nq;
+    const int n = valid(a.lens, b, a.Nk);
+    const size_t kvrow = ((size_t)b * a.Hk + h / (a.Hq / a.Hk)) * a.Nk;
+    const T *kp = static_cast<const T *>(a.k) + kvrow * D, *vp = static_cast<const T *>(a.v) + kvrow * D;
+    load_tile<T, D>(q, static_cast<const T *>(a.q) + (size_t)bh * a.Nq * D, t0, a.Nq);
+    const KeyTiles kt(t0 + off, min(t0 + kT, a.Nq) - 1 + off, a.window, a.sinks, n, kT);
+    float m[4], l[4], o[4][D / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
+    }
+    for (int it = 0; it < kt.count(); ++it) {
+        const int j0 = kt.tile(it) * kT;
+        __syncthreads();
+        load_tile<T, D>(k, kp, j0, n);
+        load_tile<T, D>(v, vp, j0, n);
+        __syncthreads();
+        float s[4][4];
+        mul_nt<D>(s, q, k, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = t0 + ty + 16 * i + off;
+            float mx = m[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = sees(p, j0 + tx + 16 * j, a.window, a.sinks, n) ? s[i][j] * a.scale : -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+            mx = max16(mx);
+            const float safe = mx == -INFINITY ? 0.f : mx;  // nothing visible yet
+            const float keep = expf(m[i] - safe);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float e = expf(s[i][j] - safe);
+                sum += e;
+                pr[(ty + 16 * i) * kPS + tx + 16 * j] = e;
+            }
+            l[i] = l[i] * keep + sum16(sum);
+            m[i] = mx;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) o[i][c] *= keep;
+        }
+        __syncthreads();
+        mul_nn<D>(o, pr, v, ty, tx);
+    }
+    T *op = static_cast<T *>(a.out) + (size_t)bh * a.Nq * D;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = t0 + ty + 16 * i;
+        if (t >= a.Nq) continue;
+        const float inv = l[i] > 0.f || isnan(l[i]) ? 1.f / l[i] : 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            op[(size_t)t * D + 32 * c + 2 * tx] = Elem<T>::from_f32(o[i][2 * c] * inv);
+            op[(size_t)t * D + 32 * c + 2 * tx + 1] = Elem<T>::from_f32(o[i][2 * c + 1] * inv);
+        }
+        if (tx == 0) a.lse[(size_t)bh * a.Nq + t] = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
+    }
+}
+
+// P and dS of one 64 x 64 block, rows of queries: s = scores, g = dO . v.
+__device__ __forceinline__ void block_ds(float (&s)[4][4], float (&g)[4][4], const float *lse, const float *delta, int t0,
+                                         int j0, int off, int n, const Args &a, int ty, int tx)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty + 16 * i, p = t0 + r + off;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool in = t0 + r < a.Nq && sees(p, j0 + tx + 16 * j, a.window, a.sinks, n);
+            const float e = in ? expf(s[i][j] * a.scale - lse[r]) : 0.f;
+            s[i][j] = e;
+            g[i][j] = in ? e * (g[i][j] - delta[r]) * a.scale : 0.f;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- backward: dq
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) window_dq_kernel(const Args a)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *q = sm, *go = q + kT * stride<D>(), *k = go + kT * stride<D>(), *v = k + kT * stride<D>();
+    float *ds = v + kT * stride<D>();
+    __shared__ float lse[kT], delta[kT];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tiles = (a.Nq + kT - 1) / kT;
+    const int bh = (int)(blockIdx.x / tiles), t0 = (int)(blockIdx.x % tiles) * kT;
+    const int b = bh / a.Hq, h = bh % a.Hq, off = a.Nk - a.Nq;
+    const int n = valid(a.lens, b, a.Nk);
+    const size_t kvrow = ((size_t)b * a.Hk + h / (a.Hq / a.Hk)) * a.Nk, qrow = (size_t)bh * a.Nq;
+    const T *kp = static_cast<const T *>(a.k) + kvrow * D, *vp = static_cast<const T *>(a.v) + kvrow * D;
+    const int rows = min(a.Nq, n - off);  // rows of tokens; the others are padding
+    load_tile<T, D>(q, static_cast<const T *>(a.q) + qrow * D, t0, rows);
+    load_tile<T, D>(go, static_cast<const T *>(a.dout) + qrow * D, t0, rows);
+    load_tile<T, D>(k, static_cast<const T *>(a.o) + qrow * D, t0, rows);
+    __syncthreads();
+    // D_p = dO . o, four threads a row
+    {
+        const int r = threadIdx.x >> 2, part = threadIdx.x & 3;
+        float x = 0.f;
+        for (int c = part; c < D; c += 4) x = fmaf(go[r * stride<D>() + c], k[r * stride<D>() + c], x);
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        if (part == 0) {
+            const bool in = t0 + r < rows;
+            lse[r] = in ? a.lse[qrow + t0 + r] : 0.f;
+            delta[r] = x;
+            if (t0 + r < a.Nq) a.delta[qrow + t0 + r] = x;
+        }
+    }
+    float acc[4][D / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+    const KeyTiles kt(t0 + off, min(t0 + kT, a.Nq) - 1 + off, a.window, a.sinks, n, kT);
+    for (int it = 0; it < kt.count(); ++it) {
+        const int j0 = kt.tile(it) * kT;
+        __syncthreads();
+        load_tile<T, D>(k, kp, j0, n);
+        load_tile<T, D>(v, vp, j0, n);
+        __syncthreads();
+        float s[4][4], g[4][4];
+        mul_nt<D>(s, q, k, ty, tx);
+        mul_nt<D>(g, go, v, ty, tx);
+        block_ds(s, g, lse, delta, t0, j0, off, n, a, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ds[(ty + 16 * i) * kPS + tx + 16 * j] = g[i][j];
+        __syncthreads();
+        mul_nn<D>(acc, ds, k, ty, tx);
+    }
+    T *dq = static_cast<T *>(a.dq) + qrow * D;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = t0 + ty + 16 * i;
+        if (t >= a.Nq) continue;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            dq[(size_t)t * D + 32 * c + 2 * tx] = Elem<T>::from_f32(acc[i][2 * c]);
+            dq[(size_t)t * D + 32 * c + 2 * tx + 1] = Elem<T>::from_f32(acc[i][2 * c + 1]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- backward: dk, dv
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) window_dkv_kernel(const Args a)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *k = sm, *v = k + kT * stride<D>(), *q = v + kT * stride<D>(), *go = q + kT * stride<D>();
+    float *pt = go + kT * stride<D>(), *dst = pt + kT * kPS;  // transposed: rows of keys
+    __shared__ float lse[kT], delta[kT];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tiles = (a.Nk + kT - 1) / kT;
+    const int bh = (int)(blockIdx.x / tiles), j0 = (int)(blockIdx.x % tiles) * kT;
+    const int b = bh / a.Hk, hk = bh % a.Hk, off = a.Nk - a.Nq, group = a.Hq / a.Hk;
+    const int n = valid(a.lens, b, a.Nk);
+    const size_t kvrow = (size_t)bh * a.Nk;
+    load_tile<T, D>(k, static_cast<const T *>(a.k) + kvrow * D, j0, n);
+    load_tile<T, D>(v, static_cast<const T *>(a.v) + kvrow * D, j0, n);
+    float dk[4][D / 16], dv[4][D / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
+    const QueryTiles qt(j0, min(j0 + kT, a.Nk) - 1, a.window, a.sinks, n, off, a.Nq, kT);
+    const int rows = min(a.Nq, n - off);
+    for (int it = qt.begin * group; it < qt.end * group; ++it) {
+        const int t0 = (it / group) * kT, h = hk * group + it % group;
+        const size_t qrow = ((size_t)b * a.Hq + h) * a.Nq;
+        __syncthreads();
+        load_tile<T, D>(q, static_cast<const T *>(a.q) + qrow * D, t0, rows);
+        load_tile<T, D>(go, static_cast<const T *>(a.dout) + qrow * D, t0, rows);
+        if (threadIdx.x < kT) {
+            const bool in = t0 + (int)threadIdx.x < rows;
+            lse[threadIdx.x] = in ? a.lse[qrow + t0 + threadIdx.x] : 0.f;
+            delta[threadIdx.x] = in ? a.delta[qrow + t0 + threadIdx.x] : 0.f;
+        }
+        __syncthreads();
+        float s[4][4], g[4][4];
+        mul_nt<D>(s, q, k, ty, tx);
+        mul_nt<D>(g, go, v, ty, tx);
+        block_ds(s, g, lse, delta, t0, j0, off, n, a, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                pt[(tx + 16 * j) * kPS + ty + 16 * i] = s[i][j];
+                dst[(tx + 16 * j) * kPS + ty + 16 * i] = g[i][j];
+            }
+        __syncthreads();
+        mul_nn<D>(dv, pt, go, ty, tx);
+        mul_nn<D>(dk, dst, q, ty, tx);
+    }
+    T *dkp = static_cast<T *>(a.dk) + kvrow * D, *dvp = static_cast<T *>(a.dv) + kvrow * D;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = j0 + ty + 16 * i;
+        if (j >= a.Nk) continue;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                dkp[(size_t)j * D + 32 * c + 2 * tx + e] = Elem<T>::from_f32(dk[i][2 * c + e]);
+                dvp[(size_t)j * D + 32 * c + 2 * tx + e] = Elem<T>::from_f32(dv[i][2 * c + e]);
+            }
+    }
+}
+
+Args args_of(const WindowProblem &p)
+{
+    Args a;
+    a.q = p.q; a.k = p.k; a.v = p.v; a.o = p.o; a.dout = p.dout;
+    a.out = p.out; a.dq = p.dq; a.dk = p.dk; a.dv = p.dv;
+    a.lse = p.lse; a.delta = p.delta; a.lens = p.lens;
+    a.Hq = p.Hq; a.Hk = p.Hk; a.Nq = p.Nq; a.Nk = p.Nk;
+    a.window = p.window; a.sinks = p.sinks; a.scale = p.scale;
+    return a;
+}
+
+template <typename K>
+la_status launch(K kern, long long ctas, size_t smem, const Args &a, cudaStream_t s)
+{
+    if (ctas > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
+    la_status st = ensure_smem((const void *)kern, (int)smem);
+    if (st != LA_OK) return st;
+    count_launches();
+    kern<<<(unsigned)ctas, kThreads, smem, s>>>(a);
+    return cuda_status(cudaGetLastError());
+}
+
+template <typename T, int D>
+la_status forward(const WindowProblem &p)
+{
+    const size_t smem = (3 * kT * stride<D>() + kT * kPS) * sizeof(float);
+    return launch(window_forward_kernel<T, D>, (long long)p.B * p.Hq * ceil_div(p.Nq, kT), smem, args_of(p), p.stream);
+}
+
+template <typename T, int D>
+la_status backward(const WindowProblem &p)
+{
+    const size_t tile = kT * stride<D>(), prob = kT * kPS;
+    la_status st = launch(window_dq_kernel<T, D>, (long long)p.B * p.Hq * ceil_div(p.Nq, kT),
+                          (4 * tile + prob) * sizeof(float), args_of(p), p.stream);
+    if (st != LA_OK) return st;
+    return launch(window_dkv_kernel<T, D>, (long long)p.B * p.Hk * ceil_div(p.Nk, kT),
+                  (4 * tile + 2 * prob) * sizeof(float), args_of(p), p.stream);
+}
+
+}  // namespace
+
+la_status window_forward_simt(const WindowProblem &p)
+{
+    if (p.dtype == LA_BF16) {
+        if (p.d == 32) return forward<__nv_bfloat16, 32>(p);
+        return p.d == 64 ? forward<__nv_bfloat16, 64>(p) : forward<__nv_bfloat16, 128>(p);
+    }
+    if (p.d == 32) return forward<float, 32>(p);
+    return p.d == 64 ? forward<float, 64>(p) : forward<float, 128>(p);
+}
+
+la_status window_backward_simt(const WindowProblem &p)
+{
+    if (p.dtype == LA_BF16) {
+        if (p.d == 32) return backward<__nv_bfloat16, 32>(p);
+        return p.d == 64 ? backward<__nv_bfloat16, 64>(p) : backward<__nv_bfloat16, 128>(p);
+    }
+    if (p.d == 32) return backward<float, 32>(p);
+    return p.d == 64 ? backward<float, 64>(p) : backward<float, 128>(p);
+}
+
+}  // namespace la

@@ -434,6 +434,149 @@ la_status la_decode_step_favor(float *S, float *z, const void *q, const void *k,
                                const void *w, int B, int H, int d, int dv, int m, float eps, la_dtype dtype,
                                la_stream_t stream);
 
+/*
+ * Rotary positions for queries and keys, ahead of the window attention below and of the
+ * *_ex forms (the retention form: identity map, decay, no normaliser).  The features of a
+ * token at position p are turned pair by pair,
+ *
+ *   a' = A (a cos(p f_i) - b sin(p f_i)),   b' = A (b cos(p f_i) + a sin(p f_i)),
+ *
+ * with f_i = base^(-2 i / rot) for pairs i = 0 .. rot/2 - 1, scaled for long contexts:
+ *   LA_ROTARY_NONE    as they are (factor, original, ramp_lo, ramp_hi ignored)
+ *   LA_ROTARY_LINEAR  f_i / factor (positions interpolated)
+ *   LA_ROTARY_NTK     base replaced by base * factor^(rot / (rot - 2)), which leaves the
+ *                     fastest pair alone and divides the slowest frequency by `factor`
+ *                     (rot = 2 has one pair, which stays)
+ *   LA_ROTARY_RAMP    by parts: with r_i = original f_i / (2 pi) turns over the original
+ *                     context and g_i = clamp((r_i - ramp_lo) / (ramp_hi - ramp_lo), 0, 1),
+ *                     f_i (g_i + (1 - g_i) / factor)
+ * and A = amplitude.  Layouts: LA_ROTARY_HALF pairs features (i, i + rot/2),
+ * LA_ROTARY_INTERLEAVED (2 i, 2 i + 1).  Features from `rot` on are copied.
+ */
+typedef enum { LA_ROTARY_HALF = 0, LA_ROTARY_INTERLEAVED = 1 } la_rotary_layout;
+typedef enum { LA_ROTARY_NONE = 0, LA_ROTARY_LINEAR = 1, LA_ROTARY_NTK = 2, LA_ROTARY_RAMP = 3 } la_rotary_scaling;
+
+typedef struct {
+    int rot;         /* even, 0 .. d */
+    int layout;      /* la_rotary_layout */
+    int scaling;     /* la_rotary_scaling */
+    int original;    /* RAMP: > 0 */
+    double base;     /* > 0 */
+    double factor;   /* LINEAR, NTK, RAMP: > 0 */
+    double ramp_lo, ramp_hi; /* RAMP: lo < hi */
+    float amplitude; /* finite */
+} la_rotary_spec;
+
+/*
+ *   q, oq : [B, Hq, N, d]   k, ok : [B, Hk, N, d]   (element type `dtype`)
+ *   positions : [B, N] int32, DEVICE memory, 4-byte aligned, any values; or NULL:
+ *               token n of every entry stands at offset + n
+ *
+ * la_rotary_forward turns q and k in one launch; la_rotary_backward applies the transpose
+ * (dq from doq, dk from dok; the same spec and positions).  Hk = 0 turns q alone (k and ok
+ * may be NULL).  oq may be q itself and ok k itself (in place); any other overlap of an
+ * output with an input, with `positions` or with the other output is LA_ERR_INVALID_ARG.
+ * The angle is reduced exactly for every 32-bit position; arithmetic is fp32, rounded once.
+ * d: a multiple of 8 up to 256; B at most 65535 (else LA_ERR_UNSUPPORTED).
+ */
+la_status la_rotary_forward(const void *q, const void *k, void *oq, void *ok, const int *positions,
+                            long long offset, const la_rotary_spec *spec, int B, int Hq, int Hk, int N, int d,
+                            la_dtype dtype, la_stream_t stream);
+la_status la_rotary_backward(const void *doq, const void *dok, void *dq, void *dk, const int *positions,
+                             long long offset, const la_rotary_spec *spec, int B, int Hq, int Hk, int N, int d,
+                             la_dtype dtype, la_stream_t stream);
+
+/*
+ * Gated recurrence, one scalar state per channel -- the vector-state relative of the gated
+ * forms above ("Linear Attention", aiwiki.thehackersbrain.dev: a linear RNN with a
+ * decay computed from the token):
+ *
+ *   h_t = alpha_t h_{t-1} + x_t,   t = 0 .. N-1,   h_{-1} = h0 (NULL: zeros)
+ *
+ *   x, h : [B, N, D] (element type `dtype`)   alpha : [B, N, D] fp32
+ *   h0, hN : [B, D] fp32, each may be NULL; hN = h_{N-1} (h0 when N = 0)
+ *
+ * The state is carried in fp32 between tokens and each h_t rounded once.  alpha is read as
+ * given (the method takes it in [0, 1]; a gate of 0 starts a new sequence, so packed
+ * sequences need no other mark).  The sequence is scanned in runs joined by the products of
+ * their gates: products must not overflow, and an infinite or NaN x or gate makes the rest of
+ * its channel non-finite or NaN.
+ *
+ * la_recurrence_backward: given h (the forward's output), dh = dL/dh and dhN = dL/dhN (NULL:
+ * zeros), writes dx, dalpha and dh0 (NULL: not wanted):
+ *   g_t = dh_t + alpha_{t+1} g_{t+1} (g_{N-1} = dh_{N-1} + dhN),
+ *   dx_t = g_t,   dalpha_t = g_t h_{t-1} (fp32),   dh0 = alpha_0 g_0.
+ * la_recurrence_step: one token; state [B, D] fp32 read and updated in place,
+ *   state = alpha state + x, h = state; x, alpha, h : [B, D].
+ *
+ * Outputs overlap no input and no other output.  B = 0 or D = 0 is an empty problem; N = 0
+ * still writes hN (dh0 = dhN).
+ */
+la_status la_recurrence_forward(const void *x, const float *alpha, const float *h0, void *h, float *hN, int B, int N,
+                                int D, la_dtype dtype, la_stream_t stream);
+la_status la_recurrence_backward(const float *alpha, const void *h, const void *dh, const float *h0,
+                                 const float *dhN, void *dx, float *dalpha, float *dh0, int B, int N, int D,
+                                 la_dtype dtype, la_stream_t stream);
+la_status la_recurrence_step(float *state, const void *x, const float *alpha, void *h, int B, int D, la_dtype dtype,
+                             la_stream_t stream);
+
+/*
+ * Softmax attention over a sliding window with sinks, for the local layers of hybrid
+ * stacks: like S and z, its memory per sequence does not grow with the length.
+ *
+ *   q, o : [B, Hq, Nq, d]   k, v : [B, Hk, Nk, d]   lse : [B, Hq, Nq] fp32
+ *
+ * Query row t stands at position p = t + Nk - Nq (the queries are the last Nq tokens) and
+ * sees key j when j <= p and (p - j < window or j < sinks):
+ *
+ *   o_t = sum_j softmax_j(scale q_t . k_j) v_j,   lse_t = log sum_j exp(scale q_t . k_j)
+ *
+ * Query head h reads key head h / (Hq / Hk).  lens ([B] int32, DEVICE memory, 4-byte
+ * aligned, or NULL: all Nk) gives the valid tokens of each entry, clamped to [0, Nk]:
+ * rows at positions >= lens[b] are padding and give o = 0 and lse = -inf, keys there are
+ * never used, whatever they hold.  Within the valid tokens an infinite or NaN k or v may
+ * also reach rows of nearby positions that do not see it.  Supported: d in {32, 64, 128},
+ * Nq <= Nk, Hq a multiple of Hk, window >= 1, sinks >= 0, scale > 0 and finite.  window >= Nk
+ * is plain causal attention.
+ *
+ * la_window_backward: given o and lse of the forward and dout = dL/do, writes dq, dk, dv
+ * (dk, dv summed over the query heads that share them; rows and keys past lens give 0).
+ * Deterministic: every sum is taken in a fixed order.  Scratch: B*Hq*Nq floats, from the
+ * stream's workspace, or stream-ordered while the stream is being captured.
+ *
+ * Arithmetic: fp32 inputs in fp32 on the CUDA cores; bf16 inputs on the tensor cores with
+ * fp32 scores, softmax and accumulation, the weights (and dS) rounded to bf16 for their
+ * products.  Outputs overlap no input and no other output.
+ */
+la_status la_window_forward(const void *q, const void *k, const void *v, void *o, float *lse, const int *lens, int B,
+                            int Hq, int Hk, int Nq, int Nk, int d, int window, int sinks, float scale, la_dtype dtype,
+                            la_stream_t stream);
+la_status la_window_backward(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                             const void *dout, void *dq, void *dk, void *dv, const int *lens, int B, int Hq, int Hk,
+                             int Nq, int Nk, int d, int window, int sinks, float scale, la_dtype dtype,
+                             la_stream_t stream);
+
+/*
+ * The window's cache, and one decode step on it (the counterparts of la_prefill_state and
+ * la_decode_step).  kc, vc : [B, Hk, sinks + window, d] hold token j in slot j while
+ * j < sinks, else in slot sinks + (j - sinks) % window, over the token that has left the
+ * window: passing them back in continues the sequence.
+ *
+ * la_window_cache: fills the slots after a prefill of k, v [B, Hk, N, d] (lens as above);
+ *   slots that hold no token are left as they were.
+ * la_window_decode_step: q, o : [B, Hq, d], k, v : [B, Hk, d], pos : [B] int32, DEVICE
+ *   memory, 4-byte aligned: the position of each entry's new token (the number of tokens
+ *   before it).  Writes k and v into their slot and returns attention over the visible
+ *   slots.  pos[b] < 0 marks an idle entry: o = 0, its cache untouched.  pos is read on the
+ *   device, so a captured step can be replayed with pos advanced.
+ * Supported sizes as above; sinks + window at most 2^31 - 1.
+ */
+la_status la_window_cache(const void *k, const void *v, void *kc, void *vc, const int *lens, int B, int Hk, int N,
+                          int d, int window, int sinks, la_dtype dtype, la_stream_t stream);
+la_status la_window_decode_step(void *kc, void *vc, const void *q, const void *k, const void *v, void *o,
+                                const int *pos, int B, int Hq, int Hk, int d, int window, int sinks, float scale,
+                                la_dtype dtype, la_stream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *la_status_string(la_status s);
 

@@ -1,0 +1,313 @@
+"""Window attention with sinks on the GPU against its float64 form (tests/hybrid_ref.py)."""
+import math
+
+import pytest
+
+import hybrid_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+T = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from causal_kernelized_attention_gb300 import build
+    build.build()
+
+
+def la():
+    import causal_kernelized_attention_gb300 as m
+    return m
+
+
+def check(dtype, B, Hq, Hk, Nq, Nk, d, window, sinks, lens=None, scale=None, spoil=False, big=1.0):
+    """Forward and backward of one problem; `spoil` fills what lies past lens with NaN and infinities."""
+    t = T[dtype]
+    q, k, v = (ref.draw(i, s, t, big) for i, s in ((1, (B, Hq, Nq, d)), (2, (B, Hk, Nk, d)), (3, (B, Hk, Nk, d))))
+    dout = ref.draw(4, (B, Hq, Nq, d), t)
+    ln = None if lens is None else torch.tensor(lens, dtype=torch.int32)
+    sc = 1 / math.sqrt(d) if scale is None else scale
+    if spoil:
+        for b in range(B):
+            n = max(0, min(lens[b], Nk))
+            k[b, :, n:], v[b, :, n:] = float("nan"), float("inf")
+            rows = max(0, n - (Nk - Nq))
+            q[b, :, rows:], dout[b, :, rows:] = float("inf"), float("nan")
+    c = [x.cuda() for x in (q, k, v)]
+    lc = None if ln is None else ln.cuda()
+    o, lse = la().la_window_forward(*c, window, sinks=sinks, lens=lc, scale=scale)
+    (wo, eo), (wl, el) = ref.window(q, k, v, window, sinks, ln, sc)
+    ref.assert_within(o, wo, eo, "o")
+    ref.assert_within(lse, wl, el, "lse")
+    so, sl = wo.to(t), wl.float()
+    if spoil:  # padding rows of o are the caller's to leave as they are
+        for b in range(B):
+            so[b, :, max(0, min(lens[b], Nk) - (Nk - Nq)):] = float("nan")
+    got = la().la_window_backward(*c, so.cuda(), sl.cuda(), dout.cuda(), window, sinks=sinks, lens=lc, scale=scale)
+    for name, x, (w, e) in zip(("dq", "dk", "dv"), got, ref.window(q, k, v, window, sinks, ln, sc, dout, so, sl)):
+        ref.assert_within(x, w, e, name)
+    assert la().la_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hk,Nq,Nk,d,window,sinks", [
+    (1, 1, 1, 1, 1, 64, 1, 0), (2, 2, 1, 5, 5, 32, 2, 1), (1, 2, 2, 64, 64, 64, 64, 0), (1, 4, 2, 65, 65, 128, 7, 3),
+    (2, 4, 1, 127, 127, 64, 50, 4), (1, 2, 1, 128, 128, 128, 128, 0), (1, 2, 2, 129, 129, 64, 1, 0),
+    (1, 2, 1, 300, 300, 64, 128, 130), (1, 2, 2, 385, 385, 32, 100, 5), (1, 3, 1, 513, 513, 128, 129, 1),
+    (1, 2, 1, 700, 700, 64, 1000000, 0), (1, 2, 2, 640, 640, 64, 257, 200), (1, 1, 1, 1, 900, 64, 256, 4),
+    (2, 2, 1, 100, 517, 128, 200, 9), (1, 16, 1, 130, 260, 64, 33, 2), (1, 1, 1, 400, 400, 64, 5, 1000)])
+def test_against_float64(dtype, B, Hq, Hk, Nq, Nk, d, window, sinks):
+    """Sizes at, below and past the tiles, windows of one token to the whole sequence, sinks inside
+    and across tiles, shared heads, and queries that are only the last of their keys."""
+    check(dtype, B, Hq, Hk, Nq, Nk, d, window, sinks)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Nq,Nk,d,window,sinks,lens", [
+    (200, 200, 64, 50, 3, [0, 1, 127]), (300, 300, 128, 128, 0, [128, 129, 300]), (64, 256, 64, 100, 2, [256, 200, 150]),
+    (150, 150, 32, 1000, 0, [-4, 75, 1000])])
+def test_padded_batches(dtype, Nq, Nk, d, window, sinks, lens):
+    """Entries of no tokens, of all and of some, out-of-range lengths, with NaN and infinities in the
+    padding of every input."""
+    check(dtype, 3, 4, 2, Nq, Nk, d, window, sinks, lens=lens, spoil=True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_large_scores(dtype):
+    """Scores of hundreds, which exp alone would overflow, and a scale of its own."""
+    check(dtype, 1, 2, 1, 200, 200, 64, 77, 2, scale=0.6, big=4.0)
+
+
+def test_lowest_values_are_not_masks():
+    """Scores at the type's lowest values still take part: equal scores give the plain mean."""
+    B, H, N, d = 1, 1, 140, 64
+    q = torch.zeros((B, H, N, d), dtype=torch.bfloat16)
+    k = torch.zeros_like(q)
+    q[..., 0], k[..., 0] = 1.0, torch.finfo(torch.bfloat16).min
+    v = ref.draw(1, (B, H, N, d), torch.bfloat16)
+    o, lse = la().la_window_forward(q.cuda(), k.cuda(), v.cuda(), 20, scale=1.0)
+    want = torch.stack([v[0, 0, max(0, p - 19):p + 1].double().mean(0) for p in range(N)])
+    ref.assert_within(o[0, 0], want, 2.0 ** -8 * (want.abs() + 1.0) + 1e-6)
+
+
+def test_deterministic_and_neighbours_untouched():
+    """The same bits twice, and nothing written around the outputs."""
+    B, Hq, Hk, N, d = 2, 4, 2, 333, 64
+    q, k, v, go = (ref.draw(i, s, torch.bfloat16).cuda() for i, s in
+                   ((1, (B, Hq, N, d)), (2, (B, Hk, N, d)), (3, (B, Hk, N, d)), (4, (B, Hq, N, d))))
+    o, lse = la().la_window_forward(q, k, v, 100, sinks=4)
+    first = la().la_window_backward(q, k, v, o, lse, go, 100, sinks=4)
+
+    def inside(like):
+        buf = torch.full((like.numel() + 512,), 99.0, dtype=like.dtype, device="cuda")
+        return buf, buf[256:256 + like.numel()].view(like.shape)
+
+    bufs = [inside(x) for x in (o, lse, *first)]
+    la().la_window_forward(q, k, v, 100, sinks=4, o=bufs[0][1], lse=bufs[1][1])
+    la().la_window_backward(q, k, v, o, lse, go, 100, sinks=4, dq=bufs[2][1], dk=bufs[3][1], dv=bufs[4][1])
+    for (buf, x), want in zip(bufs, (o, lse, *first)):
+        assert torch.equal(x, want)
+        assert bool((buf[:256] == 99).all()) and bool((buf[-256:] == 99).all())
+
+
+def test_window_of_everything_is_causal_softmax():
+    """window >= Nk with any sinks is causal attention."""
+    q, k, v = (ref.draw(i, (1, 2, 150, 64), torch.float32).cuda() for i in (1, 2, 3))
+    a = la().la_window_forward(q, k, v, 150)[0]
+    b = la().la_window_forward(q, k, v, 1, sinks=150)[0]
+    z = (q.double() @ k.double().transpose(-1, -2)) / 8
+    z = z.masked_fill(torch.ones(150, 150, dtype=torch.bool, device="cuda").triu(1), -math.inf)
+    want = torch.softmax(z, -1) @ v.double()
+    for x in (a, b):
+        assert float((x.double() - want).abs().max()) < 1e-5
+
+
+def test_empty():
+    z = torch.empty((2, 0, 5, 64), device="cuda")
+    o, lse = la().la_window_forward(z, torch.empty((2, 0, 5, 64), device="cuda"), torch.empty((2, 0, 5, 64), device="cuda"), 4)
+    assert o.numel() == 0 and lse.numel() == 0
+    # no queries: no key has a gradient
+    q, kv = torch.empty((2, 2, 0, 64), device="cuda"), torch.randn((2, 1, 7, 64), device="cuda")
+    o, lse = la().la_window_forward(q, kv, kv, 4)
+    dq, dk, dv = la().la_window_backward(q, kv, kv, o, lse, q, 4)
+    assert dq.numel() == 0 and not dk.any() and not dv.any()
+
+
+def test_graphs_and_streams():
+    """Forward and backward captured in two graphs, replayed together on new data."""
+    B, Hq, Hk, N, d = 1, 4, 2, 500, 64
+    make = lambda s: [ref.draw(i + s, sh, torch.bfloat16).cuda() for i, sh in  # noqa: E731
+                      enumerate(((B, Hq, N, d), (B, Hk, N, d), (B, Hk, N, d), (B, Hq, N, d)))]
+    sets, graphs, outs = [make(10), make(20)], [], []
+    for q, k, v, go in sets:
+        la().la_window_backward(q, k, v, *la().la_window_forward(q, k, v, 90, sinks=2), go, 90, sinks=2)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o, lse = la().la_window_forward(q, k, v, 90, sinks=2)
+            outs.append((o, lse, *la().la_window_backward(q, k, v, o, lse, go, 90, sinks=2)))
+        graphs.append(g)
+    for (q, k, v, go), n in zip(sets, (make(30), make(40))):
+        for a, b in zip((q, k, v, go), n):
+            a.copy_(b)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (q, k, v, go), out in zip(sets, outs):
+        o, lse = la().la_window_forward(q, k, v, 90, sinks=2)
+        for x, y in zip(out, (o, lse, *la().la_window_backward(q, k, v, o, lse, go, 90, sinks=2))):
+            assert torch.equal(x, y)
+
+
+# ---------------------------------------------------------------- serving
+def decode_reference(kc, vc, q, k, v, pos, window, sinks, scale):
+    """Float64 attention over the tokens that slots hold, and its bound (as hybrid_ref.window; weights
+    of 16-bit caches within 2^-16)."""
+    B, Hq, d = q.shape
+    Hk = k.shape[1]
+    o, e = torch.zeros((B, Hq, d), dtype=torch.float64), torch.zeros((B, Hq, d), dtype=torch.float64)
+    kc, vc = kc.clone(), vc.clone()
+    for b in range(B):
+        p = int(pos[b])
+        if p < 0:
+            continue
+        kc[b, :, ref.slot(p, window, sinks)], vc[b, :, ref.slot(p, window, sinks)] = k[b], v[b]
+        tokens = list(range(min(sinks, p + 1))) + list(range(max(sinks, p - window + 1), p + 1))
+        at = torch.tensor([ref.slot(t, window, sinks) for t in tokens])
+        for h in range(Hq):
+            K, V = kc[b, h // (Hq // Hk)][at].double(), vc[b, h // (Hq // Hk)][at].double()
+            Q = q[b, h].double()
+            w = torch.softmax(K @ Q * scale, 0)
+            err = 2 * float(((d + 8) * ref.U * scale * (K.abs() @ Q.abs())).max()) + (len(tokens) + 40) * ref.U
+            o[b, h] = w @ V
+            e[b, h] = (err + (2.0 ** -16 if q.dtype != torch.float32 else 0.0)) * (w @ V.abs()) + ref.half(q.dtype) * o[b, h].abs()
+    return o, e, kc, vc
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hk,d,window,sinks,pos", [
+    (1, 1, 1, 64, 1, 0, [0]), (2, 2, 1, 32, 16, 0, [3, 40]), (3, 8, 2, 128, 33, 4, [0, 3, 4]), (2, 6, 2, 64, 100, 7, [106, 107]),
+    (4, 4, 4, 128, 64, 1, [-1, 64, 65, 100000]), (1, 17, 1, 64, 50, 2, [300]), (2, 40, 2, 128, 300, 16, [315, 316]),
+    (1, 8, 1, 64, 2049, 4, [2 ** 31 - 1]), (1, 5, 5, 32, 5000, 0, [4000])])
+def test_decode_step(dtype, B, Hq, Hk, d, window, sinks, pos):
+    """Empty, partly filled and turned-over caches, idle entries, up to 20 heads a group, far positions;
+    slots that hold no token carry NaN."""
+    t = T[dtype]
+    kc, vc = ref.draw(1, (B, Hk, sinks + window, d), t), ref.draw(2, (B, Hk, sinks + window, d), t)
+    for b, p in enumerate(pos):
+        kc[b, :, max(p, 0):], vc[b, :, max(p, 0):] = float("nan"), float("inf")
+    q, k, v = ref.draw(3, (B, Hq, d), t), ref.draw(4, (B, Hk, d), t), ref.draw(5, (B, Hk, d), t)
+    p = torch.tensor(pos, dtype=torch.int32)
+    ck, cv = kc.cuda(), vc.cuda()
+    o = la().la_window_decode_step(ck, cv, q.cuda(), k.cuda(), v.cuda(), p.cuda(), window, sinks=sinks)
+    want, bound, wk, wv = decode_reference(kc, vc, q, k, v, p, window, sinks, 1 / math.sqrt(d))
+    ref.assert_within(o, want, bound)
+    for got, w in ((ck, wk), (cv, wv)):  # the new token's slot and nothing else
+        assert torch.equal(got.cpu().view(torch.uint8), w.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prefill_then_decode_is_the_forward(dtype):
+    """A ragged prefill into the ring cache and decode steps over its turn give the forward's rows."""
+    t, B, Hq, Hk, N, d, W, S = T[dtype], 3, 4, 2, 90, 64, 24, 3
+    q, k, v = (ref.draw(i, s, t) for i, s in ((1, (B, Hq, N, d)), (2, (B, Hk, N, d)), (3, (B, Hk, N, d))))
+    lens = torch.tensor([2, 20, 60], dtype=torch.int32)
+    kc, vc = la().la_window_cache(k.cuda(), v.cuda(), W, sinks=S, lens=lens.cuda())
+    for b in range(B):  # every visible token where it belongs
+        for j in range(N):
+            if j < int(lens[b]) and (j < S or int(lens[b]) - 1 - j < W):
+                assert torch.equal(kc[b, :, ref.slot(j, W, S)].cpu(), k[b, :, j])
+                assert torch.equal(vc[b, :, ref.slot(j, W, S)].cpu(), v[b, :, j])
+    (wo, eo), _ = ref.window(q, k, v, W, S, None, 1 / math.sqrt(d))
+    pos = lens.clone()
+    for _ in range(30):
+        at = pos.long()
+        row = torch.arange(B)
+        o = la().la_window_decode_step(kc, vc, q[row, :, at].cuda(), k[row, :, at].cuda(), v[row, :, at].cuda(), pos.cuda(),
+                                       W, sinks=S)
+        ref.assert_within(o, wo[row, :, at], eo[row, :, at])
+        pos += 1
+
+
+def test_decode_replayed_with_positions_advanced():
+    """One captured step, replayed as the positions and tokens move on."""
+    B, Hq, Hk, d, W, S = 2, 4, 2, 64, 20, 2
+    kc = torch.zeros((B, Hk, S + W, d), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    q, k, v = (torch.zeros((B, h, d), dtype=torch.bfloat16, device="cuda") for h in (Hq, Hk, Hk))
+    pos = torch.zeros(B, dtype=torch.int32, device="cuda")
+    o = torch.empty_like(q)
+    la().la_window_decode_step(kc, vc, q, k, v, pos, W, sinks=S, o=o)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        la().la_window_decode_step(kc, vc, q, k, v, pos, W, sinks=S, o=o)
+        pos.add_(1)
+    N = 50
+    Q, K, V = (ref.draw(i, s, torch.bfloat16) for i, s in ((1, (B, Hq, N, d)), (2, (B, Hk, N, d)), (3, (B, Hk, N, d))))
+    (wo, eo), _ = ref.window(Q, K, V, W, S, None, 1 / math.sqrt(d))
+    for i in range(N):
+        for dst, src in ((q, Q), (k, K), (v, V)):
+            dst.copy_(src[:, :, i])
+        g.replay()
+        torch.cuda.synchronize()
+        ref.assert_within(o, wo[:, :, i], eo[:, :, i], i)
+    assert pos.tolist() == [N, N]
+
+
+def test_a_hybrid_block_runs_together():
+    """Rotary positions, window attention and the gated recurrence as a block of a hybrid stack trains
+    and serves: the gradient of the whole against the float64 chain rule, then the same tokens one by
+    one from a prefill."""
+    B, H, N, d, W, S = 1, 2, 70, 32, 16, 2
+    D = H * d
+    q, k, v = (ref.draw(i, (B, H, N, d), torch.float32) for i in (1, 2, 3))
+    alpha = torch.sigmoid(ref.draw(4, (B, N, D), torch.float32) + 2)
+    w = ref.draw(5, (B, N, D), torch.float32)
+    lib = la()
+    rq, rk = lib.la_rotary_forward(q.cuda(), k.cuda())
+    o, lse = lib.la_window_forward(rq, rk, v.cuda(), W, sinks=S)
+    x = o.transpose(1, 2).reshape(B, N, D)
+    h, hN = lib.la_recurrence_forward(x, alpha.cuda())
+    dx, dalpha, _ = lib.la_recurrence_backward(alpha.cuda(), h, w.cuda())
+    do = dx.view(B, N, H, d).transpose(1, 2).contiguous()
+    drq, drk, dv = lib.la_window_backward(rq, rk, v.cuda(), o, lse, do, W, sinks=S)
+    dq, dk = lib.la_rotary_backward(drq, drk)
+
+    leaves = [t.double().requires_grad_() for t in (q, k, v, alpha)]
+    f = ref.frequencies(d)
+    ang = torch.arange(N, dtype=torch.float64)[:, None] * f
+
+    def turn(t):
+        a, b = t[..., :d // 2], t[..., d // 2:]
+        return torch.cat((a * ang.cos() - b * ang.sin(), b * ang.cos() + a * ang.sin()), -1)
+
+    z = (turn(leaves[0]) @ turn(leaves[1]).transpose(-1, -2)) / math.sqrt(d)
+    z = z.masked_fill(~ref.visible(N, N, W, S, N), -math.inf)
+    y = (torch.softmax(z, -1) @ leaves[2]).transpose(1, 2).reshape(B, N, D)
+    state, hs = torch.zeros((B, D), dtype=torch.float64), []
+    for t in range(N):
+        state = leaves[3][:, t] * state + y[:, t]
+        hs.append(state)
+    (torch.stack(hs, 1) * w.double()).sum().backward()
+    # fp32 throughout: sums of up to N * N terms, each within a few u
+    for got, leaf in zip((dq, dk, dv, dalpha), leaves):
+        scale = float(leaf.grad.abs().max())
+        assert float((got.cpu().double() - leaf.grad).abs().max()) < 2e-5 * scale
+    assert float((h.cpu().double() - torch.stack(hs, 1).detach()).abs().max()) < 2e-5 * float(state.abs().max() + 1)
+
+    P = 40
+    kc, vc = lib.la_window_cache(rk[:, :, :P].contiguous(), v[:, :, :P].contiguous().cuda(), W, sinks=S)
+    _, st = lib.la_recurrence_forward(x[:, :P].contiguous(), alpha[:, :P].contiguous().cuda())
+    for t in range(P, N):
+        pos = torch.full((B,), t, dtype=torch.int32, device="cuda")
+        tq, tk = lib.la_rotary_forward(q[:, :, t].contiguous().cuda(), k[:, :, t].contiguous().cuda(), positions=pos)
+        ot = lib.la_window_decode_step(kc, vc, tq, tk, v[:, :, t].contiguous().cuda(), pos, W, sinks=S)
+        ht = lib.la_recurrence_step(st, ot.view(B, D), alpha[:, t].contiguous().cuda())
+        assert float((ht - h[:, t]).abs().max()) < 1e-5
