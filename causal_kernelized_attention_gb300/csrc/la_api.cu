@@ -667,7 +667,10 @@ la_status la_get_device_status(la_stream_t stream)
     if (st != LA_OK) return st;
     st = tc_backward_read_status((cudaStream_t)stream, &bw_bits);
     if (st != LA_OK) return st;
-    return ((bits | nc_bits | fv_bits | cc_bits | cl_bits | bw_bits) & kStatusTimeout) ? LA_ERR_TIMEOUT : LA_OK;
+    unsigned wn_bits = 0;
+    st = tc_window_read_status((cudaStream_t)stream, &wn_bits);
+    if (st != LA_OK) return st;
+    return ((bits | nc_bits | fv_bits | cc_bits | cl_bits | bw_bits | wn_bits) & kStatusTimeout) ? LA_ERR_TIMEOUT : LA_OK;
 }
 
 int la_version(void) { return 100; }

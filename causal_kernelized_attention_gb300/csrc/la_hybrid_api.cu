@@ -205,7 +205,7 @@ la_status la_window_forward(const void *q, const void *k, const void *v, void *o
     if (!q || !k || !v || !o || !lse) return LA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(lens, 4))
         return LA_ERR_MISALIGNED;
-    if (!supported_dim(d)) return LA_ERR_UNSUPPORTED;
+    if (!supported_dim(d) || (long long)B * Hq > 0x7fffffff || (long long)B * Hk > 0x7fffffff) return LA_ERR_UNSUPPORTED;
     const size_t rows = (size_t)B * Hq * Nq, keys = (size_t)B * Hk * Nk, e = d * elem(dtype);
     const Span out[] = {{o, rows * e}, {lse, rows * 4}};
     const Span in[] = {{q, rows * e}, {k, keys * e}, {v, keys * e}, {lens, (size_t)B * 4}};
@@ -218,7 +218,7 @@ la_status la_window_forward(const void *q, const void *k, const void *v, void *o
     p.scale = scale;
     p.dtype = dtype;
     p.stream = (cudaStream_t)stream;
-    return window_forward_simt(p);
+    return dtype == LA_BF16 ? window_forward_tc(p) : window_forward_simt(p);
 }
 
 la_status la_window_backward(const void *q, const void *k, const void *v, const void *o, const float *lse,
@@ -236,7 +236,7 @@ la_status la_window_backward(const void *q, const void *k, const void *v, const 
         (rows_any && (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 16) ||
                       !aligned(dout, 16) || !aligned(dq, 16) || !aligned(lens, 4))))
         return LA_ERR_MISALIGNED;
-    if (!supported_dim(d)) return LA_ERR_UNSUPPORTED;
+    if (!supported_dim(d) || (long long)B * Hq > 0x7fffffff || (long long)B * Hk > 0x7fffffff) return LA_ERR_UNSUPPORTED;
     const size_t rows = (size_t)B * Hq * Nq, keys = (size_t)B * Hk * Nk, e = d * elem(dtype);
     const Span out[] = {{dq, rows * e}, {dk, keys * e}, {dv, keys * e}};
     const Span in[] = {{q, rows * e}, {k, keys * e}, {v, keys * e}, {o, rows * e}, {lse, rows * 4}, {dout, rows * e},

@@ -44,11 +44,11 @@ struct Slots {
 };
 
 // Joins the partial results of `parts` warps in each of the cluster's CTAs: rows of G heads,
-// m (log2 units) and l per row, then the unnormalised outputs.  Partials lie in every CTA's
+// m (the largest score before scaling by f, which turns it into log2 units) and l per row, then the unnormalised outputs.  Partials lie in every CTA's
 // shared memory at the same place.
 template <typename T, int D>
 __device__ __forceinline__ void join(const float *m, const float *l, const float *acc, int parts, int mstride, int G,
-                                     int rows, T *o, uint32_t S, uint32_t rank)
+                                     int rows, float f, T *o, uint32_t S, uint32_t rank)
 {
     const uint32_t ma = smem_u32(m), la_ = smem_u32(l), aa = smem_u32(acc);
     for (int e = rank * blockDim.x + threadIdx.x; e < rows * (D / 4); e += S * blockDim.x) {
@@ -63,10 +63,10 @@ __device__ __forceinline__ void join(const float *m, const float *l, const float
             for (int w = 0; w < parts; ++w) {
                 const float mw = ld_dsmem_f32(mapa_shared(ma + 4 * (w * mstride + r), s));
                 if (mw == -INFINITY) continue;  // no slots
-                const float f = exp2f(mw - top);
-                sum = fmaf(f, ld_dsmem_f32(mapa_shared(la_ + 4 * (w * mstride + r), s)), sum);
+                const float wt = exp2f((mw - top) * f);
+                sum = fmaf(wt, ld_dsmem_f32(mapa_shared(la_ + 4 * (w * mstride + r), s)), sum);
                 const float4 y = ld_dsmem_f4(mapa_shared(aa + 4 * ((w * G + r) * D + c), s));
-                x.x = fmaf(f, y.x, x.x); x.y = fmaf(f, y.y, x.y); x.z = fmaf(f, y.z, x.z); x.w = fmaf(f, y.w, x.w);
+                x.x = fmaf(wt, y.x, x.x); x.y = fmaf(wt, y.y, x.y); x.z = fmaf(wt, y.z, x.z); x.w = fmaf(wt, y.w, x.w);
             }
         const float inv = 1.f / sum;
         T *dst = o + (size_t)r * D + c;
@@ -115,12 +115,11 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_f32_kernel(const Args 
         if (g < rows)
             q[g] = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) +
                                                      ((size_t)b * a.Hq + hk * group + g0 + g) * D + c);
-        const float f = a.scale * kLog2e;
-        q[g].x *= f; q[g].y *= f; q[g].z *= f; q[g].w *= f;
         m[g] = -INFINITY;
         l[g] = 0.f;
         acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    const float f = a.scale * kLog2e;
     const int workers = (int)S * kSimtWarps, me = (int)rank * kSimtWarps + warp;
     for (long long j0 = (long long)me * KW * U; j0 < sl.count; j0 += (long long)workers * KW * U) {
         float4 kx[U], vx[U];
@@ -154,13 +153,13 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_f32_kernel(const Args 
 #pragma unroll
             for (int u = 0; u < U; ++u) top = fmaxf(top, s[u]);
             const float safe = top == -INFINITY ? 0.f : top;
-            const float keep = exp2f(m[g] - safe);
+            const float keep = exp2f((m[g] - safe) * f);
             m[g] = top;
             l[g] *= keep;
             acc[g].x *= keep; acc[g].y *= keep; acc[g].z *= keep; acc[g].w *= keep;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float p = exp2f(s[u] - safe);
+                const float p = exp2f((s[u] - safe) * f);
                 l[g] += p;
                 acc[g].x = fmaf(p, vx[u].x, acc[g].x);
                 acc[g].y = fmaf(p, vx[u].y, acc[g].y);
@@ -175,9 +174,9 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_f32_kernel(const Args 
         float top = m[g];
 #pragma unroll
         for (int d = LK; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float f = m[g] == -INFINITY ? 0.f : exp2f(m[g] - top);
-        float ls = l[g] * f;
-        float4 x = make_float4(acc[g].x * f, acc[g].y * f, acc[g].z * f, acc[g].w * f);
+        const float wt = m[g] == -INFINITY ? 0.f : exp2f((m[g] - top) * f);
+        float ls = l[g] * wt;
+        float4 x = make_float4(acc[g].x * wt, acc[g].y * wt, acc[g].z * wt, acc[g].w * wt);
 #pragma unroll
         for (int d = LK; d < 32; d *= 2) {
             ls += __shfl_xor_sync(0xffffffffu, ls, d);
@@ -196,7 +195,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_f32_kernel(const Args 
         cluster_sync_all();
     else
         __syncthreads();
-    join<float, D>(sm_m, sm_l, sm_acc, kSimtWarps, G, G, rows, o, S, rank);
+    join<float, D>(sm_m, sm_l, sm_acc, kSimtWarps, G, G, rows, f, o, S, rank);
     if (S > 1) cluster_sync_all();  // no CTA leaves while its shared memory is read
 }
 
@@ -345,8 +344,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32) decode_bf16_kernel(const Args 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const bool in = j0 + 8 * t + 2 * c + e < sl.count;
-                s[t][e] = in ? s[t][e] * f : -INFINITY;
-                s[t][2 + e] = in ? s[t][2 + e] * f : -INFINITY;
+                s[t][e] = in ? s[t][e] : -INFINITY;
+                s[t][2 + e] = in ? s[t][2 + e] : -INFINITY;
                 t0 = fmaxf(t0, s[t][e]);
                 t1 = fmaxf(t1, s[t][2 + e]);
             }
@@ -356,7 +355,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32) decode_bf16_kernel(const Args 
             t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
         }
         if (__any_sync(0xffffffffu, t0 > m0 || t1 > m1)) {
-            const float k0 = t0 == -INFINITY ? 1.f : exp2f(m0 - t0), k1 = t1 == -INFINITY ? 1.f : exp2f(m1 - t1);
+            const float k0 = t0 == -INFINITY ? 1.f : exp2f((m0 - t0) * f), k1 = t1 == -INFINITY ? 1.f : exp2f((m1 - t1) * f);
             l0 *= k0;
             l1 *= k1;
 #pragma unroll
@@ -376,7 +375,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32) decode_bf16_kernel(const Args 
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float z = h ? z1 : z0;
-                const float p0 = exp2f(s[t][2 * h] - z), p1 = exp2f(s[t][2 * h + 1] - z);
+                const float p0 = exp2f((s[t][2 * h] - z) * f), p1 = exp2f((s[t][2 * h + 1] - z) * f);
                 if (h) l1 += p0 + p1; else l0 += p0 + p1;
                 const __nv_bfloat162 x = __floats2bfloat162_rn(p0, p1);
                 hi[2 * t + h] = *reinterpret_cast<const uint32_t *>(&x);
@@ -436,7 +435,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32) decode_bf16_kernel(const Args 
         cluster_sync_all();
     else
         __syncthreads();
-    join<__nv_bfloat16, D>(sm.m, sm.l, reinterpret_cast<const float *>(smem_raw), kMmaWarps, kRows, kRows, rows, o, S, rank);
+    join<__nv_bfloat16, D>(sm.m, sm.l, reinterpret_cast<const float *>(smem_raw), kMmaWarps, kRows, kRows, rows, f, o, S, rank);
     if (S > 1) cluster_sync_all();  // no CTA leaves while its shared memory is read
 }
 
