@@ -272,7 +272,7 @@ la_status la_window_backward(const void *q, const void *k, const void *v, const 
         base = scratch.ptr;
     }
     p.delta = static_cast<float *>(base);
-    return window_backward_simt(p);
+    return dtype == LA_BF16 ? window_backward_tc(p) : window_backward_simt(p);
 }
 
 la_status la_window_cache(const void *k, const void *v, void *kc, void *vc, const int *lens, int B, int Hk, int N,

@@ -125,6 +125,7 @@ la_status tc_chunks_read_status(cudaStream_t s, unsigned *bits);
 la_status tc_cluster_read_status(cudaStream_t s, unsigned *bits);
 la_status tc_backward_read_status(cudaStream_t s, unsigned *bits);
 la_status tc_window_read_status(cudaStream_t s, unsigned *bits);
+la_status tc_window_bwd_read_status(cudaStream_t s, unsigned *bits);
 
 // Failure-detection test hooks (la_test_set_wait_limit_ns, la_test_drop_publication):
 // the limit of the chunk-parallel causal kernel's bounded waits (2 s unless a test
@@ -188,8 +189,9 @@ struct WindowProblem {
 };
 la_status window_forward_simt(const WindowProblem &p);
 la_status window_backward_simt(const WindowProblem &p);
-// The same on the tensor cores (la_tc_window.cu): bf16.
+// The same on the tensor cores (la_tc_window.cu, la_tc_window_bwd.cu): bf16.
 la_status window_forward_tc(const WindowProblem &p);
+la_status window_backward_tc(const WindowProblem &p);
 
 // The ring cache and the decode step (la_window_decode.cu).
 struct WindowDecodeProblem {

@@ -380,8 +380,8 @@ inline la_status bind_thread_context()
     return LA_OK;
 }
 
-// [BH, N, D] bf16 as a 3-D tensor (D, N, BH); box = 64 columns x 128 rows, 128-byte swizzle.
-inline la_status make_map(CUtensorMap *m, const void *ptr, int BH, int N, int D)
+// [BH, N, D] bf16 as a 3-D tensor (D, N, BH); box = 64 columns x `rows` rows, 128-byte swizzle.
+inline la_status make_map(CUtensorMap *m, const void *ptr, int BH, int N, int D, int rows = kC)
 {
     EncodeTiledFn enc;
     la_status st = encode_fn(&enc);
@@ -389,7 +389,7 @@ inline la_status make_map(CUtensorMap *m, const void *ptr, int BH, int N, int D)
     if (st != LA_OK) return st;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)BH};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)N * D * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)kC, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -20,28 +20,21 @@
 //
 // The weights' rounding to bf16 (2^-9 relative each, independent) enters the output like the
 // rounding of the output itself; sums, maxima and the accumulator are fp32.
-#include <math.h>
-
-#include "la_tc_common.cuh"
-#include "la_window.cuh"
+#include "la_tc_window.cuh"
 
 namespace la {
 namespace {
 
-using namespace sm100;
-using namespace tc;
 using namespace window;
 
 static __device__ unsigned g_win_status;
 
-constexpr int kT = 128;  // rows and keys of a tile
+constexpr int kT = kRows;  // rows and keys of a tile
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 320;
 constexpr int kStages = 2;
 constexpr uint32_t kTmemCols = 512;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;  // log2 units a maximum may grow before the output is rescaled
-constexpr uint64_t kDrainNs = 100000000ull;
 
 template <int DT>
 struct Smem {
@@ -55,21 +48,6 @@ struct Smem {
     int abort;
 };
 
-struct Params {
-    float *lse;
-    const int *lens;
-    int Hq, Hk, Nq, Nk, window, sinks, d;
-    int units;   // CTAs per (entry, key head)
-    int pairs;   // 1: the two tiles are the same rows of heads 2i, 2i + 1 of the group; 0: neighbouring rows
-    float scale;
-};
-
-__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity)
-{
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < kDrainNs) {
-    }
-}
 __device__ __forceinline__ bool wait_b(int *abort_flag, uint64_t *bar, uint32_t parity)
 {
     return wait_bar(&g_win_status, abort_flag, bar, parity);
@@ -78,63 +56,6 @@ __device__ __forceinline__ bool wait_w(int *abort_flag, uint64_t *bar, uint32_t 
 {
     return wait_bar_warp(&g_win_status, abort_flag, bar, parity);
 }
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// This CTA's two query tiles and the key tiles either of them reaches.
-struct Work {
-    int b, hk, h[2], t0[2], n, off;
-    KeyTiles kt[2];
-    int sink_end, begin, end;
-    __device__ __forceinline__ static KeyTiles keys(const Params &p, int t0, int n, int off)
-    {
-        return KeyTiles(t0 + off, t0 < p.Nq ? min(t0 + kT, p.Nq) - 1 + off : t0 + off - 1, p.window, p.sinks, n, kT);
-    }
-    __device__ __forceinline__ Work(const Params &p, int cta)
-        : b(cta / p.units / p.Hk), hk(cta / p.units % p.Hk), n(valid(p.lens, b, p.Nk)), off(p.Nk - p.Nq),
-          kt{{0, -1, 1, 0, 0, kT}, {0, -1, 1, 0, 0, kT}}
-    {
-        const int u = cta % p.units, group = p.Hq / p.Hk, tiles = (p.Nq + kT - 1) / kT;
-        if (p.pairs) {  // unit = (row tile, head pair), pairs of one row tile together
-            const int hp = u % (group / 2);
-            h[0] = hk * group + 2 * hp;
-            h[1] = h[0] + 1;
-            t0[0] = t0[1] = u / (group / 2) * kT;
-        } else {
-            const int duos = (tiles + 1) / 2;
-            h[0] = h[1] = hk * group + u / duos;
-            t0[0] = u % duos * 2 * kT;
-            t0[1] = t0[0] + kT;
-        }
-        kt[0] = keys(p, t0[0], n, off);
-        kt[1] = keys(p, t0[1], n, off);
-        sink_end = max(kt[0].sink_end, kt[1].sink_end);
-        const bool e0 = kt[0].count() == 0, e1 = kt[1].count() == 0;
-        begin = max(e0 ? kt[1].begin : e1 ? kt[0].begin : min(kt[0].begin, kt[1].begin), sink_end);
-        end = max(max(kt[0].end, kt[1].end), begin);
-    }
-    __device__ __forceinline__ int count() const { return sink_end + (end - begin); }
-    __device__ __forceinline__ int tile(int u) const { return u < sink_end ? u : begin + (u - sink_end); }
-    __device__ __forceinline__ bool reaches(int s, int tile) const
-    {
-        return tile < kt[s].sink_end || (tile >= kt[s].begin && tile < kt[s].end);
-    }
-};
-
-// Bits c of the 32 keys from j on that a row at position p sees.
-__device__ __forceinline__ uint32_t seen_bits(int p, int j, int window, int sinks, int n)
-{
-    if (p >= n) return 0u;
-    const int hi = min(p - j, 31), lo = max(p - window + 1 - j, 0), sk = min(sinks - 1 - j, hi);
-    const uint32_t up = hi < 0 ? 0u : 0xffffffffu >> (31 - hi);
-    const uint32_t win = lo > 31 ? 0u : up & (0xffffffffu << lo);
-    return win | (sk < 0 ? 0u : 0xffffffffu >> (31 - sk));
-}
-
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 1)
 window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -180,7 +101,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     griddep_launch_dependents();
     const uint32_t tmem = sm.tmem_base;
     int *abort_flag = &sm.abort;
-    const Work w(prm, (int)blockIdx.x);
+    const Work<kT> w(prm, (int)blockIdx.x);
     const int U = w.count();
 
     if (warp == kTmaWarp) {
@@ -414,16 +335,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 template <int DT>
 la_status forward(const WindowProblem &p)
 {
-    const int group = p.Hq / p.Hk, tiles = ceil_div(p.Nq, kT);
-    Params prm;
-    prm.lse = p.lse;
-    prm.lens = p.lens;
-    prm.Hq = p.Hq; prm.Hk = p.Hk; prm.Nq = p.Nq; prm.Nk = p.Nk;
-    prm.window = p.window; prm.sinks = p.sinks; prm.d = p.d;
-    prm.scale = p.scale;
-    // Two heads of a group reach exactly the same key tiles; neighbouring rows all but one.
-    prm.pairs = group % 2 == 0;
-    prm.units = prm.pairs ? tiles * (group / 2) : (tiles + 1) / 2 * group;
+    const Params prm = params_of(p);
     const long long ctas = (long long)p.B * p.Hk * prm.units;
     if (ctas > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
     CUtensorMap mq, mk, mv, mo;

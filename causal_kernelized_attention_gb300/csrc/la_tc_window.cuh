@@ -1,0 +1,115 @@
+// Shared pieces of the tensor-core window-attention kernels (la_tc_window.cu,
+// la_tc_window_bwd.cu): a CTA's pair of query tiles and the key tiles they reach, the mask
+// as bits, and small device helpers.
+#pragma once
+
+#include <math.h>
+
+#include "la_tc_common.cuh"
+#include "la_window.cuh"
+
+namespace la {
+namespace window {
+
+using namespace sm100;
+using namespace tc;
+
+constexpr int kRows = 128;  // rows of a query tile
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr uint64_t kDrainNs = 100000000ull;
+
+struct Params {
+    float *lse;        // forward: written; backward: read
+    float *delta;      // backward: dO . o per row
+    const void *o;     // backward
+    const int *lens;
+    int Hq, Hk, Nq, Nk, window, sinks, d;
+    int units;   // CTAs per (entry, key head)
+    int pairs;   // 1: the two tiles are the same rows of heads 2i, 2i + 1 of the group; 0: neighbouring rows
+    float scale;
+};
+
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < kDrainNs) {
+    }
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// This CTA's two query tiles and the key tiles either of them reaches.
+template <int KT>  // keys of a tile
+struct Work {
+    int b, hk, h[2], t0[2], n, off;
+    KeyTiles kt[2];
+    int sink_end, begin, end;
+    __device__ __forceinline__ static KeyTiles keys(const Params &p, int t0, int n, int off)
+    {
+        return KeyTiles(t0 + off, t0 < p.Nq ? min(t0 + kRows, p.Nq) - 1 + off : t0 + off - 1, p.window, p.sinks, n, KT);
+    }
+    __device__ __forceinline__ Work(const Params &p, int cta)
+        : b(cta / p.units / p.Hk), hk(cta / p.units % p.Hk), n(valid(p.lens, b, p.Nk)), off(p.Nk - p.Nq),
+          kt{{0, -1, 1, 0, 0, KT}, {0, -1, 1, 0, 0, KT}}
+    {
+        const int u = cta % p.units, group = p.Hq / p.Hk, tiles = (p.Nq + kRows - 1) / kRows;
+        if (p.pairs) {  // unit = (row tile, head pair), pairs of one row tile together
+            const int hp = u % (group / 2);
+            h[0] = hk * group + 2 * hp;
+            h[1] = h[0] + 1;
+            t0[0] = t0[1] = u / (group / 2) * kRows;
+        } else {
+            const int duos = (tiles + 1) / 2;
+            h[0] = h[1] = hk * group + u / duos;
+            t0[0] = u % duos * 2 * kRows;
+            t0[1] = t0[0] + kRows;
+        }
+        kt[0] = keys(p, t0[0], n, off);
+        kt[1] = keys(p, t0[1], n, off);
+        sink_end = max(kt[0].sink_end, kt[1].sink_end);
+        const bool e0 = kt[0].count() == 0, e1 = kt[1].count() == 0;
+        begin = max(e0 ? kt[1].begin : e1 ? kt[0].begin : min(kt[0].begin, kt[1].begin), sink_end);
+        end = max(max(kt[0].end, kt[1].end), begin);
+    }
+    __device__ __forceinline__ int count() const { return sink_end + (end - begin); }
+    __device__ __forceinline__ int tile(int u) const { return u < sink_end ? u : begin + (u - sink_end); }
+    __device__ __forceinline__ bool reaches(int s, int tile) const
+    {
+        return tile < kt[s].sink_end || (tile >= kt[s].begin && tile < kt[s].end);
+    }
+};
+
+// Bits c of the 32 keys from j on that a row at position p sees.
+__device__ __forceinline__ uint32_t seen_bits(int p, int j, int window, int sinks, int n)
+{
+    if (p >= n) return 0u;
+    const int hi = min(p - j, 31), lo = max(p - window + 1 - j, 0), sk = min(sinks - 1 - j, hi);
+    const uint32_t up = hi < 0 ? 0u : 0xffffffffu >> (31 - hi);
+    const uint32_t win = lo > 31 ? 0u : up & (0xffffffffu << lo);
+    return win | (sk < 0 ? 0u : 0xffffffffu >> (31 - sk));
+}
+
+// The launch's sizes; the two tiles of a CTA are heads of one group where groups are even
+// (they reach exactly the same key tiles), else neighbouring rows (all but one).
+inline Params params_of(const WindowProblem &p)
+{
+    const int group = p.Hq / p.Hk, tiles = ceil_div(p.Nq, kRows);
+    Params prm;
+    prm.lse = p.lse;
+    prm.delta = p.delta;
+    prm.o = p.o;
+    prm.lens = p.lens;
+    prm.Hq = p.Hq; prm.Hk = p.Hk; prm.Nq = p.Nq; prm.Nk = p.Nk;
+    prm.window = p.window; prm.sinks = p.sinks; prm.d = p.d;
+    prm.scale = p.scale;
+    prm.pairs = group % 2 == 0;
+    prm.units = prm.pairs ? tiles * (group / 2) : (tiles + 1) / 2 * group;
+    return prm;
+}
+
+}  // namespace window
+}  // namespace la

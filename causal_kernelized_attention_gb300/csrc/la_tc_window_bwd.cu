@@ -1,0 +1,591 @@
+// Window attention backward on the tensor cores: bf16, d <= 128 on tiles of 64 or 128
+// columns.  Two kernels, so that every gradient is summed by one CTA in a fixed order:
+//
+//   dq      (a CTA: two query tiles of 128 rows, as the forward; key tiles of 64)
+//           D = dO . o per row (kept for the second kernel), S = Q K^T, dP = dO V^T,
+//           dS = P (dP - D), dQ += dS K;                              3 products a tile
+//   dk, dv  (a CTA: 128 keys; query tiles of 64 rows, of every head of the group)
+//           S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q;   4 products a tile
+//
+// with P = exp(scale S - lse); scale multiplies dS once, in the epilogues.  A product's left
+// operand comes from TMEM where it is P or dS: each is rounded to bf16 and written over the
+// columns it was computed from, so nothing of the score matrices reaches shared memory.
+// Two groups of four warps work in turn, as in the forward: while one forms P and dS of its
+// tile (a thread a row), the tensor core runs the products of the other's.  In dk, dv a
+// thread owns a key, for which the visible queries are one interval.  The rounding of dS
+// (2^-9 relative, like P's) is the size of the gradients' own; sums are fp32.
+//
+// Rows and keys of padding: their P and dS are 0, and what a product multiplies by them is
+// zeroed in shared memory (0 times a NaN is not 0).
+#include "la_tc_window.cuh"
+
+namespace la {
+namespace {
+
+using namespace window;
+
+static __device__ unsigned g_winb_status;
+
+constexpr int kHalf = 64;  // keys (dq) or query rows (dk, dv) of a streamed tile
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 320;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kHalfBox = kHalf * 128;  // one [64 rows x 64 bf16] swizzled box: 8 KB
+constexpr uint32_t tS = 0, tP = 128, tG = 256;  // S_s at 64 s, dP_s at 128 + 64 s, gradients from 256
+
+__device__ __forceinline__ bool wait_b(int *abort_flag, uint64_t *bar, uint32_t parity)
+{
+    return wait_bar(&g_winb_status, abort_flag, bar, parity);
+}
+__device__ __forceinline__ bool wait_w(int *abort_flag, uint64_t *bar, uint32_t parity)
+{
+    return wait_bar_warp(&g_winb_status, abort_flag, bar, parity);
+}
+// Descriptors of a 64-row tile.
+__device__ __forceinline__ uint64_t kmajor_half(uint32_t tile, int kk)
+{
+    return desc_sw128(tile + (kk >> 2) * kHalfBox + (kk & 3) * 32, 16, 1024);
+}
+__device__ __forceinline__ uint64_t mnmajor_half(uint32_t tile, int kk) { return mnmajor(tile, kk, kHalfBox); }
+
+// Zeroes rows from r0 on of a 64-row tile, by one warp, visible to the tensor core.
+template <int DT>
+__device__ __forceinline__ void zero_rows(uint8_t *tile, int r0, int lane)
+{
+    r0 = max(r0, 0);
+    for (int e = lane; e < (kHalf - r0) * (DT / 8); e += 32) {
+        const int row = r0 + e / (DT / 8), ch = e % (DT / 8);
+        *reinterpret_cast<uint4 *>(tile + (ch >> 3) * kHalfBox + row * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// Row r of a 128-row output tile: 16 fp32 columns from x of TMEM address ta, times f, as bf16.
+__device__ __forceinline__ void stage16(uint8_t *tile, uint32_t ta, int r, int x, float f, bool some)
+{
+    uint32_t o[16], pk[8];
+    tmem_ld16(ta + x, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        pk[e] = some ? pack_bf16(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f) : 0u;
+    uint8_t *row = tile + x / 64 * kBox + r * 128;
+    const int ch = (x & 63) >> 3;
+    *reinterpret_cast<uint4 *>(row + ((ch ^ (r & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    *reinterpret_cast<uint4 *>(row + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+}
+
+// ---------------------------------------------------------------- dq
+constexpr int kKeyStages = 3;
+
+template <int DT>
+struct DqSmem {
+    static constexpr uint32_t kTile = kRows * DT * 2, kStage = kHalf * DT * 2;
+    uint8_t q[2][kTile];  // then dq, staged
+    uint8_t go[2][kTile];
+    uint8_t k[kKeyStages][kStage];
+    uint8_t v[kKeyStages][kStage];
+    uint64_t q_full[2], s_full[2], ds_full[2], g_full[2];
+    uint64_t k_full[kKeyStages], k_empty[kKeyStages], v_full[kKeyStages], v_empty[kKeyStages], drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 1)
+window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+             const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+             const __grid_constant__ CUtensorMap map_dq, const Params prm)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    DqSmem<DT> &sm = *reinterpret_cast<DqSmem<DT> *>(smem_raw);
+    constexpr uint32_t kTile = DqSmem<DT>::kTile, kStage = DqSmem<DT>::kStage;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sm.q_full[s], 1);
+            mbar_init(&sm.s_full[s], 1);
+            mbar_init(&sm.ds_full[s], 128);
+            mbar_init(&sm.g_full[s], 1);
+        }
+        for (int i = 0; i < kKeyStages; ++i) {
+            mbar_init(&sm.k_full[i], 1);
+            mbar_init(&sm.k_empty[i], 1);
+            mbar_init(&sm.v_full[i], 1);
+            mbar_init(&sm.v_empty[i], 1);
+        }
+        mbar_init(&sm.drain, 1);
+        sm.abort = (smem_u32(smem_raw) & 1023u) == 0 ? 0 : 1;
+        if (sm.abort) atomicOr(&g_winb_status, kStatusTimeout);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&sm.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t tmem = sm.tmem_base;
+    int *abort_flag = &sm.abort;
+    const Work<kHalf> w(prm, (int)blockIdx.x);
+    const int U = w.count();
+
+    if (warp == kTmaWarp) {
+        if (lane == 0 && !aborted(abort_flag)) {
+            const int kz = w.b * prm.Hk + w.hk;
+            int loaded = 0;
+            for (int u = 0; u < U; ++u) {
+                const int st = u % kKeyStages, j0 = w.tile(u) * kHalf;
+                const uint32_t ph = (uint32_t)(u / kKeyStages - 1) & 1u;
+                if (u >= kKeyStages && !wait_b(abort_flag, &sm.k_empty[st], ph)) break;
+                mbar_arrive_expect_tx(&sm.k_full[st], kStage);
+#pragma unroll
+                for (int x = 0; x < DT; x += 64)
+                    tma_load_3d(sm.k[st] + x / 64 * kHalfBox, &map_k, &sm.k_full[st], x, j0, kz);
+                if (u == 0)
+                    for (int s = 0; s < 2; ++s)
+                        if (w.kt[s].count() > 0) {
+                            const int z = w.b * prm.Hq + w.h[s];
+                            mbar_arrive_expect_tx(&sm.q_full[s], 2 * kTile);
+#pragma unroll
+                            for (int x = 0; x < DT; x += 64) {
+                                tma_load_3d(sm.q[s] + x / 64 * kBox, &map_q, &sm.q_full[s], x, w.t0[s], z);
+                                tma_load_3d(sm.go[s] + x / 64 * kBox, &map_do, &sm.q_full[s], x, w.t0[s], z);
+                            }
+                        }
+                loaded = u + 1;
+                if (u >= kKeyStages && !wait_b(abort_flag, &sm.v_empty[st], ph)) {
+                    mbar_arrive_expect_tx(&sm.v_full[st], 0);  // completes the phase that drain() waits for
+                    break;
+                }
+                mbar_arrive_expect_tx(&sm.v_full[st], kStage);
+#pragma unroll
+                for (int x = 0; x < DT; x += 64)
+                    tma_load_3d(sm.v[st] + x / 64 * kHalfBox, &map_v, &sm.v_full[st], x, j0, kz);
+            }
+            // no copy may still be writing shared memory when the CTA exits
+            if (loaded > 0)
+                for (int s = 0; s < 2; ++s)
+                    if (w.kt[s].count() > 0) drain(&sm.q_full[s], 0);
+            for (int u = max(loaded - kKeyStages, 0); u < loaded; ++u) {
+                drain(&sm.k_full[u % kKeyStages], (uint32_t)(u / kKeyStages) & 1u);
+                drain(&sm.v_full[u % kKeyStages], (uint32_t)(u / kKeyStages) & 1u);
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        const uint32_t id_s = idesc_bf16_f32(128, kHalf, false, false), id_g = idesc_bf16_f32(128, DT, false, true);
+        int fed[2] = {0, 0};  // tiles of s whose dS has been multiplied
+        bool pending[2] = {false, false}, ok = !aborted(abort_flag);
+        for (int u = 0; ok && u <= U; ++u) {
+            const int st = u % kKeyStages, pst = (u + kKeyStages - 1) % kKeyStages;
+            const uint32_t ph = (uint32_t)(u / kKeyStages) & 1u;
+            if (u < U) {
+                if (!(ok = wait_w(abort_flag, &sm.k_full[st], ph))) break;
+                const int j0 = w.tile(u) * kHalf;
+                if (j0 + kHalf > w.n) zero_rows<DT>(sm.k[st], w.n - j0, lane);
+                if (!(ok = wait_w(abort_flag, &sm.v_full[st], ph))) break;
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (pending[s]) {
+                    if (!(ok = wait_w(abort_flag, &sm.ds_full[s], (uint32_t)fed[s] & 1u))) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t ka = smem_u32(sm.k[pst]);
+#pragma unroll
+                        for (int kk = 0; kk < kHalf / 16; ++kk)
+                            mma_ts(tmem + tG + s * DT, tmem + tS + s * kHalf + kk * 8, mnmajor_half(ka, kk), id_g,
+                                   fed[s] > 0 || kk > 0);
+                    }
+                    ++fed[s];
+                    pending[s] = false;
+                }
+                if (u < U && w.reaches(s, w.tile(u))) {
+                    if (fed[s] == 0 && !(ok = wait_w(abort_flag, &sm.q_full[s], 0))) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t qa = smem_u32(sm.q[s]), ga = smem_u32(sm.go[s]);
+                        const uint32_t ka = smem_u32(sm.k[st]), va = smem_u32(sm.v[st]);
+#pragma unroll
+                        for (int kk = 0; kk < DT / 16; ++kk)
+                            mma_ss(tmem + tS + s * kHalf, kmajor(qa, kk), kmajor_half(ka, kk), id_s, kk > 0);
+#pragma unroll
+                        for (int kk = 0; kk < DT / 16; ++kk)
+                            mma_ss(tmem + tP + s * kHalf, kmajor(ga, kk), kmajor_half(va, kk), id_s, kk > 0);
+                        mma_commit(&sm.s_full[s]);
+                    }
+                    pending[s] = true;
+                }
+            }
+            if (ok && lane == 0) {
+                if (u < U) mma_commit(&sm.v_empty[st]);
+                if (u > 0) mma_commit(&sm.k_empty[pst]);
+                if (u == U)
+                    for (int s = 0; s < 2; ++s) mma_commit(&sm.g_full[s]);
+            }
+            __syncwarp();
+        }
+        if (lane == 0) {
+            mma_commit(&sm.drain);  // every MMA issued completes before TMEM is freed
+            drain(&sm.drain, 0);
+        }
+        __syncwarp();
+    } else {
+        const int s = warp >> 2, r = 32 * (warp & 3) + lane;
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t ts = tl + tS + s * kHalf, tp = tl + tP + s * kHalf, tg = tl + tG + s * DT;
+        const int t = w.t0[s] + r, p = t + w.off, p_first = w.t0[s] + w.off;
+        const size_t row = ((size_t)w.b * prm.Hq + w.h[s]) * prm.Nq + t;
+        const bool live = t < prm.Nq && p < w.n;
+        const float c = prm.scale * kLog2e;
+        bool ok = !aborted(abort_flag);
+        int done = 0;
+        // the row's lse in units of the raw scores, and its D
+        const float base = live ? __ldg(prm.lse + row) / prm.scale : 0.f;
+        float delta = 0.f;
+        if (ok && w.kt[s].count() > 0 && (ok = wait_w(abort_flag, &sm.q_full[s], 0)) && live) {
+            const uint4 *op = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(prm.o) + row * prm.d);
+            for (int ch = 0; ch < prm.d / 8; ++ch) {
+                const uint4 x = __ldg(op + ch);
+                const uint4 y = *reinterpret_cast<const uint4 *>(sm.go[s] + (ch >> 3) * kBox + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    delta = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), delta);
+                    delta = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), delta);
+                }
+            }
+        }
+        if (t < prm.Nq) prm.delta[row] = delta;
+        for (int u = 0; ok && u < U; ++u) {
+            const int tile = w.tile(u), j0 = tile * kHalf;
+            if (!w.reaches(s, tile)) continue;
+            if (!(ok = wait_w(abort_flag, &sm.s_full[s], (uint32_t)done & 1u))) break;
+            tc_fence_after();
+            const bool whole = j0 + kHalf - 1 <= p_first && p_first + kRows - 1 < w.n &&
+                               (p_first + kRows - 1 - j0 < prm.window || j0 + kHalf <= prm.sinks);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                uint32_t a[32], b[32], pk[16];
+                tmem_ld32(ts + 32 * g, a);
+                tmem_ld32(tp + 32 * g, b);
+                tmem_ld_wait();
+                const uint32_t bits = whole ? 0xffffffffu : seen_bits(p, j0 + 32 * g, prm.window, prm.sinks, w.n);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    a[e] = __float_as_uint(ex2((__uint_as_float(a[e]) - base) * c) * (__uint_as_float(b[e]) - delta));
+                if (!whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!((bits >> e) & 1u)) a[e] = 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
+                tmem_st16(ts + 16 * g, pk);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&sm.ds_full[s]);
+            ++done;
+        }
+        if (ok) ok = U == 0 || wait_w(abort_flag, &sm.g_full[s], 0);
+        if (ok && w.t0[s] < prm.Nq) {
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < DT; x += 16) stage16(sm.q[s], tg, r, x, prm.scale, live && done > 0);
+            fence_proxy_async_smem();
+        }
+        named_bar_sync(1 + s, 128);
+        if (ok && w.t0[s] < prm.Nq && (warp & 3) == 0 && lane == 0) {
+#pragma unroll
+            for (int x = 0; x < DT; x += 64)
+                tma_store_3d(&map_dq, sm.q[s] + x / 64 * kBox, x, w.t0[s], w.b * prm.Hq + w.h[s]);
+            tma_store_commit();
+            tma_store_wait_all();
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------- dk, dv
+constexpr int kRowStages = 5;
+
+template <int DT>
+struct DkvSmem {
+    static constexpr uint32_t kTile = kRows * DT * 2, kStage = kHalf * DT * 2;
+    uint8_t k[kTile];  // then dk, staged
+    uint8_t v[kTile];  // then dv, staged
+    uint8_t q[kRowStages][kStage];
+    uint8_t go[kRowStages][kStage];
+    float base[kRowStages][kHalf], delta[kRowStages][kHalf];
+    uint64_t kv_full, s_full[2], ds_full[2], g_full;
+    uint64_t q_full[kRowStages], q_empty[kRowStages], l_full[kRowStages], drain;
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(DkvSmem<128>) <= 232448, "fits an SM's shared memory");
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 1)
+window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+              const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+              const __grid_constant__ CUtensorMap map_dk, const __grid_constant__ CUtensorMap map_dv, const Params prm)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    DkvSmem<DT> &sm = *reinterpret_cast<DkvSmem<DT> *>(smem_raw);
+    constexpr uint32_t kTile = DkvSmem<DT>::kTile, kStage = DkvSmem<DT>::kStage;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        mbar_init(&sm.kv_full, 1);
+        mbar_init(&sm.g_full, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sm.s_full[s], 1);
+            mbar_init(&sm.ds_full[s], 128);
+        }
+        for (int i = 0; i < kRowStages; ++i) {
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_empty[i], 1);
+            mbar_init(&sm.l_full[i], 32);
+        }
+        mbar_init(&sm.drain, 1);
+        sm.abort = (smem_u32(smem_raw) & 1023u) == 0 ? 0 : 1;
+        if (sm.abort) atomicOr(&g_winb_status, kStatusTimeout);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&sm.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t tmem = sm.tmem_base;
+    int *abort_flag = &sm.abort;
+
+    const int tiles = (prm.Nk + kRows - 1) / kRows, group = prm.Hq / prm.Hk, off = prm.Nk - prm.Nq;
+    const int bh = (int)blockIdx.x / tiles, j0 = (int)blockIdx.x % tiles * kRows, b = bh / prm.Hk, hk = bh % prm.Hk;
+    const int n = valid(prm.lens, b, prm.Nk);
+    const QueryTiles qt(j0, min(j0 + kRows, prm.Nk) - 1, prm.window, prm.sinks, n, off, prm.Nq, kHalf);
+    const int per = qt.end - qt.begin, X = per * group;  // streamed tile x: head x / per of the group
+    const int rows = min(prm.Nq, n - off);               // rows of tokens
+
+    if (warp == kTmaWarp) {
+        bool ok = !aborted(abort_flag) && X > 0;
+        int loaded = 0;
+        if (ok && lane == 0) {
+            mbar_arrive_expect_tx(&sm.kv_full, 2 * kTile);
+#pragma unroll
+            for (int x = 0; x < DT; x += 64) {
+                tma_load_3d(sm.k + x / 64 * kBox, &map_k, &sm.kv_full, x, j0, bh);
+                tma_load_3d(sm.v + x / 64 * kBox, &map_v, &sm.kv_full, x, j0, bh);
+            }
+        }
+        for (int i = 0; ok && i < X; ++i) {
+            const int st = i % kRowStages, t0 = (qt.begin + i % per) * kHalf, z = b * prm.Hq + hk * group + i / per;
+            if (i >= kRowStages && !(ok = wait_w(abort_flag, &sm.q_empty[st], (uint32_t)(i / kRowStages - 1) & 1u))) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sm.q_full[st], 2 * kStage);
+#pragma unroll
+                for (int x = 0; x < DT; x += 64) {
+                    tma_load_3d(sm.q[st] + x / 64 * kHalfBox, &map_q, &sm.q_full[st], x, t0, z);
+                    tma_load_3d(sm.go[st] + x / 64 * kHalfBox, &map_do, &sm.q_full[st], x, t0, z);
+                }
+            }
+            loaded = i + 1;
+#pragma unroll
+            for (int e = lane; e < kHalf; e += 32) {
+                const bool in = t0 + e < rows;
+                const size_t at = (size_t)z * prm.Nq + t0 + e;
+                sm.base[st][e] = in ? __ldcg(prm.lse + at) / prm.scale : 0.f;
+                sm.delta[st][e] = in ? __ldcg(prm.delta + at) : 0.f;
+            }
+            mbar_arrive(&sm.l_full[st]);
+        }
+        if (lane == 0) {  // no copy may still be writing shared memory when the CTA exits
+            if (X > 0 && loaded > 0) drain(&sm.kv_full, 0);
+            for (int i = max(loaded - kRowStages, 0); i < loaded; ++i)
+                drain(&sm.q_full[i % kRowStages], (uint32_t)(i / kRowStages) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        const uint32_t id_s = idesc_bf16_f32(128, kHalf, false, false), id_g = idesc_bf16_f32(128, DT, false, true);
+        const uint32_t ka = smem_u32(sm.k), va = smem_u32(sm.v);
+        bool ok = !aborted(abort_flag) && X > 0;
+        if (ok) ok = wait_w(abort_flag, &sm.kv_full, 0);
+        for (int i = 0; ok && i < X + 2; ++i) {
+            const int s = i & 1, st = i % kRowStages, back = i - 2, bst = (i + kRowStages - 2) % kRowStages;
+            if (back >= 0) {  // the tile of this group before: its P and dS are in TMEM
+                if (!(ok = wait_w(abort_flag, &sm.ds_full[s], (uint32_t)(back >> 1) & 1u))) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t qa = smem_u32(sm.q[bst]), ga = smem_u32(sm.go[bst]);
+#pragma unroll
+                    for (int kk = 0; kk < kHalf / 16; ++kk)
+                        mma_ts(tmem + tG, tmem + tS + s * kHalf + kk * 8, mnmajor_half(ga, kk), id_g, back > 0 || kk > 0);
+#pragma unroll
+                    for (int kk = 0; kk < kHalf / 16; ++kk)
+                        mma_ts(tmem + tG + DT, tmem + tP + s * kHalf + kk * 8, mnmajor_half(qa, kk), id_g,
+                               back > 0 || kk > 0);
+                    mma_commit(&sm.q_empty[bst]);
+                }
+                __syncwarp();
+            }
+            if (i < X) {
+                if (!(ok = wait_w(abort_flag, &sm.q_full[st], (uint32_t)(i / kRowStages) & 1u))) break;
+                const int t0 = (qt.begin + i % per) * kHalf;
+                if (t0 + kHalf > rows) {
+                    zero_rows<DT>(sm.q[st], rows - t0, lane);
+                    zero_rows<DT>(sm.go[st], rows - t0, lane);
+                }
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t qa = smem_u32(sm.q[st]), ga = smem_u32(sm.go[st]);
+#pragma unroll
+                    for (int kk = 0; kk < DT / 16; ++kk)
+                        mma_ss(tmem + tS + s * kHalf, kmajor(ka, kk), kmajor_half(qa, kk), id_s, kk > 0);
+#pragma unroll
+                    for (int kk = 0; kk < DT / 16; ++kk)
+                        mma_ss(tmem + tP + s * kHalf, kmajor(va, kk), kmajor_half(ga, kk), id_s, kk > 0);
+                    mma_commit(&sm.s_full[s]);
+                }
+                __syncwarp();
+            }
+        }
+        if (lane == 0) {
+            if (ok) mma_commit(&sm.g_full);
+            mma_commit(&sm.drain);  // every MMA issued completes before TMEM is freed
+            drain(&sm.drain, 0);
+        }
+        __syncwarp();
+    } else {
+        const int s = warp >> 2, r = 32 * (warp & 3) + lane, j = j0 + r;
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t ts = tl + tS + s * kHalf, tp = tl + tP + s * kHalf;
+        const float c = prm.scale * kLog2e;
+        // positions [j, last] see key j
+        const int last = j >= n ? -1 : j < prm.sinks ? n - 1 : min(n - 1, j + prm.window - 1);
+        bool ok = !aborted(abort_flag);
+        for (int i = s; ok && i < X; i += 2) {
+            const int st = i % kRowStages, p0 = (qt.begin + i % per) * kHalf + off;
+            if (!(ok = wait_w(abort_flag, &sm.l_full[st], (uint32_t)(i / kRowStages) & 1u))) break;
+            if (!(ok = wait_w(abort_flag, &sm.s_full[s], (uint32_t)(i >> 1) & 1u))) break;
+            tc_fence_after();
+            const bool whole = j0 + kRows - 1 <= p0 && p0 + kHalf - 1 < n &&
+                               (p0 + kHalf - 1 - j0 < prm.window || j0 + kRows <= prm.sinks);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                uint32_t a[32], d[32], pk[16];
+                tmem_ld32(ts + 32 * g, a);
+                tmem_ld32(tp + 32 * g, d);
+                tmem_ld_wait();
+                const float4 *bp = reinterpret_cast<const float4 *>(&sm.base[st][32 * g]);
+                const float4 *dp = reinterpret_cast<const float4 *>(&sm.delta[st][32 * g]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float4 x = bp[e], y = dp[e];
+                    const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int i4 = 0; i4 < 4; ++i4) {
+                        const float pr = ex2((__uint_as_float(a[4 * e + i4]) - xs[i4]) * c);
+                        a[4 * e + i4] = __float_as_uint(pr);
+                        d[4 * e + i4] = __float_as_uint(pr * (__uint_as_float(d[4 * e + i4]) - ys[i4]));
+                    }
+                }
+                if (!whole) {
+                    const int lo = max(j - (p0 + 32 * g), 0), hi = min(last - (p0 + 32 * g), 31);
+                    const uint32_t bits = hi < lo || lo > 31 ? 0u : (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!((bits >> e) & 1u)) a[e] = d[e] = 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
+                tmem_st16(ts + 16 * g, pk);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]));
+                tmem_st16(tp + 16 * g, pk);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&sm.ds_full[s]);
+        }
+        if (ok && X > 0) ok = wait_w(abort_flag, &sm.g_full, 0);
+        uint8_t *out = s == 0 ? sm.v : sm.k;  // group 0: dv, group 1: dk
+        if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < DT; x += 16) stage16(out, tl + tG + s * DT, r, x, s == 0 ? 1.f : prm.scale, X > 0);
+            fence_proxy_async_smem();
+        }
+        named_bar_sync(1 + s, 128);
+        if (ok && (warp & 3) == 0 && lane == 0) {
+#pragma unroll
+            for (int x = 0; x < DT; x += 64) tma_store_3d(s == 0 ? &map_dv : &map_dk, out + x / 64 * kBox, x, j0, bh);
+            tma_store_commit();
+            tma_store_wait_all();
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int DT>
+la_status backward(const WindowProblem &p)
+{
+    const Params prm = params_of(p);
+    const long long dq_ctas = (long long)p.B * p.Hk * prm.units, dkv_ctas = (long long)p.B * p.Hk * ceil_div(p.Nk, kRows);
+    if (dq_ctas > 0x7fffffffLL || dkv_ctas > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
+    const int bq = p.B * p.Hq, bk = p.B * p.Hk;
+    CUtensorMap mq, mdo, mk, mv, mqh, mdoh, mkh, mvh, mdq, mdk, mdv;
+    la_status st = make_map(&mq, p.q, bq, p.Nq, p.d);
+    if (st == LA_OK) st = make_map(&mdo, p.dout, bq, p.Nq, p.d);
+    if (st == LA_OK) st = make_map(&mk, p.k, bk, p.Nk, p.d);
+    if (st == LA_OK) st = make_map(&mv, p.v, bk, p.Nk, p.d);
+    if (st == LA_OK) st = make_map(&mqh, p.q, bq, p.Nq, p.d, kHalf);
+    if (st == LA_OK) st = make_map(&mdoh, p.dout, bq, p.Nq, p.d, kHalf);
+    if (st == LA_OK) st = make_map(&mkh, p.k, bk, p.Nk, p.d, kHalf);
+    if (st == LA_OK) st = make_map(&mvh, p.v, bk, p.Nk, p.d, kHalf);
+    if (st == LA_OK) st = make_map(&mdq, p.dq, bq, p.Nq, p.d);
+    if (st == LA_OK) st = make_map(&mdk, p.dk, bk, p.Nk, p.d);
+    if (st == LA_OK) st = make_map(&mdv, p.dv, bk, p.Nk, p.d);
+    if (st == LA_OK) st = ensure_smem((const void *)window_tc_dq<DT>, (int)sizeof(DqSmem<DT>));
+    if (st == LA_OK) st = ensure_smem((const void *)window_tc_dkv<DT>, (int)sizeof(DkvSmem<DT>));
+    if (st != LA_OK) return st;
+    count_launches(2);
+    st = launch_dependent(window_tc_dq<DT>, (unsigned)dq_ctas, kThreads, (int)sizeof(DqSmem<DT>), p.stream, mq, mdo, mkh, mvh,
+                          mdq, prm);
+    if (st != LA_OK) return st;
+    return launch_dependent(window_tc_dkv<DT>, (unsigned)dkv_ctas, kThreads, (int)sizeof(DkvSmem<DT>), p.stream, mqh, mdoh, mk,
+                            mv, mdk, mdv, prm);
+}
+
+}  // namespace
+
+la_status window_backward_tc(const WindowProblem &p)
+{
+    return p.d <= 64 ? backward<64>(p) : backward<128>(p);
+}
+
+la_status tc_window_bwd_read_status(cudaStream_t s, unsigned *bits)
+{
+    unsigned zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_winb_status, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_winb_status, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    return cuda_status(e);
+}
+
+}  // namespace la
