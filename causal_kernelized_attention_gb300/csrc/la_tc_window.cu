@@ -32,7 +32,7 @@ static __device__ unsigned g_win_status;
 constexpr int kT = kRows;  // rows and keys of a tile
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 320;
-constexpr int kStages = 2;
+constexpr int kKStages = 2, kVStages = 3;  // V(u) is used one step after K(u)
 constexpr uint32_t kTmemCols = 512;
 constexpr float kGrow = 8.f;  // log2 units a maximum may grow before the output is rescaled
 
@@ -40,10 +40,10 @@ template <int DT>
 struct Smem {
     static constexpr uint32_t kTile = kT * DT * 2;
     uint8_t q[2][kTile];  // then the outputs, staged
-    uint8_t k[kStages][kTile];
-    uint8_t v[kStages][kTile];
+    uint8_t k[kKStages][kTile];
+    uint8_t v[kVStages][kTile];
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], drain;
+    uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], drain;
     uint32_t tmem_base;
     int abort;
 };
@@ -56,6 +56,62 @@ __device__ __forceinline__ bool wait_w(int *abort_flag, uint64_t *bar, uint32_t 
 {
     return wait_bar_warp(&g_win_status, abort_flag, bar, parity);
 }
+// A row's 128 scores from TMEM, -inf where the row does not see the key.
+__device__ __forceinline__ void load_scores(uint32_t ts, uint32_t (&a)[128], bool whole, int p, int j0, const Params &prm, int n)
+{
+#pragma unroll
+    for (int g = 0; g < 4; ++g) tmem_ld32(ts + 32 * g, reinterpret_cast<uint32_t(&)[32]>(a[32 * g]));
+    tmem_ld_wait();
+    if (!whole) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const uint32_t bits = seen_bits(p, j0 + 32 * g, prm.window, prm.sinks, n);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (!((bits >> e) & 1u)) a[32 * g + e] = 0xff800000u;
+        }
+    }
+}
+
+__device__ __forceinline__ float row_max(const uint32_t (&a)[128])
+{
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int e = 0; e < 64; ++e) mx[e & 3] = max3(mx[e & 3], __uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
+    return max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+}
+
+// exp2((s - m) c) of a row's 128 scores, rounded to bf16 into a[0 .. 63], with the scores'
+// maximum and the weights' sum (two halves).
+__device__ __forceinline__ void weights(uint32_t (&a)[128], float c, float m, float &top, uint64_t &sum)
+{
+    float base = m == -INFINITY ? 0.f : -m * c, past = 0.f;
+    const bool huge = __any_sync(0xffffffffu, fabsf(m) > 0x1p100f && m != -INFINITY);
+    if (huge) {  // m c may overflow: subtract first
+        past = row_max(a);
+        const float z = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int e = 0; e < 128; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) - z);
+        base = 0.f;
+    }
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    const uint64_t c2 = pair(c, c), base2 = pair(base, base);
+    uint64_t sums[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+    for (int e = 0; e < 64; ++e) {
+        const uint32_t s0 = a[2 * e], s1 = a[2 * e + 1];
+        mx[e & 3] = max3(mx[e & 3], __uint_as_float(s0), __uint_as_float(s1));
+        float x, y;
+        split(fma2(pair(s0, s1), c2, base2), x, y);
+        x = ex2(x);
+        y = ex2(y);
+        sums[e & 3] = add2(sums[e & 3], pair(x, y));
+        a[e] = pack_bf16(x, y);
+    }
+    top = huge ? past : max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+    sum = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 1)
 window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -65,7 +121,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     Smem<DT> &sm = *reinterpret_cast<Smem<DT> *>(smem_raw);
     constexpr uint32_t kTile = Smem<DT>::kTile;
     constexpr uint32_t tS = 0, tO = 256;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sm.q_full[s], 1);
@@ -73,9 +129,11 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             mbar_init(&sm.p_full[s], 128);
             mbar_init(&sm.o_full[s], 1);
         }
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kKStages; ++i) {
             mbar_init(&sm.k_full[i], 1);
             mbar_init(&sm.k_empty[i], 1);
+        }
+        for (int i = 0; i < kVStages; ++i) {
             mbar_init(&sm.v_full[i], 1);
             mbar_init(&sm.v_empty[i], 1);
         }
@@ -109,13 +167,13 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const int kz = w.b * prm.Hk + w.hk;
             int loaded = 0;
             for (int u = 0; u < U; ++u) {
-                const int st = u % kStages, j0 = w.tile(u) * kT;
-                const uint32_t ph = (uint32_t)(u / kStages - 1) & 1u;
-                if (u >= kStages && !wait_b(abort_flag, &sm.k_empty[st], ph)) break;
-                mbar_arrive_expect_tx(&sm.k_full[st], kTile);
+                const int ks = u % kKStages, vs = u % kVStages, j0 = w.tile(u) * kT;
+                if (u >= kKStages && !wait_b(abort_flag, &sm.k_empty[ks], (uint32_t)(u / kKStages - 1) & 1u)) break;
+                mbar_arrive_expect_tx(&sm.k_full[ks], kTile);
 #pragma unroll
-                for (int x = 0; x < DT; x += 64) tma_load_3d(sm.k[st] + x / 64 * kBox, &map_k, &sm.k_full[st], x, j0, kz);
+                for (int x = 0; x < DT; x += 64) tma_load_3d(sm.k[ks] + x / 64 * kBox, &map_k, &sm.k_full[ks], x, j0, kz);
                 if (u == 0)
+#pragma unroll
                     for (int s = 0; s < 2; ++s)
                         if (w.kt[s].count() > 0) {
                             mbar_arrive_expect_tx(&sm.q_full[s], kTile);
@@ -124,82 +182,91 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                                 tma_load_3d(sm.q[s] + x / 64 * kBox, &map_q, &sm.q_full[s], x, w.t0[s], w.b * prm.Hq + w.h[s]);
                         }
                 loaded = u + 1;
-                if (u >= kStages && !wait_b(abort_flag, &sm.v_empty[st], ph)) {
-                    mbar_arrive_expect_tx(&sm.v_full[st], 0);  // completes the phase that drain() waits for
+                if (u >= kVStages && !wait_b(abort_flag, &sm.v_empty[vs], (uint32_t)(u / kVStages - 1) & 1u)) {
+                    mbar_arrive_expect_tx(&sm.v_full[vs], 0);  // completes the phase that drain() waits for
                     break;
                 }
-                mbar_arrive_expect_tx(&sm.v_full[st], kTile);
+                mbar_arrive_expect_tx(&sm.v_full[vs], kTile);
 #pragma unroll
-                for (int x = 0; x < DT; x += 64) tma_load_3d(sm.v[st] + x / 64 * kBox, &map_v, &sm.v_full[st], x, j0, kz);
+                for (int x = 0; x < DT; x += 64) tma_load_3d(sm.v[vs] + x / 64 * kBox, &map_v, &sm.v_full[vs], x, j0, kz);
             }
             // no copy may still be writing shared memory when the CTA exits
             if (loaded > 0)
+#pragma unroll
                 for (int s = 0; s < 2; ++s)
                     if (w.kt[s].count() > 0) drain(&sm.q_full[s], 0);
-            for (int u = max(loaded - kStages, 0); u < loaded; ++u) {
-                drain(&sm.k_full[u % kStages], (uint32_t)(u / kStages) & 1u);
-                drain(&sm.v_full[u % kStages], (uint32_t)(u / kStages) & 1u);
-            }
+            for (int u = max(loaded - kKStages, 0); u < loaded; ++u)
+                drain(&sm.k_full[u % kKStages], (uint32_t)(u / kKStages) & 1u);
+            for (int u = max(loaded - kVStages, 0); u < loaded; ++u)
+                drain(&sm.v_full[u % kVStages], (uint32_t)(u / kVStages) & 1u);
         }
     } else if (warp == kMmaWarp) {
         const uint32_t id_s = idesc_bf16_f32(128, kT, false, false), id_o = idesc_bf16_f32(128, DT, false, true);
-        int pvs[2] = {0, 0};
-        bool pending[2] = {false, false}, ok = !aborted(abort_flag);
-        for (int u = 0; ok && u <= U; ++u) {
-            const int st = u % kStages, pst = (u + kStages - 1) % kStages;
-            const uint32_t ph = (uint32_t)(u / kStages) & 1u, pph = (uint32_t)((u - 1) / kStages) & 1u;
+        const uint64_t dq[2] = {kmajor(smem_u32(sm.q[0]), 0), kmajor(smem_u32(sm.q[1]), 0)};
+        const uint64_t dk = kmajor(smem_u32(sm.k[0]), 0), dv = mnmajor(smem_u32(sm.v[0]), 0, kBox);
+        uint32_t kst = 0, kph = 0, vst = 0, vph = 0;  // stages and phases of K(u) and V(u - 1)
+        uint32_t fed[2] = {0, 0};                     // products of P_s issued
+        bool pending[2] = {false, false};
+        auto wait = [&](uint64_t *bar, uint32_t parity) { wait_or_abort(&g_win_status, abort_flag, bar, parity); };
+        for (int u = 0; u <= U; ++u) {
+            if (__any_sync(0xffffffffu, aborted(abort_flag))) break;
+            const int tile = u < U ? w.tile(u) : 0;
             if (u > 0) {
-                if (!(ok = wait_w(abort_flag, &sm.v_full[pst], pph))) break;
-                // values of padding: their weights are 0, but 0 times a NaN is not
-                const int j0 = w.tile(u - 1) * kT;
-                if (j0 + kT > w.n) {
-                    const int r0 = w.n - j0;
+                wait(&sm.v_full[vst], vph);
+                // values of padding (in the last tile only): their weights are 0, but 0 times a
+                // NaN is not
+                if (u == U && w.tile(u - 1) * kT + kT > w.n) {
+                    const int r0 = w.n - w.tile(u - 1) * kT;
                     for (int e = lane; e < (kT - r0) * (DT / 8); e += 32) {
                         const int row = r0 + e / (DT / 8), ch = e % (DT / 8);
-                        *reinterpret_cast<uint4 *>(sm.v[pst] + (ch >> 3) * kBox + row * 128 + (ch & 7) * 16) =
+                        *reinterpret_cast<uint4 *>(sm.v[vst] + (ch >> 3) * kBox + row * 128 + (ch & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
             }
-            if (u < U && !(ok = wait_w(abort_flag, &sm.k_full[st], ph))) break;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if (pending[s]) {
-                    if (!(ok = wait_w(abort_flag, &sm.p_full[s], (uint32_t)pvs[s] & 1u))) break;
+                    wait(&sm.p_full[s], fed[s] & 1u);
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t va = smem_u32(sm.v[pst]);
+                    if (elect_one()) {
+                        const uint64_t d = dv + vst * (kTile >> 4);
 #pragma unroll
                         for (int kk = 0; kk < kT / 16; ++kk)
-                            mma_ts(tmem + tO + s * DT, tmem + tS + s * kT + kk * 8, mnmajor(va, kk, kBox), id_o,
-                                   pvs[s] > 0 || kk > 0);
+                            mma_ts(tmem + tO + s * DT, tmem + tS + s * kT + kk * 8, d + kk * (2048 >> 4), id_o,
+                                   fed[s] > 0 || kk > 0);
                         mma_commit(&sm.o_full[s]);
                     }
-                    ++pvs[s];
+                    ++fed[s];
                     pending[s] = false;
                 }
-                if (u < U && w.reaches(s, w.tile(u))) {
-                    if (pvs[s] == 0 && !(ok = wait_w(abort_flag, &sm.q_full[s], 0))) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t qa = smem_u32(sm.q[s]), ka = smem_u32(sm.k[st]);
+                if (s == 1 && u > 0 && elect_one()) mma_commit(&sm.v_empty[vst]);
+                if (u < U) {
+                    if (s == 0) wait(&sm.k_full[kst], kph);
+                    if (w.reaches(s, tile)) {
+                        if (fed[s] == 0) wait(&sm.q_full[s], 0);
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t d = dk + kst * (kTile >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < DT / 16; ++kk)
-                            mma_ss(tmem + tS + s * kT, kmajor(qa, kk), kmajor(ka, kk), id_s, kk > 0);
-                        mma_commit(&sm.s_full[s]);
+                            for (int kk = 0; kk < DT / 16; ++kk) {
+                                const uint64_t o = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+                                mma_ss(tmem + tS + s * kT, dq[s] + o, d + o, id_s, kk > 0);
+                            }
+                            mma_commit(&sm.s_full[s]);
+                        }
+                        pending[s] = true;
                     }
-                    pending[s] = true;
+                    if (s == 1 && elect_one()) mma_commit(&sm.k_empty[kst]);
                 }
             }
-            if (ok && lane == 0) {
-                if (u < U) mma_commit(&sm.k_empty[st]);
-                if (u > 0) mma_commit(&sm.v_empty[pst]);
-            }
+            if (u > 0 && ++vst == kVStages) vst = 0, vph ^= 1u;
+            if (++kst == kKStages) kst = 0, kph ^= 1u;
             __syncwarp();
         }
-        if (lane == 0) {
+        if (elect_one()) {
             mma_commit(&sm.drain);  // every MMA issued completes before TMEM is freed
             drain(&sm.drain, 0);
         }
@@ -208,41 +275,32 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const int s = warp >> 2, r = 32 * (warp & 3) + lane;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t ts = tl + tS + s * kT, to = tl + tO + s * DT;
-        const int t = w.t0[s] + r, p = t + w.off, p_first = w.t0[s] + w.off;
+        const KeyTiles kt = s ? w.kt[1] : w.kt[0];
+        const int t0 = s ? w.t0[1] : w.t0[0], z = w.b * prm.Hq + (s ? w.h[1] : w.h[0]);
+        const int t = t0 + r, p = t + w.off, p_first = t0 + w.off, tiles = kt.count();
         const float c = prm.scale * kLog2e;
         float m = -INFINITY, l = 0.f;
-        int done = 0;
         bool ok = !aborted(abort_flag);
-        for (int u = 0; ok && u < U; ++u) {
-            const int tile = w.tile(u), j0 = tile * kT;
-            if (!w.reaches(s, tile)) continue;
+        int done = 0;
+        for (; ok && done < tiles; ++done) {
+            const int j0 = kt.tile(done) * kT;
             if (!(ok = wait_w(abort_flag, &sm.s_full[s], (uint32_t)done & 1u))) break;
             tc_fence_after();
-            uint32_t a[4][32];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) tmem_ld32(ts + 32 * g, a[g]);
-            tmem_ld_wait();
             const bool whole = j0 + kT - 1 <= p_first && p_first + kT - 1 < w.n &&
                                (p_first + kT - 1 - j0 < prm.window || j0 + kT <= prm.sinks);
-            if (!whole) {
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const uint32_t bits = seen_bits(p, j0 + 32 * g, prm.window, prm.sinks, w.n);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!((bits >> e) & 1u)) a[g][e] = 0xff800000u;  // -inf
-                }
-            }
-            float mx[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                mx[g] = __uint_as_float(a[g][0]);
-#pragma unroll
-                for (int e = 1; e < 32; ++e) mx[g] = fmaxf(mx[g], __uint_as_float(a[g][e]));
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // The weights against the maximum so far, found together with the tile's own maximum:
+            // unless that is more than kGrow above (or there is none yet) they stand.
+            uint32_t a[128];
+            float top;
+            uint64_t sum;
+            load_scores(ts, a, whole, p, j0, prm, w.n);
+            const bool fresh = __any_sync(0xffffffffu, m == -INFINITY);
+            if (fresh)
+                top = row_max(a);
+            else
+                weights(a, c, m, top, sum);
             const bool grow = top > m && (m == -INFINITY || (top - m) * c > kGrow);
-            if (__any_sync(0xffffffffu, grow)) {
+            if (fresh || __any_sync(0xffffffffu, grow)) {
                 const float keep = grow ? (m == -INFINITY ? 0.f : ex2((m - top) * c)) : 1.f;
                 if (grow) m = top;
                 l *= keep;
@@ -259,38 +317,20 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         tmem_st16(to + x, o);
                     }
                 }
+                if (!fresh) load_scores(ts, a, whole, p, j0, prm, w.n);
+                weights(a, c, m, top, sum);
             }
-            float base = m == -INFINITY ? 0.f : -m * c;
-            if (__any_sync(0xffffffffu, fabsf(m) > 0x1p100f && m != -INFINITY)) {
-                // m c may overflow: subtract first
+            float lx, ly;
+            split(sum, lx, ly);
+            l += lx + ly;
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        a[g][e] = __float_as_uint(__uint_as_float(a[g][e]) - (m == -INFINITY ? 0.f : m));
-                base = 0.f;
-            }
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float x = ex2(fmaf(__uint_as_float(a[g][2 * e]), c, base));
-                    const float y = ex2(fmaf(__uint_as_float(a[g][2 * e + 1]), c, base));
-                    sum[e & 3] += x + y;
-                    pk[e] = pack_bf16(x, y);
-                }
-                tmem_st16(ts + 16 * g, pk);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            for (int g = 0; g < 4; ++g) tmem_st16(ts + 16 * g, reinterpret_cast<const uint32_t(&)[16]>(a[16 * g]));
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&sm.p_full[s]);
-            ++done;
         }
         if (ok && done > 0) ok = wait_w(abort_flag, &sm.o_full[s], (uint32_t)(done - 1) & 1u);
-        if (ok && w.t0[s] < prm.Nq) {
+        if (ok && t0 < prm.Nq) {
             tc_fence_after();
             // rows that saw nothing (l = 0) are zeros whatever TMEM holds
             const bool some = l != 0.f;
@@ -312,15 +352,15 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 *reinterpret_cast<uint4 *>(row + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
             }
             if (t < prm.Nq)
-                prm.lse[((size_t)w.b * prm.Hq + w.h[s]) * prm.Nq + t] =
+                prm.lse[(size_t)z * prm.Nq + t] =
                     some ? (m == -INFINITY ? 0.f : m) * prm.scale + __log2f(l) * kLn2 : -INFINITY;
             fence_proxy_async_smem();
         }
         named_bar_sync(1 + s, 128);
-        if (ok && w.t0[s] < prm.Nq && (warp & 3) == 0 && lane == 0) {
+        if (ok && t0 < prm.Nq && (warp & 3) == 0 && lane == 0) {
 #pragma unroll
             for (int x = 0; x < DT; x += 64)
-                tma_store_3d(&map_o, sm.q[s] + x / 64 * kBox, x, w.t0[s], w.b * prm.Hq + w.h[s]);
+                tma_store_3d(&map_o, sm.q[s] + x / 64 * kBox, x, t0, z);
             tma_store_commit();
             tma_store_wait_all();
         }

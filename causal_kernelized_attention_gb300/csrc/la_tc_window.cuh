@@ -42,6 +42,70 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// The warp's index as a value the compiler knows to be the same in every lane, and one
+// elected lane: the MMA warp's loop then runs on the uniform datapath, where descriptors
+// and addresses live in the registers that tcgen05.mma reads.  (With threadIdx-derived
+// branches each MMA cost about 85 cycles to issue, more than it takes to run.)
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// For the MMA warp, whose lanes must stay together: waits like wait_bar but returns nothing.
+// When the wait has run out the abort flag is set, every later wait returns at once, and
+// the loop ends at its next check of the flag; what is issued until then multiplies
+// whatever is there, which the launch's outputs being undefined allows.
+__device__ __forceinline__ void wait_or_abort(unsigned *status, int *abort_flag, uint64_t *bar, uint32_t parity)
+{
+    if (!mbar_try_wait(bar, parity)) wait_bar(status, abort_flag, bar, parity);
+    __syncwarp();
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair(uint32_t x, uint32_t y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+    return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float &x, float &y)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // This CTA's two query tiles and the key tiles either of them reaches.
 template <int KT>  // keys of a tile
 struct Work {

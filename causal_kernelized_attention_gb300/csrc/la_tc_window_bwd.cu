@@ -101,7 +101,7 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     DqSmem<DT> &sm = *reinterpret_cast<DqSmem<DT> *>(smem_raw);
     constexpr uint32_t kTile = DqSmem<DT>::kTile, kStage = DqSmem<DT>::kStage;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sm.q_full[s], 1);
@@ -147,6 +147,7 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
                 for (int x = 0; x < DT; x += 64)
                     tma_load_3d(sm.k[st] + x / 64 * kHalfBox, &map_k, &sm.k_full[st], x, j0, kz);
                 if (u == 0)
+#pragma unroll
                     for (int s = 0; s < 2; ++s)
                         if (w.kt[s].count() > 0) {
                             const int z = w.b * prm.Hq + w.h[s];
@@ -169,6 +170,7 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
             }
             // no copy may still be writing shared memory when the CTA exits
             if (loaded > 0)
+#pragma unroll
                 for (int s = 0; s < 2; ++s)
                     if (w.kt[s].count() > 0) drain(&sm.q_full[s], 0);
             for (int u = max(loaded - kKeyStages, 0); u < loaded; ++u) {
@@ -178,58 +180,65 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
         }
     } else if (warp == kMmaWarp) {
         const uint32_t id_s = idesc_bf16_f32(128, kHalf, false, false), id_g = idesc_bf16_f32(128, DT, false, true);
-        int fed[2] = {0, 0};  // tiles of s whose dS has been multiplied
-        bool pending[2] = {false, false}, ok = !aborted(abort_flag);
-        for (int u = 0; ok && u <= U; ++u) {
-            const int st = u % kKeyStages, pst = (u + kKeyStages - 1) % kKeyStages;
-            const uint32_t ph = (uint32_t)(u / kKeyStages) & 1u;
-            if (u < U) {
-                if (!(ok = wait_w(abort_flag, &sm.k_full[st], ph))) break;
-                const int j0 = w.tile(u) * kHalf;
-                if (j0 + kHalf > w.n) zero_rows<DT>(sm.k[st], w.n - j0, lane);
-                if (!(ok = wait_w(abort_flag, &sm.v_full[st], ph))) break;
-            }
+        const uint64_t qd[2] = {kmajor(smem_u32(sm.q[0]), 0), kmajor(smem_u32(sm.q[1]), 0)};
+        const uint64_t gd[2] = {kmajor(smem_u32(sm.go[0]), 0), kmajor(smem_u32(sm.go[1]), 0)};
+        const uint64_t kd = kmajor_half(smem_u32(sm.k[0]), 0), vd = kmajor_half(smem_u32(sm.v[0]), 0);
+        const uint64_t kt = mnmajor_half(smem_u32(sm.k[0]), 0);
+        uint32_t st = 0, ph = 0, pst = 0;  // stage and phase of tile u, stage of tile u - 1
+        uint32_t fed[2] = {0, 0};          // tiles of s whose dS has been multiplied
+        bool pending[2] = {false, false};
+        auto wait = [&](uint64_t *bar, uint32_t parity) { wait_or_abort(&g_winb_status, abort_flag, bar, parity); };
+        for (int u = 0; u <= U; ++u) {
+            if (__any_sync(0xffffffffu, aborted(abort_flag))) break;
+            const int tile = u < U ? w.tile(u) : 0;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if (pending[s]) {
-                    if (!(ok = wait_w(abort_flag, &sm.ds_full[s], (uint32_t)fed[s] & 1u))) break;
+                    wait(&sm.ds_full[s], fed[s] & 1u);
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t ka = smem_u32(sm.k[pst]);
+                    if (elect_one()) {
+                        const uint64_t d = kt + pst * (kStage >> 4);
 #pragma unroll
                         for (int kk = 0; kk < kHalf / 16; ++kk)
-                            mma_ts(tmem + tG + s * DT, tmem + tS + s * kHalf + kk * 8, mnmajor_half(ka, kk), id_g,
+                            mma_ts(tmem + tG + s * DT, tmem + tS + s * kHalf + kk * 8, d + kk * (2048 >> 4), id_g,
                                    fed[s] > 0 || kk > 0);
                     }
                     ++fed[s];
                     pending[s] = false;
                 }
-                if (u < U && w.reaches(s, w.tile(u))) {
-                    if (fed[s] == 0 && !(ok = wait_w(abort_flag, &sm.q_full[s], 0))) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t qa = smem_u32(sm.q[s]), ga = smem_u32(sm.go[s]);
-                        const uint32_t ka = smem_u32(sm.k[st]), va = smem_u32(sm.v[st]);
-#pragma unroll
-                        for (int kk = 0; kk < DT / 16; ++kk)
-                            mma_ss(tmem + tS + s * kHalf, kmajor(qa, kk), kmajor_half(ka, kk), id_s, kk > 0);
-#pragma unroll
-                        for (int kk = 0; kk < DT / 16; ++kk)
-                            mma_ss(tmem + tP + s * kHalf, kmajor(ga, kk), kmajor_half(va, kk), id_s, kk > 0);
-                        mma_commit(&sm.s_full[s]);
+                if (s == 1 && u > 0 && elect_one()) mma_commit(&sm.k_empty[pst]);
+                if (u < U) {
+                    if (s == 0) {
+                        wait(&sm.k_full[st], ph);
+                        if (u == U - 1 && tile * kHalf + kHalf > w.n) zero_rows<DT>(sm.k[st], w.n - tile * kHalf, lane);
+                        wait(&sm.v_full[st], ph);
                     }
-                    pending[s] = true;
+                    if (w.reaches(s, tile)) {
+                        if (fed[s] == 0) wait(&sm.q_full[s], 0);
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint32_t so = st * (kStage >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < DT / 16; ++kk)
+                                mma_ss(tmem + tS + s * kHalf, qd[s] + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4),
+                                       kd + so + (((kk >> 2) * kHalfBox + (kk & 3) * 32) >> 4), id_s, kk > 0);
+#pragma unroll
+                            for (int kk = 0; kk < DT / 16; ++kk)
+                                mma_ss(tmem + tP + s * kHalf, gd[s] + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4),
+                                       vd + so + (((kk >> 2) * kHalfBox + (kk & 3) * 32) >> 4), id_s, kk > 0);
+                            mma_commit(&sm.s_full[s]);
+                        }
+                        pending[s] = true;
+                    }
+                    if (s == 1 && elect_one()) mma_commit(&sm.v_empty[st]);
                 }
             }
-            if (ok && lane == 0) {
-                if (u < U) mma_commit(&sm.v_empty[st]);
-                if (u > 0) mma_commit(&sm.k_empty[pst]);
-                if (u == U)
-                    for (int s = 0; s < 2; ++s) mma_commit(&sm.g_full[s]);
-            }
-            __syncwarp();
+            pst = st;
+            if (++st == kKeyStages) st = 0, ph ^= 1u;
         }
-        if (lane == 0) {
+        if (elect_one())
+            for (int s = 0; s < 2; ++s) mma_commit(&sm.g_full[s]);
+        if (elect_one()) {
             mma_commit(&sm.drain);  // every MMA issued completes before TMEM is freed
             drain(&sm.drain, 0);
         }
@@ -238,16 +247,17 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
         const int s = warp >> 2, r = 32 * (warp & 3) + lane;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t ts = tl + tS + s * kHalf, tp = tl + tP + s * kHalf, tg = tl + tG + s * DT;
-        const int t = w.t0[s] + r, p = t + w.off, p_first = w.t0[s] + w.off;
-        const size_t row = ((size_t)w.b * prm.Hq + w.h[s]) * prm.Nq + t;
+        const KeyTiles kt = s ? w.kt[1] : w.kt[0];
+        const int t0 = s ? w.t0[1] : w.t0[0], z = w.b * prm.Hq + (s ? w.h[1] : w.h[0]);
+        const int t = t0 + r, p = t + w.off, p_first = t0 + w.off, tiles = kt.count();
+        const size_t row = (size_t)z * prm.Nq + t;
         const bool live = t < prm.Nq && p < w.n;
         const float c = prm.scale * kLog2e;
         bool ok = !aborted(abort_flag);
-        int done = 0;
         // the row's lse in units of the raw scores, and its D
         const float base = live ? __ldg(prm.lse + row) / prm.scale : 0.f;
         float delta = 0.f;
-        if (ok && w.kt[s].count() > 0 && (ok = wait_w(abort_flag, &sm.q_full[s], 0)) && live) {
+        if (ok && tiles > 0 && (ok = wait_w(abort_flag, &sm.q_full[s], 0)) && live) {
             const uint4 *op = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(prm.o) + row * prm.d);
             for (int ch = 0; ch < prm.d / 8; ++ch) {
                 const uint4 x = __ldg(op + ch);
@@ -261,9 +271,9 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
             }
         }
         if (t < prm.Nq) prm.delta[row] = delta;
-        for (int u = 0; ok && u < U; ++u) {
-            const int tile = w.tile(u), j0 = tile * kHalf;
-            if (!w.reaches(s, tile)) continue;
+        const uint64_t base2 = pair(-base, -base), delta2 = pair(-delta, -delta), c2 = pair(c, c);
+        for (int done = 0; ok && done < tiles; ++done) {
+            const int j0 = kt.tile(done) * kHalf;
             if (!(ok = wait_w(abort_flag, &sm.s_full[s], (uint32_t)done & 1u))) break;
             tc_fence_after();
             const bool whole = j0 + kHalf - 1 <= p_first && p_first + kRows - 1 < w.n &&
@@ -276,8 +286,14 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
                 tmem_ld_wait();
                 const uint32_t bits = whole ? 0xffffffffu : seen_bits(p, j0 + 32 * g, prm.window, prm.sinks, w.n);
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    a[e] = __float_as_uint(ex2((__uint_as_float(a[e]) - base) * c) * (__uint_as_float(b[e]) - delta));
+                for (int e = 0; e < 32; e += 2) {
+                    float x, y;
+                    split(mul2(add2(pair(a[e], a[e + 1]), base2), c2), x, y);
+                    const uint64_t d = mul2(pair(ex2(x), ex2(y)), add2(pair(b[e], b[e + 1]), delta2));
+                    split(d, x, y);
+                    a[e] = __float_as_uint(x);
+                    a[e + 1] = __float_as_uint(y);
+                }
                 if (!whole) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
@@ -290,20 +306,19 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&sm.ds_full[s]);
-            ++done;
         }
         if (ok) ok = U == 0 || wait_w(abort_flag, &sm.g_full[s], 0);
-        if (ok && w.t0[s] < prm.Nq) {
+        if (ok && t0 < prm.Nq) {
             tc_fence_after();
 #pragma unroll
-            for (int x = 0; x < DT; x += 16) stage16(sm.q[s], tg, r, x, prm.scale, live && done > 0);
+            for (int x = 0; x < DT; x += 16) stage16(sm.q[s], tg, r, x, prm.scale, live);
             fence_proxy_async_smem();
         }
         named_bar_sync(1 + s, 128);
-        if (ok && w.t0[s] < prm.Nq && (warp & 3) == 0 && lane == 0) {
+        if (ok && t0 < prm.Nq && (warp & 3) == 0 && lane == 0) {
 #pragma unroll
             for (int x = 0; x < DT; x += 64)
-                tma_store_3d(&map_dq, sm.q[s] + x / 64 * kBox, x, w.t0[s], w.b * prm.Hq + w.h[s]);
+                tma_store_3d(&map_dq, sm.q[s] + x / 64 * kBox, x, t0, z);
             tma_store_commit();
             tma_store_wait_all();
         }
@@ -325,7 +340,7 @@ struct DkvSmem {
     uint8_t v[kTile];  // then dv, staged
     uint8_t q[kRowStages][kStage];
     uint8_t go[kRowStages][kStage];
-    float base[kRowStages][kHalf], delta[kRowStages][kHalf];
+    float base[kRowStages][kHalf], delta[kRowStages][kHalf];  // -lse / scale and -D of the rows
     uint64_t kv_full, s_full[2], ds_full[2], g_full;
     uint64_t q_full[kRowStages], q_empty[kRowStages], l_full[kRowStages], drain;
     uint32_t tmem_base;
@@ -342,7 +357,7 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     DkvSmem<DT> &sm = *reinterpret_cast<DkvSmem<DT> *>(smem_raw);
     constexpr uint32_t kTile = DkvSmem<DT>::kTile, kStage = DkvSmem<DT>::kStage;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     if (tid == 0) {
         mbar_init(&sm.kv_full, 1);
         mbar_init(&sm.g_full, 1);
@@ -406,8 +421,8 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             for (int e = lane; e < kHalf; e += 32) {
                 const bool in = t0 + e < rows;
                 const size_t at = (size_t)z * prm.Nq + t0 + e;
-                sm.base[st][e] = in ? __ldcg(prm.lse + at) / prm.scale : 0.f;
-                sm.delta[st][e] = in ? __ldcg(prm.delta + at) : 0.f;
+                sm.base[st][e] = in ? -__ldcg(prm.lse + at) / prm.scale : 0.f;
+                sm.delta[st][e] = in ? -__ldcg(prm.delta + at) : 0.f;
             }
             mbar_arrive(&sm.l_full[st]);
         }
@@ -419,50 +434,59 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         __syncwarp();
     } else if (warp == kMmaWarp) {
         const uint32_t id_s = idesc_bf16_f32(128, kHalf, false, false), id_g = idesc_bf16_f32(128, DT, false, true);
-        const uint32_t ka = smem_u32(sm.k), va = smem_u32(sm.v);
-        bool ok = !aborted(abort_flag) && X > 0;
-        if (ok) ok = wait_w(abort_flag, &sm.kv_full, 0);
-        for (int i = 0; ok && i < X + 2; ++i) {
-            const int s = i & 1, st = i % kRowStages, back = i - 2, bst = (i + kRowStages - 2) % kRowStages;
+        const uint64_t kd = kmajor(smem_u32(sm.k), 0), vd = kmajor(smem_u32(sm.v), 0);
+        const uint64_t qd = kmajor_half(smem_u32(sm.q[0]), 0), gd = kmajor_half(smem_u32(sm.go[0]), 0);
+        const uint64_t qt_ = mnmajor_half(smem_u32(sm.q[0]), 0), gt = mnmajor_half(smem_u32(sm.go[0]), 0);
+        uint32_t st = 0, ph = 0, bst = 0;  // stage and phase of tile i, stage of tile i - 2
+        int at = 0;                        // tile i's place within its head
+        auto wait = [&](uint64_t *bar, uint32_t parity) { wait_or_abort(&g_winb_status, abort_flag, bar, parity); };
+        if (X > 0) wait(&sm.kv_full, 0);
+        for (int i = 0; i < (X > 0 ? X + 2 : 0); ++i) {
+            if (__any_sync(0xffffffffu, aborted(abort_flag))) break;
+            const uint32_t s = i & 1;
+            const int back = i - 2;
             if (back >= 0) {  // the tile of this group before: its P and dS are in TMEM
-                if (!(ok = wait_w(abort_flag, &sm.ds_full[s], (uint32_t)(back >> 1) & 1u))) break;
+                wait(&sm.ds_full[s], (uint32_t)(back >> 1) & 1u);
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t qa = smem_u32(sm.q[bst]), ga = smem_u32(sm.go[bst]);
+                if (elect_one()) {
+                    const uint32_t so = bst * (kStage >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kHalf / 16; ++kk)
-                        mma_ts(tmem + tG, tmem + tS + s * kHalf + kk * 8, mnmajor_half(ga, kk), id_g, back > 0 || kk > 0);
+                        mma_ts(tmem + tG, tmem + tS + s * kHalf + kk * 8, gt + so + kk * (2048 >> 4), id_g, back > 0 || kk > 0);
 #pragma unroll
                     for (int kk = 0; kk < kHalf / 16; ++kk)
-                        mma_ts(tmem + tG + DT, tmem + tP + s * kHalf + kk * 8, mnmajor_half(qa, kk), id_g,
+                        mma_ts(tmem + tG + DT, tmem + tP + s * kHalf + kk * 8, qt_ + so + kk * (2048 >> 4), id_g,
                                back > 0 || kk > 0);
                     mma_commit(&sm.q_empty[bst]);
                 }
-                __syncwarp();
+                if (++bst == kRowStages) bst = 0;
             }
             if (i < X) {
-                if (!(ok = wait_w(abort_flag, &sm.q_full[st], (uint32_t)(i / kRowStages) & 1u))) break;
-                const int t0 = (qt.begin + i % per) * kHalf;
+                wait(&sm.q_full[st], ph);
+                const int t0 = (qt.begin + at) * kHalf;
                 if (t0 + kHalf > rows) {
                     zero_rows<DT>(sm.q[st], rows - t0, lane);
                     zero_rows<DT>(sm.go[st], rows - t0, lane);
                 }
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t qa = smem_u32(sm.q[st]), ga = smem_u32(sm.go[st]);
+                if (elect_one()) {
+                    const uint32_t so = st * (kStage >> 4);
 #pragma unroll
                     for (int kk = 0; kk < DT / 16; ++kk)
-                        mma_ss(tmem + tS + s * kHalf, kmajor(ka, kk), kmajor_half(qa, kk), id_s, kk > 0);
+                        mma_ss(tmem + tS + s * kHalf, kd + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4),
+                               qd + so + (((kk >> 2) * kHalfBox + (kk & 3) * 32) >> 4), id_s, kk > 0);
 #pragma unroll
                     for (int kk = 0; kk < DT / 16; ++kk)
-                        mma_ss(tmem + tP + s * kHalf, kmajor(va, kk), kmajor_half(ga, kk), id_s, kk > 0);
+                        mma_ss(tmem + tP + s * kHalf, vd + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4),
+                               gd + so + (((kk >> 2) * kHalfBox + (kk & 3) * 32) >> 4), id_s, kk > 0);
                     mma_commit(&sm.s_full[s]);
                 }
-                __syncwarp();
+                if (++st == kRowStages) st = 0, ph ^= 1u;
+                if (++at == per) at = 0;
             }
         }
-        if (lane == 0) {
-            if (ok) mma_commit(&sm.g_full);
+        if (elect_one()) {
+            mma_commit(&sm.g_full);
             mma_commit(&sm.drain);  // every MMA issued completes before TMEM is freed
             drain(&sm.drain, 0);
         }
@@ -472,6 +496,7 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t ts = tl + tS + s * kHalf, tp = tl + tP + s * kHalf;
         const float c = prm.scale * kLog2e;
+        const uint64_t c2 = pair(c, c);
         // positions [j, last] see key j
         const int last = j >= n ? -1 : j < prm.sinks ? n - 1 : min(n - 1, j + prm.window - 1);
         bool ok = !aborted(abort_flag);
@@ -488,17 +513,22 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 tmem_ld32(ts + 32 * g, a);
                 tmem_ld32(tp + 32 * g, d);
                 tmem_ld_wait();
-                const float4 *bp = reinterpret_cast<const float4 *>(&sm.base[st][32 * g]);
-                const float4 *dp = reinterpret_cast<const float4 *>(&sm.delta[st][32 * g]);
+                const ulonglong2 *bp = reinterpret_cast<const ulonglong2 *>(&sm.base[st][32 * g]);
+                const ulonglong2 *dp = reinterpret_cast<const ulonglong2 *>(&sm.delta[st][32 * g]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float4 x = bp[e], y = dp[e];
-                    const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+                for (int e = 0; e < 32; e += 4) {
+                    const ulonglong2 nb = bp[e / 4], nd = dp[e / 4];
 #pragma unroll
-                    for (int i4 = 0; i4 < 4; ++i4) {
-                        const float pr = ex2((__uint_as_float(a[4 * e + i4]) - xs[i4]) * c);
-                        a[4 * e + i4] = __float_as_uint(pr);
-                        d[4 * e + i4] = __float_as_uint(pr * (__uint_as_float(d[4 * e + i4]) - ys[i4]));
+                    for (int h = 0; h < 4; h += 2) {
+                        float x, y;
+                        split(mul2(add2(pair(a[e + h], a[e + h + 1]), h ? nb.y : nb.x), c2), x, y);
+                        x = ex2(x);
+                        y = ex2(y);
+                        a[e + h] = __float_as_uint(x);
+                        a[e + h + 1] = __float_as_uint(y);
+                        split(mul2(pair(x, y), add2(pair(d[e + h], d[e + h + 1]), h ? nd.y : nd.x)), x, y);
+                        d[e + h] = __float_as_uint(x);
+                        d[e + h + 1] = __float_as_uint(y);
                     }
                 }
                 if (!whole) {
