@@ -257,7 +257,7 @@ la_status la_window_backward(const void *q, const void *k, const void *v, const 
     p.scale = scale;
     p.dtype = dtype;
     p.stream = s;
-    // D = dO . o per row, from the dq kernel to the dk, dv kernel.  The lock keeps two host
+    // D = dO . o per row, from the dq kernel to the dk, dv kernel, and partial sums.  The lock keeps two host
     // threads that share a stream from mixing their launches on its one workspace; a captured
     // call takes memory of its own, so that two graphs may be replayed at once.
     static std::mutex mu;
@@ -266,9 +266,10 @@ la_status la_window_backward(const void *q, const void *k, const void *v, const 
     void *base = nullptr;
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     if ((st = cuda_status(cudaStreamIsCapturing(s, &cs))) != LA_OK) return st;
-    st = cs == cudaStreamCaptureStatusNone ? data_workspace(s, rows * 4, &base) : LA_ERR_UNSUPPORTED;
+    const size_t bytes = dtype == LA_BF16 ? window_backward_tc_scratch(p) : rows * 4;
+    st = cs == cudaStreamCaptureStatusNone ? data_workspace(s, bytes, &base) : LA_ERR_UNSUPPORTED;
     if (st != LA_OK) {
-        if ((st = scratch.alloc(rows * 4, s)) != LA_OK) return st;
+        if ((st = scratch.alloc(bytes, s)) != LA_OK) return st;
         base = scratch.ptr;
     }
     p.delta = static_cast<float *>(base);

@@ -175,7 +175,8 @@ la_status recurrence_step(float *state, const void *x, const float *alpha, void 
                           cudaStream_t stream);
 
 // Window attention with sinks (la_window.cu: CUDA cores, fp32 arithmetic).  forward: out, lse;
-// backward: o, lse, dout -> dq, dk, dv, with delta (fp32, [B, Hq, Nq]) as scratch.  window
+// backward: o, lse, dout -> dq, dk, dv, with scratch at delta (fp32 [B, Hq, Nq], and more on
+// the tensor cores).  window
 // and sinks are at most Nk.
 struct WindowProblem {
     const void *q, *k, *v, *o, *dout;
@@ -192,6 +193,7 @@ la_status window_backward_simt(const WindowProblem &p);
 // The same on the tensor cores (la_tc_window.cu, la_tc_window_bwd.cu): bf16.
 la_status window_forward_tc(const WindowProblem &p);
 la_status window_backward_tc(const WindowProblem &p);
+size_t window_backward_tc_scratch(const WindowProblem &p);  // bytes at p.delta
 
 // The ring cache and the decode step (la_window_decode.cu).
 struct WindowDecodeProblem {

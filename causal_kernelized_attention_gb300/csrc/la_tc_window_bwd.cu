@@ -15,8 +15,15 @@
 // thread owns a key, for which the visible queries are one interval.  The rounding of dS
 // (2^-9 relative, like P's) is the size of the gradients' own; sums are fp32.
 //
+// A tile of sinks is seen by every later row.  Its rows are shared out over several CTAs,
+// each about a window tile's work; their fp32 sums go to scratch and a third, small kernel
+// adds them up in order (otherwise those few CTAs outlast all others: 864 us instead of
+// 150 at 8192 rows, window 1024).
+//
 // Rows and keys of padding: their P and dS are 0, and what a product multiplies by them is
 // zeroed in shared memory (0 times a NaN is not 0).
+#include <algorithm>
+
 #include "la_tc_window.cuh"
 
 namespace la {
@@ -333,6 +340,49 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
 // ---------------------------------------------------------------- dk, dv
 constexpr int kRowStages = 5;
 
+// How the tiles of sinks are shared out: `tiles` of them per key head, `parts` CTAs each.
+struct Split {
+    int tiles, parts;
+};
+Split split_of(const WindowProblem &p)
+{
+    Split sp{ceil_div(p.sinks, kRows), 1};
+    const long long tiles = ceil_div(p.Nk, kRows), whole = ceil_div(p.Nq, kHalf);
+    const long long win = std::min<long long>(whole, (p.window + kRows) / kHalf + 1);
+    // a share is a window tile's work, or what half a CTA's share of the machine comes to
+    const long long total = (long long)p.B * p.Hk * ((tiles - sp.tiles) * win + sp.tiles * whole);
+    const long long unit = std::max(win, total / (2 * sm_count()));
+    if (sp.tiles > 0) sp.parts = (int)((whole + unit - 1) / unit);
+    return sp;
+}
+size_t split_floats(const WindowProblem &p, const Split &sp, int DT)
+{
+    return sp.parts > 1 ? (size_t)p.B * p.Hk * sp.tiles * sp.parts * 2 * kRows * DT : 0;
+}
+
+// Adds up the shares of the tiles of sinks, in order: 4 features a thread.
+template <int DT>
+__global__ void __launch_bounds__(256) window_tc_sum(const float *part, __nv_bfloat16 *dk, __nv_bfloat16 *dv, const Split sp,
+                                                     int Nk, int d, float scale)
+{
+    const long long e = (long long)blockIdx.x * 256 + threadIdx.x;  // (bh, tile, dv or dk, row, 4 features)
+    const int c = (int)(e % (DT / 4)) * 4, r = (int)(e / (DT / 4) % kRows), which = (int)(e / (DT / 4) / kRows % 2);
+    const long long tile = e / (DT / 4) / kRows / 2;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int j = (int)(tile % sp.tiles) * kRows + r;
+    if (j >= Nk || c >= d) return;
+    const float *src = part + (tile * sp.parts * 2 + which) * (kRows * DT) + r * DT + c;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < sp.parts; ++i) {
+        const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + (size_t)i * 2 * kRows * DT));
+        sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
+    }
+    const float f = which ? scale : 1.f;
+    *reinterpret_cast<uint2 *>((which ? dk : dv) + ((size_t)(tile / sp.tiles) * Nk + j) * d + c) =
+        make_uint2(pack_bf16(sum.x * f, sum.y * f), pack_bf16(sum.z * f, sum.w * f));
+}
+
 template <int DT>
 struct DkvSmem {
     static constexpr uint32_t kTile = kRows * DT * 2, kStage = kHalf * DT * 2;
@@ -352,7 +402,8 @@ template <int DT>
 __global__ void __launch_bounds__(kThreads, 1)
 window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
               const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-              const __grid_constant__ CUtensorMap map_dk, const __grid_constant__ CUtensorMap map_dv, const Params prm)
+              const __grid_constant__ CUtensorMap map_dk, const __grid_constant__ CUtensorMap map_dv, const Params prm,
+              const Split sp, float *part)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     DkvSmem<DT> &sm = *reinterpret_cast<DkvSmem<DT> *>(smem_raw);
@@ -388,10 +439,15 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     int *abort_flag = &sm.abort;
 
     const int tiles = (prm.Nk + kRows - 1) / kRows, group = prm.Hq / prm.Hk, off = prm.Nk - prm.Nq;
-    const int bh = (int)blockIdx.x / tiles, j0 = (int)blockIdx.x % tiles * kRows, b = bh / prm.Hk, hk = bh % prm.Hk;
+    const int units = tiles + sp.tiles * (sp.parts - 1), bh = (int)blockIdx.x / units, unit = (int)blockIdx.x % units;
+    const bool shared = unit < sp.tiles * sp.parts && sp.parts > 1;  // a share of a tile of sinks
+    const int j0 = (shared ? unit / sp.parts : unit - sp.tiles * (sp.parts - 1)) * kRows, b = bh / prm.Hk, hk = bh % prm.Hk;
     const int n = valid(prm.lens, b, prm.Nk);
     const QueryTiles qt(j0, min(j0 + kRows, prm.Nk) - 1, prm.window, prm.sinks, n, off, prm.Nq, kHalf);
-    const int per = qt.end - qt.begin, X = per * group;  // streamed tile x: head x / per of the group
+    // streamed tile x: head x / per of the group; this CTA's from x0 on, X of them
+    const int per = qt.end - qt.begin, all = per * group, share = shared ? unit % sp.parts : 0;
+    const int x0 = shared ? (int)((long long)all * share / sp.parts) : 0;
+    const int X = (shared ? (int)((long long)all * (share + 1) / sp.parts) : all) - x0;
     const int rows = min(prm.Nq, n - off);               // rows of tokens
 
     if (warp == kTmaWarp) {
@@ -406,7 +462,8 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             }
         }
         for (int i = 0; ok && i < X; ++i) {
-            const int st = i % kRowStages, t0 = (qt.begin + i % per) * kHalf, z = b * prm.Hq + hk * group + i / per;
+            const int st = i % kRowStages, x = x0 + i;
+            const int t0 = (qt.begin + x % per) * kHalf, z = b * prm.Hq + hk * group + x / per;
             if (i >= kRowStages && !(ok = wait_w(abort_flag, &sm.q_empty[st], (uint32_t)(i / kRowStages - 1) & 1u))) break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&sm.q_full[st], 2 * kStage);
@@ -438,7 +495,7 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         const uint64_t qd = kmajor_half(smem_u32(sm.q[0]), 0), gd = kmajor_half(smem_u32(sm.go[0]), 0);
         const uint64_t qt_ = mnmajor_half(smem_u32(sm.q[0]), 0), gt = mnmajor_half(smem_u32(sm.go[0]), 0);
         uint32_t st = 0, ph = 0, bst = 0;  // stage and phase of tile i, stage of tile i - 2
-        int at = 0;                        // tile i's place within its head
+        int at = per > 0 ? x0 % per : 0;   // tile i's place within its head
         auto wait = [&](uint64_t *bar, uint32_t parity) { wait_or_abort(&g_winb_status, abort_flag, bar, parity); };
         if (X > 0) wait(&sm.kv_full, 0);
         for (int i = 0; i < (X > 0 ? X + 2 : 0); ++i) {
@@ -501,7 +558,7 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         const int last = j >= n ? -1 : j < prm.sinks ? n - 1 : min(n - 1, j + prm.window - 1);
         bool ok = !aborted(abort_flag);
         for (int i = s; ok && i < X; i += 2) {
-            const int st = i % kRowStages, p0 = (qt.begin + i % per) * kHalf + off;
+            const int st = i % kRowStages, p0 = (qt.begin + (x0 + i) % per) * kHalf + off;
             if (!(ok = wait_w(abort_flag, &sm.l_full[st], (uint32_t)(i / kRowStages) & 1u))) break;
             if (!(ok = wait_w(abort_flag, &sm.s_full[s], (uint32_t)(i >> 1) & 1u))) break;
             tc_fence_after();
@@ -551,14 +608,28 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         }
         if (ok && X > 0) ok = wait_w(abort_flag, &sm.g_full, 0);
         uint8_t *out = s == 0 ? sm.v : sm.k;  // group 0: dv, group 1: dk
-        if (ok) {
+        if (ok && shared) {
+            // this share's sums: [share][dv, dk][128][DT]
+            float *dst = part + ((((size_t)bh * sp.tiles + j0 / kRows) * sp.parts + share) * 2 + s) * (kRows * DT) + r * DT;
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < DT; x += 16) {
+                uint32_t o[16];
+                tmem_ld16(tl + tG + s * DT + x, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    *reinterpret_cast<uint4 *>(dst + x + e) =
+                        X > 0 ? make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        } else if (ok) {
             tc_fence_after();
 #pragma unroll
             for (int x = 0; x < DT; x += 16) stage16(out, tl + tG + s * DT, r, x, s == 0 ? 1.f : prm.scale, X > 0);
             fence_proxy_async_smem();
         }
         named_bar_sync(1 + s, 128);
-        if (ok && (warp & 3) == 0 && lane == 0) {
+        if (ok && !shared && (warp & 3) == 0 && lane == 0) {
 #pragma unroll
             for (int x = 0; x < DT; x += 64) tma_store_3d(s == 0 ? &map_dv : &map_dk, out + x / 64 * kBox, x, j0, bh);
             tma_store_commit();
@@ -572,12 +643,19 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
+// Scratch: D of every row, then the shares.
+size_t part_offset(const WindowProblem &p) { return ((size_t)p.B * p.Hq * p.Nq * 4 + 255) & ~(size_t)255; }
+
 template <int DT>
 la_status backward(const WindowProblem &p)
 {
     const Params prm = params_of(p);
-    const long long dq_ctas = (long long)p.B * p.Hk * prm.units, dkv_ctas = (long long)p.B * p.Hk * ceil_div(p.Nk, kRows);
-    if (dq_ctas > 0x7fffffffLL || dkv_ctas > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
+    const Split sp = split_of(p);
+    const long long dq_ctas = (long long)p.B * p.Hk * prm.units;
+    const long long dkv_ctas = (long long)p.B * p.Hk * (ceil_div(p.Nk, kRows) + sp.tiles * (sp.parts - 1LL));
+    const long long sum_ctas = (long long)split_floats(p, sp, DT) / std::max(sp.parts, 1) / 4 / 256;
+    float *part = reinterpret_cast<float *>(reinterpret_cast<char *>(p.delta) + part_offset(p));
+    if (dq_ctas > 0x7fffffffLL || dkv_ctas > 0x7fffffffLL || sum_ctas > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
     const int bq = p.B * p.Hq, bk = p.B * p.Hk;
     CUtensorMap mq, mdo, mk, mv, mqh, mdoh, mkh, mvh, mdq, mdk, mdv;
     la_status st = make_map(&mq, p.q, bq, p.Nq, p.d);
@@ -594,15 +672,23 @@ la_status backward(const WindowProblem &p)
     if (st == LA_OK) st = ensure_smem((const void *)window_tc_dq<DT>, (int)sizeof(DqSmem<DT>));
     if (st == LA_OK) st = ensure_smem((const void *)window_tc_dkv<DT>, (int)sizeof(DkvSmem<DT>));
     if (st != LA_OK) return st;
-    count_launches(2);
+    count_launches(sp.parts > 1 ? 3 : 2);
     st = launch_dependent(window_tc_dq<DT>, (unsigned)dq_ctas, kThreads, (int)sizeof(DqSmem<DT>), p.stream, mq, mdo, mkh, mvh,
                           mdq, prm);
     if (st != LA_OK) return st;
-    return launch_dependent(window_tc_dkv<DT>, (unsigned)dkv_ctas, kThreads, (int)sizeof(DkvSmem<DT>), p.stream, mqh, mdoh, mk,
-                            mv, mdk, mdv, prm);
+    st = launch_dependent(window_tc_dkv<DT>, (unsigned)dkv_ctas, kThreads, (int)sizeof(DkvSmem<DT>), p.stream, mqh, mdoh, mk, mv,
+                          mdk, mdv, prm, sp, part);
+    if (st != LA_OK || sp.parts == 1) return st;
+    return launch_dependent(window_tc_sum<DT>, (unsigned)sum_ctas, 256, 0, p.stream, (const float *)part,
+                            static_cast<__nv_bfloat16 *>(p.dk), static_cast<__nv_bfloat16 *>(p.dv), sp, p.Nk, p.d, p.scale);
 }
 
 }  // namespace
+
+size_t window_backward_tc_scratch(const WindowProblem &p)
+{
+    return part_offset(p) + split_floats(p, split_of(p), p.d <= 64 ? 64 : 128) * 4;
+}
 
 la_status window_backward_tc(const WindowProblem &p)
 {

@@ -76,6 +76,14 @@ def test_padded_batches(dtype, Nq, Nk, d, window, sinks, lens):
     check(dtype, 3, 4, 2, Nq, Nk, d, window, sinks, lens=lens, spoil=True)
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("B,Hq,Hk,Nq,Nk,window,sinks,lens", [
+    (1, 4, 2, 2100, 2100, 64, 4, None), (2, 2, 1, 1500, 1600, 30, 200, [1600, 700])])
+def test_sinks_shared_out(d, B, Hq, Hk, Nq, Nk, window, sinks, lens):
+    """Sequences many windows long: the sinks' gradients are summed from several blocks."""
+    check("bf16", B, Hq, Hk, Nq, Nk, d, window, sinks, lens=lens, spoil=lens is not None)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_large_scores(dtype):
     """Scores of hundreds, which exp alone would overflow, and a scale of its own."""
