@@ -20,10 +20,11 @@ constexpr uint64_t kDrainNs = 100000000ull;
 
 struct Params {
     float *lse;        // forward: written; backward: read
-    float *delta;      // backward: dO . o per row
+    float *delta;      // backward: -dO . o of every row, then -lse / scale, rows of an entry `padded`
     const void *o;     // backward
     const int *lens;
-    int Hq, Hk, Nq, Nk, window, sinks, d;
+    int B, Hq, Hk, Nq, Nk, window, sinks, d;
+    int padded;  // Nq rounded up to whole tiles
     int units;   // CTAs per (entry, key head)
     int pairs;   // 1: the two tiles are the same rows of heads 2i, 2i + 1 of the group; 0: neighbouring rows
     float scale;
@@ -167,7 +168,8 @@ inline Params params_of(const WindowProblem &p)
     prm.delta = p.delta;
     prm.o = p.o;
     prm.lens = p.lens;
-    prm.Hq = p.Hq; prm.Hk = p.Hk; prm.Nq = p.Nq; prm.Nk = p.Nk;
+    prm.padded = tiles * kRows;
+    prm.B = p.B; prm.Hq = p.Hq; prm.Hk = p.Hk; prm.Nq = p.Nq; prm.Nk = p.Nk;
     prm.window = p.window; prm.sinks = p.sinks; prm.d = p.d;
     prm.scale = p.scale;
     prm.pairs = group % 2 == 0;

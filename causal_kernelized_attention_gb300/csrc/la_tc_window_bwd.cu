@@ -277,7 +277,12 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
                 }
             }
         }
-        if (t < prm.Nq) prm.delta[row] = delta;
+        // for the second kernel, rows of an entry padded to whole tiles
+        if (t0 < prm.Nq) {
+            const size_t at = (size_t)z * prm.padded + t;
+            prm.delta[at] = -delta;
+            prm.delta[(size_t)prm.B * prm.Hq * prm.padded + at] = -base;
+        }
         const uint64_t base2 = pair(-base, -base), delta2 = pair(-delta, -delta), c2 = pair(c, c);
         for (int done = 0; ok && done < tiles; ++done) {
             const int j0 = kt.tile(done) * kHalf;
@@ -390,9 +395,9 @@ struct DkvSmem {
     uint8_t v[kTile];  // then dv, staged
     uint8_t q[kRowStages][kStage];
     uint8_t go[kRowStages][kStage];
-    float base[kRowStages][kHalf], delta[kRowStages][kHalf];  // -lse / scale and -D of the rows
+    float delta[kRowStages][kHalf], base[kRowStages][kHalf];  // -D and -lse / scale of the rows
     uint64_t kv_full, s_full[2], ds_full[2], g_full;
-    uint64_t q_full[kRowStages], q_empty[kRowStages], l_full[kRowStages], drain;
+    uint64_t q_full[kRowStages], q_empty[kRowStages], drain;
     uint32_t tmem_base;
     int abort;
 };
@@ -419,7 +424,6 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         for (int i = 0; i < kRowStages; ++i) {
             mbar_init(&sm.q_full[i], 1);
             mbar_init(&sm.q_empty[i], 1);
-            mbar_init(&sm.l_full[i], 32);
         }
         mbar_init(&sm.drain, 1);
         sm.abort = (smem_u32(smem_raw) & 1023u) == 0 ? 0 : 1;
@@ -448,43 +452,33 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const int per = qt.end - qt.begin, all = per * group, share = shared ? unit % sp.parts : 0;
     const int x0 = shared ? (int)((long long)all * share / sp.parts) : 0;
     const int X = (shared ? (int)((long long)all * (share + 1) / sp.parts) : all) - x0;
-    const int rows = min(prm.Nq, n - off);               // rows of tokens
+    const int rows = min(prm.Nq, n - off);  // rows of tokens
 
     if (warp == kTmaWarp) {
-        bool ok = !aborted(abort_flag) && X > 0;
-        int loaded = 0;
-        if (ok && lane == 0) {
+        if (lane == 0 && X > 0 && !aborted(abort_flag)) {
             mbar_arrive_expect_tx(&sm.kv_full, 2 * kTile);
 #pragma unroll
             for (int x = 0; x < DT; x += 64) {
                 tma_load_3d(sm.k + x / 64 * kBox, &map_k, &sm.kv_full, x, j0, bh);
                 tma_load_3d(sm.v + x / 64 * kBox, &map_v, &sm.kv_full, x, j0, bh);
             }
-        }
-        for (int i = 0; ok && i < X; ++i) {
-            const int st = i % kRowStages, x = x0 + i;
-            const int t0 = (qt.begin + x % per) * kHalf, z = b * prm.Hq + hk * group + x / per;
-            if (i >= kRowStages && !(ok = wait_w(abort_flag, &sm.q_empty[st], (uint32_t)(i / kRowStages - 1) & 1u))) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&sm.q_full[st], 2 * kStage);
+            int loaded = 0;
+            for (int i = 0; i < X; ++i) {
+                const int st = i % kRowStages, x = x0 + i;
+                const int t0 = (qt.begin + x % per) * kHalf, z = b * prm.Hq + hk * group + x / per;
+                if (i >= kRowStages && !wait_b(abort_flag, &sm.q_empty[st], (uint32_t)(i / kRowStages - 1) & 1u)) break;
+                mbar_arrive_expect_tx(&sm.q_full[st], 2 * kStage + 2 * kHalf * 4);
 #pragma unroll
-                for (int x = 0; x < DT; x += 64) {
-                    tma_load_3d(sm.q[st] + x / 64 * kHalfBox, &map_q, &sm.q_full[st], x, t0, z);
-                    tma_load_3d(sm.go[st] + x / 64 * kHalfBox, &map_do, &sm.q_full[st], x, t0, z);
+                for (int c = 0; c < DT; c += 64) {
+                    tma_load_3d(sm.q[st] + c / 64 * kHalfBox, &map_q, &sm.q_full[st], c, t0, z);
+                    tma_load_3d(sm.go[st] + c / 64 * kHalfBox, &map_do, &sm.q_full[st], c, t0, z);
                 }
+                const float *row = prm.delta + (size_t)z * prm.padded + t0;
+                bulk_load(sm.delta[st], row, kHalf * 4, &sm.q_full[st]);
+                bulk_load(sm.base[st], row + (size_t)prm.B * prm.Hq * prm.padded, kHalf * 4, &sm.q_full[st]);
+                loaded = i + 1;
             }
-            loaded = i + 1;
-#pragma unroll
-            for (int e = lane; e < kHalf; e += 32) {
-                const bool in = t0 + e < rows;
-                const size_t at = (size_t)z * prm.Nq + t0 + e;
-                sm.base[st][e] = in ? -__ldcg(prm.lse + at) / prm.scale : 0.f;
-                sm.delta[st][e] = in ? -__ldcg(prm.delta + at) : 0.f;
-            }
-            mbar_arrive(&sm.l_full[st]);
-        }
-        if (lane == 0) {  // no copy may still be writing shared memory when the CTA exits
-            if (X > 0 && loaded > 0) drain(&sm.kv_full, 0);
+            drain(&sm.kv_full, 0);  // no copy may still be writing shared memory when the CTA exits
             for (int i = max(loaded - kRowStages, 0); i < loaded; ++i)
                 drain(&sm.q_full[i % kRowStages], (uint32_t)(i / kRowStages) & 1u);
         }
@@ -559,7 +553,7 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         bool ok = !aborted(abort_flag);
         for (int i = s; ok && i < X; i += 2) {
             const int st = i % kRowStages, p0 = (qt.begin + (x0 + i) % per) * kHalf + off;
-            if (!(ok = wait_w(abort_flag, &sm.l_full[st], (uint32_t)(i / kRowStages) & 1u))) break;
+            if (!(ok = wait_w(abort_flag, &sm.q_full[st], (uint32_t)(i / kRowStages) & 1u))) break;  // base, delta
             if (!(ok = wait_w(abort_flag, &sm.s_full[s], (uint32_t)(i >> 1) & 1u))) break;
             tc_fence_after();
             const bool whole = j0 + kRows - 1 <= p0 && p0 + kHalf - 1 < n &&
@@ -643,8 +637,8 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Scratch: D of every row, then the shares.
-size_t part_offset(const WindowProblem &p) { return ((size_t)p.B * p.Hq * p.Nq * 4 + 255) & ~(size_t)255; }
+// Scratch: -D and -lse / scale of every row (rows of an entry padded to whole tiles), then the shares.
+size_t part_offset(const WindowProblem &p) { return (size_t)p.B * p.Hq * ceil_div(p.Nq, kRows) * kRows * 2 * sizeof(float); }
 
 template <int DT>
 la_status backward(const WindowProblem &p)
