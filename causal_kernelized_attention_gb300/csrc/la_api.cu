@@ -667,12 +667,14 @@ la_status la_get_device_status(la_stream_t stream)
     if (st != LA_OK) return st;
     st = tc_backward_read_status((cudaStream_t)stream, &bw_bits);
     if (st != LA_OK) return st;
-    unsigned wn_bits = 0, wb_bits = 0;
+    unsigned wn_bits = 0, wb_bits = 0, rc_bits = 0;
     st = tc_window_read_status((cudaStream_t)stream, &wn_bits);
     if (st != LA_OK) return st;
     st = tc_window_bwd_read_status((cudaStream_t)stream, &wb_bits);
     if (st != LA_OK) return st;
-    wn_bits |= wb_bits;
+    st = recurrence_read_status((cudaStream_t)stream, &rc_bits);
+    if (st != LA_OK) return st;
+    wn_bits |= wb_bits | rc_bits;
     return ((bits | nc_bits | fv_bits | cc_bits | cl_bits | bw_bits | wn_bits) & kStatusTimeout) ? LA_ERR_TIMEOUT : LA_OK;
 }
 

@@ -126,6 +126,7 @@ la_status tc_cluster_read_status(cudaStream_t s, unsigned *bits);
 la_status tc_backward_read_status(cudaStream_t s, unsigned *bits);
 la_status tc_window_read_status(cudaStream_t s, unsigned *bits);
 la_status tc_window_bwd_read_status(cudaStream_t s, unsigned *bits);
+la_status recurrence_read_status(cudaStream_t s, unsigned *bits);
 
 // Failure-detection test hooks (la_test_set_wait_limit_ns, la_test_drop_publication):
 // the limit of the chunk-parallel causal kernel's bounded waits (2 s unless a test

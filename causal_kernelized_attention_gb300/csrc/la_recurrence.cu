@@ -8,14 +8,23 @@
 // token, so one kernel does both.  A run of tokens maps the state before it, c, to A c + H
 // with A the product of its gates and H its result from zero; runs compose as
 // (A2, H2) o (A1, H1) = (A2 A1, A2 H1 + H2), without a division, so gates of 0 are exact.
+// With the state before its run a warp then steps through the run itself, so every h_t is
+// rounded as the recurrence rounds it.
 //
 // Bound by memory: alpha and x are read once, h written once (4 + 2 e bytes an element,
-// e the size of x).  A thread holds a run of R tokens of kVec neighbouring channels in
-// registers, a CTA a tile of consecutive runs; runs are joined by shuffles within a warp
-// and through shared memory between warps.  A cluster of CTAs takes consecutive tiles of
-// the same channels and exchanges its CTAs' (A, H) through distributed shared memory once a
-// step, so a sequence is split over the machine when there are few channels, in one pass
-// over the data and without a flag in global memory to wait for.
+// e the size of x).  A CTA takes a tile of consecutive tokens of neighbouring channels, a
+// warp a run of them, a lane its channels; runs are joined through shared memory.  A cluster
+// of CTAs takes consecutive tiles of the same channels and its CTAs send each other their
+// (A, H) once a step, so a sequence is split over the machine when there are few channels, in
+// one pass over the data and without a flag in global memory to wait for.  The sends are
+// asynchronous stores counted on mbarriers: a cluster barrier in their place also waits for
+// the step's global stores (695 us instead of 347 at 65536 x 4096, forward).
+//
+// Rows of whole 16-byte vectors come in by TMA, kStages tiles of 64 tokens x 64 channels deep,
+// so that the bytes in flight depend neither on registers nor on occupancy; other widths by
+// plain loads, one channel a lane.
+#include <type_traits>
+
 #include "la_common.cuh"
 #include "la_internal.h"
 #include "la_tc_common.cuh"
@@ -28,15 +37,35 @@ using namespace sm100;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kRun = 8;              // tokens of a warp's run
+constexpr int kTok = kWarps * kRun;  // tokens of a tile
+constexpr int kStages = 3;
+
+static __device__ unsigned g_rec_status;
 
 // V neighbouring elements of type T.
-template <typename T, int V> struct alignas(sizeof(T) * V) Vec {
-    T x[V];
-};
+template <typename T, int V> struct alignas(sizeof(T) * V) Vec { T x[V]; };
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> ld(const T *p) { return *reinterpret_cast<const Vec<T, V> *>(p); }
 template <typename T, int V>
 __device__ __forceinline__ void st(T *p, const Vec<T, V> &v) { *reinterpret_cast<Vec<T, V> *>(p) = v; }
+template <typename T, int V>
+__device__ __forceinline__ Vec<float, V> ldf(const T *p)
+{
+    const Vec<T, V> v = ld<T, V>(p);
+    Vec<float, V> f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) f.x[i] = Elem<T>::to_f32(v.x[i]);
+    return f;
+}
+template <typename T, int V>
+__device__ __forceinline__ void stf(T *p, const Vec<float, V> &f)
+{
+    Vec<T, V> v;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v.x[i] = Elem<T>::from_f32(f.x[i]);
+    st<T, V>(p, v);
+}
 
 template <typename T>
 struct Args {
@@ -51,215 +80,253 @@ struct Args {
     int N, D, steps;
 };
 
-// kVec channels a thread, kCL lanes of a warp side by side over channels (the other
-// 32 / kCL one after the other in time), kR tokens a thread.
-template <typename T, int kVec, int kCL, int kR, bool kBack>
-__global__ void __launch_bounds__(kThreads) recurrence_kernel(const __grid_constant__ Args<T> a)
+template <typename T, bool kBack>
+struct Tiles {  // the TMA ring
+    float alpha[kStages][kTok][64];
+    T x[kStages][kTok][64];
+    T h[kBack ? kStages : 1][kBack ? kTok : 1][64];
+};
+struct NoTiles {};
+
+template <typename T, bool kBack, bool kTma>
+struct Smem {
+    static constexpr int kPer = kTma ? 2 : 1, kCh = 32 * kPer;  // channels of a lane, of a CTA
+    typename std::conditional<kTma, Tiles<T, kBack>, NoTiles>::type t;
+    alignas(16) float wA[2][kWarps][kCh];  // the warps' runs, by step parity
+    float wH[2][kWarps][kCh];
+    float cA[2][kMaxCluster][kCh], cH[2][kMaxCluster][kCh];  // the cluster's tiles
+    uint64_t full[kStages], sent[2];
+    int abort;
+};
+
+template <typename T, bool kBack, bool kTma>
+__global__ void __launch_bounds__(kThreads)
+recurrence_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
+                  const __grid_constant__ CUtensorMap map_h, const __grid_constant__ Args<T> a)
 {
-    constexpr int kTL = 32 / kCL;
-    constexpr int kC = kCL * kVec;               // channels of a CTA
-    constexpr int kTile = kWarps * kTL * kR;     // tokens of a CTA's tile
-    __shared__ __align__(16) float wA[kWarps][kC], wH[kWarps][kC];
-    __shared__ __align__(16) float cA[2][kMaxCluster][kC], cH[2][kMaxCluster][kC];
-
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int cl = lane % kCL, tl = lane / kCL;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    typedef Smem<T, kBack, kTma> S_;
+    S_ &sm = *reinterpret_cast<S_ *>(smem_raw);
+    constexpr int kPer = S_::kPer, kCh = S_::kCh;
+    typedef Vec<float, kPer> F;
+    constexpr uint32_t kBytes = kTok * kCh * (4 + (kBack ? 2 : 1) * sizeof(T));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lc = kPer * lane;
     const uint32_t S = cluster_size(), rank = S > 1 ? cluster_ctarank() : 0;
-    const int groups = (a.D + kC - 1) / kC;
-    const int unit = (int)(blockIdx.x / S);
-    const int b = unit / groups, ch = (unit % groups) * kC + cl * kVec;
-    const bool live = ch < a.D;
-    const size_t base = (size_t)b * a.N * a.D + ch;
+    const int groups = (a.D + kCh - 1) / kCh, unit = (int)(blockIdx.x / S);
+    const int b = unit / groups, c0 = (unit % groups) * kCh, ch = c0 + lc;
+    const bool live = ch < a.D;  // (D is even where a lane has two channels)
 
-    float carry[kVec];  // the state before the cluster's step
-#pragma unroll
-    for (int v = 0; v < kVec; ++v) carry[v] = 0.f;
-    const float *first = kBack ? a.dhN : a.h0;
-    if (first && live) {
-        const Vec<float, kVec> f = ld<float, kVec>(first + (size_t)b * a.D + ch);
-#pragma unroll
-        for (int v = 0; v < kVec; ++v) carry[v] = f.x[v];
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&sm.full[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&sm.sent[i], 1);
+        sm.abort = 0;
+        fence_mbar_init();
     }
+    if (S > 1)
+        cluster_sync_all();  // every CTA of the cluster runs before its memory is written
+    else
+        __syncthreads();
 
-    if (S > 1) cluster_sync_all();  // every CTA of the cluster runs before its memory is written
+    // scan index of this CTA's first token of a step; token t = i (forward), N - 1 - i (backward):
+    // the backward's tiles lie in memory order, and are read from their last row
+    auto first_of = [&](int step) { return ((long long)step * S + rank) * kTok; };
+    auto fetch = [&](int step) {
+        if constexpr (kTma) {
+            const long long i0 = first_of(step);
+            if (step >= a.steps || i0 >= a.N) return;
+            const int s = step % kStages, t0 = kBack ? (int)(a.N - i0 - kTok) : (int)i0;
+            mbar_arrive_expect_tx(&sm.full[s], kBytes);
+            tma_load_3d(sm.t.alpha[s], &map_a, &sm.full[s], c0, kBack ? t0 + 1 : t0, b);
+            tma_load_3d(sm.t.x[s], &map_x, &sm.full[s], c0, t0, b);
+            if (kBack) tma_load_3d(sm.t.h[s], &map_h, &sm.full[s], c0, t0 - 1, b);
+        }
+    };
+    if (kTma && tid == 0)
+        for (int i = 0; i < kStages; ++i) fetch(i);
+
+    F carry, h0;  // carry: the state before the cluster's step
+#pragma unroll
+    for (int v = 0; v < kPer; ++v) carry.x[v] = h0.x[v] = 0.f;
+    const size_t base = (size_t)b * a.N * a.D + ch, at_b = (size_t)b * a.D + ch;
+    if (live && (kBack ? a.dhN : a.h0)) carry = ld<float, kPer>((kBack ? a.dhN : a.h0) + at_b);
+    if (kBack && live && a.h0) h0 = ld<float, kPer>(a.h0 + at_b);
+
+    bool ok = true;
     for (int step = 0; step < a.steps; ++step) {
-        // scan index of this thread's first token; token t = i (forward), N - 1 - i (backward)
-        const long long i0 = ((long long)step * S + rank) * kTile + (warp * kTL + tl) * kR;
-        Vec<float, kVec> al[kR];
-        Vec<T, kVec> xv[kR], hv[kR];
+        const int par = step & 1;
+        const long long i0 = first_of(step);
+        const int left = (int)min((long long)kTok, max(a.N - i0, 0ll));  // tokens of this tile
+        F al[kRun], xv[kRun], hv[kRun];
+        if constexpr (kTma) {
+            const int s = step % kStages;
+            if (left > 0) {
+                if (ok) ok = tc::wait_bar(&g_rec_status, &sm.abort, &sm.full[s], (uint32_t)(step / kStages) & 1u);
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
-            const long long i = i0 + r;
-            const bool in = live && i < a.N;
-            const long long t = kBack ? a.N - 1 - i : i;
-#pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                al[r].x[v] = 1.f;  // past the end: the identity
-                xv[r].x[v] = Elem<T>::from_f32(0.f);
-                hv[r].x[v] = Elem<T>::from_f32(0.f);
-            }
-            if (in) {
-                const size_t o = base + (size_t)t * a.D;
-                if (!kBack)
-                    al[r] = ld<float, kVec>(a.alpha + o);
-                else if (i > 0)
-                    al[r] = ld<float, kVec>(a.alpha + o + a.D);
-                xv[r] = ld<T, kVec>(a.x + o);
-                if (kBack && t > 0) hv[r] = ld<T, kVec>(a.h_in + o - a.D);
-            }
-        }
-        // this thread's run
-        float A[kVec], H[kVec];
-#pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-            A[v] = 1.f;
-            H[v] = 0.f;
-        }
-#pragma unroll
-        for (int r = 0; r < kR; ++r)
-#pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                H[v] = fmaf(al[r].x[v], H[v], Elem<T>::to_f32(xv[r].x[v]));
-                A[v] *= al[r].x[v];
-            }
-        // inclusive scan over the warp's runs of the same channels
-#pragma unroll
-        for (int m = 1; m < kTL; m *= 2)
-#pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                const float pa = __shfl_up_sync(0xffffffffu, A[v], m * kCL);
-                const float ph = __shfl_up_sync(0xffffffffu, H[v], m * kCL);
-                if (tl >= m) {
-                    H[v] = fmaf(A[v], ph, H[v]);
-                    A[v] *= pa;
+                for (int r = 0; r < kRun; ++r) {
+                    const int k = warp * kRun + r, row = kBack ? kTok - 1 - k : k;
+                    al[r] = ld<float, kPer>(&sm.t.alpha[s][row][lc]);
+                    xv[r] = ldf<T, kPer>(&sm.t.x[s][row][lc]);
+                    if (kBack) hv[r] = ldf<T, kPer>(&sm.t.h[s][row][lc]);
                 }
             }
-        if (tl == kTL - 1)
+        } else {
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                wA[warp][cl * kVec + v] = A[v];
-                wH[warp][cl * kVec + v] = H[v];
+            for (int r = 0; r < kRun; ++r) {
+                const int k = warp * kRun + r;
+                if (k < left && live) {
+                    const long long t = kBack ? a.N - 1 - (i0 + k) : i0 + k;
+                    const size_t o = base + (size_t)t * a.D;
+                    if (!kBack || i0 + k > 0) al[r] = ld<float, kPer>(a.alpha + o + (kBack ? a.D : 0));
+                    xv[r] = ldf<T, kPer>(a.x + o);
+                    if (kBack && t > 0) hv[r] = ldf<T, kPer>(a.h_in + o - a.D);
+                }
             }
-        __syncthreads();
-        // the runs before this warp's in the CTA, and the whole CTA's
-        float pA[kVec], pH[kVec], tA[kVec], tH[kVec];
+        }
+        if (left < kTok || (kBack && i0 == 0)) {
 #pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-            tA[v] = 1.f;
-            tH[v] = 0.f;
-            pA[v] = 1.f;
-            pH[v] = 0.f;
+            for (int r = 0; r < kRun; ++r) {
+                const int k = warp * kRun + r;
+#pragma unroll
+                for (int v = 0; v < kPer; ++v) {
+                    // past the end: the identity; the last token's state has no later gate
+                    if (k >= left || (kBack && i0 + k == 0)) al[r].x[v] = 1.f;
+                    if (k >= left) xv[r].x[v] = 0.f;
+                }
+            }
+        }
+        F A, H;
+#pragma unroll
+        for (int v = 0; v < kPer; ++v) {
+            A.x[v] = 1.f;
+            H.x[v] = 0.f;
+#pragma unroll
+            for (int r = 0; r < kRun; ++r) {
+                H.x[v] = fmaf(al[r].x[v], H.x[v], xv[r].x[v]);
+                A.x[v] *= al[r].x[v];
+            }
+        }
+        st<float, kPer>(&sm.wA[par][warp][lc], A);
+        st<float, kPer>(&sm.wH[par][warp][lc], H);
+        __syncthreads();  // the runs are written, and the stage is read
+        if (tid == 0) {
+            if (kTma) fetch(step + kStages);
+            if (S > 1) mbar_arrive_expect_tx(&sm.sent[par], S * kCh * 2 * 4);
+        }
+        // the runs before this warp's in the CTA, and the whole CTA's
+        F pA, pH, tA, tH;
+#pragma unroll
+        for (int v = 0; v < kPer; ++v) {
+            pA.x[v] = tA.x[v] = 1.f;
+            pH.x[v] = tH.x[v] = 0.f;
         }
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const Vec<float, kVec> xa = ld<float, kVec>(&wA[w][cl * kVec]), xh = ld<float, kVec>(&wH[w][cl * kVec]);
+            if (w == warp) {
+                pA = tA;
+                pH = tH;
+            }
+            const F xa = ld<float, kPer>(&sm.wA[par][w][lc]), xh = ld<float, kPer>(&sm.wH[par][w][lc]);
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                if (w == warp) {
-                    pA[v] = tA[v];
-                    pH[v] = tH[v];
-                }
-                tH[v] = fmaf(xa.x[v], tH[v], xh.x[v]);
-                tA[v] *= xa.x[v];
+            for (int v = 0; v < kPer; ++v) {
+                tH.x[v] = fmaf(xa.x[v], tH.x[v], xh.x[v]);
+                tA.x[v] *= xa.x[v];
             }
         }
-        float before[kVec];  // the state before this warp's runs
+        F at = carry;  // the state before this CTA's tile
         if (S > 1) {
-            const int slot = step & 1;
-            // warp w sends to rank w; the slots alternate, so a CTA still reading this
-            // step's is never overtaken (a writer of the slot after next has passed the
-            // barrier of the next step)
-            if (warp < (int)S && tl == 0) {
-                const uint32_t da = mapa_shared(smem_u32(&cA[slot][rank][cl * kVec]), warp);
-                const uint32_t dh = mapa_shared(smem_u32(&cH[slot][rank][cl * kVec]), warp);
-#pragma unroll
-                for (int v = 0; v < kVec; ++v) {
-                    st_dsmem_f32(da + 4 * v, tA[v]);
-                    st_dsmem_f32(dh + 4 * v, tH[v]);
+            // Warp w sends to rank w.  The slots alternate: a CTA that still reads this step's has
+            // not sent its next tile, which whoever writes the slot again waits for first.
+            if (warp < (int)S) {
+                const uint32_t bar = mapa_shared(smem_u32(&sm.sent[par]), warp);
+                const uint32_t da = mapa_shared(smem_u32(&sm.cA[par][rank][lc]), warp);
+                const uint32_t dh = mapa_shared(smem_u32(&sm.cH[par][rank][lc]), warp);
+                if constexpr (kPer == 2) {
+                    st_async_f32x2(da, tA.x[0], tA.x[1], bar);
+                    st_async_f32x2(dh, tH.x[0], tH.x[1], bar);
+                } else {
+                    st_async_f32(da, tA.x[0], bar);
+                    st_async_f32(dh, tH.x[0], bar);
                 }
             }
-            cluster_sync_all();
-            float at[kVec];
-#pragma unroll
-            for (int v = 0; v < kVec; ++v) at[v] = carry[v];
+            if (ok) ok = tc::wait_bar(&g_rec_status, &sm.abort, &sm.sent[par], (uint32_t)(step >> 1) & 1u);
             for (uint32_t w = 0; w < S; ++w) {
-                const Vec<float, kVec> xa = ld<float, kVec>(&cA[slot][w][cl * kVec]),
-                                       xh = ld<float, kVec>(&cH[slot][w][cl * kVec]);
+                const F xa = ld<float, kPer>(&sm.cA[par][w][lc]), xh = ld<float, kPer>(&sm.cH[par][w][lc]);
+                if (w == rank) at = carry;
 #pragma unroll
-                for (int v = 0; v < kVec; ++v) {
-                    if (w == rank) at[v] = carry[v];
-                    carry[v] = fmaf(xa.x[v], carry[v], xh.x[v]);
-                }
+                for (int v = 0; v < kPer; ++v) carry.x[v] = fmaf(xa.x[v], carry.x[v], xh.x[v]);
             }
-#pragma unroll
-            for (int v = 0; v < kVec; ++v) before[v] = fmaf(pA[v], at[v], pH[v]);
         } else {
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                before[v] = fmaf(pA[v], carry[v], pH[v]);
-                carry[v] = fmaf(tA[v], carry[v], tH[v]);
-            }
+            for (int v = 0; v < kPer; ++v) carry.x[v] = fmaf(tA.x[v], carry.x[v], tH.x[v]);
         }
-        // the state before this thread's run: through the lanes before it
-        float c[kVec];
+        F c;
 #pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-            const float pa = __shfl_up_sync(0xffffffffu, A[v], kCL % 32), ph = __shfl_up_sync(0xffffffffu, H[v], kCL % 32);
-            c[v] = tl > 0 ? fmaf(pa, before[v], ph) : before[v];
-        }
+        for (int v = 0; v < kPer; ++v) c.x[v] = fmaf(pA.x[v], at.x[v], pH.x[v]);
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
-            const long long i = i0 + r;
-            const bool in = live && i < a.N;
-            const long long t = kBack ? a.N - 1 - i : i;
-            Vec<T, kVec> o;
-            Vec<float, kVec> da;
+        for (int r = 0; r < kRun; ++r) {
+            const int k = warp * kRun + r;
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                c[v] = fmaf(al[r].x[v], c[v], Elem<T>::to_f32(xv[r].x[v]));
-                o.x[v] = Elem<T>::from_f32(c[v]);
-            }
-            if (in) {
-                const size_t at = base + (size_t)t * a.D;
-                st<T, kVec>(a.out + at, o);
+            for (int v = 0; v < kPer; ++v) c.x[v] = fmaf(al[r].x[v], c.x[v], xv[r].x[v]);
+            if (k < left && live) {
+                const long long t = kBack ? a.N - 1 - (i0 + k) : i0 + k;
+                const size_t o = base + (size_t)t * a.D;
+                stf<T, kPer>(a.out + o, c);
                 if (kBack) {
-                    Vec<float, kVec> hp;
+                    F da;
 #pragma unroll
-                    for (int v = 0; v < kVec; ++v) hp.x[v] = Elem<T>::to_f32(hv[r].x[v]);
-                    if (t == 0 && a.h0) hp = ld<float, kVec>(a.h0 + (size_t)b * a.D + ch);
-#pragma unroll
-                    for (int v = 0; v < kVec; ++v) da.x[v] = c[v] * hp.x[v];
-                    st<float, kVec>(a.dalpha + at, da);
+                    for (int v = 0; v < kPer; ++v) da.x[v] = c.x[v] * (t == 0 ? h0.x[v] : hv[r].x[v]);
+                    st<float, kPer>(a.dalpha + o, da);
                 }
             }
         }
-        __syncthreads();  // wA, wH are rewritten by the next step
     }
     // the state after the last token (forward), or alpha_0 g_0 (backward)
-    if (a.last && rank == 0 && warp == 0 && tl == 0 && live) {
-        Vec<float, kVec> o;
-#pragma unroll
-        for (int v = 0; v < kVec; ++v) o.x[v] = carry[v];
+    if (a.last && rank == 0 && warp == 0 && live) {
         if (kBack && a.N > 0) {
-            const Vec<float, kVec> f = ld<float, kVec>(a.alpha + base);
+            const F f = ld<float, kPer>(a.alpha + base);
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) o.x[v] *= f.x[v];
+            for (int v = 0; v < kPer; ++v) carry.x[v] *= f.x[v];
         }
-        st<float, kVec>(a.last + (size_t)b * a.D + ch, o);
+        st<float, kPer>(a.last + at_b, carry);
+    }
+    if (!ok) {  // a wait ran out: nothing may still arrive in this CTA's shared memory when it exits
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 100000000ull) {
+        }
     }
 }
 
-template <typename T, int kVec, int kCL, int kR, bool kBack>
+// [B, N, D] as a 3-D tensor (D, N, B); box = 64 channels x 64 tokens.
+la_status tile_map(CUtensorMap *m, const void *ptr, bool f32, int B, int N, int D)
+{
+    tc::EncodeTiledFn enc;
+    la_status st = tc::encode_fn(&enc);
+    if (st == LA_OK) st = tc::bind_thread_context();
+    if (st != LA_OK) return st;
+    const cuuint64_t e = f32 ? 4 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)B};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * e, (cuuint64_t)N * D * e};
+    const cuuint32_t box[3] = {64, kTok, 1}, estr[3] = {1, 1, 1};
+    const CUresult r = enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                           const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? LA_OK : cuda_status(cudaErrorInvalidValue);
+}
+
+template <typename T, bool kBack, bool kTma>
 la_status launch(const RecurrenceProblem &p)
 {
-    constexpr int kTile = kWarps * (32 / kCL) * kR, kC = kCL * kVec;
-    auto kern = recurrence_kernel<T, kVec, kCL, kR, kBack>;
-    const long long units = (long long)p.B * ceil_div(p.D, kC);
-    const int tiles = (int)(((long long)p.N + kTile - 1) / kTile);
-    // Split a sequence over a cluster while its CTAs still all run at once: two resident
-    // CTAs an SM are enough to keep the memory busy.
+    auto kern = recurrence_kernel<T, kBack, kTma>;
+    constexpr size_t smem = sizeof(Smem<T, kBack, kTma>);
+    constexpr bool f32 = sizeof(T) == 4;
+    const long long units = (long long)p.B * ceil_div(p.D, Smem<T, kBack, kTma>::kCh);
+    const long long tiles = ((long long)p.N + kTok - 1) / kTok;
+    // CTAs a sequence and group of channels: as many as run at once (two an SM where shared
+    // memory allows), none without a tile of its own.
+    constexpr int resident = smem <= 113 * 1024 ? 2 : 1;
     int S = 1;
-    while (S < kMaxCluster && S < tiles && units * S * 2 <= 2LL * tc::sm_count()) S *= 2;
+    while (S < kMaxCluster && S < tiles && units * S * 2 <= (long long)resident * tc::sm_count()) S *= 2;
     if (units * S > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
     Args<T> a;
     a.x = static_cast<const T *>(kBack ? p.dh : p.x);
@@ -272,10 +339,19 @@ la_status launch(const RecurrenceProblem &p)
     a.last = kBack ? p.dh0 : p.hN;
     a.N = p.N;
     a.D = p.D;
-    a.steps = (tiles + S - 1) / S;
+    a.steps = (int)((tiles + S - 1) / S);
+    CUtensorMap ma{}, mx{}, mh{};
+    la_status st = ensure_smem((const void *)kern, (int)smem);
+    if (kTma) {
+        if (st == LA_OK) st = tile_map(&ma, p.alpha, true, p.B, p.N, p.D);
+        if (st == LA_OK) st = tile_map(&mx, a.x, f32, p.B, p.N, p.D);
+        if (st == LA_OK && kBack) st = tile_map(&mh, p.h_in, f32, p.B, p.N, p.D);
+    }
+    if (st != LA_OK) return st;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)(units * S));
     lc.blockDim = dim3(kThreads);
+    lc.dynamicSmemBytes = smem;
     lc.stream = p.stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -284,15 +360,15 @@ la_status launch(const RecurrenceProblem &p)
     lc.attrs = at;
     lc.numAttrs = S > 1 ? 1 : 0;
     count_launches();
-    return cuda_status(cudaLaunchKernelEx(&lc, kern, a));
+    return cuda_status(cudaLaunchKernelEx(&lc, kern, ma, mx, mh, a));
 }
 
 template <typename T, bool kBack>
 la_status pick(const RecurrenceProblem &p)
 {
-    // Rows are whole 16-byte vectors of gates only when D is a multiple of 4.
-    if (p.D % 4 == 0) return launch<T, 4, 8, 8, kBack>(p);
-    return launch<T, 1, 32, 16, kBack>(p);
+    // TMA wants rows of whole 16-byte vectors, and a sequence to describe
+    if (p.D % (int)(16 / sizeof(T)) == 0 && p.N > 0) return launch<T, kBack, true>(p);
+    return launch<T, kBack, false>(p);
 }
 
 // ---------------------------------------------------------------- one token
@@ -334,6 +410,15 @@ la_status recurrence(const RecurrenceProblem &p)
 {
     if (p.dtype == LA_BF16) return p.backward ? pick<__nv_bfloat16, true>(p) : pick<__nv_bfloat16, false>(p);
     return p.backward ? pick<float, true>(p) : pick<float, false>(p);
+}
+
+la_status recurrence_read_status(cudaStream_t s, unsigned *bits)
+{
+    unsigned zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_rec_status, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_rec_status, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    return cuda_status(e);
 }
 
 la_status recurrence_step(float *state, const void *x, const float *alpha, void *h, int B, int D, la_dtype dtype,

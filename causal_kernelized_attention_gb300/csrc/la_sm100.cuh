@@ -341,10 +341,19 @@ __device__ __forceinline__ float ld_dsmem_f32(uint32_t a)
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
 }
-// Stores to another CTA's shared memory.
-__device__ __forceinline__ void st_dsmem_f32(uint32_t a, float v)
+// Asynchronous stores to a CTA's shared memory that count their bytes on an mbarrier of the
+// same CTA (both shared::cluster addresses).  Unlike a cluster barrier's release they order
+// nothing else, so they do not wait for the thread's outstanding global stores.
+__device__ __forceinline__ void st_async_f32(uint32_t a, float v, uint32_t bar)
 {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(a), "f"(v), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void st_async_f32x2(uint32_t a, float v0, float v1, uint32_t bar)
+{
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(a), "f"(v0),
+                 "f"(v1), "r"(bar)
+                 : "memory");
 }
 // Arrive on an mbarrier of another CTA of the cluster (shared::cluster address),
 // releasing this thread's prior writes at cluster scope.
