@@ -18,9 +18,12 @@
 // (A, H) once a step, so a sequence is split over the machine when there are few channels, in
 // one pass over the data and without a flag in global memory to wait for.  The sends are
 // asynchronous stores counted on mbarriers: a cluster barrier in their place also waits for
-// the step's global stores (695 us instead of 347 at 65536 x 4096, forward).
+// the step's global stores (695 us instead of 347 at 65536 x 4096, forward, on tiles of 64).
 //
-// Rows of whole 16-byte vectors come in by TMA, kStages tiles of 64 tokens x 64 channels deep,
+// Measured at 65536 x 4096, bf16: forward 326 us (6.6 TB/s), backward 540 us (7.0 TB/s); fp32
+// backward 852 us (6.3 TB/s).  4 x 2048 x 512 forward 7.2 us (4.6 TB/s, two steps of a cluster).
+//
+// Rows of whole 16-byte vectors come in by TMA, kStages tiles of 128 tokens x 64 channels deep,
 // so that the bytes in flight depend neither on registers nor on occupancy; other widths by
 // plain loads, one channel a lane.
 #include <type_traits>
@@ -37,9 +40,8 @@ using namespace sm100;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kRun = 8;              // tokens of a warp's run
+constexpr int kRun = 16;             // tokens of a warp's run
 constexpr int kTok = kWarps * kRun;  // tokens of a tile
-constexpr int kStages = 3;
 
 static __device__ unsigned g_rec_status;
 
@@ -80,34 +82,39 @@ struct Args {
     int N, D, steps;
 };
 
-template <typename T, bool kBack>
+template <typename T, bool kBack, bool kDeep>
 struct Tiles {  // the TMA ring
+    static constexpr int kBytes = kTok * 64 * (4 + (kBack ? 2 : 1) * (int)sizeof(T));
+    static constexpr int kStages = (kDeep ? 196 : 100) * 1024 / kBytes;
     float alpha[kStages][kTok][64];
     T x[kStages][kTok][64];
     T h[kBack ? kStages : 1][kBack ? kTok : 1][64];
 };
-struct NoTiles {};
+struct NoTiles {
+    static constexpr int kStages = 1;
+};
 
-template <typename T, bool kBack, bool kTma>
+template <typename T, bool kBack, bool kTma, bool kDeep>
 struct Smem {
     static constexpr int kPer = kTma ? 2 : 1, kCh = 32 * kPer;  // channels of a lane, of a CTA
-    typename std::conditional<kTma, Tiles<T, kBack>, NoTiles>::type t;
+    typedef typename std::conditional<kTma, Tiles<T, kBack, kDeep>, NoTiles>::type Ring;
+    Ring t;
     alignas(16) float wA[2][kWarps][kCh];  // the warps' runs, by step parity
     float wH[2][kWarps][kCh];
     float cA[2][kMaxCluster][kCh], cH[2][kMaxCluster][kCh];  // the cluster's tiles
-    uint64_t full[kStages], sent[2];
+    uint64_t full[Ring::kStages], sent[2];
     int abort;
 };
 
-template <typename T, bool kBack, bool kTma>
+template <typename T, bool kBack, bool kTma, bool kDeep>
 __global__ void __launch_bounds__(kThreads)
 recurrence_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
                   const __grid_constant__ CUtensorMap map_h, const __grid_constant__ Args<T> a)
 {
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    typedef Smem<T, kBack, kTma> S_;
+    typedef Smem<T, kBack, kTma, kDeep> S_;
     S_ &sm = *reinterpret_cast<S_ *>(smem_raw);
-    constexpr int kPer = S_::kPer, kCh = S_::kCh;
+    constexpr int kPer = S_::kPer, kCh = S_::kCh, kStages = S_::Ring::kStages;
     typedef Vec<float, kPer> F;
     constexpr uint32_t kBytes = kTok * kCh * (4 + (kBack ? 2 : 1) * sizeof(T));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lc = kPer * lane;
@@ -296,7 +303,7 @@ recurrence_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     }
 }
 
-// [B, N, D] as a 3-D tensor (D, N, B); box = 64 channels x 64 tokens.
+// [B, N, D] as a 3-D tensor (D, N, B); box = 64 channels x 128 tokens.
 la_status tile_map(CUtensorMap *m, const void *ptr, bool f32, int B, int N, int D)
 {
     tc::EncodeTiledFn enc;
@@ -314,13 +321,13 @@ la_status tile_map(CUtensorMap *m, const void *ptr, bool f32, int B, int N, int 
     return r == CUDA_SUCCESS ? LA_OK : cuda_status(cudaErrorInvalidValue);
 }
 
-template <typename T, bool kBack, bool kTma>
+template <typename T, bool kBack, bool kTma, bool kDeep = false>
 la_status launch(const RecurrenceProblem &p)
 {
-    auto kern = recurrence_kernel<T, kBack, kTma>;
-    constexpr size_t smem = sizeof(Smem<T, kBack, kTma>);
+    auto kern = recurrence_kernel<T, kBack, kTma, kDeep>;
+    constexpr size_t smem = sizeof(Smem<T, kBack, kTma, kDeep>);
     constexpr bool f32 = sizeof(T) == 4;
-    const long long units = (long long)p.B * ceil_div(p.D, Smem<T, kBack, kTma>::kCh);
+    const long long units = (long long)p.B * ceil_div(p.D, Smem<T, kBack, kTma, kDeep>::kCh);
     const long long tiles = ((long long)p.N + kTok - 1) / kTok;
     // CTAs a sequence and group of channels: as many as run at once (two an SM where shared
     // memory allows), none without a tile of its own.
@@ -367,8 +374,15 @@ template <typename T, bool kBack>
 la_status pick(const RecurrenceProblem &p)
 {
     // TMA wants rows of whole 16-byte vectors, and a sequence to describe
-    if (p.D % (int)(16 / sizeof(T)) == 0 && p.N > 0) return launch<T, kBack, true>(p);
-    return launch<T, kBack, false>(p);
+    if (p.D % (int)(16 / sizeof(T)) != 0 || p.N == 0) return launch<T, kBack, false>(p);
+    // The bf16 backward's tile is 64 KB.  Where clusters of at most two fill the machine, one
+    // CTA an SM with three tiles in its ring measures 538 us at 65536 x 4096 (7.0 TB/s), two
+    // CTAs with one tile each 630; with larger clusters, which then need whole groups of free
+    // SMs, it is 289 against 203 us (65536 x 1024).  The other forms' tiles fit twice in 100 KB
+    // (or are within 2% either way).
+    if (kBack && sizeof(T) == 2 && (long long)p.B * ceil_div(p.D, 64) * 4 > tc::sm_count())
+        return launch<T, kBack, true, (kBack && sizeof(T) == 2)>(p);
+    return launch<T, kBack, true>(p);
 }
 
 // ---------------------------------------------------------------- one token
