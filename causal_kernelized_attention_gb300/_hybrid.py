@@ -6,36 +6,73 @@ device (on ``stream``, or that device's current stream).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
-from ._binding import RotarySpec, _check, _dtype_code, _need_cuda, _same_dtype, load_library
+from ._binding import LA_BF16, LA_F32, RotarySpec, _check, load_library
 
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "ramp": 3}
 
 
+_entry = {}  # C entry points by name
+torch = None  # imported by the first call (the package itself imports without it)
+
+
+def _start():
+    global torch
+    import torch as module
+    torch = module
+
+
 def _place(*ts):
-    """Checks that the tensors given are contiguous and on one CUDA device; returns it."""
-    ts = [t for t in ts if t is not None]
-    _need_cuda(*ts)
-    dev = ts[0].device
-    for t in ts[1:]:
-        if t.device != dev:
+    """Checks that the tensors given are contiguous and on one CUDA device; returns its index."""
+    dev = -1
+    for t in ts:
+        if t is None:
+            continue
+        i = t.get_device()
+        if i < 0:
+            raise ValueError("tensors must be on a CUDA device")
+        if dev >= 0 and i != dev:
             raise ValueError("tensors must be on one device")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        dev = i
     return dev
 
 
 def _call(name, dev, stream, *args):
-    """The C entry point with its device current, on `stream` or the device's current stream."""
-    import torch
-    fn = getattr(load_library(), name)
-    with contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev):
-        s = torch.cuda.current_stream(dev) if stream is None else stream
-        if s.device != dev:
-            raise ValueError("stream must be on the tensors' device")
-        _check(name, fn(*args, ctypes.c_void_p(s.cuda_stream)))
+    """The C entry point with device `dev` current, on `stream` or the device's current stream."""
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(load_library(), name)
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError("stream must be on the tensors' device")
+    else:
+        s = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, s)
+    if st:
+        _check(name, st)
+
+
+def _dtype_code(first, *others):
+    """The element type that all the tensors share, as the library counts it."""
+    d = first.dtype
+    for t in others:
+        if t is not None and t.dtype is not d:
+            raise TypeError("tensors must share one dtype")
+    if d is torch.bfloat16:
+        return LA_BF16
+    if d is torch.float32:
+        return LA_F32
+    raise TypeError("tensors must be float32 or bfloat16, got %s" % d)
 
 
 def _ptr(t):
@@ -43,13 +80,29 @@ def _ptr(t):
 
 
 def _shaped(what, t, shape, dtype=None):
-    if t is not None and (tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype)):
+    if t is not None and (t.shape != shape or (dtype is not None and t.dtype is not dtype)):
         raise ValueError("%s must be %s%s" % (what, "" if dtype is None else "%s " % dtype, list(shape)))
+
+
+def _sizes(t):
+    """The tensor's sizes, which the library takes as 32-bit numbers."""
+    if t.numel() >= 2 ** 31 and max(t.shape) >= 2 ** 31:
+        raise ValueError("sizes must fit 32 bits")
+    return t.shape
+
+
+def _int(what, v):
+    if type(v) is not int:
+        v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError("%s must fit 32 bits" % what)
+    return v
 
 
 # ---------------------------------------------------------------- rotary positions
 def _rotary(name, q, k, oq, ok, positions, offset, rot, layout, base, scaling, factor, original, ramp, amplitude, stream):
-    import torch
+    if torch is None:
+        _start()
     if q.dim() not in (3, 4) or (k is not None and k.dim() != q.dim()):
         raise ValueError("q and k must be [B, H, N, d], or [B, H, d] for one token")
     if k is None and ok is not None:
@@ -57,21 +110,21 @@ def _rotary(name, q, k, oq, ok, positions, offset, rot, layout, base, scaling, f
     oq = torch.empty_like(q) if oq is None else oq
     ok = torch.empty_like(k) if ok is None and k is not None else ok
     dev = _place(q, k, oq, ok, positions)
-    _same_dtype(*[t for t in (q, k, oq, ok) if t is not None])
-    B, Hq, N, d = q.shape if q.dim() == 4 else (q.shape[0], q.shape[1], 1, q.shape[2])
+    code = _dtype_code(q, oq, k, ok)
+    B, Hq, N, d = _sizes(q) if q.dim() == 4 else (q.shape[0], q.shape[1], 1, q.shape[2])
     Hk = 0 if k is None else k.shape[1]
     _shaped("k", k, (B, Hk) + tuple(q.shape[2:]))
     _shaped("the output for q", oq, q.shape)
     _shaped("the output for k", ok, () if k is None else k.shape)
-    if positions is not None and (positions.dtype != torch.int32 or tuple(positions.shape) != (B, N)
-                                  and not (q.dim() == 3 and tuple(positions.shape) == (B,))):
+    if positions is not None and (positions.dtype is not torch.int32 or positions.shape != (B, N)
+                                  and not (q.dim() == 3 and positions.shape == (B,))):
         raise ValueError("positions must be int32 [B, N]")
     if layout not in _LAYOUTS or scaling not in _SCALINGS:
         raise ValueError("layout is one of %s, scaling one of %s" % (sorted(_LAYOUTS), sorted(_SCALINGS)))
-    spec = RotarySpec(d if rot is None else int(rot), _LAYOUTS[layout], _SCALINGS[scaling], int(original), float(base),
-                      float(factor), float(ramp[0]), float(ramp[1]), float(amplitude))
+    spec = RotarySpec(d if rot is None else _int("rot", rot), _LAYOUTS[layout], _SCALINGS[scaling],
+                      _int("original", original), base, factor, ramp[0], ramp[1], amplitude)
     _call(name, dev, stream, q.data_ptr(), _ptr(k), oq.data_ptr(), _ptr(ok), _ptr(positions), int(offset),
-          ctypes.byref(spec), B, Hq, Hk, N, d, _dtype_code(q))
+          ctypes.byref(spec), B, Hq, Hk, N, d, code)
     return oq if k is None else (oq, ok)
 
 
@@ -96,79 +149,78 @@ def la_rotary_backward(doq, dok=None, dq=None, dk=None, positions=None, offset: 
 
 
 # ---------------------------------------------------------------- gated recurrence
-def _gates(alpha, shape):
-    import torch
-    if alpha.dtype != torch.float32 or tuple(alpha.shape) != tuple(shape):
-        raise ValueError("alpha must be float32 %s" % list(shape))
-
-
 def la_recurrence_forward(x, alpha, h0=None, h=None, hN=None, stream=None):
     """h_t = alpha_t h_{t-1} + x_t per channel; x [B,N,D], alpha fp32 [B,N,D], h0 fp32 [B,D] (None: zeros).
     Returns (h in the dtype of x, the last state hN fp32 [B,D])."""
-    import torch
+    if torch is None:
+        _start()
     if x.dim() != 3:
         raise ValueError("x must be [B, N, D]")
-    B, N, D = x.shape
+    B, N, D = _sizes(x)
     h = torch.empty_like(x) if h is None else h
     hN = torch.empty((B, D), dtype=torch.float32, device=x.device) if hN is None else hN
     dev = _place(x, alpha, h0, h, hN)
-    _same_dtype(x, h)
-    _gates(alpha, x.shape)
+    code = _dtype_code(x, h)
+    _shaped("alpha", alpha, x.shape, torch.float32)
     _shaped("h", h, x.shape)
     _shaped("h0", h0, (B, D), torch.float32)
     _shaped("hN", hN, (B, D), torch.float32)
     _call("la_recurrence_forward", dev, stream, x.data_ptr(), alpha.data_ptr(), _ptr(h0), h.data_ptr(), hN.data_ptr(),
-          B, N, D, _dtype_code(x))
+          B, N, D, code)
     return h, hN
 
 
 def la_recurrence_backward(alpha, h, dh, h0=None, dhN=None, dx=None, dalpha=None, dh0=None, stream=None):
     """Gradients of la_recurrence_forward from its output h, dh and dhN (None: zeros).  Returns
     (dx, dalpha fp32, dh0 fp32 -- None when neither h0 nor dh0 was given)."""
-    import torch
+    if torch is None:
+        _start()
     if h.dim() != 3:
         raise ValueError("h must be [B, N, D]")
-    B, N, D = h.shape
+    B, N, D = _sizes(h)
     dx = torch.empty_like(h) if dx is None else dx
     dalpha = torch.empty_like(alpha) if dalpha is None else dalpha
     if dh0 is None and h0 is not None:
         dh0 = torch.empty_like(h0)
     dev = _place(alpha, h, dh, h0, dhN, dx, dalpha, dh0)
-    _same_dtype(h, dh, dx)
-    _gates(alpha, h.shape)
+    code = _dtype_code(h, dh, dx)
+    _shaped("alpha", alpha, h.shape, torch.float32)
     _shaped("dh", dh, h.shape)
     _shaped("dx", dx, h.shape)
     _shaped("dalpha", dalpha, h.shape, torch.float32)
     for what, t in (("h0", h0), ("dhN", dhN), ("dh0", dh0)):
         _shaped(what, t, (B, D), torch.float32)
     _call("la_recurrence_backward", dev, stream, alpha.data_ptr(), h.data_ptr(), dh.data_ptr(), _ptr(h0), _ptr(dhN),
-          dx.data_ptr(), dalpha.data_ptr(), _ptr(dh0), B, N, D, _dtype_code(h))
+          dx.data_ptr(), dalpha.data_ptr(), _ptr(dh0), B, N, D, code)
     return dx, dalpha, dh0
 
 
 def la_recurrence_step(state, x, alpha, h=None, stream=None):
     """One token of la_recurrence_forward: state fp32 [B,D] in place, x, alpha [B,D]; returns h [B,D]."""
-    import torch
+    if torch is None:
+        _start()
     if x.dim() != 2:
         raise ValueError("x must be [B, D]")
     h = torch.empty_like(x) if h is None else h
     dev = _place(state, x, alpha, h)
-    _same_dtype(x, h)
-    _gates(alpha, x.shape)
-    _shaped("state", state, x.shape, torch.float32)
-    _shaped("h", h, x.shape)
+    code = _dtype_code(x, h)
+    shape = _sizes(x)
+    _shaped("alpha", alpha, shape, torch.float32)
+    _shaped("state", state, shape, torch.float32)
+    _shaped("h", h, shape)
     _call("la_recurrence_step", dev, stream, state.data_ptr(), x.data_ptr(), alpha.data_ptr(), h.data_ptr(),
-          x.shape[0], x.shape[1], _dtype_code(x))
+          shape[0], shape[1], code)
     return h
 
 
 # ---------------------------------------------------------------- window attention
 def _window_shapes(q, k, v, lens):
-    import torch
+    if torch is None:
+        _start()
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B, Hq, Nq, d], k and v [B, Hk, Nk, d]")
     B, Hq, Nq, d = q.shape
-    Hk, Nk = k.shape[1], k.shape[2]
+    Hk, Nk = _sizes(k)[1:3]
     _shaped("k", k, (B, Hk, Nk, d))
     _shaped("v", v, k.shape)
     _shaped("lens", lens, (B,), torch.int32)
@@ -184,35 +236,38 @@ def la_window_forward(q, k, v, window: int, sinks: int = 0, lens=None, scale: fl
     """Causal softmax attention over the last `window` keys and the first `sinks`; q [B,Hq,Nq,d] (the
     last Nq tokens), k, v [B,Hk,Nk,d], lens int32 [B] valid tokens per entry (None: all), scale
     1/sqrt(d) by default.  Returns (o, lse fp32 [B,Hq,Nq]); padding rows give 0 and -inf."""
-    import torch
+    if torch is None:
+        _start()
     B, Hq, Hk, Nq, Nk, d = _window_shapes(q, k, v, lens)
     o = torch.empty_like(q) if o is None else o
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
     dev = _place(q, k, v, lens, o, lse)
-    _same_dtype(q, k, v, o)
+    code = _dtype_code(q, k, v, o)
     _shaped("o", o, q.shape)
     _shaped("lse", lse, (B, Hq, Nq), torch.float32)
     _call("la_window_forward", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-          _ptr(lens), B, Hq, Hk, Nq, Nk, d, int(window), int(sinks), _scale(scale, d), _dtype_code(q))
+          _ptr(lens), B, Hq, Hk, Nq, Nk, d, _int("window", window),
+          _int("sinks", sinks), _scale(scale, d), code)
     return o, lse
 
 
 def la_window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0, lens=None, scale: float = None, dq=None,
                        dk=None, dv=None, stream=None):
     """Gradients (dq, dk, dv) of sum(dout * o) for la_window_forward, from its o and lse."""
-    import torch
+    if torch is None:
+        _start()
     B, Hq, Hk, Nq, Nk, d = _window_shapes(q, k, v, lens)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
     dev = _place(q, k, v, o, lse, dout, lens, dq, dk, dv)
-    _same_dtype(q, k, v, o, dout, dq, dk, dv)
+    code = _dtype_code(q, k, v, o, dout, dq, dk, dv)
     for what, t, like in (("o", o, q), ("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         _shaped(what, t, like.shape)
     _shaped("lse", lse, (B, Hq, Nq), torch.float32)
     _call("la_window_backward", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-          dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(lens), B, Hq, Hk, Nq, Nk, d, int(window),
-          int(sinks), _scale(scale, d), _dtype_code(q))
+          dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(lens), B, Hq, Hk, Nq, Nk, d, _int("window", window),
+          _int("sinks", sinks), _scale(scale, d), code)
     return dq, dk, dv
 
 
@@ -220,39 +275,41 @@ def la_window_cache(k, v, window: int, sinks: int = 0, lens=None, kc=None, vc=No
     """Ring caches (kc, vc) [B,Hk,sinks+window,d] of a prefill k, v [B,Hk,N,d]: token j in slot j while
     j < sinks, else in sinks + (j - sinks) % window.  Slots without a token are left as they
     were (zeros in caches made here)."""
-    import torch
+    if torch is None:
+        _start()
     if k.dim() != 4:
         raise ValueError("k and v must be [B, Hk, N, d]")
-    B, Hk, N, d = k.shape
-    window, sinks = int(window), int(sinks)
+    B, Hk, N, d = _sizes(k)
+    window, sinks = _int("window", window), _int("sinks", sinks)
     if window < 1 or sinks < 0:
         raise ValueError("window must be at least 1, sinks at least 0")
     shape = (B, Hk, sinks + window, d)
     kc = torch.zeros(shape, dtype=k.dtype, device=k.device) if kc is None else kc
     vc = torch.zeros(shape, dtype=k.dtype, device=k.device) if vc is None else vc
     dev = _place(k, v, lens, kc, vc)
-    _same_dtype(k, v, kc, vc)
+    code = _dtype_code(k, v, kc, vc)
     _shaped("v", v, k.shape)
     _shaped("kc", kc, shape)
     _shaped("vc", vc, shape)
     _shaped("lens", lens, (B,), torch.int32)
     _call("la_window_cache", dev, stream, k.data_ptr(), v.data_ptr(), kc.data_ptr(), vc.data_ptr(), _ptr(lens), B, Hk,
-          N, d, window, sinks, _dtype_code(k))
+          N, d, window, sinks, code)
     return kc, vc
 
 
 def la_window_decode_step(kc, vc, q, k, v, pos, window: int, sinks: int = 0, scale: float = None, o=None, stream=None):
     """One decode step on ring caches kc, vc [B,Hk,sinks+window,d] (updated in place): q [B,Hq,d], k, v
     [B,Hk,d], pos int32 [B] the new token's position per entry (negative: idle).  Returns o [B,Hq,d]."""
-    import torch
+    if torch is None:
+        _start()
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [B, Hq, d], k and v [B, Hk, d]")
     B, Hq, d = q.shape
     Hk = k.shape[1]
-    window, sinks = int(window), int(sinks)
+    window, sinks = _int("window", window), _int("sinks", sinks)
     o = torch.empty_like(q) if o is None else o
     dev = _place(kc, vc, q, k, v, pos, o)
-    _same_dtype(q, k, v, kc, vc, o)
+    code = _dtype_code(q, k, v, kc, vc, o)
     _shaped("k", k, (B, Hk, d))
     _shaped("v", v, (B, Hk, d))
     _shaped("kc", kc, (B, Hk, sinks + window, d))
@@ -260,5 +317,5 @@ def la_window_decode_step(kc, vc, q, k, v, pos, window: int, sinks: int = 0, sca
     _shaped("pos", pos, (B,), torch.int32)
     _shaped("o", o, q.shape)
     _call("la_window_decode_step", dev, stream, kc.data_ptr(), vc.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-          o.data_ptr(), pos.data_ptr(), B, Hq, Hk, d, window, sinks, _scale(scale, d), _dtype_code(q))
+          o.data_ptr(), pos.data_ptr(), B, Hq, Hk, d, window, sinks, _scale(scale, d), code)
     return o

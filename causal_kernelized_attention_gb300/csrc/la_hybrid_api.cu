@@ -71,7 +71,7 @@ void fill_turns(const la_rotary_spec &s, uint64_t *turns)
             g = f * (keep + (1.0 - keep) / s.factor);
         }
         const double t = g / kTwoPi, part = t - floor(t);
-        turns[i] = (uint64_t)ldexp(part, 64);  // part < 1: at most 2^64 - 2^11
+        turns[i] = (uint64_t)(part * 0x1p64);  // part < 1: at most 2^64 - 2^11
     }
 }
 
@@ -87,7 +87,7 @@ la_status rotary_checked(const void *q, const void *k, void *oq, void *ok, const
     if ((Hq > 0 && (!aligned(q, 16) || !aligned(oq, 16))) || (Hk > 0 && (!aligned(k, 16) || !aligned(ok, 16))) ||
         !aligned(positions, 4))
         return LA_ERR_MISALIGNED;
-    if (d % 8 != 0 || d > 2 * kRotaryMaxPairs || B > 65535 || (long long)Hq + Hk > 0x7fffffff) return LA_ERR_UNSUPPORTED;
+    if (d % 8 != 0 || d > 2 * kRotaryMaxPairs || (long long)Hq + Hk > 0x7fffffff) return LA_ERR_UNSUPPORTED;
     const size_t row = (size_t)N * d * elem(dtype);
     const Span sq{Hq ? q : nullptr, B * (size_t)Hq * row}, sk{Hk ? k : nullptr, B * (size_t)Hk * row};
     const Span soq{Hq ? oq : nullptr, sq.bytes}, sok{Hk ? ok : nullptr, sk.bytes};
@@ -95,7 +95,7 @@ la_status rotary_checked(const void *q, const void *k, void *oq, void *ok, const
     if (overlap(soq, sok) || overlap(soq, sk) || overlap(sok, sq) || overlap(soq, spos) || overlap(sok, spos) ||
         (soq.p != sq.p && overlap(soq, sq)) || (sok.p != sk.p && overlap(sok, sk)))
         return LA_ERR_INVALID_ARG;
-    RotaryProblem p{};
+    RotaryProblem p;
     p.q = q; p.k = k; p.oq = oq; p.ok = ok;
     p.positions = positions;
     p.offset = offset;

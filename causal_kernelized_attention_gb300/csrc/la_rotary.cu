@@ -29,9 +29,9 @@ struct Args {
     void *oq, *ok;
     const int *positions;  // [B, N], or null: offset + n
     long long offset;
-    int B, Hq, Hk, N, d, rot;
-    int run;               // heads a thread turns
-    int groups;            // runs of heads per token
+    int Hq, Hk, N, d, rot;
+    long long tokens;      // B N
+    int run;               // heads a thread turns; a token's runs are the grid's second dimension
     float amplitude, sign;
     uint64_t turns[kRotaryMaxPairs];
 };
@@ -42,14 +42,14 @@ template <typename T, int V, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Args a)
 {
     const int units = a.d / (2 * V);  // per token
-    const long long u = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (u >= (long long)a.N * units) return;
-    const int n = (int)(u / units), c = (int)(u % units);
-    const int b = (int)(blockIdx.y / a.groups), g = (int)(blockIdx.y % a.groups);
+    const long long u = (long long)blockIdx.x * kThreads + threadIdx.x, token = u / units;
+    if (token >= a.tokens) return;
+    const int c = (int)(u % units), n = (int)(token % a.N), g = (int)blockIdx.y;
+    const long long b = token / a.N;
     const bool turned = c < a.rot / (2 * V);
     float cs[V], sn[V];
     if (turned) {
-        const long long p = a.positions ? (long long)a.positions[(size_t)b * a.N + n] : a.offset + n;
+        const long long p = a.positions ? (long long)a.positions[token] : a.offset + n;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const uint64_t t = (uint64_t)p * a.turns[c * V + i];
@@ -95,8 +95,9 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 template <typename T, int V>
 la_status launch(const Args &a, bool interleaved, cudaStream_t s)
 {
-    const long long units = (long long)a.N * (a.d / (2 * V));
-    const dim3 grid((unsigned)((units + kThreads - 1) / kThreads), (unsigned)(a.B * a.groups));
+    const long long ctas = (a.tokens * (a.d / (2 * V)) + kThreads - 1) / kThreads;
+    if (ctas > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)ctas, (unsigned)ceil_div(a.Hq + a.Hk, a.run));
     count_launches();
     if (interleaved)
         rotary_kernel<T, V, true><<<grid, kThreads, 0, s>>>(a);
@@ -113,7 +114,8 @@ la_status rotary(const RotaryProblem &p)
     a.q = p.q; a.k = p.k; a.oq = p.oq; a.ok = p.ok;
     a.positions = p.positions;
     a.offset = p.offset;
-    a.B = p.B; a.Hq = p.Hq; a.Hk = p.Hk; a.N = p.N; a.d = p.d; a.rot = p.spec.rot;
+    a.tokens = (long long)p.B * p.N;
+    a.Hq = p.Hq; a.Hk = p.Hk; a.N = p.N; a.d = p.d; a.rot = p.spec.rot;
     a.amplitude = p.spec.amplitude;
     a.sign = p.backward ? -1.f : 1.f;
     for (int i = 0; i < p.spec.rot / 2; ++i) a.turns[i] = p.turns[i];
@@ -124,16 +126,10 @@ la_status rotary(const RotaryProblem &p)
     // Heads per thread: up to 8 share a thread's sines, fewer when the tokens alone do
     // not fill the machine (152 SMs x 2048 threads), down to one head per thread.
     const int heads = p.Hq + p.Hk;
-    const long long threads = (long long)p.B * p.N * (p.d / (2 * V));
+    const long long threads = a.tokens * (p.d / (2 * V));
     int run = 8;
     while (run > 1 && threads * ceil_div(heads, run) < 152LL * 2048) run /= 2;
-    a.run = run;
-    a.groups = ceil_div(heads, run);
-    if ((long long)a.B * a.groups > 65535) {  // the grid's second dimension
-        a.run = heads;
-        a.groups = 1;
-    }
-    if (a.B > 65535) return LA_ERR_UNSUPPORTED;
+    a.run = max(run, ceil_div(heads, 65535));  // the grid's second dimension
     const bool il = p.spec.layout == LA_ROTARY_INTERLEAVED;
     if (p.dtype == LA_BF16) {
         if (V == 8) return launch<__nv_bfloat16, 8>(a, il, p.stream);

@@ -477,7 +477,7 @@ typedef struct {
  * may be NULL).  oq may be q itself and ok k itself (in place); any other overlap of an
  * output with an input, with `positions` or with the other output is LA_ERR_INVALID_ARG.
  * The angle is reduced exactly for every 32-bit position; arithmetic is fp32, rounded once.
- * d: a multiple of 8 up to 256; B at most 65535 (else LA_ERR_UNSUPPORTED).
+ * d: a multiple of 8 up to 256 (else LA_ERR_UNSUPPORTED).
  */
 la_status la_rotary_forward(const void *q, const void *k, void *oq, void *ok, const int *positions,
                             long long offset, const la_rotary_spec *spec, int B, int Hq, int Hk, int N, int d,

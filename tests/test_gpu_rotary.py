@@ -92,7 +92,9 @@ def test_empty():
 
 
 def test_many_rows():
-    """More head groups than a grid's second dimension holds."""
-    q = ref.draw(6, (40000, 2, 1, 8), torch.bfloat16)
-    pos = torch.arange(40000, dtype=torch.int32)[:, None]
+    """More entries, and more heads, than a grid's second dimension holds."""
+    q = ref.draw(7, (1, 70000, 1, 8), torch.bfloat16)
+    ref.assert_within(la().la_rotary_forward(q.cuda(), offset=77), *ref.rotary(q, torch.full((1, 1), 77.0), 8))
+    q = ref.draw(6, (70000, 2, 1, 8), torch.bfloat16)
+    pos = torch.arange(70000, dtype=torch.int32)[:, None]
     ref.assert_within(la().la_rotary_forward(q.cuda(), positions=pos.cuda()), *ref.rotary(q, pos, 8))
