@@ -266,7 +266,7 @@ la_status la_window_backward(const void *q, const void *k, const void *v, const 
     void *base = nullptr;
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     if ((st = cuda_status(cudaStreamIsCapturing(s, &cs))) != LA_OK) return st;
-    const size_t bytes = dtype == LA_BF16 ? window_backward_tc_scratch(p) : rows * 4;
+    const size_t bytes = dtype == LA_BF16 ? window_backward_tc_scratch(p) : window_backward_simt_scratch(p);
     st = cs == cudaStreamCaptureStatusNone ? data_workspace(s, bytes, &base) : LA_ERR_UNSUPPORTED;
     if (st != LA_OK) {
         if ((st = scratch.alloc(bytes, s)) != LA_OK) return st;

@@ -175,9 +175,8 @@ la_status recurrence(const RecurrenceProblem &p);
 la_status recurrence_step(float *state, const void *x, const float *alpha, void *h, int B, int D, la_dtype dtype,
                           cudaStream_t stream);
 
-// Window attention with sinks (la_window.cu: CUDA cores, fp32 arithmetic).  forward: out, lse;
-// backward: o, lse, dout -> dq, dk, dv, with scratch at delta (fp32 [B, Hq, Nq], and more on
-// the tensor cores).  window
+// Window attention with sinks (la_window.cu: fp32, on the CUDA cores).  forward: out, lse;
+// backward: o, lse, dout -> dq, dk, dv, with scratch at delta.  window
 // and sinks are at most Nk.
 struct WindowProblem {
     const void *q, *k, *v, *o, *dout;
@@ -191,6 +190,7 @@ struct WindowProblem {
 };
 la_status window_forward_simt(const WindowProblem &p);
 la_status window_backward_simt(const WindowProblem &p);
+size_t window_backward_simt_scratch(const WindowProblem &p);  // bytes at p.delta
 // The same on the tensor cores (la_tc_window.cu, la_tc_window_bwd.cu): bf16.
 la_status window_forward_tc(const WindowProblem &p);
 la_status window_backward_tc(const WindowProblem &p);

@@ -10,13 +10,17 @@
 // The forward and the dq kernel give a CTA 64 query rows and pass over the key tiles their
 // window and the sinks reach (running maximum and sum of the softmax, the output rescaled as
 // the maximum grows); the dk, dv kernel gives a CTA 64 keys and passes over the query tiles
-// that see them, of every head of the group, so each gradient is written once, by one CTA,
-// in a fixed order.  All products are fp32 fused multiply-adds on 4 x 4 register tiles fed
+// that see them, of every head of the group.  Where those CTAs are few, or a tile of sinks is
+// seen by every later row, a tile's query tiles are shared out over several CTAs, whose sums
+// a third kernel adds up; every sum is taken in a fixed order.  All products are fp32 fused multiply-adds on 4 x 4 register tiles fed
 // by 16-byte shared-memory loads (8 loads for 64 multiply-adds), rows padded by 4 floats so
 // that the 8 threads of a quarter-warp meet 8 different bank groups: bound by the CUDA
 // cores' fp32 rate.  fp32 calls run here; bf16 calls run on the tensor cores.
 #include <math.h>
 
+#include <algorithm>
+
+#include "la_tc_common.cuh"
 #include "la_window.cuh"
 
 namespace la {
@@ -31,16 +35,13 @@ constexpr int kPS = kT + 4;    // row stride of the probability tiles
 template <int D> constexpr int stride() { return D + 4; }
 
 // Rows [t0, t0 + 64) of x [N, D] into shared memory; rows at or past `rows` become zero.
-template <typename T, int D>
-__device__ __forceinline__ void load_tile(float *dst, const T *x, int t0, int rows)
+template <int D>
+__device__ __forceinline__ void load_tile(float *dst, const float *x, int t0, int rows)
 {
     for (int u = threadIdx.x; u < kT * (D / 4); u += kThreads) {
         const int r = u / (D / 4), c = (u % (D / 4)) * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t0 + r < rows) {
-            const T *p = x + (size_t)(t0 + r) * D + c;
-            v = make_float4(Elem<T>::to_f32(p[0]), Elem<T>::to_f32(p[1]), Elem<T>::to_f32(p[2]), Elem<T>::to_f32(p[3]));
-        }
+        if (t0 + r < rows) v = *reinterpret_cast<const float4 *>(x + (size_t)(t0 + r) * D + c);
         *reinterpret_cast<float4 *>(dst + r * stride<D>() + c) = v;
     }
 }
@@ -112,17 +113,26 @@ __device__ __forceinline__ float sum16(float v)
     return v;
 }
 
+// How the key tiles' query tiles are shared out: the first `sinks` tiles of a key head over
+// `sink_parts` CTAs each, the others over `parts`.
+struct Split {
+    int sinks, sink_parts, parts, tiles;
+    __host__ __device__ int units() const { return sinks * sink_parts + (tiles - sinks) * parts; }
+};
+
 struct Args {
     const void *q, *k, *v, *o, *dout;
     void *out, *dq, *dk, *dv;
     float *lse, *delta;
     const int *lens;
-    int Hq, Hk, Nq, Nk, window, sinks;
+    int B, Hq, Hk, Nq, Nk, window, sinks;
     float scale;
+    Split sp;     // dk, dv
+    float *part;  // [B Hk][units][dk, dv][64][D], of the tiles with several shares
 };
 
 // ---------------------------------------------------------------- forward
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) window_forward_kernel(const Args a)
 {
     extern __shared__ __align__(16) float sm[];
@@ -133,8 +143,8 @@ __global__ void __launch_bounds__(kThreads) window_forward_kernel(const Args a)
     const int b = bh / a.Hq, h = bh % a.Hq, off = a.Nk - a.Nq;
     const int n = valid(a.lens, b, a.Nk);
     const size_t kvrow = ((size_t)b * a.Hk + h / (a.Hq / a.Hk)) * a.Nk;
-    const T *kp = static_cast<const T *>(a.k) + kvrow * D, *vp = static_cast<const T *>(a.v) + kvrow * D;
-    load_tile<T, D>(q, static_cast<const T *>(a.q) + (size_t)bh * a.Nq * D, t0, a.Nq);
+    const float *kp = static_cast<const float *>(a.k) + kvrow * D, *vp = static_cast<const float *>(a.v) + kvrow * D;
+    load_tile<D>(q, static_cast<const float *>(a.q) + (size_t)bh * a.Nq * D, t0, a.Nq);
     const KeyTiles kt(t0 + off, min(t0 + kT, a.Nq) - 1 + off, a.window, a.sinks, n, kT);
     float m[4], l[4], o[4][D / 16];
 #pragma unroll
@@ -147,8 +157,8 @@ __global__ void __launch_bounds__(kThreads) window_forward_kernel(const Args a)
     for (int it = 0; it < kt.count(); ++it) {
         const int j0 = kt.tile(it) * kT;
         __syncthreads();
-        load_tile<T, D>(k, kp, j0, n);
-        load_tile<T, D>(v, vp, j0, n);
+        load_tile<D>(k, kp, j0, n);
+        load_tile<D>(v, vp, j0, n);
         __syncthreads();
         float s[4][4];
         mul_nt<D>(s, q, k, ty, tx);
@@ -179,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) window_forward_kernel(const Args a)
         __syncthreads();
         mul_nn<D>(o, pr, v, ty, tx);
     }
-    T *op = static_cast<T *>(a.out) + (size_t)bh * a.Nq * D;
+    float *op = static_cast<float *>(a.out) + (size_t)bh * a.Nq * D;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = t0 + ty + 16 * i;
@@ -187,8 +197,8 @@ __global__ void __launch_bounds__(kThreads) window_forward_kernel(const Args a)
         const float inv = l[i] > 0.f || isnan(l[i]) ? 1.f / l[i] : 0.f;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-            op[(size_t)t * D + 32 * c + 2 * tx] = Elem<T>::from_f32(o[i][2 * c] * inv);
-            op[(size_t)t * D + 32 * c + 2 * tx + 1] = Elem<T>::from_f32(o[i][2 * c + 1] * inv);
+            op[(size_t)t * D + 32 * c + 2 * tx] = o[i][2 * c] * inv;
+            op[(size_t)t * D + 32 * c + 2 * tx + 1] = o[i][2 * c + 1] * inv;
         }
         if (tx == 0) a.lse[(size_t)bh * a.Nq + t] = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
     }
@@ -212,7 +222,7 @@ __device__ __forceinline__ void block_ds(float (&s)[4][4], float (&g)[4][4], con
 }
 
 // ---------------------------------------------------------------- backward: dq
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) window_dq_kernel(const Args a)
 {
     extern __shared__ __align__(16) float sm[];
@@ -225,11 +235,11 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(const Args a)
     const int b = bh / a.Hq, h = bh % a.Hq, off = a.Nk - a.Nq;
     const int n = valid(a.lens, b, a.Nk);
     const size_t kvrow = ((size_t)b * a.Hk + h / (a.Hq / a.Hk)) * a.Nk, qrow = (size_t)bh * a.Nq;
-    const T *kp = static_cast<const T *>(a.k) + kvrow * D, *vp = static_cast<const T *>(a.v) + kvrow * D;
+    const float *kp = static_cast<const float *>(a.k) + kvrow * D, *vp = static_cast<const float *>(a.v) + kvrow * D;
     const int rows = min(a.Nq, n - off);  // rows of tokens; the others are padding
-    load_tile<T, D>(q, static_cast<const T *>(a.q) + qrow * D, t0, rows);
-    load_tile<T, D>(go, static_cast<const T *>(a.dout) + qrow * D, t0, rows);
-    load_tile<T, D>(k, static_cast<const T *>(a.o) + qrow * D, t0, rows);
+    load_tile<D>(q, static_cast<const float *>(a.q) + qrow * D, t0, rows);
+    load_tile<D>(go, static_cast<const float *>(a.dout) + qrow * D, t0, rows);
+    load_tile<D>(k, static_cast<const float *>(a.o) + qrow * D, t0, rows);
     __syncthreads();
     // D_p = dO . o, four threads a row
     {
@@ -254,8 +264,8 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(const Args a)
     for (int it = 0; it < kt.count(); ++it) {
         const int j0 = kt.tile(it) * kT;
         __syncthreads();
-        load_tile<T, D>(k, kp, j0, n);
-        load_tile<T, D>(v, vp, j0, n);
+        load_tile<D>(k, kp, j0, n);
+        load_tile<D>(v, vp, j0, n);
         __syncthreads();
         float s[4][4], g[4][4];
         mul_nt<D>(s, q, k, ty, tx);
@@ -268,21 +278,21 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(const Args a)
         __syncthreads();
         mul_nn<D>(acc, ds, k, ty, tx);
     }
-    T *dq = static_cast<T *>(a.dq) + qrow * D;
+    float *dq = static_cast<float *>(a.dq) + qrow * D;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = t0 + ty + 16 * i;
         if (t >= a.Nq) continue;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-            dq[(size_t)t * D + 32 * c + 2 * tx] = Elem<T>::from_f32(acc[i][2 * c]);
-            dq[(size_t)t * D + 32 * c + 2 * tx + 1] = Elem<T>::from_f32(acc[i][2 * c + 1]);
+            dq[(size_t)t * D + 32 * c + 2 * tx] = acc[i][2 * c];
+            dq[(size_t)t * D + 32 * c + 2 * tx + 1] = acc[i][2 * c + 1];
         }
     }
 }
 
 // ---------------------------------------------------------------- backward: dk, dv
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) window_dkv_kernel(const Args a)
 {
     extern __shared__ __align__(16) float sm[];
@@ -290,13 +300,15 @@ __global__ void __launch_bounds__(kThreads) window_dkv_kernel(const Args a)
     float *pt = go + kT * stride<D>(), *dst = pt + kT * kPS;  // transposed: rows of keys
     __shared__ float lse[kT], delta[kT];
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int tiles = (a.Nk + kT - 1) / kT;
-    const int bh = (int)(blockIdx.x / tiles), j0 = (int)(blockIdx.x % tiles) * kT;
+    const int units = a.sp.units(), bh = (int)(blockIdx.x / units), unit = (int)(blockIdx.x % units);
+    const int u1 = unit - a.sp.sinks * a.sp.sink_parts;  // >= 0: not a tile of sinks
+    const int parts = u1 < 0 ? a.sp.sink_parts : a.sp.parts, share = (u1 < 0 ? unit : u1) % parts;
+    const int j0 = (u1 < 0 ? unit / parts : a.sp.sinks + u1 / parts) * kT;
     const int b = bh / a.Hk, hk = bh % a.Hk, off = a.Nk - a.Nq, group = a.Hq / a.Hk;
     const int n = valid(a.lens, b, a.Nk);
     const size_t kvrow = (size_t)bh * a.Nk;
-    load_tile<T, D>(k, static_cast<const T *>(a.k) + kvrow * D, j0, n);
-    load_tile<T, D>(v, static_cast<const T *>(a.v) + kvrow * D, j0, n);
+    load_tile<D>(k, static_cast<const float *>(a.k) + kvrow * D, j0, n);
+    load_tile<D>(v, static_cast<const float *>(a.v) + kvrow * D, j0, n);
     float dk[4][D / 16], dv[4][D / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -304,12 +316,13 @@ __global__ void __launch_bounds__(kThreads) window_dkv_kernel(const Args a)
         for (int c = 0; c < D / 16; ++c) dk[i][c] = dv[i][c] = 0.f;
     const QueryTiles qt(j0, min(j0 + kT, a.Nk) - 1, a.window, a.sinks, n, off, a.Nq, kT);
     const int rows = min(a.Nq, n - off);
-    for (int it = qt.begin * group; it < qt.end * group; ++it) {
-        const int t0 = (it / group) * kT, h = hk * group + it % group;
+    const int all = (qt.end - qt.begin) * group;
+    for (int it = (int)((long long)all * share / parts); it < (int)((long long)all * (share + 1) / parts); ++it) {
+        const int t0 = (qt.begin + it / group) * kT, h = hk * group + it % group;
         const size_t qrow = ((size_t)b * a.Hq + h) * a.Nq;
         __syncthreads();
-        load_tile<T, D>(q, static_cast<const T *>(a.q) + qrow * D, t0, rows);
-        load_tile<T, D>(go, static_cast<const T *>(a.dout) + qrow * D, t0, rows);
+        load_tile<D>(q, static_cast<const float *>(a.q) + qrow * D, t0, rows);
+        load_tile<D>(go, static_cast<const float *>(a.dout) + qrow * D, t0, rows);
         if (threadIdx.x < kT) {
             const bool in = t0 + (int)threadIdx.x < rows;
             lse[threadIdx.x] = in ? a.lse[qrow + t0 + threadIdx.x] : 0.f;
@@ -331,19 +344,51 @@ __global__ void __launch_bounds__(kThreads) window_dkv_kernel(const Args a)
         mul_nn<D>(dv, pt, go, ty, tx);
         mul_nn<D>(dk, dst, q, ty, tx);
     }
-    T *dkp = static_cast<T *>(a.dk) + kvrow * D, *dvp = static_cast<T *>(a.dv) + kvrow * D;
+    if (parts > 1) {
+        float *dst = a.part + ((size_t)bh * units + unit) * 2 * kT * D;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                const int at = (ty + 16 * i) * D + 32 * c + 2 * tx;
+                *reinterpret_cast<float2 *>(dst + at) = make_float2(dk[i][2 * c], dk[i][2 * c + 1]);
+                *reinterpret_cast<float2 *>(dst + kT * D + at) = make_float2(dv[i][2 * c], dv[i][2 * c + 1]);
+            }
+        return;
+    }
+    float *dkp = static_cast<float *>(a.dk) + kvrow * D, *dvp = static_cast<float *>(a.dv) + kvrow * D;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int j = j0 + ty + 16 * i;
         if (j >= a.Nk) continue;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                dkp[(size_t)j * D + 32 * c + 2 * tx + e] = Elem<T>::from_f32(dk[i][2 * c + e]);
-                dvp[(size_t)j * D + 32 * c + 2 * tx + e] = Elem<T>::from_f32(dv[i][2 * c + e]);
-            }
+        for (int c = 0; c < D / 32; ++c) {
+            const size_t at = (size_t)j * D + 32 * c + 2 * tx;
+            *reinterpret_cast<float2 *>(dkp + at) = make_float2(dk[i][2 * c], dk[i][2 * c + 1]);
+            *reinterpret_cast<float2 *>(dvp + at) = make_float2(dv[i][2 * c], dv[i][2 * c + 1]);
+        }
     }
+}
+
+// Adds up the shares of the tiles that have several, in order: 4 features of one key a thread.
+template <int D>
+__global__ void __launch_bounds__(kThreads) window_sum_kernel(const Args a)
+{
+    const long long e = (long long)blockIdx.x * kThreads + threadIdx.x;  // (bh, key, dk or dv, 4 features)
+    const int c = (int)(e % (D / 4)) * 4, which = (int)(e / (D / 4) % 2);
+    const long long row = e / (D / 4) / 2, bh = row / a.Nk;
+    const int j = (int)(row % a.Nk), tile = j / kT;
+    const bool sink = tile < a.sp.sinks;
+    const int parts = sink ? a.sp.sink_parts : a.sp.parts;
+    if (bh >= (long long)a.B * a.Hk || parts == 1) return;
+    const int unit = sink ? tile * parts : a.sp.sinks * a.sp.sink_parts + (tile - a.sp.sinks) * parts;
+    const float *src = a.part + (((size_t)bh * a.sp.units() + unit) * 2 + which) * kT * D + (j % kT) * D + c;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < parts; ++i) {
+        const float4 x = *reinterpret_cast<const float4 *>(src + (size_t)i * 2 * kT * D);
+        sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
+    }
+    *reinterpret_cast<float4 *>(static_cast<float *>(which ? a.dv : a.dk) + row * D + c) = sum;
 }
 
 Args args_of(const WindowProblem &p)
@@ -352,7 +397,7 @@ Args args_of(const WindowProblem &p)
     a.q = p.q; a.k = p.k; a.v = p.v; a.o = p.o; a.dout = p.dout;
     a.out = p.out; a.dq = p.dq; a.dk = p.dk; a.dv = p.dv;
     a.lse = p.lse; a.delta = p.delta; a.lens = p.lens;
-    a.Hq = p.Hq; a.Hk = p.Hk; a.Nq = p.Nq; a.Nk = p.Nk;
+    a.B = p.B; a.Hq = p.Hq; a.Hk = p.Hk; a.Nq = p.Nq; a.Nk = p.Nk;
     a.window = p.window; a.sinks = p.sinks; a.scale = p.scale;
     return a;
 }
@@ -361,51 +406,74 @@ template <typename K>
 la_status launch(K kern, long long ctas, size_t smem, const Args &a, cudaStream_t s)
 {
     if (ctas > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
-    la_status st = ensure_smem((const void *)kern, (int)smem);
+    la_status st = smem ? ensure_smem((const void *)kern, (int)smem) : LA_OK;
     if (st != LA_OK) return st;
     count_launches();
     kern<<<(unsigned)ctas, kThreads, smem, s>>>(a);
     return cuda_status(cudaGetLastError());
 }
 
-template <typename T, int D>
+template <int D>
 la_status forward(const WindowProblem &p)
 {
     const size_t smem = (3 * kT * stride<D>() + kT * kPS) * sizeof(float);
-    return launch(window_forward_kernel<T, D>, (long long)p.B * p.Hq * ceil_div(p.Nq, kT), smem, args_of(p), p.stream);
+    return launch(window_forward_kernel<D>, (long long)p.B * p.Hq * ceil_div(p.Nq, kT), smem, args_of(p), p.stream);
 }
 
-template <typename T, int D>
+size_t delta_bytes(const WindowProblem &p) { return ((size_t)p.B * p.Hq * p.Nq * 4 + 255) & ~(size_t)255; }
+
+// A share is at least a query tile; shares until there are two CTAs an SM, and until a tile
+// of sinks has no more work a CTA than another tile.
+Split split_of(const WindowProblem &p)
+{
+    Split sp;
+    sp.tiles = ceil_div(p.Nk, kT);
+    sp.sinks = ceil_div(p.sinks, kT);
+    const long long group = p.Hq / p.Hk, rows = ceil_div(p.Nq, kT);
+    const long long win = std::min<long long>(rows, (long long)(p.window + kT - 2) / kT + 1) * group;
+    const long long ctas = (long long)p.B * p.Hk * sp.tiles, want = 2LL * tc::sm_count();
+    sp.parts = (int)std::max<long long>(1, std::min(win, (want + ctas - 1) / ctas));
+    const long long each = (win + sp.parts - 1) / sp.parts;
+    // (many tiles of sinks: no more shares than fill the machine several times over)
+    const long long cap = std::max<long long>(1, 4 * want / std::max<long long>(1, (long long)p.B * p.Hk * sp.sinks));
+    sp.sink_parts = (int)std::min((rows * group + each - 1) / each, std::max<long long>(cap, sp.parts));
+    return sp;
+}
+
+template <int D>
 la_status backward(const WindowProblem &p)
 {
     const size_t tile = kT * stride<D>(), prob = kT * kPS;
-    la_status st = launch(window_dq_kernel<T, D>, (long long)p.B * p.Hq * ceil_div(p.Nq, kT),
-                          (4 * tile + prob) * sizeof(float), args_of(p), p.stream);
-    if (st != LA_OK) return st;
-    return launch(window_dkv_kernel<T, D>, (long long)p.B * p.Hk * ceil_div(p.Nk, kT),
-                  (4 * tile + 2 * prob) * sizeof(float), args_of(p), p.stream);
+    Args a = args_of(p);
+    a.sp = split_of(p);
+    a.part = reinterpret_cast<float *>(reinterpret_cast<char *>(p.delta) + delta_bytes(p));
+    la_status st = launch(window_dq_kernel<D>, (long long)p.B * p.Hq * ceil_div(p.Nq, kT), (4 * tile + prob) * sizeof(float), a,
+                          p.stream);
+    if (st == LA_OK)
+        st = launch(window_dkv_kernel<D>, (long long)p.B * p.Hk * a.sp.units(), (4 * tile + 2 * prob) * sizeof(float), a, p.stream);
+    if (st != LA_OK || (a.sp.parts == 1 && (a.sp.sink_parts == 1 || a.sp.sinks == 0))) return st;
+    return launch(window_sum_kernel<D>, ((long long)p.B * p.Hk * p.Nk * 2 * (D / 4) + kThreads - 1) / kThreads, 0, a, p.stream);
 }
 
 }  // namespace
 
 la_status window_forward_simt(const WindowProblem &p)
 {
-    if (p.dtype == LA_BF16) {
-        if (p.d == 32) return forward<__nv_bfloat16, 32>(p);
-        return p.d == 64 ? forward<__nv_bfloat16, 64>(p) : forward<__nv_bfloat16, 128>(p);
-    }
-    if (p.d == 32) return forward<float, 32>(p);
-    return p.d == 64 ? forward<float, 64>(p) : forward<float, 128>(p);
+    if (p.d == 32) return forward<32>(p);
+    return p.d == 64 ? forward<64>(p) : forward<128>(p);
+}
+
+size_t window_backward_simt_scratch(const WindowProblem &p)
+{
+    const Split sp = split_of(p);
+    const bool shared = sp.parts > 1 || (sp.sinks > 0 && sp.sink_parts > 1);
+    return delta_bytes(p) + (shared ? (size_t)p.B * p.Hk * sp.units() * 2 * kT * p.d * 4 : 0);
 }
 
 la_status window_backward_simt(const WindowProblem &p)
 {
-    if (p.dtype == LA_BF16) {
-        if (p.d == 32) return backward<__nv_bfloat16, 32>(p);
-        return p.d == 64 ? backward<__nv_bfloat16, 64>(p) : backward<__nv_bfloat16, 128>(p);
-    }
-    if (p.d == 32) return backward<float, 32>(p);
-    return p.d == 64 ? backward<float, 64>(p) : backward<float, 128>(p);
+    if (p.d == 32) return backward<32>(p);
+    return p.d == 64 ? backward<64>(p) : backward<128>(p);
 }
 
 }  // namespace la

@@ -541,9 +541,9 @@ la_status la_recurrence_step(float *state, const void *x, const float *alpha, vo
  *
  * la_window_backward: given o and lse of the forward and dout = dL/do, writes dq, dk, dv
  * (dk, dv summed over the query heads that share them; rows and keys past lens give 0).
- * Deterministic: every sum is taken in a fixed order.  Scratch (about 2*B*Hq*Nq floats; bf16
- * with sinks: also the partial sums of the sinks' gradients) from the stream's workspace, or
- * stream-ordered while the stream is being captured.
+ * Deterministic: every sum is taken in a fixed order.  Scratch (at most 2*B*Hq*(Nq + 127)
+ * floats, and partial sums of dk and dv where several blocks share them) from the stream's
+ * workspace, or stream-ordered while the stream is being captured.
  *
  * Arithmetic: fp32 inputs in fp32 on the CUDA cores; bf16 inputs on the tensor cores with
  * fp32 scores, softmax and accumulation, the weights (and dS) rounded to bf16 for their
