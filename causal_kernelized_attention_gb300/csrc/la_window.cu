@@ -46,6 +46,31 @@ __device__ __forceinline__ void load_tile(float *dst, const float *x, int t0, in
     }
 }
 
+// The same in two halves, so that the next tile's loads run under this tile's products: one
+// thread's part of a tile in registers, and its way into shared memory.
+template <int D>
+struct Part {
+    static constexpr int kN = kT * (D / 4) / kThreads;
+    float4 v[kN];
+    __device__ __forceinline__ void load(const float *x, int t0, int rows)
+    {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int u = threadIdx.x + i * kThreads, r = u / (D / 4), c = (u % (D / 4)) * 4;
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t0 + r < rows) v[i] = *reinterpret_cast<const float4 *>(x + (size_t)(t0 + r) * D + c);
+        }
+    }
+    __device__ __forceinline__ void store(float *dst) const
+    {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int u = threadIdx.x + i * kThreads, r = u / (D / 4), c = (u % (D / 4)) * 4;
+            *reinterpret_cast<float4 *>(dst + r * stride<D>() + c) = v[i];
+        }
+    }
+};
+
 __device__ __forceinline__ float dot4(const float4 &a, const float4 &b, float c)
 {
     return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, c))));
@@ -154,12 +179,21 @@ __global__ void __launch_bounds__(kThreads) window_forward_kernel(const Args a)
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
     }
+    Part<D> kn, vn;
+    if (kt.count() > 0) {
+        kn.load(kp, kt.tile(0) * kT, n);
+        vn.load(vp, kt.tile(0) * kT, n);
+    }
     for (int it = 0; it < kt.count(); ++it) {
         const int j0 = kt.tile(it) * kT;
         __syncthreads();
-        load_tile<D>(k, kp, j0, n);
-        load_tile<D>(v, vp, j0, n);
+        kn.store(k);
+        vn.store(v);
         __syncthreads();
+        if (it + 1 < kt.count()) {
+            kn.load(kp, kt.tile(it + 1) * kT, n);
+            vn.load(vp, kt.tile(it + 1) * kT, n);
+        }
         float s[4][4];
         mul_nt<D>(s, q, k, ty, tx);
 #pragma unroll
@@ -261,12 +295,21 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(const Args a)
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
     const KeyTiles kt(t0 + off, min(t0 + kT, a.Nq) - 1 + off, a.window, a.sinks, n, kT);
+    Part<D> kn, vn;
+    if (kt.count() > 0) {
+        kn.load(kp, kt.tile(0) * kT, n);
+        vn.load(vp, kt.tile(0) * kT, n);
+    }
     for (int it = 0; it < kt.count(); ++it) {
         const int j0 = kt.tile(it) * kT;
         __syncthreads();
-        load_tile<D>(k, kp, j0, n);
-        load_tile<D>(v, vp, j0, n);
+        kn.store(k);
+        vn.store(v);
         __syncthreads();
+        if (it + 1 < kt.count()) {
+            kn.load(kp, kt.tile(it + 1) * kT, n);
+            vn.load(vp, kt.tile(it + 1) * kT, n);
+        }
         float s[4][4], g[4][4];
         mul_nt<D>(s, q, k, ty, tx);
         mul_nt<D>(g, go, v, ty, tx);
@@ -317,18 +360,32 @@ __global__ void __launch_bounds__(kThreads) window_dkv_kernel(const Args a)
     const QueryTiles qt(j0, min(j0 + kT, a.Nk) - 1, a.window, a.sinks, n, off, a.Nq, kT);
     const int rows = min(a.Nq, n - off);
     const int all = (qt.end - qt.begin) * group;
-    for (int it = (int)((long long)all * share / parts); it < (int)((long long)all * (share + 1) / parts); ++it) {
-        const int t0 = (qt.begin + it / group) * kT, h = hk * group + it % group;
-        const size_t qrow = ((size_t)b * a.Hq + h) * a.Nq;
-        __syncthreads();
-        load_tile<D>(q, static_cast<const float *>(a.q) + qrow * D, t0, rows);
-        load_tile<D>(go, static_cast<const float *>(a.dout) + qrow * D, t0, rows);
+    const int first = (int)((long long)all * share / parts), end = (int)((long long)all * (share + 1) / parts);
+    Part<D> qn, gn;
+    float ln = 0.f, dn = 0.f;
+    auto fetch = [&](int it) {
+        const int t0 = (qt.begin + it / group) * kT;
+        const size_t qrow = ((size_t)b * a.Hq + hk * group + it % group) * a.Nq;
+        qn.load(static_cast<const float *>(a.q) + qrow * D, t0, rows);
+        gn.load(static_cast<const float *>(a.dout) + qrow * D, t0, rows);
         if (threadIdx.x < kT) {
             const bool in = t0 + (int)threadIdx.x < rows;
-            lse[threadIdx.x] = in ? a.lse[qrow + t0 + threadIdx.x] : 0.f;
-            delta[threadIdx.x] = in ? a.delta[qrow + t0 + threadIdx.x] : 0.f;
+            ln = in ? a.lse[qrow + t0 + threadIdx.x] : 0.f;
+            dn = in ? a.delta[qrow + t0 + threadIdx.x] : 0.f;
+        }
+    };
+    if (first < end) fetch(first);
+    for (int it = first; it < end; ++it) {
+        const int t0 = (qt.begin + it / group) * kT;
+        __syncthreads();
+        qn.store(q);
+        gn.store(go);
+        if (threadIdx.x < kT) {
+            lse[threadIdx.x] = ln;
+            delta[threadIdx.x] = dn;
         }
         __syncthreads();
+        if (it + 1 < end) fetch(it + 1);
         float s[4][4], g[4][4];
         mul_nt<D>(s, q, k, ty, tx);
         mul_nt<D>(g, go, v, ty, tx);
