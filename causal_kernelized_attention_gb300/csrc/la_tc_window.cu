@@ -289,37 +289,40 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const bool whole = j0 + kT - 1 <= p_first && p_first + kT - 1 < w.n &&
                                (p_first + kT - 1 - j0 < prm.window || j0 + kT <= prm.sinks);
             // The weights against the maximum so far, found together with the tile's own maximum:
-            // unless that is more than kGrow above (or there is none yet) they stand.
+            // unless that is more than kGrow above they stand, else the scores are taken again.
             uint32_t a[128];
-            float top;
             uint64_t sum;
-            load_scores(ts, a, whole, p, j0, prm, w.n);
-            const bool fresh = __any_sync(0xffffffffu, m == -INFINITY);
-            if (fresh)
-                top = row_max(a);
-            else
+            bool again;
+            do {  // (a row's first visible tile sets its maximum ahead: it has no output to rescale)
+                load_scores(ts, a, whole, p, j0, prm, w.n);
+                if (__any_sync(0xffffffffu, m == -INFINITY)) {
+                    const float first = row_max(a);
+                    if (m == -INFINITY) m = first;
+                }
+                float top;
                 weights(a, c, m, top, sum);
-            const bool grow = top > m && (m == -INFINITY || (top - m) * c > kGrow);
-            if (fresh || __any_sync(0xffffffffu, grow)) {
-                const float keep = grow ? (m == -INFINITY ? 0.f : ex2((m - top) * c)) : 1.f;
-                if (grow) m = top;
-                l *= keep;
-                if (done > 0) {
-                    if (!(ok = wait_w(abort_flag, &sm.o_full[s], (uint32_t)(done - 1) & 1u))) break;
-                    tc_fence_after();
+                const bool grow = top > m && (top - m) * c > kGrow;
+                again = __any_sync(0xffffffffu, grow);
+                if (again) {
+                    const float keep = grow ? ex2((m - top) * c) : 1.f;
+                    if (grow) m = top;
+                    l *= keep;
+                    if (done > 0) {
+                        if (!(ok = wait_w(abort_flag, &sm.o_full[s], (uint32_t)(done - 1) & 1u))) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int x = 0; x < DT; x += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(to + x, o);
+                            tmem_ld_wait();
 #pragma unroll
-                    for (int x = 0; x < DT; x += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(to + x, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                        tmem_st16(to + x, o);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                            tmem_st16(to + x, o);
+                        }
                     }
                 }
-                if (!fresh) load_scores(ts, a, whole, p, j0, prm, w.n);
-                weights(a, c, m, top, sum);
-            }
+            } while (again);
+            if (!ok) break;
             float lx, ly;
             split(sum, lx, ly);
             l += lx + ly;
