@@ -43,37 +43,52 @@ struct Slots {
     }
 };
 
-// Joins the partial results of `parts` warps in each of the cluster's CTAs: rows of G heads,
-// m (the largest score before scaling by f, which turns it into log2 units) and l per row, then the unnormalised outputs.  Partials lie in every CTA's
-// shared memory at the same place.
-template <typename T, int D>
-__device__ __forceinline__ void join(const float *m, const float *l, const float *acc, int parts, int mstride, int G,
-                                     int rows, float f, T *o, uint32_t S, uint32_t rank)
+// Joins the partial results of kParts warps in each of the cluster's S CTAs: per row of G heads
+// m (the largest score before scaling by f, which turns it into log2 units) and l, then the
+// unnormalised outputs, at the same place in every CTA's shared memory.  First every part's
+// weight, exp2((m - top) f) / sum, then the weighted sum of the outputs, each CTA for its
+// share of them; `wt` holds G x S kParts floats twice.
+template <typename T, int D, int G, int kParts>
+__device__ __forceinline__ void join(const float *m, const float *l, const float *acc, float *wt, int rows, float f, T *o,
+                                     uint32_t S, uint32_t rank)
 {
+    const int P = (int)S * kParts;
     const uint32_t ma = smem_u32(m), la_ = smem_u32(l), aa = smem_u32(acc);
+    float *wl = wt + G * kMaxCluster * kParts;
+    for (int e = threadIdx.x; e < rows * P; e += blockDim.x) {
+        const int r = e / P, i = e % P;
+        const uint32_t at = 4 * (i % kParts * G + r), cta = i / kParts;
+        wt[e] = ld_dsmem_f32(mapa_shared(ma + at, cta));
+        wl[e] = ld_dsmem_f32(mapa_shared(la_ + at, cta));
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+        float top = -INFINITY, sum = 0.f;
+        for (int i = 0; i < P; ++i) top = fmaxf(top, wt[r * P + i]);
+        for (int i = 0; i < P; ++i) {
+            const float mi = wt[r * P + i], w = mi == -INFINITY ? 0.f : exp2f((mi - top) * f);  // -inf: no slots
+            wt[r * P + i] = w;
+            sum = fmaf(w, wl[r * P + i], sum);
+        }
+        for (int i = 0; i < P; ++i) wt[r * P + i] /= sum;
+    }
+    __syncthreads();
     for (int e = rank * blockDim.x + threadIdx.x; e < rows * (D / 4); e += S * blockDim.x) {
         const int r = e / (D / 4), c = (e % (D / 4)) * 4;
-        float top = -INFINITY;
-        for (uint32_t s = 0; s < S; ++s)
-            for (int w = 0; w < parts; ++w)
-                top = fmaxf(top, ld_dsmem_f32(mapa_shared(ma + 4 * (w * mstride + r), s)));
-        float sum = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (uint32_t s = 0; s < S; ++s)
-            for (int w = 0; w < parts; ++w) {
-                const float mw = ld_dsmem_f32(mapa_shared(ma + 4 * (w * mstride + r), s));
-                if (mw == -INFINITY) continue;  // no slots
-                const float wt = exp2f((mw - top) * f);
-                sum = fmaf(wt, ld_dsmem_f32(mapa_shared(la_ + 4 * (w * mstride + r), s)), sum);
-                const float4 y = ld_dsmem_f4(mapa_shared(aa + 4 * ((w * G + r) * D + c), s));
-                x.x = fmaf(wt, y.x, x.x); x.y = fmaf(wt, y.y, x.y); x.z = fmaf(wt, y.z, x.z); x.w = fmaf(wt, y.w, x.w);
+#pragma unroll 4
+        for (int i = 0; i < P; ++i) {
+            const float4 y = ld_dsmem_f4(mapa_shared(aa + 4 * ((i % kParts * G + r) * D + c), i / kParts));
+            const float w = wt[r * P + i];
+            if (w != 0.f) {  // (a part without slots may hold anything)
+                x.x = fmaf(w, y.x, x.x); x.y = fmaf(w, y.y, x.y); x.z = fmaf(w, y.z, x.z); x.w = fmaf(w, y.w, x.w);
             }
-        const float inv = 1.f / sum;
+        }
         T *dst = o + (size_t)r * D + c;
-        dst[0] = Elem<T>::from_f32(x.x * inv);
-        dst[1] = Elem<T>::from_f32(x.y * inv);
-        dst[2] = Elem<T>::from_f32(x.z * inv);
-        dst[3] = Elem<T>::from_f32(x.w * inv);
+        if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<float4 *>(dst) = x;
+        else
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(tc::pack_bf16(x.x, x.y), tc::pack_bf16(x.z, x.w));
     }
 }
 
@@ -92,6 +107,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_f32_kernel(const Args 
 {
     constexpr int LK = D / 4, KW = 32 / LK, U = 4;  // lanes a key, keys a warp, keys in flight per lane
     __shared__ __align__(16) float sm_m[kSimtWarps * G], sm_l[kSimtWarps * G], sm_acc[kSimtWarps * G * D];
+    __shared__ float sm_wt[2 * G * kMaxCluster * kSimtWarps];
     const uint32_t S = cluster_size(), rank = S > 1 ? cluster_ctarank() : 0;
     const int unit = (int)(blockIdx.x / S), b = unit / a.Hk, hk = unit % a.Hk, group = a.Hq / a.Hk;
     const int g0 = (int)blockIdx.y * G, rows = min(G, group - g0);
@@ -195,7 +211,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_f32_kernel(const Args 
         cluster_sync_all();
     else
         __syncthreads();
-    join<float, D>(sm_m, sm_l, sm_acc, kSimtWarps, G, G, rows, f, o, S, rank);
+    join<float, D, G, kSimtWarps>(sm_m, sm_l, sm_acc, sm_wt, rows, f, o, S, rank);
     if (S > 1) cluster_sync_all();  // no CTA leaves while its shared memory is read
 }
 
@@ -210,7 +226,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_f32_kernel(const Args 
 // of the features inside a product is free, so q and K are both read in the order the
 // bytes lie in.  P enters as a high and a low bf16 part (two products), so the only
 // rounding of the weights is at 2^-17.
-constexpr int kMmaWarps = 4;
+constexpr int kMmaWarps = 2;
 constexpr int kStages = 3;
 constexpr int kRows = 16;  // heads of one pass
 
@@ -244,7 +260,7 @@ template <int D>
 struct MmaSmem {
     static constexpr int kBlock = 16 * D * 2;  // bytes of 16 keys (or values)
     uint8_t ring[kMmaWarps][kStages][2 * kBlock];
-    float m[kMmaWarps * kRows], l[kMmaWarps * kRows];
+    float m[kMmaWarps * kRows], l[kMmaWarps * kRows], wt[2 * kRows * kMaxCluster * kMmaWarps];
     // the warps' outputs [kMmaWarps][16][D] take the ring's place at the end
     static_assert(kStages * 2 * kBlock >= kRows * D * 4, "a warp's output fits its part of the ring");
 };
@@ -435,7 +451,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32) decode_bf16_kernel(const Args 
         cluster_sync_all();
     else
         __syncthreads();
-    join<__nv_bfloat16, D>(sm.m, sm.l, reinterpret_cast<const float *>(smem_raw), kMmaWarps, kRows, kRows, rows, f, o, S, rank);
+    join<__nv_bfloat16, D, kRows, kMmaWarps>(sm.m, sm.l, reinterpret_cast<const float *>(smem_raw), sm.wt, rows, f, o, S, rank);
     if (S > 1) cluster_sync_all();  // no CTA leaves while its shared memory is read
 }
 
