@@ -99,13 +99,43 @@ __device__ __forceinline__ void write_zeros(T *o, int n)
 }
 
 // ---------------------------------------------------------------- fp32, CUDA cores
-// A lane holds 4 features of a key (D / 4 lanes a key, 128 / D keys a warp at a time); G
-// heads' queries in registers.
-constexpr int kSimtWarps = 8;
+// A lane holds 8 features of a key (D / 8 lanes a key, 256 / D keys a warp at a time), so that
+// a score costs log2(D / 8) shuffles for as many keys at once; G heads' queries in registers.
+constexpr int kSimtWarps = 4;
+constexpr int kSimtKeys = 2;  // per lane in flight: more cost occupancy (2: 562 us, 4: 758, 8: 1270 with 4 features a lane)
+
+struct Row8 {
+    float4 a, b;  // features c .. c + 3 and D / 2 + c .. + 3
+};
+template <int D>
+__device__ __forceinline__ Row8 row8(const float *p)
+{
+    return Row8{*reinterpret_cast<const float4 *>(p), *reinterpret_cast<const float4 *>(p + D / 2)};
+}
+template <int D>
+__device__ __forceinline__ void put8(float *p, const Row8 &r)
+{
+    *reinterpret_cast<float4 *>(p) = r.a;
+    *reinterpret_cast<float4 *>(p + D / 2) = r.b;
+}
+__device__ __forceinline__ float dot8(const Row8 &x, const Row8 &y)
+{
+    const float s = fmaf(x.a.w, y.a.w, fmaf(x.a.z, y.a.z, fmaf(x.a.y, y.a.y, x.a.x * y.a.x)));
+    return fmaf(x.b.w, y.b.w, fmaf(x.b.z, y.b.z, fmaf(x.b.y, y.b.y, fmaf(x.b.x, y.b.x, s))));
+}
+// r = r f + x w
+__device__ __forceinline__ void scale_add(Row8 &r, float f, const Row8 &x, float w)
+{
+    r.a.x = fmaf(x.a.x, w, r.a.x * f); r.a.y = fmaf(x.a.y, w, r.a.y * f);
+    r.a.z = fmaf(x.a.z, w, r.a.z * f); r.a.w = fmaf(x.a.w, w, r.a.w * f);
+    r.b.x = fmaf(x.b.x, w, r.b.x * f); r.b.y = fmaf(x.b.y, w, r.b.y * f);
+    r.b.z = fmaf(x.b.z, w, r.b.z * f); r.b.w = fmaf(x.b.w, w, r.b.w * f);
+}
+
 template <int D, int G>
 __global__ void __launch_bounds__(kSimtWarps * 32) decode_f32_kernel(const Args a)
 {
-    constexpr int LK = D / 4, KW = 32 / LK, U = 4;  // lanes a key, keys a warp, keys in flight per lane
+    constexpr int LK = D / 8, KW = 32 / LK, U = kSimtKeys;  // lanes a key, keys a warp
     __shared__ __align__(16) float sm_m[kSimtWarps * G], sm_l[kSimtWarps * G], sm_acc[kSimtWarps * G * D];
     __shared__ float sm_wt[2 * G * kMaxCluster * kSimtWarps];
     const uint32_t S = cluster_size(), rank = S > 1 ? cluster_ctarank() : 0;
@@ -122,69 +152,62 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_f32_kernel(const Args 
     const size_t cache = (size_t)unit * ((size_t)a.sinks + a.window) * D;
     float *kc = static_cast<float *>(a.kc) + cache, *vc = static_cast<float *>(a.vc) + cache;
     const float *kn = static_cast<const float *>(a.k) + (size_t)unit * D, *vn = static_cast<const float *>(a.v) + (size_t)unit * D;
-    float4 q[G];
+    const Row8 none{make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    Row8 q[G], acc[G];
     float m[G], l[G];
-    float4 acc[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        q[g] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (g < rows)
-            q[g] = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) +
-                                                     ((size_t)b * a.Hq + hk * group + g0 + g) * D + c);
+        q[g] = none;
+        if (g < rows) q[g] = row8<D>(static_cast<const float *>(a.q) + ((size_t)b * a.Hq + hk * group + g0 + g) * D + c);
         m[g] = -INFINITY;
         l[g] = 0.f;
-        acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+        acc[g] = none;
     }
     const float f = a.scale * kLog2e;
     const int workers = (int)S * kSimtWarps, me = (int)rank * kSimtWarps + warp;
     for (long long j0 = (long long)me * KW * U; j0 < sl.count; j0 += (long long)workers * KW * U) {
-        float4 kx[U], vx[U];
+        Row8 kx[U], vx[U];
         bool in[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const long long j = j0 + u * KW + sub;
             in[u] = j < sl.count;
-            kx[u] = vx[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            kx[u] = vx[u] = none;
             if (in[u]) {
                 const bool fresh = j == sl.fresh;
-                kx[u] = *reinterpret_cast<const float4 *>((fresh ? kn : kc + j * D) + c);
-                vx[u] = *reinterpret_cast<const float4 *>((fresh ? vn : vc + j * D) + c);
+                kx[u] = row8<D>((fresh ? kn : kc + j * D) + c);
+                vx[u] = row8<D>((fresh ? vn : vc + j * D) + c);
                 if (fresh && blockIdx.y == 0) {
-                    *reinterpret_cast<float4 *>(kc + j * D + c) = kx[u];
-                    *reinterpret_cast<float4 *>(vc + j * D + c) = vx[u];
+                    put8<D>(kc + j * D + c, kx[u]);
+                    put8<D>(vc + j * D + c, vx[u]);
                 }
             }
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            float s[U];
+            float s[U], top = m[g];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                s[u] = fmaf(q[g].w, kx[u].w, fmaf(q[g].z, kx[u].z, fmaf(q[g].y, kx[u].y, q[g].x * kx[u].x)));
+                s[u] = dot8(q[g], kx[u]);
 #pragma unroll
                 for (int d = LK / 2; d > 0; d /= 2) s[u] += __shfl_xor_sync(0xffffffffu, s[u], d);
                 if (!in[u]) s[u] = -INFINITY;
+                top = fmaxf(top, s[u]);
             }
-            float top = m[g];
-#pragma unroll
-            for (int u = 0; u < U; ++u) top = fmaxf(top, s[u]);
             const float safe = top == -INFINITY ? 0.f : top;
-            const float keep = exp2f((m[g] - safe) * f);
+            float keep = exp2f((m[g] - safe) * f);
             m[g] = top;
             l[g] *= keep;
-            acc[g].x *= keep; acc[g].y *= keep; acc[g].z *= keep; acc[g].w *= keep;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const float p = exp2f((s[u] - safe) * f);
                 l[g] += p;
-                acc[g].x = fmaf(p, vx[u].x, acc[g].x);
-                acc[g].y = fmaf(p, vx[u].y, acc[g].y);
-                acc[g].z = fmaf(p, vx[u].z, acc[g].z);
-                acc[g].w = fmaf(p, vx[u].w, acc[g].w);
+                scale_add(acc[g], keep, vx[u], p);
+                keep = 1.f;
             }
         }
     }
-    // join the warp's sub-groups, then leave the warp's result for the cluster
+    // join the warp's keys, then leave the warp's result for the cluster
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         float top = m[g];
@@ -192,16 +215,18 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_f32_kernel(const Args 
         for (int d = LK; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float wt = m[g] == -INFINITY ? 0.f : exp2f((m[g] - top) * f);
         float ls = l[g] * wt;
-        float4 x = make_float4(acc[g].x * wt, acc[g].y * wt, acc[g].z * wt, acc[g].w * wt);
+        float x[8] = {acc[g].a.x, acc[g].a.y, acc[g].a.z, acc[g].a.w, acc[g].b.x, acc[g].b.y, acc[g].b.z, acc[g].b.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= wt;
 #pragma unroll
         for (int d = LK; d < 32; d *= 2) {
             ls += __shfl_xor_sync(0xffffffffu, ls, d);
-            x.x += __shfl_xor_sync(0xffffffffu, x.x, d);
-            x.y += __shfl_xor_sync(0xffffffffu, x.y, d);
-            x.z += __shfl_xor_sync(0xffffffffu, x.z, d);
-            x.w += __shfl_xor_sync(0xffffffffu, x.w, d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += __shfl_xor_sync(0xffffffffu, x[e], d);
         }
-        if (sub == 0) *reinterpret_cast<float4 *>(&sm_acc[(warp * G + g) * D + c]) = x;
+        if (sub == 0)
+            put8<D>(&sm_acc[(warp * G + g) * D + c],
+                    Row8{make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7])});
         if (lane == 0) {
             sm_m[warp * G + g] = top;
             sm_l[warp * G + g] = ls;
@@ -492,7 +517,7 @@ template <int D>
 la_status decode(const WindowDecodeProblem &p)
 {
     if (p.dtype == LA_BF16) return launch(decode_bf16_kernel<D>, p, kRows, kMmaWarps * 32, sizeof(MmaSmem<D>), kMmaWarps * 16);
-    const int per_cta = kSimtWarps * (128 / D) * 4, group = p.Hq / p.Hk;
+    const int per_cta = kSimtWarps * (256 / D) * kSimtKeys, group = p.Hq / p.Hk;
     if (group == 1) return launch(decode_f32_kernel<D, 1>, p, 1, kSimtWarps * 32, 0, per_cta);
     if (group == 2) return launch(decode_f32_kernel<D, 2>, p, 2, kSimtWarps * 32, 0, per_cta);
     return launch(decode_f32_kernel<D, 4>, p, 4, kSimtWarps * 32, 0, per_cta);
