@@ -264,17 +264,26 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
         // the row's lse in units of the raw scores, and its D
         const float base = live ? __ldg(prm.lse + row) / prm.scale : 0.f;
         float delta = 0.f;
-        if (ok && tiles > 0 && (ok = wait_w(abort_flag, &sm.q_full[s], 0)) && live) {
+        {
+            uint4 ov[DT / 8];  // the row of o, in flight while Q and dO arrive
             const uint4 *op = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(prm.o) + row * prm.d);
-            for (int ch = 0; ch < prm.d / 8; ++ch) {
-                const uint4 x = __ldg(op + ch);
-                const uint4 y = *reinterpret_cast<const uint4 *>(sm.go[s] + (ch >> 3) * kBox + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    delta = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), delta);
-                    delta = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), delta);
+            for (int ch = 0; ch < DT / 8; ++ch)
+                ov[ch] = live && ch * 8 < prm.d ? __ldg(op + ch) : make_uint4(0u, 0u, 0u, 0u);
+            if (ok && tiles > 0 && (ok = wait_w(abort_flag, &sm.q_full[s], 0)) && live) {
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ch = 0; ch < DT / 8; ++ch) {
+                    const uint4 y =
+                        *reinterpret_cast<const uint4 *>(sm.go[s] + (ch >> 3) * kBox + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+                    const uint32_t xs[4] = {ov[ch].x, ov[ch].y, ov[ch].z, ov[ch].w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sum[e] = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), sum[e]);
+                        sum[e] = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), sum[e]);
+                    }
                 }
+                delta = (sum[0] + sum[1]) + (sum[2] + sum[3]);
             }
         }
         // for the second kernel, rows of an entry padded to whole tiles
