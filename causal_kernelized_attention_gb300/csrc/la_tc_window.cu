@@ -2,7 +2,7 @@
 // of 64 or 128 columns (narrower heads zero-filled by TMA).  The mathematics is la_window.cu's:
 // one pass over the key tiles with the running maximum and sum of the softmax.
 //
-// A CTA takes two query tiles of 128 rows -- the same rows of two heads that share a key
+// A CTA takes two query tiles of 128 rows (for short windows one: see the dispatch) -- the same rows of two heads that share a key
 // head, or neighbouring rows of one head -- so each K and V tile brought into shared memory
 // feeds two of each product.  TMEM holds S_s (128 columns each) and O_s (one per query
 // tile s); the weights P_s, rounded to bf16, are written over S_s and read from there by
@@ -30,19 +30,18 @@ using namespace window;
 static __device__ unsigned g_win_status;
 
 constexpr int kT = kRows;  // rows and keys of a tile
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 320;
-constexpr int kKStages = 2, kVStages = 3;  // V(u) is used one step after K(u)
-constexpr uint32_t kTmemCols = 512;
 constexpr float kGrow = 8.f;  // log2 units a maximum may grow before the output is rescaled
 
-template <int DT>
+// QT query tiles a CTA: two, one CTA an SM, or one, two CTAs an SM.
+template <int DT, int QT>
 struct Smem {
     static constexpr uint32_t kTile = kT * DT * 2;
-    uint8_t q[2][kTile];  // then the outputs, staged
+    // V(u) is used one step after K(u)
+    static constexpr int kKStages = QT == 1 && DT == 128 ? 1 : 2, kVStages = QT == 1 && DT == 128 ? 1 : 3;
+    uint8_t q[QT][kTile];  // then the outputs, staged
     uint8_t k[kKStages][kTile];
     uint8_t v[kVStages][kTile];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[QT], s_full[QT], p_full[QT], o_full[QT];
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], drain;
     uint32_t tmem_base;
     int abort;
@@ -112,18 +111,20 @@ __device__ __forceinline__ void weights(uint32_t (&a)[128], float c, float m, fl
     sum = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int DT, int QT>
+__global__ void __launch_bounds__(32 * (4 * QT + 2), 3 - QT)
 window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o, const Params prm)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    Smem<DT> &sm = *reinterpret_cast<Smem<DT> *>(smem_raw);
-    constexpr uint32_t kTile = Smem<DT>::kTile;
-    constexpr uint32_t tS = 0, tO = 256;
+    typedef Smem<DT, QT> Sm;
+    Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
+    constexpr uint32_t kTile = Sm::kTile;
+    constexpr int kKStages = Sm::kKStages, kVStages = Sm::kVStages, kTmaWarp = 4 * QT, kMmaWarp = kTmaWarp + 1;
+    constexpr uint32_t tS = 0, tO = QT * 128, kTmemCols = QT * 256;
     const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     if (tid == 0) {
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < QT; ++s) {
             mbar_init(&sm.q_full[s], 1);
             mbar_init(&sm.s_full[s], 1);
             mbar_init(&sm.p_full[s], 128);
@@ -174,7 +175,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 for (int x = 0; x < DT; x += 64) tma_load_3d(sm.k[ks] + x / 64 * kBox, &map_k, &sm.k_full[ks], x, j0, kz);
                 if (u == 0)
 #pragma unroll
-                    for (int s = 0; s < 2; ++s)
+                    for (int s = 0; s < QT; ++s)
                         if (w.kt[s].count() > 0) {
                             mbar_arrive_expect_tx(&sm.q_full[s], kTile);
 #pragma unroll
@@ -193,7 +194,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             // no copy may still be writing shared memory when the CTA exits
             if (loaded > 0)
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
+                for (int s = 0; s < QT; ++s)
                     if (w.kt[s].count() > 0) drain(&sm.q_full[s], 0);
             for (int u = max(loaded - kKStages, 0); u < loaded; ++u)
                 drain(&sm.k_full[u % kKStages], (uint32_t)(u / kKStages) & 1u);
@@ -202,7 +203,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         }
     } else if (warp == kMmaWarp) {
         const uint32_t id_s = idesc_bf16_f32(128, kT, false, false), id_o = idesc_bf16_f32(128, DT, false, true);
-        const uint64_t dq[2] = {kmajor(smem_u32(sm.q[0]), 0), kmajor(smem_u32(sm.q[1]), 0)};
+        const uint64_t dq[2] = {kmajor(smem_u32(sm.q[0]), 0), kmajor(smem_u32(sm.q[QT - 1]), 0)};
         const uint64_t dk = kmajor(smem_u32(sm.k[0]), 0), dv = mnmajor(smem_u32(sm.v[0]), 0, kBox);
         uint32_t kst = 0, kph = 0, vst = 0, vph = 0;  // stages and phases of K(u) and V(u - 1)
         uint32_t fed[2] = {0, 0};                     // products of P_s issued
@@ -227,7 +228,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 }
             }
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
+            for (int s = 0; s < QT; ++s) {
                 if (pending[s]) {
                     wait(&sm.p_full[s], fed[s] & 1u);
                     tc_fence_after();
@@ -242,7 +243,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     ++fed[s];
                     pending[s] = false;
                 }
-                if (s == 1 && u > 0 && elect_one()) mma_commit(&sm.v_empty[vst]);
+                if (s == QT - 1 && u > 0 && elect_one()) mma_commit(&sm.v_empty[vst]);
                 if (u < U) {
                     if (s == 0) wait(&sm.k_full[kst], kph);
                     if (w.reaches(s, tile)) {
@@ -259,7 +260,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         }
                         pending[s] = true;
                     }
-                    if (s == 1 && elect_one()) mma_commit(&sm.k_empty[kst]);
+                    if (s == QT - 1 && elect_one()) mma_commit(&sm.k_empty[kst]);
                 }
             }
             if (u > 0 && ++vst == kVStages) vst = 0, vph ^= 1u;
@@ -375,10 +376,11 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int DT>
+template <int DT, int QT>
 la_status forward(const WindowProblem &p)
 {
-    const Params prm = params_of(p);
+    typedef Smem<DT, QT> Sm;
+    const Params prm = params_of(p, QT == 1);
     const long long ctas = (long long)p.B * p.Hk * prm.units;
     if (ctas > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
     CUtensorMap mq, mk, mv, mo;
@@ -386,18 +388,24 @@ la_status forward(const WindowProblem &p)
     if (st == LA_OK) st = make_map(&mk, p.k, p.B * p.Hk, p.Nk, p.d);
     if (st == LA_OK) st = make_map(&mv, p.v, p.B * p.Hk, p.Nk, p.d);
     if (st == LA_OK) st = make_map(&mo, p.out, p.B * p.Hq, p.Nq, p.d);
-    if (st == LA_OK) st = ensure_smem((const void *)window_tc_kernel<DT>, (int)sizeof(Smem<DT>));
+    if (st == LA_OK) st = ensure_smem((const void *)window_tc_kernel<DT, QT>, (int)sizeof(Sm));
     if (st != LA_OK) return st;
     count_launches();
-    return launch_dependent(window_tc_kernel<DT>, (unsigned)ctas, kThreads, (int)sizeof(Smem<DT>), p.stream, mq, mk, mv, mo,
+    return launch_dependent(window_tc_kernel<DT, QT>, (unsigned)ctas, 32 * (4 * QT + 2), (int)sizeof(Sm), p.stream, mq, mk, mv, mo,
                             prm);
 }
 
 }  // namespace
 
+// Short windows: few key tiles a CTA, so that its start and end weigh more than the second
+// use of each K and V tile, and one query tile a CTA with two CTAs an SM is faster (8 heads,
+// d = 64: window 128 15.8 against 18.7 us, 512 24.0 / 25.0, at 1 x 512 rows 7.6 / 9.0); from a
+// window of 1024 two tiles are (1 x 8192 rows, d = 128: 72 against 79 us; 65536 rows, window
+// 2048: 788 / 892).
 la_status window_forward_tc(const WindowProblem &p)
 {
-    return p.d <= 64 ? forward<64>(p) : forward<128>(p);
+    if ((long long)p.window + p.sinks <= 640) return p.d <= 64 ? forward<64, 1>(p) : forward<128, 1>(p);
+    return p.d <= 64 ? forward<64, 2>(p) : forward<128, 2>(p);
 }
 
 la_status tc_window_read_status(cudaStream_t s, unsigned *bits)

@@ -26,7 +26,7 @@ struct Params {
     int B, Hq, Hk, Nq, Nk, window, sinks, d;
     int padded;  // Nq rounded up to whole tiles
     int units;   // CTAs per (entry, key head)
-    int pairs;   // 1: the two tiles are the same rows of heads 2i, 2i + 1 of the group; 0: neighbouring rows
+    int pairs;   // 1: the two tiles are the same rows of heads 2i, 2i + 1 of the group; 0: neighbouring rows; 2: one tile
     float scale;
 };
 
@@ -122,7 +122,11 @@ struct Work {
           kt{{0, -1, 1, 0, 0, KT}, {0, -1, 1, 0, 0, KT}}
     {
         const int u = cta % p.units, group = p.Hq / p.Hk, tiles = (p.Nq + kRows - 1) / kRows;
-        if (p.pairs) {  // unit = (row tile, head pair), pairs of one row tile together
+        if (p.pairs == 2) {  // one query tile: unit = (row tile, head), heads of one row tile together
+            h[0] = h[1] = hk * group + u % group;
+            t0[0] = u / group * kRows;
+            t0[1] = p.Nq;
+        } else if (p.pairs) {  // unit = (row tile, head pair), pairs of one row tile together
             const int hp = u % (group / 2);
             h[0] = hk * group + 2 * hp;
             h[1] = h[0] + 1;
@@ -160,7 +164,7 @@ __device__ __forceinline__ uint32_t seen_bits(int p, int j, int window, int sink
 
 // The launch's sizes; the two tiles of a CTA are heads of one group where groups are even
 // (they reach exactly the same key tiles), else neighbouring rows (all but one).
-inline Params params_of(const WindowProblem &p)
+inline Params params_of(const WindowProblem &p, bool single = false)
 {
     const int group = p.Hq / p.Hk, tiles = ceil_div(p.Nq, kRows);
     Params prm;
@@ -172,8 +176,8 @@ inline Params params_of(const WindowProblem &p)
     prm.B = p.B; prm.Hq = p.Hq; prm.Hk = p.Hk; prm.Nq = p.Nq; prm.Nk = p.Nk;
     prm.window = p.window; prm.sinks = p.sinks; prm.d = p.d;
     prm.scale = p.scale;
-    prm.pairs = group % 2 == 0;
-    prm.units = prm.pairs ? tiles * (group / 2) : (tiles + 1) / 2 * group;
+    prm.pairs = single ? 2 : group % 2 == 0;
+    prm.units = single ? tiles * group : prm.pairs ? tiles * (group / 2) : (tiles + 1) / 2 * group;
     return prm;
 }
 
