@@ -62,6 +62,21 @@ def _call(name, dev, stream, *args):
         _check(name, st)
 
 
+def _like(t, stream):
+    """A new tensor like t, of `stream`'s memory when one is given (it is written there)."""
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
+def _new(shape, dtype, device, stream, make="empty"):
+    if stream is None:
+        return getattr(torch, make)(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return getattr(torch, make)(shape, dtype=dtype, device=device)
+
+
 def _dtype_code(first, *others):
     """The element type that all the tensors share, as the library counts it."""
     d = first.dtype
@@ -107,8 +122,8 @@ def _rotary(name, q, k, oq, ok, positions, offset, rot, layout, base, scaling, f
         raise ValueError("q and k must be [B, H, N, d], or [B, H, d] for one token")
     if k is None and ok is not None:
         raise ValueError("an output for k without k")
-    oq = torch.empty_like(q) if oq is None else oq
-    ok = torch.empty_like(k) if ok is None and k is not None else ok
+    oq = _like(q, stream) if oq is None else oq
+    ok = _like(k, stream) if ok is None and k is not None else ok
     dev = _place(q, k, oq, ok, positions)
     code = _dtype_code(q, oq, k, ok)
     B, Hq, N, d = _sizes(q) if q.dim() == 4 else (q.shape[0], q.shape[1], 1, q.shape[2])
@@ -157,8 +172,8 @@ def la_recurrence_forward(x, alpha, h0=None, h=None, hN=None, stream=None):
     if x.dim() != 3:
         raise ValueError("x must be [B, N, D]")
     B, N, D = _sizes(x)
-    h = torch.empty_like(x) if h is None else h
-    hN = torch.empty((B, D), dtype=torch.float32, device=x.device) if hN is None else hN
+    h = _like(x, stream) if h is None else h
+    hN = _new((B, D), torch.float32, x.device, stream) if hN is None else hN
     dev = _place(x, alpha, h0, h, hN)
     code = _dtype_code(x, h)
     _shaped("alpha", alpha, x.shape, torch.float32)
@@ -178,10 +193,10 @@ def la_recurrence_backward(alpha, h, dh, h0=None, dhN=None, dx=None, dalpha=None
     if h.dim() != 3:
         raise ValueError("h must be [B, N, D]")
     B, N, D = _sizes(h)
-    dx = torch.empty_like(h) if dx is None else dx
-    dalpha = torch.empty_like(alpha) if dalpha is None else dalpha
+    dx = _like(h, stream) if dx is None else dx
+    dalpha = _like(alpha, stream) if dalpha is None else dalpha
     if dh0 is None and h0 is not None:
-        dh0 = torch.empty_like(h0)
+        dh0 = _like(h0, stream)
     dev = _place(alpha, h, dh, h0, dhN, dx, dalpha, dh0)
     code = _dtype_code(h, dh, dx)
     _shaped("alpha", alpha, h.shape, torch.float32)
@@ -201,7 +216,7 @@ def la_recurrence_step(state, x, alpha, h=None, stream=None):
         _start()
     if x.dim() != 2:
         raise ValueError("x must be [B, D]")
-    h = torch.empty_like(x) if h is None else h
+    h = _like(x, stream) if h is None else h
     dev = _place(state, x, alpha, h)
     code = _dtype_code(x, h)
     shape = _sizes(x)
@@ -239,8 +254,8 @@ def la_window_forward(q, k, v, window: int, sinks: int = 0, lens=None, scale: fl
     if torch is None:
         _start()
     B, Hq, Hk, Nq, Nk, d = _window_shapes(q, k, v, lens)
-    o = torch.empty_like(q) if o is None else o
-    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
+    o = _like(q, stream) if o is None else o
+    lse = _new((B, Hq, Nq), torch.float32, q.device, stream) if lse is None else lse
     dev = _place(q, k, v, lens, o, lse)
     code = _dtype_code(q, k, v, o)
     _shaped("o", o, q.shape)
@@ -257,9 +272,9 @@ def la_window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0, lens=
     if torch is None:
         _start()
     B, Hq, Hk, Nq, Nk, d = _window_shapes(q, k, v, lens)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _like(q, stream) if dq is None else dq
+    dk = _like(k, stream) if dk is None else dk
+    dv = _like(v, stream) if dv is None else dv
     dev = _place(q, k, v, o, lse, dout, lens, dq, dk, dv)
     code = _dtype_code(q, k, v, o, dout, dq, dk, dv)
     for what, t, like in (("o", o, q), ("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
@@ -284,8 +299,8 @@ def la_window_cache(k, v, window: int, sinks: int = 0, lens=None, kc=None, vc=No
     if window < 1 or sinks < 0:
         raise ValueError("window must be at least 1, sinks at least 0")
     shape = (B, Hk, sinks + window, d)
-    kc = torch.zeros(shape, dtype=k.dtype, device=k.device) if kc is None else kc
-    vc = torch.zeros(shape, dtype=k.dtype, device=k.device) if vc is None else vc
+    kc = _new(shape, k.dtype, k.device, stream, "zeros") if kc is None else kc
+    vc = _new(shape, k.dtype, k.device, stream, "zeros") if vc is None else vc
     dev = _place(k, v, lens, kc, vc)
     code = _dtype_code(k, v, kc, vc)
     _shaped("v", v, k.shape)
@@ -307,7 +322,7 @@ def la_window_decode_step(kc, vc, q, k, v, pos, window: int, sinks: int = 0, sca
     B, Hq, d = q.shape
     Hk = k.shape[1]
     window, sinks = _int("window", window), _int("sinks", sinks)
-    o = torch.empty_like(q) if o is None else o
+    o = _like(q, stream) if o is None else o
     dev = _place(kc, vc, q, k, v, pos, o)
     code = _dtype_code(q, k, v, kc, vc, o)
     _shaped("k", k, (B, Hk, d))

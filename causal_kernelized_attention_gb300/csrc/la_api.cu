@@ -109,7 +109,7 @@ la_status flag_workspace(cudaStream_t s, size_t bytes, void **out)
     return LA_OK;
 }
 
-la_status data_workspace(cudaStream_t s, size_t bytes, void **out)
+la_status data_workspace(cudaStream_t s, size_t bytes, void **out, int which)
 {
     *out = nullptr;
     if (bytes == 0) return LA_OK;
@@ -117,9 +117,10 @@ la_status data_workspace(cudaStream_t s, size_t bytes, void **out)
     la_status st = stream_key(s, &key);
     if (st != LA_OK) return st;
     static std::mutex mu;
-    static std::map<StreamKey, std::pair<void *, size_t>> spaces;
+    static std::map<std::pair<StreamKey, int>, std::pair<void *, size_t>> spaces;
     std::lock_guard<std::mutex> lock(mu);
-    auto it = spaces.find(key);
+    const auto slot = std::make_pair(key, which);
+    auto it = spaces.find(slot);
     if (it != spaces.end() && it->second.second >= bytes) {
         *out = it->second.first;
         return LA_OK;
@@ -135,7 +136,7 @@ la_status data_workspace(cudaStream_t s, size_t bytes, void **out)
         (void)cudaGetLastError();  // not sticky: the caller's per-call scratch may still fit
         return LA_ERR_UNSUPPORTED;
     }
-    spaces[key] = std::make_pair(p, size);  // an outgrown buffer stays allocated (see above)
+    spaces[slot] = std::make_pair(p, size);  // an outgrown buffer stays allocated (see above)
     *out = p;
     return LA_OK;
 }

@@ -109,6 +109,8 @@ la_status rotary_checked(const void *q, const void *k, void *oq, void *ok, const
 }
 
 // ---------------------------------------------------------------- window attention
+constexpr int kMaxTokens = 1 << 30;  // of a sequence or a cache: sums of two positions fit an int
+
 la_status check_window(int B, int Hq, int Hk, int d, int window, int sinks, float scale, la_dtype dtype)
 {
     if (B < 0 || Hq < 0 || Hk < 0 || d < 0 || window < 1 || sinks < 0 || !known(dtype)) return LA_ERR_INVALID_ARG;
@@ -205,7 +207,8 @@ la_status la_window_forward(const void *q, const void *k, const void *v, void *o
     if (!q || !k || !v || !o || !lse) return LA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(lens, 4))
         return LA_ERR_MISALIGNED;
-    if (!supported_dim(d) || (long long)B * Hq > 0x7fffffff || (long long)B * Hk > 0x7fffffff) return LA_ERR_UNSUPPORTED;
+    if (!supported_dim(d) || (long long)B * Hq > 0x7fffffff || (long long)B * Hk > 0x7fffffff || Nk > kMaxTokens)
+        return LA_ERR_UNSUPPORTED;
     const size_t rows = (size_t)B * Hq * Nq, keys = (size_t)B * Hk * Nk, e = d * elem(dtype);
     const Span out[] = {{o, rows * e}, {lse, rows * 4}};
     const Span in[] = {{q, rows * e}, {k, keys * e}, {v, keys * e}, {lens, (size_t)B * 4}};
@@ -236,7 +239,8 @@ la_status la_window_backward(const void *q, const void *k, const void *v, const 
         (rows_any && (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 16) ||
                       !aligned(dout, 16) || !aligned(dq, 16) || !aligned(lens, 4))))
         return LA_ERR_MISALIGNED;
-    if (!supported_dim(d) || (long long)B * Hq > 0x7fffffff || (long long)B * Hk > 0x7fffffff) return LA_ERR_UNSUPPORTED;
+    if (!supported_dim(d) || (long long)B * Hq > 0x7fffffff || (long long)B * Hk > 0x7fffffff || Nk > kMaxTokens)
+        return LA_ERR_UNSUPPORTED;
     const size_t rows = (size_t)B * Hq * Nq, keys = (size_t)B * Hk * Nk, e = d * elem(dtype);
     const Span out[] = {{dq, rows * e}, {dk, keys * e}, {dv, keys * e}};
     const Span in[] = {{q, rows * e}, {k, keys * e}, {v, keys * e}, {o, rows * e}, {lse, rows * 4}, {dout, rows * e},
@@ -267,7 +271,7 @@ la_status la_window_backward(const void *q, const void *k, const void *v, const 
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     if ((st = cuda_status(cudaStreamIsCapturing(s, &cs))) != LA_OK) return st;
     const size_t bytes = dtype == LA_BF16 ? window_backward_tc_scratch(p) : window_backward_simt_scratch(p);
-    st = cs == cudaStreamCaptureStatusNone ? data_workspace(s, bytes, &base) : LA_ERR_UNSUPPORTED;
+    st = cs == cudaStreamCaptureStatusNone ? data_workspace(s, bytes, &base, 1) : LA_ERR_UNSUPPORTED;
     if (st != LA_OK) {
         if ((st = scratch.alloc(bytes, s)) != LA_OK) return st;
         base = scratch.ptr;
@@ -286,7 +290,7 @@ la_status la_window_cache(const void *k, const void *v, void *kc, void *vc, cons
     if (!k || !v || !kc || !vc) return LA_ERR_INVALID_ARG;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kc, 16) || !aligned(vc, 16) || !aligned(lens, 4))
         return LA_ERR_MISALIGNED;
-    if (!supported_dim(d) || (long long)sinks + window > 0x7fffffff) return LA_ERR_UNSUPPORTED;
+    if (!supported_dim(d) || (long long)sinks + window > kMaxTokens) return LA_ERR_UNSUPPORTED;
     const size_t e = d * elem(dtype), keys = (size_t)B * Hk * N * e;
     const size_t slots = (size_t)B * Hk * ((size_t)sinks + window) * e;
     const Span out[] = {{kc, slots}, {vc, slots}}, in[] = {{k, keys}, {v, keys}, {lens, (size_t)B * 4}};
@@ -305,7 +309,7 @@ la_status la_window_decode_step(void *kc, void *vc, const void *q, const void *k
     if (!aligned(kc, 16) || !aligned(vc, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
         !aligned(o, 16) || !aligned(pos, 4))
         return LA_ERR_MISALIGNED;
-    if (!supported_dim(d) || (long long)sinks + window > 0x7fffffff) return LA_ERR_UNSUPPORTED;
+    if (!supported_dim(d) || (long long)sinks + window > kMaxTokens) return LA_ERR_UNSUPPORTED;
     const size_t e = d * elem(dtype), rows = (size_t)B * Hq * e, keys = (size_t)B * Hk * e;
     const size_t slots = keys * ((size_t)sinks + window);
     const Span out[] = {{kc, slots}, {vc, slots}, {o, rows}}, in[] = {{q, rows}, {k, keys}, {v, keys}, {pos, (size_t)B * 4}};

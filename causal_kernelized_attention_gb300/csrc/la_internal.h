@@ -234,8 +234,10 @@ la_status flag_workspace(cudaStream_t s, size_t bytes, void **out);
 // buffer it outgrows is kept, not freed, until the process exits, so a graph
 // captured against it stays valid.  Returns LA_ERR_UNSUPPORTED when it cannot
 // serve the call (a stream under capture whose buffer is too small, or the
-// allocation failed); the caller then uses per-call scratch.
-la_status data_workspace(cudaStream_t s, size_t bytes, void **out);
+// allocation failed); the caller then uses per-call scratch.  `which` tells a stream's
+// buffers apart: the window backward has one of its own (1), which its lock protects from
+// another host thread's launches on the same stream.
+la_status data_workspace(cudaStream_t s, size_t bytes, void **out, int which = 0);
 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel and device,
 // so that repeated calls (and stream capture) issue no attribute calls.

@@ -536,7 +536,7 @@ la_status la_recurrence_step(float *state, const void *x, const float *alpha, vo
  * rows at positions >= lens[b] are padding and give o = 0 and lse = -inf, keys there are
  * never used, whatever they hold.  Within the valid tokens an infinite or NaN k or v may
  * also reach rows of nearby positions that do not see it.  Supported: d in {32, 64, 128},
- * Nq <= Nk, Hq a multiple of Hk, window >= 1, sinks >= 0, scale > 0 and finite.  window >= Nk
+ * Nq <= Nk <= 2^30, Hq a multiple of Hk, window >= 1, sinks >= 0, scale > 0 and finite.  window >= Nk
  * is plain causal attention.
  *
  * la_window_backward: given o and lse of the forward and dout = dL/do, writes dq, dk, dv
@@ -570,7 +570,7 @@ la_status la_window_backward(const void *q, const void *k, const void *v, const 
  *   before it).  Writes k and v into their slot and returns attention over the visible
  *   slots.  pos[b] < 0 marks an idle entry: o = 0, its cache untouched.  pos is read on the
  *   device, so a captured step can be replayed with pos advanced.
- * Supported sizes as above; sinks + window at most 2^31 - 1.
+ * Supported sizes as above; sinks + window at most 2^30.
  */
 la_status la_window_cache(const void *k, const void *v, void *kc, void *vc, const int *lens, int B, int Hk, int N,
                           int d, int window, int sinks, la_dtype dtype, la_stream_t stream);

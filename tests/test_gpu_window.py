@@ -174,6 +174,61 @@ def test_graphs_and_streams():
             assert torch.equal(x, y)
 
 
+def test_two_host_threads_on_one_stream():
+    """Backward calls of two threads on one stream keep their row sums apart."""
+    import threading
+    B, Hq, Hk, N, d = 1, 4, 2, 700, 64
+    sets = [[ref.draw(10 * j + i, sh, torch.bfloat16).cuda() for i, sh in
+             enumerate(((B, Hq, N, d), (B, Hk, N, d), (B, Hk, N, d), (B, Hq, N, d)))] for j in (1, 2)]
+    fwd = [la().la_window_forward(q, k, v, 90, sinks=2) for q, k, v, _ in sets]
+    want = [la().la_window_backward(q, k, v, *f, go, 90, sinks=2) for (q, k, v, go), f in zip(sets, fwd)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+
+    def work(j):
+        q, k, v, go = sets[j]
+        for _ in range(20):
+            got[j].append(la().la_window_backward(q, k, v, *fwd[j], go, 90, sinks=2, stream=s))
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    s.synchronize()
+    for j in (0, 1):
+        for g in got[j]:
+            assert all(torch.equal(x, y) for x, y in zip(g, want[j]))
+
+
+def test_given_stream_owns_what_it_writes():
+    """Outputs made for a call on another stream are that stream's; the call waits for nothing else."""
+    s = torch.cuda.Stream()
+    k = ref.draw(1, (1, 2, 300, 64), torch.bfloat16).cuda()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        want = la().la_window_cache(k, k, 50, sinks=2)
+    got = la().la_window_cache(k, k, 50, sinks=2, stream=s)
+    o, lse = la().la_window_forward(k, k, k, 50, sinks=2, stream=s)
+    s.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert torch.equal(o, la().la_window_forward(k, k, k, 50, sinks=2)[0])
+    with pytest.raises(ValueError):
+        la().la_window_cache(k, k, 2 ** 31)
+    with pytest.raises(TypeError):
+        la().la_window_forward(k, k.float(), k, 50)
+
+
+def test_nonfinite_rows_stay_their_own():
+    """An infinite score, a NaN query: their rows, and no others."""
+    q, k, v = (ref.draw(i, (1, 1, 300, 64), torch.bfloat16) for i in (1, 2, 3))
+    q[0, 0, 100, 3], q[0, 0, 200, 5] = float("nan"), float("inf")
+    o, lse = la().la_window_forward(q.cuda(), k.cuda(), v.cuda(), 40, sinks=1)
+    bad = ~torch.isfinite(o[0, 0].cpu()).all(1)
+    assert bad.nonzero().flatten().tolist() == [100, 200]
+
+
 # ---------------------------------------------------------------- serving
 def decode_reference(kc, vc, q, k, v, pos, window, sinks, scale):
     """Float64 attention over the tokens that slots hold, and its bound (as hybrid_ref.window; weights
