@@ -53,7 +53,7 @@ def _call(name, dev, stream, *args):
         raise ValueError("stream must be on the tensors' device")
     else:
         s = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -106,6 +106,16 @@ def _sizes(t):
     return t.shape
 
 
+def _out(what, t, shape, dtype, dev):
+    """Checks an output that the caller supplied."""
+    if _place(t) != dev:
+        raise ValueError("tensors must be on one device")
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s" % (what, dtype))
+    _shaped(what, t, shape)
+    return t
+
+
 def _int(what, v):
     if type(v) is not int:
         v = int(v)
@@ -122,15 +132,15 @@ def _rotary(name, q, k, oq, ok, positions, offset, rot, layout, base, scaling, f
         raise ValueError("q and k must be [B, H, N, d], or [B, H, d] for one token")
     if k is None and ok is not None:
         raise ValueError("an output for k without k")
-    oq = _like(q, stream) if oq is None else oq
-    ok = _like(k, stream) if ok is None and k is not None else ok
-    dev = _place(q, k, oq, ok, positions)
-    code = _dtype_code(q, oq, k, ok)
+    dev = _place(q, k, positions)
+    code = _dtype_code(q, k)
     B, Hq, N, d = _sizes(q) if q.dim() == 4 else (q.shape[0], q.shape[1], 1, q.shape[2])
-    Hk = 0 if k is None else k.shape[1]
-    _shaped("k", k, (B, Hk) + tuple(q.shape[2:]))
-    _shaped("the output for q", oq, q.shape)
-    _shaped("the output for k", ok, () if k is None else k.shape)
+    Hk = 0
+    if k is not None:
+        Hk = k.shape[1]
+        _shaped("k", k, (B, Hk, N, d) if q.dim() == 4 else (B, Hk, d))
+        ok = _like(k, stream) if ok is None else _out("the output for k", ok, k.shape, k.dtype, dev)
+    oq = _like(q, stream) if oq is None else _out("the output for q", oq, q.shape, q.dtype, dev)
     if positions is not None and (positions.dtype is not torch.int32 or positions.shape != (B, N)
                                   and not (q.dim() == 3 and positions.shape == (B,))):
         raise ValueError("positions must be int32 [B, N]")
@@ -172,14 +182,12 @@ def la_recurrence_forward(x, alpha, h0=None, h=None, hN=None, stream=None):
     if x.dim() != 3:
         raise ValueError("x must be [B, N, D]")
     B, N, D = _sizes(x)
-    h = _like(x, stream) if h is None else h
-    hN = _new((B, D), torch.float32, x.device, stream) if hN is None else hN
-    dev = _place(x, alpha, h0, h, hN)
-    code = _dtype_code(x, h)
+    dev = _place(x, alpha, h0)
+    code = _dtype_code(x)
     _shaped("alpha", alpha, x.shape, torch.float32)
-    _shaped("h", h, x.shape)
     _shaped("h0", h0, (B, D), torch.float32)
-    _shaped("hN", hN, (B, D), torch.float32)
+    h = _like(x, stream) if h is None else _out("h", h, x.shape, x.dtype, dev)
+    hN = _new((B, D), torch.float32, x.device, stream) if hN is None else _out("hN", hN, (B, D), torch.float32, dev)
     _call("la_recurrence_forward", dev, stream, x.data_ptr(), alpha.data_ptr(), _ptr(h0), h.data_ptr(), hN.data_ptr(),
           B, N, D, code)
     return h, hN
@@ -193,18 +201,18 @@ def la_recurrence_backward(alpha, h, dh, h0=None, dhN=None, dx=None, dalpha=None
     if h.dim() != 3:
         raise ValueError("h must be [B, N, D]")
     B, N, D = _sizes(h)
-    dx = _like(h, stream) if dx is None else dx
-    dalpha = _like(alpha, stream) if dalpha is None else dalpha
-    if dh0 is None and h0 is not None:
-        dh0 = _like(h0, stream)
-    dev = _place(alpha, h, dh, h0, dhN, dx, dalpha, dh0)
-    code = _dtype_code(h, dh, dx)
+    dev = _place(alpha, h, dh, h0, dhN)
+    code = _dtype_code(h, dh)
     _shaped("alpha", alpha, h.shape, torch.float32)
     _shaped("dh", dh, h.shape)
-    _shaped("dx", dx, h.shape)
-    _shaped("dalpha", dalpha, h.shape, torch.float32)
-    for what, t in (("h0", h0), ("dhN", dhN), ("dh0", dh0)):
-        _shaped(what, t, (B, D), torch.float32)
+    _shaped("h0", h0, (B, D), torch.float32)
+    _shaped("dhN", dhN, (B, D), torch.float32)
+    dx = _like(h, stream) if dx is None else _out("dx", dx, h.shape, h.dtype, dev)
+    dalpha = _like(alpha, stream) if dalpha is None else _out("dalpha", dalpha, h.shape, torch.float32, dev)
+    if dh0 is not None:
+        _out("dh0", dh0, (B, D), torch.float32, dev)
+    elif h0 is not None:
+        dh0 = _like(h0, stream)
     _call("la_recurrence_backward", dev, stream, alpha.data_ptr(), h.data_ptr(), dh.data_ptr(), _ptr(h0), _ptr(dhN),
           dx.data_ptr(), dalpha.data_ptr(), _ptr(dh0), B, N, D, code)
     return dx, dalpha, dh0
@@ -216,13 +224,12 @@ def la_recurrence_step(state, x, alpha, h=None, stream=None):
         _start()
     if x.dim() != 2:
         raise ValueError("x must be [B, D]")
-    h = _like(x, stream) if h is None else h
-    dev = _place(state, x, alpha, h)
-    code = _dtype_code(x, h)
+    dev = _place(state, x, alpha)
+    code = _dtype_code(x)
     shape = _sizes(x)
     _shaped("alpha", alpha, shape, torch.float32)
     _shaped("state", state, shape, torch.float32)
-    _shaped("h", h, shape)
+    h = _like(x, stream) if h is None else _out("h", h, shape, x.dtype, dev)
     _call("la_recurrence_step", dev, stream, state.data_ptr(), x.data_ptr(), alpha.data_ptr(), h.data_ptr(),
           shape[0], shape[1], code)
     return h
@@ -254,12 +261,11 @@ def la_window_forward(q, k, v, window: int, sinks: int = 0, lens=None, scale: fl
     if torch is None:
         _start()
     B, Hq, Hk, Nq, Nk, d = _window_shapes(q, k, v, lens)
-    o = _like(q, stream) if o is None else o
-    lse = _new((B, Hq, Nq), torch.float32, q.device, stream) if lse is None else lse
-    dev = _place(q, k, v, lens, o, lse)
-    code = _dtype_code(q, k, v, o)
-    _shaped("o", o, q.shape)
-    _shaped("lse", lse, (B, Hq, Nq), torch.float32)
+    dev = _place(q, k, v, lens)
+    code = _dtype_code(q, k, v)
+    o = _like(q, stream) if o is None else _out("o", o, q.shape, q.dtype, dev)
+    lse = (_new((B, Hq, Nq), torch.float32, q.device, stream) if lse is None
+           else _out("lse", lse, (B, Hq, Nq), torch.float32, dev))
     _call("la_window_forward", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
           _ptr(lens), B, Hq, Hk, Nq, Nk, d, _int("window", window),
           _int("sinks", sinks), _scale(scale, d), code)
@@ -272,14 +278,14 @@ def la_window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0, lens=
     if torch is None:
         _start()
     B, Hq, Hk, Nq, Nk, d = _window_shapes(q, k, v, lens)
-    dq = _like(q, stream) if dq is None else dq
-    dk = _like(k, stream) if dk is None else dk
-    dv = _like(v, stream) if dv is None else dv
-    dev = _place(q, k, v, o, lse, dout, lens, dq, dk, dv)
-    code = _dtype_code(q, k, v, o, dout, dq, dk, dv)
-    for what, t, like in (("o", o, q), ("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _shaped(what, t, like.shape)
+    dev = _place(q, k, v, o, lse, dout, lens)
+    code = _dtype_code(q, k, v, o, dout)
+    _shaped("o", o, q.shape)
+    _shaped("dout", dout, q.shape)
     _shaped("lse", lse, (B, Hq, Nq), torch.float32)
+    dq = _like(q, stream) if dq is None else _out("dq", dq, q.shape, q.dtype, dev)
+    dk = _like(k, stream) if dk is None else _out("dk", dk, k.shape, k.dtype, dev)
+    dv = _like(v, stream) if dv is None else _out("dv", dv, v.shape, v.dtype, dev)
     _call("la_window_backward", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
           dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(lens), B, Hq, Hk, Nq, Nk, d, _int("window", window),
           _int("sinks", sinks), _scale(scale, d), code)
@@ -299,14 +305,12 @@ def la_window_cache(k, v, window: int, sinks: int = 0, lens=None, kc=None, vc=No
     if window < 1 or sinks < 0:
         raise ValueError("window must be at least 1, sinks at least 0")
     shape = (B, Hk, sinks + window, d)
-    kc = _new(shape, k.dtype, k.device, stream, "zeros") if kc is None else kc
-    vc = _new(shape, k.dtype, k.device, stream, "zeros") if vc is None else vc
-    dev = _place(k, v, lens, kc, vc)
-    code = _dtype_code(k, v, kc, vc)
+    dev = _place(k, v, lens)
+    code = _dtype_code(k, v)
     _shaped("v", v, k.shape)
-    _shaped("kc", kc, shape)
-    _shaped("vc", vc, shape)
     _shaped("lens", lens, (B,), torch.int32)
+    kc = _new(shape, k.dtype, k.device, stream, "zeros") if kc is None else _out("kc", kc, shape, k.dtype, dev)
+    vc = _new(shape, k.dtype, k.device, stream, "zeros") if vc is None else _out("vc", vc, shape, k.dtype, dev)
     _call("la_window_cache", dev, stream, k.data_ptr(), v.data_ptr(), kc.data_ptr(), vc.data_ptr(), _ptr(lens), B, Hk,
           N, d, window, sinks, code)
     return kc, vc
@@ -322,15 +326,15 @@ def la_window_decode_step(kc, vc, q, k, v, pos, window: int, sinks: int = 0, sca
     B, Hq, d = q.shape
     Hk = k.shape[1]
     window, sinks = _int("window", window), _int("sinks", sinks)
-    o = _like(q, stream) if o is None else o
-    dev = _place(kc, vc, q, k, v, pos, o)
-    code = _dtype_code(q, k, v, kc, vc, o)
+    dev = _place(kc, vc, q, k, v, pos)
+    code = _dtype_code(q, k, v, kc, vc)
     _shaped("k", k, (B, Hk, d))
     _shaped("v", v, (B, Hk, d))
-    _shaped("kc", kc, (B, Hk, sinks + window, d))
-    _shaped("vc", vc, (B, Hk, sinks + window, d))
+    shape = (B, Hk, sinks + window, d)
+    _shaped("kc", kc, shape)
+    _shaped("vc", vc, shape)
     _shaped("pos", pos, (B,), torch.int32)
-    _shaped("o", o, q.shape)
+    o = _like(q, stream) if o is None else _out("o", o, q.shape, q.dtype, dev)
     _call("la_window_decode_step", dev, stream, kc.data_ptr(), vc.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
           o.data_ptr(), pos.data_ptr(), B, Hq, Hk, d, window, sinks, _scale(scale, d), code)
     return o

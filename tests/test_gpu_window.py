@@ -374,3 +374,38 @@ def test_a_hybrid_block_runs_together():
         ot = lib.la_window_decode_step(kc, vc, tq, tk, v[:, :, t].contiguous().cuda(), pos, W, sinks=S)
         ht = lib.la_recurrence_step(st, ot.view(B, D), alpha[:, t].contiguous().cuda())
         assert float((ht - h[:, t]).abs().max()) < 1e-5
+
+
+def test_refusals_of_given_tensors():
+    """Outputs and inputs of another shape, type or layout, and tensors off the GPU."""
+    q, k = torch.zeros((1, 2, 8, 64), device="cuda"), torch.zeros((1, 1, 8, 64), device="cuda")
+    bad = [dict(o=torch.zeros((1, 2, 9, 64), device="cuda")), dict(o=q.bfloat16()), dict(lse=torch.zeros((1, 2, 8))),
+           dict(o=torch.zeros((1, 2, 64, 8), device="cuda").transpose(2, 3)), dict(lens=torch.zeros(1, device="cuda")),
+           dict(lens=torch.zeros(2, dtype=torch.int32, device="cuda"))]
+    for kw in bad:
+        with pytest.raises((ValueError, TypeError)):
+            la().la_window_forward(q, k, k, 4, **kw)
+    with pytest.raises(ValueError):
+        la().la_window_forward(q.transpose(1, 2), k, k, 4)
+    with pytest.raises(ValueError):
+        la().la_window_forward(q, k.cpu(), k, 4)
+    with pytest.raises(TypeError):
+        la().la_window_forward(q.half(), k.half(), k.half(), 4)
+    with pytest.raises(la().LAError):
+        la().la_window_forward(q, k, k, 0)
+    with pytest.raises(la().LAError):
+        la().la_window_forward(q, k, k, 4, scale=-1.0)
+    with pytest.raises(la().LAError):  # an output over an input
+        la().la_window_forward(q, k, k, 4, o=q)
+    x = torch.zeros((2, 3, 8), device="cuda")
+    for kw in (dict(h=x.bfloat16()), dict(hN=torch.zeros((2, 9), device="cuda")), dict(h0=torch.zeros((2, 8), device="cuda").half())):
+        with pytest.raises((ValueError, TypeError)):
+            la().la_recurrence_forward(x, x, **kw)
+    with pytest.raises(ValueError):
+        la().la_recurrence_forward(x, x.bfloat16())
+    with pytest.raises(ValueError):
+        la().la_rotary_forward(q, positions=torch.zeros((1, 8), dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        la().la_rotary_forward(q, layout="pairs")
+    with pytest.raises(la().LAError):
+        la().la_rotary_forward(q, rot=65)
