@@ -114,7 +114,7 @@ constexpr int kMaxTokens = 1 << 30;  // of a sequence or a cache: sums of two po
 la_status check_window(int B, int Hq, int Hk, int d, int window, int sinks, float scale, la_dtype dtype)
 {
     if (B < 0 || Hq < 0 || Hk < 0 || d < 0 || window < 1 || sinks < 0 || !known(dtype)) return LA_ERR_INVALID_ARG;
-    if (!isfinite(scale) || !(scale > 0.f)) return LA_ERR_INVALID_ARG;
+    if (!(scale >= 0x1p-100f) || !(scale <= 0x1p100f)) return LA_ERR_INVALID_ARG;
     if (Hk > 0 ? Hq % Hk != 0 : Hq != 0) return LA_ERR_INVALID_ARG;
     return LA_OK;
 }
@@ -261,7 +261,7 @@ la_status la_window_backward(const void *q, const void *k, const void *v, const 
     p.scale = scale;
     p.dtype = dtype;
     p.stream = s;
-    // D = dO . o per row, from the dq kernel to the dk, dv kernel, and partial sums.  The lock keeps two host
+    // D = dO . o per row and partial sums, from one kernel to the next.  The lock keeps two host
     // threads that share a stream from mixing their launches on its one workspace; a captured
     // call takes memory of its own, so that two graphs may be replayed at once.
     static std::mutex mu;

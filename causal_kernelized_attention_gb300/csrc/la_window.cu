@@ -7,9 +7,9 @@
 //             dq_p = sum_j dS_pj k_j,  dk_j = sum_p dS_pj q_p,  dv_j = sum_p P_pj dO_p
 //             (key and value heads: summed over the query heads that share them)
 //
-// The forward and the dq kernel give a CTA 64 query rows and pass over the key tiles their
+// The forward and the dq blocks give a CTA 64 query rows and pass over the key tiles their
 // window and the sinks reach (running maximum and sum of the softmax, the output rescaled as
-// the maximum grows); the dk, dv kernel gives a CTA 64 keys and passes over the query tiles
+// the maximum grows); the dk, dv blocks give a CTA 64 keys and passes over the query tiles
 // that see them, of every head of the group.  Where those CTAs are few, or a tile of sinks is
 // seen by every later row, a tile's query tiles are shared out over several CTAs, whose sums
 // a third kernel adds up; every sum is taken in a fixed order.  All products are fp32 fused multiply-adds on 4 x 4 register tiles fed
@@ -153,6 +153,7 @@ struct Args {
     int B, Hq, Hk, Nq, Nk, window, sinks;
     float scale;
     Split sp;     // dk, dv
+    unsigned dkv_blocks;
     float *part;  // [B Hk][units][dk, dv][64][D], of the tiles with several shares
 };
 
@@ -255,17 +256,34 @@ __device__ __forceinline__ void block_ds(float (&s)[4][4], float (&g)[4][4], con
     }
 }
 
+// ---------------------------------------------------------------- backward: D_p = dO . o
+// D / 4 lanes a row.
+template <int D>
+__global__ void __launch_bounds__(kThreads) window_delta_kernel(const Args a)
+{
+    constexpr int L = D / 4;
+    const long long row = ((long long)blockIdx.x * kThreads + threadIdx.x) / L;
+    const int c = threadIdx.x % L * 4;
+    float x = 0.f;
+    const long long rows = (long long)a.B * a.Hq * a.Nq;
+    if (row < rows)
+        x = dot4(*reinterpret_cast<const float4 *>(static_cast<const float *>(a.dout) + row * D + c),
+                 *reinterpret_cast<const float4 *>(static_cast<const float *>(a.o) + row * D + c), 0.f);
+#pragma unroll
+    for (int m = L / 2; m > 0; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
+    if (row < rows && c == 0) a.delta[row] = x;
+}
+
 // ---------------------------------------------------------------- backward: dq
 template <int D>
-__global__ void __launch_bounds__(kThreads) window_dq_kernel(const Args a)
+__device__ __forceinline__ void dq_block(const Args &a, const unsigned block, float *sm)
 {
-    extern __shared__ __align__(16) float sm[];
     float *q = sm, *go = q + kT * stride<D>(), *k = go + kT * stride<D>(), *v = k + kT * stride<D>();
     float *ds = v + kT * stride<D>();
     __shared__ float lse[kT], delta[kT];
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int tiles = (a.Nq + kT - 1) / kT;
-    const int bh = (int)(blockIdx.x / tiles), t0 = (int)(blockIdx.x % tiles) * kT;
+    const int bh = (int)(block / tiles), t0 = (int)(block % tiles) * kT;
     const int b = bh / a.Hq, h = bh % a.Hq, off = a.Nk - a.Nq;
     const int n = valid(a.lens, b, a.Nk);
     const size_t kvrow = ((size_t)b * a.Hk + h / (a.Hq / a.Hk)) * a.Nk, qrow = (size_t)bh * a.Nq;
@@ -273,21 +291,10 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(const Args a)
     const int rows = min(a.Nq, n - off);  // rows of tokens; the others are padding
     load_tile<D>(q, static_cast<const float *>(a.q) + qrow * D, t0, rows);
     load_tile<D>(go, static_cast<const float *>(a.dout) + qrow * D, t0, rows);
-    load_tile<D>(k, static_cast<const float *>(a.o) + qrow * D, t0, rows);
-    __syncthreads();
-    // D_p = dO . o, four threads a row
-    {
-        const int r = threadIdx.x >> 2, part = threadIdx.x & 3;
-        float x = 0.f;
-        for (int c = part; c < D; c += 4) x = fmaf(go[r * stride<D>() + c], k[r * stride<D>() + c], x);
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if (part == 0) {
-            const bool in = t0 + r < rows;
-            lse[r] = in ? a.lse[qrow + t0 + r] : 0.f;
-            delta[r] = x;
-            if (t0 + r < a.Nq) a.delta[qrow + t0 + r] = x;
-        }
+    if (threadIdx.x < kT) {
+        const bool in = t0 + (int)threadIdx.x < rows;
+        lse[threadIdx.x] = in ? a.lse[qrow + t0 + threadIdx.x] : 0.f;
+        delta[threadIdx.x] = in ? a.delta[qrow + t0 + threadIdx.x] : 0.f;
     }
     float acc[4][D / 16];
 #pragma unroll
@@ -336,14 +343,13 @@ __global__ void __launch_bounds__(kThreads) window_dq_kernel(const Args a)
 
 // ---------------------------------------------------------------- backward: dk, dv
 template <int D>
-__global__ void __launch_bounds__(kThreads) window_dkv_kernel(const Args a)
+__device__ __forceinline__ void dkv_block(const Args &a, const unsigned block, float *sm)
 {
-    extern __shared__ __align__(16) float sm[];
     float *k = sm, *v = k + kT * stride<D>(), *q = v + kT * stride<D>(), *go = q + kT * stride<D>();
     float *pt = go + kT * stride<D>(), *dst = pt + kT * kPS;  // transposed: rows of keys
     __shared__ float lse[kT], delta[kT];
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int units = a.sp.units(), bh = (int)(blockIdx.x / units), unit = (int)(blockIdx.x % units);
+    const int units = a.sp.units(), bh = (int)(block / units), unit = (int)(block % units);
     const int u1 = unit - a.sp.sinks * a.sp.sink_parts;  // >= 0: not a tile of sinks
     const int parts = u1 < 0 ? a.sp.sink_parts : a.sp.parts, share = (u1 < 0 ? unit : u1) % parts;
     const int j0 = (u1 < 0 ? unit / parts : a.sp.sinks + u1 / parts) * kT;
@@ -427,6 +433,18 @@ __global__ void __launch_bounds__(kThreads) window_dkv_kernel(const Args a)
     }
 }
 
+// Both kinds of blocks in one launch, the longer dk, dv ones first: neither waits for the other, and the
+// last wave is filled by either (padded batch of 3 x 509 rows: 20 + 16 us one after the other).
+template <int D>
+__global__ void __launch_bounds__(kThreads) window_backward_kernel(const Args a)
+{
+    extern __shared__ __align__(16) float sm[];
+    if (blockIdx.x < a.dkv_blocks)
+        dkv_block<D>(a, blockIdx.x, sm);
+    else
+        dq_block<D>(a, blockIdx.x - a.dkv_blocks, sm);
+}
+
 // Adds up the shares of the tiles that have several, in order: 4 features of one key a thread.
 template <int D>
 __global__ void __launch_bounds__(kThreads) window_sum_kernel(const Args a)
@@ -504,10 +522,12 @@ la_status backward(const WindowProblem &p)
     Args a = args_of(p);
     a.sp = split_of(p);
     a.part = reinterpret_cast<float *>(reinterpret_cast<char *>(p.delta) + delta_bytes(p));
-    la_status st = launch(window_dq_kernel<D>, (long long)p.B * p.Hq * ceil_div(p.Nq, kT), (4 * tile + prob) * sizeof(float), a,
-                          p.stream);
-    if (st == LA_OK)
-        st = launch(window_dkv_kernel<D>, (long long)p.B * p.Hk * a.sp.units(), (4 * tile + 2 * prob) * sizeof(float), a, p.stream);
+    const long long dkv = (long long)p.B * p.Hk * a.sp.units(), dq = (long long)p.B * p.Hq * ceil_div(p.Nq, kT);
+    if (dkv > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
+    a.dkv_blocks = (unsigned)dkv;
+    const long long rows = (long long)p.B * p.Hq * p.Nq;
+    la_status st = launch(window_delta_kernel<D>, (rows * (D / 4) + kThreads - 1) / kThreads, 0, a, p.stream);
+    if (st == LA_OK) st = launch(window_backward_kernel<D>, dkv + dq, (4 * tile + 2 * prob) * sizeof(float), a, p.stream);
     if (st != LA_OK || (a.sp.parts == 1 && (a.sp.sink_parts == 1 || a.sp.sinks == 0))) return st;
     return launch(window_sum_kernel<D>, ((long long)p.B * p.Hk * p.Nk * 2 * (D / 4) + kThreads - 1) / kThreads, 0, a, p.stream);
 }

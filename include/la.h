@@ -536,7 +536,7 @@ la_status la_recurrence_step(float *state, const void *x, const float *alpha, vo
  * rows at positions >= lens[b] are padding and give o = 0 and lse = -inf, keys there are
  * never used, whatever they hold.  Within the valid tokens an infinite or NaN k or v may
  * also reach rows of nearby positions that do not see it.  Supported: d in {32, 64, 128},
- * Nq <= Nk <= 2^30, Hq a multiple of Hk, window >= 1, sinks >= 0, scale > 0 and finite.  window >= Nk
+ * Nq <= Nk <= 2^30, Hq a multiple of Hk, window >= 1, sinks >= 0, scale in [2^-100, 2^100].  window >= Nk
  * is plain causal attention.
  *
  * la_window_backward: given o and lse of the forward and dout = dL/do, writes dq, dk, dv

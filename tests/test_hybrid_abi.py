@@ -96,7 +96,7 @@ def sized(f):
 
 
 BAD_SIZES = (dict(B=-1), dict(Hq=-4), dict(Hq=3), dict(Hk=0), dict(Nq=9), dict(Nq=-1), dict(window=0), dict(window=-5),
-             dict(sinks=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=NAN), dict(scale=INF), dict(dtype=5))
+             dict(sinks=-1), dict(scale=0.0), dict(scale=1e-38), dict(scale=1e35), dict(scale=-1.0), dict(scale=NAN), dict(scale=INF), dict(dtype=5))
 
 
 def test_window_forward(lib):
