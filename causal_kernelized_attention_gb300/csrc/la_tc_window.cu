@@ -2,9 +2,9 @@
 // of 64 or 128 columns (narrower heads zero-filled by TMA).  The mathematics is la_window.cu's:
 // one pass over the key tiles with the running maximum and sum of the softmax.
 //
-// A CTA takes two query tiles of 128 rows (for short windows one: see the dispatch) -- the same rows of two heads that share a key
+// A CTA takes two query tiles of 128 rows -- the same rows of two heads that share a key
 // head, or neighbouring rows of one head -- so each K and V tile brought into shared memory
-// feeds two of each product.  TMEM holds S_s (128 columns each) and O_s (one per query
+// feeds two of each product (for short windows one tile: see the dispatch).  TMEM holds S_s (128 columns each) and O_s (one per query
 // tile s); the weights P_s, rounded to bf16, are written over S_s and read from there by
 // the second product.  Warps 0-3 and 4-7 are the softmax groups of the two tiles (a thread
 // owns a row, no shuffles), warp 8 loads by TMA, warp 9 issues the MMAs:

@@ -21,7 +21,6 @@ constexpr uint64_t kDrainNs = 100000000ull;
 struct Params {
     float *lse;        // forward: written; backward: read
     float *delta;      // backward: -dO . o of every row, then -lse / scale, rows of an entry `padded`
-    const void *o;     // backward
     const int *lens;
     int B, Hq, Hk, Nq, Nk, window, sinks, d;
     int padded;  // Nq rounded up to whole tiles
@@ -170,7 +169,6 @@ inline Params params_of(const WindowProblem &p, bool single = false)
     Params prm;
     prm.lse = p.lse;
     prm.delta = p.delta;
-    prm.o = p.o;
     prm.lens = p.lens;
     prm.padded = tiles * kRows;
     prm.B = p.B; prm.Hq = p.Hq; prm.Hk = p.Hk; prm.Nq = p.Nq; prm.Nk = p.Nk;

@@ -1,9 +1,9 @@
 // Window attention backward on the tensor cores: bf16, d <= 128 on tiles of 64 or 128
-// columns.  Two kernels, so that every gradient is summed by one CTA in a fixed order:
+// columns.  D = dO . o of every row first (window_tc_rows), then one launch of two kinds of
+// blocks, so that every gradient is summed by one CTA in a fixed order:
 //
 //   dq      (a CTA: two query tiles of 128 rows, as the forward; key tiles of 64)
-//           D = dO . o per row (kept for the second kernel), S = Q K^T, dP = dO V^T,
-//           dS = P (dP - D), dQ += dS K;                              3 products a tile
+//           S = Q K^T, dP = dO V^T, dS = P (dP - D), dQ += dS K;      3 products a tile
 //   dk, dv  (a CTA: 128 keys; query tiles of 64 rows, of every head of the group)
 //           S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q;   4 products a tile
 //
@@ -99,13 +99,14 @@ struct DqSmem {
     int abort;
 };
 
+// The launch's tensor maps: tiles of 128 rows, and of 64 for what is streamed.
+struct Maps {
+    CUtensorMap q, go, k, v, q_half, go_half, k_half, v_half, dq, dk, dv;
+};
+
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 1)
-window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
-             const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-             const __grid_constant__ CUtensorMap map_dq, const Params prm)
+__device__ __forceinline__ void dq_block(const Maps &maps, const Params &prm, const int block, uint8_t *smem_raw)
 {
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
     DqSmem<DT> &sm = *reinterpret_cast<DqSmem<DT> *>(smem_raw);
     constexpr uint32_t kTile = DqSmem<DT>::kTile, kStage = DqSmem<DT>::kStage;
     const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
@@ -138,7 +139,7 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
     griddep_launch_dependents();
     const uint32_t tmem = sm.tmem_base;
     int *abort_flag = &sm.abort;
-    const Work<kHalf> w(prm, (int)blockIdx.x);
+    const Work<kHalf> w(prm, block);
     const int U = w.count();
 
     if (warp == kTmaWarp) {
@@ -152,7 +153,7 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
                 mbar_arrive_expect_tx(&sm.k_full[st], kStage);
 #pragma unroll
                 for (int x = 0; x < DT; x += 64)
-                    tma_load_3d(sm.k[st] + x / 64 * kHalfBox, &map_k, &sm.k_full[st], x, j0, kz);
+                    tma_load_3d(sm.k[st] + x / 64 * kHalfBox, &maps.k_half, &sm.k_full[st], x, j0, kz);
                 if (u == 0)
 #pragma unroll
                     for (int s = 0; s < 2; ++s)
@@ -161,8 +162,8 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
                             mbar_arrive_expect_tx(&sm.q_full[s], 2 * kTile);
 #pragma unroll
                             for (int x = 0; x < DT; x += 64) {
-                                tma_load_3d(sm.q[s] + x / 64 * kBox, &map_q, &sm.q_full[s], x, w.t0[s], z);
-                                tma_load_3d(sm.go[s] + x / 64 * kBox, &map_do, &sm.q_full[s], x, w.t0[s], z);
+                                tma_load_3d(sm.q[s] + x / 64 * kBox, &maps.q, &sm.q_full[s], x, w.t0[s], z);
+                                tma_load_3d(sm.go[s] + x / 64 * kBox, &maps.go, &sm.q_full[s], x, w.t0[s], z);
                             }
                         }
                 loaded = u + 1;
@@ -173,7 +174,7 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
                 mbar_arrive_expect_tx(&sm.v_full[st], kStage);
 #pragma unroll
                 for (int x = 0; x < DT; x += 64)
-                    tma_load_3d(sm.v[st] + x / 64 * kHalfBox, &map_v, &sm.v_full[st], x, j0, kz);
+                    tma_load_3d(sm.v[st] + x / 64 * kHalfBox, &maps.v_half, &sm.v_full[st], x, j0, kz);
             }
             // no copy may still be writing shared memory when the CTA exits
             if (loaded > 0)
@@ -257,42 +258,14 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
         const KeyTiles kt = s ? w.kt[1] : w.kt[0];
         const int t0 = s ? w.t0[1] : w.t0[0], z = w.b * prm.Hq + (s ? w.h[1] : w.h[0]);
         const int t = t0 + r, p = t + w.off, p_first = t0 + w.off, tiles = kt.count();
-        const size_t row = (size_t)z * prm.Nq + t;
         const bool live = t < prm.Nq && p < w.n;
         const float c = prm.scale * kLog2e;
         bool ok = !aborted(abort_flag);
-        // the row's lse in units of the raw scores, and its D
-        const float base = live ? __ldg(prm.lse + row) / prm.scale : 0.f;
-        float delta = 0.f;
-        {
-            uint4 ov[DT / 8];  // the row of o, in flight while Q and dO arrive
-            const uint4 *op = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(prm.o) + row * prm.d);
-#pragma unroll
-            for (int ch = 0; ch < DT / 8; ++ch)
-                ov[ch] = live && ch * 8 < prm.d ? __ldg(op + ch) : make_uint4(0u, 0u, 0u, 0u);
-            if (ok && tiles > 0 && (ok = wait_w(abort_flag, &sm.q_full[s], 0)) && live) {
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int ch = 0; ch < DT / 8; ++ch) {
-                    const uint4 y =
-                        *reinterpret_cast<const uint4 *>(sm.go[s] + (ch >> 3) * kBox + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-                    const uint32_t xs[4] = {ov[ch].x, ov[ch].y, ov[ch].z, ov[ch].w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        sum[e] = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), sum[e]);
-                        sum[e] = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), sum[e]);
-                    }
-                }
-                delta = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            }
-        }
-        // for the second kernel, rows of an entry padded to whole tiles
-        if (t0 < prm.Nq) {
-            const size_t at = (size_t)z * prm.padded + t;
-            prm.delta[at] = -delta;
-            prm.delta[(size_t)prm.B * prm.Hq * prm.padded + at] = -base;
-        }
-        const uint64_t base2 = pair(-base, -base), delta2 = pair(-delta, -delta), c2 = pair(c, c);
+        // the row's -lse in units of the raw scores, and its -D
+        const size_t at = (size_t)z * prm.padded + t;
+        const float delta = t0 < prm.Nq ? __ldcg(prm.delta + at) : 0.f;
+        const float base = t0 < prm.Nq ? __ldcg(prm.delta + (size_t)prm.B * prm.Hq * prm.padded + at) : 0.f;
+        const uint64_t base2 = pair(base, base), delta2 = pair(delta, delta), c2 = pair(c, c);
         for (int done = 0; ok && done < tiles; ++done) {
             const int j0 = kt.tile(done) * kHalf;
             if (!(ok = wait_w(abort_flag, &sm.s_full[s], (uint32_t)done & 1u))) break;
@@ -339,7 +312,7 @@ window_tc_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ 
         if (ok && t0 < prm.Nq && (warp & 3) == 0 && lane == 0) {
 #pragma unroll
             for (int x = 0; x < DT; x += 64)
-                tma_store_3d(&map_dq, sm.q[s] + x / 64 * kBox, x, t0, z);
+                tma_store_3d(&maps.dq, sm.q[s] + x / 64 * kBox, x, t0, z);
             tma_store_commit();
             tma_store_wait_all();
         }
@@ -388,6 +361,7 @@ __global__ void __launch_bounds__(256) window_tc_sum(const float *part, __nv_bfl
     if (j >= Nk || c >= d) return;
     const float *src = part + (tile * sp.parts * 2 + which) * (kRows * DT) + r * DT + c;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int i = 0; i < sp.parts; ++i) {
         const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + (size_t)i * 2 * kRows * DT));
         sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
@@ -413,13 +387,9 @@ struct DkvSmem {
 static_assert(sizeof(DkvSmem<128>) <= 232448, "fits an SM's shared memory");
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 1)
-window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
-              const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-              const __grid_constant__ CUtensorMap map_dk, const __grid_constant__ CUtensorMap map_dv, const Params prm,
-              const Split sp, float *part)
+__device__ __forceinline__ void dkv_block(const Maps &maps, const Params &prm, const Split &sp, float *part, const int block,
+                                          uint8_t *smem_raw)
 {
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
     DkvSmem<DT> &sm = *reinterpret_cast<DkvSmem<DT> *>(smem_raw);
     constexpr uint32_t kTile = DkvSmem<DT>::kTile, kStage = DkvSmem<DT>::kStage;
     const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
@@ -452,7 +422,7 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     int *abort_flag = &sm.abort;
 
     const int tiles = (prm.Nk + kRows - 1) / kRows, group = prm.Hq / prm.Hk, off = prm.Nk - prm.Nq;
-    const int units = tiles + sp.tiles * (sp.parts - 1), bh = (int)blockIdx.x / units, unit = (int)blockIdx.x % units;
+    const int units = tiles + sp.tiles * (sp.parts - 1), bh = block / units, unit = block % units;
     const bool shared = unit < sp.tiles * sp.parts && sp.parts > 1;  // a share of a tile of sinks
     const int j0 = (shared ? unit / sp.parts : unit - sp.tiles * (sp.parts - 1)) * kRows, b = bh / prm.Hk, hk = bh % prm.Hk;
     const int n = valid(prm.lens, b, prm.Nk);
@@ -468,8 +438,8 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             mbar_arrive_expect_tx(&sm.kv_full, 2 * kTile);
 #pragma unroll
             for (int x = 0; x < DT; x += 64) {
-                tma_load_3d(sm.k + x / 64 * kBox, &map_k, &sm.kv_full, x, j0, bh);
-                tma_load_3d(sm.v + x / 64 * kBox, &map_v, &sm.kv_full, x, j0, bh);
+                tma_load_3d(sm.k + x / 64 * kBox, &maps.k, &sm.kv_full, x, j0, bh);
+                tma_load_3d(sm.v + x / 64 * kBox, &maps.v, &sm.kv_full, x, j0, bh);
             }
             int loaded = 0;
             for (int i = 0; i < X; ++i) {
@@ -479,8 +449,8 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 mbar_arrive_expect_tx(&sm.q_full[st], 2 * kStage + 2 * kHalf * 4);
 #pragma unroll
                 for (int c = 0; c < DT; c += 64) {
-                    tma_load_3d(sm.q[st] + c / 64 * kHalfBox, &map_q, &sm.q_full[st], c, t0, z);
-                    tma_load_3d(sm.go[st] + c / 64 * kHalfBox, &map_do, &sm.q_full[st], c, t0, z);
+                    tma_load_3d(sm.q[st] + c / 64 * kHalfBox, &maps.q_half, &sm.q_full[st], c, t0, z);
+                    tma_load_3d(sm.go[st] + c / 64 * kHalfBox, &maps.go_half, &sm.q_full[st], c, t0, z);
                 }
                 const float *row = prm.delta + (size_t)z * prm.padded + t0;
                 bulk_load(sm.delta[st], row, kHalf * 4, &sm.q_full[st]);
@@ -634,7 +604,7 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         named_bar_sync(1 + s, 128);
         if (ok && !shared && (warp & 3) == 0 && lane == 0) {
 #pragma unroll
-            for (int x = 0; x < DT; x += 64) tma_store_3d(s == 0 ? &map_dv : &map_dk, out + x / 64 * kBox, x, j0, bh);
+            for (int x = 0; x < DT; x += 64) tma_store_3d(s == 0 ? &maps.dv : &maps.dk, out + x / 64 * kBox, x, j0, bh);
             tma_store_commit();
             tma_store_wait_all();
         }
@@ -644,6 +614,63 @@ window_tc_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Both kinds of blocks in one launch, the longer dk, dv ones first: neither waits for the other, and the
+// last wave is filled by either (8192 rows, d 128, window 1024: 243 us, 268 as two launches of 130
+// and 139 us, each with a last wave of its own).
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 1)
+window_tc_backward(const __grid_constant__ Maps maps, const Params prm, const Split sp, float *part, const int dkv_blocks)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    if ((int)blockIdx.x < dkv_blocks)
+        dkv_block<DT>(maps, prm, sp, part, (int)blockIdx.x, smem_raw);
+    else
+        dq_block<DT>(maps, prm, (int)blockIdx.x - dkv_blocks, smem_raw);
+}
+
+// -D = -dO . o and -lse / scale of every row, rows of an entry padded to whole tiles with zeros: 16
+// lanes a row, 64 rows of one head a CTA.
+constexpr int kRowsCta = 64;
+__global__ void __launch_bounds__(256) window_tc_rows(const __nv_bfloat16 *o, const __nv_bfloat16 *go, const Params prm)
+{
+    constexpr int kN = kRowsCta / 16;  // rows a thread
+    const int per = prm.padded / kRowsCta, z = (int)blockIdx.x / per, t0 = (int)blockIdx.x % per * kRowsCta + threadIdx.x / 16;
+    const int lane = threadIdx.x % 16;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int rows = min(prm.Nq, valid(prm.lens, z / prm.Hq, prm.Nk) - (prm.Nk - prm.Nq));  // of tokens
+    uint4 a[kN], b[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+        const int t = t0 + 16 * i;
+        if (t < rows && lane * 8 < prm.d) {
+            const size_t at = ((size_t)z * prm.Nq + t) * prm.d + lane * 8;
+            a[i] = __ldg(reinterpret_cast<const uint4 *>(o + at));
+            b[i] = __ldg(reinterpret_cast<const uint4 *>(go + at));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const uint32_t as[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, bs[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+        float x = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x = fmaf(__uint_as_float(as[e] << 16), __uint_as_float(bs[e] << 16), x);
+            x = fmaf(__uint_as_float(as[e] & 0xffff0000u), __uint_as_float(bs[e] & 0xffff0000u), x);
+        }
+#pragma unroll
+        for (int m = 8; m > 0; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
+        const int t = t0 + 16 * i;
+        if (lane == 0) {
+            const size_t at = (size_t)z * prm.padded + t;
+            prm.delta[at] = -x;
+            prm.delta[(size_t)prm.B * prm.Hq * prm.padded + at] =
+                t < rows ? -__ldg(prm.lse + (size_t)z * prm.Nq + t) / prm.scale : 0.f;
+        }
+    }
 }
 
 // Scratch: -D and -lse / scale of every row (rows of an entry padded to whole tiles), then the shares.
@@ -657,30 +684,31 @@ la_status backward(const WindowProblem &p)
     const long long dq_ctas = (long long)p.B * p.Hk * prm.units;
     const long long dkv_ctas = (long long)p.B * p.Hk * (ceil_div(p.Nk, kRows) + sp.tiles * (sp.parts - 1LL));
     const long long sum_ctas = (long long)split_floats(p, sp, DT) / std::max(sp.parts, 1) / 4 / 256;
+    const long long row_ctas = (long long)p.B * p.Hq * (prm.padded / kRowsCta);
+    if (dq_ctas + dkv_ctas > 0x7fffffffLL || sum_ctas > 0x7fffffffLL || row_ctas > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
     float *part = reinterpret_cast<float *>(reinterpret_cast<char *>(p.delta) + part_offset(p));
-    if (dq_ctas > 0x7fffffffLL || dkv_ctas > 0x7fffffffLL || sum_ctas > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
     const int bq = p.B * p.Hq, bk = p.B * p.Hk;
-    CUtensorMap mq, mdo, mk, mv, mqh, mdoh, mkh, mvh, mdq, mdk, mdv;
-    la_status st = make_map(&mq, p.q, bq, p.Nq, p.d);
-    if (st == LA_OK) st = make_map(&mdo, p.dout, bq, p.Nq, p.d);
-    if (st == LA_OK) st = make_map(&mk, p.k, bk, p.Nk, p.d);
-    if (st == LA_OK) st = make_map(&mv, p.v, bk, p.Nk, p.d);
-    if (st == LA_OK) st = make_map(&mqh, p.q, bq, p.Nq, p.d, kHalf);
-    if (st == LA_OK) st = make_map(&mdoh, p.dout, bq, p.Nq, p.d, kHalf);
-    if (st == LA_OK) st = make_map(&mkh, p.k, bk, p.Nk, p.d, kHalf);
-    if (st == LA_OK) st = make_map(&mvh, p.v, bk, p.Nk, p.d, kHalf);
-    if (st == LA_OK) st = make_map(&mdq, p.dq, bq, p.Nq, p.d);
-    if (st == LA_OK) st = make_map(&mdk, p.dk, bk, p.Nk, p.d);
-    if (st == LA_OK) st = make_map(&mdv, p.dv, bk, p.Nk, p.d);
-    if (st == LA_OK) st = ensure_smem((const void *)window_tc_dq<DT>, (int)sizeof(DqSmem<DT>));
-    if (st == LA_OK) st = ensure_smem((const void *)window_tc_dkv<DT>, (int)sizeof(DkvSmem<DT>));
+    Maps m;
+    la_status st = make_map(&m.q, p.q, bq, p.Nq, p.d);
+    if (st == LA_OK) st = make_map(&m.go, p.dout, bq, p.Nq, p.d);
+    if (st == LA_OK) st = make_map(&m.k, p.k, bk, p.Nk, p.d);
+    if (st == LA_OK) st = make_map(&m.v, p.v, bk, p.Nk, p.d);
+    if (st == LA_OK) st = make_map(&m.q_half, p.q, bq, p.Nq, p.d, kHalf);
+    if (st == LA_OK) st = make_map(&m.go_half, p.dout, bq, p.Nq, p.d, kHalf);
+    if (st == LA_OK) st = make_map(&m.k_half, p.k, bk, p.Nk, p.d, kHalf);
+    if (st == LA_OK) st = make_map(&m.v_half, p.v, bk, p.Nk, p.d, kHalf);
+    if (st == LA_OK) st = make_map(&m.dq, p.dq, bq, p.Nq, p.d);
+    if (st == LA_OK) st = make_map(&m.dk, p.dk, bk, p.Nk, p.d);
+    if (st == LA_OK) st = make_map(&m.dv, p.dv, bk, p.Nk, p.d);
+    constexpr int smem = (int)std::max(sizeof(DqSmem<DT>), sizeof(DkvSmem<DT>));
+    if (st == LA_OK) st = ensure_smem((const void *)window_tc_backward<DT>, smem);
     if (st != LA_OK) return st;
     count_launches(sp.parts > 1 ? 3 : 2);
-    st = launch_dependent(window_tc_dq<DT>, (unsigned)dq_ctas, kThreads, (int)sizeof(DqSmem<DT>), p.stream, mq, mdo, mkh, mvh,
-                          mdq, prm);
-    if (st != LA_OK) return st;
-    st = launch_dependent(window_tc_dkv<DT>, (unsigned)dkv_ctas, kThreads, (int)sizeof(DkvSmem<DT>), p.stream, mqh, mdoh, mk, mv,
-                          mdk, mdv, prm, sp, part);
+    st = launch_dependent(window_tc_rows, (unsigned)row_ctas, 256, 0, p.stream, static_cast<const __nv_bfloat16 *>(p.o),
+                          static_cast<const __nv_bfloat16 *>(p.dout), prm);
+    if (st == LA_OK)
+        st = launch_dependent(window_tc_backward<DT>, (unsigned)(dq_ctas + dkv_ctas), kThreads, smem, p.stream, m, prm, sp, part,
+                              (int)dkv_ctas);
     if (st != LA_OK || sp.parts == 1) return st;
     return launch_dependent(window_tc_sum<DT>, (unsigned)sum_ctas, 256, 0, p.stream, (const float *)part,
                             static_cast<__nv_bfloat16 *>(p.dk), static_cast<__nv_bfloat16 *>(p.dv), sp, p.Nk, p.d, p.scale);

@@ -9,13 +9,15 @@
 //
 // The forward and the dq blocks give a CTA 64 query rows and pass over the key tiles their
 // window and the sinks reach (running maximum and sum of the softmax, the output rescaled as
-// the maximum grows); the dk, dv blocks give a CTA 64 keys and passes over the query tiles
+// the maximum grows); the dk, dv blocks give a CTA 64 keys and pass over the query tiles
 // that see them, of every head of the group.  Where those CTAs are few, or a tile of sinks is
 // seen by every later row, a tile's query tiles are shared out over several CTAs, whose sums
-// a third kernel adds up; every sum is taken in a fixed order.  All products are fp32 fused multiply-adds on 4 x 4 register tiles fed
-// by 16-byte shared-memory loads (8 loads for 64 multiply-adds), rows padded by 4 floats so
-// that the 8 threads of a quarter-warp meet 8 different bank groups: bound by the CUDA
-// cores' fp32 rate.  fp32 calls run here; bf16 calls run on the tensor cores.
+// one more kernel adds up; every sum is taken in a fixed order.  All products are fp32 fused
+// multiply-adds on 4 x 4 register tiles fed by 16-byte shared-memory loads (8 loads for 64
+// multiply-adds), rows padded by 4 floats so that the 8 threads of a quarter-warp meet 8
+// different bank groups: bound by the CUDA cores' fp32 rate (2048 rows, window 512, d 128:
+// forward 43 TFLOP/s, backward 36 by the algorithm's 10 d operations a pair).  fp32 calls run
+// here; bf16 calls run on the tensor cores.
 #include <math.h>
 
 #include <algorithm>
@@ -433,8 +435,8 @@ __device__ __forceinline__ void dkv_block(const Args &a, const unsigned block, f
     }
 }
 
-// Both kinds of blocks in one launch, the longer dk, dv ones first: neither waits for the other, and the
-// last wave is filled by either (padded batch of 3 x 509 rows: 20 + 16 us one after the other).
+// Both kinds of blocks in one launch, the dk, dv ones first: neither waits for the other, and the last
+// wave is filled by either (padded batch of 3 x 509 rows: 34 us in all, 42 as two launches).
 template <int D>
 __global__ void __launch_bounds__(kThreads) window_backward_kernel(const Args a)
 {
@@ -459,6 +461,7 @@ __global__ void __launch_bounds__(kThreads) window_sum_kernel(const Args a)
     const int unit = sink ? tile * parts : a.sp.sinks * a.sp.sink_parts + (tile - a.sp.sinks) * parts;
     const float *src = a.part + (((size_t)bh * a.sp.units() + unit) * 2 + which) * kT * D + (j % kT) * D + c;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int i = 0; i < parts; ++i) {
         const float4 x = *reinterpret_cast<const float4 *>(src + (size_t)i * 2 * kT * D);
         sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
