@@ -18,7 +18,7 @@
 // 2^8 above the usual, which neither fp32 sums nor bf16's relative rounding notice, and the
 // read-modify-write of O leaves the loop.  Tiles that every row sees skip the mask.
 //
-// The weights' rounding to bf16 (2^-9 relative each, independent) enters the output like the
+// The weights' rounding to bf16 (2^-8 relative at most, each on its own) enters the output like the
 // rounding of the output itself; sums, maxima and the accumulator are fp32.
 #include "la_tc_window.cuh"
 
@@ -85,7 +85,7 @@ __device__ __forceinline__ float row_max(const uint32_t (&a)[128])
 __device__ __forceinline__ void weights(uint32_t (&a)[128], float c, float m, float &top, uint64_t &sum)
 {
     float base = m == -INFINITY ? 0.f : -m * c, past = 0.f;
-    const bool huge = __any_sync(0xffffffffu, fabsf(m) > 0x1p100f && m != -INFINITY);
+    const bool huge = __any_sync(0xffffffffu, fabsf(m) * c > 0x1p100f && m != -INFINITY);
     if (huge) {  // m c may overflow: subtract first
         past = row_max(a);
         const float z = m == -INFINITY ? 0.f : m;

@@ -13,7 +13,7 @@
 // Two groups of four warps work in turn, as in the forward: while one forms P and dS of its
 // tile (a thread a row), the tensor core runs the products of the other's.  In dk, dv a
 // thread owns a key, for which the visible queries are one interval.  The rounding of dS
-// (2^-9 relative, like P's) is the size of the gradients' own; sums are fp32.
+// (2^-8 relative at most, like P's) is the size of the gradients' own; sums are fp32.
 //
 // A tile of sinks is seen by every later row.  Its rows are shared out over several CTAs,
 // each about a window tile's work; their fp32 sums go to scratch and a third, small kernel

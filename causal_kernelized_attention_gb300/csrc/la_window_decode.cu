@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) decode_f32_kernel(const Args 
 // slots per warp in flight.  A lane's 16 bytes of a key serve two matrix steps: the order
 // of the features inside a product is free, so q and K are both read in the order the
 // bytes lie in.  P enters as a high and a low bf16 part (two products), so the only
-// rounding of the weights is at 2^-17.
+// rounding of the weights is at 2^-16.
 constexpr int kMmaWarps = 2;
 constexpr int kStages = 3;
 constexpr int kRows = 16;  // heads of one pass
