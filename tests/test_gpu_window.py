@@ -78,6 +78,15 @@ def test_padded_batches(dtype, Nq, Nk, d, window, sinks, lens):
 
 @pytest.mark.parametrize("d", [32, 64, 128])
 @pytest.mark.parametrize("B,Hq,Hk,Nq,Nk,window,sinks,lens", [
+    (2, 80, 40, 1, 1, 1, 0, None), (2, 80, 40, 129, 129, 50, 3, None), (3, 60, 20, 64, 200, 64, 65, [200, 150, 63]),
+    (3, 52, 26, 130, 130, 1000, 0, [1, 0, 129]), (2, 40, 40, 200, 333, 100, 150, None)])
+def test_many_query_tiles(d, B, Hq, Hk, Nq, Nk, window, sinks, lens):
+    """More query tiles than SMs: the forms that share an SM."""
+    check("bf16", B, Hq, Hk, Nq, Nk, d, window, sinks, lens=lens, spoil=lens is not None)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("B,Hq,Hk,Nq,Nk,window,sinks,lens", [
     (1, 4, 2, 2100, 2100, 64, 4, None), (2, 2, 1, 1500, 1600, 30, 200, [1600, 700])])
 def test_sinks_shared_out(d, B, Hq, Hk, Nq, Nk, window, sinks, lens):
     """Sequences many windows long: the sinks' gradients are summed from several blocks."""
@@ -85,14 +94,16 @@ def test_sinks_shared_out(d, B, Hq, Hk, Nq, Nk, window, sinks, lens):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_large_scores(dtype):
+@pytest.mark.parametrize("H", [2, 80])
+def test_large_scores(dtype, H):
     """Scores of hundreds, which exp alone would overflow, and a scale of its own."""
-    check(dtype, 1, 2, 1, 200, 200, 64, 77, 2, scale=0.6, big=4.0)
+    check(dtype, 1, H, H // 2, 200, 200, 64, 77, 2, scale=0.6, big=4.0)
 
 
-def test_lowest_values_are_not_masks():
+@pytest.mark.parametrize("H,d", [(1, 64), (100, 64), (1, 128)])
+def test_lowest_values_are_not_masks(H, d):
     """Scores at the type's lowest values still take part: equal scores give the plain mean."""
-    B, H, N, d = 1, 1, 140, 64
+    B, N = 1, 140
     q = torch.zeros((B, H, N, d), dtype=torch.bfloat16)
     k = torch.zeros_like(q)
     q[..., 0], k[..., 0] = 1.0, torch.finfo(torch.bfloat16).min
@@ -100,6 +111,7 @@ def test_lowest_values_are_not_masks():
     o, lse = la().la_window_forward(q.cuda(), k.cuda(), v.cuda(), 20, scale=1.0)
     want = torch.stack([v[0, 0, max(0, p - 19):p + 1].double().mean(0) for p in range(N)])
     ref.assert_within(o[0, 0], want, 2.0 ** -8 * (want.abs() + 1.0) + 1e-6)
+    assert bool(torch.isfinite(o).all())
 
 
 def test_deterministic_and_neighbours_untouched():
@@ -220,13 +232,15 @@ def test_given_stream_owns_what_it_writes():
         la().la_window_forward(k, k.float(), k, 50)
 
 
-def test_nonfinite_rows_stay_their_own():
+@pytest.mark.parametrize("H,d", [(1, 64), (60, 64), (1, 128)])
+def test_nonfinite_rows_stay_their_own(H, d):
     """An infinite score, a NaN query: their rows, and no others."""
-    q, k, v = (ref.draw(i, (1, 1, 300, 64), torch.bfloat16) for i in (1, 2, 3))
+    q, k, v = (ref.draw(i, (1, H, 300, d), torch.bfloat16) for i in (1, 2, 3))
     q[0, 0, 100, 3], q[0, 0, 200, 5] = float("nan"), float("inf")
     o, lse = la().la_window_forward(q.cuda(), k.cuda(), v.cuda(), 40, sinks=1)
     bad = ~torch.isfinite(o[0, 0].cpu()).all(1)
     assert bad.nonzero().flatten().tolist() == [100, 200]
+    assert bool(torch.isfinite(o[0, 1:]).all())
 
 
 # ---------------------------------------------------------------- serving
