@@ -12,7 +12,7 @@
 // the maximum grows); the dk, dv blocks give a CTA 64 keys and pass over the query tiles
 // that see them, of every head of the group.  Where those CTAs are few, or a tile of sinks is
 // seen by every later row, a tile's query tiles are shared out over several CTAs, whose sums
-// one more kernel adds up; every sum is taken in a fixed order.  All products are fp32 fused
+// the last of them adds up; every sum is taken in a fixed order.  All products are fp32 fused
 // multiply-adds on 4 x 4 register tiles fed by 16-byte shared-memory loads (8 loads for 64
 // multiply-adds), rows padded by 4 floats so that the 8 threads of a quarter-warp meet 8
 // different bank groups: bound by the CUDA cores' fp32 rate (2048 rows, window 512, d 128:
@@ -157,6 +157,8 @@ struct Args {
     Split sp;     // dk, dv
     unsigned dkv_blocks;
     float *part;  // [B Hk][units][dk, dv][64][D], of the tiles with several shares
+    int *left;    // [B Hk][tiles] shares left so far, zeroed by the delta kernel
+    int shared;   // B Hk tiles, or 0 where no tile has several shares
 };
 
 // ---------------------------------------------------------------- forward
@@ -259,12 +261,14 @@ __device__ __forceinline__ void block_ds(float (&s)[4][4], float (&g)[4][4], con
 }
 
 // ---------------------------------------------------------------- backward: D_p = dO . o
-// D / 4 lanes a row.
+// D / 4 lanes a row; also zeroes the counters of the shared tiles.
 template <int D>
 __global__ void __launch_bounds__(kThreads) window_delta_kernel(const Args a)
 {
     constexpr int L = D / 4;
     const long long row = ((long long)blockIdx.x * kThreads + threadIdx.x) / L;
+    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < a.shared; i += (long long)gridDim.x * kThreads)
+        a.left[i] = 0;
     const int c = threadIdx.x % L * 4;
     float x = 0.f;
     const long long rows = (long long)a.B * a.Hq * a.Nq;
@@ -419,6 +423,26 @@ __device__ __forceinline__ void dkv_block(const Args &a, const unsigned block, f
                 *reinterpret_cast<float2 *>(dst + at) = make_float2(dk[i][2 * c], dk[i][2 * c + 1]);
                 *reinterpret_cast<float2 *>(dst + kT * D + at) = make_float2(dv[i][2 * c], dv[i][2 * c + 1]);
             }
+        // the block that is the last to leave its share adds all of them up, in order
+        __shared__ int last;
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) last = atomicAdd(a.left + (size_t)bh * a.sp.tiles + j0 / kT, 1) == parts - 1;
+        __syncthreads();
+        if (!last) return;
+        __threadfence();
+        const float *src = a.part + ((size_t)bh * units + unit - share) * 2 * kT * D;
+        for (int e = threadIdx.x; e < 2 * kT * (D / 4); e += kThreads) {
+            const int c = e % (D / 4) * 4, r = e / (D / 4) % kT, which = e / (D / 4) / kT;
+            if (j0 + r >= a.Nk) continue;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int i = 0; i < parts; ++i) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + ((size_t)i * 2 + which) * kT * D + r * D + c));
+                sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
+            }
+            *reinterpret_cast<float4 *>(static_cast<float *>(which ? a.dv : a.dk) + (kvrow + j0 + r) * D + c) = sum;
+        }
         return;
     }
     float *dkp = static_cast<float *>(a.dk) + kvrow * D, *dvp = static_cast<float *>(a.dv) + kvrow * D;
@@ -445,28 +469,6 @@ __global__ void __launch_bounds__(kThreads) window_backward_kernel(const Args a)
         dkv_block<D>(a, blockIdx.x, sm);
     else
         dq_block<D>(a, blockIdx.x - a.dkv_blocks, sm);
-}
-
-// Adds up the shares of the tiles that have several, in order: 4 features of one key a thread.
-template <int D>
-__global__ void __launch_bounds__(kThreads) window_sum_kernel(const Args a)
-{
-    const long long e = (long long)blockIdx.x * kThreads + threadIdx.x;  // (bh, key, dk or dv, 4 features)
-    const int c = (int)(e % (D / 4)) * 4, which = (int)(e / (D / 4) % 2);
-    const long long row = e / (D / 4) / 2, bh = row / a.Nk;
-    const int j = (int)(row % a.Nk), tile = j / kT;
-    const bool sink = tile < a.sp.sinks;
-    const int parts = sink ? a.sp.sink_parts : a.sp.parts;
-    if (bh >= (long long)a.B * a.Hk || parts == 1) return;
-    const int unit = sink ? tile * parts : a.sp.sinks * a.sp.sink_parts + (tile - a.sp.sinks) * parts;
-    const float *src = a.part + (((size_t)bh * a.sp.units() + unit) * 2 + which) * kT * D + (j % kT) * D + c;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = 0; i < parts; ++i) {
-        const float4 x = *reinterpret_cast<const float4 *>(src + (size_t)i * 2 * kT * D);
-        sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
-    }
-    *reinterpret_cast<float4 *>(static_cast<float *>(which ? a.dv : a.dk) + row * D + c) = sum;
 }
 
 Args args_of(const WindowProblem &p)
@@ -518,6 +520,12 @@ Split split_of(const WindowProblem &p)
     return sp;
 }
 
+size_t part_floats(const WindowProblem &p, const Split &sp)
+{
+    const bool shared = sp.parts > 1 || (sp.sinks > 0 && sp.sink_parts > 1);
+    return shared ? (size_t)p.B * p.Hk * sp.units() * 2 * kT * p.d : 0;
+}
+
 template <int D>
 la_status backward(const WindowProblem &p)
 {
@@ -525,14 +533,15 @@ la_status backward(const WindowProblem &p)
     Args a = args_of(p);
     a.sp = split_of(p);
     a.part = reinterpret_cast<float *>(reinterpret_cast<char *>(p.delta) + delta_bytes(p));
+    a.left = reinterpret_cast<int *>(a.part + part_floats(p, a.sp));
     const long long dkv = (long long)p.B * p.Hk * a.sp.units(), dq = (long long)p.B * p.Hq * ceil_div(p.Nq, kT);
     if (dkv > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
     a.dkv_blocks = (unsigned)dkv;
+    a.shared = part_floats(p, a.sp) ? p.B * p.Hk * a.sp.tiles : 0;  // no more than dkv
     const long long rows = (long long)p.B * p.Hq * p.Nq;
     la_status st = launch(window_delta_kernel<D>, (rows * (D / 4) + kThreads - 1) / kThreads, 0, a, p.stream);
-    if (st == LA_OK) st = launch(window_backward_kernel<D>, dkv + dq, (4 * tile + 2 * prob) * sizeof(float), a, p.stream);
-    if (st != LA_OK || (a.sp.parts == 1 && (a.sp.sink_parts == 1 || a.sp.sinks == 0))) return st;
-    return launch(window_sum_kernel<D>, ((long long)p.B * p.Hk * p.Nk * 2 * (D / 4) + kThreads - 1) / kThreads, 0, a, p.stream);
+    if (st != LA_OK) return st;
+    return launch(window_backward_kernel<D>, dkv + dq, (4 * tile + 2 * prob) * sizeof(float), a, p.stream);
 }
 
 }  // namespace
@@ -546,8 +555,8 @@ la_status window_forward_simt(const WindowProblem &p)
 size_t window_backward_simt_scratch(const WindowProblem &p)
 {
     const Split sp = split_of(p);
-    const bool shared = sp.parts > 1 || (sp.sinks > 0 && sp.sink_parts > 1);
-    return delta_bytes(p) + (shared ? (size_t)p.B * p.Hk * sp.units() * 2 * kT * p.d * 4 : 0);
+    const size_t part = part_floats(p, sp);
+    return delta_bytes(p) + part * sizeof(float) + (part ? (size_t)p.B * p.Hk * sp.tiles * sizeof(int) : 0);
 }
 
 la_status window_backward_simt(const WindowProblem &p)
