@@ -13,7 +13,12 @@
 // Two groups of four warps work in turn, as in the forward: while one forms P and dS of its
 // tile (a thread a row), the tensor core runs the products of the other's.  In dk, dv a
 // thread owns a key, for which the visible queries are one interval.  The rounding of dS
-// (2^-8 relative at most, like P's) is the size of the gradients' own; sums are fp32.
+// (2^-8 relative at most, like P's) is the size of the gradients' own; sums are fp32.  Up to
+// 128 query rows, where a sum may have one or two large terms and their rounding would stand
+// out beside the gradients' own (up to 2.5 times it), dS is multiplied as two bf16 parts: 15.2 us instead
+// of 14.0 at 128 rows, 16 heads, d 128, where latency counts; for all sizes it would cost
+// 277 us instead of 243 at 8192, where the error is 1.4 times the gradients' own rounding for
+// any draw of the terms.
 //
 // A tile of sinks is seen by every later row.  Its rows are shared out over several CTAs,
 // each about a window tile's work; their fp32 sums go to scratch and a third, small kernel
@@ -39,6 +44,27 @@ constexpr int kThreads = 320;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kHalfBox = kHalf * 128;  // one [64 rows x 64 bf16] swizzled box: 8 KB
 constexpr uint32_t tS = 0, tP = 128, tG = 256;  // S_s at 64 s, dP_s at 128 + 64 s, gradients from 256
+// dS lies over the 32 columns that each half of it came from: 16 columns of bf16 pairs, then 16 of
+// what their rounding left (where that is multiplied too).
+constexpr uint32_t kRest = 16;
+__device__ __forceinline__ constexpr uint32_t ds_at(int kk) { return (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8); }
+
+// Rounds a half's 32 values to bf16 at TMEM address t, and with kFine the rest behind them.
+template <bool kFine>
+__device__ __forceinline__ void store_ds(uint32_t t, const uint32_t (&x)[32])
+{
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+    tmem_st16(t, pk);
+    if constexpr (kFine) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            pk[e] = pack_bf16(__uint_as_float(x[2 * e]) - __uint_as_float(pk[e] << 16),
+                              __uint_as_float(x[2 * e + 1]) - __uint_as_float(pk[e] & 0xffff0000u));
+        tmem_st16(t + kRest, pk);
+    }
+}
 
 __device__ __forceinline__ bool wait_b(int *abort_flag, uint64_t *bar, uint32_t parity)
 {
@@ -104,7 +130,7 @@ struct Maps {
     CUtensorMap q, go, k, v, q_half, go_half, k_half, v_half, dq, dk, dv;
 };
 
-template <int DT>
+template <int DT, bool kFine>
 __device__ __forceinline__ void dq_block(const Maps &maps, const Params &prm, const int block, uint8_t *smem_raw)
 {
     DqSmem<DT> &sm = *reinterpret_cast<DqSmem<DT> *>(smem_raw);
@@ -208,8 +234,13 @@ __device__ __forceinline__ void dq_block(const Maps &maps, const Params &prm, co
                         const uint64_t d = kt + pst * (kStage >> 4);
 #pragma unroll
                         for (int kk = 0; kk < kHalf / 16; ++kk)
-                            mma_ts(tmem + tG + s * DT, tmem + tS + s * kHalf + kk * 8, d + kk * (2048 >> 4), id_g,
+                            mma_ts(tmem + tG + s * DT, tmem + tS + s * kHalf + ds_at(kk), d + kk * (2048 >> 4), id_g,
                                    fed[s] > 0 || kk > 0);
+                        if (kFine)
+#pragma unroll
+                            for (int kk = 0; kk < kHalf / 16; ++kk)
+                                mma_ts(tmem + tG + s * DT, tmem + tS + s * kHalf + ds_at(kk) + kRest, d + kk * (2048 >> 4),
+                                       id_g, true);
                     }
                     ++fed[s];
                     pending[s] = false;
@@ -274,7 +305,7 @@ __device__ __forceinline__ void dq_block(const Maps &maps, const Params &prm, co
                                (p_first + kRows - 1 - j0 < prm.window || j0 + kHalf <= prm.sinks);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                uint32_t a[32], b[32], pk[16];
+                uint32_t a[32], b[32];
                 tmem_ld32(ts + 32 * g, a);
                 tmem_ld32(tp + 32 * g, b);
                 tmem_ld_wait();
@@ -293,9 +324,7 @@ __device__ __forceinline__ void dq_block(const Maps &maps, const Params &prm, co
                     for (int e = 0; e < 32; ++e)
                         if (!((bits >> e) & 1u)) a[e] = 0u;
                 }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
-                tmem_st16(ts + 16 * g, pk);
+                store_ds<kFine>(ts + 32 * g, a);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -386,7 +415,7 @@ struct DkvSmem {
 };
 static_assert(sizeof(DkvSmem<128>) <= 232448, "fits an SM's shared memory");
 
-template <int DT>
+template <int DT, bool kFine>
 __device__ __forceinline__ void dkv_block(const Maps &maps, const Params &prm, const Split &sp, float *part, const int block,
                                           uint8_t *smem_raw)
 {
@@ -485,8 +514,13 @@ __device__ __forceinline__ void dkv_block(const Maps &maps, const Params &prm, c
                         mma_ts(tmem + tG, tmem + tS + s * kHalf + kk * 8, gt + so + kk * (2048 >> 4), id_g, back > 0 || kk > 0);
 #pragma unroll
                     for (int kk = 0; kk < kHalf / 16; ++kk)
-                        mma_ts(tmem + tG + DT, tmem + tP + s * kHalf + kk * 8, qt_ + so + kk * (2048 >> 4), id_g,
+                        mma_ts(tmem + tG + DT, tmem + tP + s * kHalf + ds_at(kk), qt_ + so + kk * (2048 >> 4), id_g,
                                back > 0 || kk > 0);
+                    if (kFine)
+#pragma unroll
+                        for (int kk = 0; kk < kHalf / 16; ++kk)
+                            mma_ts(tmem + tG + DT, tmem + tP + s * kHalf + ds_at(kk) + kRest, qt_ + so + kk * (2048 >> 4),
+                                   id_g, true);
                     mma_commit(&sm.q_empty[bst]);
                 }
                 if (++bst == kRowStages) bst = 0;
@@ -571,9 +605,7 @@ __device__ __forceinline__ void dkv_block(const Maps &maps, const Params &prm, c
 #pragma unroll
                 for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
                 tmem_st16(ts + 16 * g, pk);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]));
-                tmem_st16(tp + 16 * g, pk);
+                store_ds<kFine>(tp + 32 * g, d);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -619,15 +651,15 @@ __device__ __forceinline__ void dkv_block(const Maps &maps, const Params &prm, c
 // Both kinds of blocks in one launch, the longer dk, dv ones first: neither waits for the other, and the
 // last wave is filled by either (8192 rows, d 128, window 1024: 243 us, 268 as two launches of 130
 // and 139 us, each with a last wave of its own).
-template <int DT>
+template <int DT, bool kFine>
 __global__ void __launch_bounds__(kThreads, 1)
 window_tc_backward(const __grid_constant__ Maps maps, const Params prm, const Split sp, float *part, const int dkv_blocks)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     if ((int)blockIdx.x < dkv_blocks)
-        dkv_block<DT>(maps, prm, sp, part, (int)blockIdx.x, smem_raw);
+        dkv_block<DT, kFine>(maps, prm, sp, part, (int)blockIdx.x, smem_raw);
     else
-        dq_block<DT>(maps, prm, (int)blockIdx.x - dkv_blocks, smem_raw);
+        dq_block<DT, kFine>(maps, prm, (int)blockIdx.x - dkv_blocks, smem_raw);
 }
 
 // -D = -dO . o and -lse / scale of every row, rows of an entry padded to whole tiles with zeros: 16
@@ -680,6 +712,8 @@ template <int DT>
 la_status backward(const WindowProblem &p)
 {
     const Params prm = params_of(p);
+    const bool fine = p.Nq <= kRows;
+    const auto kernel = fine ? window_tc_backward<DT, true> : window_tc_backward<DT, false>;
     const Split sp = split_of(p);
     const long long dq_ctas = (long long)p.B * p.Hk * prm.units;
     const long long dkv_ctas = (long long)p.B * p.Hk * (ceil_div(p.Nk, kRows) + sp.tiles * (sp.parts - 1LL));
@@ -701,13 +735,13 @@ la_status backward(const WindowProblem &p)
     if (st == LA_OK) st = make_map(&m.dk, p.dk, bk, p.Nk, p.d);
     if (st == LA_OK) st = make_map(&m.dv, p.dv, bk, p.Nk, p.d);
     constexpr int smem = (int)std::max(sizeof(DqSmem<DT>), sizeof(DkvSmem<DT>));
-    if (st == LA_OK) st = ensure_smem((const void *)window_tc_backward<DT>, smem);
+    if (st == LA_OK) st = ensure_smem((const void *)kernel, smem);
     if (st != LA_OK) return st;
     count_launches(sp.parts > 1 ? 3 : 2);
     st = launch_dependent(window_tc_rows, (unsigned)row_ctas, 256, 0, p.stream, static_cast<const __nv_bfloat16 *>(p.o),
                           static_cast<const __nv_bfloat16 *>(p.dout), prm);
     if (st == LA_OK)
-        st = launch_dependent(window_tc_backward<DT>, (unsigned)(dq_ctas + dkv_ctas), kThreads, smem, p.stream, m, prm, sp, part,
+        st = launch_dependent(kernel, (unsigned)(dq_ctas + dkv_ctas), kThreads, smem, p.stream, m, prm, sp, part,
                               (int)dkv_ctas);
     if (st != LA_OK || sp.parts == 1) return st;
     return launch_dependent(window_tc_sum<DT>, (unsigned)sum_ctas, 256, 0, p.stream, (const float *)part,

@@ -423,3 +423,31 @@ def test_refusals_of_given_tensors():
         la().la_rotary_forward(q, layout="pairs")
     with pytest.raises(la().LAError):
         la().la_rotary_forward(q, rot=65)
+
+
+@pytest.mark.parametrize("B,Hq,Hk,Nq,Nk,d,window,sinks", [
+    (3, 4, 2, 2, 2, 64, 20, 0), (2, 4, 1, 5, 5, 128, 3, 1), (1, 6, 3, 33, 33, 32, 16, 4), (2, 2, 1, 128, 128, 64, 50, 0),
+    (2, 4, 2, 70, 300, 128, 100, 70)])
+def test_short_gradients_are_rounded_once(B, Hq, Hk, Nq, Nk, d, window, sinks):
+    """Up to 128 query rows dq and dk carry little more than their own rounding.
+
+    Bound: half a step (2^-8) of the result, plus 2^-13 of A, the sum of scale P (|dO| . |v| + |dO| . |o|) |k|
+    (or |q|).  dS is held in two bf16 parts (2^-16 of it, |dS| <= A's terms), dP and D are sums of d products
+    in fp32 (at most d 2^-24 <= 2^-17 of their absolute values), P within 2^-16 for scores of a few units,
+    and up to 600 products of a sum add 600 2^-24 < 2^-14 of A: together below 2^-13.  One rounding of
+    dS alone would add up to 2^-8 |dS|, where |dS| is about a quarter of A's terms at d 32, an eighth at 128."""
+    q, go = ref.draw(1, (B, Hq, Nq, d), torch.bfloat16), ref.draw(2, (B, Hq, Nq, d), torch.bfloat16)
+    k, v = ref.draw(3, (B, Hk, Nk, d), torch.bfloat16), ref.draw(4, (B, Hk, Nk, d), torch.bfloat16)
+    o, lse = la().la_window_forward(q.cuda(), k.cuda(), v.cuda(), window, sinks=sinks)
+    dq, dk, _ = la().la_window_backward(q.cuda(), k.cuda(), v.cuda(), o, lse, go.cuda(), window, sinks=sinks)
+    group, scale = Hq // Hk, 1 / math.sqrt(d)
+    q, go, o, k, v = (x.cpu().double() for x in (q, go, o, k, v))
+    k, v = (x.repeat_interleave(group, 1) for x in (k, v))
+    z = q @ k.transpose(-1, -2) * scale - lse.cpu().double()[..., None]
+    p = z.exp().masked_fill(~ref.visible(Nq, Nk, window, sinks, Nk), 0.0)
+    ds = scale * p * (go @ v.transpose(-1, -2) - (go * o).sum(-1, keepdim=True))
+    da = scale * p * (go.abs() @ v.abs().transpose(-1, -2) + (go.abs() * o.abs()).sum(-1, keepdim=True))
+    shared = lambda x: x.view(B, Hk, group, Nk, d).sum(2)  # noqa: E731
+    for got, want, most in ((dq, ds @ k, da @ k.abs()),
+                            (dk, shared(ds.transpose(-1, -2) @ q), shared(da.transpose(-1, -2) @ q.abs()))):
+        ref.assert_within(got, want, 2.0 ** -8 * want.abs() + 2.0 ** -13 * most + 1e-30)
