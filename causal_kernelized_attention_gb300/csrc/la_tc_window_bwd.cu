@@ -23,7 +23,9 @@
 // A tile of sinks is seen by every later row.  Its rows are shared out over several CTAs,
 // each about a window tile's work; their fp32 sums go to scratch and a third, small kernel
 // adds them up in order (otherwise those few CTAs outlast all others: 864 us instead of
-// 150 at 8192 rows, window 1024).
+// 150 at 8192 rows, window 1024).  All tiles are shared out in the same way where the launch has
+// fewer CTAs than there are SMs (16 on 4 heads, d 128: 512 rows 34 -> 22 us, 1024 rows 61 -> 42;
+// 8 heads on one, 1500 rows 132 -> 37).
 //
 // Rows and keys of padding: their P and dS are 0, and what a product multiplies by them is
 // zeroed in shared memory (0 times a NaN is not 0).
@@ -356,7 +358,8 @@ __device__ __forceinline__ void dq_block(const Maps &maps, const Params &prm, co
 // ---------------------------------------------------------------- dk, dv
 constexpr int kRowStages = 5;
 
-// How the tiles of sinks are shared out: `tiles` of them per key head, `parts` CTAs each.
+// Which key tiles are shared out: the first `tiles` per key head, to `parts` CTAs each.  They are the
+// tiles of sinks, or all where the launch would leave SMs idle.
 struct Split {
     int tiles, parts;
 };
@@ -369,6 +372,10 @@ Split split_of(const WindowProblem &p)
     const long long total = (long long)p.B * p.Hk * ((tiles - sp.tiles) * win + sp.tiles * whole);
     const long long unit = std::max(win, total / (2 * sm_count()));
     if (sp.tiles > 0) sp.parts = (int)((whole + unit - 1) / unit);
+    // room for more CTAs, and shares of 4 query tiles (fewer than 12 are not worth the launch that adds up)
+    const long long ctas = (long long)p.B * p.Hk * tiles, dq = (long long)p.B * p.Hk * params_of(p).units;
+    const long long streamed = win * (p.Hq / p.Hk), more = std::min((sm_count() - dq) / std::max(ctas, 1LL), streamed / 4);
+    if (streamed >= 12 && more > 1 && sp.parts <= more) sp = {(int)tiles, (int)more};
     return sp;
 }
 size_t split_floats(const WindowProblem &p, const Split &sp, int DT)
@@ -376,7 +383,7 @@ size_t split_floats(const WindowProblem &p, const Split &sp, int DT)
     return sp.parts > 1 ? (size_t)p.B * p.Hk * sp.tiles * sp.parts * 2 * kRows * DT : 0;
 }
 
-// Adds up the shares of the tiles of sinks, in order: 4 features a thread.
+// Adds up the shares of the shared tiles, in order: 4 features a thread.
 template <int DT>
 __global__ void __launch_bounds__(256) window_tc_sum(const float *part, __nv_bfloat16 *dk, __nv_bfloat16 *dv, const Split sp,
                                                      int Nk, int d, float scale)
@@ -452,7 +459,7 @@ __device__ __forceinline__ void dkv_block(const Maps &maps, const Params &prm, c
 
     const int tiles = (prm.Nk + kRows - 1) / kRows, group = prm.Hq / prm.Hk, off = prm.Nk - prm.Nq;
     const int units = tiles + sp.tiles * (sp.parts - 1), bh = block / units, unit = block % units;
-    const bool shared = unit < sp.tiles * sp.parts && sp.parts > 1;  // a share of a tile of sinks
+    const bool shared = unit < sp.tiles * sp.parts && sp.parts > 1;  // a share of a tile
     const int j0 = (shared ? unit / sp.parts : unit - sp.tiles * (sp.parts - 1)) * kRows, b = bh / prm.Hk, hk = bh % prm.Hk;
     const int n = valid(prm.lens, b, prm.Nk);
     const QueryTiles qt(j0, min(j0 + kRows, prm.Nk) - 1, prm.window, prm.sinks, n, off, prm.Nq, kHalf);

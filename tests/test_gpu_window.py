@@ -93,6 +93,15 @@ def test_sinks_shared_out(d, B, Hq, Hk, Nq, Nk, window, sinks, lens):
     check("bf16", B, Hq, Hk, Nq, Nk, d, window, sinks, lens=lens, spoil=lens is not None)
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("B,Hq,Hk,Nq,Nk,window,sinks,lens", [
+    (1, 4, 1, 400, 400, 200, 0, None), (2, 8, 2, 300, 500, 1000, 3, [500, 130]), (1, 12, 1, 129, 700, 300, 500, None),
+    (2, 6, 1, 256, 256, 256, 130, [0, 200]), (1, 16, 1, 60, 1000, 700, 0, None)])
+def test_key_tiles_shared_out(d, B, Hq, Hk, Nq, Nk, window, sinks, lens):
+    """Few blocks, many query heads to a key head: every key tile's gradients are summed from several."""
+    check("bf16", B, Hq, Hk, Nq, Nk, d, window, sinks, lens=lens, spoil=lens is not None)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("H", [2, 80])
 def test_large_scores(dtype, H):
