@@ -38,6 +38,34 @@ bool disjoint(const Span (&out)[NO], const Span (&in)[NI])
     return true;
 }
 
+// What a call keeps from one of its kernels to the next.  The lock, held over its launches, keeps
+// two host threads that share a stream from mixing them on its one workspace (one of each
+// operator, `which`); a captured call takes memory of its own, so that two graphs may be replayed
+// at once.
+std::mutex g_launches;
+la_status call_scratch(cudaStream_t s, size_t bytes, int which, Scratch *own, void **base)
+{
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    la_status st = cuda_status(cudaStreamIsCapturing(s, &cs));
+    if (st != LA_OK) return st;
+    if (cs == cudaStreamCaptureStatusNone && data_workspace(s, bytes, base, which) == LA_OK) return LA_OK;
+    if ((st = own->alloc(bytes, s)) == LA_OK) *base = own->ptr;
+    return st;
+}
+
+la_status run_recurrence(RecurrenceProblem &p)
+{
+    const size_t bytes = recurrence_scratch(p);
+    if (bytes == 0) return recurrence(p);
+    std::lock_guard<std::mutex> lock(g_launches);
+    Scratch own;
+    void *base = nullptr;
+    const la_status st = call_scratch(p.stream, bytes, 2, &own, &base);
+    if (st != LA_OK) return st;
+    p.fold = static_cast<float *>(base);
+    return recurrence(p);
+}
+
 bool known(la_dtype t) { return t == LA_F32 || t == LA_BF16; }
 
 // ---------------------------------------------------------------- rotary
@@ -156,7 +184,7 @@ la_status la_recurrence_forward(const void *x, const float *alpha, const float *
     p.B = B; p.N = N; p.D = D;
     p.dtype = dtype;
     p.stream = (cudaStream_t)stream;
-    return recurrence(p);
+    return run_recurrence(p);
 }
 
 la_status la_recurrence_backward(const float *alpha, const void *h, const void *dh, const float *h0, const float *dhN,
@@ -180,7 +208,7 @@ la_status la_recurrence_backward(const float *alpha, const void *h, const void *
     p.backward = true;
     p.dtype = dtype;
     p.stream = (cudaStream_t)stream;
-    return recurrence(p);
+    return run_recurrence(p);
 }
 
 la_status la_recurrence_step(float *state, const void *x, const float *alpha, void *h, int B, int D, la_dtype dtype,
@@ -261,21 +289,12 @@ la_status la_window_backward(const void *q, const void *k, const void *v, const 
     p.scale = scale;
     p.dtype = dtype;
     p.stream = s;
-    // D = dO . o per row and partial sums, from one kernel to the next.  The lock keeps two host
-    // threads that share a stream from mixing their launches on its one workspace; a captured
-    // call takes memory of its own, so that two graphs may be replayed at once.
-    static std::mutex mu;
-    std::lock_guard<std::mutex> lock(mu);
-    Scratch scratch;
+    // D = dO . o per row and partial sums, from one kernel to the next
+    std::lock_guard<std::mutex> lock(g_launches);
+    Scratch own;
     void *base = nullptr;
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    if ((st = cuda_status(cudaStreamIsCapturing(s, &cs))) != LA_OK) return st;
-    const size_t bytes = dtype == LA_BF16 ? window_backward_tc_scratch(p) : window_backward_simt_scratch(p);
-    st = cs == cudaStreamCaptureStatusNone ? data_workspace(s, bytes, &base, 1) : LA_ERR_UNSUPPORTED;
-    if (st != LA_OK) {
-        if ((st = scratch.alloc(bytes, s)) != LA_OK) return st;
-        base = scratch.ptr;
-    }
+    st = call_scratch(s, dtype == LA_BF16 ? window_backward_tc_scratch(p) : window_backward_simt_scratch(p), 1, &own, &base);
+    if (st != LA_OK) return st;
     p.delta = static_cast<float *>(base);
     return dtype == LA_BF16 ? window_backward_tc(p) : window_backward_simt(p);
 }

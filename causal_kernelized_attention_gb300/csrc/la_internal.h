@@ -166,12 +166,14 @@ struct RecurrenceProblem {
     const float *alpha, *h0, *dhN;
     void *h, *dx;
     float *hN, *dalpha, *dh0;
+    float *fold;  // scratch of recurrence_scratch() bytes
     int B, N, D;
     bool backward;
     la_dtype dtype;
     cudaStream_t stream;
 };
 la_status recurrence(const RecurrenceProblem &p);
+size_t recurrence_scratch(const RecurrenceProblem &p);
 la_status recurrence_step(float *state, const void *x, const float *alpha, void *h, int B, int D, la_dtype dtype,
                           cudaStream_t stream);
 
@@ -235,8 +237,8 @@ la_status flag_workspace(cudaStream_t s, size_t bytes, void **out);
 // captured against it stays valid.  Returns LA_ERR_UNSUPPORTED when it cannot
 // serve the call (a stream under capture whose buffer is too small, or the
 // allocation failed); the caller then uses per-call scratch.  `which` tells a stream's
-// buffers apart: the window backward has one of its own (1), which its lock protects from
-// another host thread's launches on the same stream.
+// buffers apart: the window backward has one of its own (1), and so has the recurrence (2), which a
+// lock protects from another host thread's launches on the same stream.
 la_status data_workspace(cudaStream_t s, size_t bytes, void **out, int which = 0);
 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel and device,

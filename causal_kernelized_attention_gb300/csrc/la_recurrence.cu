@@ -23,9 +23,17 @@
 // Measured at 65536 x 4096, bf16: forward 326 us (6.6 TB/s), backward 540 us (7.0 TB/s); fp32
 // backward 852 us (6.3 TB/s).  4 x 2048 x 512 forward 7.2 us (4.6 TB/s, two steps of a cluster).
 //
+// Where the largest clusters leave half of the machine idle and a sequence is 32 tiles or longer, it
+// is split into segments instead, one CTA each: one launch finds every segment's (A, H), a
+// second joins those before its own and runs it.  That reads alpha and x twice but takes no step for
+// step exchange: 65536 x 64 forward 19 us instead of 102, 30000 x 33 backward 27 instead of 161, 16384 x
+// 512 forward 18 instead of 28; 4096 x 64 forward 7.6 instead of 8.5, below that the launch costs more
+// than it saves (2048 x 64: 7.2 instead of 5.6).
+//
 // Rows of whole 16-byte vectors come in by TMA, kStages tiles of 128 tokens x 64 channels deep,
 // so that the bytes in flight depend neither on registers nor on occupancy; other widths by
 // plain loads, one channel a lane.
+#include <algorithm>
 #include <type_traits>
 
 #include "la_common.cuh"
@@ -79,25 +87,26 @@ struct Args {
     T *out;              // forward: h; backward: dx
     float *dalpha;       // backward
     float *last;         // forward: hN; backward: dh0; may be null
-    int N, D, steps;
+    float *fold;         // [units][segs][A, H][kCh] where segs > 1
+    int N, D, steps, segs;
 };
 
-template <typename T, bool kBack, bool kDeep>
+template <typename T, bool kH, bool kDeep>
 struct Tiles {  // the TMA ring
-    static constexpr int kBytes = kTok * 64 * (4 + (kBack ? 2 : 1) * (int)sizeof(T));
+    static constexpr int kBytes = kTok * 64 * (4 + (kH ? 2 : 1) * (int)sizeof(T));
     static constexpr int kStages = (kDeep ? 196 : 100) * 1024 / kBytes;
     float alpha[kStages][kTok][64];
     T x[kStages][kTok][64];
-    T h[kBack ? kStages : 1][kBack ? kTok : 1][64];
+    T h[kH ? kStages : 1][kH ? kTok : 1][64];
 };
 struct NoTiles {
     static constexpr int kStages = 1;
 };
 
-template <typename T, bool kBack, bool kTma, bool kDeep>
+template <typename T, bool kH, bool kTma, bool kDeep>
 struct Smem {
     static constexpr int kPer = kTma ? 2 : 1, kCh = 32 * kPer;  // channels of a lane, of a CTA
-    typedef typename std::conditional<kTma, Tiles<T, kBack, kDeep>, NoTiles>::type Ring;
+    typedef typename std::conditional<kTma, Tiles<T, kH, kDeep>, NoTiles>::type Ring;
     Ring t;
     alignas(16) float wA[2][kWarps][kCh];  // the warps' runs, by step parity
     float wH[2][kWarps][kCh];
@@ -106,20 +115,26 @@ struct Smem {
     int abort;
 };
 
-template <typename T, bool kBack, bool kTma, bool kDeep>
+// kWhole: a cluster has a whole sequence.  The other two split it into a.segs segments.
+enum Mode { kWhole, kFolds, kSegment };
+
+template <typename T, bool kBack, bool kTma, bool kDeep, Mode kMode>
 __global__ void __launch_bounds__(kThreads)
 recurrence_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
                   const __grid_constant__ CUtensorMap map_h, const __grid_constant__ Args<T> a)
 {
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    typedef Smem<T, kBack, kTma, kDeep> S_;
+    constexpr bool kFold = kMode == kFolds, kH = kBack && !kFold;
+    typedef Smem<T, kH, kTma, kDeep> S_;
     S_ &sm = *reinterpret_cast<S_ *>(smem_raw);
     constexpr int kPer = S_::kPer, kCh = S_::kCh, kStages = S_::Ring::kStages;
     typedef Vec<float, kPer> F;
-    constexpr uint32_t kBytes = kTok * kCh * (4 + (kBack ? 2 : 1) * sizeof(T));
+    constexpr uint32_t kBytes = kTok * kCh * (4 + (kH ? 2 : 1) * sizeof(T));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lc = kPer * lane;
     const uint32_t S = cluster_size(), rank = S > 1 ? cluster_ctarank() : 0;
-    const int groups = (a.D + kCh - 1) / kCh, unit = (int)(blockIdx.x / S);
+    const int groups = (a.D + kCh - 1) / kCh, segs = kMode == kWhole ? 1 : a.segs, at_seg = (int)(blockIdx.x / S);
+    const int unit = at_seg / segs, seg = kMode == kWhole ? 0 : at_seg % segs;
+    if (kFold && seg == segs - 1) return;  // (no segment is after the last)
     const int b = unit / groups, c0 = (unit % groups) * kCh, ch = c0 + lc;
     const bool live = ch < a.D;  // (D is even where a lane has two channels)
 
@@ -136,7 +151,7 @@ recurrence_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 
     // scan index of this CTA's first token of a step; token t = i (forward), N - 1 - i (backward):
     // the backward's tiles lie in memory order, and are read from their last row
-    auto first_of = [&](int step) { return ((long long)step * S + rank) * kTok; };
+    auto first_of = [&](int step) { return (((long long)seg * a.steps + step) * S + rank) * kTok; };
     auto fetch = [&](int step) {
         if constexpr (kTma) {
             const long long i0 = first_of(step);
@@ -145,7 +160,7 @@ recurrence_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             mbar_arrive_expect_tx(&sm.full[s], kBytes);
             tma_load_3d(sm.t.alpha[s], &map_a, &sm.full[s], c0, kBack ? t0 + 1 : t0, b);
             tma_load_3d(sm.t.x[s], &map_x, &sm.full[s], c0, t0, b);
-            if (kBack) tma_load_3d(sm.t.h[s], &map_h, &sm.full[s], c0, t0 - 1, b);
+            if (kH) tma_load_3d(sm.t.h[s], &map_h, &sm.full[s], c0, t0 - 1, b);
         }
     };
     if (kTma && tid == 0)
@@ -155,8 +170,20 @@ recurrence_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
     for (int v = 0; v < kPer; ++v) carry.x[v] = h0.x[v] = 0.f;
     const size_t base = (size_t)b * a.N * a.D + ch, at_b = (size_t)b * a.D + ch;
-    if (live && (kBack ? a.dhN : a.h0)) carry = ld<float, kPer>((kBack ? a.dhN : a.h0) + at_b);
-    if (kBack && live && a.h0) h0 = ld<float, kPer>(a.h0 + at_b);
+    F whole;  // the gates' product over this segment
+#pragma unroll
+    for (int v = 0; v < kPer; ++v) whole.x[v] = 1.f;
+    float *const fold = a.fold + (size_t)unit * segs * 2 * kCh + lc;
+    if (!kFold && live && (kBack ? a.dhN : a.h0)) carry = ld<float, kPer>((kBack ? a.dhN : a.h0) + at_b);
+    if (kMode == kSegment && live) {
+#pragma unroll 8
+        for (int i = 0; i < seg; ++i) {
+            const F xa = ld<float, kPer>(fold + i * 2 * kCh), xh = ld<float, kPer>(fold + (i * 2 + 1) * kCh);
+#pragma unroll
+            for (int v = 0; v < kPer; ++v) carry.x[v] = fmaf(xa.x[v], carry.x[v], xh.x[v]);
+        }
+    }
+    if (kH && live && a.h0) h0 = ld<float, kPer>(a.h0 + at_b);
 
     bool ok = true;
     for (int step = 0; step < a.steps; ++step) {
@@ -173,7 +200,7 @@ recurrence_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     const int k = warp * kRun + r, row = kBack ? kTok - 1 - k : k;
                     al[r] = ld<float, kPer>(&sm.t.alpha[s][row][lc]);
                     xv[r] = ldf<T, kPer>(&sm.t.x[s][row][lc]);
-                    if (kBack) hv[r] = ldf<T, kPer>(&sm.t.h[s][row][lc]);
+                    if (kH) hv[r] = ldf<T, kPer>(&sm.t.h[s][row][lc]);
                 }
             }
         } else {
@@ -185,7 +212,7 @@ recurrence_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                     const size_t o = base + (size_t)t * a.D;
                     if (!kBack || i0 + k > 0) al[r] = ld<float, kPer>(a.alpha + o + (kBack ? a.D : 0));
                     xv[r] = ldf<T, kPer>(a.x + o);
-                    if (kBack && t > 0) hv[r] = ldf<T, kPer>(a.h_in + o - a.D);
+                    if (kH && t > 0) hv[r] = ldf<T, kPer>(a.h_in + o - a.D);
                 }
             }
         }
@@ -266,29 +293,40 @@ recurrence_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
             for (int v = 0; v < kPer; ++v) carry.x[v] = fmaf(tA.x[v], carry.x[v], tH.x[v]);
         }
-        F c;
+        if constexpr (kFold) {
 #pragma unroll
-        for (int v = 0; v < kPer; ++v) c.x[v] = fmaf(pA.x[v], at.x[v], pH.x[v]);
+            for (int v = 0; v < kPer; ++v) whole.x[v] *= tA.x[v];
+        } else {
+            F c;
 #pragma unroll
-        for (int r = 0; r < kRun; ++r) {
-            const int k = warp * kRun + r;
+            for (int v = 0; v < kPer; ++v) c.x[v] = fmaf(pA.x[v], at.x[v], pH.x[v]);
 #pragma unroll
-            for (int v = 0; v < kPer; ++v) c.x[v] = fmaf(al[r].x[v], c.x[v], xv[r].x[v]);
-            if (k < left && live) {
-                const long long t = kBack ? a.N - 1 - (i0 + k) : i0 + k;
-                const size_t o = base + (size_t)t * a.D;
-                stf<T, kPer>(a.out + o, c);
-                if (kBack) {
-                    F da;
+            for (int r = 0; r < kRun; ++r) {
+                const int k = warp * kRun + r;
 #pragma unroll
-                    for (int v = 0; v < kPer; ++v) da.x[v] = c.x[v] * (t == 0 ? h0.x[v] : hv[r].x[v]);
-                    st<float, kPer>(a.dalpha + o, da);
+                for (int v = 0; v < kPer; ++v) c.x[v] = fmaf(al[r].x[v], c.x[v], xv[r].x[v]);
+                if (k < left && live) {
+                    const long long t = kBack ? a.N - 1 - (i0 + k) : i0 + k;
+                    const size_t o = base + (size_t)t * a.D;
+                    stf<T, kPer>(a.out + o, c);
+                    if (kBack) {
+                        F da;
+#pragma unroll
+                        for (int v = 0; v < kPer; ++v) da.x[v] = c.x[v] * (t == 0 ? h0.x[v] : hv[r].x[v]);
+                        st<float, kPer>(a.dalpha + o, da);
+                    }
                 }
             }
         }
     }
+    if constexpr (kFold) {
+        if (warp == 0 && live) {
+            st<float, kPer>(fold + seg * 2 * kCh, whole);
+            st<float, kPer>(fold + (seg * 2 + 1) * kCh, carry);
+        }
+    }
     // the state after the last token (forward), or alpha_0 g_0 (backward)
-    if (a.last && rank == 0 && warp == 0 && live) {
+    if (!kFold && a.last && seg == segs - 1 && rank == 0 && warp == 0 && live) {
         if (kBack && a.N > 0) {
             const F f = ld<float, kPer>(a.alpha + base);
 #pragma unroll
@@ -321,42 +359,22 @@ la_status tile_map(CUtensorMap *m, const void *ptr, bool f32, int B, int N, int 
     return r == CUDA_SUCCESS ? LA_OK : cuda_status(cudaErrorInvalidValue);
 }
 
-template <typename T, bool kBack, bool kTma, bool kDeep = false>
-la_status launch(const RecurrenceProblem &p)
+template <typename T, bool kBack, bool kTma, bool kDeep, Mode kMode>
+la_status launch(const RecurrenceProblem &p, const Args<T> &a, long long units, int S)
 {
-    auto kern = recurrence_kernel<T, kBack, kTma, kDeep>;
-    constexpr size_t smem = sizeof(Smem<T, kBack, kTma, kDeep>);
-    constexpr bool f32 = sizeof(T) == 4;
-    const long long units = (long long)p.B * ceil_div(p.D, Smem<T, kBack, kTma, kDeep>::kCh);
-    const long long tiles = ((long long)p.N + kTok - 1) / kTok;
-    // CTAs a sequence and group of channels: as many as run at once (two an SM where shared
-    // memory allows), none without a tile of its own.
-    constexpr int resident = smem <= 113 * 1024 ? 2 : 1;
-    int S = 1;
-    while (S < kMaxCluster && S < tiles && units * S * 2 <= (long long)resident * tc::sm_count()) S *= 2;
-    if (units * S > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
-    Args<T> a;
-    a.x = static_cast<const T *>(kBack ? p.dh : p.x);
-    a.alpha = p.alpha;
-    a.h_in = static_cast<const T *>(p.h_in);
-    a.h0 = p.h0;
-    a.dhN = p.dhN;
-    a.out = static_cast<T *>(kBack ? p.dx : p.h);
-    a.dalpha = p.dalpha;
-    a.last = kBack ? p.dh0 : p.hN;
-    a.N = p.N;
-    a.D = p.D;
-    a.steps = (int)((tiles + S - 1) / S);
+    auto kern = recurrence_kernel<T, kBack, kTma, kDeep, kMode>;
+    constexpr bool kH = kBack && kMode != kFolds;
+    constexpr size_t smem = sizeof(Smem<T, kH, kTma, kDeep>);
     CUtensorMap ma{}, mx{}, mh{};
     la_status st = ensure_smem((const void *)kern, (int)smem);
     if (kTma) {
         if (st == LA_OK) st = tile_map(&ma, p.alpha, true, p.B, p.N, p.D);
-        if (st == LA_OK) st = tile_map(&mx, a.x, f32, p.B, p.N, p.D);
-        if (st == LA_OK && kBack) st = tile_map(&mh, p.h_in, f32, p.B, p.N, p.D);
+        if (st == LA_OK) st = tile_map(&mx, a.x, sizeof(T) == 4, p.B, p.N, p.D);
+        if (st == LA_OK && kH) st = tile_map(&mh, p.h_in, sizeof(T) == 4, p.B, p.N, p.D);
     }
     if (st != LA_OK) return st;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)(units * S));
+    lc.gridDim = dim3((unsigned)(units * a.segs * S));
     lc.blockDim = dim3(kThreads);
     lc.dynamicSmemBytes = smem;
     lc.stream = p.stream;
@@ -370,19 +388,64 @@ la_status launch(const RecurrenceProblem &p)
     return cuda_status(cudaLaunchKernelEx(&lc, kern, ma, mx, mh, a));
 }
 
+// Runs the problem, or with `bytes` only finds the scratch that it needs.
+template <typename T, bool kBack, bool kTma, bool kDeep = false>
+la_status run(const RecurrenceProblem &p, size_t *bytes)
+{
+    typedef Smem<T, kBack, kTma, kDeep> S_;
+    const long long units = (long long)p.B * ceil_div(p.D, S_::kCh);
+    const long long tiles = ((long long)p.N + kTok - 1) / kTok;
+    // CTAs a sequence and group of channels: as many as run at once (two an SM where shared
+    // memory allows), none without a tile of its own.
+    constexpr int resident = sizeof(S_) <= 113 * 1024 ? 2 : 1;
+    const long long room = (long long)resident * tc::sm_count() / units;
+    int S = 1;
+    while (S < kMaxCluster && S < tiles && S * 2 <= room) S *= 2;
+    if (units * S > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
+    Args<T> a;
+    a.segs = 1;
+    if (!kDeep && room >= 2 * kMaxCluster && tiles >= 4 * kMaxCluster) {  // segments (see above)
+        a.segs = (int)std::min(room, tiles);
+        S = 1;
+    }
+    a.steps = (int)((tiles + a.segs * S - 1) / (a.segs * S));
+    if (a.segs > 1) a.segs = (int)((tiles + a.steps - 1) / a.steps);  // none without a tile
+    if (bytes) {
+        *bytes = a.segs > 1 ? (size_t)units * a.segs * 2 * S_::kCh * sizeof(float) : 0;
+        return LA_OK;
+    }
+    a.x = static_cast<const T *>(kBack ? p.dh : p.x);
+    a.alpha = p.alpha;
+    a.h_in = static_cast<const T *>(p.h_in);
+    a.h0 = p.h0;
+    a.dhN = p.dhN;
+    a.out = static_cast<T *>(kBack ? p.dx : p.h);
+    a.dalpha = p.dalpha;
+    a.last = kBack ? p.dh0 : p.hN;
+    a.fold = p.fold;
+    a.N = p.N;
+    a.D = p.D;
+    if constexpr (!kDeep)
+        if (a.segs > 1) {
+            const la_status st = launch<T, kBack, kTma, false, kFolds>(p, a, units, 1);
+            return st == LA_OK ? launch<T, kBack, kTma, false, kSegment>(p, a, units, 1) : st;
+        }
+    return launch<T, kBack, kTma, kDeep, kWhole>(p, a, units, S);
+}
+
 template <typename T, bool kBack>
-la_status pick(const RecurrenceProblem &p)
+la_status pick(const RecurrenceProblem &p, size_t *bytes)
 {
     // TMA wants rows of whole 16-byte vectors, and a sequence to describe
-    if (p.D % (int)(16 / sizeof(T)) != 0 || p.N == 0) return launch<T, kBack, false>(p);
+    if (p.D % (int)(16 / sizeof(T)) != 0 || p.N == 0) return run<T, kBack, false>(p, bytes);
     // The bf16 backward's tile is 64 KB.  Where clusters of at most two fill the machine, one
     // CTA an SM with three tiles in its ring measures 538 us at 65536 x 4096 (7.0 TB/s), two
     // CTAs with one tile each 630; with larger clusters, which then need whole groups of free
     // SMs, it is 289 against 203 us (65536 x 1024).  The other forms' tiles fit twice in 100 KB
     // (or are within 2% either way).
     if (kBack && sizeof(T) == 2 && (long long)p.B * ceil_div(p.D, 64) * 4 > tc::sm_count())
-        return launch<T, kBack, true, (kBack && sizeof(T) == 2)>(p);
-    return launch<T, kBack, true>(p);
+        return run<T, kBack, true, (kBack && sizeof(T) == 2)>(p, bytes);
+    return run<T, kBack, true>(p, bytes);
 }
 
 // ---------------------------------------------------------------- one token
@@ -420,11 +483,17 @@ la_status step(float *state, const void *x, const float *alpha, void *h, long lo
 
 }  // namespace
 
-la_status recurrence(const RecurrenceProblem &p)
+static la_status any(const RecurrenceProblem &p, size_t *bytes)
 {
-    if (p.dtype == LA_BF16) return p.backward ? pick<__nv_bfloat16, true>(p) : pick<__nv_bfloat16, false>(p);
-    return p.backward ? pick<float, true>(p) : pick<float, false>(p);
+    if (p.dtype == LA_BF16) return p.backward ? pick<__nv_bfloat16, true>(p, bytes) : pick<__nv_bfloat16, false>(p, bytes);
+    return p.backward ? pick<float, true>(p, bytes) : pick<float, false>(p, bytes);
 }
+size_t recurrence_scratch(const RecurrenceProblem &p)
+{
+    size_t bytes = 0;
+    return any(p, &bytes) == LA_OK ? bytes : 0;
+}
+la_status recurrence(const RecurrenceProblem &p) { return any(p, nullptr); }
 
 la_status recurrence_read_status(cudaStream_t s, unsigned *bits)
 {

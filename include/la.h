@@ -510,7 +510,9 @@ la_status la_rotary_backward(const void *doq, const void *dok, void *dq, void *d
  *   state = alpha state + x, h = state; x, alpha, h : [B, D].
  *
  * Outputs overlap no input and no other output.  B = 0 or D = 0 is an empty problem; N = 0
- * still writes hN (dh0 = dhN).
+ * still writes hN (dh0 = dhN).  Long sequences of few channels keep (A, H) of their segments
+ * (at most 256 KB) in scratch of the stream's workspace, or stream-ordered while the stream is being
+ * captured.
  */
 la_status la_recurrence_forward(const void *x, const float *alpha, const float *h0, void *h, float *hN, int B, int N,
                                 int D, la_dtype dtype, la_stream_t stream);

@@ -169,3 +169,42 @@ def test_streams_and_graphs():
     torch.cuda.synchronize()
     want, _ = la().la_recurrence_forward(x, a)
     assert torch.equal(h, want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,N,D", [(1, 4096, 64), (1, 4097, 17), (3, 5001, 66), (2, 6000, 130), (9, 4480, 8)])
+def test_segments(dtype, B, N, D):
+    """Long sequences of few channels, split over the machine in segments: whole tiles and not, with first
+    and last states."""
+    test_forward_backward(dtype, True, B, N, D)
+
+
+def test_segments_in_graphs_on_two_streams():
+    """Two captured graphs replayed at once on new data, and eager calls on one stream between them."""
+    B, N, D = 1, 20000, 64
+    make = lambda s: [ref.draw(s, (B, N, D), torch.bfloat16).cuda(), gates(s + 1, (B, N, D)).cuda(),  # noqa: E731
+                      ref.draw(s + 2, (B, N, D), torch.bfloat16).cuda()]
+    call = lambda x, a, dh: (*la().la_recurrence_forward(x, a),  # noqa: E731
+                             *la().la_recurrence_backward(a, x, dh, dhN=None)[:2])
+    sets, graphs, outs = [make(10), make(20)], [], []
+    for s in sets:
+        call(*s)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(*s))
+        graphs.append(g)
+    for s, n in zip(sets, (make(30), make(40))):
+        for a, b in zip(s, n):
+            a.copy_(b)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = [call(*s) for s in sets]
+    torch.cuda.synchronize()
+    for got, want in zip(outs, eager):
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    assert la().la_get_device_status() == 0
