@@ -208,3 +208,22 @@ def test_segments_in_graphs_on_two_streams():
         for a, b in zip(got, want):
             assert torch.equal(a, b)
     assert la().la_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("initial", [False, True])
+@pytest.mark.parametrize("B,N,D", [
+    (2, 3900, 64), (2, 3899, 65), (1, 3001, 2048), (1, 9003, 1280), (1, 2900, 1281), (1, 1500, 3848)])
+def test_whole_sequences_over_cluster_steps(dtype, initial, B, N, D):
+    """Clusters of CTAs that take a sequence in three steps and more, by TMA and by plain loads: fewer tiles
+    than segments want (64, 65 channels), or channels enough to fill half of the machine (the others;
+    9003 tokens pass 9 steps)."""
+    test_forward_backward(dtype, initial, B, N, D)
+
+
+@pytest.mark.parametrize("initial", [False, True])
+@pytest.mark.parametrize("B,N,D", [(1, 2000, 2560), (1, 2001, 2600), (1, 1100, 4096), (2, 1001, 2568), (3, 777, 4096)])
+def test_many_channels_turn_the_ring(initial, B, N, D):
+    """Full-width training in bf16: the backward's three-stage ring of tiles goes round several times, in
+    clusters of two CTAs (one entry) and of one."""
+    test_forward_backward("bf16", initial, B, N, D)
