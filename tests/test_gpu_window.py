@@ -460,3 +460,20 @@ def test_short_gradients_are_rounded_once(B, Hq, Hk, Nq, Nk, d, window, sinks):
     for got, want, most in ((dq, ds @ k, da @ k.abs()),
                             (dk, shared(ds.transpose(-1, -2) @ q), shared(da.transpose(-1, -2) @ q.abs()))):
         ref.assert_within(got, want, 2.0 ** -8 * want.abs() + 2.0 ** -13 * most + 1e-30)
+
+
+@pytest.mark.parametrize("B,Hq,Hk,Nq,Nk,window,sinks,lens", [
+    (1, 2, 2, 900, 900, 700, 0, None), (1, 3, 1, 1300, 1300, 700, 3, None), (2, 2, 2, 1100, 1500, 5, 650, None),
+    (1, 1, 1, 1281, 1281, 1000000, 0, None), (1, 6, 2, 385, 1400, 800, 5, None), (1, 1, 1, 1, 900, 900, 0, None),
+    (3, 2, 2, 900, 900, 700, 0, [0, 130, 900]), (2, 3, 1, 1000, 1200, 5, 650, [1200, 777]),
+    (2, 4, 2, 1100, 1100, 700, 5, [1100, 300])])
+def test_wide_windows_of_wide_heads(B, Hq, Hk, Nq, Nk, window, sinks, lens):
+    """Two query tiles a block: neighbouring rows of one head (odd groups) with different key ranges, odd
+    numbers of row tiles, the same rows of two heads (even groups), padding."""
+    check("bf16", B, Hq, Hk, Nq, Nk, 128, window, sinks, lens=lens, spoil=lens is not None)
+
+
+@pytest.mark.parametrize("Hq,Hk,window", [(2, 1, 77), (2, 1, 700), (1, 1, 700), (3, 1, 1000)])
+def test_large_scores_of_wide_heads(Hq, Hk, window):
+    """Scores of hundreds at d 128: the output is rescaled as the maxima grow, in both forms."""
+    check("bf16", 1, Hq, Hk, 900, 900, 128, window, 2, scale=0.6, big=4.0)
