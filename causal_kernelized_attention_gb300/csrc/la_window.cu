@@ -145,6 +145,9 @@ __device__ __forceinline__ float sum16(float v)
 struct Split {
     int sinks, sink_parts, parts, tiles;
     __host__ __device__ int units() const { return sinks * sink_parts + (tiles - sinks) * parts; }
+    // the tiles of several shares, which come first, and those shares
+    __host__ __device__ int shared_tiles() const { return parts > 1 ? tiles : sink_parts > 1 ? sinks : 0; }
+    __host__ __device__ int shared_units() const { return parts > 1 ? units() : sink_parts > 1 ? sinks * sink_parts : 0; }
 };
 
 struct Args {
@@ -156,9 +159,9 @@ struct Args {
     float scale;
     Split sp;     // dk, dv
     unsigned dkv_blocks;
-    float *part;  // [B Hk][units][dk, dv][64][D], of the tiles with several shares
-    int *left;    // [B Hk][tiles] shares left so far, zeroed by the delta kernel
-    int shared;   // B Hk tiles, or 0 where no tile has several shares
+    float *part;  // [B Hk][shared units][dk, dv][64][D]
+    int *left;    // [B Hk][shared tiles] shares left so far, zeroed by the delta kernel
+    int shared;   // B Hk shared tiles
 };
 
 // ---------------------------------------------------------------- forward
@@ -414,7 +417,7 @@ __device__ __forceinline__ void dkv_block(const Args &a, const unsigned block, f
         mul_nn<D>(dk, dst, q, ty, tx);
     }
     if (parts > 1) {
-        float *dst = a.part + ((size_t)bh * units + unit) * 2 * kT * D;
+        float *dst = a.part + ((size_t)bh * a.sp.shared_units() + unit) * 2 * kT * D;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -427,11 +430,11 @@ __device__ __forceinline__ void dkv_block(const Args &a, const unsigned block, f
         __shared__ int last;
         __threadfence();
         __syncthreads();
-        if (threadIdx.x == 0) last = atomicAdd(a.left + (size_t)bh * a.sp.tiles + j0 / kT, 1) == parts - 1;
+        if (threadIdx.x == 0) last = atomicAdd(a.left + (size_t)bh * a.sp.shared_tiles() + j0 / kT, 1) == parts - 1;
         __syncthreads();
         if (!last) return;
         __threadfence();
-        const float *src = a.part + ((size_t)bh * units + unit - share) * 2 * kT * D;
+        const float *src = a.part + ((size_t)bh * a.sp.shared_units() + unit - share) * 2 * kT * D;
         for (int e = threadIdx.x; e < 2 * kT * (D / 4); e += kThreads) {
             const int c = e % (D / 4) * 4, r = e / (D / 4) % kT, which = e / (D / 4) / kT;
             if (j0 + r >= a.Nk) continue;
@@ -522,8 +525,7 @@ Split split_of(const WindowProblem &p)
 
 size_t part_floats(const WindowProblem &p, const Split &sp)
 {
-    const bool shared = sp.parts > 1 || (sp.sinks > 0 && sp.sink_parts > 1);
-    return shared ? (size_t)p.B * p.Hk * sp.units() * 2 * kT * p.d : 0;
+    return (size_t)p.B * p.Hk * sp.shared_units() * 2 * kT * p.d;
 }
 
 template <int D>
@@ -537,7 +539,7 @@ la_status backward(const WindowProblem &p)
     const long long dkv = (long long)p.B * p.Hk * a.sp.units(), dq = (long long)p.B * p.Hq * ceil_div(p.Nq, kT);
     if (dkv > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
     a.dkv_blocks = (unsigned)dkv;
-    a.shared = part_floats(p, a.sp) ? p.B * p.Hk * a.sp.tiles : 0;  // no more than dkv
+    a.shared = p.B * p.Hk * a.sp.shared_tiles();  // no more than dkv
     const long long rows = (long long)p.B * p.Hq * p.Nq;
     la_status st = launch(window_delta_kernel<D>, (rows * (D / 4) + kThreads - 1) / kThreads, 0, a, p.stream);
     if (st != LA_OK) return st;
@@ -555,8 +557,7 @@ la_status window_forward_simt(const WindowProblem &p)
 size_t window_backward_simt_scratch(const WindowProblem &p)
 {
     const Split sp = split_of(p);
-    const size_t part = part_floats(p, sp);
-    return delta_bytes(p) + part * sizeof(float) + (part ? (size_t)p.B * p.Hk * sp.tiles * sizeof(int) : 0);
+    return delta_bytes(p) + part_floats(p, sp) * sizeof(float) + (size_t)p.B * p.Hk * sp.shared_tiles() * sizeof(int);
 }
 
 la_status window_backward_simt(const WindowProblem &p)

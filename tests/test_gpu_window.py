@@ -477,3 +477,25 @@ def test_wide_windows_of_wide_heads(B, Hq, Hk, Nq, Nk, window, sinks, lens):
 def test_large_scores_of_wide_heads(Hq, Hk, window):
     """Scores of hundreds at d 128: the output is rescaled as the maxima grow, in both forms."""
     check("bf16", 1, Hq, Hk, 900, 900, 128, window, 2, scale=0.6, big=4.0)
+
+
+@pytest.mark.parametrize("Hq,window,sinks,lens", [(5, 64, 70, None), (10, 20, 1, [2100, 900]), (5, 300, 64, [0, 2000])])
+def test_only_the_sinks_shared_out_in_fp32(Hq, window, sinks, lens):
+    """Blocks enough for the machine: of the key tiles only the sinks' are summed from several."""
+    check("f32", 2, Hq, 5, 2100, 2100, 32, window, sinks, lens=lens, spoil=lens is not None)
+
+
+def test_backward_scratch_is_for_shared_tiles():
+    """A tile of sinks adds its own shares to a backward's scratch, not one for every other key tile: 26
+    shares of 64 KB a head and the row sums are 14 MB, the gradients of k and v 67 MB."""
+    H, N, d = 8, 8192, 128
+    q, k, v, go = (ref.draw(i, (1, H, N, d), torch.float32).cuda() for i in range(1, 5))
+    o, lse = la().la_window_forward(q, k, v, 256, sinks=1)
+    grads = la().la_window_backward(q, k, v, o, lse, go, 256, sinks=1)  # loads the kernels
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    la().la_window_backward(q, k, v, o, lse, go, 256, sinks=1, dq=grads[0], dk=grads[1], dv=grads[2], stream=s)
+    s.synchronize()
+    assert before - torch.cuda.mem_get_info()[0] <= 24 * 2 ** 20
