@@ -116,6 +116,13 @@ struct Work {
     {
         return KeyTiles(t0 + off, t0 < p.Nq ? min(t0 + kRows, p.Nq) - 1 + off : t0 + off - 1, p.window, p.sinks, n, KT);
     }
+    // The first tile's first row, of unit u of an (entry, key head).
+    __device__ __forceinline__ static int first_row(const Params &p, int u)
+    {
+        const int group = p.Hq / p.Hk, tiles = (p.Nq + kRows - 1) / kRows;
+        if (p.pairs == 2) return u / group * kRows;
+        return p.pairs ? u / (group / 2) * kRows : u % ((tiles + 1) / 2) * 2 * kRows;
+    }
     __device__ __forceinline__ Work(const Params &p, int cta)
         : b(cta / p.units / p.Hk), hk(cta / p.units % p.Hk), n(valid(p.lens, b, p.Nk)), off(p.Nk - p.Nq),
           kt{{0, -1, 1, 0, 0, KT}, {0, -1, 1, 0, 0, KT}}
@@ -123,17 +130,17 @@ struct Work {
         const int u = cta % p.units, group = p.Hq / p.Hk, tiles = (p.Nq + kRows - 1) / kRows;
         if (p.pairs == 2) {  // one query tile: unit = (row tile, head), heads of one row tile together
             h[0] = h[1] = hk * group + u % group;
-            t0[0] = u / group * kRows;
+            t0[0] = first_row(p, u);
             t0[1] = p.Nq;
         } else if (p.pairs) {  // unit = (row tile, head pair), pairs of one row tile together
             const int hp = u % (group / 2);
             h[0] = hk * group + 2 * hp;
             h[1] = h[0] + 1;
-            t0[0] = t0[1] = u / (group / 2) * kRows;
+            t0[0] = t0[1] = first_row(p, u);
         } else {
             const int duos = (tiles + 1) / 2;
             h[0] = h[1] = hk * group + u / duos;
-            t0[0] = u % duos * 2 * kRows;
+            t0[0] = first_row(p, u);
             t0[1] = t0[0] + kRows;
         }
         kt[0] = keys(p, t0[0], n, off);

@@ -12,24 +12,26 @@
 // columns it was computed from, so nothing of the score matrices reaches shared memory.
 // Two groups of four warps work in turn, as in the forward: while one forms P and dS of its
 // tile (a thread a row), the tensor core runs the products of the other's.  In dk, dv a
-// thread owns a key, for which the visible queries are one interval.  The rounding of dS
-// (2^-8 relative at most, like P's) is the size of the gradients' own; sums are fp32.  Up to
-// 128 query rows, where a sum may have one or two large terms and their rounding would stand
-// out beside the gradients' own (up to 2.5 times it), dS is multiplied as two bf16 parts: 15.2 us instead
-// of 14.0 at 128 rows, 16 heads, d 128, where latency counts; for all sizes it would cost
-// 277 us instead of 243 at 8192, where the error is 1.4 times the gradients' own rounding for
-// any draw of the terms.
+// thread owns a key, for which the visible queries are one interval.  Sums are fp32.
+//
+// The rounding of P and dS (2^-8 relative at most, each on its own) averages out in a long sum, where the
+// gradients' error is about 1.4 times that of their own rounding, but not in a short one: of a row that sees two keys
+// the two dS are each other's negatives, and all of dq is off by what they are.  A block whose shortest sum (a
+// row's visible keys, a key's query rows) has at most 256 terms therefore multiplies P and dS as two
+// bf16 parts each (2^-16): 16 heads on 4, d 128, 128 rows 16.2 us (14.0 with one part), 8192 rows of window 128 98 us (91);
+// long sums would pay more for it (8192 rows, window 1024: 277 us instead of 244) and have less need.
 //
 // A tile of sinks is seen by every later row.  Its rows are shared out over several CTAs,
 // each about a window tile's work; their fp32 sums go to scratch and a third, small kernel
 // adds them up in order (otherwise those few CTAs outlast all others: 864 us instead of
 // 150 at 8192 rows, window 1024).  All tiles are shared out in the same way where the launch has
-// fewer CTAs than there are SMs (16 on 4 heads, d 128: 512 rows 34 -> 22 us, 1024 rows 61 -> 42;
+// fewer CTAs than there are SMs (16 on 4 heads, d 128: 512 rows 34 -> 24 us, 1024 rows 61 -> 42;
 // 8 heads on one, 1500 rows 132 -> 37).
 //
 // Rows and keys of padding: their P and dS are 0, and what a product multiplies by them is
 // zeroed in shared memory (0 times a NaN is not 0).
 #include <algorithm>
+#include <type_traits>
 
 #include "la_tc_window.cuh"
 
@@ -46,14 +48,15 @@ constexpr int kThreads = 320;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kHalfBox = kHalf * 128;  // one [64 rows x 64 bf16] swizzled box: 8 KB
 constexpr uint32_t tS = 0, tP = 128, tG = 256;  // S_s at 64 s, dP_s at 128 + 64 s, gradients from 256
-// dS lies over the 32 columns that each half of it came from: 16 columns of bf16 pairs, then 16 of
+constexpr int kFewTerms = 256;  // of a sum, up to which P and dS are multiplied as two parts
+// P and dS lie over the 32 columns that each half of them came from: 16 columns of bf16 pairs, then 16 of
 // what their rounding left (where that is multiplied too).
 constexpr uint32_t kRest = 16;
-__device__ __forceinline__ constexpr uint32_t ds_at(int kk) { return (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8); }
+__device__ __forceinline__ constexpr uint32_t half_at(int kk) { return (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8); }
 
 // Rounds a half's 32 values to bf16 at TMEM address t, and with kFine the rest behind them.
 template <bool kFine>
-__device__ __forceinline__ void store_ds(uint32_t t, const uint32_t (&x)[32])
+__device__ __forceinline__ void store_half(uint32_t t, const uint32_t (&x)[32])
 {
     uint32_t pk[16];
 #pragma unroll
@@ -132,6 +135,14 @@ struct Maps {
     CUtensorMap q, go, k, v, q_half, go_half, k_half, v_half, dq, dk, dv;
 };
 
+// Whether the first row of a dq block, which sees the fewest keys, has few terms.
+__device__ __forceinline__ bool few_keys(const Params &prm, int block)
+{
+    const int p = Work<kHalf>::first_row(prm, block % prm.units) + prm.Nk - prm.Nq;
+    return p < kFewTerms || (prm.window <= kFewTerms && prm.sinks <= kFewTerms - prm.window);
+}
+
+// kFine: dS is multiplied as two parts.
 template <int DT, bool kFine>
 __device__ __forceinline__ void dq_block(const Maps &maps, const Params &prm, const int block, uint8_t *smem_raw)
 {
@@ -236,12 +247,12 @@ __device__ __forceinline__ void dq_block(const Maps &maps, const Params &prm, co
                         const uint64_t d = kt + pst * (kStage >> 4);
 #pragma unroll
                         for (int kk = 0; kk < kHalf / 16; ++kk)
-                            mma_ts(tmem + tG + s * DT, tmem + tS + s * kHalf + ds_at(kk), d + kk * (2048 >> 4), id_g,
+                            mma_ts(tmem + tG + s * DT, tmem + tS + s * kHalf + half_at(kk), d + kk * (2048 >> 4), id_g,
                                    fed[s] > 0 || kk > 0);
                         if (kFine)
 #pragma unroll
                             for (int kk = 0; kk < kHalf / 16; ++kk)
-                                mma_ts(tmem + tG + s * DT, tmem + tS + s * kHalf + ds_at(kk) + kRest, d + kk * (2048 >> 4),
+                                mma_ts(tmem + tG + s * DT, tmem + tS + s * kHalf + half_at(kk) + kRest, d + kk * (2048 >> 4),
                                        id_g, true);
                     }
                     ++fed[s];
@@ -326,7 +337,7 @@ __device__ __forceinline__ void dq_block(const Maps &maps, const Params &prm, co
                     for (int e = 0; e < 32; ++e)
                         if (!((bits >> e) & 1u)) a[e] = 0u;
                 }
-                store_ds<kFine>(ts + 32 * g, a);
+                store_half<kFine>(ts + 32 * g, a);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -422,7 +433,7 @@ struct DkvSmem {
 };
 static_assert(sizeof(DkvSmem<128>) <= 232448, "fits an SM's shared memory");
 
-template <int DT, bool kFine>
+template <int DT>
 __device__ __forceinline__ void dkv_block(const Maps &maps, const Params &prm, const Split &sp, float *part, const int block,
                                           uint8_t *smem_raw)
 {
@@ -468,7 +479,171 @@ __device__ __forceinline__ void dkv_block(const Maps &maps, const Params &prm, c
     const int x0 = shared ? (int)((long long)all * share / sp.parts) : 0;
     const int X = (shared ? (int)((long long)all * (share + 1) / sp.parts) : all) - x0;
     const int rows = min(prm.Nq, n - off);  // rows of tokens
+    // the query rows that see key j; the fewest of a tile are at its ends, or where the sinks end
+    const int j1 = min(j0 + kRows, n) - 1;
+    auto few = [&](int j) {
+        const int last = j < prm.sinks ? n - 1 : min(n - 1, j + prm.window - 1);
+        return (last - max(j, off) + 1) * (long long)group <= kFewTerms;
+    };
+    const bool fine = few(j0) || few(j1) || (j0 < prm.sinks && prm.sinks <= j1 && few(prm.sinks));
 
+    // the products and the softmax groups, with P and dS in two parts or one
+    auto run = [&](auto parts) {
+        constexpr bool kFine = decltype(parts)::value;
+        if (warp == kMmaWarp) {
+            const uint32_t id_s = idesc_bf16_f32(128, kHalf, false, false), id_g = idesc_bf16_f32(128, DT, false, true);
+            const uint64_t kd = kmajor(smem_u32(sm.k), 0), vd = kmajor(smem_u32(sm.v), 0);
+            const uint64_t qd = kmajor_half(smem_u32(sm.q[0]), 0), gd = kmajor_half(smem_u32(sm.go[0]), 0);
+            const uint64_t qt_ = mnmajor_half(smem_u32(sm.q[0]), 0), gt = mnmajor_half(smem_u32(sm.go[0]), 0);
+            uint32_t st = 0, ph = 0, bst = 0;  // stage and phase of tile i, stage of tile i - 2
+            int at = per > 0 ? x0 % per : 0;   // tile i's place within its head
+            auto wait = [&](uint64_t *bar, uint32_t parity) { wait_or_abort(&g_winb_status, abort_flag, bar, parity); };
+            if (X > 0) wait(&sm.kv_full, 0);
+            for (int i = 0; i < (X > 0 ? X + 2 : 0); ++i) {
+                if (__any_sync(0xffffffffu, aborted(abort_flag))) break;
+                const uint32_t s = i & 1;
+                const int back = i - 2;
+                if (back >= 0) {  // the tile of this group before: its P and dS are in TMEM
+                    wait(&sm.ds_full[s], (uint32_t)(back >> 1) & 1u);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t so = bst * (kStage >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < kHalf / 16; ++kk)
+                            mma_ts(tmem + tG, tmem + tS + s * kHalf + half_at(kk), gt + so + kk * (2048 >> 4), id_g,
+                                   back > 0 || kk > 0);
+#pragma unroll
+                        for (int kk = 0; kk < kHalf / 16; ++kk)
+                            mma_ts(tmem + tG + DT, tmem + tP + s * kHalf + half_at(kk), qt_ + so + kk * (2048 >> 4), id_g,
+                                   back > 0 || kk > 0);
+                        if (kFine)
+#pragma unroll
+                            for (int kk = 0; kk < kHalf / 16; ++kk) {
+                                mma_ts(tmem + tG, tmem + tS + s * kHalf + half_at(kk) + kRest, gt + so + kk * (2048 >> 4),
+                                       id_g, true);
+                                mma_ts(tmem + tG + DT, tmem + tP + s * kHalf + half_at(kk) + kRest,
+                                       qt_ + so + kk * (2048 >> 4), id_g, true);
+                            }
+                        mma_commit(&sm.q_empty[bst]);
+                    }
+                    if (++bst == kRowStages) bst = 0;
+                }
+                if (i < X) {
+                    wait(&sm.q_full[st], ph);
+                    const int t0 = (qt.begin + at) * kHalf;
+                    if (t0 + kHalf > rows) {
+                        zero_rows<DT>(sm.q[st], rows - t0, lane);
+                        zero_rows<DT>(sm.go[st], rows - t0, lane);
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t so = st * (kStage >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < DT / 16; ++kk)
+                            mma_ss(tmem + tS + s * kHalf, kd + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4),
+                                   qd + so + (((kk >> 2) * kHalfBox + (kk & 3) * 32) >> 4), id_s, kk > 0);
+#pragma unroll
+                        for (int kk = 0; kk < DT / 16; ++kk)
+                            mma_ss(tmem + tP + s * kHalf, vd + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4),
+                                   gd + so + (((kk >> 2) * kHalfBox + (kk & 3) * 32) >> 4), id_s, kk > 0);
+                        mma_commit(&sm.s_full[s]);
+                    }
+                    if (++st == kRowStages) st = 0, ph ^= 1u;
+                    if (++at == per) at = 0;
+                }
+            }
+            if (elect_one()) {
+                mma_commit(&sm.g_full);
+                mma_commit(&sm.drain);  // every MMA issued completes before TMEM is freed
+                drain(&sm.drain, 0);
+            }
+            __syncwarp();
+        } else {
+            const int s = warp >> 2, r = 32 * (warp & 3) + lane, j = j0 + r;
+            const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+            const uint32_t ts = tl + tS + s * kHalf, tp = tl + tP + s * kHalf;
+            const float c = prm.scale * kLog2e;
+            const uint64_t c2 = pair(c, c);
+            // positions [j, last] see key j
+            const int last = j >= n ? -1 : j < prm.sinks ? n - 1 : min(n - 1, j + prm.window - 1);
+            bool ok = !aborted(abort_flag);
+            for (int i = s; ok && i < X; i += 2) {
+                const int st = i % kRowStages, p0 = (qt.begin + (x0 + i) % per) * kHalf + off;
+                if (!(ok = wait_w(abort_flag, &sm.q_full[st], (uint32_t)(i / kRowStages) & 1u))) break;  // base, delta
+                if (!(ok = wait_w(abort_flag, &sm.s_full[s], (uint32_t)(i >> 1) & 1u))) break;
+                tc_fence_after();
+                const bool whole = j0 + kRows - 1 <= p0 && p0 + kHalf - 1 < n &&
+                                   (p0 + kHalf - 1 - j0 < prm.window || j0 + kRows <= prm.sinks);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t a[32], d[32];
+                    tmem_ld32(ts + 32 * g, a);
+                    tmem_ld32(tp + 32 * g, d);
+                    tmem_ld_wait();
+                    const ulonglong2 *bp = reinterpret_cast<const ulonglong2 *>(&sm.base[st][32 * g]);
+                    const ulonglong2 *dp = reinterpret_cast<const ulonglong2 *>(&sm.delta[st][32 * g]);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const ulonglong2 nb = bp[e / 4], nd = dp[e / 4];
+#pragma unroll
+                        for (int h = 0; h < 4; h += 2) {
+                            float x, y;
+                            split(mul2(add2(pair(a[e + h], a[e + h + 1]), h ? nb.y : nb.x), c2), x, y);
+                            x = ex2(x);
+                            y = ex2(y);
+                            a[e + h] = __float_as_uint(x);
+                            a[e + h + 1] = __float_as_uint(y);
+                            split(mul2(pair(x, y), add2(pair(d[e + h], d[e + h + 1]), h ? nd.y : nd.x)), x, y);
+                            d[e + h] = __float_as_uint(x);
+                            d[e + h + 1] = __float_as_uint(y);
+                        }
+                    }
+                    if (!whole) {
+                        const int lo = max(j - (p0 + 32 * g), 0), hi = min(last - (p0 + 32 * g), 31);
+                        const uint32_t bits = hi < lo || lo > 31 ? 0u : (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((bits >> e) & 1u)) a[e] = d[e] = 0u;
+                    }
+                    store_half<kFine>(ts + 32 * g, a);
+                    store_half<kFine>(tp + 32 * g, d);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&sm.ds_full[s]);
+            }
+            if (ok && X > 0) ok = wait_w(abort_flag, &sm.g_full, 0);
+            uint8_t *out = s == 0 ? sm.v : sm.k;  // group 0: dv, group 1: dk
+            if (ok && shared) {
+                // this share's sums: [share][dv, dk][128][DT]
+                float *dst = part + ((((size_t)bh * sp.tiles + j0 / kRows) * sp.parts + share) * 2 + s) * (kRows * DT) + r * DT;
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < DT; x += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(tl + tG + s * DT + x, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<uint4 *>(dst + x + e) =
+                            X > 0 ? make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            } else if (ok) {
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < DT; x += 16) stage16(out, tl + tG + s * DT, r, x, s == 0 ? 1.f : prm.scale, X > 0);
+                fence_proxy_async_smem();
+            }
+            named_bar_sync(1 + s, 128);
+            if (ok && !shared && (warp & 3) == 0 && lane == 0) {
+#pragma unroll
+                for (int x = 0; x < DT; x += 64) tma_store_3d(s == 0 ? &maps.dv : &maps.dk, out + x / 64 * kBox, x, j0, bh);
+                tma_store_commit();
+                tma_store_wait_all();
+            }
+            __syncwarp();
+        }
+    };
     if (warp == kTmaWarp) {
         if (lane == 0 && X > 0 && !aborted(abort_flag)) {
             mbar_arrive_expect_tx(&sm.kv_full, 2 * kTile);
@@ -498,156 +673,10 @@ __device__ __forceinline__ void dkv_block(const Maps &maps, const Params &prm, c
                 drain(&sm.q_full[i % kRowStages], (uint32_t)(i / kRowStages) & 1u);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
-        const uint32_t id_s = idesc_bf16_f32(128, kHalf, false, false), id_g = idesc_bf16_f32(128, DT, false, true);
-        const uint64_t kd = kmajor(smem_u32(sm.k), 0), vd = kmajor(smem_u32(sm.v), 0);
-        const uint64_t qd = kmajor_half(smem_u32(sm.q[0]), 0), gd = kmajor_half(smem_u32(sm.go[0]), 0);
-        const uint64_t qt_ = mnmajor_half(smem_u32(sm.q[0]), 0), gt = mnmajor_half(smem_u32(sm.go[0]), 0);
-        uint32_t st = 0, ph = 0, bst = 0;  // stage and phase of tile i, stage of tile i - 2
-        int at = per > 0 ? x0 % per : 0;   // tile i's place within its head
-        auto wait = [&](uint64_t *bar, uint32_t parity) { wait_or_abort(&g_winb_status, abort_flag, bar, parity); };
-        if (X > 0) wait(&sm.kv_full, 0);
-        for (int i = 0; i < (X > 0 ? X + 2 : 0); ++i) {
-            if (__any_sync(0xffffffffu, aborted(abort_flag))) break;
-            const uint32_t s = i & 1;
-            const int back = i - 2;
-            if (back >= 0) {  // the tile of this group before: its P and dS are in TMEM
-                wait(&sm.ds_full[s], (uint32_t)(back >> 1) & 1u);
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t so = bst * (kStage >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < kHalf / 16; ++kk)
-                        mma_ts(tmem + tG, tmem + tS + s * kHalf + kk * 8, gt + so + kk * (2048 >> 4), id_g, back > 0 || kk > 0);
-#pragma unroll
-                    for (int kk = 0; kk < kHalf / 16; ++kk)
-                        mma_ts(tmem + tG + DT, tmem + tP + s * kHalf + ds_at(kk), qt_ + so + kk * (2048 >> 4), id_g,
-                               back > 0 || kk > 0);
-                    if (kFine)
-#pragma unroll
-                        for (int kk = 0; kk < kHalf / 16; ++kk)
-                            mma_ts(tmem + tG + DT, tmem + tP + s * kHalf + ds_at(kk) + kRest, qt_ + so + kk * (2048 >> 4),
-                                   id_g, true);
-                    mma_commit(&sm.q_empty[bst]);
-                }
-                if (++bst == kRowStages) bst = 0;
-            }
-            if (i < X) {
-                wait(&sm.q_full[st], ph);
-                const int t0 = (qt.begin + at) * kHalf;
-                if (t0 + kHalf > rows) {
-                    zero_rows<DT>(sm.q[st], rows - t0, lane);
-                    zero_rows<DT>(sm.go[st], rows - t0, lane);
-                }
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t so = st * (kStage >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < DT / 16; ++kk)
-                        mma_ss(tmem + tS + s * kHalf, kd + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4),
-                               qd + so + (((kk >> 2) * kHalfBox + (kk & 3) * 32) >> 4), id_s, kk > 0);
-#pragma unroll
-                    for (int kk = 0; kk < DT / 16; ++kk)
-                        mma_ss(tmem + tP + s * kHalf, vd + (((kk >> 2) * kBox + (kk & 3) * 32) >> 4),
-                               gd + so + (((kk >> 2) * kHalfBox + (kk & 3) * 32) >> 4), id_s, kk > 0);
-                    mma_commit(&sm.s_full[s]);
-                }
-                if (++st == kRowStages) st = 0, ph ^= 1u;
-                if (++at == per) at = 0;
-            }
-        }
-        if (elect_one()) {
-            mma_commit(&sm.g_full);
-            mma_commit(&sm.drain);  // every MMA issued completes before TMEM is freed
-            drain(&sm.drain, 0);
-        }
-        __syncwarp();
+    } else if (fine) {
+        run(std::true_type{});
     } else {
-        const int s = warp >> 2, r = 32 * (warp & 3) + lane, j = j0 + r;
-        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const uint32_t ts = tl + tS + s * kHalf, tp = tl + tP + s * kHalf;
-        const float c = prm.scale * kLog2e;
-        const uint64_t c2 = pair(c, c);
-        // positions [j, last] see key j
-        const int last = j >= n ? -1 : j < prm.sinks ? n - 1 : min(n - 1, j + prm.window - 1);
-        bool ok = !aborted(abort_flag);
-        for (int i = s; ok && i < X; i += 2) {
-            const int st = i % kRowStages, p0 = (qt.begin + (x0 + i) % per) * kHalf + off;
-            if (!(ok = wait_w(abort_flag, &sm.q_full[st], (uint32_t)(i / kRowStages) & 1u))) break;  // base, delta
-            if (!(ok = wait_w(abort_flag, &sm.s_full[s], (uint32_t)(i >> 1) & 1u))) break;
-            tc_fence_after();
-            const bool whole = j0 + kRows - 1 <= p0 && p0 + kHalf - 1 < n &&
-                               (p0 + kHalf - 1 - j0 < prm.window || j0 + kRows <= prm.sinks);
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint32_t a[32], d[32], pk[16];
-                tmem_ld32(ts + 32 * g, a);
-                tmem_ld32(tp + 32 * g, d);
-                tmem_ld_wait();
-                const ulonglong2 *bp = reinterpret_cast<const ulonglong2 *>(&sm.base[st][32 * g]);
-                const ulonglong2 *dp = reinterpret_cast<const ulonglong2 *>(&sm.delta[st][32 * g]);
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const ulonglong2 nb = bp[e / 4], nd = dp[e / 4];
-#pragma unroll
-                    for (int h = 0; h < 4; h += 2) {
-                        float x, y;
-                        split(mul2(add2(pair(a[e + h], a[e + h + 1]), h ? nb.y : nb.x), c2), x, y);
-                        x = ex2(x);
-                        y = ex2(y);
-                        a[e + h] = __float_as_uint(x);
-                        a[e + h + 1] = __float_as_uint(y);
-                        split(mul2(pair(x, y), add2(pair(d[e + h], d[e + h + 1]), h ? nd.y : nd.x)), x, y);
-                        d[e + h] = __float_as_uint(x);
-                        d[e + h + 1] = __float_as_uint(y);
-                    }
-                }
-                if (!whole) {
-                    const int lo = max(j - (p0 + 32 * g), 0), hi = min(last - (p0 + 32 * g), 31);
-                    const uint32_t bits = hi < lo || lo > 31 ? 0u : (0xffffffffu >> (31 - hi)) & (0xffffffffu << lo);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!((bits >> e) & 1u)) a[e] = d[e] = 0u;
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1]));
-                tmem_st16(ts + 16 * g, pk);
-                store_ds<kFine>(tp + 32 * g, d);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&sm.ds_full[s]);
-        }
-        if (ok && X > 0) ok = wait_w(abort_flag, &sm.g_full, 0);
-        uint8_t *out = s == 0 ? sm.v : sm.k;  // group 0: dv, group 1: dk
-        if (ok && shared) {
-            // this share's sums: [share][dv, dk][128][DT]
-            float *dst = part + ((((size_t)bh * sp.tiles + j0 / kRows) * sp.parts + share) * 2 + s) * (kRows * DT) + r * DT;
-            tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < DT; x += 16) {
-                uint32_t o[16];
-                tmem_ld16(tl + tG + s * DT + x, o);
-                tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 16; e += 4)
-                    *reinterpret_cast<uint4 *>(dst + x + e) =
-                        X > 0 ? make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_uint4(0u, 0u, 0u, 0u);
-            }
-        } else if (ok) {
-            tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < DT; x += 16) stage16(out, tl + tG + s * DT, r, x, s == 0 ? 1.f : prm.scale, X > 0);
-            fence_proxy_async_smem();
-        }
-        named_bar_sync(1 + s, 128);
-        if (ok && !shared && (warp & 3) == 0 && lane == 0) {
-#pragma unroll
-            for (int x = 0; x < DT; x += 64) tma_store_3d(s == 0 ? &maps.dv : &maps.dk, out + x / 64 * kBox, x, j0, bh);
-            tma_store_commit();
-            tma_store_wait_all();
-        }
-        __syncwarp();
+        run(std::false_type{});
     }
     tc_fence_before();
     __syncthreads();
@@ -656,17 +685,19 @@ __device__ __forceinline__ void dkv_block(const Maps &maps, const Params &prm, c
 }
 
 // Both kinds of blocks in one launch, the longer dk, dv ones first: neither waits for the other, and the
-// last wave is filled by either (8192 rows, d 128, window 1024: 243 us, 268 as two launches of 130
+// last wave is filled by either (8192 rows, d 128, window 1024: 244 us, 268 as two launches of 130
 // and 139 us, each with a last wave of its own).
-template <int DT, bool kFine>
+template <int DT>
 __global__ void __launch_bounds__(kThreads, 1)
 window_tc_backward(const __grid_constant__ Maps maps, const Params prm, const Split sp, float *part, const int dkv_blocks)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     if ((int)blockIdx.x < dkv_blocks)
-        dkv_block<DT, kFine>(maps, prm, sp, part, (int)blockIdx.x, smem_raw);
+        dkv_block<DT>(maps, prm, sp, part, (int)blockIdx.x, smem_raw);
+    else if (few_keys(prm, (int)blockIdx.x - dkv_blocks))
+        dq_block<DT, true>(maps, prm, (int)blockIdx.x - dkv_blocks, smem_raw);
     else
-        dq_block<DT, kFine>(maps, prm, (int)blockIdx.x - dkv_blocks, smem_raw);
+        dq_block<DT, false>(maps, prm, (int)blockIdx.x - dkv_blocks, smem_raw);
 }
 
 // -D = -dO . o and -lse / scale of every row, rows of an entry padded to whole tiles with zeros: 16
@@ -719,8 +750,7 @@ template <int DT>
 la_status backward(const WindowProblem &p)
 {
     const Params prm = params_of(p);
-    const bool fine = p.Nq <= kRows;
-    const auto kernel = fine ? window_tc_backward<DT, true> : window_tc_backward<DT, false>;
+    const auto kernel = window_tc_backward<DT>;
     const Split sp = split_of(p);
     const long long dq_ctas = (long long)p.B * p.Hk * prm.units;
     const long long dkv_ctas = (long long)p.B * p.Hk * (ceil_div(p.Nk, kRows) + sp.tiles * (sp.parts - 1LL));

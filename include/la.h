@@ -548,8 +548,12 @@ la_status la_recurrence_step(float *state, const void *x, const float *alpha, vo
  * workspace, or stream-ordered while the stream is being captured.
  *
  * Arithmetic: fp32 inputs in fp32 on the CUDA cores; bf16 inputs on the tensor cores with
- * fp32 scores, softmax and accumulation, the weights (and dS) rounded to bf16 for their
- * products.  Outputs overlap no input and no other output.
+ * fp32 scores, softmax and accumulation.  The forward rounds the weights to bf16 for their
+ * products (each by 2^-8 of itself at most, the output's own rounding again).  The
+ * backward does so with the weights and dS in sums of more than 256 products; a row of dq
+ * whose query sees at most 256 keys, and a row of dk or dv whose key is seen by at most 256
+ * query rows (of all heads that share it), takes them as two bf16 parts, within 2^-16.
+ * Outputs overlap no input and no other output.
  */
 la_status la_window_forward(const void *q, const void *k, const void *v, void *o, float *lse, const int *lens, int B,
                             int Hq, int Hk, int Nq, int Nk, int d, int window, int sinks, float scale, la_dtype dtype,

@@ -499,3 +499,41 @@ def test_backward_scratch_is_for_shared_tiles():
     la().la_window_backward(q, k, v, o, lse, go, 256, sinks=1, dq=grads[0], dk=grads[1], dv=grads[2], stream=s)
     s.synchronize()
     assert before - torch.cuda.mem_get_info()[0] <= 24 * 2 ** 20
+
+
+@pytest.mark.parametrize("B,Hq,Hk,Nq,Nk,d,window,sinks,lens", [
+    (1, 2, 2, 1500, 1500, 64, 16, 0, None), (2, 4, 2, 1000, 1000, 128, 100, 4, None), (1, 2, 1, 129, 129, 64, 1000, 0, None),
+    (1, 2, 1, 700, 700, 128, 1000, 0, None), (1, 3, 1, 900, 900, 64, 254, 2, None), (1, 4, 4, 900, 1400, 32, 256, 0, None),
+    (1, 2, 1, 900, 900, 64, 255, 2, None), (2, 2, 1, 600, 800, 128, 40, 300, [800, 700]), (1, 8, 1, 64, 1500, 64, 2, 0, None)])
+def test_gradients_of_few_terms_are_rounded_once(B, Hq, Hk, Nq, Nk, d, window, sinks, lens):
+    """A row of dq, dk or dv that sums at most 256 products carries little more than its own rounding, whatever
+    else the call holds: short windows, the first rows and last keys of long sequences.
+
+    Bound: half a step (2^-8) of the result, plus 2^-13 of A, the sum of scale P (|dO| . |v| + |dO| . |o|) |k|
+    (or |q|), for dv of P |dO|.  Where P and dS are held in two bf16 parts they are off by 2^-16 of themselves;
+    dP and D are sums of d products in fp32 (at most d 2^-24 <= 2^-17 of their absolute values), P is within
+    2^-16 for scores of a few units, and 256 products of a sum add 2^-16 of A: together below 2^-13.  Longer
+    sums may hold P and dS in one part, half a step more of each term: 2^-8 of their absolute sum."""
+    q, go = ref.draw(1, (B, Hq, Nq, d), torch.bfloat16), ref.draw(2, (B, Hq, Nq, d), torch.bfloat16)
+    k, v = ref.draw(3, (B, Hk, Nk, d), torch.bfloat16), ref.draw(4, (B, Hk, Nk, d), torch.bfloat16)
+    ln = None if lens is None else torch.tensor(lens, dtype=torch.int32)
+    opt = dict(sinks=sinks, lens=None if ln is None else ln.cuda())
+    o, lse = la().la_window_forward(q.cuda(), k.cuda(), v.cuda(), window, **opt)
+    grads = la().la_window_backward(q.cuda(), k.cuda(), v.cuda(), o, lse, go.cuda(), window, **opt)
+    group, scale = Hq // Hk, 1 / math.sqrt(d)
+    q, go, o, k, v = (x.cpu().double() for x in (q, go, o, k, v))
+    k, v = (x.repeat_interleave(group, 1) for x in (k, v))
+    see = torch.stack([ref.visible(Nq, Nk, window, sinks, Nk if ln is None else int(ln[b])) for b in range(B)])[:, None]
+    z = q @ k.transpose(-1, -2) * scale - lse.cpu().double()[..., None]
+    p = z.exp().masked_fill(~see, 0.0)
+    ds = scale * p * (go @ v.transpose(-1, -2) - (go * o).sum(-1, keepdim=True))
+    da = scale * p * (go.abs() @ v.abs().transpose(-1, -2) + (go.abs() * o.abs()).sum(-1, keepdim=True))
+    shared = lambda x: x.view(B, Hk, group, Nk, d).sum(2)  # noqa: E731
+    turned = lambda x: x.transpose(-1, -2)  # noqa: E731
+    rows, keys = see.sum(-1)[..., None], see.sum(-2)[..., None] * group
+    for name, got, terms, want, size, most in (
+            ("dq", grads[0], rows, ds @ k, ds.abs() @ k.abs(), da @ k.abs()),
+            ("dk", grads[1], keys, *(shared(turned(x) @ y) for x, y in ((ds, q), (ds.abs(), q.abs()), (da, q.abs())))),
+            ("dv", grads[2], keys, *(shared(turned(p) @ y) for y in (go, go.abs(), go.abs())))):
+        once = 2.0 ** -8 * want.abs() + 2.0 ** -13 * most + 1e-30
+        ref.assert_within(got, want, torch.where(terms <= 256, once, once + 2.0 ** -8 * size), name)
