@@ -340,8 +340,8 @@ window_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (ok && done > 0) ok = wait_w(abort_flag, &sm.o_full[s], (uint32_t)(done - 1) & 1u);
         if (ok && t0 < prm.Nq) {
             tc_fence_after();
-            // rows that saw nothing (l = 0) are zeros whatever TMEM holds
-            const bool some = l != 0.f;
+            // padding gives zeros whatever TMEM holds, a row of no finite score 0 / 0
+            const bool some = p < w.n;
             const float inv = 1.f / l;
 #pragma unroll
             for (int x = 0; x < DT; x += 16) {
@@ -560,7 +560,7 @@ window_tc_small_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_c
         if (ok && done > 0) ok = wait_w(abort_flag, &sm.o_full, (uint32_t)(done - 1) & 1u);
         if (ok) {
             tc_fence_after();
-            const bool some = l != 0.f;
+            const bool some = p < w.n;
             const float inv = 1.f / l;
 #pragma unroll
             for (int x = 0; x < 64; x += 16) {

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) window_forward_kernel(const Args a)
     for (int i = 0; i < 4; ++i) {
         const int t = t0 + ty + 16 * i;
         if (t >= a.Nq) continue;
-        const float inv = l[i] > 0.f || isnan(l[i]) ? 1.f / l[i] : 0.f;
+        const float inv = t + off < n ? 1.f / l[i] : 0.f;  // padding gives zeros, a row of no finite score 0 / 0
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
             op[(size_t)t * D + 32 * c + 2 * tx] = o[i][2 * c] * inv;

@@ -537,7 +537,8 @@ la_status la_recurrence_step(float *state, const void *x, const float *alpha, vo
  * aligned, or NULL: all Nk) gives the valid tokens of each entry, clamped to [0, Nk]:
  * rows at positions >= lens[b] are padding and give o = 0 and lse = -inf, keys there are
  * never used, whatever they hold.  Within the valid tokens an infinite or NaN k or v may
- * also reach rows of nearby positions that do not see it.  Supported: d in {32, 64, 128},
+ * also reach rows of nearby positions that do not see it, and a row whose scores are all
+ * -inf gives o = NaN and lse = -inf (a decode step NaN too).  Supported: d in {32, 64, 128},
  * Nq <= Nk <= 2^30, Hq a multiple of Hk, window >= 1, sinks >= 0, scale in [2^-100, 2^100].  window >= Nk
  * is plain causal attention.
  *

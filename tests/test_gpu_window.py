@@ -537,3 +537,22 @@ def test_gradients_of_few_terms_are_rounded_once(B, Hq, Hk, Nq, Nk, d, window, s
             ("dv", grads[2], keys, *(shared(turned(p) @ y) for y in (go, go.abs(), go.abs())))):
         once = 2.0 ** -8 * want.abs() + 2.0 ** -13 * most + 1e-30
         ref.assert_within(got, want, torch.where(terms <= 256, once, once + 2.0 ** -8 * size), name)
+
+
+@pytest.mark.parametrize("dtype,H,d", [("f32", 1, 64), ("bf16", 1, 64), ("bf16", 60, 64), ("bf16", 1, 128), ("f32", 2, 32)])
+def test_rows_of_no_finite_score(dtype, H, d):
+    """A softmax over scores that are all -inf has no value: NaN, not the zeros of a padding row, in the
+    forward as in a decode step; the other rows are their own."""
+    t, N, W = T[dtype], 150, 20
+    q, k, v = (ref.draw(i, (1, H, N, d), t) for i in (1, 2, 3))
+    k[..., 0] = 1.0
+    q[0, 0, 70, 0] = q[0, 0, 0, 0] = -math.inf
+    o, lse = la().la_window_forward(q.cuda(), k.cuda(), v.cuda(), W, sinks=1)
+    (wo, eo), (wl, el) = ref.window(q, k, v, W, 1, None, 1 / math.sqrt(d))
+    assert bool(torch.isnan(wo[0, 0, 70]).all()) and float(wl[0, 0, 70]) == -math.inf
+    ref.assert_within(o, wo, eo)
+    ref.assert_within(lse, wl, el)
+    kc, vc = la().la_window_cache(k[:, :, :70].contiguous().cuda(), v[:, :, :70].contiguous().cuda(), W, sinks=1)
+    one = [x[:, :, 70].contiguous().cuda() for x in (q, k, v)]
+    step = la().la_window_decode_step(kc, vc, *one, torch.tensor([70], dtype=torch.int32, device="cuda"), W, sinks=1)
+    assert torch.equal(torch.isnan(step), torch.isnan(o[:, :, 70]))
