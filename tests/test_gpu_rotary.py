@@ -98,3 +98,27 @@ def test_many_rows():
     q = ref.draw(6, (70000, 2, 1, 8), torch.bfloat16)
     pos = torch.arange(70000, dtype=torch.int32)[:, None]
     ref.assert_within(la().la_rotary_forward(q.cuda(), positions=pos.cuda()), *ref.rotary(q, pos, 8))
+
+
+@pytest.mark.parametrize("base", [34, 10000])
+@pytest.mark.parametrize("offset", [0, 2 ** 31 - 4, 2 ** 40])
+def test_frequencies_of_wide_heads(base, offset):
+    """128 pairs at far positions against 60-digit angles.  A frequency is a product of at most 7 powers of the
+    base: 7 (2^-52 + 2^-53), the exponents' rounding ln(base) 2^-53 and 3 2^-53 on the way to turns are below
+    2^-48 of the angle; the fraction of a turn ends at 2^-64, 2 pi 2^-64 for each position."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+    N, rot = 3, 256
+    ang = torch.empty((N, rot // 2), dtype=torch.float64)
+    full = torch.empty_like(ang)
+    for i in range(rot // 2):
+        f = (-Decimal(base).ln() * 2 * i / rot).exp()
+        for n in range(N):
+            full[n, i], ang[n, i] = float((offset + n) * f), float((offset + n) * f % (2 * pi))
+    x = torch.zeros((1, 1, N, rot))
+    x[..., :rot // 2] = 1.0
+    got = la().la_rotary_forward(x.cuda(), offset=offset, base=float(base))[0, 0]
+    off = 7 * ref.U + full * 2.0 ** -48 + (torch.arange(N)[:, None] + offset) * 6.3 * 2.0 ** -64
+    ref.assert_within(got[:, :rot // 2], ang.cos(), off, "cosines")
+    ref.assert_within(got[:, rot // 2:], ang.sin(), off, "sines")
