@@ -83,8 +83,8 @@ la_status check_spec(const la_rotary_spec *s, int d)
 }
 
 // Pair frequencies in turns per position, times 2^64 (modulo whole turns: a frequency of a
-// turn or more per position acts as its fraction).
-void fill_turns(const la_rotary_spec &s, uint64_t *turns)
+// turn or more per position acts as its fraction).  False where one is not finite.
+bool fill_turns(const la_rotary_spec &s, uint64_t *turns)
 {
     constexpr double kTwoPi = 6.283185307179586476925286766559;
     double base = s.base;
@@ -105,9 +105,11 @@ void fill_turns(const la_rotary_spec &s, uint64_t *turns)
             const double keep = fmin(1.0, fmax(0.0, (s.original * f / kTwoPi - s.ramp_lo) / (s.ramp_hi - s.ramp_lo)));
             g = f * (keep + (1.0 - keep) / s.factor);
         }
+        if (!isfinite(g)) return false;
         const double t = g / kTwoPi, part = t - floor(t);
         turns[i] = (uint64_t)(part * 0x1p64);  // part < 1: at most 2^64 - 2^11
     }
+    return true;
 }
 
 la_status rotary_checked(const void *q, const void *k, void *oq, void *ok, const int *positions, long long offset,
@@ -139,7 +141,7 @@ la_status rotary_checked(const void *q, const void *k, void *oq, void *ok, const
     p.backward = backward;
     p.dtype = dtype;
     p.stream = (cudaStream_t)stream;
-    fill_turns(*spec, p.turns);
+    if (!fill_turns(*spec, p.turns)) return LA_ERR_INVALID_ARG;
     return rotary(p);
 }
 

@@ -450,7 +450,8 @@ la_status la_decode_step_favor(float *S, float *z, const void *q, const void *k,
  *   LA_ROTARY_RAMP    by parts: with r_i = original f_i / (2 pi) turns over the original
  *                     context and g_i = clamp((r_i - ramp_lo) / (ramp_hi - ramp_lo), 0, 1),
  *                     f_i (g_i + (1 - g_i) / factor)
- * and A = amplitude.  Layouts: LA_ROTARY_HALF pairs features (i, i + rot/2),
+ * and A = amplitude; frequencies that overflow (a base or factor next to 0) are
+ * LA_ERR_INVALID_ARG.  Layouts: LA_ROTARY_HALF pairs features (i, i + rot/2),
  * LA_ROTARY_INTERLEAVED (2 i, 2 i + 1).  Features from `rot` on are copied.
  */
 typedef enum { LA_ROTARY_HALF = 0, LA_ROTARY_INTERLEAVED = 1 } la_rotary_layout;

@@ -162,3 +162,11 @@ def test_python_refusals():
         la.la_window_cache(x, x, 0)
     with pytest.raises(ValueError):
         la.la_window_decode_step(x, x, x, x, x, x, 4)
+
+
+@pytest.mark.parametrize("name", ["la_rotary_forward", "la_rotary_backward"])
+def test_rotary_frequencies_that_overflow(lib, name):
+    """A base or factor next to 0 leaves pairs without a finite frequency."""
+    for bad in (dict(scaling=1, factor=1e-310), dict(scaling=2, factor=1e-300, rot=4, base=1e-20), dict(base=1e-320, scaling=1, factor=1e-10),
+                dict(scaling=3, factor=1e-310, original=4096)):
+        assert rotary(lib, name, spec(**bad)) == INVALID, bad
