@@ -116,11 +116,17 @@ def _out(what, t, shape, dtype, dev):
     return t
 
 
-def _int(what, v):
+def _int(what, v, bits=32):
     if type(v) is not int:
-        v = int(v)
-    if not -2 ** 31 <= v < 2 ** 31:
-        raise ValueError("%s must fit 32 bits" % what)
+        try:
+            i = int(v)
+        except (TypeError, ValueError, OverflowError):
+            i = None
+        if i is None or i != v:
+            raise TypeError("%s must be a whole number, got %r" % (what, v))
+        v = i
+    if not -1 << bits - 1 <= v < 1 << bits - 1:
+        raise ValueError("%s must fit %d bits" % (what, bits))
     return v
 
 
@@ -132,6 +138,8 @@ def _rotary(name, q, k, oq, ok, positions, offset, rot, layout, base, scaling, f
         raise ValueError("q and k must be [B, H, N, d], or [B, H, d] for one token")
     if k is None and ok is not None:
         raise ValueError("an output for k without k")
+    offset, original = _int("offset", offset, 64), _int("original", original)
+    rot = q.shape[-1] if rot is None else _int("rot", rot)
     dev = _place(q, k, positions)
     code = _dtype_code(q, k)
     B, Hq, N, d = _sizes(q) if q.dim() == 4 else (q.shape[0], q.shape[1], 1, q.shape[2])
@@ -146,9 +154,8 @@ def _rotary(name, q, k, oq, ok, positions, offset, rot, layout, base, scaling, f
         raise ValueError("positions must be int32 [B, N]")
     if layout not in _LAYOUTS or scaling not in _SCALINGS:
         raise ValueError("layout is one of %s, scaling one of %s" % (sorted(_LAYOUTS), sorted(_SCALINGS)))
-    spec = RotarySpec(d if rot is None else _int("rot", rot), _LAYOUTS[layout], _SCALINGS[scaling],
-                      _int("original", original), base, factor, ramp[0], ramp[1], amplitude)
-    _call(name, dev, stream, q.data_ptr(), _ptr(k), oq.data_ptr(), _ptr(ok), _ptr(positions), int(offset),
+    spec = RotarySpec(rot, _LAYOUTS[layout], _SCALINGS[scaling], original, base, factor, ramp[0], ramp[1], amplitude)
+    _call(name, dev, stream, q.data_ptr(), _ptr(k), oq.data_ptr(), _ptr(ok), _ptr(positions), offset,
           ctypes.byref(spec), B, Hq, Hk, N, d, code)
     return oq if k is None else (oq, ok)
 
@@ -261,14 +268,14 @@ def la_window_forward(q, k, v, window: int, sinks: int = 0, lens=None, scale: fl
     if torch is None:
         _start()
     B, Hq, Hk, Nq, Nk, d = _window_shapes(q, k, v, lens)
+    window, sinks = _int("window", window), _int("sinks", sinks)
     dev = _place(q, k, v, lens)
     code = _dtype_code(q, k, v)
     o = _like(q, stream) if o is None else _out("o", o, q.shape, q.dtype, dev)
     lse = (_new((B, Hq, Nq), torch.float32, q.device, stream) if lse is None
            else _out("lse", lse, (B, Hq, Nq), torch.float32, dev))
     _call("la_window_forward", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-          _ptr(lens), B, Hq, Hk, Nq, Nk, d, _int("window", window),
-          _int("sinks", sinks), _scale(scale, d), code)
+          _ptr(lens), B, Hq, Hk, Nq, Nk, d, window, sinks, _scale(scale, d), code)
     return o, lse
 
 
@@ -278,6 +285,7 @@ def la_window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0, lens=
     if torch is None:
         _start()
     B, Hq, Hk, Nq, Nk, d = _window_shapes(q, k, v, lens)
+    window, sinks = _int("window", window), _int("sinks", sinks)
     dev = _place(q, k, v, o, lse, dout, lens)
     code = _dtype_code(q, k, v, o, dout)
     _shaped("o", o, q.shape)
@@ -287,8 +295,8 @@ def la_window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0, lens=
     dk = _like(k, stream) if dk is None else _out("dk", dk, k.shape, k.dtype, dev)
     dv = _like(v, stream) if dv is None else _out("dv", dv, v.shape, v.dtype, dev)
     _call("la_window_backward", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-          dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(lens), B, Hq, Hk, Nq, Nk, d, _int("window", window),
-          _int("sinks", sinks), _scale(scale, d), code)
+          dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(lens), B, Hq, Hk, Nq, Nk, d, window, sinks,
+          _scale(scale, d), code)
     return dq, dk, dv
 
 

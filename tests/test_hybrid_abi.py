@@ -170,3 +170,23 @@ def test_rotary_frequencies_that_overflow(lib, name):
     for bad in (dict(scaling=1, factor=1e-310), dict(scaling=2, factor=1e-300, rot=4, base=1e-20), dict(base=1e-320, scaling=1, factor=1e-10),
                 dict(scaling=3, factor=1e-310, original=4096)):
         assert rotary(lib, name, spec(**bad)) == INVALID, bad
+
+
+def test_whole_numbers_are_not_bent():
+    """A window of 4.7 is no window of 4, an offset past 64 bits none modulo them."""
+    x, y = torch.zeros((1, 2, 4, 64)), torch.zeros((1, 2, 64))
+    lse, pos = torch.zeros((1, 2, 4)), torch.zeros(1, dtype=torch.int32)
+    for kw in (dict(window=4.7), dict(window=4, sinks=1.5), dict(window="4"), dict(window=float("nan")), dict(window=None)):
+        for call in (lambda: la.la_window_forward(x, x, x, **kw), lambda: la.la_window_backward(x, x, x, x, lse, x, **kw),
+                     lambda: la.la_window_cache(x, x, **kw), lambda: la.la_window_decode_step(x, x, y, y, y, pos, **kw)):
+            with pytest.raises(TypeError, match="whole number"):
+                call()
+    for kw in (dict(rot=32.5), dict(offset=float("inf")), dict(offset=0.5), dict(scaling="ramp", original=4096.5)):
+        for call in (la.la_rotary_forward, la.la_rotary_backward):
+            with pytest.raises(TypeError, match="whole number"):
+                call(x, **kw)
+    for kw, bits in ((dict(offset=2 ** 63), 64), (dict(offset=-2 ** 63 - 1), 64), (dict(rot=2 ** 31), 32)):
+        with pytest.raises(ValueError, match="%d bits" % bits):
+            la.la_rotary_forward(x, **kw)
+    with pytest.raises(ValueError, match="CUDA device"):  # numbers of other kinds that are whole
+        la.la_window_forward(x, x, x, torch.tensor(4), sinks=2.0)
