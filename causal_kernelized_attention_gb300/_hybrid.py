@@ -101,7 +101,7 @@ def _shaped(what, t, shape, dtype=None):
 
 def _sizes(t):
     """The tensor's sizes, which the library takes as 32-bit numbers."""
-    if t.numel() >= 2 ** 31 and max(t.shape) >= 2 ** 31:
+    if not 0 < t.numel() < 2 ** 31 and max(t.shape) >= 2 ** 31:  # (an empty tensor may have any)
         raise ValueError("sizes must fit 32 bits")
     return t.shape
 
@@ -138,11 +138,14 @@ def _rotary(name, q, k, oq, ok, positions, offset, rot, layout, base, scaling, f
         raise ValueError("q and k must be [B, H, N, d], or [B, H, d] for one token")
     if k is None and ok is not None:
         raise ValueError("an output for k without k")
+    _sizes(q)
+    if k is not None:
+        _sizes(k)
     offset, original = _int("offset", offset, 64), _int("original", original)
     rot = q.shape[-1] if rot is None else _int("rot", rot)
     dev = _place(q, k, positions)
     code = _dtype_code(q, k)
-    B, Hq, N, d = _sizes(q) if q.dim() == 4 else (q.shape[0], q.shape[1], 1, q.shape[2])
+    B, Hq, N, d = q.shape if q.dim() == 4 else (q.shape[0], q.shape[1], 1, q.shape[2])
     Hk = 0
     if k is not None:
         Hk = k.shape[1]
@@ -231,9 +234,9 @@ def la_recurrence_step(state, x, alpha, h=None, stream=None):
         _start()
     if x.dim() != 2:
         raise ValueError("x must be [B, D]")
+    shape = _sizes(x)
     dev = _place(state, x, alpha)
     code = _dtype_code(x)
-    shape = _sizes(x)
     _shaped("alpha", alpha, shape, torch.float32)
     _shaped("state", state, shape, torch.float32)
     h = _like(x, stream) if h is None else _out("h", h, shape, x.dtype, dev)
@@ -248,7 +251,7 @@ def _window_shapes(q, k, v, lens):
         _start()
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B, Hq, Nq, d], k and v [B, Hk, Nk, d]")
-    B, Hq, Nq, d = q.shape
+    B, Hq, Nq, d = _sizes(q)
     Hk, Nk = _sizes(k)[1:3]
     _shaped("k", k, (B, Hk, Nk, d))
     _shaped("v", v, k.shape)
@@ -331,8 +334,8 @@ def la_window_decode_step(kc, vc, q, k, v, pos, window: int, sinks: int = 0, sca
         _start()
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [B, Hq, d], k and v [B, Hk, d]")
-    B, Hq, d = q.shape
-    Hk = k.shape[1]
+    B, Hq, d = _sizes(q)
+    Hk = _sizes(k)[1]
     window, sinks = _int("window", window), _int("sinks", sinks)
     dev = _place(kc, vc, q, k, v, pos)
     code = _dtype_code(q, k, v, kc, vc)

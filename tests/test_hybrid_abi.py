@@ -190,3 +190,22 @@ def test_whole_numbers_are_not_bent():
             la.la_rotary_forward(x, **kw)
     with pytest.raises(ValueError, match="CUDA device"):  # numbers of other kinds that are whole
         la.la_window_forward(x, x, x, torch.tensor(4), sinks=2.0)
+
+
+def test_sizes_that_pass_32_bits():
+    """Every size that the library takes as 32 bits, none modulo them; empty tensors too."""
+    big = 2 ** 32 + 5
+    wide = lambda *shape: torch.zeros(1).expand(shape)  # noqa: E731
+    x, one = wide(1, 1, 8, 64), wide(1, 1, 64)
+    pos = torch.zeros(1, dtype=torch.int32)
+    for call in (lambda: la.la_window_forward(wide(1, 1, big, 64), x, x, 4), lambda: la.la_window_forward(wide(1, big, 8, 64), x, x, 4),
+                 lambda: la.la_window_forward(x, wide(1, 1, big, 64), wide(1, 1, big, 64), 4),
+                 lambda: la.la_window_backward(wide(1, 1, big, 64), x, x, x, x, x, 4),
+                 lambda: la.la_window_cache(wide(big, 0, 8, 64), wide(big, 0, 8, 64), 4),
+                 lambda: la.la_window_decode_step(x, x, wide(1, big, 64), one, one, pos, 4),
+                 lambda: la.la_window_decode_step(x, x, one, wide(1, big, 64), one, pos, 4),
+                 lambda: la.la_rotary_forward(wide(1, big, 64)), lambda: la.la_rotary_forward(wide(big, 0, 8, 64), wide(big, 1, 8, 64)),
+                 lambda: la.la_rotary_forward(x, wide(1, big, 8, 64)),
+                 lambda: la.la_recurrence_forward(wide(big, 0, 8), wide(big, 0, 8)), lambda: la.la_recurrence_step(one[0], wide(1, big), one[0])):
+        with pytest.raises(ValueError, match="fit 32 bits"):
+            call()
