@@ -52,6 +52,7 @@ constexpr int kRun = 16;             // tokens of a warp's run
 constexpr int kTok = kWarps * kRun;  // tokens of a tile
 
 static __device__ unsigned g_rec_status;
+std::atomic<bool> g_launched{false};
 
 // V neighbouring elements of type T.
 template <typename T, int V> struct alignas(sizeof(T) * V) Vec { T x[V]; };
@@ -384,6 +385,7 @@ la_status launch(const RecurrenceProblem &p, const Args<T> &a, long long units, 
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     lc.attrs = at;
     lc.numAttrs = S > 1 ? 1 : 0;
+    g_launched = true;
     count_launches();
     return cuda_status(cudaLaunchKernelEx(&lc, kern, ma, mx, mh, a));
 }
@@ -497,11 +499,7 @@ la_status recurrence(const RecurrenceProblem &p) { return any(p, nullptr); }
 
 la_status recurrence_read_status(cudaStream_t s, unsigned *bits)
 {
-    unsigned zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_rec_status, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_rec_status, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    return cuda_status(e);
+    return tc::read_status(g_launched, g_rec_status, s, bits);
 }
 
 la_status recurrence_step(float *state, const void *x, const float *alpha, void *h, int B, int D, la_dtype dtype,

@@ -6,6 +6,7 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <mutex>
 #include <unordered_map>
 
@@ -425,6 +426,19 @@ inline la_status launch_dependent(void (*kern)(Params...), unsigned grid, int th
     lc.attrs = at;
     lc.numAttrs = dependent_launch_allowed(s) ? 1 : 0;
     return cuda_status(cudaLaunchKernelEx(&lc, kern, args...));
+}
+
+// Reads and clears a unit's status word once one of its kernels has been launched (or captured) in this
+// process: a read takes some 16 us, which callers of other operators need not spend.
+inline la_status read_status(const std::atomic<bool> &launched, unsigned &word, cudaStream_t s, unsigned *bits)
+{
+    *bits = 0;
+    if (!launched.load(std::memory_order_relaxed)) return LA_OK;
+    unsigned zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(bits, word, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(word, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    return cuda_status(e);
 }
 
 inline int sm_count()

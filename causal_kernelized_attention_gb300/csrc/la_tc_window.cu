@@ -29,6 +29,7 @@ namespace {
 using namespace window;
 
 static __device__ unsigned g_win_status;
+std::atomic<bool> g_launched{false};
 
 constexpr int kT = kRows;  // rows and keys of a tile
 constexpr float kGrow = 8.f;  // log2 units a maximum may grow before the output is rescaled
@@ -609,6 +610,7 @@ la_status forward_small(const WindowProblem &p)
     if (st == LA_OK) st = make_map(&mo, p.out, p.B * p.Hq, p.Nq, p.d);
     if (st == LA_OK) st = ensure_smem((const void *)window_tc_small_kernel, (int)sizeof(SmallSmem));
     if (st != LA_OK) return st;
+    g_launched = true;
     count_launches();
     return launch_dependent(window_tc_small_kernel, (unsigned)ctas, 160, (int)sizeof(SmallSmem), p.stream, mq, mk, mv, mo, prm);
 }
@@ -627,6 +629,7 @@ la_status forward(const WindowProblem &p)
     if (st == LA_OK) st = make_map(&mo, p.out, p.B * p.Hq, p.Nq, p.d);
     if (st == LA_OK) st = ensure_smem((const void *)window_tc_kernel<DT, QT>, (int)sizeof(Sm));
     if (st != LA_OK) return st;
+    g_launched = true;
     count_launches();
     return launch_dependent(window_tc_kernel<DT, QT>, (unsigned)ctas, 32 * (4 * QT + 2), (int)sizeof(Sm), p.stream, mq, mk, mv, mo,
                             prm);
@@ -652,11 +655,7 @@ la_status window_forward_tc(const WindowProblem &p)
 
 la_status tc_window_read_status(cudaStream_t s, unsigned *bits)
 {
-    unsigned zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_win_status, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_win_status, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    return cuda_status(e);
+    return read_status(g_launched, g_win_status, s, bits);
 }
 
 }  // namespace la

@@ -41,6 +41,7 @@ namespace {
 using namespace window;
 
 static __device__ unsigned g_winb_status;
+std::atomic<bool> g_launched{false};
 
 constexpr int kHalf = 64;  // keys (dq) or query rows (dk, dv) of a streamed tile
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
@@ -774,6 +775,7 @@ la_status backward(const WindowProblem &p)
     constexpr int smem = (int)std::max(sizeof(DqSmem<DT>), sizeof(DkvSmem<DT>));
     if (st == LA_OK) st = ensure_smem((const void *)kernel, smem);
     if (st != LA_OK) return st;
+    g_launched = true;
     count_launches(sp.parts > 1 ? 3 : 2);
     st = launch_dependent(window_tc_rows, (unsigned)row_ctas, 256, 0, p.stream, static_cast<const __nv_bfloat16 *>(p.o),
                           static_cast<const __nv_bfloat16 *>(p.dout), prm);
@@ -799,11 +801,7 @@ la_status window_backward_tc(const WindowProblem &p)
 
 la_status tc_window_bwd_read_status(cudaStream_t s, unsigned *bits)
 {
-    unsigned zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_winb_status, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_winb_status, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    return cuda_status(e);
+    return read_status(g_launched, g_winb_status, s, bits);
 }
 
 }  // namespace la

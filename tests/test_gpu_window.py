@@ -556,3 +556,36 @@ def test_rows_of_no_finite_score(dtype, H, d):
     one = [x[:, :, 70].contiguous().cuda() for x in (q, k, v)]
     step = la().la_window_decode_step(kc, vc, *one, torch.tensor([70], dtype=torch.int32, device="cuda"), W, sinks=1)
     assert torch.equal(torch.isnan(step), torch.isnan(o[:, :, 70]))
+
+
+def test_status_reads_what_ran():
+    """A process that runs none of these operators does not pay for reading their status: the call is quicker
+    by two of the eight words (recurrence and window) than after them."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import time
+import torch
+import causal_kernelized_attention_gb300 as la
+
+def quickest():
+    best = 1e9
+    for _ in range(300):
+        t = time.perf_counter()
+        la.la_get_device_status()
+        best = min(best, time.perf_counter() - t)
+    return best
+
+q = torch.randn(1, 2, 256, 64, device="cuda").bfloat16()
+la.la_forward_causal(q, q, q)
+before = quickest()
+la.la_window_forward(q, q, q, 20)
+la.la_recurrence_forward(q[:, 0].contiguous(), torch.rand(1, 256, 64, device="cuda"))
+after = quickest()
+print(before, after)
+assert before < 0.87 * after  # 6 reads against 8: 0.75
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
