@@ -15,9 +15,10 @@
 // the last of them adds up; every sum is taken in a fixed order.  All products are fp32 fused
 // multiply-adds on 4 x 4 register tiles fed by 16-byte shared-memory loads (8 loads for 64
 // multiply-adds), rows padded by 4 floats so that the 8 threads of a quarter-warp meet 8
-// different bank groups: bound by the CUDA cores' fp32 rate (2048 rows, window 512, d 128:
-// forward 43 TFLOP/s, backward 36 by the algorithm's 10 d operations a pair).  fp32 calls run
-// here; bf16 calls run on the tensor cores.
+// different bank groups.  Bound by the shared-memory loads between the multiply-adds: 2048
+// rows, window 512, d 128 run at 58% of the CUDA cores' fp32 rate (forward 43 TFLOP/s, backward
+// 36 by the algorithm's 10 d operations a pair, about 50 executed).  fp32 calls run here; bf16
+// calls run on the tensor cores.
 #include <math.h>
 
 #include <algorithm>
@@ -144,10 +145,8 @@ __device__ __forceinline__ float sum16(float v)
 // `sink_parts` CTAs each, the others over `parts`.
 struct Split {
     int sinks, sink_parts, parts, tiles;
+    int shared_tiles, shared_units;  // of a key head: the tiles of several shares, which come first, and those shares
     __host__ __device__ int units() const { return sinks * sink_parts + (tiles - sinks) * parts; }
-    // the tiles of several shares, which come first, and those shares
-    __host__ __device__ int shared_tiles() const { return parts > 1 ? tiles : sink_parts > 1 ? sinks : 0; }
-    __host__ __device__ int shared_units() const { return parts > 1 ? units() : sink_parts > 1 ? sinks * sink_parts : 0; }
 };
 
 struct Args {
@@ -417,7 +416,7 @@ __device__ __forceinline__ void dkv_block(const Args &a, const unsigned block, f
         mul_nn<D>(dk, dst, q, ty, tx);
     }
     if (parts > 1) {
-        float *dst = a.part + ((size_t)bh * a.sp.shared_units() + unit) * 2 * kT * D;
+        float *dst = a.part + (size_t)(bh * a.sp.shared_units + unit) * 2 * kT * D;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -430,11 +429,11 @@ __device__ __forceinline__ void dkv_block(const Args &a, const unsigned block, f
         __shared__ int last;
         __threadfence();
         __syncthreads();
-        if (threadIdx.x == 0) last = atomicAdd(a.left + (size_t)bh * a.sp.shared_tiles() + j0 / kT, 1) == parts - 1;
+        if (threadIdx.x == 0) last = atomicAdd(a.left + bh * a.sp.shared_tiles + j0 / kT, 1) == parts - 1;
         __syncthreads();
         if (!last) return;
         __threadfence();
-        const float *src = a.part + ((size_t)bh * a.sp.shared_units() + unit - share) * 2 * kT * D;
+        const float *src = a.part + (size_t)(bh * a.sp.shared_units + unit - share) * 2 * kT * D;
         for (int e = threadIdx.x; e < 2 * kT * (D / 4); e += kThreads) {
             const int c = e % (D / 4) * 4, r = e / (D / 4) % kT, which = e / (D / 4) / kT;
             if (j0 + r >= a.Nk) continue;
@@ -463,7 +462,7 @@ __device__ __forceinline__ void dkv_block(const Args &a, const unsigned block, f
 }
 
 // Both kinds of blocks in one launch, the dk, dv ones first: neither waits for the other, and the last
-// wave is filled by either (padded batch of 3 x 509 rows: 34 us in all, 42 as two launches).
+// wave is filled by either (padded batch of 3 x 509 rows: 42 -> 34 us by it, 30 with the shares added up here).
 template <int D>
 __global__ void __launch_bounds__(kThreads) window_backward_kernel(const Args a)
 {
@@ -520,12 +519,14 @@ Split split_of(const WindowProblem &p)
     // (many tiles of sinks: no more shares than fill the machine several times over)
     const long long cap = std::max<long long>(1, 4 * want / std::max<long long>(1, (long long)p.B * p.Hk * sp.sinks));
     sp.sink_parts = (int)std::min((rows * group + each - 1) / each, std::max<long long>(cap, sp.parts));
+    sp.shared_tiles = sp.parts > 1 ? sp.tiles : sp.sink_parts > 1 ? sp.sinks : 0;
+    sp.shared_units = sp.parts > 1 ? sp.units() : sp.shared_tiles * sp.sink_parts;
     return sp;
 }
 
 size_t part_floats(const WindowProblem &p, const Split &sp)
 {
-    return (size_t)p.B * p.Hk * sp.shared_units() * 2 * kT * p.d;
+    return (size_t)p.B * p.Hk * sp.shared_units * 2 * kT * p.d;
 }
 
 template <int D>
@@ -539,7 +540,7 @@ la_status backward(const WindowProblem &p)
     const long long dkv = (long long)p.B * p.Hk * a.sp.units(), dq = (long long)p.B * p.Hq * ceil_div(p.Nq, kT);
     if (dkv > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
     a.dkv_blocks = (unsigned)dkv;
-    a.shared = p.B * p.Hk * a.sp.shared_tiles();  // no more than dkv
+    a.shared = p.B * p.Hk * a.sp.shared_tiles;  // no more than dkv
     const long long rows = (long long)p.B * p.Hq * p.Nq;
     la_status st = launch(window_delta_kernel<D>, (rows * (D / 4) + kThreads - 1) / kThreads, 0, a, p.stream);
     if (st != LA_OK) return st;
@@ -557,7 +558,7 @@ la_status window_forward_simt(const WindowProblem &p)
 size_t window_backward_simt_scratch(const WindowProblem &p)
 {
     const Split sp = split_of(p);
-    return delta_bytes(p) + part_floats(p, sp) * sizeof(float) + (size_t)p.B * p.Hk * sp.shared_tiles() * sizeof(int);
+    return delta_bytes(p) + part_floats(p, sp) * sizeof(float) + (size_t)p.B * p.Hk * sp.shared_tiles * sizeof(int);
 }
 
 la_status window_backward_simt(const WindowProblem &p)
