@@ -99,11 +99,10 @@ def _shaped(what, t, shape, dtype=None):
         raise ValueError("%s must be %s%s" % (what, "" if dtype is None else "%s " % dtype, list(shape)))
 
 
-def _sizes(t):
-    """The tensor's sizes, which the library takes as 32-bit numbers."""
-    if not 0 < t.numel() < 2 ** 31 and max(t.shape) >= 2 ** 31:  # (an empty tensor may have any)
+def _fit(sizes):
+    """Checks the bits of all sizes, which the library takes as 32-bit numbers."""
+    if sizes >> 31:
         raise ValueError("sizes must fit 32 bits")
-    return t.shape
 
 
 def _out(what, t, shape, dtype, dev):
@@ -116,17 +115,21 @@ def _out(what, t, shape, dtype, dev):
     return t
 
 
-def _int(what, v, bits=32):
+def _whole(what, v):
+    try:
+        i = int(v)
+    except (TypeError, ValueError, OverflowError):
+        i = None
+    if i is None or i != v:
+        raise TypeError("%s must be a whole number, got %r" % (what, v))
+    return i
+
+
+def _int(what, v):
     if type(v) is not int:
-        try:
-            i = int(v)
-        except (TypeError, ValueError, OverflowError):
-            i = None
-        if i is None or i != v:
-            raise TypeError("%s must be a whole number, got %r" % (what, v))
-        v = i
-    if not -1 << bits - 1 <= v < 1 << bits - 1:
-        raise ValueError("%s must fit %d bits" % (what, bits))
+        v = _whole(what, v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError("%s must fit 32 bits" % what)
     return v
 
 
@@ -138,17 +141,17 @@ def _rotary(name, q, k, oq, ok, positions, offset, rot, layout, base, scaling, f
         raise ValueError("q and k must be [B, H, N, d], or [B, H, d] for one token")
     if k is None and ok is not None:
         raise ValueError("an output for k without k")
-    _sizes(q)
-    if k is not None:
-        _sizes(k)
-    offset, original = _int("offset", offset, 64), _int("original", original)
-    rot = q.shape[-1] if rot is None else _int("rot", rot)
+    B, Hq, N, d = q.shape if q.dim() == 4 else (q.shape[0], q.shape[1], 1, q.shape[2])
+    Hk = 0 if k is None else k.shape[1]
+    _fit(B | Hq | Hk | N | d)
+    if type(offset) is not int:
+        offset = _whole("offset", offset)
+    if not -2 ** 63 <= offset < 2 ** 63:
+        raise ValueError("offset must fit 64 bits")
+    original, rot = _int("original", original), d if rot is None else _int("rot", rot)
     dev = _place(q, k, positions)
     code = _dtype_code(q, k)
-    B, Hq, N, d = q.shape if q.dim() == 4 else (q.shape[0], q.shape[1], 1, q.shape[2])
-    Hk = 0
     if k is not None:
-        Hk = k.shape[1]
         _shaped("k", k, (B, Hk, N, d) if q.dim() == 4 else (B, Hk, d))
         ok = _like(k, stream) if ok is None else _out("the output for k", ok, k.shape, k.dtype, dev)
     oq = _like(q, stream) if oq is None else _out("the output for q", oq, q.shape, q.dtype, dev)
@@ -191,7 +194,8 @@ def la_recurrence_forward(x, alpha, h0=None, h=None, hN=None, stream=None):
         _start()
     if x.dim() != 3:
         raise ValueError("x must be [B, N, D]")
-    B, N, D = _sizes(x)
+    B, N, D = x.shape
+    _fit(B | N | D)
     dev = _place(x, alpha, h0)
     code = _dtype_code(x)
     _shaped("alpha", alpha, x.shape, torch.float32)
@@ -210,7 +214,8 @@ def la_recurrence_backward(alpha, h, dh, h0=None, dhN=None, dx=None, dalpha=None
         _start()
     if h.dim() != 3:
         raise ValueError("h must be [B, N, D]")
-    B, N, D = _sizes(h)
+    B, N, D = h.shape
+    _fit(B | N | D)
     dev = _place(alpha, h, dh, h0, dhN)
     code = _dtype_code(h, dh)
     _shaped("alpha", alpha, h.shape, torch.float32)
@@ -234,7 +239,8 @@ def la_recurrence_step(state, x, alpha, h=None, stream=None):
         _start()
     if x.dim() != 2:
         raise ValueError("x must be [B, D]")
-    shape = _sizes(x)
+    shape = x.shape
+    _fit(shape[0] | shape[1])
     dev = _place(state, x, alpha)
     code = _dtype_code(x)
     _shaped("alpha", alpha, shape, torch.float32)
@@ -251,8 +257,9 @@ def _window_shapes(q, k, v, lens):
         _start()
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B, Hq, Nq, d], k and v [B, Hk, Nk, d]")
-    B, Hq, Nq, d = _sizes(q)
-    Hk, Nk = _sizes(k)[1:3]
+    B, Hq, Nq, d = q.shape
+    Hk, Nk = k.shape[1:3]
+    _fit(B | Hq | Hk | Nq | Nk | d)
     _shaped("k", k, (B, Hk, Nk, d))
     _shaped("v", v, k.shape)
     _shaped("lens", lens, (B,), torch.int32)
@@ -311,7 +318,8 @@ def la_window_cache(k, v, window: int, sinks: int = 0, lens=None, kc=None, vc=No
         _start()
     if k.dim() != 4:
         raise ValueError("k and v must be [B, Hk, N, d]")
-    B, Hk, N, d = _sizes(k)
+    B, Hk, N, d = k.shape
+    _fit(B | Hk | N | d)
     window, sinks = _int("window", window), _int("sinks", sinks)
     if window < 1 or sinks < 0:
         raise ValueError("window must be at least 1, sinks at least 0")
@@ -334,8 +342,9 @@ def la_window_decode_step(kc, vc, q, k, v, pos, window: int, sinks: int = 0, sca
         _start()
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [B, Hq, d], k and v [B, Hk, d]")
-    B, Hq, d = _sizes(q)
-    Hk = _sizes(k)[1]
+    B, Hq, d = q.shape
+    Hk = k.shape[1]
+    _fit(B | Hq | Hk | d)
     window, sinks = _int("window", window), _int("sinks", sinks)
     dev = _place(kc, vc, q, k, v, pos)
     code = _dtype_code(q, k, v, kc, vc)
