@@ -18,6 +18,7 @@
 
 #include "la_common.cuh"
 #include "la_internal.h"
+#include "la_tc_common.cuh"
 
 namespace la {
 namespace {
@@ -124,11 +125,11 @@ la_status rotary(const RotaryProblem &p)
     int V = top;
     while (V > 1 && (p.spec.rot % (2 * V) != 0 || p.d % (2 * V) != 0)) V /= 2;
     // Heads per thread: up to 8 share a thread's sines, fewer when the tokens alone do
-    // not fill the machine (152 SMs x 2048 threads), down to one head per thread.
+    // not fill the machine (2048 threads an SM), down to one head per thread.
     const int heads = p.Hq + p.Hk;
     const long long threads = a.tokens * (p.d / (2 * V));
     int run = 8;
-    while (run > 1 && threads * ceil_div(heads, run) < 152LL * 2048) run /= 2;
+    while (run > 1 && threads * ceil_div(heads, run) < 2048LL * tc::sm_count()) run /= 2;
     a.run = max(run, ceil_div(heads, 65535));  // the grid's second dimension
     const bool il = p.spec.layout == LA_ROTARY_INTERLEAVED;
     if (p.dtype == LA_BF16) {
