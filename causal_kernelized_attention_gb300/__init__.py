@@ -17,7 +17,10 @@ Tensors are PyTorch CUDA tensors (PyTorch supplies device memory and streams):
   FAVOR+ forms: projections w [m, d] of the inputs' dtype, features [B, H, N, m];
   hybrid layers: rotary positions (int32 [B, N] or an offset), the gated recurrence
   x [B, N, D] with gates alpha fp32, and softmax attention over a sliding window with
-  sinks (q [B, Hq, N, d], k, v [B, Hk, N, d]; ring caches [B, Hk, sinks + window, d]).
+  sinks (q [B, Hq, N, d], k, v [B, Hk, N, d]; ring caches [B, Hk, sinks + window, d]);
+  the gated delta rule q, k [B, Hk, N, dk], v [B, H, N, dv], log gates g and beta fp32
+  [B, H, N], states fp32 [B, H, dk, dv]; group norm x [B, L, C] (or heads first) with an
+  activation or a gate.
 """
 from __future__ import annotations
 
@@ -28,7 +31,8 @@ from ._binding import (LA_BF16, LA_F32, LA_PHI_ELU1, LA_PHI_IDENTITY, LA_PHI_REL
                        la_prefill_state_ex, la_forward_noncausal_noalloc, la_get_device_status, la_kernel_launches, la_last_cuda_error,
                        la_prefill_state, la_prefill_state_decay, la_status_string, la_version, load_library,
                        la_forward_causal_gated, la_prefill_state_gated, la_decode_step_gated)
-from ._hybrid import (la_recurrence_backward, la_recurrence_forward, la_recurrence_step, la_rotary_backward,
+from ._hybrid import (la_delta_backward, la_delta_forward, la_delta_step, la_group_norm_backward,
+                      la_group_norm_forward, la_recurrence_backward, la_recurrence_forward, la_recurrence_step, la_rotary_backward,
                       la_rotary_forward, la_window_backward, la_window_cache, la_window_decode_step, la_window_forward)
 
 __all__ = [
@@ -41,5 +45,6 @@ __all__ = [
     "la_prefill_state_decay", "la_forward_causal_gated", "la_prefill_state_gated", "la_decode_step_gated",
     "la_rotary_forward", "la_rotary_backward", "la_recurrence_forward", "la_recurrence_backward", "la_recurrence_step",
     "la_window_forward", "la_window_backward", "la_window_cache", "la_window_decode_step",
+    "la_delta_forward", "la_delta_backward", "la_delta_step", "la_group_norm_forward", "la_group_norm_backward",
     "la_status_string", "la_version", "load_library",
 ]

@@ -40,6 +40,12 @@ class RotarySpec(ctypes.Structure):
                 ("ramp_hi", ctypes.c_double), ("amplitude", ctypes.c_float)]
 
 
+class GroupNormSpec(ctypes.Structure):
+    """la_group_norm_spec of include/la.h."""
+    _fields_ = [("groups", ctypes.c_int), ("per_token", ctypes.c_int), ("heads_first", ctypes.c_int),
+                ("center", ctypes.c_int), ("act", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
 LA_PHI_ELU1, LA_PHI_RELU, LA_PHI_IDENTITY = 0, 1, 2
 _FMAPS = {"elu1": LA_PHI_ELU1, "relu": LA_PHI_RELU, "identity": LA_PHI_IDENTITY}
 
@@ -104,7 +110,7 @@ def _declare(lib):
 
 def _hybrid_signatures(P, I, F):
     L = ctypes.c_longlong
-    S = ctypes.POINTER(RotarySpec)
+    S, G = ctypes.POINTER(RotarySpec), ctypes.POINTER(GroupNormSpec)
     return {
         "la_rotary_forward": [P, P, P, P, P, L, S, I, I, I, I, I, I, P],
         "la_rotary_backward": [P, P, P, P, P, L, S, I, I, I, I, I, I, P],
@@ -115,6 +121,11 @@ def _hybrid_signatures(P, I, F):
         "la_window_backward": [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, I, P],
         "la_window_cache": [P, P, P, P, P, I, I, I, I, I, I, I, P],
         "la_window_decode_step": [P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, P],
+        "la_delta_forward": [P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, P],
+        "la_delta_backward": [P, P, P, P, P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, P],
+        "la_delta_step": [P, P, P, P, P, P, P, I, I, I, I, I, F, I, P],
+        "la_group_norm_forward": [P, P, P, P, P, P, P, G, I, I, I, I, P],
+        "la_group_norm_backward": [P, P, P, P, P, P, P, P, P, P, P, G, I, I, I, I, P],
     }
 
 

@@ -1,4 +1,5 @@
-"""Hybrid-layer operators: rotary positions, the gated recurrence, window attention with sinks.
+"""Hybrid-layer operators: rotary positions, the gated recurrence, window attention with sinks, the
+gated delta rule, group norm with an activation or a gate.
 
 Marshalling only, as in ``_binding``: each function checks shapes and types, allocates the
 outputs that were not given and calls the C entry point of the same name on the tensors'
@@ -9,9 +10,10 @@ from __future__ import annotations
 import ctypes
 import math
 
-from ._binding import LA_BF16, LA_F32, RotarySpec, _check, load_library
+from ._binding import LA_BF16, LA_F32, GroupNormSpec, RotarySpec, _check, load_library
 
 _LAYOUTS = {"half": 0, "interleaved": 1}
+_ACTS = {"none": 0, "silu": 1}
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "ramp": 3}
 
 
@@ -358,3 +360,166 @@ def la_window_decode_step(kc, vc, q, k, v, pos, window: int, sinks: int = 0, sca
     _call("la_window_decode_step", dev, stream, kc.data_ptr(), vc.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
           o.data_ptr(), pos.data_ptr(), B, Hq, Hk, d, window, sinks, _scale(scale, d), code)
     return o
+
+
+# ---------------------------------------------------------------- gated delta rule
+def _delta_shapes(q, k, v, g, beta, S0):
+    if torch is None:
+        _start()
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and k must be [B, Hk, N, dk], v [B, H, N, dv]")
+    B, Hk, N, dk = q.shape
+    H, dv = v.shape[1], v.shape[3]
+    _fit(B | Hk | H | N | dk | dv)
+    _shaped("k", k, q.shape)
+    _shaped("v", v, (B, H, N, dv))
+    _shaped("g", g, (B, H, N), torch.float32)
+    _shaped("beta", beta, (B, H, N), torch.float32)
+    _shaped("S0", S0, (B, H, dk, dv), torch.float32)
+    return B, Hk, H, N, dk, dv
+
+
+def la_delta_forward(q, k, v, g, beta, S0=None, scale: float = None, o=None, SN=None, stream=None):
+    """The gated delta rule S_t = a S_{t-1} + k (beta (v - a S_{t-1}^T k))^T, a = exp(g), o_t = scale S_t^T q:
+    q, k [B,Hk,N,dk], v [B,H,N,dv], g and beta fp32 [B,H,N], S0 fp32 [B,H,dk,dv] (None: zeros), scale
+    1/sqrt(dk) by default.  Returns (o, the last state SN fp32 [B,H,dk,dv])."""
+    B, Hk, H, N, dk, dv = _delta_shapes(q, k, v, g, beta, S0)
+    dev = _place(q, k, v, g, beta, S0)
+    code = _dtype_code(q, k, v)
+    shape = (B, H, dk, dv)
+    o = _like(v, stream) if o is None else _out("o", o, v.shape, v.dtype, dev)
+    SN = _new(shape, torch.float32, v.device, stream) if SN is None else _out("SN", SN, shape, torch.float32, dev)
+    _call("la_delta_forward", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0),
+          o.data_ptr(), SN.data_ptr(), B, Hk, H, N, dk, dv, _scale(scale, dk), code)
+    return o, SN
+
+
+def la_delta_backward(q, k, v, g, beta, dout, S0=None, dSN=None, scale: float = None, dq=None, dk=None, dv=None, dg=None,
+                      dbeta=None, dS0=None, stream=None):
+    """Gradients of la_delta_forward from dout and dSN (None: zeros).  Returns (dq, dk, dv, dg fp32, dbeta fp32,
+    dS0 fp32 -- None when neither S0 nor dS0 was given)."""
+    B, Hk, H, N, d_k, d_v = _delta_shapes(q, k, v, g, beta, S0)
+    dev = _place(q, k, v, g, beta, dout, S0, dSN)
+    code = _dtype_code(q, k, v, dout)
+    shape, f32 = (B, H, d_k, d_v), torch.float32
+    _shaped("dout", dout, v.shape)
+    _shaped("dSN", dSN, shape, f32)
+    dq = _like(q, stream) if dq is None else _out("dq", dq, q.shape, q.dtype, dev)
+    dk = _like(k, stream) if dk is None else _out("dk", dk, k.shape, k.dtype, dev)
+    dv = _like(v, stream) if dv is None else _out("dv", dv, v.shape, v.dtype, dev)
+    dg = _like(g, stream) if dg is None else _out("dg", dg, g.shape, f32, dev)
+    dbeta = _like(beta, stream) if dbeta is None else _out("dbeta", dbeta, beta.shape, f32, dev)
+    if dS0 is not None:
+        _out("dS0", dS0, shape, f32, dev)
+    elif S0 is not None:
+        dS0 = _like(S0, stream)
+    _call("la_delta_backward", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0),
+          dout.data_ptr(), _ptr(dSN), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _ptr(dS0),
+          B, Hk, H, N, d_k, d_v, _scale(scale, d_k), code)
+    return dq, dk, dv, dg, dbeta, dS0
+
+
+def la_delta_step(S, q, k, v, g, beta, scale: float = None, o=None, stream=None):
+    """One token of la_delta_forward: S fp32 [B,H,dk,dv] in place; q, k [B,Hk,dk], v [B,H,dv], g, beta fp32
+    [B,H].  Returns o [B,H,dv]."""
+    if torch is None:
+        _start()
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and k must be [B, Hk, dk], v [B, H, dv]")
+    B, Hk, dk = q.shape
+    H, dv = v.shape[1:]
+    _fit(B | Hk | H | dk | dv)
+    dev = _place(S, q, k, v, g, beta)
+    code = _dtype_code(q, k, v)
+    f32 = torch.float32
+    _shaped("k", k, q.shape)
+    _shaped("v", v, (B, H, dv))
+    _shaped("S", S, (B, H, dk, dv), f32)
+    _shaped("g", g, (B, H), f32)
+    _shaped("beta", beta, (B, H), f32)
+    o = _like(v, stream) if o is None else _out("o", o, v.shape, v.dtype, dev)
+    _call("la_delta_step", dev, stream, S.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+          o.data_ptr(), B, Hk, H, dk, dv, _scale(scale, dk), code)
+    return o
+
+
+# ---------------------------------------------------------------- group norm
+def _norm_shapes(x, groups, w, b, gate, act, eps, per_token, heads_first, center):
+    """(B, L, C), the shape of y, that of the statistics, and the C options."""
+    if torch is None:
+        _start()
+    groups = _int("groups", groups)
+    if groups < 1 or act not in _ACTS:
+        raise ValueError("groups must be at least 1, act one of %s" % sorted(_ACTS))
+    if heads_first:
+        if not per_token or x.dim() != 4 or x.shape[1] != groups:
+            raise ValueError("heads_first needs per_token and x [B, groups, L, C / groups]")
+        B, L, C = x.shape[0], x.shape[2], groups * x.shape[3]
+    else:
+        if x.dim() != 3:
+            raise ValueError("x must be [B, L, C]")
+        B, L, C = x.shape
+    _fit(B | L | C)
+    shape, f32 = (B, L, C), torch.float32
+    _shaped("w", w, (C,), f32)
+    _shaped("b", b, (C,), f32)
+    _shaped("gate", gate, shape)
+    spec = GroupNormSpec(groups, bool(per_token), bool(heads_first), bool(center), _ACTS[act], eps)
+    return shape, (B, L, groups) if per_token else (B, groups), spec
+
+
+def la_group_norm_forward(x, groups: int, w=None, b=None, gate=None, act="none", eps: float = 1e-5, per_token=False,
+                          heads_first=False, center=True, y=None, mean=None, rstd=None, stream=None):
+    """y = act(z), or z * act(gate), with z = (x - mean) rstd w + b over groups of channels; x, gate, y
+    [B,L,C], w, b fp32 [C].  Statistics over all positions ([B,groups]), or each token's alone (per_token:
+    [B,L,groups]); heads_first: x [B,groups,L,C/groups].  center=False: the root mean square, no mean (None
+    returned).  act "none" or "silu".  Returns (y, mean, rstd)."""
+    shape, stats, spec = _norm_shapes(x, groups, w, b, gate, act, eps, per_token, heads_first, center)
+    dev = _place(x, gate, w, b)
+    code = _dtype_code(x, gate)
+    f32 = torch.float32
+    y = _new(shape, x.dtype, x.device, stream) if y is None else _out("y", y, shape, x.dtype, dev)
+    if not center:
+        if mean is not None:
+            raise ValueError("no mean without centring")
+    else:
+        mean = _new(stats, f32, x.device, stream) if mean is None else _out("mean", mean, stats, f32, dev)
+    rstd = _new(stats, f32, x.device, stream) if rstd is None else _out("rstd", rstd, stats, f32, dev)
+    _call("la_group_norm_forward", dev, stream, x.data_ptr(), _ptr(gate), _ptr(w), _ptr(b), y.data_ptr(), _ptr(mean),
+          rstd.data_ptr(), ctypes.byref(spec), *shape, code)
+    return y, mean, rstd
+
+
+def la_group_norm_backward(x, groups: int, mean, rstd, dy, w=None, b=None, gate=None, act="none", eps: float = 1e-5,
+                           per_token=False, heads_first=False, center=True, dx=None, dgate=None, dw=None, db=None,
+                           stream=None):
+    """Gradients of la_group_norm_forward (same options) from its statistics and dy.  Returns (dx, dgate -- None
+    without a gate --, dw, db -- each fp32 [C], None where neither it nor its weight was given)."""
+    shape, stats, spec = _norm_shapes(x, groups, w, b, gate, act, eps, per_token, heads_first, center)
+    if not center:
+        mean = None
+    elif mean is None:
+        raise ValueError("mean is needed")
+    dev = _place(x, gate, w, b, mean, rstd, dy)
+    code = _dtype_code(x, gate, dy)
+    f32 = torch.float32
+    _shaped("mean", mean, stats, f32)
+    _shaped("rstd", rstd, stats, f32)
+    _shaped("dy", dy, shape)
+    dx = _like(x, stream) if dx is None else _out("dx", dx, x.shape, x.dtype, dev)
+    if gate is None:
+        if dgate is not None:
+            raise ValueError("an output for the gate without a gate")
+    else:
+        dgate = _like(gate, stream) if dgate is None else _out("dgate", dgate, shape, x.dtype, dev)
+    if dw is not None:
+        _out("dw", dw, (shape[2],), f32, dev)
+    elif w is not None:
+        dw = _like(w, stream)
+    if db is not None:
+        _out("db", db, (shape[2],), f32, dev)
+    elif b is not None:
+        db = _like(b, stream)
+    _call("la_group_norm_backward", dev, stream, x.data_ptr(), _ptr(gate), _ptr(w), _ptr(b), _ptr(mean), rstd.data_ptr(),
+          dy.data_ptr(), dx.data_ptr(), _ptr(dgate), _ptr(dw), _ptr(db), ctypes.byref(spec), *shape, code)
+    return dx, dgate, dw, db

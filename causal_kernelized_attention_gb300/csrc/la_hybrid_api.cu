@@ -1,5 +1,5 @@
 // C ABI entry points of the hybrid-layer operators (rotary positions, the gated recurrence,
-// window attention): argument validation and dispatch.
+// window attention, the gated delta rule, group norm): argument validation and dispatch.
 #include <math.h>
 #include <stdint.h>
 
@@ -154,6 +154,58 @@ la_status check_window(int B, int Hq, int Hk, int d, int window, int sinks, floa
     if (!(scale >= 0x1p-100f) || !(scale <= 0x1p100f)) return LA_ERR_INVALID_ARG;
     if (Hk > 0 ? Hq % Hk != 0 : Hq != 0) return LA_ERR_INVALID_ARG;
     return LA_OK;
+}
+
+// ---------------------------------------------------------------- gated delta rule
+la_status check_delta(int B, int Hk, int H, int N, int dk, int dv, float scale, la_dtype dtype)
+{
+    if (B < 0 || Hk < 0 || H < 0 || N < 0 || dk < 0 || dv < 0 || !known(dtype) || !isfinite(scale)) return LA_ERR_INVALID_ARG;
+    if (Hk > 0 ? H % Hk != 0 : H != 0) return LA_ERR_INVALID_ARG;
+    return LA_OK;
+}
+// What the kernels' grids and 32-bit row counts hold.
+bool delta_supported(int B, int H, int N, int dk, int dv)
+{
+    return supported_dim(dk) && supported_dim(dv) && N <= kMaxTokens && (long long)B * H <= 0x7fffffff / 4 &&
+           (long long)B * H * ((N + 31LL) / 32) <= 0x7fffffff;
+}
+struct DeltaSizes {
+    size_t keys, values, gates, states;
+    DeltaSizes(int B, int Hk, int H, int N, int dk, int dv, la_dtype t)
+        : keys((size_t)B * Hk * N * dk * elem(t)), values((size_t)B * H * N * dv * elem(t)), gates((size_t)B * H * N * 4),
+          states((size_t)B * H * dk * dv * 4)
+    {
+    }
+};
+
+// ---------------------------------------------------------------- group norm
+la_status check_norm(const la_group_norm_spec *s, int B, int L, int C, la_dtype dtype)
+{
+    if (!s || B < 0 || L < 0 || C < 0 || !known(dtype) || s->groups < 1 || C % s->groups != 0) return LA_ERR_INVALID_ARG;
+    if ((s->per_token & ~1) || (s->heads_first & ~1) || (s->center & ~1) || (s->heads_first && !s->per_token))
+        return LA_ERR_INVALID_ARG;
+    if (s->act != LA_ACT_NONE && s->act != LA_ACT_SILU) return LA_ERR_INVALID_ARG;
+    return isfinite(s->eps) && s->eps >= 0.f ? LA_OK : LA_ERR_INVALID_ARG;
+}
+bool norm_supported(const la_group_norm_spec *s, int B, int L, int C)
+{
+    if (s->heads_first && C / s->groups > kNormTokenChannels) return false;
+    const long long tokens = (long long)B * L, entries = s->per_token ? tokens : B;
+    // groups, and blocks of sums (at most 152 * 6 + entries each of up to 2^16 / 256 columns of blocks), in 32 bits
+    return L <= kMaxTokens && tokens <= 0x3fffffff && C <= 0x3fffff && entries * s->groups <= 0x7fffffff;
+}
+
+la_status run_norm(NormProblem &p)
+{
+    const size_t bytes = norm_scratch(p);
+    if (bytes == 0) return group_norm(p);
+    std::lock_guard<std::mutex> lock(g_launches);
+    Scratch own;
+    void *base = nullptr;
+    const la_status st = call_scratch(p.stream, bytes, 4, &own, &base);
+    if (st != LA_OK) return st;
+    p.scratch = static_cast<float *>(base);
+    return group_norm(p);
 }
 
 }  // namespace
@@ -344,6 +396,157 @@ la_status la_window_decode_step(void *kc, void *vc, const void *q, const void *k
     if (!disjoint(out, in)) return LA_ERR_INVALID_ARG;
     WindowDecodeProblem p{kc, vc, q, k, v, o, pos, B, Hq, Hk, d, window, sinks, scale, dtype, (cudaStream_t)stream};
     return window_decode(p);
+}
+
+la_status la_delta_forward(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                           const float *S0, void *o, float *SN, int B, int Hk, int H, int N, int dk, int dv, float scale,
+                           la_dtype dtype, la_stream_t stream)
+{
+    la_status st = check_delta(B, Hk, H, N, dk, dv, scale, dtype);
+    if (st != LA_OK) return st;
+    if (B == 0 || H == 0 || dk == 0 || dv == 0 || (N == 0 && !SN)) return LA_OK;
+    if (N > 0 && (!q || !k || !v || !g || !beta || !o)) return LA_ERR_INVALID_ARG;
+    if (!aligned(S0, 16) || !aligned(SN, 16) ||
+        (N > 0 && (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(g, 4) || !aligned(beta, 4) || !aligned(o, 16))))
+        return LA_ERR_MISALIGNED;
+    if (!delta_supported(B, H, N, dk, dv)) return LA_ERR_UNSUPPORTED;
+    const DeltaSizes z(B, Hk, H, N, dk, dv, dtype);
+    const Span out[] = {{o, z.values}, {SN, z.states}};
+    const Span in[] = {{q, z.keys}, {k, z.keys}, {v, z.values}, {g, z.gates}, {beta, z.gates}, {S0, z.states}};
+    if (!disjoint(out, in)) return LA_ERR_INVALID_ARG;
+    DeltaProblem p{};
+    p.q = q; p.k = k; p.v = v; p.g = g; p.beta = beta; p.S0 = S0; p.o = o; p.SN = SN;
+    p.B = B; p.Hk = Hk; p.H = H; p.N = N; p.dk = dk; p.dv = dv;
+    p.scale = scale;
+    p.dtype = dtype;
+    p.stream = (cudaStream_t)stream;
+    return delta_forward_simt(p);
+}
+
+la_status la_delta_backward(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                            const float *S0, const void *dout, const float *dSN, void *dq, void *dk, void *dv, float *dg,
+                            float *dbeta, float *dS0, int B, int Hk, int H, int N, int d_k, int d_v, float scale,
+                            la_dtype dtype, la_stream_t stream)
+{
+    la_status st = check_delta(B, Hk, H, N, d_k, d_v, scale, dtype);
+    if (st != LA_OK) return st;
+    if (B == 0 || H == 0 || d_k == 0 || d_v == 0 || (N == 0 && !dS0)) return LA_OK;
+    if (N > 0 && (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta)) return LA_ERR_INVALID_ARG;
+    if (!aligned(S0, 16) || !aligned(dSN, 16) || !aligned(dS0, 16) ||
+        (N > 0 && (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(g, 4) || !aligned(beta, 4) ||
+                   !aligned(dout, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(dg, 4) ||
+                   !aligned(dbeta, 4))))
+        return LA_ERR_MISALIGNED;
+    if (!delta_supported(B, H, N, d_k, d_v)) return LA_ERR_UNSUPPORTED;
+    const DeltaSizes z(B, Hk, H, N, d_k, d_v, dtype);
+    const Span out[] = {{dq, z.keys}, {dk, z.keys}, {dv, z.values}, {dg, z.gates}, {dbeta, z.gates}, {dS0, z.states}};
+    const Span in[] = {{q, z.keys}, {k, z.keys}, {v, z.values}, {g, z.gates}, {beta, z.gates}, {S0, z.states},
+                       {dout, z.values}, {dSN, z.states}};
+    if (!disjoint(out, in)) return LA_ERR_INVALID_ARG;
+    DeltaProblem p{};
+    p.q = q; p.k = k; p.v = v; p.g = g; p.beta = beta; p.S0 = S0; p.dout = dout; p.dSN = dSN;
+    p.dq = dq; p.dk_out = dk; p.dv_out = dv; p.dg = dg; p.dbeta = dbeta; p.dS0 = dS0;
+    p.B = B; p.Hk = Hk; p.H = H; p.N = N; p.dk = d_k; p.dv = d_v;
+    p.scale = scale;
+    p.dtype = dtype;
+    p.stream = (cudaStream_t)stream;
+    std::lock_guard<std::mutex> lock(g_launches);
+    Scratch own;
+    void *base = nullptr;
+    const size_t bytes = delta_backward_simt_scratch(p);
+    if (bytes > 0 && (st = call_scratch(p.stream, bytes, 3, &own, &base)) != LA_OK) return st;
+    p.scratch = static_cast<float *>(base);
+    return delta_backward_simt(p);
+}
+
+la_status la_delta_step(float *S, const void *q, const void *k, const void *v, const float *g, const float *beta, void *o,
+                        int B, int Hk, int H, int dk, int dv, float scale, la_dtype dtype, la_stream_t stream)
+{
+    const la_status st = check_delta(B, Hk, H, 1, dk, dv, scale, dtype);
+    if (st != LA_OK) return st;
+    if (B == 0 || H == 0 || dk == 0 || dv == 0) return LA_OK;
+    if (!S || !q || !k || !v || !g || !beta || !o) return LA_ERR_INVALID_ARG;
+    if (!aligned(S, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(g, 4) || !aligned(beta, 4) ||
+        !aligned(o, 16))
+        return LA_ERR_MISALIGNED;
+    if (!delta_supported(B, H, 1, dk, dv)) return LA_ERR_UNSUPPORTED;
+    const DeltaSizes z(B, Hk, H, 1, dk, dv, dtype);
+    const Span out[] = {{S, z.states}, {o, z.values}};
+    const Span in[] = {{q, z.keys}, {k, z.keys}, {v, z.values}, {g, z.gates}, {beta, z.gates}};
+    if (!disjoint(out, in)) return LA_ERR_INVALID_ARG;
+    DeltaProblem p{};
+    p.q = q; p.k = k; p.v = v; p.g = g; p.beta = beta; p.o = o;
+    p.B = B; p.Hk = Hk; p.H = H; p.N = 1; p.dk = dk; p.dv = dv;
+    p.scale = scale;
+    p.dtype = dtype;
+    p.stream = (cudaStream_t)stream;
+    return delta_step(p, S);
+}
+
+la_status la_group_norm_forward(const void *x, const void *gate, const float *w, const float *b, void *y, float *mean,
+                                float *rstd, const la_group_norm_spec *spec, int B, int L, int C, la_dtype dtype,
+                                la_stream_t stream)
+{
+    const la_status st = check_norm(spec, B, L, C, dtype);
+    if (st != LA_OK) return st;
+    if (B == 0 || L == 0 || C == 0) return LA_OK;
+    if (!x || !y) return LA_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(gate, 16) || !aligned(w, 4) || !aligned(b, 4) || !aligned(y, 16) || !aligned(mean, 4) ||
+        !aligned(rstd, 4))
+        return LA_ERR_MISALIGNED;
+    if (!norm_supported(spec, B, L, C)) return LA_ERR_UNSUPPORTED;
+    const size_t n = (size_t)B * L * C * elem(dtype), c = (size_t)C * 4;
+    const size_t stats = (size_t)B * (spec->per_token ? L : 1) * spec->groups * 4;
+    const Span out[] = {{y, n}, {spec->center ? mean : nullptr, stats}, {rstd, stats}};
+    const Span in[] = {{x, n}, {gate, n}, {w, c}, {b, c}};
+    if (!disjoint(out, in)) return LA_ERR_INVALID_ARG;
+    NormProblem p{};
+    p.x = x; p.gate = gate; p.w = w; p.b = b; p.y = y; p.mean_out = spec->center ? mean : nullptr; p.rstd_out = rstd;
+    p.B = B; p.L = L; p.C = C;
+    p.spec = *spec;
+    p.dtype = dtype;
+    p.stream = (cudaStream_t)stream;
+    return run_norm(p);
+}
+
+la_status la_group_norm_backward(const void *x, const void *gate, const float *w, const float *b, const float *mean,
+                                 const float *rstd, const void *dy, void *dx, void *dgate, float *dw, float *db,
+                                 const la_group_norm_spec *spec, int B, int L, int C, la_dtype dtype,
+                                 la_stream_t stream)
+{
+    la_status st = check_norm(spec, B, L, C, dtype);
+    if (st != LA_OK) return st;
+    if (C == 0) return LA_OK;
+    if (!aligned(dw, 4) || !aligned(db, 4)) return LA_ERR_MISALIGNED;
+    const size_t n = (size_t)B * L * C * elem(dtype), c = (size_t)C * 4;
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (B == 0 || L == 0) {  // sums over nothing
+        if (overlap({dw, c}, {db, c})) return LA_ERR_INVALID_ARG;
+        for (float *grad : {dw, db})
+            if (grad) {
+                count_launches();
+                if ((st = cuda_status(cudaMemsetAsync(grad, 0, c, s))) != LA_OK) return st;
+            }
+        return LA_OK;
+    }
+    if (!x || !dy || !dx || !rstd || (spec->center && !mean) || (gate && !dgate)) return LA_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(gate, 16) || !aligned(w, 4) || !aligned(b, 4) || !aligned(mean, 4) || !aligned(rstd, 4) ||
+        !aligned(dy, 16) || !aligned(dx, 16) || !aligned(dgate, 16))
+        return LA_ERR_MISALIGNED;
+    if (!norm_supported(spec, B, L, C)) return LA_ERR_UNSUPPORTED;
+    const size_t stats = (size_t)B * (spec->per_token ? L : 1) * spec->groups * 4;
+    const Span out[] = {{dx, n}, {gate ? dgate : nullptr, n}, {dw, c}, {db, c}};
+    const Span in[] = {{x, n}, {gate, n}, {w, c}, {b, c}, {spec->center ? mean : nullptr, stats}, {rstd, stats}, {dy, n}};
+    if (!disjoint(out, in)) return LA_ERR_INVALID_ARG;
+    NormProblem p{};
+    p.x = x; p.gate = gate; p.dy = dy; p.w = w; p.b = b; p.mean = mean; p.rstd = rstd;
+    p.dx = dx; p.dgate = dgate; p.dw = dw; p.db = db;
+    p.B = B; p.L = L; p.C = C;
+    p.spec = *spec;
+    p.backward = true;
+    p.dtype = dtype;
+    p.stream = s;
+    return run_norm(p);
 }
 
 }  // extern "C"

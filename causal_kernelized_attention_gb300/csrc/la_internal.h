@@ -213,6 +213,41 @@ la_status window_decode(const WindowDecodeProblem &p);
 la_status window_cache(const void *k, const void *v, void *kc, void *vc, const int *lens, int B, int Hk, int N, int d,
                        int window, int sinks, la_dtype dtype, cudaStream_t stream);
 
+// Gated delta rule (la_delta.cu: the CUDA cores): forward o, SN; backward dout, dSN -> dq, dk_out, dv_out, dg,
+// dbeta, dS0, with scratch.
+struct DeltaProblem {
+    const void *q, *k, *v, *dout;
+    const float *g, *beta, *S0, *dSN;
+    void *o, *dq, *dk_out, *dv_out;
+    float *SN, *dg, *dbeta, *dS0;
+    float *scratch;
+    int B, Hk, H, N, dk, dv;
+    float scale;
+    la_dtype dtype;
+    cudaStream_t stream;
+};
+la_status delta_forward_simt(const DeltaProblem &p);
+la_status delta_backward_simt(const DeltaProblem &p);
+size_t delta_backward_simt_scratch(const DeltaProblem &p);  // bytes at p.scratch
+la_status delta_step(const DeltaProblem &p, float *S);
+
+// Group norm with an activation or a gate (la_norm.cu): forward y, mean_out, rstd_out; backward dy -> dx, dgate,
+// dw, db.  Scratch of norm_scratch() bytes.
+constexpr int kNormTokenChannels = 512;  // channels of a token's group that lanes hold in registers
+struct NormProblem {
+    const void *x, *gate, *dy;
+    const float *w, *b, *mean, *rstd;
+    void *y, *dx, *dgate;
+    float *mean_out, *rstd_out, *dw, *db, *scratch;
+    int B, L, C;
+    la_group_norm_spec spec;
+    bool backward;
+    la_dtype dtype;
+    cudaStream_t stream;
+};
+la_status group_norm(const NormProblem &p);
+size_t norm_scratch(const NormProblem &p);
+
 bool supported_dim(int d);
 
 // Counts every kernel launch / memset the library enqueues (la_kernel_launches).
@@ -237,8 +272,8 @@ la_status flag_workspace(cudaStream_t s, size_t bytes, void **out);
 // captured against it stays valid.  Returns LA_ERR_UNSUPPORTED when it cannot
 // serve the call (a stream under capture whose buffer is too small, or the
 // allocation failed); the caller then uses per-call scratch.  `which` tells a stream's
-// buffers apart: the window backward has one of its own (1), and so has the recurrence (2), which a
-// lock protects from another host thread's launches on the same stream.
+// buffers apart: the window backward has one of its own (1), and so have the recurrence (2), the delta
+// rule (3) and group norm (4), which a lock protects from another host thread's launches on the same stream.
 la_status data_workspace(cudaStream_t s, size_t bytes, void **out, int which = 0);
 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel and device,

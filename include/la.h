@@ -586,6 +586,86 @@ la_status la_window_decode_step(void *kc, void *vc, const void *q, const void *k
                                 const int *pos, int B, int Hq, int Hk, int d, int window, int sinks, float scale,
                                 la_dtype dtype, la_stream_t stream);
 
+/*
+ * Gated delta rule: the linear-attention state with a correcting write.  A token's value is
+ * stored less what the decayed state already answers for its key ("Linear Attention",
+ * aiwiki.thehackersbrain.dev, names the delta rule among the linear RNNs):
+ *
+ *   D_t = a_t S_{t-1},   a_t = exp(g_t),   S_t = D_t + k_t (beta_t (v_t - D_t^T k_t))^T,
+ *   o_t = scale S_t^T q_t,                 S_{-1} = S0 (NULL: zeros)
+ *
+ *   q, k : [B, Hk, N, dk]   v, o : [B, H, N, dv]   (element type `dtype`)
+ *   g, beta : [B, H, N] fp32   S0, SN : [B, H, dk, dv] fp32, each may be NULL; SN = S_{N-1} (S0 when N = 0)
+ *
+ * Head h reads key head h / (H / Hk).  No feature map, no normaliser; callers normalise the keys (with
+ * beta in [0, 1] and |k| <= 1 a write never overshoots; other values are computed as they stand).
+ * g <= 0 in the method and any value that is not NaN here, as long as products of gates do not overflow; a gate of
+ * -inf starts a new state, so packed sequences need no other mark.  A token with beta = 0 and g = 0 leaves the
+ * state as it is, so padding needs no lengths (its row of o is S^T q).  An infinite or NaN input makes rows of its
+ * chunk of 64 tokens and all that follow NaN or infinite, whatever gates lie between.
+ *
+ * la_delta_backward: given dout = dL/do and dSN = dL/dSN (NULL: zeros), writes dq, dk (summed over the heads
+ * that share them), dv, dg, dbeta (fp32) and dS0 (NULL: not wanted).  Recomputes the states (no saved
+ * activations).  Scratch: the state before and its gradient behind every chunk, and two rows of dv floats a token and head.
+ * Deterministic: every sum is taken in a fixed order.
+ * la_delta_step: one token; S [B, H, dk, dv] fp32 read and updated in place; q, k : [B, Hk, dk],
+ *   v, o : [B, H, dv], g, beta : [B, H].
+ *
+ * Supported: dk, dv in {32, 64, 128}, H a multiple of Hk, finite scale; g, beta, dg and dbeta need only their own
+ * 4-byte alignment.  Outputs overlap no input and no other output.  B = 0, H = 0, dk = 0 or dv = 0 is an empty problem; N = 0 still writes SN (dS0 = dSN).
+ */
+la_status la_delta_forward(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                           const float *S0, void *o, float *SN, int B, int Hk, int H, int N, int dk, int dv, float scale,
+                           la_dtype dtype, la_stream_t stream);
+la_status la_delta_backward(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                            const float *S0, const void *dout, const float *dSN, void *dq, void *dk, void *dv, float *dg,
+                            float *dbeta, float *dS0, int B, int Hk, int H, int N, int d_k, int d_v, float scale,
+                            la_dtype dtype, la_stream_t stream);
+la_status la_delta_step(float *S, const void *q, const void *k, const void *v, const float *g, const float *beta, void *o,
+                        int B, int Hk, int H, int dk, int dv, float scale, la_dtype dtype, la_stream_t stream);
+
+/*
+ * Group norm with an activation or a gate, channels last: behind the heads of the decayed forms and of
+ * the delta rule (per_token, each head of a token by itself), or over the positions of a feature map.
+ *
+ *   h = (x - mean) rstd,  rstd = 1 / sqrt(var + eps),   z = h w + b,   y = act(z), or z act(gate) with a gate
+ *
+ *   x, y, gate : [B, L, C] (element type `dtype`)   w, b : [C] fp32 (NULL: ones, zeros)   gate may be NULL
+ *   mean, rstd : [B, groups] fp32 over the L positions and C / groups channels of a group; with per_token
+ *                [B, L, groups], over a token's channels alone
+ *
+ * heads_first (with per_token): x is [B, groups, L, C / groups], as attention leaves its heads, and y and
+ * gate stay [B, L, C].  center = 0 takes no mean off (the root mean square; mean is neither read nor
+ * written).  act: LA_ACT_NONE or LA_ACT_SILU, z sigmoid(z).
+ *
+ * la_group_norm_forward: mean and rstd may be NULL (not wanted).
+ * la_group_norm_backward: from the forward's inputs, mean and rstd, writes dx (laid out as x), dgate, and
+ * dw, db (fp32, summed over all positions; each may be NULL: not wanted; they are deterministic).
+ *
+ * Supported: C a multiple of groups, L <= 2^30; heads_first with up to 512 channels a group; w, b, mean, rstd, dw and
+ * db need only their own 4-byte alignment.  Statistics and sums are fp32.  Outputs overlap no input and no other output.
+ * B, L or C = 0 is an empty problem (dw, db = 0).  Scratch (partial sums) from the stream's workspace, or
+ * stream-ordered while the stream is being captured.
+ */
+typedef enum { LA_ACT_NONE = 0, LA_ACT_SILU = 1 } la_act;
+
+typedef struct {
+    int groups;      /* >= 1 */
+    int per_token;   /* 0 or 1 */
+    int heads_first; /* 0 or 1; 1 needs per_token */
+    int center;      /* 0 or 1 */
+    int act;         /* la_act */
+    float eps;       /* >= 0, finite */
+} la_group_norm_spec;
+
+la_status la_group_norm_forward(const void *x, const void *gate, const float *w, const float *b, void *y, float *mean,
+                                float *rstd, const la_group_norm_spec *spec, int B, int L, int C, la_dtype dtype,
+                                la_stream_t stream);
+la_status la_group_norm_backward(const void *x, const void *gate, const float *w, const float *b, const float *mean,
+                                 const float *rstd, const void *dy, void *dx, void *dgate, float *dw, float *db,
+                                 const la_group_norm_spec *spec, int B, int L, int C, la_dtype dtype,
+                                 la_stream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *la_status_string(la_status s);
 

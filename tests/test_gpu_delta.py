@@ -1,0 +1,242 @@
+"""Gated delta rule on the GPU against the recurrence in float64."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import causal_kernelized_attention_gb300 as la  # noqa: E402
+from delta_ref import assert_near, delta, delta_inputs, delta_tolerance  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+F32 = ("SN", "dg", "dbeta", "dS0")
+
+
+def on_gpu(s):
+    return {i: None if x is None else x.cuda() for i, x in s.items()}
+
+
+def forward(s, scale=None, **kw):
+    return la.la_delta_forward(s["q"], s["k"], s["v"], s["g"], s["beta"], S0=s["S0"], scale=scale, **kw)
+
+
+def backward(s, scale=None, **kw):
+    got = la.la_delta_backward(s["q"], s["k"], s["v"], s["g"], s["beta"], s["dout"], S0=s["S0"], dSN=s["dSN"], scale=scale, **kw)
+    return dict(zip(("dq", "dk", "dv", "dg", "dbeta", "dS0"), got))
+
+
+def check(got, want, dtype, names):
+    for i in names:
+        out = torch.float32 if i in F32 else dtype
+        if got[i] is not None:
+            assert got[i].dtype == out
+            assert_near(got[i], want[i], delta_tolerance(dtype, out, True), i)
+
+
+CASES = [
+    # B, Hk, H, N, dk, dv, initial, resets
+    (1, 1, 1, 1, 64, 64, True, ()),
+    (2, 1, 2, 1, 128, 128, False, ()),
+    (1, 2, 2, 63, 64, 64, True, ()),
+    (1, 2, 2, 64, 128, 128, True, ()),
+    (1, 2, 4, 65, 128, 64, False, (64,)),
+    (2, 3, 3, 130, 64, 128, True, (0, 70)),
+    (1, 1, 3, 200, 128, 128, True, (129,)),
+    (1, 2, 2, 333, 64, 64, True, ()),
+    (2, 1, 4, 77, 32, 64, True, (5,)),
+    (1, 2, 2, 97, 64, 32, True, (31, 32)),
+    (1, 2, 4, 150, 32, 32, False, ()),
+    (1, 1, 1, 257, 32, 128, True, ()),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", CASES)
+def test_forward(case, dtype):
+    B, Hk, H, N, dk, dv, initial, resets = case
+    s = delta_inputs(1, B, Hk, H, N, dk, dv, TYPES[dtype], initial, resets)
+    want = delta(s, dk ** -0.5, backward=False)
+    o, SN = forward(on_gpu(s))
+    check(dict(o=o, SN=SN), want, TYPES[dtype], ("o", "SN"))
+    assert la.la_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", CASES)
+def test_backward(case, dtype):
+    B, Hk, H, N, dk, dv, initial, resets = case
+    s = delta_inputs(2, B, Hk, H, N, dk, dv, TYPES[dtype], initial, resets)
+    want = delta(s, 0.3)
+    check(backward(on_gpu(s), 0.3), want, TYPES[dtype], ("dq", "dk", "dv", "dg", "dbeta", "dS0"))
+    assert la.la_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_backward_is_deterministic_and_independent_of_what_ran_before(dtype):
+    a, b = (on_gpu(delta_inputs(i, 2, 2, 4, 190, 128, 128, TYPES[dtype])) for i in (3, 4))
+    first = backward(a)
+    backward(b)
+    again = backward(a)
+    for i, x in first.items():
+        assert torch.equal(x, again[i]), i
+
+
+def test_gradients_against_differences():
+    """fp32: the directional derivative of sum(o dout) + sum(SN dSN) by central differences of the float64 recurrence, along
+    unit directions: with a step of 2^-10 off by 2^-20 / 6 of the third derivative, 1e-4 of the gradient's norm at most as long
+    as that derivative is under 600 of them; the gradient itself is within 128 u."""
+    s = delta_inputs(5, 1, 2, 4, 70, 32, 32, torch.float32)
+    got = backward(on_gpu(s), 0.3)
+    gen = torch.Generator().manual_seed(6)
+    for name, grad in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("g", "dg"), ("beta", "dbeta"), ("S0", "dS0")):
+        d = torch.randn(s[name].shape, generator=gen, dtype=torch.float64)
+        d /= d.norm()
+        h = 2.0 ** -10
+
+        def loss(step):
+            r = delta({**s, name: s[name].double() + step * d}, 0.3, backward=False)
+            return float((r["o"] * s["dout"].double()).sum() + (r["SN"] * s["dSN"].double()).sum())
+
+        slope = (loss(h) - loss(-h)) / (2 * h)  # float64: off by h^2 of the third derivative
+        mine = float((got[grad].cpu().double() * d).sum())
+        size = float(got[grad].double().norm())
+        assert abs(mine - slope) <= 1e-4 * size, (name, mine, slope)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hk,H,dk,dv", [(1, 1, 1, 64, 64), (3, 2, 4, 128, 128), (5, 1, 3, 32, 64), (2, 2, 2, 128, 32), (2, 4, 4, 64, 128)])
+def test_step(B, Hk, H, dk, dv, dtype):
+    t = TYPES[dtype]
+    s = delta_inputs(7, B, Hk, H, 3, dk, dv, t)
+    s["g"][:, 0, 1] = -math.inf
+    want = delta(s, dk ** -0.5, backward=False)
+    d = on_gpu(s)
+    S = d["S0"].clone()
+    for i in range(3):
+        one = [d[n][:, :, i].contiguous() for n in ("q", "k", "v", "g", "beta")]
+        o = la.la_delta_step(S, *one)
+        assert_near(o[:, :, None], want["o"][:, :, i:i + 1], delta_tolerance(t, t, False), "o")
+    assert_near(S, want["SN"], delta_tolerance(t, torch.float32, False), "S")
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128), ("bf16", 32)])
+def test_prefill_then_steps_is_the_whole_sequence(dtype, d):
+    t = TYPES[dtype]
+    s = delta_inputs(8, 2, 2, 4, 140, d, d, t)
+    want = delta(s, d ** -0.5, backward=False)
+    g = on_gpu(s)
+    head = {n: g[n][:, :, :137].contiguous() for n in ("q", "k", "v", "g", "beta")}
+    o, S = la.la_delta_forward(**head, S0=g["S0"])
+    assert_near(o, want["o"][:, :, :137], delta_tolerance(t, t, True), "prefill")
+    for i in range(137, 140):
+        o = la.la_delta_step(S, *[g[n][:, :, i].contiguous() for n in ("q", "k", "v", "g", "beta")])
+        assert_near(o[:, :, None], want["o"][:, :, i:i + 1], delta_tolerance(t, t, True), "step")
+    assert_near(S, want["SN"], delta_tolerance(t, torch.float32, True), "S")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_no_tokens_and_padding_tokens(dtype):
+    t = TYPES[dtype]
+    s = on_gpu(delta_inputs(9, 1, 2, 2, 90, 64, 64, t))
+    none = {n: s[n][:, :, :0].contiguous() for n in ("q", "k", "v", "g", "beta", "dout")}
+    o, SN = forward({**none, "S0": s["S0"]})
+    assert o.numel() == 0 and torch.equal(SN, s["S0"])
+    assert torch.equal(backward({**none, "S0": s["S0"], "dSN": s["dSN"]})["dS0"], s["dSN"])
+    _, SN = forward({**none, "S0": None})
+    assert not SN.any()
+    # tokens with beta = 0 and g = 0 leave the state as it is, whatever they hold
+    short = {n: s[n][:, :, :70].contiguous() for n in ("q", "k", "v", "g", "beta")}
+    padded = {n: s[n].clone() for n in ("q", "k", "v", "g", "beta")}
+    padded["beta"][:, :, 70:], padded["g"][:, :, 70:] = 0.0, 0.0
+    padded["v"][:, :, 70:] = 1e4
+    a, b = forward({**short, "S0": s["S0"]}), forward({**padded, "S0": s["S0"]})
+    tol = delta_tolerance(t, torch.float32, True)
+    assert_near(b[1], a[1].cpu().double(), 2 * tol)
+    assert_near(b[0][:, :, :70], a[0].cpu().double(), 2 * delta_tolerance(t, t, True))
+
+
+def test_a_reset_is_a_new_sequence():
+    s = on_gpu(delta_inputs(10, 1, 1, 2, 150, 64, 64, torch.bfloat16, True, (83,)))
+    o, SN = forward(s)
+    tail = {n: s[n][:, :, 83:].contiguous() for n in ("q", "k", "v", "g", "beta")}
+    o2, SN2 = forward({**tail, "S0": None})
+    assert_near(o[:, :, 83:], o2.cpu().double(), 2 * delta_tolerance(torch.bfloat16, torch.bfloat16, True))
+    assert_near(SN, SN2.cpu().double(), 2 * delta_tolerance(torch.bfloat16, torch.float32, True))
+    got = backward(s)
+    head = {n: s[n][:, :, :83].contiguous() for n in ("q", "k", "v", "g", "beta", "dout")}
+    alone = backward({**head, "S0": s["S0"], "dSN": None})  # nothing comes back across the reset
+    assert not got["dg"][:, :, 83].any()
+    assert_near(got["dS0"], alone["dS0"].cpu().double(), 2 * delta_tolerance(torch.bfloat16, torch.float32, True))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_graphs_streams_and_given_outputs(dtype):
+    """A captured forward, backward and step, replayed with other inputs in place, beside an eager call on another stream."""
+    t = TYPES[dtype]
+    a, b = (delta_inputs(i, 1, 2, 4, 100, 64, 64, t) for i in (11, 12))
+    want = delta(b, 0.25)
+    s = on_gpu(a)
+    S = s["S0"].clone()
+    one = [s[n][:, :, 0].contiguous() for n in ("q", "k", "v", "g", "beta")]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        forward(s, 0.25), backward(s, 0.25)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, SN = forward(s, 0.25)
+        grads = backward(s, 0.25)
+        la.la_delta_step(S, *one, scale=0.25)
+    for n, x in on_gpu(b).items():
+        s[n].copy_(x)
+    S.copy_(s["S0"])
+    for x, n in zip(one, ("q", "k", "v", "g", "beta")):
+        x.copy_(s[n][:, :, 0])
+    other = on_gpu(delta_inputs(13, 1, 2, 4, 300, 64, 64, t))
+    side.wait_stream(torch.cuda.current_stream())
+    graph.replay()
+    with torch.cuda.stream(side):
+        forward(other, stream=side), backward(other, stream=side)
+    torch.cuda.synchronize()
+    check(dict(o=o, SN=SN, **grads), want, t, ("o", "SN", "dq", "dk", "dv", "dg", "dbeta", "dS0"))
+    first = {n: b[n][:, :, :1] if n not in ("S0", "dSN") else b[n] for n in b}
+    assert_near(S, delta(first, 0.25, backward=False)["SN"], delta_tolerance(t, torch.float32, True))
+    # outputs given by the caller
+    out = dict(o=torch.empty_like(o), SN=torch.empty_like(SN))
+    r = forward(s, 0.25, **out)
+    assert r[0] is out["o"] and r[1] is out["SN"] and torch.equal(r[0], o) and torch.equal(r[1], SN)
+
+
+def test_a_layer_of_delta_rule_and_head_norm():
+    """The two operators as a layer uses them: heads normalised per token, gated, channels last; forward and gradients
+    against float64 autograd of the plain formulas."""
+    B, H, N, d = 2, 3, 130, 64
+    s = delta_inputs(14, B, H, H, N, d, d, torch.bfloat16, False)
+    gen = torch.Generator().manual_seed(15)
+    gate, dy = (torch.randn((B, N, H * d), generator=gen).bfloat16() for _ in range(2))
+    w = 1 + 0.1 * torch.randn(H * d, generator=gen)
+    g = on_gpu(s)
+    o, _ = forward(g)
+    y, mean, rstd = la.la_group_norm_forward(o, H, w=w.cuda(), gate=gate.cuda(), act="silu", per_token=True, heads_first=True,
+                                             center=False)
+    do, dgate, dw, _ = la.la_group_norm_backward(o, H, mean, rstd, dy.cuda(), w=w.cuda(), gate=gate.cuda(), act="silu",
+                                                 per_token=True, heads_first=True, center=False)
+    got = la.la_delta_backward(g["q"], g["k"], g["v"], g["g"], g["beta"], do)
+    # the plain layer; the norm's gradient is handed on as float64
+    want = delta(s, d ** -0.5, backward=False)["o"].clone().requires_grad_()
+    h = want * (want.square().mean(-1, keepdim=True) + 1e-5).rsqrt()
+    z = h.transpose(1, 2).reshape(B, N, H * d) * w.double()
+    gd = gate.double().requires_grad_()
+    out = z * gd * torch.sigmoid(gd)
+    out.backward(dy.double())
+    tol = delta_tolerance(torch.bfloat16, torch.bfloat16, True)
+    assert_near(y.reshape(B, N, H, d).transpose(1, 2), out.detach().reshape(B, N, H, d).transpose(1, 2), 3 * tol, "y")
+    assert_near(do, want.grad, 4 * tol, "do")
+    s["dout"] = want.grad
+    ref = delta(s, d ** -0.5)
+    for i, x in zip(("dq", "dk", "dv"), got):
+        assert_near(x, ref[i], 5 * tol, i)
+    assert_near(dgate.reshape(B, N, H, d).transpose(1, 2), gd.grad.reshape(B, N, H, d).transpose(1, 2), 4 * tol, "dgate")
