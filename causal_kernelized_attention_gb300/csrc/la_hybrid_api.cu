@@ -420,7 +420,13 @@ la_status la_delta_forward(const void *q, const void *k, const void *v, const fl
     p.scale = scale;
     p.dtype = dtype;
     p.stream = (cudaStream_t)stream;
-    return delta_forward_simt(p);
+    if (!delta_tc_eligible(p)) return delta_forward_simt(p);
+    std::lock_guard<std::mutex> lock(g_launches);
+    Scratch own;
+    void *base = nullptr;
+    if ((st = call_scratch(p.stream, delta_forward_tc_scratch(p), 3, &own, &base)) != LA_OK) return st;
+    p.scratch = static_cast<float *>(base);
+    return delta_forward_tc(p);
 }
 
 la_status la_delta_backward(const void *q, const void *k, const void *v, const float *g, const float *beta,

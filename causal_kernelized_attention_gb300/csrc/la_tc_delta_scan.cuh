@@ -1,0 +1,856 @@
+// The preparing kernel and the scan of the tensor-core gated delta rule (bf16, d_k and d_v in {64, 128}): forward
+// (la_tc_delta.cu), and for the backward pass forward without o and in reverse (la_tc_delta_bwd.cu).
+//
+// The scan is a chain, chunk by chunk.  It is laid out so that a CTA owns a (b, h) and every product has
+// the value features as its 128 rows: E^T and what S^T gains appear in TMEM with one thread (of each half of the columns) to a feature,
+// the state itself in those threads' registers,
+// so that each step's result becomes the left operand of the next (tcgen05.ld, scale, split, tcgen05.st)
+// without passing through shared memory or another thread.  What the state feeds is held to fp32's
+// neighbourhood: T, W, S and U are multiplied as two bf16 parts (within 2^-17; the product of two low parts is
+// left out), K, Q, V and dO are exact; only products that end in o alone take single parts.
+#pragma once
+
+#include "la_tc_delta.cuh"
+
+namespace la {
+
+static __device__ unsigned g_delta_status = 0;  // one for each translation unit
+static std::atomic<bool> g_launched{false};
+
+namespace delta {
+namespace {
+
+// ---------------------------------------------------------------- preparing kernel
+// A CTA a (b, h, chunk): [Q; K] K^T in one product of 128 rows (TMEM lanes 0-63: Q K^T, 64-127: K K^T); N in
+// shared memory, inverted in place by blocks; T back as an operand for W.  Four warps, or eight (kBack): the
+// second four invert diag(beta) N, and what follows is shared out.
+constexpr int kRowStride = kChunk + 4;
+typedef float Square[kChunk][kRowStride];
+
+template <int DK, bool kBack> struct PrepSmem {
+    union alignas(1024) {
+        uint8_t qk[DK / 64][2 * kSq];             // per 64 columns: 64 rows of Q, 64 of K
+        uint8_t w[2][DK / 64][kSq];               // then W (or W2)
+    };
+    uint8_t extra[DK == 64 ? kSq : 1024];         // where Q leaves room for one part of T alone
+    uint8_t p[kBack ? 2 : 1][kBack ? 2 * kSq : 1024];  // P, as 128 rows of which the second half is not used
+    Square a[kBack ? 2 : 1];
+    Scalars s;
+    double G[kChunk];
+    uint64_t full, done;
+    uint32_t tmem_base;
+    int abort;
+};
+
+// (I + A)^-1 in place, A strictly lower triangular: 16-wide diagonal blocks by substitution (a thread a column),
+// then the blocks below them, T10 = -T11 (A10 T00), for 16 and for 32.  128 threads t, barrier `bar`.
+__device__ __forceinline__ void invert(Square &a, int t, int bar)
+{
+    {
+        const int b = (t >> 4) & 3, c = t & 15;
+        float x[16];
+        if (t < 64) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float s[4] = {i == c ? 1.f : 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < i; j += 4) {
+                    const float4 r = *reinterpret_cast<const float4 *>(&a[16 * b + i][16 * b + j]);
+                    s[0] = fmaf(-r.x, x[j], s[0]);
+                    if (j + 1 < i) s[1] = fmaf(-r.y, x[j + 1], s[1]);
+                    if (j + 2 < i) s[2] = fmaf(-r.z, x[j + 2], s[2]);
+                    if (j + 3 < i) s[3] = fmaf(-r.w, x[j + 3], s[3]);
+                }
+                x[i] = (s[0] + s[1]) + (s[2] + s[3]);
+            }
+        }
+        named_bar_sync(bar, 128);
+        if (t < 64)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) a[16 * b + i][16 * b + c] = x[i];
+        named_bar_sync(bar, 128);
+    }
+    {
+        const int o = 32 * (t >> 6), r = (t & 63) >> 2, c = 4 * (t & 3);
+#pragma unroll
+        for (int step = 0; step < 2; ++step) {  // A10 T00, then -T11 of that
+            const float *l = step ? &a[o + 16 + r][o + 16] : &a[o + 16 + r][o];
+            const int k0 = step ? o + 16 : o;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float w = l[k];
+                const float4 z = *reinterpret_cast<const float4 *>(&a[k0 + k][o + c]);
+                y.x = fmaf(w, z.x, y.x), y.y = fmaf(w, z.y, y.y), y.z = fmaf(w, z.z, y.z), y.w = fmaf(w, z.w, y.w);
+            }
+            if (step) y = make_float4(-y.x, -y.y, -y.z, -y.w);
+            named_bar_sync(bar, 128);
+            *reinterpret_cast<float4 *>(&a[o + 16 + r][o + c]) = y;
+            named_bar_sync(bar, 128);
+        }
+    }
+    {
+        const int r = 2 * (t >> 3), c = 4 * (t & 7);
+#pragma unroll
+        for (int step = 0; step < 2; ++step) {
+            const int k0 = step ? 32 : 0;
+            float4 y[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+                float4 z[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[e] = *reinterpret_cast<const float4 *>(&a[k0 + k + e][c]);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float4 l = *reinterpret_cast<const float4 *>(&a[32 + r + u][k0 + k]);
+                    const float w[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        y[u].x = fmaf(w[e], z[e].x, y[u].x), y[u].y = fmaf(w[e], z[e].y, y[u].y);
+                        y[u].z = fmaf(w[e], z[e].z, y[u].z), y[u].w = fmaf(w[e], z[e].w, y[u].w);
+                    }
+                }
+            }
+            named_bar_sync(bar, 128);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (step) y[u] = make_float4(-y[u].x, -y[u].y, -y[u].z, -y[u].w);
+                *reinterpret_cast<float4 *>(&a[32 + r + u][c]) = y[u];
+            }
+            named_bar_sync(bar, 128);
+        }
+    }
+}
+
+// Eight values to both parts of a swizzled row: 16 bytes each.
+__device__ __forceinline__ void split8(const float (&x)[8], uint4 &hi, uint4 &lo)
+{
+    split2(x[0], x[1], hi.x, lo.x);
+    split2(x[2], x[3], hi.y, lo.y);
+    split2(x[4], x[5], hi.z, lo.z);
+    split2(x[6], x[7], hi.w, lo.w);
+}
+
+// 32 columns x0 .. of TMEM (lane f: key feature; column: token) to both parts of an image [token][d_k] in shared memory.
+template <int DK> __device__ __forceinline__ void put_tokens(uint32_t taddr, uint8_t (*w)[DK / 64][kSq], int f, int x0, float sign)
+{
+    uint32_t a[32];
+    tmem_ld32(taddr + x0, a);
+    tmem_ld_wait();
+    if (f >= DK) return;
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        uint32_t hi, lo;
+        split2(sign * __uint_as_float(a[e]), sign * __uint_as_float(a[e + 1]), hi, lo);
+        const uint32_t p = sw128_offset(x0 + e, f & 63), q = sw128_offset(x0 + e + 1, f & 63);
+        *reinterpret_cast<uint16_t *>(w[0][f >> 6] + p) = (uint16_t)hi;
+        *reinterpret_cast<uint16_t *>(w[0][f >> 6] + q) = (uint16_t)(hi >> 16);
+        *reinterpret_cast<uint16_t *>(w[1][f >> 6] + p) = (uint16_t)lo;
+        *reinterpret_cast<uint16_t *>(w[1][f >> 6] + q) = (uint16_t)(lo >> 16);
+    }
+}
+
+template <int DK, bool kBack>
+__global__ void __launch_bounds__(kBack ? 256 : 128)
+delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k, const Params p, uint8_t *images)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    typedef PrepSmem<DK, kBack> Sm;
+    typedef Layout<DK> Lay;
+    constexpr int kNT = kBack ? 256 : 128;
+    constexpr uint32_t kTmem = kBack ? 256 : 128;
+    Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
+    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
+    const int chunks = (p.N + kChunk - 1) / kChunk, bh = blockIdx.x / chunks, chunk = blockIdx.x % chunks, t0 = chunk * kChunk;
+    const int bhk = bh / p.H * p.Hk + bh % p.H / (p.H / p.Hk);
+    uint8_t *image = images + (size_t)blockIdx.x * (kBack ? Lay::backward_bytes : Lay::forward_bytes);
+    if (tid == 0) {
+        mbar_init(&sm.full, 1);
+        mbar_init(&sm.done, 1);
+        sm.abort = (smem_u32(smem_raw) & 1023u) == 0 ? 0 : 1;
+        if (sm.abort) atomicOr(&g_delta_status, kStatusTimeout);
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&sm.tmem_base, kTmem);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t tmem = sm.tmem_base;
+    const bool sound = !aborted(&sm.abort);
+    if (warp == 0 && sound && elect_one()) {
+        mbar_arrive_expect_tx(&sm.full, DK / 64 * 2 * kSq);
+        for (int x = 0; x < DK / 64; ++x) {
+            tma_load_3d(sm.qk[x], &map_q, &sm.full, 64 * x, t0, bhk);
+            tma_load_3d(sm.qk[x] + kSq, &map_k, &sm.full, 64 * x, t0, bhk);
+        }
+    }
+    __syncwarp();
+    float gate = 0.f;
+    if (tid < 64) {  // the running sum of the gates (a gate below -200 closes as well as -inf), summed in 64 bits
+        const size_t at = (size_t)bh * p.N + t0 + tid;
+        gate = t0 + tid < p.N ? p.beta[at] : 0.f;
+        const float g = t0 + tid < p.N ? p.g[at] : 0.f;
+        double G = g < -200.f ? -200.f : g;
+        for (int d = 1; d < 32; d *= 2) {
+            const double x = __shfl_up_sync(0xffffffffu, G, d);
+            if (lane >= d) G += x;
+        }
+        sm.G[tid] = G;
+    }
+    __syncthreads();
+    if (tid < 64) {
+        const double half = sm.G[31], G = sm.G[tid] + (tid >= 32 ? half : 0.0), end = sm.G[63] + half;
+        const float first = expf((float)G), last = expf((float)(end - G));
+        Scalars &s = sm.s;
+        s.hi[tid] = (float)G;
+        s.lo[tid] = (float)(G - (double)(float)G);
+        s.first[tid] = first;
+        s.last[tid] = last;
+        s.beta[tid] = gate;
+        s.back[tid] = -gate * first;
+        s.write[tid] = gate * last;
+        s.spare[tid] = 0.f;
+    }
+    bool ok = sound;
+    if (warp == 0) {
+        ok = ok && wait_bar_warp(&g_delta_status, &sm.abort, &sm.full, 0);
+        if (ok) {
+            tc_fence_after();
+            if (elect_one()) {
+                constexpr uint32_t id = idesc_bf16_f32(128, kChunk, false, false);
+                const uint32_t a = smem_u32(sm.qk[0]);
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk)
+                    mma_ss(tmem, rows_k(a, kk, 2 * kSq), rows_k(a + kSq, kk, 2 * kSq), id, kk > 0);
+                mma_commit(&sm.done);
+            }
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    ok = sound && wait_bar_warp(&g_delta_status, &sm.abort, &sm.done, 0);
+    tc_fence_after();
+    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    if (ok) {
+        for (int i = tid; i < (int)sizeof(Scalars) / 16; i += kNT) reinterpret_cast<uint4 *>(image)[i] = reinterpret_cast<uint4 *>(&sm.s)[i];
+        const int row = 32 * (warp & 3) + lane, i = row & 63;
+        const float hi = sm.s.hi[i], lo = sm.s.lo[i], bi = sm.s.beta[i];
+        constexpr float kLog2e = 1.4426950408889634f;
+#pragma unroll 1
+        for (int j0 = kBack ? 32 * (warp >> 2) : 0; j0 < kChunk; j0 += kBack ? kChunk : 32) {
+            uint32_t s[32];
+            tmem_ld32(tl + j0, s);
+            tmem_ld_wait();
+            float d[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const int j = j0 + e;
+                float w;
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(kLog2e * ((hi - sm.s.hi[j]) + (lo - sm.s.lo[j]))));
+                d[e] = j <= i ? __uint_as_float(s[e]) * w : 0.f;
+            }
+            if (row < 64) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float x[8] = {d[8 * c], d[8 * c + 1], d[8 * c + 2], d[8 * c + 3], d[8 * c + 4], d[8 * c + 5], d[8 * c + 6], d[8 * c + 7]};
+                    uint4 h, l;
+                    split8(x, h, l);
+                    const uint32_t at = sw128_offset(i, j0 + 8 * c);
+                    if (kBack) {
+                        *reinterpret_cast<uint4 *>(sm.p[0] + at) = h;
+                        *reinterpret_cast<uint4 *>(sm.p[kBack ? 1 : 0] + at) = l;
+                    } else {
+                        *reinterpret_cast<uint4 *>(image + Lay::p + at) = h;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const int j = j0 + e;
+                    const float4 b = *reinterpret_cast<const float4 *>(&sm.s.beta[j]);
+                    const float4 n = make_float4(j < i ? d[e] : 0.f, j + 1 < i ? d[e + 1] : 0.f, j + 2 < i ? d[e + 2] : 0.f, j + 3 < i ? d[e + 3] : 0.f);
+                    *reinterpret_cast<float4 *>(&sm.a[0][i][j]) = make_float4(n.x * b.x, n.y * b.y, n.z * b.z, n.w * b.w);
+                    if (kBack) *reinterpret_cast<float4 *>(&sm.a[kBack ? 1 : 0][i][j]) = make_float4(bi * n.x, bi * n.y, bi * n.z, bi * n.w);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (!kBack || warp < 4)
+        invert(sm.a[0], tid & 127, 1);
+    else
+        invert(sm.a[kBack ? 1 : 0], tid & 127, 2);
+    __syncthreads();
+    // T to global memory, and T exp(G) over the rows of Q; then (kBack) T2 and exp(G_C - G) T2
+    uint8_t *tp[2] = {sm.qk[0], DK == 64 ? sm.extra : sm.qk[DK / 64 - 1]};
+    for (int u = tid; u < kChunk * 8; u += kNT) {
+        const int i = u >> 3, c = 8 * (u & 7);
+        const uint32_t at = sw128_offset(i, c);
+        float x[8], y[8];
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) *reinterpret_cast<float4 *>(&x[e]) = *reinterpret_cast<const float4 *>(&sm.a[0][i][c + e]);
+        uint4 h, l;
+        split8(x, h, l);
+        *reinterpret_cast<uint4 *>(image + Lay::t + at) = h;
+        *reinterpret_cast<uint4 *>(image + Lay::t + kSq + at) = l;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = x[e] * sm.s.first[c + e];
+        split8(y, h, l);
+        *reinterpret_cast<uint4 *>(tp[0] + at) = h;
+        *reinterpret_cast<uint4 *>(tp[1] + at) = l;
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    constexpr uint32_t id_w = idesc_bf16_f32(128, kChunk, true, false), id_w2 = idesc_bf16_f32(128, kChunk, true, true);
+    constexpr uint32_t lbo = DK == 128 ? 2 * kSq : 0;
+    const uint32_t ka = smem_u32(sm.qk[0]) + kSq;
+    if (warp == 0) {
+        tc_fence_after();
+        if (ok && elect_one()) {  // W^T = K^T (T exp(G))^T
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ss(tmem + 64, cols_mn(ka, kk, lbo), rows_k(smem_u32(tp[part]), kk), id_w, part + kk > 0);
+            mma_commit(&sm.done);
+        }
+        __syncwarp();
+    }
+    ok = ok && wait_bar_warp(&g_delta_status, &sm.abort, &sm.done, 1);
+    tc_fence_after();
+    if (!kBack) {
+        if (ok)
+            for (int x = 0; x < kChunk; x += 32) put_tokens<DK>(tl + 64, sm.w, 32 * warp + lane, x, -1.f);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (warp == 0) {
+            if (ok && elect_one()) {
+                bulk_store(image + Lay::w, sm.w, Lay::w_bytes);
+                tma_store_commit();
+                tma_store_wait_all();
+            }
+            __syncwarp();
+        }
+    } else {
+        // T2 over T exp(G) as operands: for Z = scale P T2, then scaled for W2^T = K^T (exp(G_C - G) T2)
+        const float scale = p.scale;
+        constexpr uint32_t id_z = idesc_bf16_f32(128, kChunk, false, true);
+        for (int pass = 0; pass < 2; ++pass) {
+            if (ok)
+                for (int u = tid; u < kChunk * 8; u += kNT) {
+                    const int i = u >> 3, c = 8 * (u & 7);
+                    const uint32_t at = sw128_offset(i, c);
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) *reinterpret_cast<float4 *>(&x[e]) = *reinterpret_cast<const float4 *>(&sm.a[kBack ? 1 : 0][i][c + e]);
+                    const float f = pass ? sm.s.last[i] : 1.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= f;
+                    uint4 h, l;
+                    split8(x, h, l);
+                    *reinterpret_cast<uint4 *>(tp[0] + at) = h;
+                    *reinterpret_cast<uint4 *>(tp[1] + at) = l;
+                }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncthreads();
+            if (warp == 0) {
+                tc_fence_after();
+                if (ok && elect_one()) {
+                    const uint32_t ph = smem_u32(sm.p[0]), pl = smem_u32(sm.p[kBack ? 1 : 0]), th = smem_u32(tp[0]), tlo = smem_u32(tp[1]);
+                    if (pass == 0) {
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_ss(tmem + 128, rows_k(part == 1 ? pl : ph, kk), cols_mn(part == 2 ? tlo : th, kk), id_z, part + kk > 0);
+                    } else {
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_ss(tmem + 192, cols_mn(ka, kk, lbo), cols_mn(part ? tlo : th, kk), id_w2, part + kk > 0);
+                    }
+                    mma_commit(&sm.done);
+                }
+                __syncwarp();
+            }
+            ok = ok && wait_bar_warp(&g_delta_status, &sm.abort, &sm.done, pass);
+            tc_fence_after();
+        }
+        const int half = warp >> 2, row = 32 * (warp & 3) + lane;
+        if (ok && row < 64) {
+            uint32_t a[32];
+            tmem_ld32(tl + 128 + 32 * half, a);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = scale * __uint_as_float(a[8 * c + e]);
+                uint4 h, l;
+                split8(x, h, l);
+                const uint32_t at = sw128_offset(row, 32 * half + 8 * c);
+                *reinterpret_cast<uint4 *>(sm.p[0] + at) = h;
+                *reinterpret_cast<uint4 *>(sm.p[kBack ? 1 : 0] + at) = l;
+            }
+        }
+        for (int which = 0; which < 2; ++which) {
+            if (ok) put_tokens<DK>(tl + (which ? 192 : 64), sm.w, row, 32 * half, which ? 1.f : -1.f);
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncthreads();
+            if (warp == 0) {
+                if (ok && elect_one()) {
+                    if (which == 0) {
+                        bulk_store(image + Lay::z, sm.p[0], kSq);
+                        bulk_store(image + Lay::z + kSq, sm.p[kBack ? 1 : 0], kSq);
+                    }
+                    bulk_store(image + (which ? Lay::w2 : Lay::w), sm.w, Lay::w_bytes);
+                    tma_store_commit();
+                    tma_store_wait_all();
+                }
+                __syncwarp();
+            }
+            __syncthreads();
+        }
+    }
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, kTmem);
+}
+
+// ---------------------------------------------------------------- scan
+// kForward: o and the last state.  kSave: instead of o the state before each chunk, as MMA operand images [d_v rows of
+// 64 d_k columns] of its two parts, and E as images [64 tokens of 64 d_v columns].  kReverse: the same of R and dX, chunks
+// in descending order, dO in the place of V.
+enum Mode { kForward, kSave, kReverse };
+// Warps 0-7: the chain (warp w: value features 32 (w % 4) .. + 31, half w / 4 of the columns);
+// warps 8-11: o, or E's images and dO as an operand; warp 12: products; warp 13: copies.
+constexpr int kChainWarps = 8, kOutWarp = 8, kMmaWarp = 12, kCopyWarp = 13, kThreads = 14 * 32;
+
+constexpr uint32_t state_bytes(int DK, int DV) { return 2u * DK * DV * 2; }  // both parts of a state's image
+constexpr uint32_t rows_bytes(int DV) { return 2u * kChunk * DV * 2; }       // both parts of a chunk's rows
+
+template <int DK, int DV, int kMode> struct ScanSmem {
+    // K (and in reverse Q) are needed late in a chunk: one stage where shared memory is short
+    static constexpr int kKeyStages = kMode == kForward ? 2 : 1;
+    static constexpr bool kOutOverW = kMode != kForward && DK >= DV;  // E's rows are staged where W was
+    static constexpr uint32_t kMats = 2 * kSq + Layout<DK>::w_bytes;
+    uint8_t v[2][DV / 64][kSq];
+    uint8_t mats[2][kMats];  // T or Z, W or W2
+    uint8_t p[kMode == kForward ? 2 : 1][kMode == kForward ? kSq : 1024];
+    uint8_t k[kKeyStages][DK / 64][kSq];
+    uint8_t q[kMode == kSave ? 1 : kKeyStages][kMode == kSave ? 1 : DK / 64][kSq];  // (kSave: not used)
+    union {  // o is staged by one mode, a state by the others
+        uint8_t state[kMode == kForward ? rows_bytes(DV) / 2 : state_bytes(DK, DV)];
+        uint8_t o[rows_bytes(DV) / 2];
+    };
+    uint8_t e[kMode == kForward || kOutOverW ? 16 : rows_bytes(DV)];  // E's rows
+    float scalars[3][3][kChunk];  // beta, write, first; in reverse write, first, back
+    uint64_t full[2];                       // a stage's V and matrices are there (and scalars, but for kForward)
+    uint64_t keys_full[2], rows_read;       // its K, Q, P (and scalars) are; (kOutOverW) the store of E's rows has read them
+    uint64_t s_ready, u_ready, d_ready;     // left operands are in TMEM (256, 256, 128 arrivals)
+    uint64_t e_full, s_full, o_full, o_read;  // products are there; the warps of o have read theirs
+    uint64_t stored;                        // the state's image has been read by its store
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+// TMEM columns: what S^T gains in a chunk; S^T's bf16 parts (low part: later U^T for o); E^T of two chunks (forward: later U^T's parts);
+// forward: (Q S)^T and (P U)^T; otherwise U^T's parts and dO^T's
+template <int DK> struct Columns {
+    static constexpr uint32_t S = 0, parts = DK, e = 2 * DK, qs = e + 128, pu = qs + 64;
+};
+
+template <int DK, int DV, int kMode>
+__device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_v,
+                                          const CUtensorMap &map_o, const Params &p, const float *first_state, float *last_state,
+                                          const uint8_t *images, uint8_t *states, uint8_t *rows, int bh, uint8_t *smem_raw)
+{
+    typedef ScanSmem<DK, DV, kMode> Sm;
+    typedef Columns<DK> Col;
+    typedef Layout<DK> Lay;
+    constexpr bool kKeep = kMode != kForward;
+    constexpr uint32_t kStride = kKeep ? Lay::backward_bytes : Lay::forward_bytes;
+    Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
+    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
+    const int bhk = bh / p.H * p.Hk + bh % p.H / (p.H / p.Hk), chunks = (p.N + kChunk - 1) / kChunk;
+    if (tid == 0) {
+        uint64_t *one[] = {&sm.full[0], &sm.full[1], &sm.keys_full[0], &sm.keys_full[1], &sm.rows_read, &sm.e_full,
+                           &sm.s_full, &sm.o_full, &sm.stored, &sm.drain};
+        for (uint64_t *b : one) mbar_init(b, 1);
+        mbar_init(&sm.s_ready, 32 * kChainWarps);
+        mbar_init(&sm.u_ready, 32 * kChainWarps);
+        mbar_init(&sm.d_ready, 128);
+        mbar_init(&sm.o_read, 128);
+        sm.abort = (smem_u32(smem_raw) & 1023u) == 0 ? 0 : 1;
+        if (sm.abort) atomicOr(&g_delta_status, kStatusTimeout);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&sm.tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t tmem = sm.tmem_base;
+    int *abort_flag = &sm.abort;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_bar_warp(&g_delta_status, abort_flag, bar, parity); };
+    auto chunk_of = [&](int c) { return kMode == kReverse ? chunks - 1 - c : c; };
+    bool ok = !aborted(abort_flag);
+
+    if (warp == kCopyWarp) {
+        fence_proxy_async_global();  // the images were written by plain stores
+        constexpr uint32_t kKeyBytes = (kMode == kSave ? 1 : 2) * (DK / 64) * kSq + (kKeep ? 0 : kSq + kScanScalars);
+        int c = 0;
+        for (; ok && c < chunks; ++c) {
+            const int st = c & 1, x = chunk_of(c);
+            const uint8_t *img = images + ((size_t)bh * chunks + x) * kStride;
+            // V and the matrices of chunk c - 2 end with its E (where E's rows are staged over W, with their store)
+            if (c >= 2 && !(ok = wait(Sm::kOutOverW ? &sm.rows_read : &sm.e_full, (uint32_t)c & 1u))) break;
+            if (__any_sync(0xffffffffu, aborted(abort_flag))) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&sm.full[st], DV / 64 * kSq + Sm::kMats + (kKeep ? kScanScalars : 0));
+                if (kKeep) bulk_load(sm.scalars[c % 3], img + (kMode == kReverse ? kChunk * 4 : 0), kScanScalars, &sm.full[st]);
+                bulk_load(sm.mats[st], img + (kMode == kReverse ? Lay::z : Lay::t), Sm::kMats, &sm.full[st]);
+                for (int b = 0; b < DV / 64; ++b) tma_load_3d(sm.v[st][b], &map_v, &sm.full[st], 64 * b, x * kChunk, bh);
+            }
+            __syncwarp();
+            // K, Q and P end with the chunk's last product
+            const int ks = kKeep ? 0 : st, back = kKeep ? 1 : 2;
+            if (c >= back && !(ok = wait(kKeep ? &sm.s_full : &sm.o_full, (uint32_t)(c - back) & 1u))) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&sm.keys_full[ks], kKeyBytes);
+                for (int b = 0; b < DK / 64; ++b) {
+                    if (kMode != kSave) tma_load_3d(sm.q[ks][b], &map_q, &sm.keys_full[ks], 64 * b, x * kChunk, bhk);
+                    tma_load_3d(sm.k[ks][b], &map_k, &sm.keys_full[ks], 64 * b, x * kChunk, bhk);
+                }
+                if (!kKeep) bulk_load(sm.p[st], img + Lay::p, kSq, &sm.keys_full[ks]);
+                if (!kKeep) bulk_load(sm.scalars[c % 3], img, kScanScalars, &sm.keys_full[ks]);
+            }
+            __syncwarp();
+        }
+        if (c < chunks && c > 0) let_copies_land();
+    } else if (warp == kMmaWarp) {
+        // The loop's control and operands stay in uniform registers (an MMA issued from elsewhere costs more to issue
+        // than to run): waits return nothing here, and an abort is seen at the head of the next chunk.
+        constexpr uint32_t id = idesc_bf16_f32(128, kChunk, false, false), id_s = idesc_bf16_f32(128, DK, false, true);
+        constexpr uint32_t id_v = idesc_bf16_f32(128, kChunk, true, kMode == kReverse);
+        constexpr uint32_t kBox = kSq >> 4;  // descriptors count 16 bytes
+        const uint64_t dv = cols_mn(smem_u32(sm.v[0][0]), 0, DV == 128 ? kSq : 0);
+        const uint64_t dt = kMode == kReverse ? cols_mn(smem_u32(sm.mats[0]), 0) : rows_k(smem_u32(sm.mats[0]), 0);
+        const uint64_t dw = rows_k(smem_u32(sm.mats[0]) + 2 * kSq, 0), dp = rows_k(smem_u32(sm.p[0]), 0);
+        const uint64_t dk = cols_mn(smem_u32(sm.k[0][0]), 0), dq = rows_k(smem_u32(sm.q[0][0]), 0), dqm = cols_mn(smem_u32(sm.q[0][0]), 0);
+        auto wait = [&](uint64_t *bar, uint32_t parity) { wait_or_abort(&g_delta_status, abort_flag, bar, parity); };
+        // E^T = V^T T^T (in reverse dO^T Z), ahead of the state's part
+        auto from_values = [&](int c) {
+            const uint32_t st = (uint32_t)c & 1u;
+            wait(&sm.full[st], (uint32_t)(c >> 1) & 1u);
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t a = dv + st * (DV / 64 * kBox), b = dt + st * (Sm::kMats >> 4);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ss(tmem + Col::e + 64 * st, a + kk * (2048 >> 4), b + part * kBox + kk * (kMode == kReverse ? 2048 >> 4 : 2),
+                               id_v, part + kk > 0);
+            }
+            __syncwarp();
+        };
+        if (chunks > 0 && !__any_sync(0xffffffffu, aborted(abort_flag))) from_values(0);
+        for (int c = 0; c < chunks; ++c) {
+            if (__any_sync(0xffffffffu, aborted(abort_flag))) break;
+            const uint32_t st = (uint32_t)c & 1u, ph = st;
+            const uint32_t tE = tmem + Col::e + 64 * st, tU = kKeep ? tmem + Col::qs : tE;
+            wait(&sm.s_ready, ph);
+            tc_fence_after();
+            if (elect_one()) {  // E^T += S^T W^T: high high, low high, high low
+                const uint64_t b = dw + st * (Sm::kMats >> 4);
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < DK / 16; ++kk)
+                        mma_ts(tE, tmem + Col::parts + (part == 1) * (DK / 2) + kk * 8,
+                               b + (part == 2) * (DK / 64) * kBox + (kk >> 2) * kBox + (kk & 3) * 2, id, 1);
+                mma_commit(&sm.e_full);
+            }
+            __syncwarp();
+            if (c > 0) wait(&sm.o_read, ph ^ 1u);
+            if (kKeep)
+                wait(&sm.keys_full[0], ph);
+            else
+                wait(&sm.keys_full[st], (uint32_t)(c >> 1) & 1u);
+            if (!kKeep) {
+                tc_fence_after();
+                if (elect_one()) {  // (Q S)^T
+                    const uint64_t b = dq + st * (DK / 64 * kBox);
+#pragma unroll
+                    for (int kk = 0; kk < DK / 16; ++kk)
+                        mma_ts(tmem + Col::qs, tmem + Col::parts + kk * 8, b + (kk >> 2) * kBox + (kk & 3) * 2, id, kk > 0);
+                }
+                __syncwarp();
+            }
+            if (kMode == kReverse) wait(&sm.d_ready, ph);
+            wait(&sm.u_ready, ph);
+            tc_fence_after();
+            if (elect_one()) {  // what the state gains, U^T K (in reverse also dO^T Q), both parts; (P U)^T
+                const uint64_t b = dk + (kKeep ? 0 : st * (DK / 64 * kBox));
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        mma_ts(tmem + Col::S, tU + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, b + kk * (2048 >> 4), id_s, part + kk > 0);
+                        if (kMode == kReverse)
+                            mma_ts(tmem + Col::S, tmem + Col::pu + part * 32 + kk * 8, dqm + kk * (2048 >> 4), id_s, 1);
+                    }
+                mma_commit(&sm.s_full);
+                if (!kKeep) {
+                    const uint64_t bp = dp + st * kBox;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ts(tmem + Col::pu, tmem + Col::parts + DK / 2 + kk * 8, bp + kk * 2, id, kk > 0);
+                    mma_commit(&sm.o_full);
+                }
+            }
+            __syncwarp();
+            if (c + 1 < chunks) from_values(c + 1);
+        }
+        if (elect_one()) {
+            mma_commit(&sm.drain);  // every MMA issued completes before TMEM is freed
+            drain(&sm.drain, 0);
+        }
+        __syncwarp();
+    } else if (warp < kChainWarps) {
+        const int half = warp >> 2, f = 32 * (warp & 3) + lane;  // value feature
+        const bool live = f < DV;
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t tS = tl + Col::S + half * (DK / 2), tP = tl + Col::parts + half * (DK / 4);
+        const size_t state = (size_t)bh * DK * DV + (size_t)half * (DK / 2) * DV + f;
+        // 16 state values, of key features half DK / 2 + x .., as two parts: to TMEM and to the image that is kept
+        auto put_parts = [&](int x, const float *s) {
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) split2(s[2 * e], s[2 * e + 1], hi[e], lo[e]);
+            tmem_st8(tP + x / 2, hi);
+            tmem_st8(tP + DK / 2 + x / 2, lo);
+            if (kKeep && live) {
+                const int k0 = half * (DK / 2) + x;
+                uint8_t *at = sm.state + (k0 >> 6) * (DV * 128);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t off = sw128_offset(f, (k0 & 63) + 8 * e);
+                    *reinterpret_cast<uint4 *>(at + off) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+                    *reinterpret_cast<uint4 *>(at + state_bytes(DK, DV) / 2 + off) = make_uint4(lo[4 * e], lo[4 * e + 1], lo[4 * e + 2], lo[4 * e + 3]);
+                }
+            }
+        };
+        float s[DK / 2];
+#pragma unroll
+        for (int e = 0; e < DK / 2; ++e) s[e] = first_state && live ? first_state[state + (size_t)e * DV] : 0.f;
+        for (int c = 0; ok && c < chunks; ++c) {
+            const int st = c & 1;
+            const uint32_t ph = (uint32_t)c & 1u;
+            if (kKeep && c > 0 && !(ok = wait(&sm.stored, ph ^ 1u))) break;
+            if (!kKeep && c > 0 && !(ok = wait(&sm.o_full, ph ^ 1u))) break;  // P U has read U
+#pragma unroll
+            for (int x = 0; x < DK / 2; x += 16) put_parts(x, s + x);
+            if (kKeep) fence_proxy_async_smem();
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&sm.s_ready);
+            if (!(ok = wait(kKeep ? &sm.full[st] : &sm.keys_full[st], (uint32_t)(c >> 1) & 1u))) break;
+            const float (*scalars)[kChunk] = sm.scalars[c % 3];
+            const float whole = scalars[kMode == kReverse ? 1 : 2][kChunk - 1];
+            if (!(ok = wait(&sm.e_full, ph))) break;
+            tc_fence_after();
+            const uint32_t tE = tl + Col::e + 64 * st + 32 * half;
+            uint32_t a[32];
+            tmem_ld32(tE, a);
+            tmem_ld_wait();
+            {
+                const float *mul = scalars[kMode == kReverse ? 2 : 1] + 32 * half, *beta = scalars[0] + 32 * half;
+                const uint32_t tU = kKeep ? tl + Col::qs + 32 * half : tE;
+#pragma unroll
+                for (int y = 0; y < 32; y += 16) {
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const float4 w = *reinterpret_cast<const float4 *>(mul + y + e);
+                        split2(w.x * __uint_as_float(a[y + e]), w.y * __uint_as_float(a[y + e + 1]), hi[e / 2], lo[e / 2]);
+                        split2(w.z * __uint_as_float(a[y + e + 2]), w.w * __uint_as_float(a[y + e + 3]), hi[e / 2 + 1], lo[e / 2 + 1]);
+                    }
+                    tmem_st8(tU + y / 2, hi);
+                    tmem_st8(tU + 16 + y / 2, lo);
+                }
+                if (!kKeep) {  // U for o, in one part
+                    uint32_t u[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 w = *reinterpret_cast<const float4 *>(beta + e);
+                        u[e / 2] = pack_bf16(w.x * __uint_as_float(a[e]), w.y * __uint_as_float(a[e + 1]));
+                        u[e / 2 + 1] = pack_bf16(w.z * __uint_as_float(a[e + 2]), w.w * __uint_as_float(a[e + 3]));
+                    }
+                    tmem_st16(tl + Col::parts + DK / 2 + 16 * half, u);
+                }
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&sm.u_ready);
+            if (!(ok = wait(&sm.s_full, ph))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < DK / 2; x += 32) {
+                tmem_ld32(tS + x, a);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s[x + e] = fmaf(whole, s[x + e], __uint_as_float(a[e]));
+            }
+        }
+        if (ok && last_state && live)
+#pragma unroll
+            for (int e = 0; e < DK / 2; ++e) last_state[state + (size_t)e * DV] = s[e];
+    } else if (warp < kMmaWarp) {
+        const int f = 32 * (warp & 3) + lane;
+        const bool live = f < DV;
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        uint32_t at[8];  // (row e, feature f) of a tile of 64-column boxes
+#pragma unroll
+        for (int e = 0; e < 8; ++e) at[e] = ((f & 127) >> 6) * kSq + sw128_offset(e, f & 63);
+        for (int c = 0; ok && c < chunks; ++c) {
+            const int st = c & 1, x = chunk_of(c);
+            const uint32_t ph = (uint32_t)c & 1u;
+            uint8_t *out = !kKeep ? sm.o : Sm::kOutOverW ? sm.mats[st] + 2 * kSq : sm.e;
+            if (kMode == kReverse) {  // scale exp(G) dO as a left operand, once the last state product has read it
+                if (!(ok = wait(&sm.full[st], (uint32_t)(c >> 1) & 1u))) break;
+                if (c > 0 && !(ok = wait(&sm.s_full, ph ^ 1u))) break;
+                const uint8_t *v = sm.v[st][0];
+#pragma unroll
+                for (int y = 0; y < kChunk; y += 32) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const uint8_t *r = v + (y + e) / 8 * 1024;
+                        const float d0 = live ? bf16_at(r + at[e & 7]) : 0.f, d1 = live ? bf16_at(r + at[(e + 1) & 7]) : 0.f;
+                        const float2 w = *reinterpret_cast<const float2 *>(&sm.scalars[c % 3][1][y + e]);
+                        split2(p.scale * w.x * d0, p.scale * w.y * d1, hi[e / 2], lo[e / 2]);
+                    }
+                    tmem_st16(tl + Col::pu + y / 2, hi);
+                    tmem_st16(tl + Col::pu + 32 + y / 2, lo);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&sm.d_ready);
+            }
+            if (kKeep) {  // the state before the chunk, once its image is written
+                if (!(ok = wait(&sm.s_ready, ph))) break;
+                if (warp == kOutWarp && lane == 0) {
+                    bulk_store(states + ((size_t)bh * chunks + x) * state_bytes(DK, DV), sm.state, state_bytes(DK, DV));
+                    tma_store_commit();
+                    tma_store_wait_read_all();
+                    mbar_arrive(&sm.stored);
+                }
+                __syncwarp();
+                if (!(ok = wait(&sm.e_full, ph))) break;
+                tc_fence_after();
+                if (!Sm::kOutOverW && c > 0) named_bar_sync(1, 128);  // (the store above waited for the last rows' too)
+#pragma unroll
+                for (int y = 0; y < kChunk; y += 32) {
+                    uint32_t a[32];
+                    tmem_ld32(tl + Col::e + 64 * st + y, a);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        uint32_t hi, lo;
+                        split2(__uint_as_float(a[e]), __uint_as_float(a[e + 1]), hi, lo);
+                        uint8_t *to = out + (y + e) / 8 * 1024;
+                        if (live) {
+                            *reinterpret_cast<uint16_t *>(to + at[e & 7]) = (uint16_t)hi;
+                            *reinterpret_cast<uint16_t *>(to + at[(e + 1) & 7]) = (uint16_t)(hi >> 16);
+                            *reinterpret_cast<uint16_t *>(to + rows_bytes(DV) / 2 + at[e & 7]) = (uint16_t)lo;
+                            *reinterpret_cast<uint16_t *>(to + rows_bytes(DV) / 2 + at[(e + 1) & 7]) = (uint16_t)(lo >> 16);
+                        }
+                    }
+                }
+                tc_fence_before();
+                fence_proxy_async_smem();
+                mbar_arrive(&sm.o_read);
+                named_bar_sync(1, 128);
+                if (warp == kOutWarp && lane == 0) {
+                    bulk_store(rows + ((size_t)bh * chunks + x) * rows_bytes(DV), out, rows_bytes(DV));
+                    tma_store_commit();
+                    if (Sm::kOutOverW) {
+                        tma_store_wait_read_all();
+                        mbar_arrive(&sm.rows_read);
+                    }
+                }
+                __syncwarp();
+            } else {
+                if (!(ok = wait(&sm.o_full, ph))) break;
+                tc_fence_after();
+                if (c > 0) {  // the last store has read the tile
+                    if (warp == kOutWarp && lane == 0) tma_store_wait_read_all();
+                    __syncwarp();
+                    named_bar_sync(1, 128);
+                }
+#pragma unroll
+                for (int y = 0; y < kChunk; y += 32) {
+                    uint32_t a[32], b[32];
+                    tmem_ld32(tl + Col::qs + y, a);
+                    tmem_ld32(tl + Col::pu + y, b);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float o = p.scale * fmaf(sm.scalars[c % 3][2][y + e], __uint_as_float(a[e]), __uint_as_float(b[e]));
+                        if (live) *reinterpret_cast<__nv_bfloat16 *>(out + (y + e) / 8 * 1024 + at[e & 7]) = __float2bfloat16_rn(o);
+                    }
+                }
+                tc_fence_before();
+                fence_proxy_async_smem();
+                mbar_arrive(&sm.o_read);
+                named_bar_sync(1, 128);
+                if (warp == kOutWarp && lane == 0) {
+                    for (int b = 0; b < DV / 64; ++b) tma_store_3d(&map_o, out + b * kSq, 64 * b, x * kChunk, bh);
+                    tma_store_commit();
+                }
+                __syncwarp();
+            }
+        }
+        if (warp == kOutWarp && lane == 0) tma_store_wait_all();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Prepares the chunks' images, for the forward pass or (kBack) for the backward.
+template <int DK, bool kBack>
+la_status prepare(const DeltaProblem &p, const Params &prm, uint8_t *images, CUtensorMap *mq, CUtensorMap *mk)
+{
+    typedef PrepSmem<DK, kBack> Sm;
+    la_status st = make_map(mq, p.q, p.B * p.Hk, p.N, DK, kChunk);
+    if (st == LA_OK) st = make_map(mk, p.k, p.B * p.Hk, p.N, DK, kChunk);
+    if (st == LA_OK) st = ensure_smem((const void *)delta_prepare<DK, kBack>, (int)sizeof(Sm));
+    if (st != LA_OK) return st;
+    g_launched = true;
+    count_launches();
+    return launch_dependent(delta_prepare<DK, kBack>, (unsigned)(p.B * p.H * ceil_div(p.N, kChunk)), kBack ? 256 : 128, (int)sizeof(Sm),
+                            p.stream, *mq, *mk, prm, images);
+}
+
+}  // namespace
+}  // namespace delta
+}  // namespace la
