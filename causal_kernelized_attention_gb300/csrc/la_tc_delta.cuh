@@ -28,7 +28,8 @@ constexpr uint64_t kDrainNs = 100000000ull;
 // The scalars of a chunk, by token; a scan loads three of the first four.
 struct Scalars {
     float beta[kChunk], write[kChunk], first[kChunk], back[kChunk];  // beta, beta exp(G_C - G), exp(G), -beta exp(G)
-    float last[kChunk], hi[kChunk], lo[kChunk], spare[kChunk];       // exp(G_C - G), G as two floats
+    // exp(G_C - G); G log2(e) as two floats (differences of the pairs carry no more than their own rounding)
+    float last[kChunk], hi[kChunk], lo[kChunk], spare[kChunk];
 };
 static_assert(sizeof(Scalars) == 2048, "");
 constexpr uint32_t kScanScalars = 3 * kChunk * 4;
@@ -88,6 +89,40 @@ __device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t 
                  : "memory");
 }
 __device__ __forceinline__ uint32_t ld_shared32(const void *p) { return *reinterpret_cast<const uint32_t *>(p); }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// D_ij = exp(G_i - G_j) of a row's 2 columns: hi, lo (G_i log2(e)) twice, and the columns' as they are.
+__device__ __forceinline__ uint64_t decay2(uint64_t hi, uint64_t lo, float2 hj, float2 lj)
+{
+    float x, y;
+    unpair(add2(add2(hi, pair(-hj.x, -hj.y)), add2(lo, pair(-lj.x, -lj.y))), x, y);
+    return pair(ex2(x), ex2(y));
+}
 
 // Descriptors of a 64-row tile: K-major (rows M or N), k step kk; 64 columns a box of `box` bytes.
 __device__ __forceinline__ uint64_t rows_k(uint32_t tile, int kk, uint32_t box = kSq)

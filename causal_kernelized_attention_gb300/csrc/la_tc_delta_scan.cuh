@@ -89,36 +89,40 @@ __device__ __forceinline__ void invert(Square &a, int t, int bar)
             named_bar_sync(bar, 128);
         }
     }
-    {
-        const int r = 2 * (t >> 3), c = 4 * (t & 7);
-#pragma unroll
-        for (int step = 0; step < 2; ++step) {
-            const int k0 = step ? 32 : 0;
-            float4 y[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll
-            for (int k = 0; k < 32; k += 4) {
+    {   // a warp takes 8 columns of A10 T00, whose rows k before them are 0, then 8 rows of T11, 0 behind them
+        const int w = t >> 5, l = t & 31;
+        auto product = [&](int r, int c, int k0, int from, int to, float4 (&y)[2]) {
+            y[0] = y[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int k = from; k < to; k += 4) {
                 float4 z[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) z[e] = *reinterpret_cast<const float4 *>(&a[k0 + k + e][c]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const float4 l = *reinterpret_cast<const float4 *>(&a[32 + r + u][k0 + k]);
-                    const float w[4] = {l.x, l.y, l.z, l.w};
+                    const float4 q = *reinterpret_cast<const float4 *>(&a[32 + r + u][k0 + k]);
+                    const float f[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        y[u].x = fmaf(w[e], z[e].x, y[u].x), y[u].y = fmaf(w[e], z[e].y, y[u].y);
-                        y[u].z = fmaf(w[e], z[e].z, y[u].z), y[u].w = fmaf(w[e], z[e].w, y[u].w);
+                        y[u].x = fmaf(f[e], z[e].x, y[u].x), y[u].y = fmaf(f[e], z[e].y, y[u].y);
+                        y[u].z = fmaf(f[e], z[e].z, y[u].z), y[u].w = fmaf(f[e], z[e].w, y[u].w);
                     }
                 }
             }
-            named_bar_sync(bar, 128);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (step) y[u] = make_float4(-y[u].x, -y[u].y, -y[u].z, -y[u].w);
-                *reinterpret_cast<float4 *>(&a[32 + r + u][c]) = y[u];
-            }
-            named_bar_sync(bar, 128);
-        }
+        };
+        float4 y[2];
+        int r = 2 * (l >> 1), c = 8 * w + 4 * (l & 1);
+        product(r, c, 0, 8 * w, 32, y);
+        named_bar_sync(bar, 128);
+        *reinterpret_cast<float4 *>(&a[32 + r][c]) = y[0];
+        *reinterpret_cast<float4 *>(&a[33 + r][c]) = y[1];
+        named_bar_sync(bar, 128);
+        r = 8 * w + 2 * (l >> 3), c = 4 * (l & 7);
+        product(r, c, 32, 0, 8 * w + 8, y);
+        named_bar_sync(bar, 128);
+        *reinterpret_cast<float4 *>(&a[32 + r][c]) = make_float4(-y[0].x, -y[0].y, -y[0].z, -y[0].w);
+        *reinterpret_cast<float4 *>(&a[33 + r][c]) = make_float4(-y[1].x, -y[1].y, -y[1].z, -y[1].w);
+        named_bar_sync(bar, 128);
     }
 }
 
@@ -131,22 +135,25 @@ __device__ __forceinline__ void split8(const float (&x)[8], uint4 &hi, uint4 &lo
     split2(x[6], x[7], hi.w, lo.w);
 }
 
-// 32 columns x0 .. of TMEM (lane f: key feature; column: token) to both parts of an image [token][d_k] in shared memory.
-template <int DK> __device__ __forceinline__ void put_tokens(uint32_t taddr, uint8_t (*w)[DK / 64][kSq], int f, int x0, float sign)
+// Columns x0 .. x1 of a row (token i: its TMEM lane) to both parts of an image [token][d_k] in shared memory.
+template <int DK> __device__ __forceinline__ void put_row(uint32_t taddr, uint8_t (*w)[DK / 64][kSq], int i, int x0, int x1)
 {
-    uint32_t a[32];
-    tmem_ld32(taddr + x0, a);
-    tmem_ld_wait();
-    if (f >= DK) return;
+#pragma unroll 1
+    for (int x = x0; x < x1; x += 32) {
+        uint32_t a[32];
+        tmem_ld32(taddr + x, a);
+        tmem_ld_wait();
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-        uint32_t hi, lo;
-        split2(sign * __uint_as_float(a[e]), sign * __uint_as_float(a[e + 1]), hi, lo);
-        const uint32_t p = sw128_offset(x0 + e, f & 63), q = sw128_offset(x0 + e + 1, f & 63);
-        *reinterpret_cast<uint16_t *>(w[0][f >> 6] + p) = (uint16_t)hi;
-        *reinterpret_cast<uint16_t *>(w[0][f >> 6] + q) = (uint16_t)(hi >> 16);
-        *reinterpret_cast<uint16_t *>(w[1][f >> 6] + p) = (uint16_t)lo;
-        *reinterpret_cast<uint16_t *>(w[1][f >> 6] + q) = (uint16_t)(lo >> 16);
+        for (int e = 0; e < 32; e += 8) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = __uint_as_float(a[e + u]);
+            uint4 hi, lo;
+            split8(v, hi, lo);
+            const uint32_t at = sw128_offset(i, (x + e) & 63);
+            *reinterpret_cast<uint4 *>(w[0][x >> 6] + at) = hi;
+            *reinterpret_cast<uint4 *>(w[1][x >> 6] + at) = lo;
+        }
     }
 }
 
@@ -158,7 +165,7 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     typedef PrepSmem<DK, kBack> Sm;
     typedef Layout<DK> Lay;
     constexpr int kNT = kBack ? 256 : 128;
-    constexpr uint32_t kTmem = kBack ? 256 : 128;
+    constexpr uint32_t kTmem = kBack ? 256 : DK;  // scores, then W over them; Z, then W2 over it
     Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
     const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     const int chunks = (p.N + kChunk - 1) / kChunk, bh = blockIdx.x / chunks, chunk = blockIdx.x % chunks, t0 = chunk * kChunk;
@@ -207,8 +214,9 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         const double half = sm.G[31], G = sm.G[tid] + (tid >= 32 ? half : 0.0), end = sm.G[63] + half;
         const float first = expf((float)G), last = expf((float)(end - G));
         Scalars &s = sm.s;
-        s.hi[tid] = (float)G;
-        s.lo[tid] = (float)(G - (double)(float)G);
+        const double G2 = G * 1.4426950408889634074;
+        s.hi[tid] = (float)G2;
+        s.lo[tid] = (float)(G2 - (double)(float)G2);
         s.first[tid] = first;
         s.last[tid] = last;
         s.beta[tid] = gate;
@@ -239,20 +247,28 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     if (ok) {
         for (int i = tid; i < (int)sizeof(Scalars) / 16; i += kNT) reinterpret_cast<uint4 *>(image)[i] = reinterpret_cast<uint4 *>(&sm.s)[i];
         const int row = 32 * (warp & 3) + lane, i = row & 63;
-        const float hi = sm.s.hi[i], lo = sm.s.lo[i], bi = sm.s.beta[i];
-        constexpr float kLog2e = 1.4426950408889634f;
+        const uint64_t hi = pair(sm.s.hi[i], sm.s.hi[i]), lo = pair(sm.s.lo[i], sm.s.lo[i]);
+        const float bi = sm.s.beta[i];
 #pragma unroll 1
         for (int j0 = kBack ? 32 * (warp >> 2) : 0; j0 < kChunk; j0 += kBack ? kChunk : 32) {
-            uint32_t s[32];
-            tmem_ld32(tl + j0, s);
-            tmem_ld_wait();
             float d[32];
+            if (j0 > 0 && (warp & 1) == 0) {  // above the diagonal
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const int j = j0 + e;
-                float w;
-                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(kLog2e * ((hi - sm.s.hi[j]) + (lo - sm.s.lo[j]))));
-                d[e] = j <= i ? __uint_as_float(s[e]) * w : 0.f;
+                for (int e = 0; e < 32; ++e) d[e] = 0.f;
+            } else {
+                uint32_t s[32];
+                tmem_ld32(tl + j0, s);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const uint64_t w = decay2(hi, lo, *reinterpret_cast<const float2 *>(&sm.s.hi[j0 + e]), *reinterpret_cast<const float2 *>(&sm.s.lo[j0 + e]));
+                    unpair(mul2(w, pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1]))), d[e], d[e + 1]);
+                }
+                if (j0 == 32 * (warp & 1)) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (e > lane) d[e] = 0.f;
+                }
             }
             if (row < 64) {
 #pragma unroll
@@ -273,7 +289,7 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 for (int e = 0; e < 32; e += 4) {
                     const int j = j0 + e;
                     const float4 b = *reinterpret_cast<const float4 *>(&sm.s.beta[j]);
-                    const float4 n = make_float4(j < i ? d[e] : 0.f, j + 1 < i ? d[e + 1] : 0.f, j + 2 < i ? d[e + 2] : 0.f, j + 3 < i ? d[e + 3] : 0.f);
+                    const float4 n = make_float4(j == i ? 0.f : d[e], j + 1 == i ? 0.f : d[e + 1], j + 2 == i ? 0.f : d[e + 2], j + 3 == i ? 0.f : d[e + 3]);
                     *reinterpret_cast<float4 *>(&sm.a[0][i][j]) = make_float4(n.x * b.x, n.y * b.y, n.z * b.z, n.w * b.w);
                     if (kBack) *reinterpret_cast<float4 *>(&sm.a[kBack ? 1 : 0][i][j]) = make_float4(bi * n.x, bi * n.y, bi * n.z, bi * n.w);
                 }
@@ -287,7 +303,7 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     else
         invert(sm.a[kBack ? 1 : 0], tid & 127, 2);
     __syncthreads();
-    // T to global memory, and T exp(G) over the rows of Q; then (kBack) T2 and exp(G_C - G) T2
+    // T to global memory, and -T exp(G) over the rows of Q
     uint8_t *tp[2] = {sm.qk[0], DK == 64 ? sm.extra : sm.qk[DK / 64 - 1]};
     for (int u = tid; u < kChunk * 8; u += kNT) {
         const int i = u >> 3, c = 8 * (u & 7);
@@ -300,7 +316,7 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         *reinterpret_cast<uint4 *>(image + Lay::t + at) = h;
         *reinterpret_cast<uint4 *>(image + Lay::t + kSq + at) = l;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[e] * sm.s.first[c + e];
+        for (int e = 0; e < 8; ++e) y[e] = x[e] * -sm.s.first[c + e];
         split8(y, h, l);
         *reinterpret_cast<uint4 *>(tp[0] + at) = h;
         *reinterpret_cast<uint4 *>(tp[1] + at) = l;
@@ -308,40 +324,27 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
-    constexpr uint32_t id_w = idesc_bf16_f32(128, kChunk, true, false), id_w2 = idesc_bf16_f32(128, kChunk, true, true);
-    constexpr uint32_t lbo = DK == 128 ? 2 * kSq : 0;
-    const uint32_t ka = smem_u32(sm.qk[0]) + kSq;
+    const int row = 32 * (warp & 3) + lane, half = warp >> 2;
+    // W = -T exp(G) K: rows 0-63 of 128 (the rest of the left operand is whatever follows it)
+    constexpr uint32_t id_w = idesc_bf16_f32(128, DK, false, true), id_w2 = idesc_bf16_f32(128, DK, true, true);
+    constexpr uint32_t tW = 0, tZ = 128, tW2 = 128;
+    const uint32_t ka = smem_u32(sm.qk[0]) + kSq, th = smem_u32(tp[0]), tlo = smem_u32(tp[1]);
     if (warp == 0) {
         tc_fence_after();
-        if (ok && elect_one()) {  // W^T = K^T (T exp(G))^T
+        if (ok && elect_one()) {
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ss(tmem + 64, cols_mn(ka, kk, lbo), rows_k(smem_u32(tp[part]), kk), id_w, part + kk > 0);
+                    mma_ss(tmem + tW, rows_k(part ? tlo : th, kk), cols_mn(ka, kk, 2 * kSq), id_w, part + kk > 0);
             mma_commit(&sm.done);
         }
         __syncwarp();
     }
     ok = ok && wait_bar_warp(&g_delta_status, &sm.abort, &sm.done, 1);
     tc_fence_after();
-    if (!kBack) {
-        if (ok)
-            for (int x = 0; x < kChunk; x += 32) put_tokens<DK>(tl + 64, sm.w, 32 * warp + lane, x, -1.f);
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        if (warp == 0) {
-            if (ok && elect_one()) {
-                bulk_store(image + Lay::w, sm.w, Lay::w_bytes);
-                tma_store_commit();
-                tma_store_wait_all();
-            }
-            __syncwarp();
-        }
-    } else {
-        // T2 over T exp(G) as operands: for Z = scale P T2, then scaled for W2^T = K^T (exp(G_C - G) T2)
-        const float scale = p.scale;
+    if (kBack) {
+        // T2 over T exp(G) as an operand: Z = scale P T2; then scaled, W2 = (exp(G_C - G) T2)^T K
         constexpr uint32_t id_z = idesc_bf16_f32(128, kChunk, false, true);
         for (int pass = 0; pass < 2; ++pass) {
             if (ok)
@@ -365,19 +368,19 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             if (warp == 0) {
                 tc_fence_after();
                 if (ok && elect_one()) {
-                    const uint32_t ph = smem_u32(sm.p[0]), pl = smem_u32(sm.p[kBack ? 1 : 0]), th = smem_u32(tp[0]), tlo = smem_u32(tp[1]);
+                    const uint32_t ph = smem_u32(sm.p[0]), pl = smem_u32(sm.p[kBack ? 1 : 0]);
                     if (pass == 0) {
 #pragma unroll
                         for (int part = 0; part < 3; ++part)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                mma_ss(tmem + 128, rows_k(part == 1 ? pl : ph, kk), cols_mn(part == 2 ? tlo : th, kk), id_z, part + kk > 0);
+                                mma_ss(tmem + tZ, rows_k(part == 1 ? pl : ph, kk), cols_mn(part == 2 ? tlo : th, kk), id_z, part + kk > 0);
                     } else {
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                mma_ss(tmem + 192, cols_mn(ka, kk, lbo), cols_mn(part ? tlo : th, kk), id_w2, part + kk > 0);
+                                mma_ss(tmem + tW2, cols_mn(part ? tlo : th, kk, 0), cols_mn(ka, kk, 2 * kSq), id_w2, part + kk > 0);
                     }
                     mma_commit(&sm.done);
                 }
@@ -385,43 +388,45 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             }
             ok = ok && wait_bar_warp(&g_delta_status, &sm.abort, &sm.done, pass);
             tc_fence_after();
-        }
-        const int half = warp >> 2, row = 32 * (warp & 3) + lane;
-        if (ok && row < 64) {
-            uint32_t a[32];
-            tmem_ld32(tl + 128 + 32 * half, a);
-            tmem_ld_wait();
+            if (pass == 0 && ok && row < 64) {
+                uint32_t a[32];
+                tmem_ld32(tl + tZ + 32 * half, a);
+                tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float x[8];
+                for (int c = 0; c < 4; ++c) {
+                    float x[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = scale * __uint_as_float(a[8 * c + e]);
-                uint4 h, l;
-                split8(x, h, l);
-                const uint32_t at = sw128_offset(row, 32 * half + 8 * c);
-                *reinterpret_cast<uint4 *>(sm.p[0] + at) = h;
-                *reinterpret_cast<uint4 *>(sm.p[kBack ? 1 : 0] + at) = l;
-            }
-        }
-        for (int which = 0; which < 2; ++which) {
-            if (ok) put_tokens<DK>(tl + (which ? 192 : 64), sm.w, row, 32 * half, which ? 1.f : -1.f);
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncthreads();
-            if (warp == 0) {
-                if (ok && elect_one()) {
-                    if (which == 0) {
-                        bulk_store(image + Lay::z, sm.p[0], kSq);
-                        bulk_store(image + Lay::z + kSq, sm.p[kBack ? 1 : 0], kSq);
-                    }
-                    bulk_store(image + (which ? Lay::w2 : Lay::w), sm.w, Lay::w_bytes);
-                    tma_store_commit();
-                    tma_store_wait_all();
+                    for (int e = 0; e < 8; ++e) x[e] = p.scale * __uint_as_float(a[8 * c + e]);
+                    uint4 h, l;
+                    split8(x, h, l);
+                    const uint32_t at = sw128_offset(row, 32 * half + 8 * c);
+                    *reinterpret_cast<uint4 *>(sm.p[0] + at) = h;
+                    *reinterpret_cast<uint4 *>(sm.p[kBack ? 1 : 0] + at) = l;
                 }
-                __syncwarp();
             }
-            __syncthreads();
         }
+    }
+    for (int which = 0; which < (kBack ? 2 : 1); ++which) {
+        if (ok && row < 64) put_row<DK>(tl + (which ? tW2 : tW), sm.w, row, half * (DK / 2), kBack ? (half + 1) * (DK / 2) : DK);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        if (warp == 0) {
+            if (ok && elect_one()) {
+                if (kBack && which == 0) {
+                    bulk_store(image + Lay::z, sm.p[0], kSq);
+                    bulk_store(image + Lay::z + kSq, sm.p[kBack ? 1 : 0], kSq);
+                }
+                bulk_store(image + (which ? Lay::w2 : Lay::w), sm.w, Lay::w_bytes);
+                tma_store_commit();
+                if (kBack && which == 0)
+                    tma_store_wait_read_all();
+                else
+                    tma_store_wait_all();
+            }
+            __syncwarp();
+        }
+        if (kBack && which == 0) __syncthreads();
     }
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, kTmem);
@@ -432,9 +437,11 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 // 64 d_k columns] of its two parts, and E as images [64 tokens of 64 d_v columns].  kReverse: the same of R and dX, chunks
 // in descending order, dO in the place of V.
 enum Mode { kForward, kSave, kReverse };
-// Warps 0-7: the chain (warp w: value features 32 (w % 4) .. + 31, half w / 4 of the columns);
-// warps 8-11: o, or E's images and dO as an operand; warp 12: products; warp 13: copies.
-constexpr int kChainWarps = 8, kOutWarp = 8, kMmaWarp = 12, kCopyWarp = 13, kThreads = 14 * 32;
+// Warps 0-15: the chain (warp w: value features 32 (w % 4) .. + 31, quarter w / 4 of the columns; with halves
+// the chain's own steps took 1.6 times as long, as two warps do not fill an SM partition's issue slots);
+// warps 16-19: o, or E's images and dO as an operand; warp 20: products; warp 21: copies.
+constexpr int kParts = 4, kChainWarps = 4 * kParts, kOutWarp = kChainWarps, kMmaWarp = kOutWarp + 4, kCopyWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kCopyWarp + 1);
 
 constexpr uint32_t state_bytes(int DK, int DV) { return 2u * DK * DV * 2; }  // both parts of a state's image
 constexpr uint32_t rows_bytes(int DV) { return 2u * kChunk * DV * 2; }       // both parts of a chunk's rows
@@ -457,7 +464,7 @@ template <int DK, int DV, int kMode> struct ScanSmem {
     float scalars[3][3][kChunk];  // beta, write, first; in reverse write, first, back
     uint64_t full[2];                       // a stage's V and matrices are there (and scalars, but for kForward)
     uint64_t keys_full[2], rows_read;       // its K, Q, P (and scalars) are; (kOutOverW) the store of E's rows has read them
-    uint64_t s_ready, u_ready, d_ready;     // left operands are in TMEM (256, 256, 128 arrivals)
+    uint64_t s_ready, u_ready, d_ready;     // left operands are in TMEM (512, 512, 128 arrivals)
     uint64_t e_full, s_full, o_full, o_read;  // products are there; the warps of o have read theirs
     uint64_t stored;                        // the state's image has been read by its store
     uint64_t drain;
@@ -611,7 +618,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
-                        mma_ts(tmem + Col::S, tU + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, b + kk * (2048 >> 4), id_s, part + kk > 0);
+                        mma_ts(tmem + Col::S, tU + kk * 16 + part * 8, b + kk * (2048 >> 4), id_s, part + kk > 0);
                         if (kMode == kReverse)
                             mma_ts(tmem + Col::S, tmem + Col::pu + part * 32 + kk * 8, dqm + kk * (2048 >> 4), id_s, 1);
                     }
@@ -633,39 +640,38 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
         }
         __syncwarp();
     } else if (warp < kChainWarps) {
-        const int half = warp >> 2, f = 32 * (warp & 3) + lane;  // value feature
-        const bool live = f < DV;
+        constexpr int kKeys = DK / kParts, kTokens = kChunk / kParts;  // columns of S, of E, a thread
+        const int part = warp >> 2, f = 32 * (warp & 3) + lane;        // value feature
+        const bool live = 32 * (warp & 3) < DV;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const uint32_t tS = tl + Col::S + half * (DK / 2), tP = tl + Col::parts + half * (DK / 4);
-        const size_t state = (size_t)bh * DK * DV + (size_t)half * (DK / 2) * DV + f;
-        // 16 state values, of key features half DK / 2 + x .., as two parts: to TMEM and to the image that is kept
-        auto put_parts = [&](int x, const float *s) {
-            uint32_t hi[8], lo[8];
+        const uint32_t tS = tl + Col::S + part * kKeys, tP = tl + Col::parts + part * (kKeys / 2);
+        const size_t state = (size_t)bh * DK * DV + (size_t)part * kKeys * DV + f;
+        float s[kKeys];  // the state: key features part kKeys ..
 #pragma unroll
-            for (int e = 0; e < 8; ++e) split2(s[2 * e], s[2 * e + 1], hi[e], lo[e]);
-            tmem_st8(tP + x / 2, hi);
-            tmem_st8(tP + DK / 2 + x / 2, lo);
-            if (kKeep && live) {
-                const int k0 = half * (DK / 2) + x;
-                uint8_t *at = sm.state + (k0 >> 6) * (DV * 128);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t off = sw128_offset(f, (k0 & 63) + 8 * e);
-                    *reinterpret_cast<uint4 *>(at + off) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
-                    *reinterpret_cast<uint4 *>(at + state_bytes(DK, DV) / 2 + off) = make_uint4(lo[4 * e], lo[4 * e + 1], lo[4 * e + 2], lo[4 * e + 3]);
-                }
-            }
-        };
-        float s[DK / 2];
-#pragma unroll
-        for (int e = 0; e < DK / 2; ++e) s[e] = first_state && live ? first_state[state + (size_t)e * DV] : 0.f;
+        for (int e = 0; e < kKeys; ++e) s[e] = first_state && live ? first_state[state + (size_t)e * DV] : 0.f;
         for (int c = 0; ok && c < chunks; ++c) {
             const int st = c & 1;
             const uint32_t ph = (uint32_t)c & 1u;
             if (kKeep && c > 0 && !(ok = wait(&sm.stored, ph ^ 1u))) break;
             if (!kKeep && c > 0 && !(ok = wait(&sm.o_full, ph ^ 1u))) break;  // P U has read U
 #pragma unroll
-            for (int x = 0; x < DK / 2; x += 16) put_parts(x, s + x);
+            for (int x = 0; x < kKeys; x += 16) {  // two parts: to TMEM and to the image that is kept
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) split2(s[x + 2 * e], s[x + 2 * e + 1], hi[e], lo[e]);
+                tmem_st8(tP + x / 2, hi);
+                tmem_st8(tP + DK / 2 + x / 2, lo);
+                if (kKeep && live) {
+                    const int k0 = part * kKeys + x;
+                    uint8_t *at = sm.state + (k0 >> 6) * (DV * 128);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t off = sw128_offset(f, (k0 & 63) + 8 * e);
+                        *reinterpret_cast<uint4 *>(at + off) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+                        *reinterpret_cast<uint4 *>(at + state_bytes(DK, DV) / 2 + off) = make_uint4(lo[4 * e], lo[4 * e + 1], lo[4 * e + 2], lo[4 * e + 3]);
+                    }
+                }
+            }
             if (kKeep) fence_proxy_async_smem();
             tmem_st_wait();
             tc_fence_before();
@@ -675,34 +681,31 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
             const float whole = scalars[kMode == kReverse ? 1 : 2][kChunk - 1];
             if (!(ok = wait(&sm.e_full, ph))) break;
             tc_fence_after();
-            const uint32_t tE = tl + Col::e + 64 * st + 32 * half;
-            uint32_t a[32];
-            tmem_ld32(tE, a);
+            const uint32_t tE = tl + Col::e + 64 * st + kTokens * part;
+            uint32_t a[16];
+            static_assert(kTokens == 16, "");
+            tmem_ld16(tE, a);
             tmem_ld_wait();
             {
-                const float *mul = scalars[kMode == kReverse ? 2 : 1] + 32 * half, *beta = scalars[0] + 32 * half;
-                const uint32_t tU = kKeep ? tl + Col::qs + 32 * half : tE;
+                const float *mul = scalars[kMode == kReverse ? 2 : 1] + kTokens * part, *beta = scalars[0] + kTokens * part;
+                const uint32_t tU = kKeep ? tl + Col::qs + kTokens * part : tE;
+                uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int y = 0; y < 32; y += 16) {
-                    uint32_t hi[8], lo[8];
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 w = *reinterpret_cast<const float4 *>(mul + e);
+                    split2(w.x * __uint_as_float(a[e]), w.y * __uint_as_float(a[e + 1]), hi[e / 2], lo[e / 2]);
+                    split2(w.z * __uint_as_float(a[e + 2]), w.w * __uint_as_float(a[e + 3]), hi[e / 2 + 1], lo[e / 2 + 1]);
+                }
+                tmem_st8(tU, hi);
+                tmem_st8(tU + 8, lo);
+                if (!kKeep) {  // U for o, in one part
 #pragma unroll
                     for (int e = 0; e < 16; e += 4) {
-                        const float4 w = *reinterpret_cast<const float4 *>(mul + y + e);
-                        split2(w.x * __uint_as_float(a[y + e]), w.y * __uint_as_float(a[y + e + 1]), hi[e / 2], lo[e / 2]);
-                        split2(w.z * __uint_as_float(a[y + e + 2]), w.w * __uint_as_float(a[y + e + 3]), hi[e / 2 + 1], lo[e / 2 + 1]);
-                    }
-                    tmem_st8(tU + y / 2, hi);
-                    tmem_st8(tU + 16 + y / 2, lo);
-                }
-                if (!kKeep) {  // U for o, in one part
-                    uint32_t u[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
                         const float4 w = *reinterpret_cast<const float4 *>(beta + e);
-                        u[e / 2] = pack_bf16(w.x * __uint_as_float(a[e]), w.y * __uint_as_float(a[e + 1]));
-                        u[e / 2 + 1] = pack_bf16(w.z * __uint_as_float(a[e + 2]), w.w * __uint_as_float(a[e + 3]));
+                        hi[e / 2] = pack_bf16(w.x * __uint_as_float(a[e]), w.y * __uint_as_float(a[e + 1]));
+                        hi[e / 2 + 1] = pack_bf16(w.z * __uint_as_float(a[e + 2]), w.w * __uint_as_float(a[e + 3]));
                     }
-                    tmem_st16(tl + Col::parts + DK / 2 + 16 * half, u);
+                    tmem_st8(tl + Col::parts + DK / 2 + 8 * part, hi);
                 }
             }
             tmem_st_wait();
@@ -711,19 +714,19 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
             if (!(ok = wait(&sm.s_full, ph))) break;
             tc_fence_after();
 #pragma unroll
-            for (int x = 0; x < DK / 2; x += 32) {
-                tmem_ld32(tS + x, a);
+            for (int x = 0; x < kKeys; x += 16) {
+                tmem_ld16(tS + x, a);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) s[x + e] = fmaf(whole, s[x + e], __uint_as_float(a[e]));
+                for (int e = 0; e < 16; ++e) s[x + e] = fmaf(whole, s[x + e], __uint_as_float(a[e]));
             }
         }
         if (ok && last_state && live)
 #pragma unroll
-            for (int e = 0; e < DK / 2; ++e) last_state[state + (size_t)e * DV] = s[e];
+            for (int e = 0; e < kKeys; ++e) last_state[state + (size_t)e * DV] = s[e];
     } else if (warp < kMmaWarp) {
         const int f = 32 * (warp & 3) + lane;
-        const bool live = f < DV;
+        const bool live = 32 * (warp & 3) < DV;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         uint32_t at[8];  // (row e, feature f) of a tile of 64-column boxes
 #pragma unroll
@@ -737,17 +740,17 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                 if (c > 0 && !(ok = wait(&sm.s_full, ph ^ 1u))) break;
                 const uint8_t *v = sm.v[st][0];
 #pragma unroll
-                for (int y = 0; y < kChunk; y += 32) {
-                    uint32_t hi[16], lo[16];
+                for (int y = 0; y < kChunk; y += 16) {
+                    uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
+                    for (int e = 0; e < 16; e += 2) {
                         const uint8_t *r = v + (y + e) / 8 * 1024;
                         const float d0 = live ? bf16_at(r + at[e & 7]) : 0.f, d1 = live ? bf16_at(r + at[(e + 1) & 7]) : 0.f;
                         const float2 w = *reinterpret_cast<const float2 *>(&sm.scalars[c % 3][1][y + e]);
                         split2(p.scale * w.x * d0, p.scale * w.y * d1, hi[e / 2], lo[e / 2]);
                     }
-                    tmem_st16(tl + Col::pu + y / 2, hi);
-                    tmem_st16(tl + Col::pu + 32 + y / 2, lo);
+                    tmem_st8(tl + Col::pu + y / 2, hi);
+                    tmem_st8(tl + Col::pu + 32 + y / 2, lo);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -765,24 +768,23 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                 if (!(ok = wait(&sm.e_full, ph))) break;
                 tc_fence_after();
                 if (!Sm::kOutOverW && c > 0) named_bar_sync(1, 128);  // (the store above waited for the last rows' too)
+                if (live)
 #pragma unroll
-                for (int y = 0; y < kChunk; y += 32) {
-                    uint32_t a[32];
-                    tmem_ld32(tl + Col::e + 64 * st + y, a);
-                    tmem_ld_wait();
+                    for (int y = 0; y < kChunk; y += 16) {
+                        uint32_t a[16];
+                        tmem_ld16(tl + Col::e + 64 * st + y, a);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        uint32_t hi, lo;
-                        split2(__uint_as_float(a[e]), __uint_as_float(a[e + 1]), hi, lo);
-                        uint8_t *to = out + (y + e) / 8 * 1024;
-                        if (live) {
+                        for (int e = 0; e < 16; e += 2) {
+                            uint32_t hi, lo;
+                            split2(__uint_as_float(a[e]), __uint_as_float(a[e + 1]), hi, lo);
+                            uint8_t *to = out + (y + e) / 8 * 1024;
                             *reinterpret_cast<uint16_t *>(to + at[e & 7]) = (uint16_t)hi;
                             *reinterpret_cast<uint16_t *>(to + at[(e + 1) & 7]) = (uint16_t)(hi >> 16);
                             *reinterpret_cast<uint16_t *>(to + rows_bytes(DV) / 2 + at[e & 7]) = (uint16_t)lo;
                             *reinterpret_cast<uint16_t *>(to + rows_bytes(DV) / 2 + at[(e + 1) & 7]) = (uint16_t)(lo >> 16);
                         }
                     }
-                }
                 tc_fence_before();
                 fence_proxy_async_smem();
                 mbar_arrive(&sm.o_read);
@@ -804,18 +806,24 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                     __syncwarp();
                     named_bar_sync(1, 128);
                 }
+                const float *first = sm.scalars[c % 3][2];
+                if (live)
 #pragma unroll
-                for (int y = 0; y < kChunk; y += 32) {
-                    uint32_t a[32], b[32];
-                    tmem_ld32(tl + Col::qs + y, a);
-                    tmem_ld32(tl + Col::pu + y, b);
-                    tmem_ld_wait();
+                    for (int y = 0; y < kChunk; y += 16) {
+                        uint32_t a[16], b[16];
+                        tmem_ld16(tl + Col::qs + y, a);
+                        tmem_ld16(tl + Col::pu + y, b);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float o = p.scale * fmaf(sm.scalars[c % 3][2][y + e], __uint_as_float(a[e]), __uint_as_float(b[e]));
-                        if (live) *reinterpret_cast<__nv_bfloat16 *>(out + (y + e) / 8 * 1024 + at[e & 7]) = __float2bfloat16_rn(o);
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 w = *reinterpret_cast<const float2 *>(first + y + e);
+                            const uint32_t o = pack_bf16(p.scale * fmaf(w.x, __uint_as_float(a[e]), __uint_as_float(b[e])),
+                                                         p.scale * fmaf(w.y, __uint_as_float(a[e + 1]), __uint_as_float(b[e + 1])));
+                            uint8_t *to = out + (y + e) / 8 * 1024;
+                            *reinterpret_cast<uint16_t *>(to + at[e & 7]) = (uint16_t)o;
+                            *reinterpret_cast<uint16_t *>(to + at[(e + 1) & 7]) = (uint16_t)(o >> 16);
+                        }
                     }
-                }
                 tc_fence_before();
                 fence_proxy_async_smem();
                 mbar_arrive(&sm.o_read);
