@@ -675,10 +675,12 @@ la_status la_get_device_status(la_stream_t stream)
     if (st != LA_OK) return st;
     st = recurrence_read_status((cudaStream_t)stream, &rc_bits);
     if (st != LA_OK) return st;
-    unsigned dl_bits = 0;
+    unsigned dl_bits = 0, db_bits = 0;
     st = tc_delta_read_status((cudaStream_t)stream, &dl_bits);
     if (st != LA_OK) return st;
-    wn_bits |= wb_bits | rc_bits | dl_bits;
+    st = tc_delta_bwd_read_status((cudaStream_t)stream, &db_bits);
+    if (st != LA_OK) return st;
+    wn_bits |= wb_bits | rc_bits | dl_bits | db_bits;
     return ((bits | nc_bits | fv_bits | cc_bits | cl_bits | bw_bits | wn_bits) & kStatusTimeout) ? LA_ERR_TIMEOUT : LA_OK;
 }
 

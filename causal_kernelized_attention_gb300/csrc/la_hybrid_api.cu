@@ -459,10 +459,11 @@ la_status la_delta_backward(const void *q, const void *k, const void *v, const f
     std::lock_guard<std::mutex> lock(g_launches);
     Scratch own;
     void *base = nullptr;
-    const size_t bytes = delta_backward_simt_scratch(p);
+    const bool tc = delta_tc_eligible(p);
+    const size_t bytes = tc ? delta_backward_tc_scratch(p) : delta_backward_simt_scratch(p);
     if (bytes > 0 && (st = call_scratch(p.stream, bytes, 3, &own, &base)) != LA_OK) return st;
     p.scratch = static_cast<float *>(base);
-    return delta_backward_simt(p);
+    return tc ? delta_backward_tc(p) : delta_backward_simt(p);
 }
 
 la_status la_delta_step(float *S, const void *q, const void *k, const void *v, const float *g, const float *beta, void *o,

@@ -234,7 +234,10 @@ la_status delta_step(const DeltaProblem &p, float *S);
 bool delta_tc_eligible(const DeltaProblem &p);
 la_status delta_forward_tc(const DeltaProblem &p);
 size_t delta_forward_tc_scratch(const DeltaProblem &p);  // bytes at p.scratch
+la_status delta_backward_tc(const DeltaProblem &p);      // (la_tc_delta_bwd.cu)
+size_t delta_backward_tc_scratch(const DeltaProblem &p);
 la_status tc_delta_read_status(cudaStream_t s, unsigned *bits);
+la_status tc_delta_bwd_read_status(cudaStream_t s, unsigned *bits);
 
 // Group norm with an activation or a gate (la_norm.cu): forward y, mean_out, rstd_out; backward dy -> dx, dgate,
 // dw, db.  Scratch of norm_scratch() bytes.

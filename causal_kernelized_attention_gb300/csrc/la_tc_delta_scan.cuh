@@ -453,19 +453,22 @@ template <int DK, int DV, int kMode> struct ScanSmem {
     static constexpr uint32_t kMats = 2 * kSq + Layout<DK>::w_bytes;
     uint8_t v[2][DV / 64][kSq];
     uint8_t mats[2][kMats];  // T or Z, W or W2
-    uint8_t p[kMode == kForward ? 2 : 1][kMode == kForward ? kSq : 1024];
     uint8_t k[kKeyStages][DK / 64][kSq];
     uint8_t q[kMode == kSave ? 1 : kKeyStages][kMode == kSave ? 1 : DK / 64][kSq];  // (kSave: not used)
     union {  // o is staged by one mode, a state by the others
         uint8_t state[kMode == kForward ? rows_bytes(DV) / 2 : state_bytes(DK, DV)];
         uint8_t o[rows_bytes(DV) / 2];
     };
-    uint8_t e[kMode == kForward || kOutOverW ? 16 : rows_bytes(DV)];  // E's rows
+    union {
+        uint8_t p[kMode == kForward ? 2 : 1][kMode == kForward ? kSq : 16];
+        uint8_t e[kMode == kForward || kOutOverW ? 16 : rows_bytes(DV)];  // E's rows
+    };
     float scalars[3][3][kChunk];  // beta, write, first; in reverse write, first, back
     uint64_t full[2];                       // a stage's V and matrices are there (and scalars, but for kForward)
-    uint64_t keys_full[2], rows_read;       // its K, Q, P (and scalars) are; (kOutOverW) the store of E's rows has read them
+    uint64_t keys_full[2], rows_read[2];    // its K, Q, P (and scalars) are; (kOutOverW) the store of E's rows has read them
     uint64_t s_ready, u_ready, d_ready;     // left operands are in TMEM (512, 512, 128 arrivals)
-    uint64_t e_full, s_full, o_full, o_read;  // products are there; the warps of o have read theirs
+    // products are there (one barrier a stage where a waiter may come a chunk late); the warps of o have read theirs
+    uint64_t e_full[2], s_full, o_full[2], o_read;
     uint64_t stored;                        // the state's image has been read by its store
     uint64_t drain;
     uint32_t tmem_base;
@@ -491,8 +494,8 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
     const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     const int bhk = bh / p.H * p.Hk + bh % p.H / (p.H / p.Hk), chunks = (p.N + kChunk - 1) / kChunk;
     if (tid == 0) {
-        uint64_t *one[] = {&sm.full[0], &sm.full[1], &sm.keys_full[0], &sm.keys_full[1], &sm.rows_read, &sm.e_full,
-                           &sm.s_full, &sm.o_full, &sm.stored, &sm.drain};
+        uint64_t *one[] = {&sm.full[0], &sm.full[1], &sm.keys_full[0], &sm.keys_full[1], &sm.rows_read[0], &sm.rows_read[1],
+                           &sm.e_full[0], &sm.e_full[1], &sm.s_full, &sm.o_full[0], &sm.o_full[1], &sm.stored, &sm.drain};
         for (uint64_t *b : one) mbar_init(b, 1);
         mbar_init(&sm.s_ready, 32 * kChainWarps);
         mbar_init(&sm.u_ready, 32 * kChainWarps);
@@ -525,7 +528,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
             const int st = c & 1, x = chunk_of(c);
             const uint8_t *img = images + ((size_t)bh * chunks + x) * kStride;
             // V and the matrices of chunk c - 2 end with its E (where E's rows are staged over W, with their store)
-            if (c >= 2 && !(ok = wait(Sm::kOutOverW ? &sm.rows_read : &sm.e_full, (uint32_t)c & 1u))) break;
+            if (c >= 2 && !(ok = wait(Sm::kOutOverW ? &sm.rows_read[st] : &sm.e_full[st], (uint32_t)((c >> 1) - 1) & 1u))) break;
             if (__any_sync(0xffffffffu, aborted(abort_flag))) break;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&sm.full[st], DV / 64 * kSq + Sm::kMats + (kKeep ? kScanScalars : 0));
@@ -536,7 +539,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
             __syncwarp();
             // K, Q and P end with the chunk's last product
             const int ks = kKeep ? 0 : st, back = kKeep ? 1 : 2;
-            if (c >= back && !(ok = wait(kKeep ? &sm.s_full : &sm.o_full, (uint32_t)(c - back) & 1u))) break;
+            if (c >= back && !(ok = wait(kKeep ? &sm.s_full : &sm.o_full[st], (uint32_t)(kKeep ? c - 1 : (c >> 1) - 1) & 1u))) break;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&sm.keys_full[ks], kKeyBytes);
                 for (int b = 0; b < DK / 64; ++b) {
@@ -591,7 +594,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                     for (int kk = 0; kk < DK / 16; ++kk)
                         mma_ts(tE, tmem + Col::parts + (part == 1) * (DK / 2) + kk * 8,
                                b + (part == 2) * (DK / 64) * kBox + (kk >> 2) * kBox + (kk & 3) * 2, id, 1);
-                mma_commit(&sm.e_full);
+                mma_commit(&sm.e_full[st]);
             }
             __syncwarp();
             if (c > 0) wait(&sm.o_read, ph ^ 1u);
@@ -628,7 +631,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_ts(tmem + Col::pu, tmem + Col::parts + DK / 2 + kk * 8, bp + kk * 2, id, kk > 0);
-                    mma_commit(&sm.o_full);
+                    mma_commit(&sm.o_full[st]);
                 }
             }
             __syncwarp();
@@ -653,7 +656,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
             const int st = c & 1;
             const uint32_t ph = (uint32_t)c & 1u;
             if (kKeep && c > 0 && !(ok = wait(&sm.stored, ph ^ 1u))) break;
-            if (!kKeep && c > 0 && !(ok = wait(&sm.o_full, ph ^ 1u))) break;  // P U has read U
+            if (!kKeep && c > 0 && !(ok = wait(&sm.o_full[st ^ 1], (uint32_t)((c - 1) >> 1) & 1u))) break;  // P U has read U
 #pragma unroll
             for (int x = 0; x < kKeys; x += 16) {  // two parts: to TMEM and to the image that is kept
                 uint32_t hi[8], lo[8];
@@ -679,7 +682,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
             if (!(ok = wait(kKeep ? &sm.full[st] : &sm.keys_full[st], (uint32_t)(c >> 1) & 1u))) break;
             const float (*scalars)[kChunk] = sm.scalars[c % 3];
             const float whole = scalars[kMode == kReverse ? 1 : 2][kChunk - 1];
-            if (!(ok = wait(&sm.e_full, ph))) break;
+            if (!(ok = wait(&sm.e_full[st], (uint32_t)(c >> 1) & 1u))) break;
             tc_fence_after();
             const uint32_t tE = tl + Col::e + 64 * st + kTokens * part;
             uint32_t a[16];
@@ -765,7 +768,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                     mbar_arrive(&sm.stored);
                 }
                 __syncwarp();
-                if (!(ok = wait(&sm.e_full, ph))) break;
+                if (!(ok = wait(&sm.e_full[st], (uint32_t)(c >> 1) & 1u))) break;
                 tc_fence_after();
                 if (!Sm::kOutOverW && c > 0) named_bar_sync(1, 128);  // (the store above waited for the last rows' too)
                 if (live)
@@ -794,12 +797,12 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                     tma_store_commit();
                     if (Sm::kOutOverW) {
                         tma_store_wait_read_all();
-                        mbar_arrive(&sm.rows_read);
+                        mbar_arrive(&sm.rows_read[st]);
                     }
                 }
                 __syncwarp();
             } else {
-                if (!(ok = wait(&sm.o_full, ph))) break;
+                if (!(ok = wait(&sm.o_full[st], (uint32_t)(c >> 1) & 1u))) break;
                 tc_fence_after();
                 if (c > 0) {  // the last store has read the tile
                     if (warp == kOutWarp && lane == 0) tma_store_wait_read_all();
