@@ -10,6 +10,7 @@
 
 #include "la_common.cuh"
 #include "la_internal.h"
+#include "la_tc_common.cuh"
 
 namespace la {
 namespace {
@@ -22,34 +23,41 @@ struct Params {
     float *part;  // partial sums: [rows][2][C]
     int B, L, C, G, D;
     float eps;
-    int heads_first, center, act;
-    int splits, rows;  // over positions: splits of an entry, positions a split
+    int heads_first, center;
+    int splits, rows, zs;  // over positions: splits of an entry, positions a split, blocks across the channels
 };
 
-// VEC elements of T at p as floats, and back.
+// VEC elements of T as they lie in memory (loaded ahead of their use), as floats, and back.
 template <typename T, int VEC> struct Pack {
-    static __device__ __forceinline__ void get(const T *p, float (&v)[VEC])
+    typedef T Raw;
+    static __device__ __forceinline__ Raw none() { return Elem<T>::from_f32(0.f); }
+    static __device__ __forceinline__ Raw load(const T *p) { return __ldcs(p); }
+    static __device__ __forceinline__ Raw keep(const T *p) { return __ldg(p); }
+    static __device__ __forceinline__ void open(Raw r, float (&v)[VEC])
     {
         static_assert(VEC == 1, "");
-        v[0] = Elem<T>::to_f32(__ldg(p));
+        v[0] = Elem<T>::to_f32(r);
     }
-    static __device__ __forceinline__ void put(T *p, const float (&v)[VEC]) { p[0] = Elem<T>::from_f32(v[0]); }
+    static __device__ __forceinline__ void put(T *p, const float (&v)[VEC]) { __stcs(p, Elem<T>::from_f32(v[0])); }
 };
 template <> struct Pack<float, 4> {
-    static __device__ __forceinline__ void get(const float *p, float (&v)[4])
-    {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    }
+    typedef float4 Raw;
+    static __device__ __forceinline__ Raw none() { return make_float4(0.f, 0.f, 0.f, 0.f); }
+    static __device__ __forceinline__ Raw load(const float *p) { return __ldcs(reinterpret_cast<const float4 *>(p)); }
+    static __device__ __forceinline__ Raw keep(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
+    static __device__ __forceinline__ void open(const Raw &a, float (&v)[4]) { v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w; }
     static __device__ __forceinline__ void put(float *p, const float (&v)[4])
     {
-        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
     }
 };
 template <> struct Pack<__nv_bfloat16, 8> {
-    static __device__ __forceinline__ void get(const __nv_bfloat16 *p, float (&v)[8])
+    typedef uint4 Raw;
+    static __device__ __forceinline__ Raw none() { return make_uint4(0u, 0u, 0u, 0u); }
+    static __device__ __forceinline__ Raw load(const __nv_bfloat16 *p) { return __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    static __device__ __forceinline__ Raw keep(const __nv_bfloat16 *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
+    static __device__ __forceinline__ void open(const Raw &a, float (&v)[8])
     {
-        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
         const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
@@ -62,19 +70,24 @@ template <> struct Pack<__nv_bfloat16, 8> {
             const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             u[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+        __stcs(reinterpret_cast<uint4 *>(p), make_uint4(u[0], u[1], u[2], u[3]));
     }
 };
 
-// silu and its slope.  bf16 results take the fast exponential and division (2 ulp of fp32 each).
+// silu and its slope (kAct; otherwise the identity).  bf16 results take the hardware's exponential and reciprocal
+// (within 2^-21 together; a sigmoid that underflows is 0).
 template <typename T> __device__ __forceinline__ float sigmoid(float z)
 {
-    return std::is_same<T, float>::value ? 1.f / (1.f + expf(-z)) : __fdividef(1.f, 1.f + __expf(-z));
+    if (std::is_same<T, float>::value) return 1.f / (1.f + expf(-z));
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
 }
-template <typename T> __device__ __forceinline__ float act_of(float z, int act) { return act == LA_ACT_SILU ? z * sigmoid<T>(z) : z; }
-template <typename T> __device__ __forceinline__ float act_slope(float z, int act, float *value)
+template <typename T, bool kAct> __device__ __forceinline__ float act_of(float z) { return kAct ? z * sigmoid<T>(z) : z; }
+template <typename T, bool kAct> __device__ __forceinline__ float act_slope(float z, float *value)
 {
-    if (act != LA_ACT_SILU) {
+    if (!kAct) {
         *value = z;
         return 1.f;
     }
@@ -84,13 +97,13 @@ template <typename T> __device__ __forceinline__ float act_slope(float z, int ac
 }
 
 // What one element passes back: dz = dL/dz, and dL/dgate.
-template <typename T, bool kGate>
-__device__ __forceinline__ float back(float h, float w, float b, float dy, float gate, int act, float *dgate)
+template <typename T, bool kGate, bool kAct>
+__device__ __forceinline__ float back(float h, float w, float b, float dy, float gate, float *dgate)
 {
     const float z = fmaf(h, w, b);
     float value;
-    if (!kGate) return dy * act_slope<T>(z, act, &value);
-    const float slope = act_slope<T>(gate, act, &value);
+    if (!kGate) return dy * act_slope<T, kAct>(z, &value);
+    const float slope = act_slope<T, kAct>(gate, &value);
     *dgate = dy * z * slope;
     return dy * value;
 }
@@ -104,13 +117,17 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes)
 // ---------------------------------------------------------------- a token's groups
 // `lanes` lanes hold a group, VEC neighbouring channels at a time, NV times.  A slot of lanes keeps
 // to one group of channels (slot % G), so weights, and the sums for their gradients, stay in
-// registers, and walks over the tokens; the launch has a whole number of slots for each group.
-template <typename T, int VEC, int NV, bool kGate, bool kBack>
-__global__ void __launch_bounds__(256) norm_tokens(Params p, int lanes, long long slots)
+// registers, and walks over the tokens, the next one's loads under way while one is computed; the launch has a
+// whole number of slots for each group.
+template <typename T, int VEC, int NV, bool kGate, bool kBack, bool kAct>
+__global__ void __launch_bounds__(256, VEC * NV > 8 ? 1 : kBack ? (VEC * NV > 4 ? 2 : 3) : VEC * NV > 4 ? 3 : 4) norm_tokens(Params p, int lanes, long long slots)
 {
+    typedef Pack<T, VEC> Pk;
+    sm100::griddep_wait();
+    sm100::griddep_launch_dependents();
     const int lane = threadIdx.x & (lanes - 1), per_block = 256 / lanes, local = threadIdx.x / lanes;
-    const long long slot = (long long)blockIdx.x * per_block + local, tokens = (long long)p.B * p.L;
-    const int g = (int)(slot % p.G);
+    const long long slot = (long long)blockIdx.x * per_block + local;
+    const int tokens = p.B * p.L, g = (int)(slot % p.G);
     const float inv = 1.f / p.D;
     float w[NV][VEC], b[NV][VEC], dw[kBack ? NV : 1][VEC], db[kBack ? NV : 1][VEC];
     bool in[NV];
@@ -125,31 +142,47 @@ __global__ void __launch_bounds__(256) norm_tokens(Params p, int lanes, long lon
             if (kBack) dw[n][e] = db[n][e] = 0.f;
         }
     }
-    // every lane of a warp runs the same trips (the sums take all lanes): a slot past the last
-    // token reads nothing and writes nothing
-    const long long step = slots / p.G, first = slot / p.G, warp_first = ((long long)blockIdx.x * per_block + (threadIdx.x & ~31) / lanes) / p.G;
-    for (long long t = first, wt = warp_first; wt < tokens; t += step, wt += step) {
-        const bool live = t < tokens;
-        const size_t flat = ((size_t)t * p.G + g) * p.D;
-        const size_t xat = p.heads_first ? ((size_t)(t / p.L * p.G + g) * p.L + t % p.L) * p.D : flat;
-        float x[NV][VEC], ga[kGate ? NV : 1][VEC], dy[kBack ? NV : 1][VEC];
+    // every lane of a warp runs the same trips (the sums take all lanes): a slot past the last token reads and
+    // writes nothing.  Token t is position l of entry bi.
+    const int step = (int)(slots / p.G), step_b = step / p.L, step_l = step % p.L;
+    int t = (int)(slot / p.G), wt = (int)(((long long)blockIdx.x * per_block + (threadIdx.x & ~31) / lanes) / p.G);
+    int bi = t / p.L, l = t % p.L;
+    auto at_x = [&]() { return p.heads_first ? (((size_t)bi * p.G + g) * p.L + l) * p.D : ((size_t)t * p.G + g) * p.D; };
+    typename Pk::Raw rx[NV], rg[kGate ? NV : 1], rd[kBack ? NV : 1];
+    float rm = 0.f, rr = 0.f;
+    size_t next_x, next_st;  // where token t's group starts in x; its place among all groups
+    auto load = [&]() {
+        next_x = at_x(), next_st = (size_t)t * p.G + g;
+        const size_t xat = next_x, st = next_st, flat = st * p.D;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int c = (lane + n * lanes) * VEC;
-            const bool on = live && in[n];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                x[n][e] = 0.f;
-                if (kGate) ga[n][e] = 0.f;
-                if (kBack) dy[n][e] = 0.f;
-            }
-            if (on) {
-                Pack<T, VEC>::get(static_cast<const T *>(p.x) + xat + c, x[n]);
-                if (kGate) Pack<T, VEC>::get(static_cast<const T *>(p.gate) + flat + c, ga[n]);
-                if (kBack) Pack<T, VEC>::get(static_cast<const T *>(p.dy) + flat + c, dy[n]);
-            }
+            const bool on = t < tokens && in[n];
+            rx[n] = on ? Pk::load(static_cast<const T *>(p.x) + xat + c) : Pk::none();
+            if (kGate) rg[n] = on ? Pk::load(static_cast<const T *>(p.gate) + flat + c) : Pk::none();
+            if (kBack) rd[n] = on ? Pk::load(static_cast<const T *>(p.dy) + flat + c) : Pk::none();
         }
-        const size_t st = (size_t)t * p.G + g;
+        if (kBack && t < tokens) {
+            rm = p.center ? __ldg(p.mean + st) : 0.f;
+            rr = __ldg(p.rstd + st);
+        }
+    };
+    load();
+    while (wt < tokens) {
+        const bool live = t < tokens;
+        const size_t st = next_st, flat = st * p.D, xat = next_x;
+        float x[NV][VEC], ga[kGate ? NV : 1][VEC], dy[kBack ? NV : 1][VEC];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            Pk::open(rx[n], x[n]);
+            if (kGate) Pk::open(rg[n], ga[n]);
+            if (kBack) Pk::open(rd[n], dy[n]);
+        }
+        const float m_in = rm, r_in = rr;
+        t = tokens - t > step ? t + step : tokens, wt = tokens - wt > step ? wt + step : tokens;
+        bi += step_b, l += step_l;
+        if (l >= p.L) l -= p.L, ++bi;
+        load();
         if (!kBack) {
             float m = 0.f, v = 0.f;
             if (p.center) {
@@ -163,8 +196,8 @@ __global__ void __launch_bounds__(256) norm_tokens(Params p, int lanes, long lon
             for (int n = 0; n < NV; ++n)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    x[n][e] -= m;
-                    if (in[n]) v = fmaf(x[n][e], x[n][e], v);
+                    x[n][e] = in[n] ? x[n][e] - m : 0.f;
+                    v = fmaf(x[n][e], x[n][e], v);
                 }
             const float r = 1.f / sqrtf(fmaf(lanes_sum(v, lanes), inv, p.eps));
             if (!live) continue;
@@ -177,26 +210,24 @@ __global__ void __launch_bounds__(256) norm_tokens(Params p, int lanes, long lon
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const float z = fmaf(x[n][e] * r, w[n][e], b[n][e]);
-                    x[n][e] = kGate ? z * act_of<T>(ga[n][e], p.act) : act_of<T>(z, p.act);
+                    x[n][e] = kGate ? z * act_of<T, kAct>(ga[n][e]) : act_of<T, kAct>(z);
                 }
-                if (in[n]) Pack<T, VEC>::put(static_cast<T *>(p.y) + flat + (lane + n * lanes) * VEC, x[n]);
+                if (in[n]) Pk::put(static_cast<T *>(p.y) + flat + (lane + n * lanes) * VEC, x[n]);
             }
         } else {
-            const float m = live && p.center ? __ldg(p.mean + st) : 0.f, r = live ? __ldg(p.rstd + st) : 0.f;
             float s1 = 0.f, s2 = 0.f;
 #pragma unroll
             for (int n = 0; n < NV; ++n)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    const float h = (x[n][e] - m) * r;
+                    const float h = (x[n][e] - m_in) * r_in;
                     float dg = 0.f;
-                    const float dz = back<T, kGate>(h, w[n][e], b[n][e], dy[n][e], kGate ? ga[n][e] : 0.f, p.act, &dg);
+                    const float dz = back<T, kGate, kAct>(h, w[n][e], b[n][e], dy[n][e], kGate ? ga[n][e] : 0.f, &dg);
                     if (kGate) ga[n][e] = dg;
-                    if (in[n] && live) {
-                        dw[n][e] = fmaf(dz, h, dw[n][e]);
-                        db[n][e] += dz;
-                    }
-                    const float dh = in[n] ? dz * w[n][e] : 0.f;
+                    // dy is 0 past the channels and the tokens, so dz is (w is 0 there too)
+                    dw[n][e] = fmaf(dz, h, dw[n][e]);
+                    db[n][e] += dz;
+                    const float dh = dz * w[n][e];
                     s1 += dh;
                     s2 = fmaf(dh, h, s2);
                     x[n][e] = h;
@@ -208,10 +239,10 @@ __global__ void __launch_bounds__(256) norm_tokens(Params p, int lanes, long lon
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) x[n][e] = r * (dy[n][e] - s1 - x[n][e] * s2);
+                for (int e = 0; e < VEC; ++e) x[n][e] = r_in * (dy[n][e] - s1 - x[n][e] * s2);
                 if (in[n]) {
-                    Pack<T, VEC>::put(static_cast<T *>(p.dx) + xat + (lane + n * lanes) * VEC, x[n]);
-                    if (kGate) Pack<T, VEC>::put(static_cast<T *>(p.dgate) + flat + (lane + n * lanes) * VEC, ga[n]);
+                    Pk::put(static_cast<T *>(p.dx) + xat + (lane + n * lanes) * VEC, x[n]);
+                    if (kGate) Pk::put(static_cast<T *>(p.dgate) + flat + (lane + n * lanes) * VEC, ga[n]);
                 }
             }
         }
@@ -243,55 +274,92 @@ __global__ void __launch_bounds__(256) norm_tokens(Params p, int lanes, long lon
 }
 
 // ---------------------------------------------------------------- groups over all positions
+// f(e, group of channel c + e) for e < VEC, groups of D channels.
+template <int VEC, typename F> __device__ __forceinline__ void for_groups(int c, int D, F f)
+{
+    int g = c / D, r = c - g * D;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        f(e, g);
+        if (++r == D) r = 0, ++g;
+    }
+}
+
 // Columns of VEC channels, `cols` of them to a block of 256 threads; the other threads of a column take
 // further positions.  Sums per channel and split, joined in shared memory in a fixed order.
-template <typename T, int VEC, bool kGate, bool kBack>
+template <typename T, int VEC, bool kGate, bool kBack, bool kAct>
 __global__ void __launch_bounds__(256) norm_sums(Params p, int cols)
 {
+    typedef Pack<T, VEC> Pk;
     extern __shared__ float sums[];  // [2][threads of a column][cols * VEC]
+    sm100::griddep_wait();
+    sm100::griddep_launch_dependents();
     const int tx = threadIdx.x % cols, ty = threadIdx.x / cols, ny = 256 / cols;
-    const int c = (blockIdx.z * cols + tx) * VEC, bi = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
+    const int z = blockIdx.x % p.zs, c = (z * cols + tx) * VEC, bi = blockIdx.x / p.zs / p.splits, split = blockIdx.x / p.zs % p.splits;
     const bool on = ty < ny && c < p.C;
     float s1[VEC] = {}, s2[VEC] = {};
     if (on) {
         const T *x = static_cast<const T *>(p.x) + (size_t)bi * p.L * p.C + c;
         const T *dy = static_cast<const T *>(p.dy) + (kBack ? (size_t)bi * p.L * p.C + c : 0);
         const T *gate = static_cast<const T *>(p.gate) + (kGate ? (size_t)bi * p.L * p.C + c : 0);
+        constexpr int kAhead = kBack ? (kGate ? 2 : 3) : 4;  // rows whose loads are under way while as many are summed
+        const int l1 = min(p.L, (split + 1) * p.rows);
+        typename Pk::Raw rx[kAhead], rd[kBack ? kAhead : 1], rg[kGate ? kAhead : 1];
+        auto load = [&](int l) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (l + u * ny >= l1) break;
+                const size_t at = (size_t)(l + u * ny) * p.C;
+                rx[u] = Pk::keep(x + at);
+                if (kBack) rd[u] = Pk::keep(dy + at);
+                if (kGate) rg[u] = Pk::keep(gate + at);
+            }
+        };
+        int l = split * p.rows + ty;
+        load(l);
         float shift[VEC], r[VEC], w[VEC], b[VEC];
-        if (!kBack) {
-            Pack<T, VEC>::get(x, shift);  // differences from the channel's first value (from 0 without centring)
-            if (!p.center)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) shift[e] = 0.f;
-        } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const size_t st = (size_t)bi * p.G + (c + e) / p.D;
+        for_groups<VEC>(c, p.D, [&](int e, int g) {
+            if (!kBack) {  // differences from the group's first value (from 0 without centring)
+                shift[e] = p.center ? Elem<T>::to_f32(__ldg(static_cast<const T *>(p.x) + (size_t)bi * p.L * p.C + g * p.D)) : 0.f;
+            } else {
+                const size_t st = (size_t)bi * p.G + g;
                 shift[e] = p.center ? __ldg(p.mean + st) : 0.f;
                 r[e] = __ldg(p.rstd + st);
                 w[e] = p.w ? __ldg(p.w + c + e) : 1.f;
                 b[e] = p.b ? __ldg(p.b + c + e) : 0.f;
             }
-        }
-        const int l1 = min(p.L, (split + 1) * p.rows);
-#pragma unroll 4
-        for (int l = split * p.rows + ty; l < l1; l += ny) {
-            float v[VEC], d[VEC], ga[VEC];
-            Pack<T, VEC>::get(x + (size_t)l * p.C, v);
-            if (kBack) Pack<T, VEC>::get(dy + (size_t)l * p.C, d);
-            if (kGate) Pack<T, VEC>::get(gate + (size_t)l * p.C, ga);
+        });
+        while (l < l1) {
+            typename Pk::Raw cx[kAhead], cd[kBack ? kAhead : 1], cg[kGate ? kAhead : 1];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                if (kBack) {
-                    const float h = (v[e] - shift[e]) * r[e];
-                    float dg;
-                    const float dz = back<T, kGate>(h, w[e], b[e], d[e], kGate ? ga[e] : 0.f, p.act, &dg);
-                    s1[e] = fmaf(dz, h, s1[e]);
-                    s2[e] += dz;
-                } else {
-                    const float t = v[e] - shift[e];
-                    s1[e] += t;
-                    s2[e] = fmaf(t, t, s2[e]);
+            for (int u = 0; u < kAhead; ++u) {
+                cx[u] = rx[u];
+                if (kBack) cd[u] = rd[u];
+                if (kGate) cg[u] = rg[u];
+            }
+            const int l0 = l;
+            l += kAhead * ny;
+            load(l);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (l0 + u * ny >= l1) break;
+                float v[VEC], d[VEC], ga[VEC];
+                Pk::open(cx[u], v);
+                if (kBack) Pk::open(cd[u], d);
+                if (kGate) Pk::open(cg[u], ga);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    if (kBack) {
+                        const float h = (v[e] - shift[e]) * r[e];
+                        float dg;
+                        const float dz = back<T, kGate, kAct>(h, w[e], b[e], d[e], kGate ? ga[e] : 0.f, &dg);
+                        s1[e] = fmaf(dz, h, s1[e]);
+                        s2[e] += dz;
+                    } else {
+                        const float t = v[e] - shift[e];
+                        s1[e] += t;
+                        s2[e] = fmaf(t, t, s2[e]);
+                    }
                 }
             }
         }
@@ -306,12 +374,14 @@ __global__ void __launch_bounds__(256) norm_sums(Params p, int cols)
     __syncthreads();
     float *out = p.part + ((size_t)bi * p.splits + split) * 2 * p.C;
     for (int i = threadIdx.x; i < 2 * width; i += 256) {
-        const int which = i / width, j = i % width, ch = blockIdx.z * width + j;
+        const int which = i / width, j = i % width, ch = z * width + j;
         float v = 0.f;
         for (int k = 0; k < ny; ++k) v += sums[(which * ny + k) * width + j];
         if (ch < p.C) out[(size_t)which * p.C + ch] = v;
     }
 }
+
+constexpr int kFinish = 512;  // threads of the blocks that finish sums
 
 __device__ __forceinline__ float block_sum(float v, float *tmp)
 {
@@ -319,137 +389,169 @@ __device__ __forceinline__ float block_sum(float v, float *tmp)
     __syncthreads();
     if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
     __syncthreads();
-    return (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
+    v = tmp[threadIdx.x & (kFinish / 32 - 1)];
+    return lanes_sum(v, kFinish / 32);
 }
 
-// A group's statistics from its channels' sums: the mean of the channels' means, and their
-// squared deviations about it.
-template <typename T>
-__global__ void __launch_bounds__(128) norm_statistics(Params p)
+// The two sums of a group, over its channels and the splits of its entry: of value 0 and value 1 of the
+// partial sums, with the channels' weights where kWeighted.
+template <bool kWeighted> __device__ __forceinline__ void group_sums(const Params &p, int bg, float *tmp, float &s0, float &s1)
 {
-    __shared__ float tmp[4];
-    const int bi = blockIdx.x / p.G, g = blockIdx.x % p.G;
-    const float *part = p.part + (size_t)bi * p.splits * 2 * p.C;
-    const T *x = static_cast<const T *>(p.x) + (size_t)bi * p.L * p.C;
-    auto channel = [&](int c, float *mean, float *m2) {
-        float s1 = 0.f, s2 = 0.f;
-        for (int s = 0; s < p.splits; ++s) {
-            s1 += part[(size_t)s * 2 * p.C + c];
-            s2 += part[((size_t)s * 2 + 1) * p.C + c];
-        }
-        if (!p.center) {
-            *mean = 0.f, *m2 = s2;
-            return;
-        }
-        const float d = s1 / p.L;
-        *mean = Elem<T>::to_f32(x[c]) + d;
-        *m2 = fmaxf(0.f, fmaf(-s1, d, s2));
-    };
-    const float inv = 1.f / p.D;
-    float a = 0.f, mean0 = 0.f, sq0 = 0.f;  // the thread's first channel is kept: most groups have no more
-    for (int c = threadIdx.x; c < p.D; c += 128) {
-        float mc, m2;
-        channel(g * p.D + c, &mc, &m2);
-        if (c == threadIdx.x) mean0 = mc, sq0 = m2;
-        a += mc;
+    const int bi = bg / p.G, g = bg % p.G, n = p.D * p.splits;
+    const float *part = p.part + (size_t)bi * p.splits * 2 * p.C + g * p.D;
+    s0 = s1 = 0.f;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += kFinish) {
+        const int split = i / p.D, c = i - split * p.D;
+        const float *at = part + (size_t)split * 2 * p.C + c, w = kWeighted && p.w ? __ldg(p.w + g * p.D + c) : 1.f;
+        s0 = fmaf(w, at[0], s0);
+        s1 = fmaf(w, at[p.C], s1);
     }
-    const float m = block_sum(a, tmp) * inv;
-    float v = 0.f;
-    for (int c = threadIdx.x; c < p.D; c += 128) {
-        float mc = mean0, m2 = sq0;
-        if (c != threadIdx.x) channel(g * p.D + c, &mc, &m2);
-        const float d = p.center ? mc - m : 0.f;
-        v += fmaf(d * d, (float)p.L, m2);
-    }
-    v = block_sum(v, tmp) * inv / p.L;
+    s0 = block_sum(s0, tmp);
+    s1 = block_sum(s1, tmp);
+}
+
+// Forward: mean and rstd of each group.
+template <typename T>
+__global__ void __launch_bounds__(kFinish) norm_statistics(Params p)
+{
+    __shared__ float tmp[kFinish / 32];
+    sm100::griddep_wait();
+    sm100::griddep_launch_dependents();
+    float s0, s1;
+    group_sums<false>(p, blockIdx.x, tmp, s0, s1);
     if (threadIdx.x == 0) {
-        if (p.center) p.mean_out[blockIdx.x] = m;
+        const int bi = blockIdx.x / p.G, g = blockIdx.x % p.G;
+        const float inv = 1.f / p.D / p.L;
+        float v = s1 * inv;
+        if (p.center) {
+            const float d = s0 * inv;
+            v = fmaxf(0.f, fmaf(-d, d, v));
+            p.mean_out[blockIdx.x] = Elem<T>::to_f32(static_cast<const T *>(p.x)[(size_t)bi * p.L * p.C + g * p.D]) + d;
+        }
         p.rstd_out[blockIdx.x] = 1.f / sqrtf(v + p.eps);
     }
 }
 
-// The two means of a group that its dx takes off: of dh = dz w (into mean_out) and of dh h (rstd_out).
-__global__ void __launch_bounds__(128) norm_group_means(Params p)
+// dw or db: the sum of all rows of the partial sums, in a fixed order; 32 channels, a warp to every 16th row.
+__device__ __forceinline__ void weight_grads(const float *part, float *out, long long rows, int C, int block, int which, float (*tmp)[33])
 {
-    __shared__ float tmp[4];
-    const int bi = blockIdx.x / p.G, g = blockIdx.x % p.G;
-    const float *part = p.part + (size_t)bi * p.splits * 2 * p.C;
-    float a = 0.f, v = 0.f;
-    for (int i = threadIdx.x; i < p.D * p.splits; i += 128) {
-        const int c = g * p.D + i % p.D;
-        const float *at = part + (size_t)(i / p.D) * 2 * p.C + c, w = p.w ? p.w[c] : 1.f;
-        v = fmaf(w, at[0], v);
-        a = fmaf(w, at[p.C], a);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = block * 32 + lane;
+    float v = 0.f;
+    if (c < C)
+#pragma unroll 8
+        for (long long r = warp; r < rows; r += kFinish / 32) v += part[((size_t)r * 2 + which) * C + c];
+    tmp[warp][lane] = v;
+    __syncthreads();
+    v = lanes_sum(tmp[lane & (kFinish / 32 - 1)][threadIdx.x >> 4], kFinish / 32);
+    const int cy = block * 32 + (threadIdx.x >> 4);
+    if ((threadIdx.x & 15) == 0 && cy < C) out[cy] = v;
+}
+
+// Backward: the two means of a group that its dx takes off, of dh = dz w (into mean_out) and of dh h (rstd_out);
+// blocks past the groups find dw, those past them db.
+__global__ void __launch_bounds__(kFinish) norm_group_means(Params p, float *dw, float *db)
+{
+    __shared__ float tmp[kFinish / 32][33];
+    sm100::griddep_wait();
+    sm100::griddep_launch_dependents();
+    const int groups = p.B * p.G, block = (int)blockIdx.x - groups, per = (p.C + 31) / 32;
+    if (block >= 0) {
+        const int which = block >= per;
+        if (which ? db != nullptr : dw != nullptr)
+            weight_grads(p.part, which ? db : dw, (long long)p.B * p.splits, p.C, block - which * per, which, tmp);
+        return;
     }
-    const float inv = 1.f / p.D / p.L;
-    a = block_sum(a, tmp);
-    v = block_sum(v, tmp);
+    float dhh, dh;
+    group_sums<true>(p, blockIdx.x, tmp[0], dhh, dh);
     if (threadIdx.x == 0) {
-        p.mean_out[blockIdx.x] = p.center ? a * inv : 0.f;
-        p.rstd_out[blockIdx.x] = v * inv;
+        const float inv = 1.f / p.D / p.L;
+        p.mean_out[blockIdx.x] = p.center ? dh * inv : 0.f;
+        p.rstd_out[blockIdx.x] = dhh * inv;
     }
 }
 
+__global__ void __launch_bounds__(kFinish) norm_weight_grads(const float *part, float *dw, float *db, long long rows, int C)
+{
+    __shared__ float tmp[kFinish / 32][33];
+    sm100::griddep_wait();
+    sm100::griddep_launch_dependents();
+    const int per = (C + 31) / 32, which = (int)blockIdx.x >= per;
+    float *out = which ? db : dw;
+    if (out) weight_grads(part, out, rows, C, blockIdx.x - which * per, which, tmp);
+}
+
 // y, or dx and dgate, of all positions.
-template <typename T, int VEC, bool kGate, bool kBack>
+template <typename T, int VEC, bool kGate, bool kBack, bool kAct>
 __global__ void __launch_bounds__(256) norm_apply(Params p, int cols)
 {
+    typedef Pack<T, VEC> Pk;
+    sm100::griddep_wait();
+    sm100::griddep_launch_dependents();
     const int tx = threadIdx.x % cols, ty = threadIdx.x / cols, ny = 256 / cols;
-    const int c = (blockIdx.z * cols + tx) * VEC, bi = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
+    const int z = blockIdx.x % p.zs, c = (z * cols + tx) * VEC, bi = blockIdx.x / p.zs / p.splits, split = blockIdx.x / p.zs % p.splits;
     if (ty >= ny || c >= p.C) return;
-    float m[VEC], r[VEC], w[VEC], b[VEC], a1[VEC], a2[VEC];
+    constexpr int kAhead = kBack && kGate ? 1 : 2;  // rows whose loads are under way while as many are computed
+    const size_t base = (size_t)bi * p.L * p.C + c;
+    const int l1 = min(p.L, (split + 1) * p.rows);
+    typename Pk::Raw rx[kAhead], rd[kBack ? kAhead : 1], rg[kGate ? kAhead : 1];
+    auto load = [&](int l) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        const size_t st = (size_t)bi * p.G + (c + e) / p.D;
+        for (int u = 0; u < kAhead; ++u) {
+            if (l + u * ny >= l1) break;
+            const size_t at = base + (size_t)(l + u * ny) * p.C;
+            rx[u] = Pk::load(static_cast<const T *>(p.x) + at);
+            if (kGate) rg[u] = Pk::load(static_cast<const T *>(p.gate) + at);
+            if (kBack) rd[u] = Pk::load(static_cast<const T *>(p.dy) + at);
+        }
+    };
+    int l = split * p.rows + ty;
+    load(l);
+    float m[VEC], r[VEC], w[VEC], b[VEC], a1[VEC], a2[VEC];
+    for_groups<VEC>(c, p.D, [&](int e, int g) {
+        const size_t st = (size_t)bi * p.G + g;
         m[e] = p.center ? p.mean[st] : 0.f;
         r[e] = p.rstd[st];
         w[e] = p.w ? __ldg(p.w + c + e) : 1.f;
         b[e] = p.b ? __ldg(p.b + c + e) : 0.f;
         if (kBack) a1[e] = p.mean_out[st], a2[e] = p.rstd_out[st];
-    }
-    const size_t base = (size_t)bi * p.L * p.C + c;
-    const int l1 = min(p.L, (split + 1) * p.rows);
-#pragma unroll 4
-    for (int l = split * p.rows + ty; l < l1; l += ny) {
-        const size_t at = base + (size_t)l * p.C;
-        float v[VEC], d[VEC], ga[VEC];
-        Pack<T, VEC>::get(static_cast<const T *>(p.x) + at, v);
-        if (kGate) Pack<T, VEC>::get(static_cast<const T *>(p.gate) + at, ga);
-        if (kBack) Pack<T, VEC>::get(static_cast<const T *>(p.dy) + at, d);
+    });
+    while (l < l1) {
+        typename Pk::Raw cx[kAhead], cd[kBack ? kAhead : 1], cg[kGate ? kAhead : 1];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float h = (v[e] - m[e]) * r[e];
-            if (kBack) {
-                float dg = 0.f;
-                const float dz = back<T, kGate>(h, w[e], b[e], d[e], kGate ? ga[e] : 0.f, p.act, &dg);
-                v[e] = r[e] * (fmaf(dz, w[e], -a1[e]) - h * a2[e]);
-                ga[e] = dg;
-            } else {
-                const float z = fmaf(h, w[e], b[e]);
-                v[e] = kGate ? z * act_of<T>(ga[e], p.act) : act_of<T>(z, p.act);
-            }
+        for (int u = 0; u < kAhead; ++u) {
+            cx[u] = rx[u];
+            if (kBack) cd[u] = rd[u];
+            if (kGate) cg[u] = rg[u];
         }
-        Pack<T, VEC>::put(static_cast<T *>(kBack ? p.dx : p.y) + at, v);
-        if (kBack && kGate) Pack<T, VEC>::put(static_cast<T *>(p.dgate) + at, ga);
+        const int l0 = l;
+        l += kAhead * ny;
+        load(l);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (l0 + u * ny >= l1) break;
+            const size_t at = base + (size_t)(l0 + u * ny) * p.C;
+            float v[VEC], d[VEC], ga[VEC];
+            Pk::open(cx[u], v);
+            if (kGate) Pk::open(cg[u], ga);
+            if (kBack) Pk::open(cd[u], d);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float h = (v[e] - m[e]) * r[e];
+                if (kBack) {
+                    float dg = 0.f;
+                    const float dz = back<T, kGate, kAct>(h, w[e], b[e], d[e], kGate ? ga[e] : 0.f, &dg);
+                    v[e] = r[e] * (fmaf(dz, w[e], -a1[e]) - h * a2[e]);
+                    ga[e] = dg;
+                } else {
+                    const float z = fmaf(h, w[e], b[e]);
+                    v[e] = kGate ? z * act_of<T, kAct>(ga[e]) : act_of<T, kAct>(z);
+                }
+            }
+            Pk::put(static_cast<T *>(kBack ? p.dx : p.y) + at, v);
+            if (kBack && kGate) Pk::put(static_cast<T *>(p.dgate) + at, ga);
+        }
     }
-}
-
-// dw and db: the sum of all rows of the partial sums, 32 channels a block, in a fixed order.
-__global__ void __launch_bounds__(1024) norm_weight_grads(const float *part, float *dw, float *db, long long rows, int C)
-{
-    __shared__ float tmp[32][33];
-    const int c = blockIdx.x * 32 + threadIdx.x, which = blockIdx.y;
-    float *out = which ? db : dw;
-    if (!out) return;
-    float v = 0.f;
-    if (c < C)
-#pragma unroll 8
-        for (long long r = threadIdx.y; r < rows; r += 32) v += part[((size_t)r * 2 + which) * C + c];
-    tmp[threadIdx.y][threadIdx.x] = v;
-    __syncthreads();
-    v = lanes_sum(tmp[threadIdx.x][threadIdx.y], 32);
-    const int cy = blockIdx.x * 32 + threadIdx.y;
-    if (threadIdx.x == 0 && cy < C) out[cy] = v;
 }
 
 // ---------------------------------------------------------------- launches
@@ -461,7 +563,7 @@ Params params_of(const NormProblem &p)
     q.x = p.x, q.gate = p.gate, q.dy = p.dy, q.w = p.w, q.b = p.b, q.mean = p.mean, q.rstd = p.rstd;
     q.y = p.y, q.dx = p.dx, q.dgate = p.dgate, q.mean_out = p.mean_out, q.rstd_out = p.rstd_out;
     q.B = p.B, q.L = p.L, q.C = p.C, q.G = p.spec.groups, q.D = p.C / p.spec.groups;
-    q.eps = p.spec.eps, q.heads_first = p.spec.heads_first, q.center = p.spec.center, q.act = p.spec.act;
+    q.eps = p.spec.eps, q.heads_first = p.spec.heads_first, q.center = p.spec.center;
     return q;
 }
 
@@ -511,8 +613,8 @@ MapShape map_shape(const NormProblem &p)
     s.cols = ceil_div(n, s.zs);
     const int ny = 256 / s.cols;
     const long long blocks = (long long)p.B * s.zs;
-    int want = (int)((kSMs * 6 + blocks - 1) / blocks);
-    const int most = ceil_div(p.L, ny * 4);
+    int want = (int)((kSMs * 4 + blocks - 1) / blocks);
+    const int most = ceil_div(p.L, ny * 6);
     want = want < most ? want : most;
     if (want < 1) want = 1;
     s.rows = ceil_div(p.L, want);
@@ -530,54 +632,58 @@ NormProblem as_map(const NormProblem &p)
     return q;
 }
 
-template <typename T, bool kGate, bool kBack> la_status launch_tokens(const NormProblem &p, Params q)
+template <typename T, bool kGate, bool kBack, bool kAct> la_status launch_tokens(const NormProblem &p, Params q)
 {
     const TokenShape s = token_shape(p);
     const int smem = kBack && q.part ? 256 / s.lanes * q.D * 4 : 0;  // at most 16 KB
     constexpr int kFull = std::is_same<T, float>::value ? 4 : 8;
     auto go = [&](auto kernel) {
         count_launches();
-        kernel<<<(unsigned)s.blocks, 256, smem, p.stream>>>(q, s.lanes, s.slots);
-        return cuda_status(cudaGetLastError());
+        return tc::launch_dependent(kernel, (unsigned)s.blocks, 256, smem, p.stream, q, s.lanes, s.slots);
     };
     if (s.vec == 1) {
-        if (s.nv == 1) return go(&norm_tokens<T, 1, 1, kGate, kBack>);
-        if (s.nv == 4) return go(&norm_tokens<T, 1, 4, kGate, kBack>);
-        return go(&norm_tokens<T, 1, 16, kGate, kBack>);
+        if (s.nv == 1) return go(&norm_tokens<T, 1, 1, kGate, kBack, kAct>);
+        if (s.nv == 4) return go(&norm_tokens<T, 1, 4, kGate, kBack, kAct>);
+        return go(&norm_tokens<T, 1, 16, kGate, kBack, kAct>);
     }
-    if (s.nv == 1) return go(&norm_tokens<T, kFull, 1, kGate, kBack>);
-    if (s.nv == 2) return go(&norm_tokens<T, kFull, 2, kGate, kBack>);
-    return go(&norm_tokens<T, kFull, 4, kGate, kBack>);
+    if (s.nv == 1) return go(&norm_tokens<T, kFull, 1, kGate, kBack, kAct>);
+    if constexpr (kFull == 4)
+        if (s.nv == 4) return go(&norm_tokens<T, kFull, 4, kGate, kBack, kAct>);
+    return go(&norm_tokens<T, kFull, 2, kGate, kBack, kAct>);
 }
 
-template <typename T, bool kGate, bool kBack> la_status launch_map(const NormProblem &p, Params q)
+template <typename T, bool kGate, bool kBack, bool kAct> la_status launch_map(const NormProblem &p, Params q)
 {
     const MapShape s = map_shape(p);
     constexpr int kFull = std::is_same<T, float>::value ? 4 : 8;
-    q.splits = s.splits, q.rows = s.rows;
-    const dim3 grid((unsigned)s.splits * p.B, 1, (unsigned)s.zs);
+    q.splits = s.splits, q.rows = s.rows, q.zs = s.zs;
     const int smem = 2 * (256 / s.cols) * s.cols * s.vec * 4;
-    auto sums = s.vec == 1 ? &norm_sums<T, 1, kGate && kBack, kBack> : &norm_sums<T, kFull, kGate && kBack, kBack>;
-    auto apply = s.vec == 1 ? &norm_apply<T, 1, kGate, kBack> : &norm_apply<T, kFull, kGate, kBack>;
+    auto sums = s.vec == 1 ? &norm_sums<T, 1, kGate && kBack, kBack, kBack && kAct> : &norm_sums<T, kFull, kGate && kBack, kBack, kBack && kAct>;
+    auto apply = s.vec == 1 ? &norm_apply<T, 1, kGate, kBack, kAct> : &norm_apply<T, kFull, kGate, kBack, kAct>;
+    const unsigned grid = (unsigned)(s.splits * s.zs) * p.B, groups = (unsigned)(p.B * q.G);
     count_launches(3);
-    sums<<<grid, 256, smem, p.stream>>>(q, s.cols);
+    la_status st = tc::launch_dependent(sums, grid, 256, smem, p.stream, q, s.cols);
+    if (st != LA_OK) return st;
     if (kBack)
-        norm_group_means<<<(unsigned)(p.B * q.G), 128, 0, p.stream>>>(q);
+        st = tc::launch_dependent(&norm_group_means, groups + (p.dw || p.db ? 2u * ceil_div(p.C, 32) : 0u), kFinish, 0, p.stream, q, p.dw, p.db);
     else
-        norm_statistics<T><<<(unsigned)(p.B * q.G), 128, 0, p.stream>>>(q);
+        st = tc::launch_dependent(&norm_statistics<T>, groups, kFinish, 0, p.stream, q);
+    if (st != LA_OK) return st;
     if (!kBack) q.mean = q.mean_out, q.rstd = q.rstd_out;
-    apply<<<grid, 256, 0, p.stream>>>(q, s.cols);
-    return cuda_status(cudaGetLastError());
+    return tc::launch_dependent(apply, grid, 256, 0, p.stream, q, s.cols);
 }
 
 template <bool kBack> la_status launch(const NormProblem &p, const Params &q)
 {
-    auto go = [&](auto t, auto gate) {
+    auto go = [&](auto t, auto gate, auto act) {
         using T = decltype(t);
-        return by_token(p) ? launch_tokens<T, decltype(gate)::value, kBack>(p, q)
-                           : launch_map<T, decltype(gate)::value, kBack>(p, q);
+        return by_token(p) ? launch_tokens<T, decltype(gate)::value, kBack, decltype(act)::value>(p, q)
+                           : launch_map<T, decltype(gate)::value, kBack, decltype(act)::value>(p, q);
     };
-    auto typed = [&](auto t) { return p.gate ? go(t, std::true_type()) : go(t, std::false_type()); };
+    auto acted = [&](auto t, auto gate) {
+        return p.spec.act == LA_ACT_SILU ? go(t, gate, std::true_type()) : go(t, gate, std::false_type());
+    };
+    auto typed = [&](auto t) { return p.gate ? acted(t, std::true_type()) : acted(t, std::false_type()); };
     return p.dtype == LA_F32 ? typed(0.f) : typed(__nv_bfloat16());
 }
 
@@ -597,22 +703,19 @@ la_status group_norm(const NormProblem &given)
     const bool tokens = by_token(given), grads = given.backward && (given.dw || given.db);
     const NormProblem p = tokens ? given : as_map(given);
     Params q = params_of(p);
-    long long rows = 0;
     if (tokens) {
         q.part = grads ? p.scratch : nullptr;
-        if (grads) rows = token_shape(p).part_rows;
     } else {
         q.part = p.scratch;
-        rows = (long long)p.B * map_shape(p).splits;
-        float *means = p.scratch + rows * 2 * p.C;
+        float *means = p.scratch + (size_t)p.B * map_shape(p).splits * 2 * p.C;
         if (p.backward || !q.mean_out) q.mean_out = means;
         if (p.backward || !q.rstd_out) q.rstd_out = means + (size_t)p.B * q.G;
     }
     la_status st = p.backward ? launch<true>(p, q) : launch<false>(p, q);
-    if (st != LA_OK || !grads) return st;
+    if (st != LA_OK || !grads || !tokens) return st;
     count_launches();
-    norm_weight_grads<<<dim3((unsigned)ceil_div(p.C, 32), 2), dim3(32, 32), 0, p.stream>>>(q.part, p.dw, p.db, rows, p.C);
-    return cuda_status(cudaGetLastError());
+    return tc::launch_dependent(&norm_weight_grads, 2u * ceil_div(p.C, 32), kFinish, 0, p.stream, (const float *)q.part, p.dw, p.db,
+                                token_shape(p).part_rows, p.C);
 }
 
 }  // namespace la
