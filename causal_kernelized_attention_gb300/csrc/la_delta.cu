@@ -1,12 +1,15 @@
-// Gated delta rule on the CUDA cores: the token-by-token scan, its reverse, the gradients of a
-// chunk, and the decode step.
+// Gated delta rule on the CUDA cores: for fp32 the scan, its reverse and the gradients of a chunk; and the
+// decode step.
 //
 //   D_t = a_t S_{t-1},  e_t = v_t - D_t^T k_t,  S_t = D_t + k_t (b_t e_t)^T,  o_t = scale S_t^T q_t
 //
 // with a_t = exp(g_t).  Columns of S (one per value feature) do not meet, so a scan's blocks take
-// 32 columns each and hold them in registers.  The scans are bound by the chain of a token (a dot
-// product over d_k, two shuffles, the update), not by memory; they serve fp32 and the widths that
-// the tensor-core kernels are not built for.
+// 32 columns each and hold them in registers.  Token by token a scan waits: a dot product over d_k, two
+// shuffles and the update follow one another (345 cycles a token at d_k 32, whatever the machine has free).  So
+// eight tokens are taken together: with G the running sum of g from their first on and D_ij = exp(G_i - G_j),
+//   e_i = v_i - exp(G_i) S^T k_i - sum_{j<i} D_ij (k_i.k_j) u_j,   u = b e,
+//   o_i = scale (exp(G_i) S^T q_i + sum_{j<=i} D_ij (q_i.k_j) u_j),   S' = exp(G_8) S + sum_j exp(G_8 - G_j) k_j u_j^T,
+// where the 16 dot products with S are independent and the small matrices are found once for all columns.
 #include "la_common.cuh"
 #include "la_delta.cuh"
 #include "la_internal.h"
@@ -16,7 +19,10 @@ namespace delta {
 namespace {
 
 constexpr int kTile = 16;   // tokens staged in shared memory at a time
-constexpr int kCols = 32;   // columns of S per block: 4 warps of 8, four lanes to a column
+constexpr int kB = 8;       // tokens taken together
+constexpr int kCols = 32;   // columns of S per block
+constexpr int kRows = 8;    // rows of S a lane holds: d_k / 8 lanes share a column
+constexpr int kMakers = 128;  // threads that load and prepare the tiles
 constexpr int kC = 32;      // tokens of a chunk of the backward pass
 
 template <typename T> struct Vec4;
@@ -32,168 +38,340 @@ template <> struct Vec4<__nv_bfloat16> {
     }
 };
 
-__device__ __forceinline__ void copy16(void *dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src));
-}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void named_bar(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 template <int n> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
 
-// The rows of one tile: keys, queries, a slice of 32 values (forward: v, reverse: dO), gates.
-template <typename T, int DK> struct alignas(16) Stage {
-    T k[kTile][DK], q[kTile][DK], v[kTile][kCols];
-    float alpha[kTile], beta[kTile];
+// The rows of one tile: keys, queries (four floats further apart than they are long: the pairs' dot products read
+// eight rows at once), a slice of 32 values (forward: v, reverse: dO), gates.
+template <int DK> struct alignas(16) Stage {
+    float k[kTile][DK + 4], q[kTile][DK + 4], v[kTile][kCols];
+    float g[kTile], beta[kTile];
+};
+// What a tile's groups of 8 tokens need: D_ij (k_i.k_j) below the diagonal, D_ij (q_i.k_j) up to it (and their
+// transposes, which the reverse reads).
+struct alignas(16) Group {
+    float N[kB][kB], P[kB][kB], first[kB], last[kB], whole[4];
+};
+// Three tiles are under way: one scanned, the next one's groups made by the last four warps, a third loaded.
+template <int DK> struct ScanSmem {
+    Stage<DK> stage[3];
+    Group groups[2][2];
 };
 
-template <typename T, int DK>
-__device__ __forceinline__ void load_stage(Stage<T, DK> &s, const T *k, const T *q, const T *v, const float *g,
-                                           const float *beta, int t0, int n, int dv, bool want_q)
+// Rows t0 .. of one tile, by the kMakers threads; rows past the sequence are zeros (which leave S as it is).
+template <int DK, int DV>
+__device__ __forceinline__ void load_stage(Stage<DK> &s, const float *k, const float *q, const float *v, const float *g,
+                                           const float *beta, int t0, int n, int tid)
 {
-    constexpr int kPer = 16 / sizeof(T);
-    const int rows = min(kTile, n - t0), tid = threadIdx.x;
-    for (int i = tid; i < rows * (DK / kPer); i += 128) {
-        const int r = i / (DK / kPer), c = i % (DK / kPer) * kPer;
-        copy16(&s.k[r][c], k + (size_t)(t0 + r) * DK + c);
-        if (want_q) copy16(&s.q[r][c], q + (size_t)(t0 + r) * DK + c);
+    const int rows = min(kTile, n - t0);
+    auto copy = [&](float *dst, const float *src, bool on) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                     "r"(on ? 16 : 0));
+    };
+    for (int i = tid; i < kTile * (DK / 4); i += kMakers) {
+        const int r = i / (DK / 4), c = i % (DK / 4) * 4;
+        const size_t at = r < rows ? (size_t)(t0 + r) * DK + c : 0;
+        copy(&s.k[r][c], k + at, r < rows);
+        copy(&s.q[r][c], q + at, r < rows);
     }
-    for (int i = tid; i < rows * (kCols / kPer); i += 128) {
-        const int r = i / (kCols / kPer), c = i % (kCols / kPer) * kPer;
-        copy16(&s.v[r][c], v + (size_t)(t0 + r) * dv + c);
+    {
+        const int r = tid / (kCols / 4), c = tid % (kCols / 4) * 4;
+        copy(&s.v[r][c], v + (r < rows ? (size_t)(t0 + r) * DV + c : 0), r < rows);
     }
-    copies_commit();
-    if (tid < rows) {
-        s.alpha[tid] = expf(g[t0 + tid]);
-        s.beta[tid] = beta[t0 + tid];
+    if (tid < 2 * kTile) {
+        const int t = tid & (kTile - 1);
+        const float *src = (tid < kTile ? g : beta) + (t < rows ? t0 + t : 0);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(tid < kTile ? &s.g[t] : &s.beta[t])),
+                     "l"(src), "r"(t < rows ? 4 : 0));
     }
 }
 
-// Four lanes share a column: lane part p holds rows 16 m + 4 p .. + 3, so that a warp's reads of a
-// key are 64 consecutive bytes (fp32).
-template <typename T, int DK> __device__ __forceinline__ float dot_rows(const T *x, const float (&S)[DK / 4], int part)
+// The tile's two groups, by the kMakers threads: 36 pairs (i, j <= i) each, a thread to a pair.  The sums of at most 8
+// gates are taken as they are, without differences.
+template <int DK, bool kTransposed> __device__ __forceinline__ void make_groups(const Stage<DK> &s, Group (&out)[2], int tid)
 {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int m = 0; m < DK / 16; ++m) {
-        const float4 a = Vec4<T>::get(x + 16 * m + 4 * part);
-        s[0] = fmaf(a.x, S[4 * m], s[0]);
-        s[1] = fmaf(a.y, S[4 * m + 1], s[1]);
-        s[2] = fmaf(a.z, S[4 * m + 2], s[2]);
-        s[3] = fmaf(a.w, S[4 * m + 3], s[3]);
+    const int h = tid >> 6, pair = tid & 63;
+    Group &o = out[h];
+    int i = 0, j = pair;
+    while (j > i) j -= ++i;  // pair = i (i + 1) / 2 + j
+    const float *g = s.g + kB * h;
+    if (i < kB) {
+        const float4 *ki = reinterpret_cast<const float4 *>(s.k[kB * h + i]), *kj = reinterpret_cast<const float4 *>(s.k[kB * h + j]);
+        const float4 *qi = reinterpret_cast<const float4 *>(s.q[kB * h + i]);
+        float kk[2] = {}, qk[2] = {};
+#pragma unroll 4
+        for (int c = 0; c < DK / 4; ++c) {
+            const float4 x = ki[c], y = kj[c], z = qi[c];
+            kk[0] = fmaf(x.x, y.x, fmaf(x.y, y.y, kk[0]));
+            kk[1] = fmaf(x.z, y.z, fmaf(x.w, y.w, kk[1]));
+            qk[0] = fmaf(z.x, y.x, fmaf(z.y, y.y, qk[0]));
+            qk[1] = fmaf(z.z, y.z, fmaf(z.w, y.w, qk[1]));
+        }
+        float d = 0.f;  // G_i - G_j
+        for (int t = j + 1; t <= i; ++t) d += g[t];
+        const float D = expf(d);
+        (kTransposed ? o.N[j][i] : o.N[i][j]) = D * (kk[0] + kk[1]);
+        (kTransposed ? o.P[j][i] : o.P[i][j]) = D * (qk[0] + qk[1]);
+        if (i != j) (kTransposed ? o.P[i][j] : o.P[j][i]) = 0.f;
+    } else if (pair >= 36 && pair < 36 + kB) {
+        const int t = pair - 36;
+        float a = 0.f, b = 0.f;
+        for (int u = 0; u < kB; ++u) (u <= t ? a : b) += g[u];
+        o.first[t] = expf(a);
+        o.last[t] = expf(b);
+        if (t == kB - 1) o.whole[0] = expf(a);
     }
-    float r = (s[0] + s[1]) + (s[2] + s[3]);
-    r += __shfl_xor_sync(0xffffffffu, r, 1);
-    return r + __shfl_xor_sync(0xffffffffu, r, 2);
-}
-// S = c S + x w
-template <typename T, int DK> __device__ __forceinline__ void update_rows(float (&S)[DK / 4], float c, const T *x, float w, int part)
-{
-#pragma unroll
-    for (int m = 0; m < DK / 16; ++m) {
-        const float4 a = Vec4<T>::get(x + 16 * m + 4 * part);
-        S[4 * m] = fmaf(a.x, w, c * S[4 * m]);
-        S[4 * m + 1] = fmaf(a.y, w, c * S[4 * m + 1]);
-        S[4 * m + 2] = fmaf(a.z, w, c * S[4 * m + 2]);
-        S[4 * m + 3] = fmaf(a.w, w, c * S[4 * m + 3]);
-    }
-}
-template <int DK> __device__ __forceinline__ void state_out(float *at, const float (&S)[DK / 4], int part, int dv)
-{
-#pragma unroll
-    for (int r = 0; r < DK / 4; ++r) at[(size_t)(r / 4 * 16 + part * 4 + r % 4) * dv] = S[r];
-}
-template <int DK> __device__ __forceinline__ void state_in(const float *at, float (&S)[DK / 4], int part, int dv)
-{
-#pragma unroll
-    for (int r = 0; r < DK / 4; ++r) S[r] = at ? at[(size_t)(r / 4 * 16 + part * 4 + r % 4) * dv] : 0.f;
 }
 
-// kSave: instead of o, the errors e_t (fp32) and the state before each chunk of kC tokens.
-template <typename T, int DK, bool kSave>
-__global__ void __launch_bounds__(128) delta_scan(Params p, float *errors, float *before)
+// DK / 8 lanes share a column: lane `part` holds rows 4 part .. + 3 of each half, so that a warp's reads
+// of a key are consecutive.  The lane's share of x^T S:
+template <int DK> __device__ __forceinline__ float dot_rows(const float *x, const float (&S)[kRows], int part)
 {
-    __shared__ Stage<T, DK> stage[2];
-    const int slices = p.dv / kCols, bh = blockIdx.x / slices, c0 = blockIdx.x % slices * kCols;
-    const int part = threadIdx.x & 3, col = threadIdx.x >> 2;
-    const int b = bh / p.H, bhk = b * p.Hk + bh % p.H / (p.H / p.Hk);
-    const T *k = static_cast<const T *>(p.k) + (size_t)bhk * p.N * DK, *q = static_cast<const T *>(p.q) + (size_t)bhk * p.N * DK;
-    const T *v = static_cast<const T *>(p.v) + (size_t)bh * p.N * p.dv + c0;
-    const float *g = p.g + (size_t)bh * p.N, *beta = p.beta + (size_t)bh * p.N;
-    const size_t at = (size_t)bh * DK * p.dv + c0 + col;
-    float S[DK / 4];
-    state_in<DK>(p.S0 ? p.S0 + at : nullptr, S, part, p.dv);
-    const int tiles = (p.N + kTile - 1) / kTile, chunks = (p.N + kC - 1) / kC;
-    if (tiles > 0) load_stage<T, DK>(stage[0], k, q, v, g, beta, 0, p.N, p.dv, !kSave);
+    const float4 a = Vec4<float>::get(x + 4 * part), b = Vec4<float>::get(x + DK / 2 + 4 * part);
+    const float s = fmaf(a.x, S[0], fmaf(a.y, S[1], fmaf(a.z, S[2], a.w * S[3])));
+    return s + fmaf(b.x, S[4], fmaf(b.y, S[5], fmaf(b.z, S[6], b.w * S[7])));
+}
+template <int DK> __device__ __forceinline__ void add_row(float (&S)[kRows], const float *x, float w, int part)
+{
+    const float4 a = Vec4<float>::get(x + 4 * part), b = Vec4<float>::get(x + DK / 2 + 4 * part);
+    S[0] = fmaf(a.x, w, S[0]), S[1] = fmaf(a.y, w, S[1]), S[2] = fmaf(a.z, w, S[2]), S[3] = fmaf(a.w, w, S[3]);
+    S[4] = fmaf(b.x, w, S[4]), S[5] = fmaf(b.y, w, S[5]), S[6] = fmaf(b.z, w, S[6]), S[7] = fmaf(b.w, w, S[7]);
+}
+// Sums of 8 values over the L lanes of a column: lane p gets that of value p % 8, and with four lanes that of p + 4.
+template <int L> __device__ __forceinline__ void lane_sums(const float (&v)[kB], int part, float (&out)[L == 4 ? 2 : 1])
+{
+    float a[4], b[2];
+    auto swap = [](float keep, float give, int d) { return keep + __shfl_xor_sync(0xffffffffu, give, d); };
+    const bool b0 = part & 1, b1 = part & 2, b2 = part & 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] = swap(b0 ? v[2 * e + 1] : v[2 * e], b0 ? v[2 * e] : v[2 * e + 1], 1);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) b[e] = swap(b1 ? a[2 * e + 1] : a[2 * e], b1 ? a[2 * e] : a[2 * e + 1], 2);
+    if constexpr (L == 4) {
+        out[0] = b[0], out[1] = b[1];
+    } else {
+        out[0] = swap(b2 ? b[1] : b[0], b2 ? b[0] : b[1], 4);
+        if (L == 16) out[0] += __shfl_xor_sync(0xffffffffu, out[0], 8);
+    }
+}
+// All 8 sums in every lane of the column.
+template <int L> __device__ __forceinline__ void all_sums(float (&v)[kB], int part)
+{
+    float own[L == 4 ? 2 : 1];
+    lane_sums<L>(v, part, own);
+#pragma unroll
+    for (int j = 0; j < kB; ++j) v[j] = __shfl_sync(0xffffffffu, own[L == 4 ? j >> 2 : 0], L == 4 ? j & 3 : j, L);
+}
+template <int DK, int DV> __device__ __forceinline__ void state_out(float *at, const float (&S)[kRows], int part)
+{
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) at[(size_t)(r / 4 * (DK / 2) + part * 4 + r % 4) * DV] = S[r];
+}
+template <int DK, int DV> __device__ __forceinline__ void state_in(const float *at, float (&S)[kRows], int part)
+{
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) S[r] = at ? at[(size_t)(r / 4 * (DK / 2) + part * 4 + r % 4) * DV] : 0.f;
+}
+__device__ __forceinline__ void row8(const float *p, float (&v)[kB])
+{
+    const float4 a = Vec4<float>::get(p), b = Vec4<float>::get(p + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// The tiles of one slice in order (kDown: from the last): one(stage, groups, tile) by all but the last four warps
+// on a tile that is there.
+template <int DK, int DV, bool kDown, typename F>
+__device__ __forceinline__ void over_tiles(ScanSmem<DK> &sm, const float *k, const float *q, const float *v, const float *g,
+                                           const float *beta, int n, F one)
+{
+    constexpr int kScanners = kCols * DK / kRows;
+    const int tiles = (n + kTile - 1) / kTile, tid = (int)threadIdx.x - kScanners;
+    const bool maker = tid >= 0;
+    auto tile = [&](int i) { return kDown ? tiles - 1 - i : i; };
+    auto load = [&](int i) {
+        if (i < tiles) load_stage<DK, DV>(sm.stage[i % 3], k, q, v, g, beta, tile(i) * kTile, n, tid);
+        copies_commit();
+    };
+    if (maker) {
+        load(0);
+        load(1);
+        copies_wait<1>();
+        named_bar(1, kMakers);  // tile 0 of all the makers
+        if (tiles > 0) make_groups<DK, kDown>(sm.stage[0], sm.groups[0], tid);
+    }
+    __syncthreads();
     for (int i = 0; i < tiles; ++i) {
-        if (i + 1 < tiles) {
-            load_stage<T, DK>(stage[(i + 1) & 1], k, q, v, g, beta, (i + 1) * kTile, p.N, p.dv, !kSave);
+        if (maker) {
+            load(i + 2);
             copies_wait<1>();
+            named_bar(1, kMakers);
+            if (i + 1 < tiles) make_groups<DK, kDown>(sm.stage[(i + 1) % 3], sm.groups[(i + 1) & 1], tid);
         } else {
-            copies_wait<0>();
-        }
-        __syncthreads();
-        const Stage<T, DK> &s = stage[i & 1];
-        const int t0 = i * kTile, rows = min(kTile, p.N - t0);
-        if (kSave && t0 % kC == 0)
-            state_out<DK>(before + ((size_t)bh * chunks + t0 / kC) * DK * p.dv + c0 + col, S, part, p.dv);
-        for (int t = 0; t < rows; ++t) {
-            const float a = s.alpha[t];
-            const float e = Elem<T>::to_f32(s.v[t][col]) - a * dot_rows<T, DK>(s.k[t], S, part);
-            update_rows<T, DK>(S, a, s.k[t], s.beta[t] * e, part);
-            const size_t row = ((size_t)bh * p.N + t0 + t) * p.dv + c0 + col;
-            if (kSave) {
-                if (part == 0) errors[row] = e;
-            } else {
-                const float o = p.scale * dot_rows<T, DK>(s.q[t], S, part);
-                if (part == 0) static_cast<T *>(p.o)[row] = Elem<T>::from_f32(o);
-            }
+            one(sm.stage[i % 3], sm.groups[i & 1], tile(i));
         }
         __syncthreads();
     }
-    if (!kSave && p.SN) state_out<DK>(p.SN + at, S, part, p.dv);
 }
 
-// The reverse scan of R = dL/dS:  R += q (scale dO)^T;  dX = R^T k;  dv = b dX;  R = a (R - k dv^T).
-// Writes dv, dX (fp32), R behind each chunk (before the chunk's own dO) and dS0.
-template <typename T, int DK>
-__global__ void __launch_bounds__(128) delta_reverse(Params p, float *dX, float *after)
+// kSave: instead of o, the errors e_t and the state before each chunk of kC tokens.
+template <int DK, int DV, bool kSave>
+__global__ void __launch_bounds__(kCols * DK / kRows + kMakers) delta_scan(Params p, float *errors, float *before)
 {
-    __shared__ Stage<T, DK> stage[2];
-    const int slices = p.dv / kCols, bh = blockIdx.x / slices, c0 = blockIdx.x % slices * kCols;
-    const int part = threadIdx.x & 3, col = threadIdx.x >> 2;
+    extern __shared__ float4 smem_raw[];
+    ScanSmem<DK> &sm = *reinterpret_cast<ScanSmem<DK> *>(smem_raw);
+    constexpr int slices = DV / kCols;
+    const int bh = blockIdx.x / slices, c0 = blockIdx.x % slices * kCols;
+    constexpr int L = DK / kRows;  // lanes of a column
+    const int part = threadIdx.x % L, col = threadIdx.x / L % kCols;
+    const bool scanner = threadIdx.x < kCols * L;
     const int b = bh / p.H, bhk = b * p.Hk + bh % p.H / (p.H / p.Hk);
-    const T *k = static_cast<const T *>(p.k) + (size_t)bhk * p.N * DK, *q = static_cast<const T *>(p.q) + (size_t)bhk * p.N * DK;
-    const T *dout = static_cast<const T *>(p.dout) + (size_t)bh * p.N * p.dv + c0;
-    const float *g = p.g + (size_t)bh * p.N, *beta = p.beta + (size_t)bh * p.N;
-    const size_t at = (size_t)bh * DK * p.dv + c0 + col;
-    float R[DK / 4];
-    state_in<DK>(p.dSN ? p.dSN + at : nullptr, R, part, p.dv);
-    const int tiles = (p.N + kTile - 1) / kTile, chunks = (p.N + kC - 1) / kC;
-    if (tiles > 0) load_stage<T, DK>(stage[(tiles - 1) & 1], k, q, dout, g, beta, (tiles - 1) * kTile, p.N, p.dv, true);
-    for (int i = tiles - 1; i >= 0; --i) {
-        if (i > 0) {
-            load_stage<T, DK>(stage[(i - 1) & 1], k, q, dout, g, beta, (i - 1) * kTile, p.N, p.dv, true);
-            copies_wait<1>();
-        } else {
-            copies_wait<0>();
+    const float *k = static_cast<const float *>(p.k) + (size_t)bhk * p.N * DK, *q = static_cast<const float *>(p.q) + (size_t)bhk * p.N * DK;
+    const float *v = static_cast<const float *>(p.v) + (size_t)bh * p.N * DV + c0;
+    const size_t at = (size_t)bh * DK * DV + c0 + col;
+    const int chunks = (p.N + kC - 1) / kC;
+    float S[kRows];
+    state_in<DK, DV>(p.S0 && scanner ? p.S0 + at : nullptr, S, part);
+    over_tiles<DK, DV, false>(sm, k, q, v, p.g + (size_t)bh * p.N, p.beta + (size_t)bh * p.N, p.N,
+                              [&](const Stage<DK> &s, const Group (&groups)[2], int tile) {
+        const int t0 = tile * kTile;
+        if (kSave && t0 % kC == 0)
+            state_out<DK, DV>(before + ((size_t)bh * chunks + t0 / kC) * DK * DV + c0 + col, S, part);
+#pragma unroll 1
+        for (int h = 0; h < kTile / kB; ++h) {
+            const Group &m = groups[h];
+            const int r0 = kB * h;
+            float u[kB], d[kB], first[kB], beta[kB];
+#pragma unroll
+            for (int j = 0; j < kB; ++j) u[j] = dot_rows<DK>(s.k[r0 + j], S, part);
+            if (!kSave)
+#pragma unroll
+                for (int j = 0; j < kB; ++j) d[j] = dot_rows<DK>(s.q[r0 + j], S, part);
+            row8(m.first, first);
+            row8(s.beta + r0, beta);
+            constexpr int kOwn = L == 4 ? 2 : 1;  // tokens whose results the lane writes: part % 8, and with four lanes part + 4
+            float e[kOwn] = {};
+            all_sums<L>(u, part);
+#pragma unroll
+            for (int j = 0; j < kB; ++j) u[j] = fmaf(-first[j], u[j], s.v[r0 + j][col]);
+#pragma unroll
+            for (int j = 0; j < kB; ++j) {
+                float n[kB], x = u[j];
+                row8(m.N[j], n);
+#pragma unroll
+                for (int c = 0; c < j; ++c) x = fmaf(-n[c], u[c], x);
+                if (kSave && (j & (L == 4 ? 3 : 7)) == (part & 7)) e[L == 4 ? j >> 2 : 0] = x;
+                u[j] = beta[j] * x;
+            }
+            if (!kSave) {
+                lane_sums<L>(d, part, e);
+#pragma unroll
+                for (int y = 0; y < kOwn; ++y) {
+                    const int t = (part & 7) + 4 * y;
+                    float w[kB];
+                    row8(m.P[t], w);
+                    e[y] *= m.first[t];
+#pragma unroll
+                    for (int c = 0; c < kB; ++c) e[y] = fmaf(w[c], u[c], e[y]);
+                    e[y] *= p.scale;
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < kOwn; ++y) {
+                const int t = t0 + r0 + (part & 7) + 4 * y;
+                if (part < 8 && t < p.N) (kSave ? errors : static_cast<float *>(p.o))[((size_t)bh * p.N + t) * DV + c0 + col] = e[y];
+            }
+            float last[kB];
+            row8(m.last, last);
+            const float whole = m.whole[0];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) S[r] *= whole;
+#pragma unroll
+            for (int j = 0; j < kB; ++j) add_row<DK>(S, s.k[r0 + j], last[j] * u[j], part);
         }
-        __syncthreads();
-        const Stage<T, DK> &s = stage[i & 1];
-        const int t0 = i * kTile, rows = min(kTile, p.N - t0);
-        if (i == tiles - 1 || (t0 + kTile) % kC == 0)
-            state_out<DK>(after + ((size_t)bh * chunks + t0 / kC) * DK * p.dv + c0 + col, R, part, p.dv);
-        for (int t = rows - 1; t >= 0; --t) {
-            update_rows<T, DK>(R, 1.f, s.q[t], p.scale * Elem<T>::to_f32(s.v[t][col]), part);
-            const float x = dot_rows<T, DK>(s.k[t], R, part), y = s.beta[t] * x, a = s.alpha[t];
-            update_rows<T, DK>(R, a, s.k[t], -a * y, part);
-            const size_t row = ((size_t)bh * p.N + t0 + t) * p.dv + c0 + col;
-            if (part == 0) {
-                dX[row] = x;
-                static_cast<T *>(p.dv_out)[row] = Elem<T>::from_f32(y);
+    });
+    if (!kSave && p.SN && scanner) state_out<DK, DV>(p.SN + at, S, part);
+}
+
+// The reverse scan of R = dL/dS, 8 tokens together from the last on:
+//   dX_j = exp(G_8 - G_j) R^T k_j + sum_{i>=j} D_ij (q_i.k_j) scale dO_i - sum_{i>j} D_ij (k_i.k_j) b_i dX_i,   dv = b dX,
+//   R' = exp(G_8) R + sum_i exp(G_i) (q_i scale dO_i^T - k_i dv_i^T).
+// Writes dv, dX, R behind each chunk (before the chunk's own dO) and dS0.
+template <int DK, int DV>
+__global__ void __launch_bounds__(kCols * DK / kRows + kMakers) delta_reverse(Params p, float *dX, float *after)
+{
+    extern __shared__ float4 smem_raw[];
+    ScanSmem<DK> &sm = *reinterpret_cast<ScanSmem<DK> *>(smem_raw);
+    constexpr int slices = DV / kCols;
+    const int bh = blockIdx.x / slices, c0 = blockIdx.x % slices * kCols;
+    constexpr int L = DK / kRows;  // lanes of a column
+    const int part = threadIdx.x % L, col = threadIdx.x / L % kCols;
+    const bool scanner = threadIdx.x < kCols * L;
+    const int b = bh / p.H, bhk = b * p.Hk + bh % p.H / (p.H / p.Hk);
+    const float *k = static_cast<const float *>(p.k) + (size_t)bhk * p.N * DK, *q = static_cast<const float *>(p.q) + (size_t)bhk * p.N * DK;
+    const float *dout = static_cast<const float *>(p.dout) + (size_t)bh * p.N * DV + c0;
+    const size_t at = (size_t)bh * DK * DV + c0 + col;
+    const int tiles = (p.N + kTile - 1) / kTile, chunks = (p.N + kC - 1) / kC;
+    float R[kRows];
+    state_in<DK, DV>(p.dSN && scanner ? p.dSN + at : nullptr, R, part);
+    over_tiles<DK, DV, true>(sm, k, q, dout, p.g + (size_t)bh * p.N, p.beta + (size_t)bh * p.N, p.N,
+                             [&](const Stage<DK> &s, const Group (&groups)[2], int tile) {
+        const int t0 = tile * kTile;
+        if (tile == tiles - 1 || (t0 + kTile) % kC == 0)
+            state_out<DK, DV>(after + ((size_t)bh * chunks + t0 / kC) * DK * DV + c0 + col, R, part);
+#pragma unroll 1
+        for (int h = kTile / kB - 1; h >= 0; --h) {
+            const Group &m = groups[h];
+            const int r0 = kB * h;
+            float x[kB], o[kB], w[kB], beta[kB];
+#pragma unroll
+            for (int j = 0; j < kB; ++j) {
+                x[j] = dot_rows<DK>(s.k[r0 + j], R, part);
+                o[j] = p.scale * s.v[r0 + j][col];
+            }
+            row8(m.last, w);
+            row8(s.beta + r0, beta);
+            all_sums<L>(x, part);
+#pragma unroll
+            for (int j = 0; j < kB; ++j) x[j] *= w[j];
+#pragma unroll
+            for (int j = 0; j < kB; ++j) {
+                row8(m.P[j], w);
+#pragma unroll
+                for (int c = j; c < kB; ++c) x[j] = fmaf(w[c], o[c], x[j]);
+            }
+            constexpr int kOwn = L == 4 ? 2 : 1;
+            float dx[kOwn] = {}, y[kB];  // dX of the lane's own tokens; y = dv
+#pragma unroll
+            for (int j = kB - 1; j >= 0; --j) {
+                row8(m.N[j], w);
+#pragma unroll
+                for (int c = kB - 1; c > j; --c) x[j] = fmaf(-w[c], y[c], x[j]);
+                if ((j & (L == 4 ? 3 : 7)) == (part & 7)) dx[L == 4 ? j >> 2 : 0] = x[j];
+                y[j] = beta[j] * x[j];
+            }
+#pragma unroll
+            for (int u = 0; u < kOwn; ++u) {
+                const int t = t0 + r0 + (part & 7) + 4 * u;
+                const size_t row = ((size_t)bh * p.N + t) * DV + c0 + col;
+                if (part < 8 && t < p.N) {
+                    dX[row] = dx[u];
+                    static_cast<float *>(p.dv_out)[row] = s.beta[t - t0] * dx[u];
+                }
+            }
+            row8(m.first, w);
+            const float whole = m.whole[0];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) R[r] *= whole;
+#pragma unroll
+            for (int j = 0; j < kB; ++j) {
+                add_row<DK>(R, s.q[r0 + j], w[j] * o[j], part);
+                add_row<DK>(R, s.k[r0 + j], -w[j] * y[j], part);
             }
         }
-        __syncthreads();
-    }
-    if (p.dS0) state_out<DK>(p.dS0 + at, R, part, p.dv);
+    });
+    if (p.dS0 && scanner) state_out<DK, DV>(p.dS0 + at, R, part);
 }
 
 // Gradients within a chunk of kC tokens of one key head, over the heads that share it.  With
@@ -213,7 +391,7 @@ template <int DK, int DV> struct LocalSmem {
     float hi[kC], lo[kC], first[kC], last[kC], beta[kC], reads[kC], writes[kC], sums[8];
 };
 
-template <typename T, int DK, int DV>
+template <int DK, int DV>
 __global__ void __launch_bounds__(256) delta_local(Params p, const float *errors, const float *dX, const float *before,
                                                    const float *after)
 {
@@ -226,8 +404,8 @@ __global__ void __launch_bounds__(256) delta_local(Params p, const float *errors
     for (int i = tid; i < kC * DK; i += 256) {
         const int r = i / DK, c = i % DK;
         const size_t at = ((size_t)bhk * p.N + t0 + r) * DK + c;
-        s.K[r][c] = r < rows ? Elem<T>::to_f32(static_cast<const T *>(p.k)[at]) : 0.f;
-        s.Q[r][c] = r < rows ? Elem<T>::to_f32(static_cast<const T *>(p.q)[at]) : 0.f;
+        s.K[r][c] = r < rows ? static_cast<const float *>(p.k)[at] : 0.f;
+        s.Q[r][c] = r < rows ? static_cast<const float *>(p.q)[at] : 0.f;
     }
     float dq[kI][4] = {}, dk[kI][4] = {};
     for (int h = 0; h < group; ++h) {
@@ -256,7 +434,7 @@ __global__ void __launch_bounds__(256) delta_local(Params p, const float *errors
             for (int c = tid % 8; c < DV; c += 8) {
                 const size_t at = ((size_t)bh * p.N + t0 + r) * DV + c;
                 const float e = r < rows ? errors[at] : 0.f, x = r < rows ? dX[at] : 0.f;
-                s.O[r][c] = r < rows ? p.scale * Elem<T>::to_f32(static_cast<const T *>(p.dout)[at]) : 0.f;
+                s.O[r][c] = r < rows ? p.scale * static_cast<const float *>(p.dout)[at] : 0.f;
                 s.U[r][c] = bt * e;
                 s.Y[r][c] = bt * x;
                 db = fmaf(x, e, db);
@@ -383,8 +561,8 @@ __global__ void __launch_bounds__(256) delta_local(Params p, const float *errors
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const size_t at = ((size_t)bhk * p.N + t0 + i0 + i) * DK + kg + m * kKG;
-                static_cast<T *>(p.dq)[at] = Elem<T>::from_f32(dq[i][m]);
-                static_cast<T *>(p.dk_out)[at] = Elem<T>::from_f32(dk[i][m]);
+                static_cast<float *>(p.dq)[at] = dq[i][m];
+                static_cast<float *>(p.dk_out)[at] = dk[i][m];
             }
 }
 
@@ -456,27 +634,40 @@ __global__ void __launch_bounds__(128) delta_step_kernel(Params p, float *S)
     }
 }
 
-// Calls f with the element type and d_k as types.
-template <typename F> la_status by_width(const DeltaProblem &p, F f)
+// Calls f with d_k, or with d_k and d_v, as types.
+template <typename F> la_status by_width(int d, F f)
 {
-    if (p.dtype == LA_F32)
-        return p.dk == 32 ? f(0.f, std::integral_constant<int, 32>()) : p.dk == 64 ? f(0.f, std::integral_constant<int, 64>())
-                                                                                   : f(0.f, std::integral_constant<int, 128>());
-    const __nv_bfloat16 h{};
-    return p.dk == 32 ? f(h, std::integral_constant<int, 32>()) : p.dk == 64 ? f(h, std::integral_constant<int, 64>())
-                                                                             : f(h, std::integral_constant<int, 128>());
+    return d == 32   ? f(std::integral_constant<int, 32>())
+           : d == 64 ? f(std::integral_constant<int, 64>())
+                     : f(std::integral_constant<int, 128>());
+}
+template <typename F> la_status by_widths(const DeltaProblem &p, F f)
+{
+    return by_width(p.dk, [&](auto dk) { return by_width(p.dv, [&](auto dv) { return f(dk, dv); }); });
 }
 
-template <typename T, int DK, int DV>
+// A scan's launch: a block to 32 columns of a head's state.
+template <int DK, int DV, typename... Args>
+la_status launch_scan(const DeltaProblem &p, void (*kernel)(Params, Args...), const Params &prm, Args... args)
+{
+    const int smem = (int)sizeof(ScanSmem<DK>);
+    const la_status st = ensure_smem(reinterpret_cast<const void *>(kernel), smem);
+    if (st != LA_OK) return st;
+    count_launches();
+    kernel<<<(unsigned)(p.B * p.H * (DV / kCols)), kCols * DK / kRows + kMakers, smem, p.stream>>>(prm, args...);
+    return cuda_status(cudaGetLastError());
+}
+
+template <int DK, int DV>
 la_status launch_local(const DeltaProblem &p, const Params &prm, const float *errors, const float *dX, const float *before,
                        const float *after)
 {
     const int smem = (int)sizeof(LocalSmem<DK, DV>);
-    const la_status st = ensure_smem(reinterpret_cast<const void *>(&delta_local<T, DK, DV>), smem);
+    const la_status st = ensure_smem(reinterpret_cast<const void *>(&delta_local<DK, DV>), smem);
     if (st != LA_OK) return st;
     const unsigned grid = (unsigned)p.B * p.Hk * ceil_div(p.N, kC);
     count_launches();
-    delta_local<T, DK, DV><<<grid, 256, smem, p.stream>>>(prm, errors, dX, before, after);
+    delta_local<DK, DV><<<grid, 256, smem, p.stream>>>(prm, errors, dX, before, after);
     return cuda_status(cudaGetLastError());
 }
 
@@ -487,12 +678,9 @@ using namespace delta;
 
 la_status delta_forward_simt(const DeltaProblem &p)
 {
-    const Params prm = params_of(p);
-    return by_width(p, [&](auto t, auto dk) {
-        count_launches();
-        delta_scan<decltype(t), decltype(dk)::value, false>
-            <<<(unsigned)(p.B * p.H * (p.dv / kCols)), 128, 0, p.stream>>>(prm, nullptr, nullptr);
-        return cuda_status(cudaGetLastError());
+    return by_widths(p, [&](auto dk, auto dv) {
+        constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
+        return launch_scan<DK, DV>(p, &delta_scan<DK, DV, false>, params_of(p), (float *)nullptr, (float *)nullptr);
     });
 }
 
@@ -507,31 +695,26 @@ la_status delta_backward_simt(const DeltaProblem &p)
     const Params prm = params_of(p);
     const size_t rows = (size_t)p.B * p.H * p.N * p.dv, states = (size_t)p.B * p.H * ceil_div(p.N, kC) * p.dk * p.dv;
     float *before = p.scratch, *after = before + states, *errors = after + states, *dX = errors + rows;
-    return by_width(p, [&](auto t, auto dk) {
-        using T = decltype(t);
-        constexpr int DK = decltype(dk)::value;
-        const unsigned grid = (unsigned)(p.B * p.H * (p.dv / kCols));
-        if (p.N > 0) {
-            count_launches();
-            delta_scan<T, DK, true><<<grid, 128, 0, p.stream>>>(prm, errors, before);
-        }
-        count_launches();
-        delta_reverse<T, DK><<<grid, 128, 0, p.stream>>>(prm, dX, after);
-        const la_status st = cuda_status(cudaGetLastError());
+    return by_widths(p, [&](auto dk, auto dv) {
+        constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
+        la_status st = p.N > 0 ? launch_scan<DK, DV>(p, &delta_scan<DK, DV, true>, prm, errors, before) : LA_OK;
+        if (st == LA_OK) st = launch_scan<DK, DV>(p, &delta_reverse<DK, DV>, prm, dX, after);
         if (st != LA_OK || p.N == 0) return st;
-        return p.dv == 32   ? launch_local<T, DK, 32>(p, prm, errors, dX, before, after)
-               : p.dv == 64 ? launch_local<T, DK, 64>(p, prm, errors, dX, before, after)
-                            : launch_local<T, DK, 128>(p, prm, errors, dX, before, after);
+        return launch_local<DK, DV>(p, prm, errors, dX, before, after);
     });
 }
 
 la_status delta_step(const DeltaProblem &p, float *S)
 {
     const Params prm = params_of(p);
-    return by_width(p, [&](auto t, auto dk) {
+    return by_width(p.dk, [&](auto dk) {
+        constexpr int DK = decltype(dk)::value;
+        const unsigned grid = (unsigned)(p.B * p.H * (p.dv / kCols));
         count_launches();
-        delta_step_kernel<decltype(t), decltype(dk)::value>
-            <<<(unsigned)(p.B * p.H * (p.dv / kCols)), 128, 0, p.stream>>>(prm, S);
+        if (p.dtype == LA_F32)
+            delta_step_kernel<float, DK><<<grid, 128, 0, p.stream>>>(prm, S);
+        else
+            delta_step_kernel<__nv_bfloat16, DK><<<grid, 128, 0, p.stream>>>(prm, S);
         return cuda_status(cudaGetLastError());
     });
 }

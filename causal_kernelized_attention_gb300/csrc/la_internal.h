@@ -230,7 +230,7 @@ la_status delta_forward_simt(const DeltaProblem &p);
 la_status delta_backward_simt(const DeltaProblem &p);
 size_t delta_backward_simt_scratch(const DeltaProblem &p);  // bytes at p.scratch
 la_status delta_step(const DeltaProblem &p, float *S);
-// The same on the tensor cores (la_tc_delta.cu): bf16, dk and dv 64 or 128, N > 0.
+// The same on the tensor cores (la_tc_delta.cu): bf16, N > 0.
 bool delta_tc_eligible(const DeltaProblem &p);
 la_status delta_forward_tc(const DeltaProblem &p);
 size_t delta_forward_tc_scratch(const DeltaProblem &p);  // bytes at p.scratch

@@ -1,4 +1,4 @@
-// Gated delta rule on the tensor cores: the forward pass (bf16, d_k and d_v in {64, 128}), two launches: the
+// Gated delta rule on the tensor cores: the forward pass (bf16), two launches: the
 // chunks' matrices, then the scan.
 #include "la_tc_delta_scan.cuh"
 
@@ -23,8 +23,8 @@ template <int DK, int DV> la_status forward(const DeltaProblem &p)
     const Params prm = params_of(p);
     uint8_t *images = reinterpret_cast<uint8_t *>(p.scratch);
     CUtensorMap mq, mk, mv, mo;
-    la_status st = make_map(&mv, p.v, p.B * p.H, p.N, DV, kChunk);
-    if (st == LA_OK) st = make_map(&mo, p.o, p.B * p.H, p.N, DV, kChunk);
+    la_status st = make_map(&mv, p.v, p.B * p.H, p.N, p.dv, kChunk);
+    if (st == LA_OK) st = make_map(&mo, p.o, p.B * p.H, p.N, p.dv, kChunk);
     if (st == LA_OK) st = ensure_smem((const void *)delta_scan_tc<DK, DV>, (int)sizeof(Sm));
     if (st == LA_OK) st = prepare<DK, false>(p, prm, images, &mq, &mk);
     if (st != LA_OK) return st;
@@ -40,18 +40,18 @@ using namespace delta;
 
 bool delta_tc_eligible(const DeltaProblem &p)
 {
-    return p.dtype == LA_BF16 && p.dk >= 64 && p.dv >= 64 && p.N > 0;
+    return p.dtype == LA_BF16 && p.N > 0;
 }
 
 size_t delta_forward_tc_scratch(const DeltaProblem &p)
 {
-    return (size_t)p.B * p.H * ceil_div(p.N, kChunk) * (p.dk == 64 ? Layout<64>::forward_bytes : Layout<128>::forward_bytes);
+    return (size_t)p.B * p.H * ceil_div(p.N, kChunk) * (p.dk <= 64 ? Layout<64>::forward_bytes : Layout<128>::forward_bytes);
 }
 
 la_status delta_forward_tc(const DeltaProblem &p)
 {
-    if (p.dk == 64) return p.dv == 64 ? forward<64, 64>(p) : forward<64, 128>(p);
-    return p.dv == 64 ? forward<128, 64>(p) : forward<128, 128>(p);
+    if (p.dk <= 64) return p.dv <= 64 ? forward<64, 64>(p) : forward<64, 128>(p);
+    return p.dv <= 64 ? forward<128, 64>(p) : forward<128, 128>(p);
 }
 
 la_status tc_delta_read_status(cudaStream_t s, unsigned *bits) { return read_status(g_launched, g_delta_status, s, bits); }

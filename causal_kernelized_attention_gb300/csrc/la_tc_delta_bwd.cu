@@ -1,4 +1,4 @@
-// Gated delta rule on the tensor cores: the backward pass (bf16, d_k and d_v in {64, 128}), three launches: the
+// Gated delta rule on the tensor cores: the backward pass (bf16), three launches: the
 // chunks' matrices; the scan of the states forward and of their gradients in reverse, side by side; and
 // the gradients of each chunk, all chunks at once.
 #include "la_tc_delta_scan.cuh"
@@ -537,11 +537,11 @@ template <int DK, int DV> la_status backward(const DeltaProblem &p)
     uint8_t *images = reinterpret_cast<uint8_t *>(p.scratch), *before = images + n * Sc::images, *after = before + n * Sc::state;
     uint8_t *errors = after + n * Sc::state, *dx = errors + n * Sc::rows;
     CUtensorMap mq, mk, mv, mo, mdq, mdk, mdv;
-    la_status st = make_map(&mv, p.v, p.B * p.H, p.N, DV, kChunk);
-    if (st == LA_OK) st = make_map(&mo, p.dout, p.B * p.H, p.N, DV, kChunk);
-    if (st == LA_OK) st = make_map(&mdq, p.dq, p.B * p.Hk, p.N, DK, kChunk);
-    if (st == LA_OK) st = make_map(&mdk, p.dk_out, p.B * p.Hk, p.N, DK, kChunk);
-    if (st == LA_OK) st = make_map(&mdv, p.dv_out, p.B * p.H, p.N, DV, kChunk);
+    la_status st = make_map(&mv, p.v, p.B * p.H, p.N, p.dv, kChunk);
+    if (st == LA_OK) st = make_map(&mo, p.dout, p.B * p.H, p.N, p.dv, kChunk);
+    if (st == LA_OK) st = make_map(&mdq, p.dq, p.B * p.Hk, p.N, p.dk, kChunk);
+    if (st == LA_OK) st = make_map(&mdk, p.dk_out, p.B * p.Hk, p.N, p.dk, kChunk);
+    if (st == LA_OK) st = make_map(&mdv, p.dv_out, p.B * p.H, p.N, p.dv, kChunk);
     if (st == LA_OK) st = ensure_smem((const void *)delta_scans_tc<DK, DV>, (int)scans);
     if (st == LA_OK) st = ensure_smem((const void *)delta_local_tc<DK, DV>, (int)sizeof(Loc));
     if (st == LA_OK) st = prepare<DK, true>(p, prm, images, &mq, &mk);
@@ -564,14 +564,14 @@ using namespace delta;
 size_t delta_backward_tc_scratch(const DeltaProblem &p)
 {
     const size_t n = (size_t)p.B * p.H * ceil_div(p.N, kChunk);
-    if (p.dk == 64) return n * (p.dv == 64 ? Scratch4<64, 64>::total : Scratch4<64, 128>::total);
-    return n * (p.dv == 64 ? Scratch4<128, 64>::total : Scratch4<128, 128>::total);
+    if (p.dk <= 64) return n * (p.dv <= 64 ? Scratch4<64, 64>::total : Scratch4<64, 128>::total);
+    return n * (p.dv <= 64 ? Scratch4<128, 64>::total : Scratch4<128, 128>::total);
 }
 
 la_status delta_backward_tc(const DeltaProblem &p)
 {
-    if (p.dk == 64) return p.dv == 64 ? backward<64, 64>(p) : backward<64, 128>(p);
-    return p.dv == 64 ? backward<128, 64>(p) : backward<128, 128>(p);
+    if (p.dk <= 64) return p.dv <= 64 ? backward<64, 64>(p) : backward<64, 128>(p);
+    return p.dv <= 64 ? backward<128, 64>(p) : backward<128, 128>(p);
 }
 
 la_status tc_delta_bwd_read_status(cudaStream_t s, unsigned *bits) { return read_status(g_launched, g_delta_status, s, bits); }

@@ -1,4 +1,4 @@
-// The preparing kernel and the scan of the tensor-core gated delta rule (bf16, d_k and d_v in {64, 128}): forward
+// The preparing kernel and the scan of the tensor-core gated delta rule (bf16; d_k and d_v of 32 as 64): forward
 // (la_tc_delta.cu), and for the backward pass forward without o and in reverse (la_tc_delta_bwd.cu).
 //
 // The scan is a chain, chunk by chunk.  It is laid out so that a CTA owns a (b, h) and every product has
@@ -648,10 +648,13 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
         const bool live = 32 * (warp & 3) < DV;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t tS = tl + Col::S + part * kKeys, tP = tl + Col::parts + part * (kKeys / 2);
-        const size_t state = (size_t)bh * DK * DV + (size_t)part * kKeys * DV + f;
+        // (widths of 32 fill half of the tiles: their copies read zeros past the rows' ends)
+        const bool mine = f < p.dv;
+        const size_t state = (size_t)bh * p.dk * p.dv + (size_t)part * kKeys * p.dv + f;
         float s[kKeys];  // the state: key features part kKeys ..
 #pragma unroll
-        for (int e = 0; e < kKeys; ++e) s[e] = first_state && live ? first_state[state + (size_t)e * DV] : 0.f;
+        for (int e = 0; e < kKeys; ++e)
+            s[e] = first_state && mine && part * kKeys + e < p.dk ? first_state[state + (size_t)e * p.dv] : 0.f;
         for (int c = 0; ok && c < chunks; ++c) {
             const int st = c & 1;
             const uint32_t ph = (uint32_t)c & 1u;
@@ -724,9 +727,10 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                 for (int e = 0; e < 16; ++e) s[x + e] = fmaf(whole, s[x + e], __uint_as_float(a[e]));
             }
         }
-        if (ok && last_state && live)
+        if (ok && last_state && mine)
 #pragma unroll
-            for (int e = 0; e < kKeys; ++e) last_state[state + (size_t)e * DV] = s[e];
+            for (int e = 0; e < kKeys; ++e)
+                if (part * kKeys + e < p.dk) last_state[state + (size_t)e * p.dv] = s[e];
     } else if (warp < kMmaWarp) {
         const int f = 32 * (warp & 3) + lane;
         const bool live = 32 * (warp & 3) < DV;
@@ -852,8 +856,8 @@ template <int DK, bool kBack>
 la_status prepare(const DeltaProblem &p, const Params &prm, uint8_t *images, CUtensorMap *mq, CUtensorMap *mk)
 {
     typedef PrepSmem<DK, kBack> Sm;
-    la_status st = make_map(mq, p.q, p.B * p.Hk, p.N, DK, kChunk);
-    if (st == LA_OK) st = make_map(mk, p.k, p.B * p.Hk, p.N, DK, kChunk);
+    la_status st = make_map(mq, p.q, p.B * p.Hk, p.N, p.dk, kChunk);
+    if (st == LA_OK) st = make_map(mk, p.k, p.B * p.Hk, p.N, p.dk, kChunk);
     if (st == LA_OK) st = ensure_smem((const void *)delta_prepare<DK, kBack>, (int)sizeof(Sm));
     if (st != LA_OK) return st;
     g_launched = true;

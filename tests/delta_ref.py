@@ -86,9 +86,9 @@ def delta_tolerance(dtype, out, parts):
     return 8 * 2.0 ** -17 if parts and dtype != torch.float32 else 128 * U
 
 
-def assert_near(got, want, tol, what="", block=32):
+def assert_near(got, want, tol, what="", block=32, floor=0.02):
     """Blocks of `block` tokens of each (b, h) (or whole states) within tol of their own 2-norm; a block far below
-    the others counts as a fiftieth of their mean."""
+    the others counts as `floor` of their mean."""
     got, want = got.detach().cpu().to(F64), want.to(F64)
     assert got.shape == want.shape, (what, got.shape, want.shape)
     assert bool(torch.isfinite(got).all()), (what, "not finite")
@@ -102,7 +102,7 @@ def assert_near(got, want, tol, what="", block=32):
         off.append((got - want)[:, :, t:t + block].square().sum((2, 3)).sqrt())
         size.append(want[:, :, t:t + block].square().sum((2, 3)).sqrt())
     off, size = torch.stack(off, 2), torch.stack(size, 2)
-    bound = tol * size.clamp(min=float(size.mean()) / 50)
+    bound = tol * size.clamp(min=float(size.mean()) * floor)
     worst = float((off / bound.clamp(min=TINY)).max())
     assert worst <= 1, (what, "off by", worst, "of what is allowed, in block", int((off / bound.clamp(min=TINY)).argmax()))
 

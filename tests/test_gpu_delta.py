@@ -32,7 +32,10 @@ def check(got, want, dtype, names):
         out = torch.float32 if i in F32 else dtype
         if got[i] is not None:
             assert got[i].dtype == out
-            assert_near(got[i], want[i], delta_tolerance(dtype, out, True), i)
+            # dg and dbeta are sums of products of either sign (dbeta_t = sum_f dX_f E_f, relative errors r of its factors
+            # independent: off by r (2 sum_f (dX_f E_f)^2)^(1/2)), so that a token's sum may cancel to far less than what
+            # its error goes by.  That is as large as for the other tokens, whose mean size stands for it.
+            assert_near(got[i], want[i], delta_tolerance(dtype, out, True), i, floor=1.0 if i in ("dg", "dbeta") else 0.02)
 
 
 CASES = [
