@@ -13,6 +13,7 @@
 #include "la_common.cuh"
 #include "la_delta.cuh"
 #include "la_internal.h"
+#include "la_tc_common.cuh"
 
 namespace la {
 namespace delta {
@@ -20,7 +21,7 @@ namespace {
 
 constexpr int kTile = 16;   // tokens staged in shared memory at a time
 constexpr int kB = 8;       // tokens taken together
-constexpr int kCols = 32;   // columns of S per block
+constexpr int kStepCols = 32;  // columns of S a block of the decode step
 constexpr int kRows = 8;    // rows of S a lane holds: d_k / 8 lanes share a column
 constexpr int kMakers = 128;  // threads that load and prepare the tiles
 constexpr int kC = 32;      // tokens of a chunk of the backward pass
@@ -43,9 +44,9 @@ __device__ __forceinline__ void named_bar(int id, int threads) { asm volatile("b
 template <int n> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
 
 // The rows of one tile: keys, queries (four floats further apart than they are long: the pairs' dot products read
-// eight rows at once), a slice of 32 values (forward: v, reverse: dO), gates.
-template <int DK> struct alignas(16) Stage {
-    float k[kTile][DK + 4], q[kTile][DK + 4], v[kTile][kCols];
+// eight rows at once), a slice of CB values (forward: v, reverse: dO), gates.
+template <int DK, int CB> struct alignas(16) Stage {
+    float k[kTile][DK + 4], q[kTile][DK + 4], v[kTile][CB];
     float g[kTile], beta[kTile];
 };
 // What a tile's groups of 8 tokens need: D_ij (k_i.k_j) below the diagonal, D_ij (q_i.k_j) up to it (and their
@@ -54,15 +55,15 @@ struct alignas(16) Group {
     float N[kB][kB], P[kB][kB], first[kB], last[kB], whole[4];
 };
 // Three tiles are under way: one scanned, the next one's groups made by the last four warps, a third loaded.
-template <int DK> struct ScanSmem {
-    Stage<DK> stage[3];
+template <int DK, int CB> struct ScanSmem {
+    Stage<DK, CB> stage[3];
     Group groups[2][2];
 };
 
 // Rows t0 .. of one tile, by the kMakers threads; rows past the sequence are zeros (which leave S as it is).
-template <int DK, int DV>
-__device__ __forceinline__ void load_stage(Stage<DK> &s, const float *k, const float *q, const float *v, const float *g,
-                                           const float *beta, int t0, int n, int tid)
+template <int DK, int CB>
+__device__ __forceinline__ void load_stage(Stage<DK, CB> &s, const float *k, const float *q, const float *v, const float *g,
+                                           const float *beta, int t0, int n, int dv, int tid)
 {
     const int rows = min(kTile, n - t0);
     auto copy = [&](float *dst, const float *src, bool on) {
@@ -75,9 +76,9 @@ __device__ __forceinline__ void load_stage(Stage<DK> &s, const float *k, const f
         copy(&s.k[r][c], k + at, r < rows);
         copy(&s.q[r][c], q + at, r < rows);
     }
-    {
-        const int r = tid / (kCols / 4), c = tid % (kCols / 4) * 4;
-        copy(&s.v[r][c], v + (r < rows ? (size_t)(t0 + r) * DV + c : 0), r < rows);
+    if (tid < kTile * CB / 4) {
+        const int r = tid / (CB / 4), c = tid % (CB / 4) * 4;
+        copy(&s.v[r][c], v + (r < rows ? (size_t)(t0 + r) * dv + c : 0), r < rows);
     }
     if (tid < 2 * kTile) {
         const int t = tid & (kTile - 1);
@@ -90,7 +91,8 @@ __device__ __forceinline__ void load_stage(Stage<DK> &s, const float *k, const f
 
 // The tile's two groups, by the kMakers threads: 36 pairs (i, j <= i) each, a thread to a pair.  The sums of at most 8
 // gates are taken as they are, without differences.
-template <int DK, bool kTransposed> __device__ __forceinline__ void make_groups(const Stage<DK> &s, Group (&out)[2], int tid)
+template <int DK, int CB, bool kTransposed>
+__device__ __forceinline__ void make_groups(const Stage<DK, CB> &s, Group (&out)[2], int tid)
 {
     const int h = tid >> 6, pair = tid & 63;
     Group &o = out[h];
@@ -164,15 +166,15 @@ template <int L> __device__ __forceinline__ void all_sums(float (&v)[kB], int pa
 #pragma unroll
     for (int j = 0; j < kB; ++j) v[j] = __shfl_sync(0xffffffffu, own[L == 4 ? j >> 2 : 0], L == 4 ? j & 3 : j, L);
 }
-template <int DK, int DV> __device__ __forceinline__ void state_out(float *at, const float (&S)[kRows], int part)
+template <int DK> __device__ __forceinline__ void state_out(float *at, const float (&S)[kRows], int part, int dv)
 {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) at[(size_t)(r / 4 * (DK / 2) + part * 4 + r % 4) * DV] = S[r];
+    for (int r = 0; r < kRows; ++r) at[(size_t)(r / 4 * (DK / 2) + part * 4 + r % 4) * dv] = S[r];
 }
-template <int DK, int DV> __device__ __forceinline__ void state_in(const float *at, float (&S)[kRows], int part)
+template <int DK> __device__ __forceinline__ void state_in(const float *at, float (&S)[kRows], int part, int dv)
 {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) S[r] = at ? at[(size_t)(r / 4 * (DK / 2) + part * 4 + r % 4) * DV] : 0.f;
+    for (int r = 0; r < kRows; ++r) S[r] = at ? at[(size_t)(r / 4 * (DK / 2) + part * 4 + r % 4) * dv] : 0.f;
 }
 __device__ __forceinline__ void row8(const float *p, float (&v)[kB])
 {
@@ -182,16 +184,16 @@ __device__ __forceinline__ void row8(const float *p, float (&v)[kB])
 
 // The tiles of one slice in order (kDown: from the last): one(stage, groups, tile) by all but the last four warps
 // on a tile that is there.
-template <int DK, int DV, bool kDown, typename F>
-__device__ __forceinline__ void over_tiles(ScanSmem<DK> &sm, const float *k, const float *q, const float *v, const float *g,
-                                           const float *beta, int n, F one)
+template <int DK, int CB, bool kDown, typename F>
+__device__ __forceinline__ void over_tiles(ScanSmem<DK, CB> &sm, const float *k, const float *q, const float *v, const float *g,
+                                           const float *beta, int n, int dv, F one)
 {
-    constexpr int kScanners = kCols * DK / kRows;
+    constexpr int kScanners = CB * DK / kRows;
     const int tiles = (n + kTile - 1) / kTile, tid = (int)threadIdx.x - kScanners;
     const bool maker = tid >= 0;
     auto tile = [&](int i) { return kDown ? tiles - 1 - i : i; };
     auto load = [&](int i) {
-        if (i < tiles) load_stage<DK, DV>(sm.stage[i % 3], k, q, v, g, beta, tile(i) * kTile, n, tid);
+        if (i < tiles) load_stage<DK, CB>(sm.stage[i % 3], k, q, v, g, beta, tile(i) * kTile, n, dv, tid);
         copies_commit();
     };
     if (maker) {
@@ -199,7 +201,7 @@ __device__ __forceinline__ void over_tiles(ScanSmem<DK> &sm, const float *k, con
         load(1);
         copies_wait<1>();
         named_bar(1, kMakers);  // tile 0 of all the makers
-        if (tiles > 0) make_groups<DK, kDown>(sm.stage[0], sm.groups[0], tid);
+        if (tiles > 0) make_groups<DK, CB, kDown>(sm.stage[0], sm.groups[0], tid);
     }
     __syncthreads();
     for (int i = 0; i < tiles; ++i) {
@@ -207,7 +209,7 @@ __device__ __forceinline__ void over_tiles(ScanSmem<DK> &sm, const float *k, con
             load(i + 2);
             copies_wait<1>();
             named_bar(1, kMakers);
-            if (i + 1 < tiles) make_groups<DK, kDown>(sm.stage[(i + 1) % 3], sm.groups[(i + 1) & 1], tid);
+            if (i + 1 < tiles) make_groups<DK, CB, kDown>(sm.stage[(i + 1) % 3], sm.groups[(i + 1) & 1], tid);
         } else {
             one(sm.stage[i % 3], sm.groups[i & 1], tile(i));
         }
@@ -216,28 +218,27 @@ __device__ __forceinline__ void over_tiles(ScanSmem<DK> &sm, const float *k, con
 }
 
 // kSave: instead of o, the errors e_t and the state before each chunk of kC tokens.
-template <int DK, int DV, bool kSave>
-__global__ void __launch_bounds__(kCols * DK / kRows + kMakers) delta_scan(Params p, float *errors, float *before)
+template <int DK, int CB, bool kSave>
+__global__ void __launch_bounds__(CB * DK / kRows + kMakers) delta_scan(Params p, float *errors, float *before)
 {
     extern __shared__ float4 smem_raw[];
-    ScanSmem<DK> &sm = *reinterpret_cast<ScanSmem<DK> *>(smem_raw);
-    constexpr int slices = DV / kCols;
-    const int bh = blockIdx.x / slices, c0 = blockIdx.x % slices * kCols;
+    ScanSmem<DK, CB> &sm = *reinterpret_cast<ScanSmem<DK, CB> *>(smem_raw);
+    const int slices = p.dv / CB, bh = blockIdx.x / slices, c0 = blockIdx.x % slices * CB;
     constexpr int L = DK / kRows;  // lanes of a column
-    const int part = threadIdx.x % L, col = threadIdx.x / L % kCols;
-    const bool scanner = threadIdx.x < kCols * L;
+    const int part = threadIdx.x % L, col = threadIdx.x / L % CB;
+    const bool scanner = threadIdx.x < CB * L;
     const int b = bh / p.H, bhk = b * p.Hk + bh % p.H / (p.H / p.Hk);
     const float *k = static_cast<const float *>(p.k) + (size_t)bhk * p.N * DK, *q = static_cast<const float *>(p.q) + (size_t)bhk * p.N * DK;
-    const float *v = static_cast<const float *>(p.v) + (size_t)bh * p.N * DV + c0;
-    const size_t at = (size_t)bh * DK * DV + c0 + col;
+    const float *v = static_cast<const float *>(p.v) + (size_t)bh * p.N * p.dv + c0;
+    const size_t at = (size_t)bh * DK * p.dv + c0 + col;
     const int chunks = (p.N + kC - 1) / kC;
     float S[kRows];
-    state_in<DK, DV>(p.S0 && scanner ? p.S0 + at : nullptr, S, part);
-    over_tiles<DK, DV, false>(sm, k, q, v, p.g + (size_t)bh * p.N, p.beta + (size_t)bh * p.N, p.N,
-                              [&](const Stage<DK> &s, const Group (&groups)[2], int tile) {
+    state_in<DK>(p.S0 && scanner ? p.S0 + at : nullptr, S, part, p.dv);
+    over_tiles<DK, CB, false>(sm, k, q, v, p.g + (size_t)bh * p.N, p.beta + (size_t)bh * p.N, p.N, p.dv,
+                              [&](const Stage<DK, CB> &s, const Group (&groups)[2], int tile) {
         const int t0 = tile * kTile;
         if (kSave && t0 % kC == 0)
-            state_out<DK, DV>(before + ((size_t)bh * chunks + t0 / kC) * DK * DV + c0 + col, S, part);
+            state_out<DK>(before + ((size_t)bh * chunks + t0 / kC) * DK * p.dv + c0 + col, S, part, p.dv);
 #pragma unroll 1
         for (int h = 0; h < kTile / kB; ++h) {
             const Group &m = groups[h];
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kCols * DK / kRows + kMakers) delta_scan(Param
 #pragma unroll
             for (int y = 0; y < kOwn; ++y) {
                 const int t = t0 + r0 + (part & 7) + 4 * y;
-                if (part < 8 && t < p.N) (kSave ? errors : static_cast<float *>(p.o))[((size_t)bh * p.N + t) * DV + c0 + col] = e[y];
+                if (part < 8 && t < p.N) (kSave ? errors : static_cast<float *>(p.o))[((size_t)bh * p.N + t) * p.dv + c0 + col] = e[y];
             }
             float last[kB];
             row8(m.last, last);
@@ -291,35 +292,34 @@ __global__ void __launch_bounds__(kCols * DK / kRows + kMakers) delta_scan(Param
             for (int j = 0; j < kB; ++j) add_row<DK>(S, s.k[r0 + j], last[j] * u[j], part);
         }
     });
-    if (!kSave && p.SN && scanner) state_out<DK, DV>(p.SN + at, S, part);
+    if (!kSave && p.SN && scanner) state_out<DK>(p.SN + at, S, part, p.dv);
 }
 
 // The reverse scan of R = dL/dS, 8 tokens together from the last on:
 //   dX_j = exp(G_8 - G_j) R^T k_j + sum_{i>=j} D_ij (q_i.k_j) scale dO_i - sum_{i>j} D_ij (k_i.k_j) b_i dX_i,   dv = b dX,
 //   R' = exp(G_8) R + sum_i exp(G_i) (q_i scale dO_i^T - k_i dv_i^T).
 // Writes dv, dX, R behind each chunk (before the chunk's own dO) and dS0.
-template <int DK, int DV>
-__global__ void __launch_bounds__(kCols * DK / kRows + kMakers) delta_reverse(Params p, float *dX, float *after)
+template <int DK, int CB>
+__global__ void __launch_bounds__(CB * DK / kRows + kMakers) delta_reverse(Params p, float *dX, float *after)
 {
     extern __shared__ float4 smem_raw[];
-    ScanSmem<DK> &sm = *reinterpret_cast<ScanSmem<DK> *>(smem_raw);
-    constexpr int slices = DV / kCols;
-    const int bh = blockIdx.x / slices, c0 = blockIdx.x % slices * kCols;
+    ScanSmem<DK, CB> &sm = *reinterpret_cast<ScanSmem<DK, CB> *>(smem_raw);
+    const int slices = p.dv / CB, bh = blockIdx.x / slices, c0 = blockIdx.x % slices * CB;
     constexpr int L = DK / kRows;  // lanes of a column
-    const int part = threadIdx.x % L, col = threadIdx.x / L % kCols;
-    const bool scanner = threadIdx.x < kCols * L;
+    const int part = threadIdx.x % L, col = threadIdx.x / L % CB;
+    const bool scanner = threadIdx.x < CB * L;
     const int b = bh / p.H, bhk = b * p.Hk + bh % p.H / (p.H / p.Hk);
     const float *k = static_cast<const float *>(p.k) + (size_t)bhk * p.N * DK, *q = static_cast<const float *>(p.q) + (size_t)bhk * p.N * DK;
-    const float *dout = static_cast<const float *>(p.dout) + (size_t)bh * p.N * DV + c0;
-    const size_t at = (size_t)bh * DK * DV + c0 + col;
+    const float *dout = static_cast<const float *>(p.dout) + (size_t)bh * p.N * p.dv + c0;
+    const size_t at = (size_t)bh * DK * p.dv + c0 + col;
     const int tiles = (p.N + kTile - 1) / kTile, chunks = (p.N + kC - 1) / kC;
     float R[kRows];
-    state_in<DK, DV>(p.dSN && scanner ? p.dSN + at : nullptr, R, part);
-    over_tiles<DK, DV, true>(sm, k, q, dout, p.g + (size_t)bh * p.N, p.beta + (size_t)bh * p.N, p.N,
-                             [&](const Stage<DK> &s, const Group (&groups)[2], int tile) {
+    state_in<DK>(p.dSN && scanner ? p.dSN + at : nullptr, R, part, p.dv);
+    over_tiles<DK, CB, true>(sm, k, q, dout, p.g + (size_t)bh * p.N, p.beta + (size_t)bh * p.N, p.N, p.dv,
+                             [&](const Stage<DK, CB> &s, const Group (&groups)[2], int tile) {
         const int t0 = tile * kTile;
         if (tile == tiles - 1 || (t0 + kTile) % kC == 0)
-            state_out<DK, DV>(after + ((size_t)bh * chunks + t0 / kC) * DK * DV + c0 + col, R, part);
+            state_out<DK>(after + ((size_t)bh * chunks + t0 / kC) * DK * p.dv + c0 + col, R, part, p.dv);
 #pragma unroll 1
         for (int h = kTile / kB - 1; h >= 0; --h) {
             const Group &m = groups[h];
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kCols * DK / kRows + kMakers) delta_reverse(Pa
 #pragma unroll
             for (int u = 0; u < kOwn; ++u) {
                 const int t = t0 + r0 + (part & 7) + 4 * u;
-                const size_t row = ((size_t)bh * p.N + t) * DV + c0 + col;
+                const size_t row = ((size_t)bh * p.N + t) * p.dv + c0 + col;
                 if (part < 8 && t < p.N) {
                     dX[row] = dx[u];
                     static_cast<float *>(p.dv_out)[row] = s.beta[t - t0] * dx[u];
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kCols * DK / kRows + kMakers) delta_reverse(Pa
             }
         }
     });
-    if (p.dS0 && scanner) state_out<DK, DV>(p.dS0 + at, R, part);
+    if (p.dS0 && scanner) state_out<DK>(p.dS0 + at, R, part, p.dv);
 }
 
 // Gradients within a chunk of kC tokens of one key head, over the heads that share it.  With
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(128) delta_step_kernel(Params p, float *S)
 {
     __shared__ float ks[DK], qs[DK];
     __shared__ float4 part[2][4][8];
-    const int slices = p.dv / kCols, bh = blockIdx.x / slices, c0 = blockIdx.x % slices * kCols;
+    const int slices = p.dv / kStepCols, bh = blockIdx.x / slices, c0 = blockIdx.x % slices * kStepCols;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cg = tid & 7, r0 = tid >> 3;
     const int bhk = bh / p.H * p.Hk + bh % p.H / (p.H / p.Hk);
     float4 *at = reinterpret_cast<float4 *>(S + (size_t)bh * DK * p.dv + c0) + cg;
@@ -646,16 +646,27 @@ template <typename F> la_status by_widths(const DeltaProblem &p, F f)
     return by_width(p.dk, [&](auto dk) { return by_width(p.dv, [&](auto dv) { return f(dk, dv); }); });
 }
 
-// A scan's launch: a block to 32 columns of a head's state.
-template <int DK, int DV, typename... Args>
+// A scan's launch, with CB columns of a head's state to a block.
+template <int DK, int CB, typename... Args>
 la_status launch_scan(const DeltaProblem &p, void (*kernel)(Params, Args...), const Params &prm, Args... args)
 {
-    const int smem = (int)sizeof(ScanSmem<DK>);
+    const int smem = (int)sizeof(ScanSmem<DK, CB>);
     const la_status st = ensure_smem(reinterpret_cast<const void *>(kernel), smem);
     if (st != LA_OK) return st;
     count_launches();
-    kernel<<<(unsigned)(p.B * p.H * (DV / kCols)), kCols * DK / kRows + kMakers, smem, p.stream>>>(prm, args...);
+    kernel<<<(unsigned)(p.B * p.H * (p.dv / CB)), CB * DK / kRows + kMakers, smem, p.stream>>>(prm, args...);
     return cuda_status(cudaGetLastError());
+}
+// Blocks of 32 columns or of 8: a narrow block's chain is shorter (at 128 value features, d_k 32, 64, 128: 90, 129, 217 us
+// for 1000 tokens against 115, 163, 412), a wide one shares its tiles with more columns.  The time is a block's, times the
+// rounds in which the machine takes them all, two narrow ones to an SM, wide ones two at d_k 32 and one above.
+bool wide_slices(const DeltaProblem &p)
+{
+    const int sms = tc::sm_count();
+    const long long columns = (long long)p.B * p.H * p.dv;
+    auto rounds = [](long long blocks, int slots) { return (double)((blocks + slots - 1) / slots); };
+    const double longer = p.dk == 128 ? 1.9 : 1.27;
+    return longer * rounds(columns / 32, p.dk == 32 ? 2 * sms : sms) < rounds(columns / 8, 2 * sms);
 }
 
 template <int DK, int DV>
@@ -678,9 +689,11 @@ using namespace delta;
 
 la_status delta_forward_simt(const DeltaProblem &p)
 {
-    return by_widths(p, [&](auto dk, auto dv) {
-        constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
-        return launch_scan<DK, DV>(p, &delta_scan<DK, DV, false>, params_of(p), (float *)nullptr, (float *)nullptr);
+    float *const none = nullptr;
+    return by_width(p.dk, [&](auto dk) {
+        constexpr int DK = decltype(dk)::value;
+        return wide_slices(p) ? launch_scan<DK, 32>(p, &delta_scan<DK, 32, false>, params_of(p), none, none)
+                              : launch_scan<DK, 8>(p, &delta_scan<DK, 8, false>, params_of(p), none, none);
     });
 }
 
@@ -697,8 +710,14 @@ la_status delta_backward_simt(const DeltaProblem &p)
     float *before = p.scratch, *after = before + states, *errors = after + states, *dX = errors + rows;
     return by_widths(p, [&](auto dk, auto dv) {
         constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
-        la_status st = p.N > 0 ? launch_scan<DK, DV>(p, &delta_scan<DK, DV, true>, prm, errors, before) : LA_OK;
-        if (st == LA_OK) st = launch_scan<DK, DV>(p, &delta_reverse<DK, DV>, prm, dX, after);
+        la_status st = LA_OK;
+        if (wide_slices(p)) {
+            if (p.N > 0) st = launch_scan<DK, 32>(p, &delta_scan<DK, 32, true>, prm, errors, before);
+            if (st == LA_OK) st = launch_scan<DK, 32>(p, &delta_reverse<DK, 32>, prm, dX, after);
+        } else {
+            if (p.N > 0) st = launch_scan<DK, 8>(p, &delta_scan<DK, 8, true>, prm, errors, before);
+            if (st == LA_OK) st = launch_scan<DK, 8>(p, &delta_reverse<DK, 8>, prm, dX, after);
+        }
         if (st != LA_OK || p.N == 0) return st;
         return launch_local<DK, DV>(p, prm, errors, dX, before, after);
     });
@@ -709,7 +728,7 @@ la_status delta_step(const DeltaProblem &p, float *S)
     const Params prm = params_of(p);
     return by_width(p.dk, [&](auto dk) {
         constexpr int DK = decltype(dk)::value;
-        const unsigned grid = (unsigned)(p.B * p.H * (p.dv / kCols));
+        const unsigned grid = (unsigned)(p.B * p.H * (p.dv / kStepCols));
         count_launches();
         if (p.dtype == LA_F32)
             delta_step_kernel<float, DK><<<grid, 128, 0, p.stream>>>(prm, S);

@@ -614,8 +614,6 @@ __global__ void __launch_bounds__(256) norm_apply(Params p, int cols)
 }
 
 // ---------------------------------------------------------------- launches
-constexpr int kSMs = 152;
-
 Params params_of(const NormProblem &p)
 {
     Params q{};
@@ -651,7 +649,7 @@ TokenShape token_shape(const NormProblem &p)
         b = t;
     }
     const long long unit = G / a;
-    const long long need = (all + per_block - 1) / per_block, most = (long long)kSMs * (p.backward ? 4 : 8);
+    const long long need = (all + per_block - 1) / per_block, most = (long long)tc::sm_count() * (p.backward ? 4 : 8);
     s.blocks = (need < most ? need : most);
     s.blocks = (s.blocks + unit - 1) / unit * unit;
     s.slots = s.blocks * per_block;
@@ -672,7 +670,7 @@ MapShape map_shape(const NormProblem &p)
     s.cols = ceil_div(n, s.zs);
     const int ny = 256 / s.cols;
     const long long blocks = (long long)p.B * s.zs;
-    int want = (int)((kSMs * 4 + blocks - 1) / blocks);
+    int want = (int)((tc::sm_count() * 4 + blocks - 1) / blocks);
     const int most = ceil_div(p.L, ny * 6);
     want = want < most ? want : most;
     if (want < 1) want = 1;
