@@ -17,9 +17,9 @@ delta_scans_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const int n = p.B * p.H, bh = (int)blockIdx.x;
     if (bh < n)
-        scan_body<DK, DV, kSave>(map_q, map_k, map_v, map_v, p, p.S0, nullptr, images, before, errors, bh, smem_raw);
+        scan_body<DK, DV, kSave>(map_q, map_k, map_v, map_v, p, p.S0, nullptr, images, nullptr, before, errors, bh, smem_raw);
     else
-        scan_body<DK, DV, kReverse>(map_q, map_k, map_do, map_do, p, p.dSN, p.dS0, images, after, dx, bh - n, smem_raw);
+        scan_body<DK, DV, kReverse>(map_q, map_k, map_do, map_do, p, p.dSN, p.dS0, images, nullptr, after, dx, bh - n, smem_raw);
 }
 
 // ---------------------------------------------------------------- gradients of a chunk

@@ -157,38 +157,18 @@ template <int DK> __device__ __forceinline__ void put_row(uint32_t taddr, uint8_
     }
 }
 
-template <int DK, bool kBack>
-__global__ void __launch_bounds__(kBack ? 256 : 128)
-delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k, const Params p, uint8_t *images)
+// One chunk by kBack ? 256 : 128 threads `tid`, whose barrier is sync(); barriers of sm initialised, `ok` unless it aborted.
+// `turn`: how many chunks the threads have prepared before (the parity of sm.full).  `bar`: a barrier for 128 of them
+// (kBack: and the next one, for the others).  `stay` leaves the last store to the caller, committed by an elected
+// thread of warp 0, and the other stores visible to the device.
+template <int DK, bool kBack, typename Sync>
+__device__ __forceinline__ void prepare_chunk(PrepSmem<DK, kBack> &sm, const CUtensorMap &map_q, const CUtensorMap &map_k, const Params &p,
+                                              uint8_t *image, int bh, int chunk, int tid, int warp, uint32_t tmem, uint32_t turn,
+                                              bool sound, int bar, bool stay, Sync sync)
 {
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    typedef PrepSmem<DK, kBack> Sm;
     typedef Layout<DK> Lay;
     constexpr int kNT = kBack ? 256 : 128;
-    constexpr uint32_t kTmem = kBack ? 256 : DK;  // scores, then W over them; Z, then W2 over it
-    Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
-    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
-    const int chunks = (p.N + kChunk - 1) / kChunk, bh = blockIdx.x / chunks, chunk = blockIdx.x % chunks, t0 = chunk * kChunk;
-    const int bhk = bh / p.H * p.Hk + bh % p.H / (p.H / p.Hk);
-    uint8_t *image = images + (size_t)blockIdx.x * (kBack ? Lay::backward_bytes : Lay::forward_bytes);
-    if (tid == 0) {
-        mbar_init(&sm.full, 1);
-        mbar_init(&sm.done, 1);
-        sm.abort = (smem_u32(smem_raw) & 1023u) == 0 ? 0 : 1;
-        if (sm.abort) atomicOr(&g_delta_status, kStatusTimeout);
-        fence_mbar_init();
-    }
-    if (warp == 0) {
-        tmem_alloc(&sm.tmem_base, kTmem);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    griddep_wait();
-    griddep_launch_dependents();
-    const uint32_t tmem = sm.tmem_base;
-    const bool sound = !aborted(&sm.abort);
+    const int lane = tid & 31, t0 = chunk * kChunk, bhk = bh / p.H * p.Hk + bh % p.H / (p.H / p.Hk);
     if (warp == 0 && sound && elect_one()) {
         mbar_arrive_expect_tx(&sm.full, DK / 64 * 2 * kSq);
         for (int x = 0; x < DK / 64; ++x) {
@@ -209,7 +189,7 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         }
         sm.G[tid] = G;
     }
-    __syncthreads();
+    sync();
     if (tid < 64) {
         const double half = sm.G[31], G = sm.G[tid] + (tid >= 32 ? half : 0.0), end = sm.G[63] + half;
         const float first = expf((float)G), last = expf((float)(end - G));
@@ -226,7 +206,7 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     }
     bool ok = sound;
     if (warp == 0) {
-        ok = ok && wait_bar_warp(&g_delta_status, &sm.abort, &sm.full, 0);
+        ok = ok && wait_bar_warp(&g_delta_status, &sm.abort, &sm.full, turn & 1u);
         if (ok) {
             tc_fence_after();
             if (elect_one()) {
@@ -240,7 +220,7 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         }
         __syncwarp();
     }
-    __syncthreads();
+    sync();
     ok = sound && wait_bar_warp(&g_delta_status, &sm.abort, &sm.done, 0);
     tc_fence_after();
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -297,12 +277,12 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         }
     }
     tc_fence_before();
-    __syncthreads();
+    sync();
     if (!kBack || warp < 4)
-        invert(sm.a[0], tid & 127, 1);
+        invert(sm.a[0], tid & 127, bar);
     else
-        invert(sm.a[kBack ? 1 : 0], tid & 127, 2);
-    __syncthreads();
+        invert(sm.a[kBack ? 1 : 0], tid & 127, bar + 1);
+    sync();
     // T to global memory, and -T exp(G) over the rows of Q
     uint8_t *tp[2] = {sm.qk[0], DK == 64 ? sm.extra : sm.qk[DK / 64 - 1]};
     for (int u = tid; u < kChunk * 8; u += kNT) {
@@ -323,7 +303,7 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     }
     fence_proxy_async_smem();
     tc_fence_before();
-    __syncthreads();
+    sync();
     const int row = 32 * (warp & 3) + lane, half = warp >> 2;
     // W = -T exp(G) K: rows 0-63 of 128 (the rest of the left operand is whatever follows it)
     constexpr uint32_t id_w = idesc_bf16_f32(128, DK, false, true), id_w2 = idesc_bf16_f32(128, DK, true, true);
@@ -364,7 +344,7 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 }
             fence_proxy_async_smem();
             tc_fence_before();
-            __syncthreads();
+            sync();
             if (warp == 0) {
                 tc_fence_after();
                 if (ok && elect_one()) {
@@ -410,7 +390,8 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         if (ok && row < 64) put_row<DK>(tl + (which ? tW2 : tW), sm.w, row, half * (DK / 2), kBack ? (half + 1) * (DK / 2) : DK);
         fence_proxy_async_smem();
         tc_fence_before();
-        __syncthreads();
+        if (stay) __threadfence();
+        sync();
         if (warp == 0) {
             if (ok && elect_one()) {
                 if (kBack && which == 0) {
@@ -419,17 +400,76 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 }
                 bulk_store(image + (which ? Lay::w2 : Lay::w), sm.w, Lay::w_bytes);
                 tma_store_commit();
-                if (kBack && which == 0)
+                if ((kBack && which == 0) || stay)
                     tma_store_wait_read_all();
                 else
                     tma_store_wait_all();
             }
             __syncwarp();
         }
-        if (kBack && which == 0) __syncthreads();
+        if (kBack && which == 0) sync();
     }
+}
+
+constexpr uint32_t prep_columns(int DK, bool back) { return back ? 256 : DK; }  // of TMEM: scores, then W over them; Z, then W2 over it
+
+// The barriers and the sound state of one set of preparing threads.
+template <int DK, bool kBack> __device__ __forceinline__ void prepare_start(PrepSmem<DK, kBack> &sm)
+{
+    mbar_init(&sm.full, 1);
+    mbar_init(&sm.done, 1);
+    sm.abort = (smem_u32(&sm) & 1023u) == 0 ? 0 : 1;
+    if (sm.abort) atomicOr(&g_delta_status, kStatusTimeout);
+}
+
+template <int DK, bool kBack>
+__global__ void __launch_bounds__(kBack ? 256 : 128)
+delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k, const Params p, uint8_t *images)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    typedef PrepSmem<DK, kBack> Sm;
+    typedef Layout<DK> Lay;
+    Sm &sm = *reinterpret_cast<Sm *>(smem_raw);
+    const int tid = threadIdx.x, warp = uniform_warp(), chunks = (p.N + kChunk - 1) / kChunk;
+    if (tid == 0) {
+        prepare_start(sm);
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&sm.tmem_base, prep_columns(DK, kBack));
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(tmem, kTmem);
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t tmem = sm.tmem_base;
+    uint8_t *image = images + (size_t)blockIdx.x * (kBack ? Lay::backward_bytes : Lay::forward_bytes);
+    prepare_chunk<DK, kBack>(sm, map_q, map_k, p, image, blockIdx.x / chunks, blockIdx.x % chunks, tid, warp, tmem, 0,
+                             !aborted(&sm.abort), 1, false, [] { __syncthreads(); });
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, prep_columns(DK, kBack));
+}
+
+// Waits (with the limit of every wait) until another CTA of the launch has published a chunk's image.
+__device__ __forceinline__ bool wait_flag(const unsigned *flag, int *abort_flag)
+{
+    const uint64_t t0 = globaltimer_ns();
+    bool there;
+    while (!(there = __all_sync(0xffffffffu, ld_acquire_gpu(flag) != 0))) {
+        if (__any_sync(0xffffffffu, aborted(abort_flag))) return false;
+        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) {
+            *(volatile int *)abort_flag = 1;
+            atomicOr(&g_delta_status, kStatusTimeout);
+            return false;
+        }
+        __nanosleep(100);
+    }
+    fence_proxy_async_global();
+    return there;
 }
 
 // ---------------------------------------------------------------- scan
@@ -483,7 +523,8 @@ template <int DK> struct Columns {
 template <int DK, int DV, int kMode>
 __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_v,
                                           const CUtensorMap &map_o, const Params &p, const float *first_state, float *last_state,
-                                          const uint8_t *images, uint8_t *states, uint8_t *rows, int bh, uint8_t *smem_raw)
+                                          const uint8_t *images, const unsigned *ready, uint8_t *states, uint8_t *rows, int bh,
+                                          uint8_t *smem_raw)
 {
     typedef ScanSmem<DK, DV, kMode> Sm;
     typedef Columns<DK> Col;
@@ -529,6 +570,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
             const uint8_t *img = images + ((size_t)bh * chunks + x) * kStride;
             // V and the matrices of chunk c - 2 end with its E (where E's rows are staged over W, with their store)
             if (c >= 2 && !(ok = wait(Sm::kOutOverW ? &sm.rows_read[st] : &sm.e_full[st], (uint32_t)((c >> 1) - 1) & 1u))) break;
+            if (ready && !(ok = wait_flag(ready + (size_t)bh * chunks + x, abort_flag))) break;
             if (__any_sync(0xffffffffu, aborted(abort_flag))) break;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&sm.full[st], DV / 64 * kSq + Sm::kMats + (kKeep ? kScanScalars : 0));
