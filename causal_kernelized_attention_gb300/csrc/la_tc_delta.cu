@@ -65,12 +65,17 @@ delta_both_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             __syncwarp();
         };
         uint32_t turn = 0;
-        for (long long i = (long long)blockIdx.x * kSets + set; i < items; i += step, ++turn) {
+        const long long start = (long long)blockIdx.x * kSets + set;
+        float2 gates = start < items ? load_gates(p, (int)(start % heads), (int)(start / heads), tid) : make_float2(0.f, 0.f);
+        for (long long i = start; i < items; i += step, ++turn) {
             if (__any_sync(0xffffffffu, aborted(&mine.abort))) break;
             const int chunk = (int)(i / heads), bh = (int)(i % heads);
             const long long at = (long long)bh * chunks + chunk;
+            const float2 now = gates;
+            const long long next = i + step;
+            if (next < items) gates = load_gates(p, (int)(next % heads), (int)(next / heads), tid);
             named_bar_sync(1 + set, 128);  // the last chunk's operands are read
-            prepare_chunk<DK, false>(mine, map_q, map_k, p, images + at * Layout<DK>::forward_bytes, bh, chunk, tid, warp & 3, tmem, turn,
+            prepare_chunk<DK, false>(mine, map_q, map_k, p, images + at * Layout<DK>::forward_bytes, now, bh, chunk, tid, warp & 3, tmem, turn,
                                      true, 1 + set, true, [&] { named_bar_sync(1 + set, 128); });
             last = at;
             publish();

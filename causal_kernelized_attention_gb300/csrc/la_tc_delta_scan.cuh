@@ -36,7 +36,7 @@ template <int DK, bool kBack> struct PrepSmem {
     uint8_t p[kBack ? 2 : 1][kBack ? 2 * kSq : 1024];  // P, as 128 rows of which the second half is not used
     Square a[kBack ? 2 : 1];
     Scalars s;
-    double G[kChunk];
+    long long G[kChunk];
     uint64_t full, done;
     uint32_t tmem_base;
     int abort;
@@ -157,13 +157,22 @@ template <int DK> __device__ __forceinline__ void put_row(uint32_t taddr, uint8_
     }
 }
 
+// (g, beta) of the chunk's token tid; tokens past the sequence leave the state as it is.
+__device__ __forceinline__ float2 load_gates(const Params &p, int bh, int chunk, int tid)
+{
+    const int t = chunk * kChunk + tid;
+    if (tid >= kChunk || t >= p.N) return make_float2(0.f, 0.f);
+    const size_t at = (size_t)bh * p.N + t;
+    return make_float2(__ldg(p.g + at), __ldg(p.beta + at));
+}
+
 // One chunk by kBack ? 256 : 128 threads `tid`, whose barrier is sync(); barriers of sm initialised, `ok` unless it aborted.
-// `turn`: how many chunks the threads have prepared before (the parity of sm.full).  `bar`: a barrier for 128 of them
+// `gates`: load_gates of the thread.  `turn`: how many chunks the threads have prepared before (the parity of sm.full).  `bar`: a barrier for 128 of them
 // (kBack: and the next one, for the others).  `stay` leaves the last store to the caller, committed by an elected
 // thread of warp 0, and the other stores visible to the device.
 template <int DK, bool kBack, typename Sync>
 __device__ __forceinline__ void prepare_chunk(PrepSmem<DK, kBack> &sm, const CUtensorMap &map_q, const CUtensorMap &map_k, const Params &p,
-                                              uint8_t *image, int bh, int chunk, int tid, int warp, uint32_t tmem, uint32_t turn,
+                                              uint8_t *image, float2 gates, int bh, int chunk, int tid, int warp, uint32_t tmem, uint32_t turn,
                                               bool sound, int bar, bool stay, Sync sync)
 {
     typedef Layout<DK> Lay;
@@ -177,31 +186,43 @@ __device__ __forceinline__ void prepare_chunk(PrepSmem<DK, kBack> &sm, const CUt
         }
     }
     __syncwarp();
-    float gate = 0.f;
-    if (tid < 64) {  // the running sum of the gates (a gate below -200 closes as well as -inf), summed in 64 bits
-        const size_t at = (size_t)bh * p.N + t0 + tid;
-        gate = t0 + tid < p.N ? p.beta[at] : 0.f;
-        const float g = t0 + tid < p.N ? p.g[at] : 0.f;
-        double G = g < -200.f ? -200.f : g;
+    // The running sum of the gates, in units of 2^-40 as 64-bit integers (doubles cost a thousand cycles here, and floats
+    // would lose what differences of large sums need).  A gate below -200 closes as well as -inf.
+    long long G = 0;
+    if (tid < 64) {
+        G = __float2ll_rn(fminf(fmaxf(gates.x, -200.f), 65536.f) * 0x1p40f);
+        if (gates.x != gates.x) gates.y = gates.x;  // a NaN gate makes what the token writes NaN
+#pragma unroll
         for (int d = 1; d < 32; d *= 2) {
-            const double x = __shfl_up_sync(0xffffffffu, G, d);
+            const long long x = __shfl_up_sync(0xffffffffu, G, d);
             if (lane >= d) G += x;
         }
         sm.G[tid] = G;
     }
     sync();
     if (tid < 64) {
-        const double half = sm.G[31], G = sm.G[tid] + (tid >= 32 ? half : 0.0), end = sm.G[63] + half;
-        const float first = expf((float)G), last = expf((float)(end - G));
+        const long long half = sm.G[31], end = sm.G[63] + half;
+        if (tid >= 32) G += half;
+        // as two floats, times log2(e) (its head and tail)
+        auto scaled = [](long long v, float &lo) {
+            const float h = __ll2float_rn(v) * 0x1p-40f, l = __ll2float_rn(v - __float2ll_rn(h * 0x1p40f)) * 0x1p-40f;
+            constexpr double kLog2e = 1.4426950408889634074;
+            constexpr float head = (float)kLog2e, tail = (float)(kLog2e - (double)head);
+            const float hi = h * head;
+            lo = fmaf(h, head, -hi) + fmaf(h, tail, l * head);
+            return hi;
+        };
+        float lo, lo_end;
+        const float hi = scaled(G, lo), rest = scaled(end - G, lo_end);
+        const float first = exp2f(hi) * exp2f(lo), last = exp2f(rest) * exp2f(lo_end);
         Scalars &s = sm.s;
-        const double G2 = G * 1.4426950408889634074;
-        s.hi[tid] = (float)G2;
-        s.lo[tid] = (float)(G2 - (double)(float)G2);
+        s.hi[tid] = hi;
+        s.lo[tid] = lo;
         s.first[tid] = first;
         s.last[tid] = last;
-        s.beta[tid] = gate;
-        s.back[tid] = -gate * first;
-        s.write[tid] = gate * last;
+        s.beta[tid] = gates.y;
+        s.back[tid] = -gates.y * first;
+        s.write[tid] = gates.y * last;
         s.spare[tid] = 0.f;
     }
     bool ok = sound;
@@ -445,8 +466,9 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     griddep_wait();
     griddep_launch_dependents();
     const uint32_t tmem = sm.tmem_base;
+    const int bh = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
     uint8_t *image = images + (size_t)blockIdx.x * (kBack ? Lay::backward_bytes : Lay::forward_bytes);
-    prepare_chunk<DK, kBack>(sm, map_q, map_k, p, image, blockIdx.x / chunks, blockIdx.x % chunks, tid, warp, tmem, 0,
+    prepare_chunk<DK, kBack>(sm, map_q, map_k, p, image, load_gates(p, bh, chunk, tid), bh, chunk, tid, warp, tmem, 0,
                              !aborted(&sm.abort), 1, false, [] { __syncthreads(); });
     tc_fence_before();
     __syncthreads();
