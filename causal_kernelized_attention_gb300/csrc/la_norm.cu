@@ -121,8 +121,8 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes)
 // to one group of channels (slot % G), so weights, and the sums for their gradients, stay in
 // registers, and walks over the tokens; the launch has a whole number of slots for each group.  The loads of the
 // next tokens are under way meanwhile: each thread copies its vectors asynchronously into a ring of its own in
-// shared memory, kRing tokens deep (held in registers, one token ahead, they left HBM idle: 45 us against
-// 38 us for 16384 tokens of 16 x 128 gated channels in bf16); channels by ones are loaded one token ahead.
+// shared memory, kRing tokens deep (held in registers, one token ahead, they were too few to keep HBM busy: 47 us
+// against 41 for 16384 tokens of 16 x 128 gated channels in bf16); channels by ones are loaded one token ahead.
 constexpr int kRing = 4;
 __device__ __forceinline__ void copy_async(void *dst, const void *src, bool on)  // 16 bytes, or zeros
 {
@@ -613,6 +613,189 @@ __global__ void __launch_bounds__(256) norm_apply(Params p, int cols)
     }
 }
 
+// ---------------------------------------------------------------- groups that fit on chip
+// An entry's slab of neighbouring groups (rows of 128 bytes or more where there are as many channels) is held in the shared
+// memory of one cluster, its positions split over the CTAs: one launch, every tensor read once.  A thread keeps
+// to a column of VEC channels, so that what it copies in (asynchronously) only it reads; the sums of a group go over threads,
+// then over the CTAs of the cluster, in a fixed order.
+constexpr int kFusedThreads = 256, kFusedMost = 8 /* CTAs of a cluster */, kFusedGroups = 64 /* of a slab */;
+constexpr int kFusedSmem = 200 << 10, kFusedShare = 72 << 10;  // of a CTA: at most, and if the cluster can be that large (three share an SM)
+struct Slab {
+    int groups, slabs, rows, cols;  // groups of a slab, slabs of an entry, positions a CTA, columns
+};
+
+template <typename T, int VEC, bool kGate, bool kBack, bool kAct>
+__global__ void __launch_bounds__(kFusedThreads) norm_fused(Params p, Slab q)
+{
+    typedef Pack<T, VEC> Pk;
+    typedef typename Pk::Raw Raw;
+    extern __shared__ __align__(16) uint8_t shared[];
+    __shared__ float mine[2][kFusedGroups], all[kFusedMost][2][kFusedGroups], done[2][kFusedGroups];
+    sm100::griddep_wait();
+    sm100::griddep_launch_dependents();
+    const int rank = (int)sm100::cluster_ctarank(), size = (int)sm100::cluster_size();
+    const int entry = blockIdx.x / size / q.slabs, slab = blockIdx.x / size % q.slabs;
+    const int g0 = slab * q.groups, groups = min(q.groups, p.G - g0), width = groups * p.D;
+    const int tx = threadIdx.x % q.cols, ty = threadIdx.x / q.cols, ny = kFusedThreads / q.cols, c = tx * VEC;
+    const bool on = ty < ny && c < width;
+    const int l0 = rank * q.rows, rows = max(0, min(q.rows, p.L - l0));
+    const size_t base = ((size_t)entry * p.L + l0) * p.C + (size_t)g0 * p.D + c;
+    const T *x = static_cast<const T *>(p.x) + base, *dy = static_cast<const T *>(p.dy) + (kBack ? base : 0);
+    const T *gate = static_cast<const T *>(p.gate) + (kGate ? base : 0);
+    constexpr bool kKeepGate = kGate && kBack;
+    Raw *sx = reinterpret_cast<Raw *>(shared), *sd = sx + (kBack ? (size_t)q.rows * q.cols : 0), *sg = sd + (kKeepGate ? (size_t)q.rows * q.cols : 0);
+    float *sums = reinterpret_cast<float *>(shared + ((reinterpret_cast<uint8_t *>(sg + (size_t)q.rows * q.cols) - shared + 15) & ~15));  // [2][ny][cols * VEC]
+    if (size > 1) sm100::cluster_sync_all();  // every CTA's shared memory may be written from here on
+    auto copy = [&](Raw *dst, const T *src) {
+        if constexpr (sizeof(Raw) == 16)
+            copy_async(dst, src, true);
+        else if constexpr (sizeof(Raw) == 4)
+            copy_async4(dst, src, true);
+        else
+            *dst = __ldg(src);
+    };
+    constexpr int kWaits = 4;  // the first quarter of the rows is summed while the others are on their way
+    const int mine_rows = on && rows > ty ? (rows - ty + ny - 1) / ny : 0, quarter = (mine_rows + kWaits - 1) / kWaits;
+    for (int w = 0; w < kWaits; ++w) {
+        for (int i = w * quarter; i < min(mine_rows, (w + 1) * quarter); ++i) {
+            const int l = ty + i * ny, at = l * q.cols + tx;
+            copy(sx + at, x + (size_t)l * p.C);
+            if (kBack) copy(sd + at, dy + (size_t)l * p.C);
+            if (kKeepGate) copy(sg + at, gate + (size_t)l * p.C);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    float shift[VEC], r[VEC], wv[VEC], b[VEC], s1[VEC] = {}, s2[VEC] = {};
+    if (on)
+        for_groups<VEC>(c, p.D, [&](int e, int g) {
+            const size_t st = (size_t)entry * p.G + g0 + g;
+            if (c + e >= width) {
+                shift[e] = 0.f, r[e] = 0.f, wv[e] = 0.f, b[e] = 0.f;
+                return;
+            }
+            if (kBack)
+                shift[e] = p.center ? __ldg(p.mean + st) : 0.f, r[e] = __ldg(p.rstd + st);
+            else  // differences from the group's first value (from 0 without centring)
+                shift[e] = p.center ? Elem<T>::to_f32(__ldg(static_cast<const T *>(p.x) + (size_t)entry * p.L * p.C + (size_t)(g0 + g) * p.D)) : 0.f;
+            wv[e] = p.w ? __ldg(p.w + g0 * p.D + c + e) : 1.f;
+            b[e] = p.b ? __ldg(p.b + g0 * p.D + c + e) : 0.f;
+        });
+    auto sum_rows = [&](int w) {
+        for (int i = w * quarter; i < min(mine_rows, (w + 1) * quarter); ++i) {
+            const int at = (ty + i * ny) * q.cols + tx;
+            float v[VEC], d[VEC], ga[VEC];
+            Pk::open(sx[at], v);
+            if (kBack) Pk::open(sd[at], d);
+            if (kKeepGate) Pk::open(sg[at], ga);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                if (kBack) {
+                    const float h = (v[e] - shift[e]) * r[e];
+                    float dg;
+                    const float dz = back<T, kGate, kAct>(h, wv[e], b[e], d[e], kGate ? ga[e] : 0.f, &dg);
+                    s1[e] = fmaf(dz, h, s1[e]);
+                    s2[e] += dz;
+                } else {
+                    const float t = v[e] - shift[e];
+                    s1[e] += t;
+                    s2[e] = fmaf(t, t, s2[e]);
+                }
+            }
+        }
+    };
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+    sum_rows(0);
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+    sum_rows(1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    sum_rows(2);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    sum_rows(3);
+    const int wide = q.cols * VEC;
+    if (ty < ny)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sums[ty * wide + c + e] = s1[e], sums[(ny + ty) * wide + c + e] = s2[e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * width; i += kFusedThreads) {  // the channels' sums, over row 0 of each
+        float *at = sums + (i < width ? 0 : ny * wide - width) + i;
+        float v = at[0];
+        for (int k = 1; k < ny; ++k) v += at[k * wide];
+        at[0] = v;
+        if (kBack && p.part) p.part[((size_t)(entry * size + rank) * 2 + (i >= width)) * p.C + (size_t)g0 * p.D + (i < width ? i : i - width)] = v;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x >> 5; i < 2 * groups; i += kFusedThreads / 32) {  // a warp to a group's sum
+        const int which = i >= groups, g = i - which * groups;
+        float v = 0.f;
+        for (int k = threadIdx.x & 31; k < p.D; k += 32) {
+            const float one = sums[which * ny * wide + g * p.D + k];
+            v += kBack && p.w ? one * __ldg(p.w + (size_t)(g0 + g) * p.D + k) : one;
+        }
+        v = lanes_sum(v, 32);
+        if ((threadIdx.x & 31) == 0) mine[which][g] = v;
+    }
+    __syncthreads();
+    if (size > 1) {
+        for (int i = threadIdx.x; i < size * 2 * groups; i += kFusedThreads) {  // to every CTA of the cluster
+            const int to = i / (2 * groups), which = i % (2 * groups) / groups, g = i % groups;
+            const uint32_t at = sm100::mapa_shared(sm100::smem_u32(&all[rank][which][g]), (uint32_t)to);
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(mine[which][g]) : "memory");
+        }
+        sm100::cluster_sync_all();
+    }
+    for (int i = threadIdx.x; i < groups; i += kFusedThreads) {
+        float a0 = size > 1 ? 0.f : mine[0][i], a1 = size > 1 ? 0.f : mine[1][i];
+        for (int k = 0; size > 1 && k < size; ++k) a0 += all[k][0][i], a1 += all[k][1][i];
+        const float inv = 1.f / p.D / p.L;
+        const size_t st = (size_t)entry * p.G + g0 + i;
+        if (kBack) {  // the means of dh h and of dh
+            done[0][i] = a0 * inv;
+            done[1][i] = p.center ? a1 * inv : 0.f;
+        } else {
+            float m = 0.f, v = a1 * inv;
+            if (p.center) {
+                const float d = a0 * inv;
+                v = fmaxf(0.f, fmaf(-d, d, v));
+                m = Elem<T>::to_f32(static_cast<const T *>(p.x)[(size_t)entry * p.L * p.C + (size_t)(g0 + i) * p.D]) + d;
+            }
+            const float rs = rsqrtf(v + p.eps);
+            done[0][i] = m, done[1][i] = rs;
+            if (rank == 0) {
+                if (p.center && p.mean_out) p.mean_out[st] = m;
+                if (p.rstd_out) p.rstd_out[st] = rs;
+            }
+        }
+    }
+    __syncthreads();
+    if (!on) return;
+    float a0[VEC], a1[VEC];
+    for_groups<VEC>(c, p.D, [&](int e, int g) { a0[e] = done[0][min(g, groups - 1)], a1[e] = done[1][min(g, groups - 1)]; });
+#pragma unroll 2
+    for (int i = 0; i < mine_rows; ++i) {
+        const int l = ty + i * ny, at = l * q.cols + tx;
+        float v[VEC], d[VEC], ga[VEC];
+        if (kGate && !kBack) Pk::open(Pk::load(gate + (size_t)l * p.C), ga);
+        Pk::open(sx[at], v);
+        if (kBack) Pk::open(sd[at], d);
+        if (kKeepGate) Pk::open(sg[at], ga);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            if (kBack) {
+                const float h = (v[e] - shift[e]) * r[e];
+                float dg = 0.f;
+                const float dz = back<T, kGate, kAct>(h, wv[e], b[e], d[e], kGate ? ga[e] : 0.f, &dg);
+                v[e] = r[e] * (fmaf(dz, wv[e], -a1[e]) - h * a0[e]);
+                ga[e] = dg;
+            } else {
+                const float z = fmaf((v[e] - a0[e]) * a1[e], wv[e], b[e]);
+                v[e] = kGate ? z * act_of<T, kAct>(ga[e]) : act_of<T, kAct>(z);
+            }
+        }
+        Pk::put(static_cast<T *>(kBack ? p.dx : p.y) + base + (size_t)l * p.C, v);
+        if (kKeepGate) Pk::put(static_cast<T *>(p.dgate) + base + (size_t)l * p.C, ga);
+    }
+}
+
 // ---------------------------------------------------------------- launches
 Params params_of(const NormProblem &p)
 {
@@ -679,6 +862,41 @@ MapShape map_shape(const NormProblem &p)
     return s;
 }
 
+// The slab and cluster of norm_fused; size 0 where the groups do not fit, or the tensors are so large that three launches
+// of many small blocks do better (GPU times in bf16, one launch against three: 2.1 M elements forward 6.9 / 14.5 us, 5.2 M
+// 11.4 / 20.3, 10.5 M 20 / 26, 33.6 M 50 / 43; backward 5.2 M 22 / 29, 10.5 M 39 / 38, 21 M 69 / 61: a CTA that holds
+// its part of a group loads it, sums it and stores it one after another, with few of its kind beside it).
+struct FusedShape {
+    int vec, size, smem;
+    Slab slab;
+};
+FusedShape fused_shape(const NormProblem &p)
+{
+    FusedShape f{};
+    const int G = p.spec.groups, D = p.C / G, e = p.dtype == LA_F32 ? 4 : 2, full = 16 / e;
+    const int tensors = 1 + (p.backward ? 1 + (p.gate != nullptr) : 0);
+    int groups = 1;
+    while (groups < G && groups < kFusedGroups && groups * D * e < 128) ++groups;
+    while (groups < G && groups < kFusedGroups && groups * D % full != 0) ++groups;  // whole vectors
+    const int width = groups * D;
+    if ((long long)p.B * p.L * p.C * e * tensors > 32ll << 20) return f;
+    f.vec = p.C % full == 0 && width % full == 0 ? full : 1;
+    f.slab.groups = groups, f.slab.slabs = ceil_div(G, groups), f.slab.cols = width / f.vec;
+    if (f.slab.cols > kFusedThreads) return f;
+    const int ny = kFusedThreads / f.slab.cols, raw = f.vec * e, sums = 2 * ny * width * 4;
+    const long long slabs = (long long)p.B * f.slab.slabs;
+    for (int size = 1; size <= kFusedMost; size *= 2) {
+        const int rows = ceil_div(p.L, size);
+        const long long smem = (long long)rows * f.slab.cols * raw * tensors + 16 + sums;
+        if (smem > (size < kFusedMost ? kFusedShare : kFusedSmem)) continue;
+        // as many CTAs as there are SMs, if a CTA's rows still occupy its threads
+        if (slabs * size * 2 <= tc::sm_count() && size < kFusedMost && rows >= 8 * ny) continue;
+        f.size = size, f.slab.rows = rows, f.smem = (int)smem;
+        return f;
+    }
+    return f;
+}
+
 bool by_token(const NormProblem &p) { return p.spec.per_token && p.C / p.spec.groups <= kNormTokenChannels; }
 
 // An entry's groups of one token wider than the token kernel's registers: entries of one position.
@@ -714,8 +932,35 @@ template <typename T, bool kGate, bool kBack, bool kAct> la_status launch_tokens
     return go(&norm_tokens<T, kFull, 2, kGate, kBack, kAct>);
 }
 
+template <typename T, int VEC, bool kGate, bool kBack, bool kAct>
+la_status launch_fused(const NormProblem &p, const Params &q, const FusedShape &f)
+{
+    auto kernel = &norm_fused<T, VEC, kGate, kBack, kAct>;
+    const la_status st = ensure_smem(reinterpret_cast<const void *>(kernel), kFusedSmem);
+    if (st != LA_OK) return st;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)(p.B * f.slab.slabs * f.size));
+    lc.blockDim = dim3(kFusedThreads);
+    lc.dynamicSmemBytes = (size_t)f.smem;
+    lc.stream = p.stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)f.size, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = tc::dependent_launch_allowed(p.stream) ? 2 : 1;
+    count_launches();
+    return cuda_status(cudaLaunchKernelEx(&lc, kernel, q, f.slab));
+}
+
 template <typename T, bool kGate, bool kBack, bool kAct> la_status launch_map(const NormProblem &p, Params q)
 {
+    const FusedShape f = fused_shape(p);
+    if (f.size > 0) {
+        constexpr int kWide = std::is_same<T, float>::value ? 4 : 8;
+        return f.vec == 1 ? launch_fused<T, 1, kGate, kBack, kAct>(p, q, f) : launch_fused<T, kWide, kGate, kBack, kAct>(p, q, f);
+    }
     const MapShape s = map_shape(p);
     constexpr int kFull = std::is_same<T, float>::value ? 4 : 8;
     q.splits = s.splits, q.rows = s.rows, q.zs = s.zs;
@@ -751,12 +996,14 @@ template <bool kBack> la_status launch(const NormProblem &p, const Params &q)
 
 }  // namespace
 
-// Scratch: partial sums, then two values a group.
+// Scratch: partial sums, then (groups that do not fit on chip) two values a group.
 size_t norm_scratch(const NormProblem &p)
 {
     const bool grads = p.backward && (p.dw || p.db);
     if (by_token(p)) return grads ? (size_t)token_shape(p).part_rows * 2 * p.C * 4 : 0;
     const NormProblem q = as_map(p);
+    const FusedShape f = fused_shape(q);
+    if (f.size > 0) return grads ? (size_t)q.B * f.size * 2 * p.C * 4 : 0;
     return ((size_t)q.B * map_shape(q).splits * 2 * p.C + 2 * (size_t)q.B * p.spec.groups) * 4;
 }
 
@@ -764,20 +1011,19 @@ la_status group_norm(const NormProblem &given)
 {
     const bool tokens = by_token(given), grads = given.backward && (given.dw || given.db);
     const NormProblem p = tokens ? given : as_map(given);
+    const int fused = tokens ? 0 : fused_shape(p).size;
     Params q = params_of(p);
-    if (tokens) {
-        q.part = grads ? p.scratch : nullptr;
-    } else {
-        q.part = p.scratch;
+    q.part = grads || !(tokens || fused) ? p.scratch : nullptr;
+    if (!tokens && !fused) {
         float *means = p.scratch + (size_t)p.B * map_shape(p).splits * 2 * p.C;
         if (p.backward || !q.mean_out) q.mean_out = means;
         if (p.backward || !q.rstd_out) q.rstd_out = means + (size_t)p.B * q.G;
     }
     la_status st = p.backward ? launch<true>(p, q) : launch<false>(p, q);
-    if (st != LA_OK || !grads || !tokens) return st;
+    if (st != LA_OK || !grads || !(tokens || fused)) return st;
     count_launches();
     return tc::launch_dependent(&norm_weight_grads, 2u * ceil_div(p.C, 32), kFinish, 0, p.stream, (const float *)q.part, p.dw, p.db,
-                                token_shape(p).part_rows, p.C);
+                                tokens ? token_shape(p).part_rows : (long long)p.B * fused, p.C);
 }
 
 }  // namespace la

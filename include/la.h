@@ -606,10 +606,17 @@ la_status la_window_decode_step(void *kc, void *vc, const void *q, const void *k
  *
  * la_delta_backward: given dout = dL/do and dSN = dL/dSN (NULL: zeros), writes dq, dk (summed over the heads
  * that share them), dv, dg, dbeta (fp32) and dS0 (NULL: not wanted).  Recomputes the states (no saved
- * activations).  Scratch: the state before and its gradient behind every chunk, and two rows of dv floats a token and head.
- * Deterministic: every sum is taken in a fixed order.
+ * activations).  Deterministic: every sum is taken in a fixed order.
  * la_delta_step: one token; S [B, H, dk, dv] fp32 read and updated in place; q, k : [B, Hk, dk],
  *   v, o : [B, H, dv], g, beta : [B, H].
+ *
+ * Arithmetic: fp32 inputs in fp32 on the CUDA cores, 8 tokens at a time.  bf16 inputs on the tensor cores, 64 tokens at a
+ * time: the states and all that feeds fp32 results (SN, dS0, dg, dbeta) multiply bf16 inputs with intermediate values in two
+ * bf16 parts (within 2^-17 each; sums fp32); products that end in o, dq or dk alone round one factor once more (2^-8 at most,
+ * as the result's own rounding).  The decode step is fp32 throughout.
+ * Scratch, from the stream's workspace or stream-ordered while the stream is being captured.  Forward (bf16): 26 KB and
+ * 256 dk bytes a head and 64 tokens.  Backward: bf16 34 KB and 512 dk, 8 dk dv and 512 dv bytes a head and 64 tokens; fp32 the state before
+ * and its gradient behind every 32 tokens, and two rows of dv floats a token and head.
  *
  * Supported: dk, dv in {32, 64, 128}, H a multiple of Hk, finite scale; g, beta, dg and dbeta need only their own
  * 4-byte alignment.  Outputs overlap no input and no other output.  B = 0, H = 0, dk = 0 or dv = 0 is an empty problem; N = 0 still writes SN (dS0 = dSN).

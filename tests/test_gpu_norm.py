@@ -77,7 +77,9 @@ def test_tokens(B, L, G, D, dtype, gate):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("B,L,G,D", [(1, 1, 1, 1), (1, 2, 3, 1), (2, 1, 4, 8), (3, 777, 11, 3), (1, 1000, 1, 64), (2, 256, 32, 40),
-                                     (5, 33, 1, 7), (1, 19, 2, 1200), (1, 4001, 8, 10), (70, 3, 2, 8), (1, 5, 1, 2056)])
+                                     (5, 33, 1, 7), (1, 19, 2, 1200), (1, 4001, 8, 10), (70, 3, 2, 8), (1, 5, 1, 2056),
+                                     # too long for one cluster's shared memory; and, with a ragged edge in channels, too wide
+                                     (1, 60000, 2, 16), (2, 3001, 3, 700)])
 @pytest.mark.parametrize("gate", [False, True])
 def test_maps(B, L, G, D, dtype, gate):
     s, dy = inputs(4, B, L, G, D, TYPES[dtype], False, gate, True)
