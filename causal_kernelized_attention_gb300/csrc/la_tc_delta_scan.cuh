@@ -513,6 +513,8 @@ template <int DK, int DV, int kMode> struct ScanSmem {
     static constexpr int kKeyStages = kMode == kForward ? 2 : 1;
     static constexpr bool kOutOverW = kMode != kForward && DK >= DV;  // E's rows are staged where W was
     static constexpr uint32_t kMats = 2 * kSq + Layout<DK>::w_bytes;
+    // forward, d_k 64: the products of o have room for two chunks, so that the chain does not wait for the warps of o
+    static constexpr int kOuts = kMode == kForward && DK == 64 ? 2 : 1, kScalarRing = kOuts + 2;
     uint8_t v[2][DV / 64][kSq];
     uint8_t mats[2][kMats];  // T or Z, W or W2
     uint8_t k[kKeyStages][DK / 64][kSq];
@@ -525,12 +527,12 @@ template <int DK, int DV, int kMode> struct ScanSmem {
         uint8_t p[kMode == kForward ? 2 : 1][kMode == kForward ? kSq : 16];
         uint8_t e[kMode == kForward || kOutOverW ? 16 : rows_bytes(DV)];  // E's rows
     };
-    float scalars[3][3][kChunk];  // beta, write, first; in reverse write, first, back
+    float scalars[kScalarRing][3][kChunk];  // beta, write, first; in reverse write, first, back
     uint64_t full[2];                       // a stage's V and matrices are there (and scalars, but for kForward)
-    uint64_t keys_full[2], rows_read[2];    // its K, Q, P (and scalars) are; (kOutOverW) the store of E's rows has read them
+    uint64_t keys_full[2], rows_read[2];    // its K, Q, P (and scalars) are; the warps of E's rows are done with it
     uint64_t s_ready, u_ready, d_ready;     // left operands are in TMEM (512, 512, 128 arrivals)
     // products are there (one barrier a stage where a waiter may come a chunk late); the warps of o have read theirs
-    uint64_t e_full[2], s_full, o_full[2], o_read;
+    uint64_t e_full[2], s_full, o_full[2], o_read[2];
     uint64_t stored;                        // the state's image has been read by its store
     uint64_t drain;
     uint32_t tmem_base;
@@ -563,7 +565,8 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
         mbar_init(&sm.s_ready, 32 * kChainWarps);
         mbar_init(&sm.u_ready, 32 * kChainWarps);
         mbar_init(&sm.d_ready, 128);
-        mbar_init(&sm.o_read, 128);
+        mbar_init(&sm.o_read[0], 128);
+        mbar_init(&sm.o_read[1], 128);
         sm.abort = (smem_u32(smem_raw) & 1023u) == 0 ? 0 : 1;
         if (sm.abort) atomicOr(&g_delta_status, kStatusTimeout);
         fence_mbar_init();
@@ -590,13 +593,14 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
         for (; ok && c < chunks; ++c) {
             const int st = c & 1, x = chunk_of(c);
             const uint8_t *img = images + ((size_t)bh * chunks + x) * kStride;
-            // V and the matrices of chunk c - 2 end with its E (where E's rows are staged over W, with their store)
-            if (c >= 2 && !(ok = wait(Sm::kOutOverW ? &sm.rows_read[st] : &sm.e_full[st], (uint32_t)((c >> 1) - 1) & 1u))) break;
+            // V and the matrices of chunk c - 2 end with its E; where states are kept, the warps of E's rows tell when they have
+            // read them, too, and (rows staged over W) when the rows' store has
+            if (c >= 2 && !(ok = wait(kKeep ? &sm.rows_read[st] : &sm.e_full[st], (uint32_t)((c >> 1) - 1) & 1u))) break;
             if (ready && !(ok = wait_flag(ready + (size_t)bh * chunks + x, abort_flag))) break;
             if (__any_sync(0xffffffffu, aborted(abort_flag))) break;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&sm.full[st], DV / 64 * kSq + Sm::kMats + (kKeep ? kScanScalars : 0));
-                if (kKeep) bulk_load(sm.scalars[c % 3], img + (kMode == kReverse ? kChunk * 4 : 0), kScanScalars, &sm.full[st]);
+                if (kKeep) bulk_load(sm.scalars[c % Sm::kScalarRing], img + (kMode == kReverse ? kChunk * 4 : 0), kScanScalars, &sm.full[st]);
                 bulk_load(sm.mats[st], img + (kMode == kReverse ? Lay::z : Lay::t), Sm::kMats, &sm.full[st]);
                 for (int b = 0; b < DV / 64; ++b) tma_load_3d(sm.v[st][b], &map_v, &sm.full[st], 64 * b, x * kChunk, bh);
             }
@@ -611,7 +615,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                     tma_load_3d(sm.k[ks][b], &map_k, &sm.keys_full[ks], 64 * b, x * kChunk, bhk);
                 }
                 if (!kKeep) bulk_load(sm.p[st], img + Lay::p, kSq, &sm.keys_full[ks]);
-                if (!kKeep) bulk_load(sm.scalars[c % 3], img, kScanScalars, &sm.keys_full[ks]);
+                if (!kKeep) bulk_load(sm.scalars[c % Sm::kScalarRing], img, kScanScalars, &sm.keys_full[ks]);
             }
             __syncwarp();
         }
@@ -620,14 +624,14 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
         // The loop's control and operands stay in uniform registers (an MMA issued from elsewhere costs more to issue
         // than to run): waits return nothing here, and an abort is seen at the head of the next chunk.
         constexpr uint32_t id = idesc_bf16_f32(128, kChunk, false, false), id_s = idesc_bf16_f32(128, DK, false, true);
-        constexpr uint32_t id_v = idesc_bf16_f32(128, kChunk, true, kMode == kReverse);
         constexpr uint32_t kBox = kSq >> 4;  // descriptors count 16 bytes
         const uint64_t dv = cols_mn(smem_u32(sm.v[0][0]), 0, DV == 128 ? kSq : 0);
         const uint64_t dt = kMode == kReverse ? cols_mn(smem_u32(sm.mats[0]), 0) : rows_k(smem_u32(sm.mats[0]), 0);
         const uint64_t dw = rows_k(smem_u32(sm.mats[0]) + 2 * kSq, 0), dp = rows_k(smem_u32(sm.p[0]), 0);
         const uint64_t dk = cols_mn(smem_u32(sm.k[0][0]), 0), dq = rows_k(smem_u32(sm.q[0][0]), 0), dqm = cols_mn(smem_u32(sm.q[0][0]), 0);
         auto wait = [&](uint64_t *bar, uint32_t parity) { wait_or_abort(&g_delta_status, abort_flag, bar, parity); };
-        // E^T = V^T T^T (in reverse dO^T Z), ahead of the state's part
+        // E^T = V^T T^T (in reverse dO^T Z), ahead of the state's part.  T and Z are lower triangular: step kk of 16
+        // tokens reaches the columns from 16 kk on (in reverse those up to 16 kk + 15, so the last step comes first).
         auto from_values = [&](int c) {
             const uint32_t st = (uint32_t)c & 1u;
             wait(&sm.full[st], (uint32_t)(c >> 1) & 1u);
@@ -637,9 +641,15 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(tmem + Col::e + 64 * st, a + kk * (2048 >> 4), b + part * kBox + kk * (kMode == kReverse ? 2048 >> 4 : 2),
-                               id_v, part + kk > 0);
+                    for (int u = 0; u < 4; ++u) {
+                        const int kk = kMode == kReverse ? 3 - u : u;
+                        if (kMode == kReverse)
+                            mma_ss(tmem + Col::e + 64 * st, a + kk * (2048 >> 4), b + part * kBox + kk * (2048 >> 4),
+                                   idesc_bf16_f32(128, 16 * (kk + 1), true, true), part + u > 0);
+                        else
+                            mma_ss(tmem + Col::e + 64 * st + 16 * kk, a + kk * (2048 >> 4), b + part * kBox + kk * 2 + kk * (2048 >> 4),
+                                   idesc_bf16_f32(128, kChunk - 16 * kk, true, false), part + u > 0);
+                    }
             }
             __syncwarp();
         };
@@ -661,7 +671,9 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                 mma_commit(&sm.e_full[st]);
             }
             __syncwarp();
-            if (c > 0) wait(&sm.o_read, ph ^ 1u);
+            // what the warps of o (or of E's rows) read of the chunk before, or of the one before that
+            if (c >= Sm::kOuts) wait(&sm.o_read[(c - Sm::kOuts) & 1], (uint32_t)((c - Sm::kOuts) >> 1) & 1u);
+            const uint32_t tQ = tmem + Col::qs + (Sm::kOuts == 2 ? 128 * st : 0);
             if (kKeep)
                 wait(&sm.keys_full[0], ph);
             else
@@ -672,7 +684,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                     const uint64_t b = dq + st * (DK / 64 * kBox);
 #pragma unroll
                     for (int kk = 0; kk < DK / 16; ++kk)
-                        mma_ts(tmem + Col::qs, tmem + Col::parts + kk * 8, b + (kk >> 2) * kBox + (kk & 3) * 2, id, kk > 0);
+                        mma_ts(tQ, tmem + Col::parts + kk * 8, b + (kk >> 2) * kBox + (kk & 3) * 2, id, kk > 0);
                 }
                 __syncwarp();
             }
@@ -693,8 +705,9 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                 if (!kKeep) {
                     const uint64_t bp = dp + st * kBox;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ts(tmem + Col::pu, tmem + Col::parts + DK / 2 + kk * 8, bp + kk * 2, id, kk > 0);
+                    for (int kk = 0; kk < 4; ++kk)  // (lower triangular)
+                        mma_ts(tQ + 64 + 16 * kk, tmem + Col::parts + DK / 2 + kk * 8, bp + kk * 2 + kk * (2048 >> 4),
+                               idesc_bf16_f32(128, kChunk - 16 * kk, false, false), kk > 0);
                     mma_commit(&sm.o_full[st]);
                 }
             }
@@ -747,7 +760,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
             tc_fence_before();
             mbar_arrive(&sm.s_ready);
             if (!(ok = wait(kKeep ? &sm.full[st] : &sm.keys_full[st], (uint32_t)(c >> 1) & 1u))) break;
-            const float (*scalars)[kChunk] = sm.scalars[c % 3];
+            const float (*scalars)[kChunk] = sm.scalars[c % Sm::kScalarRing];
             const float whole = scalars[kMode == kReverse ? 1 : 2][kChunk - 1];
             if (!(ok = wait(&sm.e_full[st], (uint32_t)(c >> 1) & 1u))) break;
             tc_fence_after();
@@ -809,6 +822,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
             if (kMode == kReverse) {  // scale exp(G) dO as a left operand, once the last state product has read it
                 if (!(ok = wait(&sm.full[st], (uint32_t)(c >> 1) & 1u))) break;
                 if (c > 0 && !(ok = wait(&sm.s_full, ph ^ 1u))) break;
+                tc_fence_after();
                 const uint8_t *v = sm.v[st][0];
 #pragma unroll
                 for (int y = 0; y < kChunk; y += 16) {
@@ -817,7 +831,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                     for (int e = 0; e < 16; e += 2) {
                         const uint8_t *r = v + (y + e) / 8 * 1024;
                         const float d0 = live ? bf16_at(r + at[e & 7]) : 0.f, d1 = live ? bf16_at(r + at[(e + 1) & 7]) : 0.f;
-                        const float2 w = *reinterpret_cast<const float2 *>(&sm.scalars[c % 3][1][y + e]);
+                        const float2 w = *reinterpret_cast<const float2 *>(&sm.scalars[c % Sm::kScalarRing][1][y + e]);
                         split2(p.scale * w.x * d0, p.scale * w.y * d1, hi[e / 2], lo[e / 2]);
                     }
                     tmem_st8(tl + Col::pu + y / 2, hi);
@@ -858,15 +872,13 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                     }
                 tc_fence_before();
                 fence_proxy_async_smem();
-                mbar_arrive(&sm.o_read);
+                mbar_arrive(&sm.o_read[st]);
                 named_bar_sync(1, 128);
                 if (warp == kOutWarp && lane == 0) {
                     bulk_store(rows + ((size_t)bh * chunks + x) * rows_bytes(DV), out, rows_bytes(DV));
                     tma_store_commit();
-                    if (Sm::kOutOverW) {
-                        tma_store_wait_read_all();
-                        mbar_arrive(&sm.rows_read[st]);
-                    }
+                    if (Sm::kOutOverW) tma_store_wait_read_all();
+                    mbar_arrive(&sm.rows_read[st]);
                 }
                 __syncwarp();
             } else {
@@ -877,13 +889,14 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                     __syncwarp();
                     named_bar_sync(1, 128);
                 }
-                const float *first = sm.scalars[c % 3][2];
+                const float *first = sm.scalars[c % Sm::kScalarRing][2];
                 if (live)
 #pragma unroll
                     for (int y = 0; y < kChunk; y += 16) {
                         uint32_t a[16], b[16];
-                        tmem_ld16(tl + Col::qs + y, a);
-                        tmem_ld16(tl + Col::pu + y, b);
+                        const uint32_t tQ = tl + Col::qs + (Sm::kOuts == 2 ? 128 * st : 0);
+                        tmem_ld16(tQ + y, a);
+                        tmem_ld16(tQ + 64 + y, b);
                         tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
@@ -897,7 +910,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                     }
                 tc_fence_before();
                 fence_proxy_async_smem();
-                mbar_arrive(&sm.o_read);
+                mbar_arrive(&sm.o_read[st]);
                 named_bar_sync(1, 128);
                 if (warp == kOutWarp && lane == 0) {
                     for (int b = 0; b < DV / 64; ++b) tma_store_3d(&map_o, out + b * kSq, 64 * b, x * kChunk, bh);
