@@ -35,25 +35,52 @@ static_assert(sizeof(Scalars) == 2048, "");
 constexpr uint32_t kScanScalars = 3 * kChunk * 4;
 
 // A chunk's image: the scalars, then matrices in two bf16 parts (high, then low: the value within 2^-17) as 128-byte
-// swizzled MMA operands: T [i][j]; W [i][d_k], in boxes of 64 columns; P [i][j] (high part alone) for the forward
-// pass, or Z [i][j] and W2 [j][d_k] for the backward.
+// swizzled MMA operands: T [i][j]; W [i][d_k], in boxes of 64 columns; P diag(beta) [i][j] (high part alone) for the
+// forward pass, or Z [i][j] and W2 [j][d_k] for the backward.
 template <int DK> struct Layout {
     static constexpr uint32_t w_bytes = 2 * (DK / 64) * kSq;
     static constexpr uint32_t t = sizeof(Scalars), w = t + 2 * kSq, p = w + w_bytes, z = p, w2 = z + 2 * kSq;
     static constexpr uint32_t forward_bytes = p + kSq, backward_bytes = w2 + w_bytes;
 };
 
-// Two values as bf16 high parts and the bf16 rounding of what is left: together within 2^-17 of each.
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo)
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y)
 {
-    hi = pack_bf16(a, b);
-    float x, y;  // both differences in one instruction
-    asm("{\n\t.reg .b64 v, h, m;\n\tmov.b64 v, {%2, %3};\n\tmov.b64 h, {%4, %5};\n\tmov.b64 m, {%6, %6};\n\t"
-        "fma.rn.f32x2 v, h, m, v;\n\tmov.b64 {%0, %1}, v;\n\t}"
-        : "=f"(x), "=f"(y)
-        : "f"(a), "f"(b), "r"(hi << 16), "r"(hi & 0xffff0000u), "f"(-1.f));
-    lo = pack_bf16(x, y);
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
 }
+__device__ __forceinline__ void unpair(uint64_t v, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Two values as bf16 high parts and the bf16 rounding of what is left: together within 2^-17 of each.
+__device__ __forceinline__ void split2(uint64_t v, uint32_t &hi, uint32_t &lo)
+{
+    float a, b;
+    unpair(v, a, b);
+    hi = pack_bf16(a, b);
+    const uint64_t h = pair(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+    unpair(fma2(h, pair(-1.f, -1.f), v), a, b);
+    lo = pack_bf16(a, b);
+}
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) { split2(pair(a, b), hi, lo); }
 __device__ __forceinline__ float bf16_at(const uint8_t *p) { return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(p) << 16); }
 
 __device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
@@ -90,26 +117,6 @@ __device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t 
 }
 __device__ __forceinline__ uint32_t ld_shared32(const void *p) { return *reinterpret_cast<const uint32_t *>(p); }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pair(float x, float y)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ float ex2(float x)
 {
     float y;

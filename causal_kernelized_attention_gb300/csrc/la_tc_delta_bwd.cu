@@ -68,12 +68,6 @@ __device__ __forceinline__ float transposed_sums(float (&v)[32], int lane)
     return v[0];
 }
 __device__ __forceinline__ uint64_t both(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kLocalThreads, 1)

@@ -276,12 +276,15 @@ __device__ __forceinline__ void prepare_chunk(PrepSmem<DK, kBack> &sm, const CUt
                 for (int c = 0; c < 4; ++c) {
                     const float x[8] = {d[8 * c], d[8 * c + 1], d[8 * c + 2], d[8 * c + 3], d[8 * c + 4], d[8 * c + 5], d[8 * c + 6], d[8 * c + 7]};
                     uint4 h, l;
-                    split8(x, h, l);
                     const uint32_t at = sw128_offset(i, j0 + 8 * c);
                     if (kBack) {
+                        split8(x, h, l);
                         *reinterpret_cast<uint4 *>(sm.p[0] + at) = h;
                         *reinterpret_cast<uint4 *>(sm.p[kBack ? 1 : 0] + at) = l;
                     } else {
+                        const float *b = sm.s.beta + j0 + 8 * c;
+                        h = make_uint4(pack_bf16(b[0] * x[0], b[1] * x[1]), pack_bf16(b[2] * x[2], b[3] * x[3]),
+                                       pack_bf16(b[4] * x[4], b[5] * x[5]), pack_bf16(b[6] * x[6], b[7] * x[7]));
                         *reinterpret_cast<uint4 *>(image + Lay::p + at) = h;
                     }
                 }
@@ -770,24 +773,20 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
             tmem_ld16(tE, a);
             tmem_ld_wait();
             {
-                const float *mul = scalars[kMode == kReverse ? 2 : 1] + kTokens * part, *beta = scalars[0] + kTokens * part;
+                const float *mul = scalars[kMode == kReverse ? 2 : 1] + kTokens * part;
                 const uint32_t tU = kKeep ? tl + Col::qs + kTokens * part : tE;
                 uint32_t hi[8], lo[8];
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     const float4 w = *reinterpret_cast<const float4 *>(mul + e);
-                    split2(w.x * __uint_as_float(a[e]), w.y * __uint_as_float(a[e + 1]), hi[e / 2], lo[e / 2]);
-                    split2(w.z * __uint_as_float(a[e + 2]), w.w * __uint_as_float(a[e + 3]), hi[e / 2 + 1], lo[e / 2 + 1]);
+                    split2(mul2(pair(w.x, w.y), pair(__uint_as_float(a[e]), __uint_as_float(a[e + 1]))), hi[e / 2], lo[e / 2]);
+                    split2(mul2(pair(w.z, w.w), pair(__uint_as_float(a[e + 2]), __uint_as_float(a[e + 3]))), hi[e / 2 + 1], lo[e / 2 + 1]);
                 }
                 tmem_st8(tU, hi);
                 tmem_st8(tU + 8, lo);
-                if (!kKeep) {  // U for o, in one part
+                if (!kKeep) {  // E for o, in one part (P is scaled by beta)
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const float4 w = *reinterpret_cast<const float4 *>(beta + e);
-                        hi[e / 2] = pack_bf16(w.x * __uint_as_float(a[e]), w.y * __uint_as_float(a[e + 1]));
-                        hi[e / 2 + 1] = pack_bf16(w.z * __uint_as_float(a[e + 2]), w.w * __uint_as_float(a[e + 3]));
-                    }
+                    for (int e = 0; e < 16; e += 2) hi[e / 2] = pack_bf16(__uint_as_float(a[e]), __uint_as_float(a[e + 1]));
                     tmem_st8(tl + Col::parts + DK / 2 + 8 * part, hi);
                 }
             }
@@ -801,7 +800,9 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                 tmem_ld16(tS + x, a);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) s[x + e] = fmaf(whole, s[x + e], __uint_as_float(a[e]));
+                for (int e = 0; e < 16; e += 2)
+                    unpair(fma2(pair(whole, whole), pair(s[x + e], s[x + e + 1]), pair(__uint_as_float(a[e]), __uint_as_float(a[e + 1]))),
+                           s[x + e], s[x + e + 1]);
             }
         }
         if (ok && last_state && mine)
@@ -901,8 +902,10 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
                             const float2 w = *reinterpret_cast<const float2 *>(first + y + e);
-                            const uint32_t o = pack_bf16(p.scale * fmaf(w.x, __uint_as_float(a[e]), __uint_as_float(b[e])),
-                                                         p.scale * fmaf(w.y, __uint_as_float(a[e + 1]), __uint_as_float(b[e + 1])));
+                            float o0, o1;
+                            unpair(mul2(pair(p.scale, p.scale), fma2(pair(w.x, w.y), pair(__uint_as_float(a[e]), __uint_as_float(a[e + 1])),
+                                                                     pair(__uint_as_float(b[e]), __uint_as_float(b[e + 1])))), o0, o1);
+                            const uint32_t o = pack_bf16(o0, o1);
                             uint8_t *to = out + (y + e) / 8 * 1024;
                             *reinterpret_cast<uint16_t *>(to + at[e & 7]) = (uint16_t)o;
                             *reinterpret_cast<uint16_t *>(to + at[(e + 1) & 7]) = (uint16_t)(o >> 16);
