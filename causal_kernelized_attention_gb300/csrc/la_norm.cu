@@ -122,7 +122,9 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes)
 // registers, and walks over the tokens; the launch has a whole number of slots for each group.  The loads of the
 // next tokens are under way meanwhile: each thread copies its vectors asynchronously into a ring of its own in
 // shared memory, kRing tokens deep (held in registers, one token ahead, they were too few to keep HBM busy: 47 us
-// against 41 for 16384 tokens of 16 x 128 gated channels in bf16); channels by ones are loaded one token ahead.
+// against 41 for 16384 tokens of 16 x 128 gated channels in bf16, 37 with today's grid: 5.4 TB/s; backward 70 us, 4.8
+// TB/s); channels by ones are loaded one token ahead.  What bounds them then is instructions: an issue slot is used in 3 of 4
+// cycles, by the exponentials, conversions and the sums over lanes.
 constexpr int kRing = 4;
 __device__ __forceinline__ void copy_async(void *dst, const void *src, bool on)  // 16 bytes, or zeros
 {
@@ -832,7 +834,11 @@ TokenShape token_shape(const NormProblem &p)
         b = t;
     }
     const long long unit = G / a;
-    const long long need = (all + per_block - 1) / per_block, most = (long long)tc::sm_count() * (p.backward ? 4 : 8);
+    // About one round of resident blocks, each walking over many tokens: more blocks only repeat the start (weights, first
+    // loads) and, backward, add rows of partial sums (16384 tokens of 16 x 128 gated channels in bf16, forward 36 us at 3
+    // blocks an SM, 37 at 6, 39 at 8; backward 65 at 2, 74 at 3 and 4; channels by ones, 30 of them, backward 62 / 51 / 52).
+    const int per_sm = s.vec > 1 ? (p.backward ? 2 : 3) : (p.backward ? 3 : 6);
+    const long long need = (all + per_block - 1) / per_block, most = (long long)tc::sm_count() * per_sm;
     s.blocks = (need < most ? need : most);
     s.blocks = (s.blocks + unit - 1) / unit * unit;
     s.slots = s.blocks * per_block;
