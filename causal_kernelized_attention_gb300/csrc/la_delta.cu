@@ -4,7 +4,7 @@
 //   D_t = a_t S_{t-1},  e_t = v_t - D_t^T k_t,  S_t = D_t + k_t (b_t e_t)^T,  o_t = scale S_t^T q_t
 //
 // with a_t = exp(g_t).  Columns of S (one per value feature) do not meet, so a scan's blocks take
-// 32 columns each and hold them in registers.  Token by token a scan waits: a dot product over d_k, two
+// 8 or 32 columns each and hold them in registers.  Token by token a scan waits: a dot product over d_k, two
 // shuffles and the update follow one another (345 cycles a token at d_k 32, whatever the machine has free).  So
 // eight tokens are taken together: with G the running sum of g from their first on and D_ij = exp(G_i - G_j),
 //   e_i = v_i - exp(G_i) S^T k_i - sum_{j<i} D_ij (k_i.k_j) u_j,   u = b e,
@@ -22,7 +22,9 @@ namespace {
 constexpr int kTile = 16;   // tokens staged in shared memory at a time
 constexpr int kB = 8;       // tokens taken together
 constexpr int kStepCols = 32;  // columns of S a block of the decode step
-constexpr int kRows = 8;    // rows of S a lane holds: d_k / 8 lanes share a column
+// Rows of S a lane holds in a scan of CB columns a block; d_k / rows lanes share a column.
+constexpr int rows_of(int CB) { return CB == 8 ? 4 : 8; }
+template <int DK, int CB> constexpr int scan_threads() { return CB * DK / rows_of(CB); }
 constexpr int kMakers = 128;  // threads that load and prepare the tiles
 constexpr int kC = 32;      // tokens of a chunk of the backward pass
 
@@ -127,19 +129,30 @@ __device__ __forceinline__ void make_groups(const Stage<DK, CB> &s, Group (&out)
     }
 }
 
-// DK / 8 lanes share a column: lane `part` holds rows 4 part .. + 3 of each half, so that a warp's reads
-// of a key are consecutive.  The lane's share of x^T S:
-template <int DK> __device__ __forceinline__ float dot_rows(const float *x, const float (&S)[kRows], int part)
+// R rows of a column to a lane, DK / R lanes to a column: lane `part` holds rows 4 part .. + 3 of each R / 4-th of
+// them, so that a warp's reads of a key are consecutive.  The lane's share of x^T S:
+template <int DK, int R> __device__ __forceinline__ float dot_rows(const float *x, const uint64_t (&S)[R / 2], int part)
 {
-    const float4 a = Vec4<float>::get(x + 4 * part), b = Vec4<float>::get(x + DK / 2 + 4 * part);
-    const float s = fmaf(a.x, S[0], fmaf(a.y, S[1], fmaf(a.z, S[2], a.w * S[3])));
-    return s + fmaf(b.x, S[4], fmaf(b.y, S[5], fmaf(b.z, S[6], b.w * S[7])));
+    uint64_t sum = 0;
+#pragma unroll
+    for (int r = 0; r < R / 2; r += 2) {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(x + r / 2 * (4 * DK / R) + 4 * part);
+        sum = r ? fma2(a.x, S[r], sum) : mul2(a.x, S[r]);
+        sum = fma2(a.y, S[r + 1], sum);
+    }
+    float u, v;
+    unpair(sum, u, v);
+    return u + v;
 }
-template <int DK> __device__ __forceinline__ void add_row(float (&S)[kRows], const float *x, float w, int part)
+template <int DK, int R> __device__ __forceinline__ void add_row(uint64_t (&S)[R / 2], const float *x, float w, int part)
 {
-    const float4 a = Vec4<float>::get(x + 4 * part), b = Vec4<float>::get(x + DK / 2 + 4 * part);
-    S[0] = fmaf(a.x, w, S[0]), S[1] = fmaf(a.y, w, S[1]), S[2] = fmaf(a.z, w, S[2]), S[3] = fmaf(a.w, w, S[3]);
-    S[4] = fmaf(b.x, w, S[4]), S[5] = fmaf(b.y, w, S[5]), S[6] = fmaf(b.z, w, S[6]), S[7] = fmaf(b.w, w, S[7]);
+    const uint64_t ww = pair(w, w);
+#pragma unroll
+    for (int r = 0; r < R / 2; r += 2) {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(x + r / 2 * (4 * DK / R) + 4 * part);
+        S[r] = fma2(a.x, ww, S[r]);
+        S[r + 1] = fma2(a.y, ww, S[r + 1]);
+    }
 }
 // Sums of 8 values over the L lanes of a column: lane p gets that of value p % 8, and with four lanes that of p + 4.
 template <int L> __device__ __forceinline__ void lane_sums(const float (&v)[kB], int part, float (&out)[L == 4 ? 2 : 1])
@@ -155,7 +168,8 @@ template <int L> __device__ __forceinline__ void lane_sums(const float (&v)[kB],
         out[0] = b[0], out[1] = b[1];
     } else {
         out[0] = swap(b2 ? b[1] : b[0], b2 ? b[0] : b[1], 4);
-        if (L == 16) out[0] += __shfl_xor_sync(0xffffffffu, out[0], 8);
+        if (L >= 16) out[0] += __shfl_xor_sync(0xffffffffu, out[0], 8);
+        if (L == 32) out[0] += __shfl_xor_sync(0xffffffffu, out[0], 16);
     }
 }
 // All 8 sums in every lane of the column.
@@ -166,15 +180,23 @@ template <int L> __device__ __forceinline__ void all_sums(float (&v)[kB], int pa
 #pragma unroll
     for (int j = 0; j < kB; ++j) v[j] = __shfl_sync(0xffffffffu, own[L == 4 ? j >> 2 : 0], L == 4 ? j & 3 : j, L);
 }
-template <int DK> __device__ __forceinline__ void state_out(float *at, const float (&S)[kRows], int part, int dv)
+template <int DK, int R> __device__ __forceinline__ void state_out(float *at, const uint64_t (&S)[R / 2], int part, int dv)
 {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) at[(size_t)(r / 4 * (DK / 2) + part * 4 + r % 4) * dv] = S[r];
+    for (int r = 0; r < R; r += 2) {
+        float x, y;
+        unpair(S[r / 2], x, y);
+        float *to = at + (size_t)(r / 4 * (4 * DK / R) + part * 4 + r % 4) * dv;
+        to[0] = x, to[dv] = y;
+    }
 }
-template <int DK> __device__ __forceinline__ void state_in(const float *at, float (&S)[kRows], int part, int dv)
+template <int DK, int R> __device__ __forceinline__ void state_in(const float *at, uint64_t (&S)[R / 2], int part, int dv)
 {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) S[r] = at ? at[(size_t)(r / 4 * (DK / 2) + part * 4 + r % 4) * dv] : 0.f;
+    for (int r = 0; r < R; r += 2) {
+        const float *from = at + (size_t)(r / 4 * (4 * DK / R) + part * 4 + r % 4) * dv;
+        S[r / 2] = at ? pair(from[0], from[dv]) : 0;
+    }
 }
 __device__ __forceinline__ void row8(const float *p, float (&v)[kB])
 {
@@ -188,8 +210,7 @@ template <int DK, int CB, bool kDown, typename F>
 __device__ __forceinline__ void over_tiles(ScanSmem<DK, CB> &sm, const float *k, const float *q, const float *v, const float *g,
                                            const float *beta, int n, int dv, F one)
 {
-    constexpr int kScanners = CB * DK / kRows;
-    const int tiles = (n + kTile - 1) / kTile, tid = (int)threadIdx.x - kScanners;
+    const int tiles = (n + kTile - 1) / kTile, tid = (int)threadIdx.x - scan_threads<DK, CB>();
     const bool maker = tid >= 0;
     auto tile = [&](int i) { return kDown ? tiles - 1 - i : i; };
     auto load = [&](int i) {
@@ -219,12 +240,10 @@ __device__ __forceinline__ void over_tiles(ScanSmem<DK, CB> &sm, const float *k,
 
 // kSave: instead of o, the errors e_t and the state before each chunk of kC tokens.
 template <int DK, int CB, bool kSave>
-__global__ void __launch_bounds__(CB * DK / kRows + kMakers) delta_scan(Params p, float *errors, float *before)
+__device__ __forceinline__ void scan(ScanSmem<DK, CB> &sm, const Params &p, int block, float *errors, float *before)
 {
-    extern __shared__ float4 smem_raw[];
-    ScanSmem<DK, CB> &sm = *reinterpret_cast<ScanSmem<DK, CB> *>(smem_raw);
-    const int slices = p.dv / CB, bh = blockIdx.x / slices, c0 = blockIdx.x % slices * CB;
-    constexpr int L = DK / kRows;  // lanes of a column
+    const int slices = p.dv / CB, bh = block / slices, c0 = block % slices * CB;
+    constexpr int R = rows_of(CB), L = DK / R;  // rows of a lane, lanes of a column
     const int part = threadIdx.x % L, col = threadIdx.x / L % CB;
     const bool scanner = threadIdx.x < CB * L;
     const int b = bh / p.H, bhk = b * p.Hk + bh % p.H / (p.H / p.Hk);
@@ -232,23 +251,23 @@ __global__ void __launch_bounds__(CB * DK / kRows + kMakers) delta_scan(Params p
     const float *v = static_cast<const float *>(p.v) + (size_t)bh * p.N * p.dv + c0;
     const size_t at = (size_t)bh * DK * p.dv + c0 + col;
     const int chunks = (p.N + kC - 1) / kC;
-    float S[kRows];
-    state_in<DK>(p.S0 && scanner ? p.S0 + at : nullptr, S, part, p.dv);
+    uint64_t S[R / 2];
+    state_in<DK, R>(p.S0 && scanner ? p.S0 + at : nullptr, S, part, p.dv);
     over_tiles<DK, CB, false>(sm, k, q, v, p.g + (size_t)bh * p.N, p.beta + (size_t)bh * p.N, p.N, p.dv,
                               [&](const Stage<DK, CB> &s, const Group (&groups)[2], int tile) {
         const int t0 = tile * kTile;
         if (kSave && t0 % kC == 0)
-            state_out<DK>(before + ((size_t)bh * chunks + t0 / kC) * DK * p.dv + c0 + col, S, part, p.dv);
+            state_out<DK, R>(before + ((size_t)bh * chunks + t0 / kC) * DK * p.dv + c0 + col, S, part, p.dv);
 #pragma unroll 1
         for (int h = 0; h < kTile / kB; ++h) {
             const Group &m = groups[h];
             const int r0 = kB * h;
             float u[kB], d[kB], first[kB], beta[kB];
 #pragma unroll
-            for (int j = 0; j < kB; ++j) u[j] = dot_rows<DK>(s.k[r0 + j], S, part);
+            for (int j = 0; j < kB; ++j) u[j] = dot_rows<DK, R>(s.k[r0 + j], S, part);
             if (!kSave)
 #pragma unroll
-                for (int j = 0; j < kB; ++j) d[j] = dot_rows<DK>(s.q[r0 + j], S, part);
+                for (int j = 0; j < kB; ++j) d[j] = dot_rows<DK, R>(s.q[r0 + j], S, part);
             row8(m.first, first);
             row8(s.beta + r0, beta);
             constexpr int kOwn = L == 4 ? 2 : 1;  // tokens whose results the lane writes: part % 8, and with four lanes part + 4
@@ -287,12 +306,12 @@ __global__ void __launch_bounds__(CB * DK / kRows + kMakers) delta_scan(Params p
             row8(m.last, last);
             const float whole = m.whole[0];
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) S[r] *= whole;
+            for (int r = 0; r < R / 2; ++r) S[r] = mul2(S[r], pair(whole, whole));
 #pragma unroll
-            for (int j = 0; j < kB; ++j) add_row<DK>(S, s.k[r0 + j], last[j] * u[j], part);
+            for (int j = 0; j < kB; ++j) add_row<DK, R>(S, s.k[r0 + j], last[j] * u[j], part);
         }
     });
-    if (!kSave && p.SN && scanner) state_out<DK>(p.SN + at, S, part, p.dv);
+    if (!kSave && p.SN && scanner) state_out<DK, R>(p.SN + at, S, part, p.dv);
 }
 
 // The reverse scan of R = dL/dS, 8 tokens together from the last on:
@@ -300,12 +319,10 @@ __global__ void __launch_bounds__(CB * DK / kRows + kMakers) delta_scan(Params p
 //   R' = exp(G_8) R + sum_i exp(G_i) (q_i scale dO_i^T - k_i dv_i^T).
 // Writes dv, dX, R behind each chunk (before the chunk's own dO) and dS0.
 template <int DK, int CB>
-__global__ void __launch_bounds__(CB * DK / kRows + kMakers) delta_reverse(Params p, float *dX, float *after)
+__device__ __forceinline__ void reverse_scan(ScanSmem<DK, CB> &sm, const Params &p, int block, float *dX, float *after)
 {
-    extern __shared__ float4 smem_raw[];
-    ScanSmem<DK, CB> &sm = *reinterpret_cast<ScanSmem<DK, CB> *>(smem_raw);
-    const int slices = p.dv / CB, bh = blockIdx.x / slices, c0 = blockIdx.x % slices * CB;
-    constexpr int L = DK / kRows;  // lanes of a column
+    const int slices = p.dv / CB, bh = block / slices, c0 = block % slices * CB;
+    constexpr int R = rows_of(CB), L = DK / R;  // rows of a lane, lanes of a column
     const int part = threadIdx.x % L, col = threadIdx.x / L % CB;
     const bool scanner = threadIdx.x < CB * L;
     const int b = bh / p.H, bhk = b * p.Hk + bh % p.H / (p.H / p.Hk);
@@ -313,13 +330,13 @@ __global__ void __launch_bounds__(CB * DK / kRows + kMakers) delta_reverse(Param
     const float *dout = static_cast<const float *>(p.dout) + (size_t)bh * p.N * p.dv + c0;
     const size_t at = (size_t)bh * DK * p.dv + c0 + col;
     const int tiles = (p.N + kTile - 1) / kTile, chunks = (p.N + kC - 1) / kC;
-    float R[kRows];
-    state_in<DK>(p.dSN && scanner ? p.dSN + at : nullptr, R, part, p.dv);
+    uint64_t S[R / 2];  // dL/dS
+    state_in<DK, R>(p.dSN && scanner ? p.dSN + at : nullptr, S, part, p.dv);
     over_tiles<DK, CB, true>(sm, k, q, dout, p.g + (size_t)bh * p.N, p.beta + (size_t)bh * p.N, p.N, p.dv,
                              [&](const Stage<DK, CB> &s, const Group (&groups)[2], int tile) {
         const int t0 = tile * kTile;
         if (tile == tiles - 1 || (t0 + kTile) % kC == 0)
-            state_out<DK>(after + ((size_t)bh * chunks + t0 / kC) * DK * p.dv + c0 + col, R, part, p.dv);
+            state_out<DK, R>(after + ((size_t)bh * chunks + t0 / kC) * DK * p.dv + c0 + col, S, part, p.dv);
 #pragma unroll 1
         for (int h = kTile / kB - 1; h >= 0; --h) {
             const Group &m = groups[h];
@@ -327,7 +344,7 @@ __global__ void __launch_bounds__(CB * DK / kRows + kMakers) delta_reverse(Param
             float x[kB], o[kB], w[kB], beta[kB];
 #pragma unroll
             for (int j = 0; j < kB; ++j) {
-                x[j] = dot_rows<DK>(s.k[r0 + j], R, part);
+                x[j] = dot_rows<DK, R>(s.k[r0 + j], S, part);
                 o[j] = p.scale * s.v[r0 + j][col];
             }
             row8(m.last, w);
@@ -363,15 +380,34 @@ __global__ void __launch_bounds__(CB * DK / kRows + kMakers) delta_reverse(Param
             row8(m.first, w);
             const float whole = m.whole[0];
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) R[r] *= whole;
+            for (int r = 0; r < R / 2; ++r) S[r] = mul2(S[r], pair(whole, whole));
 #pragma unroll
             for (int j = 0; j < kB; ++j) {
-                add_row<DK>(R, s.q[r0 + j], w[j] * o[j], part);
-                add_row<DK>(R, s.k[r0 + j], -w[j] * y[j], part);
+                add_row<DK, R>(S, s.q[r0 + j], w[j] * o[j], part);
+                add_row<DK, R>(S, s.k[r0 + j], -w[j] * y[j], part);
             }
         }
     });
-    if (p.dS0 && scanner) state_out<DK>(p.dS0 + at, R, part, p.dv);
+    if (p.dS0 && scanner) state_out<DK, R>(p.dS0 + at, S, part, p.dv);
+}
+
+template <int DK, int CB> __global__ void __launch_bounds__(scan_threads<DK, CB>() + kMakers) delta_scan(Params p)
+{
+    extern __shared__ float4 smem_raw[];
+    scan<DK, CB, false>(*reinterpret_cast<ScanSmem<DK, CB> *>(smem_raw), p, blockIdx.x, nullptr, nullptr);
+}
+// Both scans of the backward pass, which do not meet: the first half of the blocks goes forward, the second in reverse.
+template <int DK, int CB>
+__global__ void __launch_bounds__(scan_threads<DK, CB>() + kMakers)
+delta_scans(Params p, float *errors, float *before, float *dX, float *after)
+{
+    extern __shared__ float4 smem_raw[];
+    ScanSmem<DK, CB> &sm = *reinterpret_cast<ScanSmem<DK, CB> *>(smem_raw);
+    const int half = gridDim.x / 2;
+    if ((int)blockIdx.x < half)
+        scan<DK, CB, true>(sm, p, blockIdx.x, errors, before);
+    else
+        reverse_scan<DK, CB>(sm, p, blockIdx.x - half, dX, after);
 }
 
 // Gradients within a chunk of kC tokens of one key head, over the heads that share it.  With
@@ -648,25 +684,24 @@ template <typename F> la_status by_widths(const DeltaProblem &p, F f)
 
 // A scan's launch, with CB columns of a head's state to a block.
 template <int DK, int CB, typename... Args>
-la_status launch_scan(const DeltaProblem &p, void (*kernel)(Params, Args...), const Params &prm, Args... args)
+la_status launch_scan(const DeltaProblem &p, int scans, void (*kernel)(Params, Args...), const Params &prm, Args... args)
 {
     const int smem = (int)sizeof(ScanSmem<DK, CB>);
     const la_status st = ensure_smem(reinterpret_cast<const void *>(kernel), smem);
     if (st != LA_OK) return st;
     count_launches();
-    kernel<<<(unsigned)(p.B * p.H * (p.dv / CB)), CB * DK / kRows + kMakers, smem, p.stream>>>(prm, args...);
+    kernel<<<(unsigned)(scans * p.B * p.H * (p.dv / CB)), scan_threads<DK, CB>() + kMakers, smem, p.stream>>>(prm, args...);
     return cuda_status(cudaGetLastError());
 }
-// Blocks of 32 columns or of 8: a narrow block's chain is shorter (at 128 value features, d_k 32, 64, 128: 90, 129, 217 us
-// for 1000 tokens against 115, 163, 412), a wide one shares its tiles with more columns.  The time is a block's, times the
-// rounds in which the machine takes them all, two narrow ones to an SM, wide ones two at d_k 32 and one above.
-bool wide_slices(const DeltaProblem &p)
+// Blocks of 32 columns or of 8: a narrow block's chain is shorter (at d_k 32, 64, 128 and 128 value features, 1000 tokens: 71,
+// 98, 159 us against 93, 158, 370), but two of them share an SM (87, 140, 312 us a round), a wide one has it alone: wide ones
+// where they take fewer rounds (24 heads: 93, 159, 370 us against 165, 227, 462; 19 heads, one round of either: narrow).
+bool wide_slices(const DeltaProblem &p, int scans)
 {
     const int sms = tc::sm_count();
-    const long long columns = (long long)p.B * p.H * p.dv;
-    auto rounds = [](long long blocks, int slots) { return (double)((blocks + slots - 1) / slots); };
-    const double longer = p.dk == 128 ? 1.9 : 1.27;
-    return longer * rounds(columns / 32, p.dk == 32 ? 2 * sms : sms) < rounds(columns / 8, 2 * sms);
+    const long long columns = (long long)scans * p.B * p.H * p.dv;
+    auto rounds = [](long long blocks, int slots) { return (blocks + slots - 1) / slots; };
+    return rounds(columns / 32, sms) < rounds(columns / 8, 2 * sms);
 }
 
 template <int DK, int DV>
@@ -689,11 +724,10 @@ using namespace delta;
 
 la_status delta_forward_simt(const DeltaProblem &p)
 {
-    float *const none = nullptr;
     return by_width(p.dk, [&](auto dk) {
         constexpr int DK = decltype(dk)::value;
-        return wide_slices(p) ? launch_scan<DK, 32>(p, &delta_scan<DK, 32, false>, params_of(p), none, none)
-                              : launch_scan<DK, 8>(p, &delta_scan<DK, 8, false>, params_of(p), none, none);
+        return wide_slices(p, 1) ? launch_scan<DK, 32>(p, 1, &delta_scan<DK, 32>, params_of(p))
+                                 : launch_scan<DK, 8>(p, 1, &delta_scan<DK, 8>, params_of(p));
     });
 }
 
@@ -710,14 +744,9 @@ la_status delta_backward_simt(const DeltaProblem &p)
     float *before = p.scratch, *after = before + states, *errors = after + states, *dX = errors + rows;
     return by_widths(p, [&](auto dk, auto dv) {
         constexpr int DK = decltype(dk)::value, DV = decltype(dv)::value;
-        la_status st = LA_OK;
-        if (wide_slices(p)) {
-            if (p.N > 0) st = launch_scan<DK, 32>(p, &delta_scan<DK, 32, true>, prm, errors, before);
-            if (st == LA_OK) st = launch_scan<DK, 32>(p, &delta_reverse<DK, 32>, prm, dX, after);
-        } else {
-            if (p.N > 0) st = launch_scan<DK, 8>(p, &delta_scan<DK, 8, true>, prm, errors, before);
-            if (st == LA_OK) st = launch_scan<DK, 8>(p, &delta_reverse<DK, 8>, prm, dX, after);
-        }
+        const la_status st = wide_slices(p, 2)
+                                 ? launch_scan<DK, 32>(p, 2, &delta_scans<DK, 32>, prm, errors, before, dX, after)
+                                 : launch_scan<DK, 8>(p, 2, &delta_scans<DK, 8>, prm, errors, before, dX, after);
         if (st != LA_OK || p.N == 0) return st;
         return launch_local<DK, DV>(p, prm, errors, dX, before, after);
     });
