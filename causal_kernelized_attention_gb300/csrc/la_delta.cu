@@ -91,41 +91,50 @@ __device__ __forceinline__ void load_stage(Stage<DK, CB> &s, const float *k, con
     }
 }
 
-// The tile's two groups, by the kMakers threads: 36 pairs (i, j <= i) each, a thread to a pair.  The sums of at most 8
-// gates are taken as they are, without differences.
+__device__ __forceinline__ void row8(const float *p, float (&v)[kB])
+{
+    const float4 a = Vec4<float>::get(p), b = Vec4<float>::get(p + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// The tile's two groups, by the kMakers threads, 64 to a group and each with one product of rows: thread (x, y) has
+// q_x.k_y for y <= x, else k_y.k_x.  The sums of at most 8 gates are taken as they are, without differences.
 template <int DK, int CB, bool kTransposed>
 __device__ __forceinline__ void make_groups(const Stage<DK, CB> &s, Group (&out)[2], int tid)
 {
-    const int h = tid >> 6, pair = tid & 63;
-    Group &o = out[h];
-    int i = 0, j = pair;
-    while (j > i) j -= ++i;  // pair = i (i + 1) / 2 + j
-    const float *g = s.g + kB * h;
-    if (i < kB) {
-        const float4 *ki = reinterpret_cast<const float4 *>(s.k[kB * h + i]), *kj = reinterpret_cast<const float4 *>(s.k[kB * h + j]);
-        const float4 *qi = reinterpret_cast<const float4 *>(s.q[kB * h + i]);
-        float kk[2] = {}, qk[2] = {};
-#pragma unroll 4
-        for (int c = 0; c < DK / 4; ++c) {
-            const float4 x = ki[c], y = kj[c], z = qi[c];
-            kk[0] = fmaf(x.x, y.x, fmaf(x.y, y.y, kk[0]));
-            kk[1] = fmaf(x.z, y.z, fmaf(x.w, y.w, kk[1]));
-            qk[0] = fmaf(z.x, y.x, fmaf(z.y, y.y, qk[0]));
-            qk[1] = fmaf(z.z, y.z, fmaf(z.w, y.w, qk[1]));
-        }
-        float d = 0.f;  // G_i - G_j
-        for (int t = j + 1; t <= i; ++t) d += g[t];
-        const float D = expf(d);
-        (kTransposed ? o.N[j][i] : o.N[i][j]) = D * (kk[0] + kk[1]);
-        (kTransposed ? o.P[j][i] : o.P[i][j]) = D * (qk[0] + qk[1]);
+    const int x = tid >> 3 & 7, y = tid & 7, r0 = tid >> 6 << 3, i = x > y ? x : y, j = x > y ? y : x;
+    Group &o = out[tid >> 6];
+    float g[kB];
+    row8(s.g + r0, g);
+    const ulonglong2 *a = reinterpret_cast<const ulonglong2 *>(y <= x ? s.q[r0 + i] : s.k[r0 + i]);
+    const ulonglong2 *b = reinterpret_cast<const ulonglong2 *>(s.k[r0 + j]);
+    uint64_t s0 = 0, s1 = 0;
+#pragma unroll 8
+    for (int c = 0; c < DK / 4; ++c) {
+        const ulonglong2 u = a[c], w = b[c];
+        s0 = fma2(u.x, w.x, s0);
+        s1 = fma2(u.y, w.y, s1);
+    }
+    float d = 0.f, up = 0.f, down = 0.f, e, f;  // G_i - G_j, G_i, G_8 - G_i
+#pragma unroll
+    for (int t = 0; t < kB; ++t) {
+        d += t > j && t <= i ? g[t] : 0.f;
+        up += t <= i ? g[t] : 0.f;
+        down += t > i ? g[t] : 0.f;
+    }
+    unpair(add2(s0, s1), e, f);
+    const float product = expf(d) * (e + f);
+    if (y <= x) {
+        (kTransposed ? o.P[j][i] : o.P[i][j]) = product;
         if (i != j) (kTransposed ? o.P[i][j] : o.P[j][i]) = 0.f;
-    } else if (pair >= 36 && pair < 36 + kB) {
-        const int t = pair - 36;
-        float a = 0.f, b = 0.f;
-        for (int u = 0; u < kB; ++u) (u <= t ? a : b) += g[u];
-        o.first[t] = expf(a);
-        o.last[t] = expf(b);
-        if (t == kB - 1) o.whole[0] = expf(a);
+    } else {
+        (kTransposed ? o.N[j][i] : o.N[i][j]) = product;
+    }
+    if (i == j) {
+        const float all = expf(up);
+        o.first[i] = all;
+        o.last[i] = expf(down);
+        if (i == kB - 1) o.whole[0] = all;
     }
 }
 
@@ -198,12 +207,6 @@ template <int DK, int R> __device__ __forceinline__ void state_in(const float *a
         S[r / 2] = at ? pair(from[0], from[dv]) : 0;
     }
 }
-__device__ __forceinline__ void row8(const float *p, float (&v)[kB])
-{
-    const float4 a = Vec4<float>::get(p), b = Vec4<float>::get(p + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-
 // The tiles of one slice in order (kDown: from the last): one(stage, groups, tile) by all but the last four warps
 // on a tile that is there.
 template <int DK, int CB, bool kDown, typename F>
@@ -258,7 +261,7 @@ __device__ __forceinline__ void scan(ScanSmem<DK, CB> &sm, const Params &p, int 
         const int t0 = tile * kTile;
         if (kSave && t0 % kC == 0)
             state_out<DK, R>(before + ((size_t)bh * chunks + t0 / kC) * DK * p.dv + c0 + col, S, part, p.dv);
-#pragma unroll 1
+#pragma unroll  // the second group's dot products fill the waits of the first one's outputs (68 us -> 55 at 3 x 5 heads of 32 x 64, 1021 tokens)
         for (int h = 0; h < kTile / kB; ++h) {
             const Group &m = groups[h];
             const int r0 = kB * h;
@@ -337,7 +340,7 @@ __device__ __forceinline__ void reverse_scan(ScanSmem<DK, CB> &sm, const Params 
         const int t0 = tile * kTile;
         if (tile == tiles - 1 || (t0 + kTile) % kC == 0)
             state_out<DK, R>(after + ((size_t)bh * chunks + t0 / kC) * DK * p.dv + c0 + col, S, part, p.dv);
-#pragma unroll 1
+#pragma unroll
         for (int h = kTile / kB - 1; h >= 0; --h) {
             const Group &m = groups[h];
             const int r0 = kB * h;
@@ -693,9 +696,9 @@ la_status launch_scan(const DeltaProblem &p, int scans, void (*kernel)(Params, A
     kernel<<<(unsigned)(scans * p.B * p.H * (p.dv / CB)), scan_threads<DK, CB>() + kMakers, smem, p.stream>>>(prm, args...);
     return cuda_status(cudaGetLastError());
 }
-// Blocks of 32 columns or of 8: a narrow block's chain is shorter (at d_k 32, 64, 128 and 128 value features, 1000 tokens: 71,
-// 98, 159 us against 93, 158, 370), but two of them share an SM (87, 140, 312 us a round), a wide one has it alone: wide ones
-// where they take fewer rounds (24 heads: 93, 159, 370 us against 165, 227, 462; 19 heads, one round of either: narrow).
+// Blocks of 32 columns or of 8: a narrow block's chain is shorter (at d_k 32, 64, 128 and 128 value features, 1000 tokens: 57,
+// 87, 137 us against 86, 143, 367), but two of them share an SM (75, 132, 270 us a round), a wide one has it alone: wide ones
+// where they take fewer rounds (24 heads: 87, 142, 367 us against 142, 212, 400; 19 heads, one round of either: narrow).
 bool wide_slices(const DeltaProblem &p, int scans)
 {
     const int sms = tc::sm_count();
