@@ -174,6 +174,71 @@ def test_a_reset_is_a_new_sequence():
     assert_near(got["dS0"], alone["dS0"].cpu().double(), 2 * delta_tolerance(torch.bfloat16, torch.float32, True))
 
 
+@pytest.mark.parametrize("dk, dv", [(64, 64), (128, 128), (32, 64), (128, 32)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_more_heads_than_the_machine_takes_at_once(dtype, dk, dv):
+    """Heads enough for other launches than a few take (96 and, in the backward, twice that)."""
+    t = TYPES[dtype]
+    s = delta_inputs(16, 2, 24, 48, 150, dk, dv, t, True, (77,))
+    g, scale = on_gpu(s), dk ** -0.5
+    o, SN = forward(g)
+    check(dict(o=o, SN=SN, **backward(g)), delta(s, scale), t, ("o", "SN", "dq", "dk", "dv", "dg", "dbeta", "dS0"))
+    assert la.la_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_poisoned_head_stays_alone(dtype):
+    """NaN, infinities and wide open gates in one head: the others, and its own earlier tokens, are as without them."""
+    t = TYPES[dtype]
+    s = on_gpu(delta_inputs(17, 1, 2, 4, 200, 64, 64, t))
+    o, SN = forward(s)
+    grads = backward(s)
+    for where, value in (("v", math.nan), ("v", math.inf), ("g", math.nan), ("g", 1e4), ("beta", math.nan), ("beta", math.inf)):
+        bad = {n: x.clone() for n, x in s.items()}
+        bad[where][0, 1, 130] = value
+        o2, SN2 = forward(bad)
+        got = backward(bad)
+        others = [0, 2, 3]
+        assert torch.equal(o2[:, others], o[:, others]) and torch.equal(SN2[:, others], SN[:, others])
+        assert torch.equal(o2[:, 1, :128], o[:, 1, :128])
+        assert not torch.isfinite(SN2[:, 1]).all() and not torch.isfinite(o2[:, 1, 130:]).all()
+        for n in ("dv", "dg", "dbeta", "dS0"):
+            assert torch.equal(got[n][:, others], grads[n][:, others]), (where, n)
+        for n in ("dq", "dk"):
+            assert torch.equal(got[n][:, 1], grads[n][:, 1]), (where, n)
+    assert la.la_get_device_status() == 0
+
+
+def test_two_graphs_and_an_eager_call_at_once():
+    """Captured calls keep workspaces of their own: two graphs and eager calls of the same shapes on three streams."""
+    t = torch.bfloat16
+    data = [delta_inputs(20 + i, 2, 4, 8, 700, 64, 64, t) for i in range(3)]
+    s = [on_gpu(x) for x in data]
+    want = [(forward(x), backward(x)) for x in s]
+    streams = [torch.cuda.Stream() for _ in s]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x, st in zip(s[:2], streams):
+        with torch.cuda.stream(st):
+            forward(x, stream=st), backward(x, stream=st)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=st):
+            outs.append((forward(x, stream=st), backward(x, stream=st)))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        with torch.cuda.stream(streams[2]):
+            eager = forward(s[2], stream=streams[2]), backward(s[2], stream=streams[2])
+    torch.cuda.synchronize()
+    for (f, b), (wf, wb) in zip(outs + [eager], want):
+        assert all(torch.equal(x, y) for x, y in zip(f, wf))
+        assert all(torch.equal(b[n], wb[n]) for n in wb)
+    assert la.la_get_device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_graphs_streams_and_given_outputs(dtype):
     """A captured forward, backward and step, replayed with other inputs in place, beside an eager call on another stream."""
