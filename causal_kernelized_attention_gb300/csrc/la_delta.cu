@@ -397,6 +397,8 @@ __device__ __forceinline__ void reverse_scan(ScanSmem<DK, CB> &sm, const Params 
 template <int DK, int CB> __global__ void __launch_bounds__(scan_threads<DK, CB>() + kMakers) delta_scan(Params p)
 {
     extern __shared__ float4 smem_raw[];
+    sm100::griddep_wait();
+    sm100::griddep_launch_dependents();
     scan<DK, CB, false>(*reinterpret_cast<ScanSmem<DK, CB> *>(smem_raw), p, blockIdx.x, nullptr, nullptr);
 }
 // Both scans of the backward pass, which do not meet: the first half of the blocks goes forward, the second in reverse.
@@ -406,6 +408,8 @@ delta_scans(Params p, float *errors, float *before, float *dX, float *after)
 {
     extern __shared__ float4 smem_raw[];
     ScanSmem<DK, CB> &sm = *reinterpret_cast<ScanSmem<DK, CB> *>(smem_raw);
+    sm100::griddep_wait();
+    sm100::griddep_launch_dependents();
     const int half = gridDim.x / 2;
     if ((int)blockIdx.x < half)
         scan<DK, CB, true>(sm, p, blockIdx.x, errors, before);
@@ -435,6 +439,8 @@ __global__ void __launch_bounds__(256) delta_local(Params p, const float *errors
                                                    const float *after)
 {
     extern __shared__ float4 smem_raw[];
+    sm100::griddep_wait();
+    sm100::griddep_launch_dependents();
     LocalSmem<DK, DV> &s = *reinterpret_cast<LocalSmem<DK, DV> *>(smem_raw);
     constexpr int kKG = DK / 4, kI = DK / 32;  // threads along d_k; rows a thread
     const int chunks = (p.N + kC - 1) / kC, bhk = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
@@ -611,6 +617,8 @@ __global__ void __launch_bounds__(256) delta_local(Params p, const float *errors
 template <typename T, int DK>
 __global__ void __launch_bounds__(128) delta_step_kernel(Params p, float *S)
 {
+    sm100::griddep_wait();
+    sm100::griddep_launch_dependents();
     __shared__ float ks[DK], qs[DK];
     __shared__ float4 part[2][4][8];
     const int slices = p.dv / kStepCols, bh = blockIdx.x / slices, c0 = blockIdx.x % slices * kStepCols;
@@ -693,8 +701,7 @@ la_status launch_scan(const DeltaProblem &p, int scans, void (*kernel)(Params, A
     const la_status st = ensure_smem(reinterpret_cast<const void *>(kernel), smem);
     if (st != LA_OK) return st;
     count_launches();
-    kernel<<<(unsigned)(scans * p.B * p.H * (p.dv / CB)), scan_threads<DK, CB>() + kMakers, smem, p.stream>>>(prm, args...);
-    return cuda_status(cudaGetLastError());
+    return tc::launch_dependent(kernel, (unsigned)(scans * p.B * p.H * (p.dv / CB)), scan_threads<DK, CB>() + kMakers, smem, p.stream, prm, args...);
 }
 // Blocks of 32 columns or of 8: a narrow block's chain is shorter (at d_k 32, 64, 128 and 128 value features, 1000 tokens: 57,
 // 87, 137 us against 86, 143, 367), but two of them share an SM (75, 132, 270 us a round), a wide one has it alone: wide ones
@@ -716,8 +723,7 @@ la_status launch_local(const DeltaProblem &p, const Params &prm, const float *er
     if (st != LA_OK) return st;
     const unsigned grid = (unsigned)p.B * p.Hk * ceil_div(p.N, kC);
     count_launches();
-    delta_local<DK, DV><<<grid, 256, smem, p.stream>>>(prm, errors, dX, before, after);
-    return cuda_status(cudaGetLastError());
+    return tc::launch_dependent(&delta_local<DK, DV>, grid, 256, smem, p.stream, prm, errors, dX, before, after);
 }
 
 }  // namespace
@@ -762,11 +768,8 @@ la_status delta_step(const DeltaProblem &p, float *S)
         constexpr int DK = decltype(dk)::value;
         const unsigned grid = (unsigned)(p.B * p.H * (p.dv / kStepCols));
         count_launches();
-        if (p.dtype == LA_F32)
-            delta_step_kernel<float, DK><<<grid, 128, 0, p.stream>>>(prm, S);
-        else
-            delta_step_kernel<__nv_bfloat16, DK><<<grid, 128, 0, p.stream>>>(prm, S);
-        return cuda_status(cudaGetLastError());
+        return p.dtype == LA_F32 ? tc::launch_dependent(&delta_step_kernel<float, DK>, grid, 128, 0, p.stream, prm, S)
+                                 : tc::launch_dependent(&delta_step_kernel<__nv_bfloat16, DK>, grid, 128, 0, p.stream, prm, S);
     });
 }
 
