@@ -191,7 +191,7 @@ bool norm_supported(const la_group_norm_spec *s, int B, int L, int C)
 {
     if (s->heads_first && C / s->groups > kNormTokenChannels) return false;
     const long long tokens = (long long)B * L, entries = s->per_token ? tokens : B;
-    // groups, and blocks of sums (at most 152 * 6 + entries each of up to 2^16 / 256 columns of blocks), in 32 bits
+    // groups in 32 bits; so are the blocks over positions (a round of them, and an entry's runs of columns) of what fits in memory
     return L <= kMaxTokens && tokens <= 0x3fffffff && C <= 0x3fffff && entries * s->groups <= 0x7fffffff;
 }
 

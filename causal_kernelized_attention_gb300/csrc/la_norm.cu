@@ -346,10 +346,15 @@ template <int VEC, typename F> __device__ __forceinline__ void for_groups(int c,
     }
 }
 
+// Blocks that the registers let an SM hold; a launch is one round of them (16 x 1024 positions of 32 x 40 channels, backward: 60
+// us with rounds and a third, and a thread a column of 160, 43 so; 16 x 4096 of 32 x 16 forward 42 -> 38, gated 58 -> 44).
+constexpr int sums_per_sm(bool back) { return back ? 2 : 4; }
+constexpr int apply_per_sm(bool gate, bool back) { return back ? 2 : gate ? 3 : 4; }
+
 // Columns of VEC channels, `cols` of them to a block of 256 threads; the other threads of a column take
 // further positions.  Sums per channel and split, joined in shared memory in a fixed order.
 template <typename T, int VEC, bool kGate, bool kBack, bool kAct>
-__global__ void __launch_bounds__(256) norm_sums(Params p, int cols)
+__global__ void __launch_bounds__(256, sums_per_sm(kBack)) norm_sums(Params p, int cols)
 {
     typedef Pack<T, VEC> Pk;
     extern __shared__ float sums[];  // [2][threads of a column][cols * VEC]
@@ -544,7 +549,7 @@ __global__ void __launch_bounds__(kFinish) norm_weight_grads(const float *part, 
 
 // y, or dx and dgate, of all positions.
 template <typename T, int VEC, bool kGate, bool kBack, bool kAct>
-__global__ void __launch_bounds__(256) norm_apply(Params p, int cols)
+__global__ void __launch_bounds__(256, apply_per_sm(kGate, kBack)) norm_apply(Params p, int cols)
 {
     typedef Pack<T, VEC> Pk;
     sm100::griddep_wait();
@@ -849,17 +854,23 @@ TokenShape token_shape(const NormProblem &p)
 struct MapShape {
     int vec, cols, zs, splits, rows;
 };
-MapShape map_shape(const NormProblem &p)
+MapShape map_shape(const NormProblem &p, int per_sm)
 {
     MapShape s;
     const int full = p.dtype == LA_F32 ? 4 : 8;
     s.vec = p.C % full == 0 ? full : 1;
     const int n = p.C / s.vec;
-    s.zs = ceil_div(n, 256);
-    s.cols = ceil_div(n, s.zs);
+    // the fewest runs of columns that leave no more than a tenth of the threads idle (160 columns: two of 80, three threads
+    // a column), or else the one that leaves fewest
+    int best = 0;
+    for (int zs = ceil_div(n, 256); zs <= 8 * ceil_div(n, 256) && best * 10 < 256 * 9; ++zs) {
+        if (best && (long long)p.B * zs > 1 << 24) break;  // (a grid's size)
+        const int cols = ceil_div(n, zs), busy = 256 / cols * n / zs;
+        if (busy > best && (zs == ceil_div(n, 256) || cols >= 8)) best = busy, s.zs = zs, s.cols = cols;
+    }
     const int ny = 256 / s.cols;
     const long long blocks = (long long)p.B * s.zs;
-    int want = (int)((tc::sm_count() * 4 + blocks - 1) / blocks);
+    int want = (int)(tc::sm_count() * per_sm / blocks);
     const int most = ceil_div(p.L, ny * 6);
     want = want < most ? want : most;
     if (want < 1) want = 1;
@@ -868,10 +879,10 @@ MapShape map_shape(const NormProblem &p)
     return s;
 }
 
-// The slab and cluster of norm_fused; size 0 where the groups do not fit, or the tensors are so large that three launches
-// of many small blocks do better (GPU times in bf16, one launch against three: 2.1 M elements forward 6.9 / 14.5 us, 5.2 M
-// 11.4 / 20.3, 10.5 M 20 / 26, 33.6 M 50 / 43; backward 5.2 M 22 / 29, 10.5 M 39 / 38, 21 M 69 / 61: a CTA that holds
-// its part of a group loads it, sums it and stores it one after another, with few of its kind beside it).
+// The slab and cluster of norm_fused; size 0 where the groups do not fit, or what would be held is so large that three
+// launches of many small blocks do better (device times in bf16, one launch against three: forward 2.1 M elements 7.8 / 12.0 us,
+// 8.4 M 14.9 / 18.7, 10.5 M 19.9 / 20.7 and gated 28.6 / 22.2; backward 2.1 M 12.4 / 15.1, 5.2 M 22.2 / 18.6, gated 31.5 / 19.7:
+// a CTA that holds its part of a group loads it, sums it and stores it one after another, with few of its kind beside it).
 struct FusedShape {
     int vec, size, smem;
     Slab slab;
@@ -885,7 +896,7 @@ FusedShape fused_shape(const NormProblem &p)
     while (groups < G && groups < kFusedGroups && groups * D * e < 128) ++groups;
     while (groups < G && groups < kFusedGroups && groups * D % full != 0) ++groups;  // whole vectors
     const int width = groups * D;
-    if ((long long)p.B * p.L * p.C * e * tensors > 32ll << 20) return f;
+    if ((long long)p.B * p.L * p.C * e * tensors > 16ll << 20) return f;
     f.vec = p.C % full == 0 && width % full == 0 ? full : 1;
     f.slab.groups = groups, f.slab.slabs = ceil_div(G, groups), f.slab.cols = width / f.vec;
     if (f.slab.cols > kFusedThreads) return f;
@@ -967,7 +978,7 @@ template <typename T, bool kGate, bool kBack, bool kAct> la_status launch_map(co
         constexpr int kWide = std::is_same<T, float>::value ? 4 : 8;
         return f.vec == 1 ? launch_fused<T, 1, kGate, kBack, kAct>(p, q, f) : launch_fused<T, kWide, kGate, kBack, kAct>(p, q, f);
     }
-    const MapShape s = map_shape(p);
+    const MapShape s = map_shape(p, sums_per_sm(kBack)), a = map_shape(p, apply_per_sm(kGate, kBack));
     constexpr int kFull = std::is_same<T, float>::value ? 4 : 8;
     q.splits = s.splits, q.rows = s.rows, q.zs = s.zs;
     const int smem = 2 * (256 / s.cols) * s.cols * s.vec * 4;
@@ -983,7 +994,8 @@ template <typename T, bool kGate, bool kBack, bool kAct> la_status launch_map(co
         st = tc::launch_dependent(&norm_statistics<T>, groups, kFinish, 0, p.stream, q);
     if (st != LA_OK) return st;
     if (!kBack) q.mean = q.mean_out, q.rstd = q.rstd_out;
-    return tc::launch_dependent(apply, grid, 256, 0, p.stream, q, s.cols);
+    q.splits = a.splits, q.rows = a.rows;
+    return tc::launch_dependent(apply, (unsigned)(a.splits * a.zs) * p.B, 256, 0, p.stream, q, s.cols);
 }
 
 template <bool kBack> la_status launch(const NormProblem &p, const Params &q)
@@ -1010,7 +1022,7 @@ size_t norm_scratch(const NormProblem &p)
     const NormProblem q = as_map(p);
     const FusedShape f = fused_shape(q);
     if (f.size > 0) return grads ? (size_t)q.B * f.size * 2 * p.C * 4 : 0;
-    return ((size_t)q.B * map_shape(q).splits * 2 * p.C + 2 * (size_t)q.B * p.spec.groups) * 4;
+    return ((size_t)q.B * map_shape(q, sums_per_sm(q.backward)).splits * 2 * p.C + 2 * (size_t)q.B * p.spec.groups) * 4;
 }
 
 la_status group_norm(const NormProblem &given)
@@ -1021,7 +1033,7 @@ la_status group_norm(const NormProblem &given)
     Params q = params_of(p);
     q.part = grads || !(tokens || fused) ? p.scratch : nullptr;
     if (!tokens && !fused) {
-        float *means = p.scratch + (size_t)p.B * map_shape(p).splits * 2 * p.C;
+        float *means = p.scratch + (size_t)p.B * map_shape(p, sums_per_sm(p.backward)).splits * 2 * p.C;
         if (p.backward || !q.mean_out) q.mean_out = means;
         if (p.backward || !q.rstd_out) q.rstd_out = means + (size_t)p.B * q.G;
     }

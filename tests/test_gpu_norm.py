@@ -152,3 +152,11 @@ def test_graph(per_token):
     graph.replay()
     for got, ref in zip(fwd + bwd, want[0] + want[1]):
         assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,L,G,D,gate", [(3, 2900, 32, 40, False), (2, 4100, 32, 40, True), (1, 9000, 10, 206, False), (40, 700, 5, 52, True)])
+def test_large_maps(B, L, G, D, dtype, gate):
+    """Tensors beyond what one launch holds on chip, with columns that share a block and that do not."""
+    s, dy = inputs(11, B, L, G, D, TYPES[dtype], False, gate, True)
+    check(s, dy, G, "silu", False, False, True)
