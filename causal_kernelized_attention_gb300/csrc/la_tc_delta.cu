@@ -1,5 +1,5 @@
-// Gated delta rule on the tensor cores: the forward pass (bf16), two launches: the
-// chunks' matrices, then the scan.
+// Gated delta rule on the tensor cores: the forward pass (bf16): the chunks' matrices, then the scan, in two
+// launches or, for calls that are long enough, side by side in one.
 #include "la_tc_delta_scan.cuh"
 
 namespace la {
@@ -110,9 +110,21 @@ template <int DK, int DV> la_status forward_both(const DeltaProblem &p)
                             prm, images, ready, workers);
 }
 
+// One launch clears its flags and fills its pipeline first (7 us), and hides the preparing kernel behind the scan: it pays from 5
+// chunks an SM, at 16 chunks a head and more (with fewer the scan is over before the rest is hidden), while half of the
+// SMs are left to prepare.  One launch against two, us, d 64 / d 128: 32 heads of 8 chunks 32 / 39 against 26 / 32, of 16
+// 42 / 53 against 40 / 50, of 24 52 / 69 against 56 / 72, of 64 108 / 133 against 129 / 165; 64 of 12 46 / 54 against
+// 40 / 52, of 16 52 / 62 against 51 / 63, of 64 142 / 168 against 163 / 206; 8 of 32 63 / 79 against 56 / 73, of
+// 64 102 / 133 against 101 / 133; 90 of 64 258 / 289 against 192 / 240.
+bool one_launch(const DeltaProblem &p)
+{
+    const long long heads = (long long)p.B * p.H, chunks = ceil_div(p.N, kChunk);
+    return heads * 2 <= sm_count() && chunks >= 16 && heads * chunks >= 5LL * sm_count();
+}
+
 template <int DK, int DV> la_status forward(const DeltaProblem &p)
 {
-    if (p.B * p.H * 2 <= sm_count()) return forward_both<DK, DV>(p);
+    if (one_launch(p)) return forward_both<DK, DV>(p);
     typedef ScanSmem<DK, DV, kForward> Sm;
     static_assert(sizeof(Sm) <= 227 * 1024, "");
     const Params prm = params_of(p);

@@ -186,6 +186,38 @@ def test_more_heads_than_the_machine_takes_at_once(dtype, dk, dv):
     assert la.la_get_device_status() == 0
 
 
+@pytest.mark.parametrize("dk, dv", [(64, 64), (128, 128), (64, 128), (128, 64), (32, 64)])
+def test_long_calls_of_some_heads(dk, dv):
+    """Heads and chunks enough for preparation and scan side by side (48 heads of 16 chunks, the last one odd), in
+    two graphs at once on inputs of their own, and with a head poisoned."""
+    s = [on_gpu(delta_inputs(30 + i, 1, 24, 48, 1009, dk, dv, torch.bfloat16, True, (500,))) for i in range(2)]
+    want = [forward(x) for x in s]
+    exact = delta(s[0], dk ** -0.5, backward=False)
+    check(dict(zip(("o", "SN"), want[0])), {n: x.cpu() for n, x in exact.items()}, torch.bfloat16, ("o", "SN"))
+    streams = [torch.cuda.Stream() for _ in s]
+    graphs, outs = [], []
+    for x, st in zip(s, streams):
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=st):
+            outs.append(forward(x, stream=st))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for got, w in zip(outs, want):
+        assert all(torch.equal(x, y) for x, y in zip(got, w))
+    bad = {n: x.clone() for n, x in s[0].items()}
+    bad["v"][0, 7, 900] = math.nan
+    o, SN = forward(bad)
+    others = [h for h in range(48) if h != 7]
+    assert torch.equal(o[:, others], want[0][0][:, others]) and torch.equal(SN[:, others], want[0][1][:, others])
+    assert torch.equal(o[:, 7, :896], want[0][0][:, 7, :896]) and not torch.isfinite(SN[:, 7]).all()
+    assert la.la_get_device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_a_poisoned_head_stays_alone(dtype):
     """NaN, infinities and wide open gates in one head: the others, and its own earlier tokens, are as without them."""
