@@ -491,8 +491,8 @@ __global__ void __launch_bounds__(kFinish) norm_statistics(Params p)
         const float inv = 1.f / p.D / p.L;
         float v = s1 * inv;
         if (p.center) {
-            const float d = s0 * inv;
-            v = fmaxf(0.f, fmaf(-d, d, v));
+            const float d = s0 * inv, e = fmaf(-d, d, v);
+            v = e < 0.f ? 0.f : e;  // (a NaN stays)
             p.mean_out[blockIdx.x] = Elem<T>::to_f32(static_cast<const T *>(p.x)[(size_t)bi * p.L * p.C + g * p.D]) + d;
         }
         p.rstd_out[blockIdx.x] = rsqrtf(v + p.eps);
@@ -761,8 +761,8 @@ __global__ void __launch_bounds__(kFusedThreads) norm_fused(Params p, Slab q)
         } else {
             float m = 0.f, v = a1 * inv;
             if (p.center) {
-                const float d = a0 * inv;
-                v = fmaxf(0.f, fmaf(-d, d, v));
+                const float d = a0 * inv, e = fmaf(-d, d, v);
+                v = e < 0.f ? 0.f : e;  // (a NaN stays)
                 m = Elem<T>::to_f32(static_cast<const T *>(p.x)[(size_t)entry * p.L * p.C + (size_t)(g0 + i) * p.D]) + d;
             }
             const float rs = rsqrtf(v + p.eps);

@@ -650,7 +650,8 @@ la_status la_delta_step(float *S, const void *q, const void *k, const void *v, c
  * dw, db (fp32, summed over all positions; each may be NULL: not wanted; they are deterministic).
  *
  * Supported: C a multiple of groups, L <= 2^30; heads_first with up to 512 channels a group; w, b, mean, rstd, dw and
- * db need only their own 4-byte alignment.  Statistics and sums are fp32.  Outputs overlap no input and no other output.
+ * db need only their own 4-byte alignment.  Statistics and sums are fp32: an infinity or a NaN makes its group's rstd
+ * NaN (an infinity without centring: 0), and values whose squares overflow make it 0.  Outputs overlap no input and no other output.
  * B, L or C = 0 is an empty problem (dw, db = 0).  Scratch (partial sums) from the stream's workspace, or
  * stream-ordered while the stream is being captured.
  */

@@ -160,3 +160,24 @@ def test_large_maps(B, L, G, D, dtype, gate):
     """Tensors beyond what one launch holds on chip, with columns that share a block and that do not."""
     s, dy = inputs(11, B, L, G, D, TYPES[dtype], False, gate, True)
     check(s, dy, G, "silu", False, False, True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,L,G,D", [(2, 64, 4, 16), (2, 4200, 32, 40)])  # one launch, and three
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 1e25])
+def test_infinities_and_overflow_over_positions(value, B, L, G, D, dtype):
+    """An infinity or a NaN makes its group's statistics NaN or infinite and y NaN; finite values whose squares overflow fp32
+    have a variance of infinity (rstd = 0).  Neither looks like a spread of 0 (rstd = 1 / sqrt(eps)).  The other groups are as without."""
+    s, dy = inputs(12, B, L, G, D, TYPES[dtype], False, False, True)
+    (y, mean, rstd), _ = run(s, dy, G, "none", False, False, True)
+    s["x"][1, L // 3, D + 2] = value
+    (y2, mean2, rstd2), _ = run(s, dy, G, "none", False, False, True)
+    if value == 1e25:
+        assert float(rstd2[1, 1]) == 0 and torch.equal(y2[1, :, D:2 * D].cpu(), s["b"][D:2 * D].to(TYPES[dtype]).expand(L, D))
+    else:
+        assert bool(rstd2[1, 1].isnan()) and not bool(mean2[1, 1].isfinite()) and bool(y2[1, :, D:2 * D].isnan().all())
+    y2[1, :, D:2 * D], mean2[1, 1], rstd2[1, 1] = y[1, :, D:2 * D], mean[1, 1], rstd[1, 1]
+    assert torch.equal(y2, y) and torch.equal(mean2, mean) and torch.equal(rstd2, rstd)
+    # without centring the mean square is infinite, too
+    (y3, _, rstd3), _ = run(s, dy, G, "none", False, False, False)
+    assert bool(rstd3[1, 1].isnan()) if value != value else float(rstd3[1, 1]) == 0
