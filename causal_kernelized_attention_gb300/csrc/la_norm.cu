@@ -5,7 +5,8 @@
 // Two shapes of problem, both bound by memory: groups of one token's channels (per_token, the norm
 // behind the heads of linear attention), where a few lanes hold a group in registers and every
 // tensor is read once; and groups over all positions, where sums per channel come first.  Statistics
-// are fp32 sums of differences (from the mean, or from the channel's first value).
+// are fp32: a token's are sums of differences from the mean; over positions each thread keeps the mean of a channel and the
+// squares about it, and these are joined as such, so that no value counts for more than it is worth.
 #include <type_traits>
 
 #include "la_common.cuh"
@@ -38,6 +39,7 @@ template <typename T, int VEC> struct Pack {
         static_assert(VEC == 1, "");
         v[0] = Elem<T>::to_f32(r);
     }
+    static __device__ __forceinline__ float at(Raw r, int) { return Elem<T>::to_f32(r); }
     static __device__ __forceinline__ void put(T *p, const float (&v)[VEC]) { __stcs(p, Elem<T>::from_f32(v[0])); }
 };
 template <> struct Pack<float, 4> {
@@ -46,6 +48,7 @@ template <> struct Pack<float, 4> {
     static __device__ __forceinline__ Raw load(const float *p) { return __ldcs(reinterpret_cast<const float4 *>(p)); }
     static __device__ __forceinline__ Raw keep(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
     static __device__ __forceinline__ void open(const Raw &a, float (&v)[4]) { v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w; }
+    static __device__ __forceinline__ float at(const Raw &a, int e) { return e == 0 ? a.x : e == 1 ? a.y : e == 2 ? a.z : a.w; }
     static __device__ __forceinline__ void put(float *p, const float (&v)[4])
     {
         __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
@@ -61,6 +64,11 @@ template <> struct Pack<__nv_bfloat16, 8> {
         const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+    static __device__ __forceinline__ float at(const Raw &a, int e)
+    {
+        const uint32_t u = e < 2 ? a.x : e < 4 ? a.y : e < 6 ? a.z : a.w;
+        return __uint_as_float(e & 1 ? u & 0xffff0000u : u << 16);
     }
     static __device__ __forceinline__ void put(__nv_bfloat16 *p, const float (&v)[8])
     {
@@ -351,8 +359,54 @@ template <int VEC, typename F> __device__ __forceinline__ void for_groups(int c,
 constexpr int sums_per_sm(bool back) { return back ? 2 : 4; }
 constexpr int apply_per_sm(bool gate, bool back) { return back ? 2 : gate ? 3 : 4; }
 
+// The mean m of the rows so far of a thread's channels, and the sum q of the squares about it (without centring about 0).
+// With the sum s of K new rows' differences from m, n rows with them: m' = m + s / n, and q' = q + (their squares) - s^2 / n.
+// Differences are from the rows before, so neither a large mean nor an outlier, first or later, cancels: one shift for a whole
+// group, its first value, lost 2^-24 (mean - shift)^2 of the variance.
+template <typename T, int VEC> struct Moments {
+    typedef Pack<T, VEC> Pk;
+    float m[VEC] = {}, q[VEC] = {};
+    int n = 0;
+    template <int K> __device__ __forceinline__ void add(const typename Pk::Raw *r, bool center)
+    {
+        if (center && n == 0) Pk::open(r[0], m);
+        n += K;
+        const float part = __frcp_rn((float)n);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            float s = 0.f;
+#pragma unroll
+            for (int u = 0; u < K; ++u) {
+                const float d = Pk::at(r[u], e) - m[e];
+                s += d;
+                q[e] = fmaf(d, d, q[e]);
+            }
+            if (center) {
+                const float t = s * part;
+                m[e] += t;
+                q[e] = fmaf(-s, t, q[e]);
+            }
+        }
+    }
+};
+// The moments of one channel over `ny` threads, `step` floats apart, whose means stand at `m` and squares at `q`; thread k
+// has n / ny rows, one more if k < n % ny.
+__device__ __forceinline__ void join_moments(const float *m, const float *q, int step, int ny, int n, float &mean, float &squares)
+{
+    const int base = n / ny, more = n % ny;
+    const float ref = m[0];
+    float s = 0.f, v = 0.f;
+    for (int k = 0; k < ny; ++k) s = fmaf((float)(base + (k < more)), m[k * step] - ref, s);
+    mean = n > 0 ? ref + s / n : 0.f;
+    for (int k = 0; k < ny; ++k) {
+        const float d = m[k * step] - mean;
+        v += fmaf((float)(base + (k < more)) * d, d, q[k * step]);
+    }
+    squares = v;
+}
+
 // Columns of VEC channels, `cols` of them to a block of 256 threads; the other threads of a column take
-// further positions.  Sums per channel and split, joined in shared memory in a fixed order.
+// further positions.  Moments (forward) or sums (backward) per channel and split, joined in shared memory in a fixed order.
 template <typename T, int VEC, bool kGate, bool kBack, bool kAct>
 __global__ void __launch_bounds__(256, sums_per_sm(kBack)) norm_sums(Params p, int cols)
 {
@@ -364,6 +418,7 @@ __global__ void __launch_bounds__(256, sums_per_sm(kBack)) norm_sums(Params p, i
     const int z = blockIdx.x % p.zs, c = (z * cols + tx) * VEC, bi = blockIdx.x / p.zs / p.splits, split = blockIdx.x / p.zs % p.splits;
     const bool on = ty < ny && c < p.C;
     float s1[VEC] = {}, s2[VEC] = {};
+    Moments<T, VEC> so_far;
     if (on) {
         const T *x = static_cast<const T *>(p.x) + (size_t)bi * p.L * p.C + c;
         const T *dy = static_cast<const T *>(p.dy) + (kBack ? (size_t)bi * p.L * p.C + c : 0);
@@ -383,18 +438,15 @@ __global__ void __launch_bounds__(256, sums_per_sm(kBack)) norm_sums(Params p, i
         };
         int l = split * p.rows + ty;
         load(l);
-        float shift[VEC], r[VEC], w[VEC], b[VEC];
-        for_groups<VEC>(c, p.D, [&](int e, int g) {
-            if (!kBack) {  // differences from the group's first value (from 0 without centring)
-                shift[e] = p.center ? Elem<T>::to_f32(__ldg(static_cast<const T *>(p.x) + (size_t)bi * p.L * p.C + g * p.D)) : 0.f;
-            } else {
+        float m[VEC], r[VEC], w[VEC], b[VEC];
+        if (kBack)
+            for_groups<VEC>(c, p.D, [&](int e, int g) {
                 const size_t st = (size_t)bi * p.G + g;
-                shift[e] = p.center ? __ldg(p.mean + st) : 0.f;
+                m[e] = p.center ? __ldg(p.mean + st) : 0.f;
                 r[e] = __ldg(p.rstd + st);
                 w[e] = p.w ? __ldg(p.w + c + e) : 1.f;
                 b[e] = p.b ? __ldg(p.b + c + e) : 0.f;
-            }
-        });
+            });
         while (l < l1) {
             typename Pk::Raw cx[kAhead], cd[kBack ? kAhead : 1], cg[kGate ? kAhead : 1];
 #pragma unroll
@@ -406,25 +458,29 @@ __global__ void __launch_bounds__(256, sums_per_sm(kBack)) norm_sums(Params p, i
             const int l0 = l;
             l += kAhead * ny;
             load(l);
+            if constexpr (!kBack) {
+                if (l0 + (kAhead - 1) * ny < l1) {
+                    so_far.template add<kAhead>(cx, p.center);
+                } else {
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                if (l0 + u * ny >= l1) break;
-                float v[VEC], d[VEC], ga[VEC];
-                Pk::open(cx[u], v);
-                if (kBack) Pk::open(cd[u], d);
-                if (kGate) Pk::open(cg[u], ga);
+                    for (int u = 0; u < kAhead; ++u)
+                        if (l0 + u * ny < l1) so_far.template add<1>(cx + u, p.center);
+                }
+            } else {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    if (kBack) {
-                        const float h = (v[e] - shift[e]) * r[e];
+                for (int u = 0; u < kAhead; ++u) {
+                    if (l0 + u * ny >= l1) break;
+                    float v[VEC], d[VEC], ga[VEC];
+                    Pk::open(cx[u], v);
+                    Pk::open(cd[u], d);
+                    if (kGate) Pk::open(cg[u], ga);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float h = (v[e] - m[e]) * r[e];
                         float dg;
                         const float dz = back<T, kGate, kAct>(h, w[e], b[e], d[e], kGate ? ga[e] : 0.f, &dg);
                         s1[e] = fmaf(dz, h, s1[e]);
                         s2[e] += dz;
-                    } else {
-                        const float t = v[e] - shift[e];
-                        s1[e] += t;
-                        s2[e] = fmaf(t, t, s2[e]);
                     }
                 }
             }
@@ -434,16 +490,26 @@ __global__ void __launch_bounds__(256, sums_per_sm(kBack)) norm_sums(Params p, i
     if (ty < ny)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            sums[ty * width + tx * VEC + e] = s1[e];
-            sums[(ny + ty) * width + tx * VEC + e] = s2[e];
+            sums[ty * width + tx * VEC + e] = kBack ? s1[e] : so_far.m[e];
+            sums[(ny + ty) * width + tx * VEC + e] = kBack ? s2[e] : so_far.q[e];
         }
     __syncthreads();
     float *out = p.part + ((size_t)bi * p.splits + split) * 2 * p.C;
-    for (int i = threadIdx.x; i < 2 * width; i += 256) {
-        const int which = i / width, j = i % width, ch = z * width + j;
-        float v = 0.f;
-        for (int k = 0; k < ny; ++k) v += sums[(which * ny + k) * width + j];
-        if (ch < p.C) out[(size_t)which * p.C + ch] = v;
+    if constexpr (!kBack) {
+        const int n = min(p.L, (split + 1) * p.rows) - split * p.rows;
+        for (int i = threadIdx.x; i < width && z * width + i < p.C; i += 256) {
+            float mean, squares;
+            join_moments(sums + i, sums + ny * width + i, width, ny, n, mean, squares);
+            out[z * width + i] = mean;
+            out[p.C + z * width + i] = squares;
+        }
+    } else {
+        for (int i = threadIdx.x; i < 2 * width; i += 256) {
+            const int which = i / width, j = i % width, ch = z * width + j;
+            float v = 0.f;
+            for (int k = 0; k < ny; ++k) v += sums[(which * ny + k) * width + j];
+            if (ch < p.C) out[(size_t)which * p.C + ch] = v;
+        }
     }
 }
 
@@ -460,8 +526,8 @@ __device__ __forceinline__ float block_sum(float v, float *tmp)
 }
 
 // The two sums of a group, over its channels and the splits of its entry: of value 0 and value 1 of the
-// partial sums, with the channels' weights where kWeighted.
-template <bool kWeighted> __device__ __forceinline__ void group_sums(const Params &p, int bg, float *tmp, float &s0, float &s1)
+// partial sums, with the channels' weights.
+__device__ __forceinline__ void group_sums(const Params &p, int bg, float *tmp, float &s0, float &s1)
 {
     const int bi = bg / p.G, g = bg % p.G, n = p.D * p.splits;
     const float *part = p.part + (size_t)bi * p.splits * 2 * p.C + g * p.D;
@@ -469,7 +535,7 @@ template <bool kWeighted> __device__ __forceinline__ void group_sums(const Param
 #pragma unroll 4
     for (int i = threadIdx.x; i < n; i += kFinish) {
         const int split = i / p.D, c = i - split * p.D;
-        const float *at = part + (size_t)split * 2 * p.C + c, w = kWeighted && p.w ? __ldg(p.w + g * p.D + c) : 1.f;
+        const float *at = part + (size_t)split * 2 * p.C + c, w = p.w ? __ldg(p.w + g * p.D + c) : 1.f;
         s0 = fmaf(w, at[0], s0);
         s1 = fmaf(w, at[p.C], s1);
     }
@@ -477,24 +543,28 @@ template <bool kWeighted> __device__ __forceinline__ void group_sums(const Param
     s1 = block_sum(s1, tmp);
 }
 
-// Forward: mean and rstd of each group.
-template <typename T>
+// Forward: mean and rstd of each group, from the moments of its channels' splits.
 __global__ void __launch_bounds__(kFinish) norm_statistics(Params p)
 {
     __shared__ float tmp[kFinish / 32];
     sm100::griddep_wait();
     sm100::griddep_launch_dependents();
-    float s0, s1;
-    group_sums<false>(p, blockIdx.x, tmp, s0, s1);
-    if (threadIdx.x == 0) {
-        const int bi = blockIdx.x / p.G, g = blockIdx.x % p.G;
-        const float inv = 1.f / p.D / p.L;
-        float v = s1 * inv;
-        if (p.center) {
-            const float d = s0 * inv, e = fmaf(-d, d, v);
-            v = e < 0.f ? 0.f : e;  // (a NaN stays)
-            p.mean_out[blockIdx.x] = Elem<T>::to_f32(static_cast<const T *>(p.x)[(size_t)bi * p.L * p.C + g * p.D]) + d;
+    const int bi = blockIdx.x / p.G, g = blockIdx.x % p.G, n = p.D * p.splits;
+    const float *part = p.part + (size_t)bi * p.splits * 2 * p.C + g * p.D, ref = part[0], inv = 1.f / p.D / p.L;
+    auto sum = [&](auto f) {
+        float s = 0.f;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n; i += kFinish) {
+            const int split = i / p.D, c = i - split * p.D;
+            const float *at = part + (size_t)split * 2 * p.C + c;
+            s += f((float)(min(p.L, (split + 1) * p.rows) - split * p.rows), at[0], at[p.C]);
         }
+        return block_sum(s, tmp);
+    };
+    const float mean = ref + sum([&](float rows, float m, float) { return rows * (m - ref); }) * inv;
+    const float v = sum([&](float rows, float m, float q) { return fmaf(rows * (m - mean), m - mean, q); }) * inv;
+    if (threadIdx.x == 0) {
+        if (p.center) p.mean_out[blockIdx.x] = mean;
         p.rstd_out[blockIdx.x] = rsqrtf(v + p.eps);
     }
 }
@@ -529,7 +599,7 @@ __global__ void __launch_bounds__(kFinish) norm_group_means(Params p, float *dw,
         return;
     }
     float dhh, dh;
-    group_sums<true>(p, blockIdx.x, tmp[0], dhh, dh);
+    group_sums(p, blockIdx.x, tmp[0], dhh, dh);
     if (threadIdx.x == 0) {
         const float inv = 1.f / p.D / p.L;
         p.mean_out[blockIdx.x] = p.center ? dh * inv : 0.f;
@@ -672,40 +742,45 @@ __global__ void __launch_bounds__(kFusedThreads) norm_fused(Params p, Slab q)
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    float shift[VEC], r[VEC], wv[VEC], b[VEC], s1[VEC] = {}, s2[VEC] = {};
+    float m_in[VEC], r[VEC], wv[VEC], b[VEC], s1[VEC] = {}, s2[VEC] = {};
+    Moments<T, VEC> so_far;
     if (on)
         for_groups<VEC>(c, p.D, [&](int e, int g) {
             const size_t st = (size_t)entry * p.G + g0 + g;
             if (c + e >= width) {
-                shift[e] = 0.f, r[e] = 0.f, wv[e] = 0.f, b[e] = 0.f;
+                m_in[e] = 0.f, r[e] = 0.f, wv[e] = 0.f, b[e] = 0.f;
                 return;
             }
-            if (kBack)
-                shift[e] = p.center ? __ldg(p.mean + st) : 0.f, r[e] = __ldg(p.rstd + st);
-            else  // differences from the group's first value (from 0 without centring)
-                shift[e] = p.center ? Elem<T>::to_f32(__ldg(static_cast<const T *>(p.x) + (size_t)entry * p.L * p.C + (size_t)(g0 + g) * p.D)) : 0.f;
+            if (kBack) m_in[e] = p.center ? __ldg(p.mean + st) : 0.f, r[e] = __ldg(p.rstd + st);
             wv[e] = p.w ? __ldg(p.w + g0 * p.D + c + e) : 1.f;
             b[e] = p.b ? __ldg(p.b + g0 * p.D + c + e) : 0.f;
         });
     auto sum_rows = [&](int w) {
-        for (int i = w * quarter; i < min(mine_rows, (w + 1) * quarter); ++i) {
-            const int at = (ty + i * ny) * q.cols + tx;
-            float v[VEC], d[VEC], ga[VEC];
-            Pk::open(sx[at], v);
-            if (kBack) Pk::open(sd[at], d);
-            if (kKeepGate) Pk::open(sg[at], ga);
+        int i = w * quarter;
+        const int end = min(mine_rows, (w + 1) * quarter), at0 = ty * q.cols + tx, step = ny * q.cols;
+        if constexpr (!kBack) {
+            constexpr int kRows = 4;
+            for (; i + kRows <= end; i += kRows) {
+                Raw v[kRows];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                if (kBack) {
-                    const float h = (v[e] - shift[e]) * r[e];
+                for (int u = 0; u < kRows; ++u) v[u] = sx[at0 + (i + u) * step];
+                so_far.template add<kRows>(v, p.center);
+            }
+            for (; i < end; ++i) so_far.template add<1>(sx + at0 + i * step, p.center);
+        } else {
+            for (; i < end; ++i) {
+                const int at = at0 + i * step;
+                float v[VEC], d[VEC], ga[VEC];
+                Pk::open(sx[at], v);
+                Pk::open(sd[at], d);
+                if (kKeepGate) Pk::open(sg[at], ga);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float h = (v[e] - m_in[e]) * r[e];
                     float dg;
                     const float dz = back<T, kGate, kAct>(h, wv[e], b[e], d[e], kGate ? ga[e] : 0.f, &dg);
                     s1[e] = fmaf(dz, h, s1[e]);
                     s2[e] += dz;
-                } else {
-                    const float t = v[e] - shift[e];
-                    s1[e] += t;
-                    s2[e] = fmaf(t, t, s2[e]);
                 }
             }
         }
@@ -721,25 +796,47 @@ __global__ void __launch_bounds__(kFusedThreads) norm_fused(Params p, Slab q)
     const int wide = q.cols * VEC;
     if (ty < ny)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) sums[ty * wide + c + e] = s1[e], sums[(ny + ty) * wide + c + e] = s2[e];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * width; i += kFusedThreads) {  // the channels' sums, over row 0 of each
-        float *at = sums + (i < width ? 0 : ny * wide - width) + i;
-        float v = at[0];
-        for (int k = 1; k < ny; ++k) v += at[k * wide];
-        at[0] = v;
-        if (kBack && p.part) p.part[((size_t)(entry * size + rank) * 2 + (i >= width)) * p.C + (size_t)g0 * p.D + (i < width ? i : i - width)] = v;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x >> 5; i < 2 * groups; i += kFusedThreads / 32) {  // a warp to a group's sum
-        const int which = i >= groups, g = i - which * groups;
-        float v = 0.f;
-        for (int k = threadIdx.x & 31; k < p.D; k += 32) {
-            const float one = sums[which * ny * wide + g * p.D + k];
-            v += kBack && p.w ? one * __ldg(p.w + (size_t)(g0 + g) * p.D + k) : one;
+        for (int e = 0; e < VEC; ++e) {
+            sums[ty * wide + c + e] = kBack ? s1[e] : so_far.m[e];
+            sums[(ny + ty) * wide + c + e] = kBack ? s2[e] : so_far.q[e];
         }
-        v = lanes_sum(v, 32);
-        if ((threadIdx.x & 31) == 0) mine[which][g] = v;
+    __syncthreads();
+    if constexpr (!kBack) {
+        for (int i = threadIdx.x; i < width; i += kFusedThreads) {  // the channels' moments, over row 0 of each
+            float mean, squares;
+            join_moments(sums + i, sums + ny * wide + i, wide, ny, rows, mean, squares);
+            sums[i] = mean;
+            sums[ny * wide + i] = squares;
+        }
+        __syncthreads();
+        for (int g = threadIdx.x >> 5; g < groups; g += kFusedThreads / 32) {  // a warp to a group's
+            const float *m = sums + g * p.D, *sq = m + ny * wide;
+            float s = 0.f, v = 0.f;
+            for (int k = threadIdx.x & 31; k < p.D; k += 32) s += m[k] - m[0];
+            const float mean = m[0] + lanes_sum(s, 32) / p.D;
+            for (int k = threadIdx.x & 31; k < p.D; k += 32) v += fmaf((float)rows * (m[k] - mean), m[k] - mean, sq[k]);
+            v = lanes_sum(v, 32);
+            if ((threadIdx.x & 31) == 0) mine[0][g] = mean, mine[1][g] = v;
+        }
+    } else {
+        for (int i = threadIdx.x; i < 2 * width; i += kFusedThreads) {  // the channels' sums, over row 0 of each
+            float *at = sums + (i < width ? 0 : ny * wide - width) + i;
+            float v = at[0];
+            for (int k = 1; k < ny; ++k) v += at[k * wide];
+            at[0] = v;
+            if (p.part) p.part[((size_t)(entry * size + rank) * 2 + (i >= width)) * p.C + (size_t)g0 * p.D + (i < width ? i : i - width)] = v;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x >> 5; i < 2 * groups; i += kFusedThreads / 32) {  // a warp to a group's sum
+            const int which = i >= groups, g = i - which * groups;
+            float v = 0.f;
+            for (int k = threadIdx.x & 31; k < p.D; k += 32) {
+                const float one = sums[which * ny * wide + g * p.D + k];
+                v += p.w ? one * __ldg(p.w + (size_t)(g0 + g) * p.D + k) : one;
+            }
+            v = lanes_sum(v, 32);
+            if ((threadIdx.x & 31) == 0) mine[which][g] = v;
+        }
     }
     __syncthreads();
     if (size > 1) {
@@ -751,20 +848,20 @@ __global__ void __launch_bounds__(kFusedThreads) norm_fused(Params p, Slab q)
         sm100::cluster_sync_all();
     }
     for (int i = threadIdx.x; i < groups; i += kFusedThreads) {
-        float a0 = size > 1 ? 0.f : mine[0][i], a1 = size > 1 ? 0.f : mine[1][i];
-        for (int k = 0; size > 1 && k < size; ++k) a0 += all[k][0][i], a1 += all[k][1][i];
         const float inv = 1.f / p.D / p.L;
         const size_t st = (size_t)entry * p.G + g0 + i;
+        auto one = [&](int k, int which) { return size > 1 ? all[k][which][i] : mine[which][i]; };
         if (kBack) {  // the means of dh h and of dh
+            float a0 = 0.f, a1 = 0.f;
+            for (int k = 0; k < size; ++k) a0 += one(k, 0), a1 += one(k, 1);
             done[0][i] = a0 * inv;
             done[1][i] = p.center ? a1 * inv : 0.f;
         } else {
-            float m = 0.f, v = a1 * inv;
-            if (p.center) {
-                const float d = a0 * inv, e = fmaf(-d, d, v);
-                v = e < 0.f ? 0.f : e;  // (a NaN stays)
-                m = Elem<T>::to_f32(static_cast<const T *>(p.x)[(size_t)entry * p.L * p.C + (size_t)(g0 + i) * p.D]) + d;
-            }
+            auto share = [&](int k) { return (float)max(0, min(q.rows, p.L - k * q.rows)) / p.L; };  // of the positions
+            float d = 0.f, v = 0.f;
+            for (int k = 1; k < size; ++k) d = fmaf(share(k), one(k, 0) - one(0, 0), d);
+            const float m = one(0, 0) + d;
+            for (int k = 0; k < size; ++k) v += fmaf(share(k) * (one(k, 0) - m), one(k, 0) - m, one(k, 1) * inv);
             const float rs = rsqrtf(v + p.eps);
             done[0][i] = m, done[1][i] = rs;
             if (rank == 0) {
@@ -788,7 +885,7 @@ __global__ void __launch_bounds__(kFusedThreads) norm_fused(Params p, Slab q)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             if (kBack) {
-                const float h = (v[e] - shift[e]) * r[e];
+                const float h = (v[e] - m_in[e]) * r[e];
                 float dg = 0.f;
                 const float dz = back<T, kGate, kAct>(h, wv[e], b[e], d[e], kGate ? ga[e] : 0.f, &dg);
                 v[e] = r[e] * (fmaf(dz, wv[e], -a1[e]) - h * a0[e]);
@@ -991,7 +1088,7 @@ template <typename T, bool kGate, bool kBack, bool kAct> la_status launch_map(co
     if (kBack)
         st = tc::launch_dependent(&norm_group_means, groups + (p.dw || p.db ? 2u * ceil_div(p.C, 32) : 0u), kFinish, 0, p.stream, q, p.dw, p.db);
     else
-        st = tc::launch_dependent(&norm_statistics<T>, groups, kFinish, 0, p.stream, q);
+        st = tc::launch_dependent(&norm_statistics, groups, kFinish, 0, p.stream, q);
     if (st != LA_OK) return st;
     if (!kBack) q.mean = q.mean_out, q.rstd = q.rstd_out;
     q.splits = a.splits, q.rows = a.rows;

@@ -7,7 +7,7 @@ torch = pytest.importorskip("torch")
 
 import causal_kernelized_attention_gb300 as la  # noqa: E402
 from delta_ref import norm_backward, norm_forward  # noqa: E402
-from hybrid_ref import assert_within  # noqa: E402
+from hybrid_ref import U, assert_within, half  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -181,3 +181,37 @@ def test_infinities_and_overflow_over_positions(value, B, L, G, D, dtype):
     # without centring the mean square is infinite, too
     (y3, _, rstd3), _ = run(s, dy, G, "none", False, False, False)
     assert bool(rstd3[1, 1].isnan()) if value != value else float(rstd3[1, 1]) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,L,G,D", [(2, 1024, 4, 16), (1, 19, 2, 1200), (1, 16384, 4, 64), (2, 8191, 8, 40), (1, 262144, 1, 7)])
+@pytest.mark.parametrize("place,value,mean,spread", [("first", 300.0, 0.0, 1.0), ("first", 1e4, 0.0, 1.0), ("last", -1e4, 0.0, 1.0), ("middle", 3e3, 5.0, 1.0),
+                                                     ("first", 0.0, 1000.0, 0.1), ("first", 0.0, 100.0, 0.1)])
+def test_an_outlier_over_positions(place, value, mean, spread, B, L, G, D, dtype):
+    """One value far from the others of its group, the first, the last or another.  The variance is a sum of squares, none
+    negative, of which a thread adds at most 200 one after another here, a block at most 256, the join 64 and its trees 9: each
+    addition and each square's own steps are off by at most u of what stands, 600 u of the variance together, 300 u of rstd; the
+    mean by as many u of the spread, and 4 u of itself.  (Differences from any one value of the group would cost u (mean -
+    value)^2 as often as there are values.)"""
+    s, _ = inputs(13, B, L, G, D, TYPES[dtype], False, False, True)
+    gen = torch.Generator().manual_seed(14)
+    x = (mean + spread * torch.randn((B, L, G, D), generator=gen)).to(TYPES[dtype])
+    at = {"first": (0, 0), "last": (L - 1, D - 1), "middle": (L // 2, D // 3)}[place]
+    x[:, at[0], :, at[1]] = value
+    s["x"] = x.reshape(B, L, G * D)
+    c = {i: None if t is None else t.cuda() for i, t in s.items()}
+    y, m, r = la.la_group_norm_forward(c["x"], G, w=c["w"], b=c["b"])
+    x64 = x.double()
+    want = x64.mean((1, 3), keepdim=True)
+    var = (x64 - want).square().mean((1, 3), keepdim=True)
+    rstd = (var + 1e-5).rsqrt()
+    em = 300 * U * var.sqrt() + 4 * U * want.abs()
+    assert_within(m, want.reshape(B, G), em.reshape(B, G), "mean")
+    # (an error of the mean adds its square to the variance)
+    er = rstd * (300 * U + 0.5 * (em * rstd).square())
+    assert_within(r, rstd.reshape(B, G), er.reshape(B, G), "rstd")
+    h = (x64 - want) * rstd
+    z = (h * s["w"].double().reshape(G, D) + s["b"].double().reshape(G, D)).reshape(B, L, G * D)
+    eh = em * rstd + h.abs() * (er / rstd + 4 * U) + 2 * U * want.abs() * rstd
+    ez = (eh * s["w"].double().abs().reshape(G, D)).reshape(B, L, G * D) + 4 * U * (z.abs() + s["b"].double().abs())
+    assert_within(y, z, ez + half(TYPES[dtype]) * z.abs() + 1e-30, "y")
