@@ -8,6 +8,8 @@
 // (exp(G) and exp(G_C - G) scale rows).  The way back through a chunk, of R = dL/dS', has the same form,
 //   dX = Z^T dO + W2 R,   Z = scale P T2,  T2 = (I + diag(beta) N)^-1,  W2 = T2^T exp(G_C - G) K,
 //   dL/dS = exp(G_C) R + scale (exp(G) Q)^T dO - K^T exp(G) beta dX,        dV = beta dX.
+// Forward, O takes the operand that S' does: with U' = beta exp(r) E, r = G_C - G (at least -kClosed: P U = P' U' needs its
+// inverse), P' = P exp(-r), S' = exp(G_C) S + K^T U'.
 // All that does not depend on the states is prepared for all chunks at once, so that a step of a scan
 // is two products: the errors from the state, the next state from the errors.
 #pragma once
@@ -23,24 +25,27 @@ using namespace tc;
 
 constexpr int kChunk = 64;
 constexpr uint32_t kSq = kChunk * 128;  // a [64 x 64] bf16 image, 128-byte swizzled: 8 KB
+// Gates that close what a token writes to exp(-64) by its chunk's end close it no further in S' (1.6e-28 of it is left): its
+// inverse, 6e27, leaves room for q.k up to 5e10.
+constexpr float kClosed = 64.f;
 constexpr uint64_t kDrainNs = 100000000ull;
 
 // The scalars of a chunk, by token; a scan loads three of the first four.
 struct Scalars {
-    float beta[kChunk], write[kChunk], first[kChunk], back[kChunk];  // beta, beta exp(G_C - G), exp(G), -beta exp(G)
+    float beta[kChunk], write[kChunk], first[kChunk], back[kChunk];  // beta, beta exp(G_C - G) (forward: exp(r)), exp(G), -beta exp(G)
     // exp(G_C - G); G log2(e) as two floats (differences of the pairs carry no more than their own rounding)
-    float last[kChunk], hi[kChunk], lo[kChunk], spare[kChunk];
+    float last[kChunk], hi[kChunk], lo[kChunk], open[kChunk];  // (forward: open = exp(-r))
 };
 static_assert(sizeof(Scalars) == 2048, "");
 constexpr uint32_t kScanScalars = 3 * kChunk * 4;
 
 // A chunk's image: the scalars, then matrices in two bf16 parts (high, then low: the value within 2^-17) as 128-byte
-// swizzled MMA operands: T [i][j]; W [i][d_k], in boxes of 64 columns; P diag(beta) [i][j] (high part alone) for the
-// forward pass, or Z [i][j] and W2 [j][d_k] for the backward.
+// swizzled MMA operands: T [i][j]; W [i][d_k], in boxes of 64 columns; P' [i][j] for the forward pass, or Z [i][j]
+// and W2 [j][d_k] for the backward.
 template <int DK> struct Layout {
     static constexpr uint32_t w_bytes = 2 * (DK / 64) * kSq;
     static constexpr uint32_t t = sizeof(Scalars), w = t + 2 * kSq, p = w + w_bytes, z = p, w2 = z + 2 * kSq;
-    static constexpr uint32_t forward_bytes = p + kSq, backward_bytes = w2 + w_bytes;
+    static constexpr uint32_t forward_bytes = p + 2 * kSq, backward_bytes = w2 + w_bytes;
 };
 
 // Two values as bf16 high parts and the bf16 rounding of what is left: together within 2^-17 of each.

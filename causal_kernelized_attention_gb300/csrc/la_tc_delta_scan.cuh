@@ -7,7 +7,9 @@
 // so that each step's result becomes the left operand of the next (tcgen05.ld, scale, split, tcgen05.st)
 // without passing through shared memory or another thread.  What the state feeds is held to fp32's
 // neighbourhood: T, W, S and U are multiplied as two bf16 parts (within 2^-17; the product of two low parts is
-// left out), K, Q, V and dO are exact; only products that end in o alone take single parts.
+// left out), K, Q, V and dO are exact.  So is what ends in o, whose two terms, the state's answer and that of the chunk's own
+// writes, nearly cancel where a key is overwritten (with E, P and S in one part there, o of near-parallel keys was off by
+// 1.6%, four times its own rounding).
 #pragma once
 
 #include "la_tc_delta.cuh"
@@ -215,6 +217,9 @@ __device__ __forceinline__ void prepare_chunk(PrepSmem<DK, kBack> &sm, const CUt
         float lo, lo_end;
         const float hi = scaled(G, lo), rest = scaled(end - G, lo_end);
         const float first = exp2f(hi) * exp2f(lo), last = exp2f(rest) * exp2f(lo_end);
+        constexpr float kLeast = -kClosed * 1.4426950408889634f;  // (kClosed in powers of two)
+        const bool closed = rest < kLeast;
+        const float open = closed ? exp2f(-kLeast) : exp2f(-rest) * exp2f(-lo_end);
         Scalars &s = sm.s;
         s.hi[tid] = hi;
         s.lo[tid] = lo;
@@ -222,9 +227,10 @@ __device__ __forceinline__ void prepare_chunk(PrepSmem<DK, kBack> &sm, const CUt
         s.last[tid] = last;
         s.beta[tid] = gates.y;
         s.back[tid] = -gates.y * first;
-        s.write[tid] = gates.y * last;
-        s.spare[tid] = 0.f;
+        s.write[tid] = gates.y * (!kBack && closed ? exp2f(kLeast) : last);
+        s.open[tid] = open;
     }
+    uint8_t *tp[2] = {sm.qk[0], DK == 64 ? sm.extra : sm.qk[DK / 64 - 1]};  // over Q, once its product is done: P', then T's parts
     bool ok = sound;
     if (warp == 0) {
         ok = ok && wait_bar_warp(&g_delta_status, &sm.abort, &sm.full, turn & 1u);
@@ -282,10 +288,13 @@ __device__ __forceinline__ void prepare_chunk(PrepSmem<DK, kBack> &sm, const CUt
                         *reinterpret_cast<uint4 *>(sm.p[0] + at) = h;
                         *reinterpret_cast<uint4 *>(sm.p[kBack ? 1 : 0] + at) = l;
                     } else {
-                        const float *b = sm.s.beta + j0 + 8 * c;
-                        h = make_uint4(pack_bf16(b[0] * x[0], b[1] * x[1]), pack_bf16(b[2] * x[2], b[3] * x[3]),
-                                       pack_bf16(b[4] * x[4], b[5] * x[5]), pack_bf16(b[6] * x[6], b[7] * x[7]));
-                        *reinterpret_cast<uint4 *>(image + Lay::p + at) = h;
+                        const ulonglong2 *b = reinterpret_cast<const ulonglong2 *>(sm.s.open + j0 + 8 * c);
+                        split2(mul2(b[0].x, pair(x[0], x[1])), h.x, l.x);
+                        split2(mul2(b[0].y, pair(x[2], x[3])), h.y, l.y);
+                        split2(mul2(b[1].x, pair(x[4], x[5])), h.z, l.z);
+                        split2(mul2(b[1].y, pair(x[6], x[7])), h.w, l.w);
+                        *reinterpret_cast<uint4 *>(tp[0] + at) = h;
+                        *reinterpret_cast<uint4 *>(tp[1] + at) = l;
                     }
                 }
             } else {
@@ -300,15 +309,27 @@ __device__ __forceinline__ void prepare_chunk(PrepSmem<DK, kBack> &sm, const CUt
             }
         }
     }
+    if (!kBack) fence_proxy_async_smem();
     tc_fence_before();
     sync();
+    if (!kBack && warp == 0) {  // P', while T is found
+        if (ok && elect_one()) {
+            bulk_store(image + Lay::p, tp[0], kSq);
+            bulk_store(image + Lay::p + kSq, tp[1], kSq);
+            tma_store_commit();
+        }
+        __syncwarp();
+    }
     if (!kBack || warp < 4)
         invert(sm.a[0], tid & 127, bar);
     else
         invert(sm.a[kBack ? 1 : 0], tid & 127, bar + 1);
+    if (!kBack && warp == 0) {
+        if (elect_one()) tma_store_wait_read_all();
+        __syncwarp();
+    }
     sync();
     // T to global memory, and -T exp(G) over the rows of Q
-    uint8_t *tp[2] = {sm.qk[0], DK == 64 ? sm.extra : sm.qk[DK / 64 - 1]};
     for (int u = tid; u < kChunk * 8; u += kNT) {
         const int i = u >> 3, c = 8 * (u & 7);
         const uint32_t at = sw128_offset(i, c);
@@ -515,6 +536,8 @@ template <int DK, int DV, int kMode> struct ScanSmem {
     // K (and in reverse Q) are needed late in a chunk: one stage where shared memory is short
     static constexpr int kKeyStages = kMode == kForward ? 2 : 1;
     static constexpr bool kOutOverW = kMode != kForward && DK >= DV;  // E's rows are staged where W was
+    // forward, d_k and d_v 128: no room to stage o (d 64 without a stage: 67.8 us of a call against 64)
+    static constexpr bool kStageO = kMode == kForward && DK + DV < 256;
     static constexpr uint32_t kMats = 2 * kSq + Layout<DK>::w_bytes;
     // forward, d_k 64: the products of o have room for two chunks, so that the chain does not wait for the warps of o
     static constexpr int kOuts = kMode == kForward && DK == 64 ? 2 : 1, kScalarRing = kOuts + 2;
@@ -522,14 +545,11 @@ template <int DK, int DV, int kMode> struct ScanSmem {
     uint8_t mats[2][kMats];  // T or Z, W or W2
     uint8_t k[kKeyStages][DK / 64][kSq];
     uint8_t q[kMode == kSave ? 1 : kKeyStages][kMode == kSave ? 1 : DK / 64][kSq];  // (kSave: not used)
-    union {  // o is staged by one mode, a state by the others
-        uint8_t state[kMode == kForward ? rows_bytes(DV) / 2 : state_bytes(DK, DV)];
-        uint8_t o[rows_bytes(DV) / 2];
+    union {  // P is used by one mode, a state kept by the others
+        uint8_t p[kMode == kForward ? 2 : 1][kMode == kForward ? 2 * kSq : 16];
+        uint8_t state[kMode == kForward ? 16 : state_bytes(DK, DV)];
     };
-    union {
-        uint8_t p[kMode == kForward ? 2 : 1][kMode == kForward ? kSq : 16];
-        uint8_t e[kMode == kForward || kOutOverW ? 16 : rows_bytes(DV)];  // E's rows
-    };
+    uint8_t rows[kStageO ? rows_bytes(DV) / 2 : kMode == kForward || kOutOverW ? 16 : rows_bytes(DV)];  // of o, or of E
     float scalars[kScalarRing][3][kChunk];  // beta, write, first; in reverse write, first, back
     uint64_t full[2];                       // a stage's V and matrices are there (and scalars, but for kForward)
     uint64_t keys_full[2], rows_read[2];    // its K, Q, P (and scalars) are; the warps of E's rows are done with it
@@ -541,8 +561,8 @@ template <int DK, int DV, int kMode> struct ScanSmem {
     uint32_t tmem_base;
     int abort;
 };
-// TMEM columns: what S^T gains in a chunk; S^T's bf16 parts (low part: later U^T for o); E^T of two chunks (forward: later U^T's parts);
-// forward: (Q S)^T and (P U)^T; otherwise U^T's parts and dO^T's
+// TMEM columns: what S^T gains in a chunk; S^T's bf16 parts; E^T of two chunks (forward: later U'^T's parts);
+// forward: (Q S)^T and (P' U')^T; otherwise U^T's parts and dO^T's
 template <int DK> struct Columns {
     static constexpr uint32_t S = 0, parts = DK, e = 2 * DK, qs = e + 128, pu = qs + 64;
 };
@@ -591,7 +611,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
 
     if (warp == kCopyWarp) {
         fence_proxy_async_global();  // the images were written by plain stores
-        constexpr uint32_t kKeyBytes = (kMode == kSave ? 1 : 2) * (DK / 64) * kSq + (kKeep ? 0 : kSq + kScanScalars);
+        constexpr uint32_t kKeyBytes = (kMode == kSave ? 1 : 2) * (DK / 64) * kSq + (kKeep ? 0 : 2 * kSq + kScanScalars);
         int c = 0;
         for (; ok && c < chunks; ++c) {
             const int st = c & 1, x = chunk_of(c);
@@ -617,7 +637,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                     if (kMode != kSave) tma_load_3d(sm.q[ks][b], &map_q, &sm.keys_full[ks], 64 * b, x * kChunk, bhk);
                     tma_load_3d(sm.k[ks][b], &map_k, &sm.keys_full[ks], 64 * b, x * kChunk, bhk);
                 }
-                if (!kKeep) bulk_load(sm.p[st], img + Lay::p, kSq, &sm.keys_full[ks]);
+                if (!kKeep) bulk_load(sm.p[st], img + Lay::p, 2 * kSq, &sm.keys_full[ks]);
                 if (!kKeep) bulk_load(sm.scalars[c % Sm::kScalarRing], img, kScanScalars, &sm.keys_full[ks]);
             }
             __syncwarp();
@@ -683,18 +703,20 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                 wait(&sm.keys_full[st], (uint32_t)(c >> 1) & 1u);
             if (!kKeep) {
                 tc_fence_after();
-                if (elect_one()) {  // (Q S)^T
+                if (elect_one()) {  // (Q S)^T, both parts
                     const uint64_t b = dq + st * (DK / 64 * kBox);
 #pragma unroll
-                    for (int kk = 0; kk < DK / 16; ++kk)
-                        mma_ts(tQ, tmem + Col::parts + kk * 8, b + (kk >> 2) * kBox + (kk & 3) * 2, id, kk > 0);
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int kk = 0; kk < DK / 16; ++kk)
+                            mma_ts(tQ, tmem + Col::parts + part * (DK / 2) + kk * 8, b + (kk >> 2) * kBox + (kk & 3) * 2, id, part + kk > 0);
                 }
                 __syncwarp();
             }
             if (kMode == kReverse) wait(&sm.d_ready, ph);
             wait(&sm.u_ready, ph);
             tc_fence_after();
-            if (elect_one()) {  // what the state gains, U^T K (in reverse also dO^T Q), both parts; (P U)^T
+            if (elect_one()) {  // what the state gains, U^T K (in reverse also dO^T Q), both parts; (P' U')^T
                 const uint64_t b = dk + (kKeep ? 0 : st * (DK / 64 * kBox));
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
@@ -706,15 +728,21 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                     }
                 mma_commit(&sm.s_full);
                 if (!kKeep) {
-                    const uint64_t bp = dp + st * kBox;
+                    // high high, low high, high low (P' lower triangular); the low parts take 3 of 68 us (32 heads of 2048, d 64),
+                    // and behind the next errors' product, where the chain leaves the tensor cores idle, 5
+                    const uint64_t bp = dp + st * (2 * kBox);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)  // (lower triangular)
-                        mma_ts(tQ + 64 + 16 * kk, tmem + Col::parts + DK / 2 + kk * 8, bp + kk * 2 + kk * (2048 >> 4),
-                               idesc_bf16_f32(128, kChunk - 16 * kk, false, false), kk > 0);
+                    for (int part = 0; part < 3; ++part)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ts(tQ + 64 + 16 * kk, tU + kk * 16 + (part == 1) * 8, bp + (part == 2) * kBox + kk * 2 + kk * (2048 >> 4),
+                                   idesc_bf16_f32(128, kChunk - 16 * kk, false, false), part + kk > 0);
                     mma_commit(&sm.o_full[st]);
                 }
             }
             __syncwarp();
+            // (the next E^T goes over operands that P' U' of the chunk before has read)
+            if (!kKeep && c > 0) wait(&sm.o_full[st ^ 1], (uint32_t)((c - 1) >> 1) & 1u);
             if (c + 1 < chunks) from_values(c + 1);
         }
         if (elect_one()) {
@@ -739,7 +767,6 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
             const int st = c & 1;
             const uint32_t ph = (uint32_t)c & 1u;
             if (kKeep && c > 0 && !(ok = wait(&sm.stored, ph ^ 1u))) break;
-            if (!kKeep && c > 0 && !(ok = wait(&sm.o_full[st ^ 1], (uint32_t)((c - 1) >> 1) & 1u))) break;  // P U has read U
 #pragma unroll
             for (int x = 0; x < kKeys; x += 16) {  // two parts: to TMEM and to the image that is kept
                 uint32_t hi[8], lo[8];
@@ -784,11 +811,6 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                 }
                 tmem_st8(tU, hi);
                 tmem_st8(tU + 8, lo);
-                if (!kKeep) {  // E for o, in one part (P is scaled by beta)
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) hi[e / 2] = pack_bf16(__uint_as_float(a[e]), __uint_as_float(a[e + 1]));
-                    tmem_st8(tl + Col::parts + DK / 2 + 8 * part, hi);
-                }
             }
             tmem_st_wait();
             tc_fence_before();
@@ -819,7 +841,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
         for (int c = 0; ok && c < chunks; ++c) {
             const int st = c & 1, x = chunk_of(c);
             const uint32_t ph = (uint32_t)c & 1u;
-            uint8_t *out = !kKeep ? sm.o : Sm::kOutOverW ? sm.mats[st] + 2 * kSq : sm.e;
+            uint8_t *out = Sm::kOutOverW ? sm.mats[st] + 2 * kSq : sm.rows;
             if (kMode == kReverse) {  // scale exp(G) dO as a left operand, once the last state product has read it
                 if (!(ok = wait(&sm.full[st], (uint32_t)(c >> 1) & 1u))) break;
                 if (c > 0 && !(ok = wait(&sm.s_full, ph ^ 1u))) break;
@@ -885,13 +907,16 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
             } else {
                 if (!(ok = wait(&sm.o_full[st], (uint32_t)(c >> 1) & 1u))) break;
                 tc_fence_after();
-                if (c > 0) {  // the last store has read the tile
+                if (Sm::kStageO && c > 0) {  // the last store has read the tile
                     if (warp == kOutWarp && lane == 0) tma_store_wait_read_all();
                     __syncwarp();
                     named_bar_sync(1, 128);
                 }
                 const float *first = sm.scalars[c % Sm::kScalarRing][2];
-                if (live)
+                const int t0 = x * kChunk;
+                // (without a stage: a warp writes 32 neighbouring features of a row, whole sectors)
+                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + ((size_t)bh * p.N + t0) * p.dv + f;
+                if (Sm::kStageO ? live : f < p.dv)
 #pragma unroll
                     for (int y = 0; y < kChunk; y += 16) {
                         uint32_t a[16], b[16];
@@ -905,21 +930,30 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
                             float o0, o1;
                             unpair(mul2(pair(p.scale, p.scale), fma2(pair(w.x, w.y), pair(__uint_as_float(a[e]), __uint_as_float(a[e + 1])),
                                                                      pair(__uint_as_float(b[e]), __uint_as_float(b[e + 1])))), o0, o1);
-                            const uint32_t o = pack_bf16(o0, o1);
-                            uint8_t *to = out + (y + e) / 8 * 1024;
-                            *reinterpret_cast<uint16_t *>(to + at[e & 7]) = (uint16_t)o;
-                            *reinterpret_cast<uint16_t *>(to + at[(e + 1) & 7]) = (uint16_t)(o >> 16);
+                            if constexpr (Sm::kStageO) {
+                                const uint32_t both = pack_bf16(o0, o1);
+                                uint8_t *to = out + (y + e) / 8 * 1024;
+                                *reinterpret_cast<uint16_t *>(to + at[e & 7]) = (uint16_t)both;
+                                *reinterpret_cast<uint16_t *>(to + at[(e + 1) & 7]) = (uint16_t)(both >> 16);
+                            } else {
+                                if (t0 + y + e < p.N) o[(size_t)(y + e) * p.dv] = __float2bfloat16_rn(o0);
+                                if (t0 + y + e + 1 < p.N) o[(size_t)(y + e + 1) * p.dv] = __float2bfloat16_rn(o1);
+                            }
                         }
                     }
                 tc_fence_before();
-                fence_proxy_async_smem();
-                mbar_arrive(&sm.o_read[st]);
-                named_bar_sync(1, 128);
-                if (warp == kOutWarp && lane == 0) {
-                    for (int b = 0; b < DV / 64; ++b) tma_store_3d(&map_o, out + b * kSq, 64 * b, x * kChunk, bh);
-                    tma_store_commit();
+                if constexpr (Sm::kStageO) {
+                    fence_proxy_async_smem();
+                    mbar_arrive(&sm.o_read[st]);
+                    named_bar_sync(1, 128);
+                    if (warp == kOutWarp && lane == 0) {
+                        for (int b = 0; b < DV / 64; ++b) tma_store_3d(&map_o, out + b * kSq, 64 * b, t0, bh);
+                        tma_store_commit();
+                    }
+                    __syncwarp();
+                } else {
+                    mbar_arrive(&sm.o_read[st]);
                 }
-                __syncwarp();
             }
         }
         if (warp == kOutWarp && lane == 0) tma_store_wait_all();

@@ -340,3 +340,59 @@ def test_a_layer_of_delta_rule_and_head_norm():
     for i, x in zip(("dq", "dk", "dv"), got):
         assert_near(x, ref[i], 5 * tol, i)
     assert_near(dgate.reshape(B, N, H, d).transpose(1, 2), gd.grad.reshape(B, N, H, d).transpose(1, 2), 4 * tol, "dgate")
+
+
+def correlated(seed, kind, B, Hk, H, N, d, dtype):
+    """Keys that overwrite one another: 8 keys in turn, read back; a token repeated 16 times; keys near one direction; positive
+    ones.  Writes are nearly whole (beta 0.7 to 1), gates nearly open."""
+    s = delta_inputs(seed, B, Hk, H, N, d, d, torch.float32)
+    gen = torch.Generator().manual_seed(seed + 1)
+    if kind == "overwritten":
+        few = torch.randn((B, Hk, 8, d), generator=gen)
+        k = few[:, :, torch.arange(N) % 8]
+        q = few[:, :, (torch.arange(N) * 5 + 3) % 8]
+    elif kind == "repeated":
+        k = s["k"][:, :, ::16].repeat_interleave(16, 2)[:, :, :N]
+        q = k.roll(-3, 2)
+    elif kind == "parallel":
+        base = torch.randn((B, Hk, 1, d), generator=gen)
+        k, q = (base + 0.1 * torch.randn((B, Hk, N, d), generator=gen) for _ in range(2))
+    else:
+        k, q = s["k"].abs(), s["q"].abs()
+    s["k"], s["q"] = ((x / x.norm(dim=-1, keepdim=True)).to(dtype) for x in (k, q))
+    s["v"], s["dout"] = s["v"].to(dtype), s["dout"].to(dtype)
+    s["beta"] = 1 - 0.3 * torch.rand((B, H, N), generator=gen)
+    s["g"] = -0.02 * torch.rand((B, H, N), generator=gen)
+    return s
+
+
+KINDS = ["overwritten", "repeated", "parallel", "positive"]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kind", KINDS)
+def test_keys_that_overwrite_one_another(kind, d, dtype):
+    """What is read back is the difference of what the state and the chunk's own writes answer, each as large as the old
+    value.  Every operand is held to 2^-17 (fp32: u), so that terms some times as large as o leave o's own rounding what
+    counts; the states, whose old content goes in the keys' directions, may be off by four times as much of their own size."""
+    t = TYPES[dtype]
+    s = correlated(40, kind, 2, 1, 2, 190, d, t)
+    want = delta(s, d ** -0.5, backward=False)
+    o, SN = forward(on_gpu(s))
+    assert_near(o, want["o"], delta_tolerance(t, t, True), "o")
+    assert_near(SN, want["SN"], 4 * delta_tolerance(t, torch.float32, True), "SN")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("gate", [-0.9, -1.1, -4.0, -90.0])
+def test_gates_that_close_within_a_chunk(gate, d, dtype):
+    """A chunk's first writes are closed to exp(-57), exp(-70), less than fp32 holds by its end, and are read before that."""
+    t = TYPES[dtype]
+    s = delta_inputs(42, 1, 2, 2, 150, d, d, t)
+    s["g"] = gate * (0.9 + 0.2 * torch.rand(s["g"].shape, generator=torch.Generator().manual_seed(1)))
+    want = delta(s, 0.5)
+    g = on_gpu(s)
+    o, SN = forward(g, 0.5)
+    check(dict(o=o, SN=SN, **backward(g, 0.5)), want, t, ("o", "SN", "dq", "dk", "dv", "dg", "dbeta", "dS0") if gate > -90 else ("o", "SN", "dq", "dk", "dv", "dbeta"))
