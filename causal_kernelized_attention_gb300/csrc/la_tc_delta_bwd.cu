@@ -29,6 +29,7 @@ delta_scans_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 //   DP = scale D beta_j (dO E^T),  M = -D beta_i beta_j (dX E^T) below the diagonal;
 //   dq = scale exp(G) B dO + DP K,   dk = -beta exp(G) B dX + beta exp(G_C - G) A E + DP^T Q + (M + M^T) K;
 //   dbeta_i = (dX E^T)_ii,   dv = beta dX;
+// DP and M are multiplied in two parts as well: dq's two terms nearly cancel where keys overwrite one another, and dk's.
 // and g_t stands in each decay that crosses from before t to t or later: dg_t = sum over i >= t > j of (Q K^T DP + K K^T M)_ij
 // + the reads of B at i >= t (q.dq, k.dk of the B terms) + the writes into A at j < t + exp(G_C) <B, A>.
 // Products with the states have the key features as rows, so that a thread sums its feature's gradients over the
@@ -42,9 +43,10 @@ template <int DK, int DV> struct LocalSmem {
     uint8_t b[2][DK / 64][DV * 128];
     uint8_t a[DK / 64][DV * 128];      // one part at a time
     uint8_t dp[kSq], m[kSq];           // dp: then partial sums
+    uint8_t low[DV == 128 ? 16 : 2 * kSq];  // their low parts (d_v 128: over E's low part, once that has been read)
     Scalars s;
     float row[2][32];                  // sums of the first 32 columns of rows 32-63, of both matrices
-    uint64_t keys_in, rows_in, b_in, a_in, mat_full, st_full, wk_full, dp_ready, a_free, head_free, drain;
+    uint64_t keys_in, rows_in, b_in, a_in, mat_full, st_full, wk_full, dp_ready, low_ready, a_free, head_free, drain;
     uint32_t tmem_base;
     int abort;
 };
@@ -86,7 +88,7 @@ delta_local_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     if (tid == 0) {
         uint64_t *one[] = {&sm.keys_in, &sm.rows_in, &sm.b_in, &sm.a_in, &sm.mat_full, &sm.st_full, &sm.wk_full, &sm.drain};
         for (uint64_t *b : one) mbar_init(b, 1);
-        uint64_t *all[] = {&sm.dp_ready, &sm.a_free, &sm.head_free};
+        uint64_t *all[] = {&sm.dp_ready, &sm.low_ready, &sm.a_free, &sm.head_free};
         for (uint64_t *b : all) mbar_init(b, 32 * kLocalWarps);
         sm.abort = (smem_u32(smem_raw) & 1023u) == 0 ? 0 : 1;
         if (sm.abort) atomicOr(&g_delta_status, kStatusTimeout);
@@ -104,6 +106,7 @@ delta_local_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     const uint32_t tmem = sm.tmem_base;
     int *abort_flag = &sm.abort;
     bool ok = !aborted(abort_flag);
+    uint8_t *const low = DV == 128 ? sm.e[1][0] : sm.low;  // of DP, then of M
 
     if (warp == kLocalCopy) {
         auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_bar_warp(&g_delta_status, abort_flag, bar, parity); };
@@ -155,6 +158,7 @@ delta_local_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const uint64_t dkeys = rows_k(smem_u32(sm.qk[0]), 0), dx_ = rows_k(smem_u32(sm.x[0]), 0), de = rows_k(smem_u32(sm.e[0][0]), 0);
         const uint64_t db = cols_mn(smem_u32(sm.b[0][0]), 0, kLboState), da = cols_mn(smem_u32(sm.a[0]), 0, kLboState);
         const uint64_t dq = cols_mn(smem_u32(sm.qk[0]), 0, kLboKeys), dp_k = rows_k(smem_u32(sm.dp), 0), dp_mn = cols_mn(smem_u32(sm.dp), 0);
+        const uint64_t low_k = rows_k(smem_u32(low), 0), low_mn = cols_mn(smem_u32(low), 0);
         auto wait = [&](uint64_t *bar, uint32_t parity) { wait_or_abort(&g_delta_status, abort_flag, bar, parity); };
         // 16-column steps of rows of 64-column boxes `box` apart
         auto step = [](int kk, uint32_t box) { return (uint32_t)(kk >> 2) * box + (uint32_t)(kk & 3) * 2; };
@@ -214,18 +218,23 @@ delta_local_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             __syncwarp();
             wait(&sm.dp_ready, ph);
             tc_fence_after();
-            if (elect_one()) {
-                const uint64_t k = dq + kBox, m_k = dp_k + kBox, m_mn = dp_mn + kBox;
+            auto within = [&](uint64_t p_k, uint64_t p_mn, bool add) {
+                const uint64_t k = dq + kBox, m_k = p_k + kBox, m_mn = p_mn + kBox;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) mma_ss(tmem + tDq, k + kk * (2048 >> 4), dp_k + kk * 2, id_mn, h > 0 || kk > 0);  // DP K
+                for (int kk = 0; kk < 4; ++kk) mma_ss(tmem + tDq, k + kk * (2048 >> 4), p_k + kk * 2, id_mn, add || kk > 0);  // DP K
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ss(tmem + tDk, dq + kk * (2048 >> 4), dp_mn + kk * (2048 >> 4), id_both, h > 0 || kk > 0);  // DP^T Q
+                    mma_ss(tmem + tDk, dq + kk * (2048 >> 4), p_mn + kk * (2048 >> 4), id_both, add || kk > 0);  // DP^T Q
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) mma_ss(tmem + tDk, k + kk * (2048 >> 4), m_k + kk * 2, id_mn, 1);  // M K
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) mma_ss(tmem + tDk, k + kk * (2048 >> 4), m_mn + kk * (2048 >> 4), id_both, 1);  // M^T K
-            }
+            };
+            if (elect_one()) within(dp_k, dp_mn, h > 0);
+            __syncwarp();
+            wait(&sm.low_ready, ph);
+            tc_fence_after();
+            if (elect_one()) within(low_k, low_mn, true);
             __syncwarp();
             wait(&sm.a_in, 1);
             tc_fence_after();
@@ -261,13 +270,14 @@ delta_local_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             tc_fence_after();
             // ---- the matrices of the chunk: row i of DP (lanes 0-63) or of M, columns c0 ..
             float pairs = 0.f;
+            uint32_t lows[16];
             {
                 const int i = f & 63;
                 const bool is_m = q >= 2, upper = half == 1 && (q & 1) == 0, diagonal = half == (q & 1);
                 float r[32];
                 if (upper) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = 0.f;
+                    for (int e = 0; e < 32; ++e) r[e] = 0.f, lows[e / 2] = 0u;
                     uint8_t *to = is_m ? sm.m : sm.dp;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4 *>(to + sw128_offset(i, c0 + 8 * c)) = make_uint4(0u, 0u, 0u, 0u);
@@ -305,10 +315,12 @@ delta_local_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                                 if (y + e > lane || (is_m && y + e == lane)) v[e] = 0.f;
                         }
 #pragma unroll
-                        for (int e = 0; e < 16; e += 8)
-                            *reinterpret_cast<uint4 *>(to + sw128_offset(i, c0 + y + e)) =
-                                make_uint4(pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]), pack_bf16(v[e + 4], v[e + 5]),
-                                           pack_bf16(v[e + 6], v[e + 7]));
+                        for (int e = 0; e < 16; e += 8) {
+                            uint32_t hi4[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) split2(v[e + 2 * u], v[e + 2 * u + 1], hi4[u], lows[(y + e) / 2 + u]);
+                            *reinterpret_cast<uint4 *>(to + sw128_offset(i, c0 + y + e)) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+                        }
                         tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 16; ++e) r[y + e] = (diagonal && y + e == lane) ? 0.f : v[e] * __uint_as_float(a[e]);
@@ -361,6 +373,12 @@ delta_local_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             if (!(ok = wait(&sm.st_full, ph))) break;
             tc_fence_after();
             mbar_arrive(&sm.a_free);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<uint4 *>(low + (q >= 2) * kSq + sw128_offset(f & 63, c0 + 8 * c)) =
+                    make_uint4(lows[4 * c], lows[4 * c + 1], lows[4 * c + 2], lows[4 * c + 3]);
+            fence_proxy_async_smem();
+            mbar_arrive(&sm.low_ready);
             // ---- reads of B
             float reads = 0.f, writes = 0.f;
             if (live) {

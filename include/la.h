@@ -612,9 +612,8 @@ la_status la_window_decode_step(void *kc, void *vc, const void *q, const void *k
  *
  * Arithmetic: fp32 inputs in fp32 on the CUDA cores, 8 tokens at a time.  bf16 inputs on the tensor cores, 64 tokens at a
  * time: the states and all that feeds fp32 results (SN, dS0, dg, dbeta) multiply bf16 inputs with intermediate values in two
- * bf16 parts (within 2^-17 each; sums fp32), and so do the two terms of o, the state's answer and that of the chunk's own
- * writes, which may be many times larger than o where keys overwrite one another; products that end in dq or dk alone round
- * one factor once more (2^-8 of the terms at most).  A write that later gates of its 64 tokens close to less than exp(-64)
+ * bf16 parts (within 2^-17 each; sums fp32), and so do the terms of o, dq and dk, the state's answer and that of the chunk's
+ * own writes, which may be many times larger than what is left of them where keys overwrite one another.  A write that later gates of its 64 tokens close to less than exp(-64)
  * stays in the forward's state as exp(-64) of itself (1.6e-28).  The decode step is fp32 throughout.
  * Scratch, from the stream's workspace or stream-ordered while the stream is being captured.  Forward (bf16): 34 KB and
  * 256 dk bytes a head and 64 tokens.  Backward: bf16 34 KB and 512 dk, 8 dk dv and 512 dv bytes a head and 64 tokens; fp32 the state before

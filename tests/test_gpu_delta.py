@@ -396,3 +396,18 @@ def test_gates_that_close_within_a_chunk(gate, d, dtype):
     g = on_gpu(s)
     o, SN = forward(g, 0.5)
     check(dict(o=o, SN=SN, **backward(g, 0.5)), want, t, ("o", "SN", "dq", "dk", "dv", "dg", "dbeta", "dS0") if gate > -90 else ("o", "SN", "dq", "dk", "dv", "dbeta"))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kind", KINDS)
+def test_gradients_of_keys_that_overwrite_one_another(kind, d, dtype):
+    """dq is read from the same two terms as o, and dk from those of the gradients; what ends in fp32 as the states above."""
+    t = TYPES[dtype]
+    s = correlated(44, kind, 2, 1, 2, 190, d, t)
+    want = delta(s, d ** -0.5)
+    got = backward(on_gpu(s), d ** -0.5)
+    for i in ("dq", "dk", "dv"):
+        assert_near(got[i], want[i], delta_tolerance(t, t, True), i)
+    for i in ("dg", "dbeta", "dS0"):
+        assert_near(got[i], want[i], 4 * delta_tolerance(t, torch.float32, True), i, floor=0.02 if i == "dS0" else 1.0)
