@@ -169,6 +169,13 @@ bool delta_supported(int B, int H, int N, int dk, int dv)
     return supported_dim(dk) && supported_dim(dv) && N <= kMaxTokens && (long long)B * H <= 0x7fffffff / 4 &&
            (long long)B * H * ((N + 31LL) / 32) <= 0x7fffffff;
 }
+// A result that sums over nothing (where it is wanted).
+la_status zeros(void *p, size_t bytes, la_stream_t s)
+{
+    if (!p || bytes == 0) return LA_OK;
+    count_launches();
+    return cuda_status(cudaMemsetAsync(p, 0, bytes, (cudaStream_t)s));
+}
 struct DeltaSizes {
     size_t keys, values, gates, states;
     DeltaSizes(int B, int Hk, int H, int N, int dk, int dv, la_dtype t)
@@ -404,7 +411,8 @@ la_status la_delta_forward(const void *q, const void *k, const void *v, const fl
 {
     la_status st = check_delta(B, Hk, H, N, dk, dv, scale, dtype);
     if (st != LA_OK) return st;
-    if (B == 0 || H == 0 || dk == 0 || dv == 0 || (N == 0 && !SN)) return LA_OK;
+    if (B == 0 || H == 0 || dv == 0 || (N == 0 && !SN)) return LA_OK;
+    if (dk == 0) return zeros(o, DeltaSizes(B, Hk, H, N, dk, dv, dtype).values, stream);
     if (N > 0 && (!q || !k || !v || !g || !beta || !o)) return LA_ERR_INVALID_ARG;
     if (!aligned(S0, 16) || !aligned(SN, 16) ||
         (N > 0 && (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(g, 4) || !aligned(beta, 4) || !aligned(o, 16))))
@@ -436,7 +444,14 @@ la_status la_delta_backward(const void *q, const void *k, const void *v, const f
 {
     la_status st = check_delta(B, Hk, H, N, d_k, d_v, scale, dtype);
     if (st != LA_OK) return st;
-    if (B == 0 || H == 0 || d_k == 0 || d_v == 0 || (N == 0 && !dS0)) return LA_OK;
+    if (B == 0 || (N == 0 && !dS0)) return LA_OK;
+    if (H == 0 || d_k == 0 || d_v == 0) {  // what is not empty of the gradients is zero
+        const DeltaSizes z(B, Hk, H, N, d_k, d_v, dtype);
+        void *out[] = {dq, dk, dv, dg, dbeta};
+        const size_t bytes[] = {z.keys, z.keys, z.values, z.gates, z.gates};
+        for (int i = 0; i < 5 && st == LA_OK; ++i) st = zeros(out[i], bytes[i], stream);
+        return st;
+    }
     if (N > 0 && (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta)) return LA_ERR_INVALID_ARG;
     if (!aligned(S0, 16) || !aligned(dSN, 16) || !aligned(dS0, 16) ||
         (N > 0 && (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(g, 4) || !aligned(beta, 4) ||
@@ -471,7 +486,8 @@ la_status la_delta_step(float *S, const void *q, const void *k, const void *v, c
 {
     const la_status st = check_delta(B, Hk, H, 1, dk, dv, scale, dtype);
     if (st != LA_OK) return st;
-    if (B == 0 || H == 0 || dk == 0 || dv == 0) return LA_OK;
+    if (B == 0 || H == 0 || dv == 0) return LA_OK;
+    if (dk == 0) return zeros(o, DeltaSizes(B, Hk, H, 1, dk, dv, dtype).values, stream);
     if (!S || !q || !k || !v || !g || !beta || !o) return LA_ERR_INVALID_ARG;
     if (!aligned(S, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(g, 4) || !aligned(beta, 4) ||
         !aligned(o, 16))

@@ -620,7 +620,8 @@ la_status la_window_decode_step(void *kc, void *vc, const void *q, const void *k
  * and its gradient behind every 32 tokens, and two rows of dv floats a token and head.
  *
  * Supported: dk, dv in {32, 64, 128}, H a multiple of Hk, finite scale; g, beta, dg and dbeta need only their own
- * 4-byte alignment.  Outputs overlap no input and no other output.  B = 0, H = 0, dk = 0 or dv = 0 is an empty problem; N = 0 still writes SN (dS0 = dSN).
+ * 4-byte alignment.  Outputs overlap no input and no other output.  B = 0, H = 0, dk = 0 or dv = 0 is an empty problem (outputs
+ * that are not empty by themselves are zeros); N = 0 still writes SN (dS0 = dSN).
  */
 la_status la_delta_forward(const void *q, const void *k, const void *v, const float *g, const float *beta,
                            const float *S0, void *o, float *SN, int B, int Hk, int H, int N, int dk, int dv, float scale,

@@ -411,3 +411,21 @@ def test_gradients_of_keys_that_overwrite_one_another(kind, d, dtype):
         assert_near(got[i], want[i], delta_tolerance(t, t, True), i)
     for i in ("dg", "dbeta", "dS0"):
         assert_near(got[i], want[i], 4 * delta_tolerance(t, torch.float32, True), i, floor=0.02 if i == "dS0" else 1.0)
+
+
+@pytest.mark.parametrize("H,dk,dv", [(0, 64, 64), (2, 0, 64), (2, 64, 0)])
+def test_sizes_of_nothing_give_zeros(H, dk, dv):
+    """No heads that read the keys, no key features, no value features: what is left of the outputs sums over nothing."""
+    def full(*shape, dtype=torch.bfloat16):
+        return torch.full(shape, 3.0, dtype=dtype, device="cuda")
+
+    q, v, g = full(2, 2, 5, dk), full(2, H, 5, dv), full(2, H, 5, dtype=torch.float32)
+    out = dict(dq=full(2, 2, 5, dk), dk=full(2, 2, 5, dk), dv=full(2, H, 5, dv), dg=full(2, H, 5, dtype=torch.float32),
+               dbeta=full(2, H, 5, dtype=torch.float32))
+    o, SN = la.la_delta_forward(q, q, v, g, g, scale=1.0, o=full(2, H, 5, dv))
+    assert not o.any() and SN.numel() == 0
+    la.la_delta_backward(q, q, v, g, g, v, scale=1.0, **out)
+    assert not any(x.any() for x in out.values())
+    o = la.la_delta_step(SN, q[:, :, 0].contiguous(), q[:, :, 0].contiguous(), v[:, :, 0].contiguous(), g[:, :, 0].contiguous(),
+                         g[:, :, 0].contiguous(), scale=1.0, o=full(2, H, dv))
+    assert not o.any()
