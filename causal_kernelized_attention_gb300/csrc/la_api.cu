@@ -129,14 +129,26 @@ la_status data_workspace(cudaStream_t s, size_t bytes, void **out, int which)
     cudaError_t e = cudaStreamIsCapturing(s, &cs);
     if (e != cudaSuccess) return cuda_status(e);
     if (cs != cudaStreamCaptureStatusNone) return LA_ERR_UNSUPPORTED;
-    size_t size = it != spaces.end() ? std::max(bytes, 2 * it->second.second) : bytes;
+    size_t size = bytes;
+    if (it != spaces.end() && which == 0) {
+        size = std::max(bytes, 2 * it->second.second);
+    } else if (it != spaces.end()) {
+        // No graph holds these buffers, which reach gigabytes: the outgrown one is freed once the stream has done with it (the
+        // caller's lock keeps new work off it), and its successor leaves a quarter for calls that grow a little each time.
+        if (cudaStreamSynchronize(s) != cudaSuccess || cudaFree(it->second.first) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return LA_ERR_UNSUPPORTED;
+        }
+        size = std::max(bytes, it->second.second / 4 * 5);
+        spaces.erase(it);
+    }
     size = (size + (2u << 20) - 1) / (2u << 20) * (2u << 20);
     void *p = nullptr;
     if (cudaMalloc(&p, size) != cudaSuccess) {
         (void)cudaGetLastError();  // not sticky: the caller's per-call scratch may still fit
         return LA_ERR_UNSUPPORTED;
     }
-    spaces[slot] = std::make_pair(p, size);  // an outgrown buffer stays allocated (see above)
+    spaces[slot] = std::make_pair(p, size);  // (which 0: an outgrown buffer stays allocated, see above)
     *out = p;
     return LA_OK;
 }

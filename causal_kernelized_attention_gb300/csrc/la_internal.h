@@ -281,7 +281,8 @@ la_status flag_workspace(cudaStream_t s, size_t bytes, void **out);
 // serve the call (a stream under capture whose buffer is too small, or the
 // allocation failed); the caller then uses per-call scratch.  `which` tells a stream's
 // buffers apart: the window backward has one of its own (1), and so have the recurrence (2), the delta
-// rule (3) and group norm (4), which a lock protects from another host thread's launches on the same stream.
+// rule (3) and group norm (4), which a lock protects from another host thread's launches on the same stream.  Captured
+// calls take none of these (1 to 4), so that an outgrown one of them is freed.
 la_status data_workspace(cudaStream_t s, size_t bytes, void **out, int which = 0);
 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel and device,

@@ -615,7 +615,8 @@ la_status la_window_decode_step(void *kc, void *vc, const void *q, const void *k
  * bf16 parts (within 2^-17 each; sums fp32), and so do the terms of o, dq and dk, the state's answer and that of the chunk's
  * own writes, which may be many times larger than what is left of them where keys overwrite one another.  A write that later gates of its 64 tokens close to less than exp(-64)
  * stays in the forward's state as exp(-64) of itself (1.6e-28).  The decode step is fp32 throughout.
- * Scratch, from the stream's workspace or stream-ordered while the stream is being captured.  Forward (bf16): 34 KB and
+ * Scratch, from the stream's workspace (kept for the stream's next calls: one buffer, at most a quarter larger than the largest
+ * call's so far; growing it waits for the stream) or stream-ordered while the stream is being captured.  Forward (bf16): 34 KB and
  * 256 dk bytes a head and 64 tokens.  Backward: bf16 34 KB and 512 dk, 8 dk dv and 512 dv bytes a head and 64 tokens; fp32 the state before
  * and its gradient behind every 32 tokens, and two rows of dv floats a token and head.
  *

@@ -429,3 +429,26 @@ def test_sizes_of_nothing_give_zeros(H, dk, dv):
     o = la.la_delta_step(SN, q[:, :, 0].contiguous(), q[:, :, 0].contiguous(), v[:, :, 0].contiguous(), g[:, :, 0].contiguous(),
                          g[:, :, 0].contiguous(), scale=1.0, o=full(2, H, dv))
     assert not o.any()
+
+
+def test_workspaces_of_growing_calls():
+    """A stream keeps one buffer for its calls, at most a quarter larger than the largest of them needs (0.297 MB a head and
+    chunk in the backward at d 128), and the buffers that it has outgrown are freed."""
+    import gc
+    def calls(chunks, stream):
+        s = on_gpu(delta_inputs(50, 1, 4, 8, 2, 128, 128, torch.bfloat16, False))
+        g = {n: None if x is None else x[:, :, :1].repeat(*((1, 1, 64 * chunks) + (1,) * (x.dim() - 3))).contiguous() for n, x in s.items()}
+        torch.cuda.synchronize()
+        first, again = backward(g, stream=stream), backward(g, stream=stream)
+        torch.cuda.synchronize()
+        assert all(x is None or torch.equal(x, again[n]) for n, x in first.items())
+
+    stream = torch.cuda.Stream()
+    calls(4, torch.cuda.default_stream())  # code that the steps below load, 100 MB of it PyTorch's, is not counted
+    gc.collect(), torch.cuda.synchronize(), torch.cuda.empty_cache()
+    before = torch.cuda.mem_get_info()[0]
+    for chunks in (40, 85, 175, 360, 365, 370):
+        calls(chunks, stream)
+    gc.collect(), torch.cuda.synchronize(), torch.cuda.empty_cache()
+    held = before - torch.cuda.mem_get_info()[0]
+    assert held <= 1.25 * 8 * 370 * 0.297e6 + 64e6, held
