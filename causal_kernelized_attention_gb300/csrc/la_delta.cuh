@@ -17,12 +17,14 @@ struct Params {
     float *SN, *dg, *dbeta, *dS0;
     int B, Hk, H, N, dk, dv;
     float scale;
+    unsigned long long wait_ns;  // limit of a wait for a published chunk; the work item that is not published (a test's), or -1
+    long long drop;
 };
 
 inline Params params_of(const DeltaProblem &p)
 {
     return {p.q,  p.k,  p.v,     p.dout, p.g, p.beta, p.S0, p.dSN, p.o,  p.dq, p.dk_out,
-            p.dv_out, p.SN, p.dg, p.dbeta, p.dS0, p.B, p.Hk, p.H, p.N, p.dk, p.dv, p.scale};
+            p.dv_out, p.SN, p.dg, p.dbeta, p.dS0, p.B, p.Hk, p.H, p.N, p.dk, p.dv, p.scale, test_wait_limit_ns(), test_drop_ticket()};
 }
 
 // Two fp32 operations in one instruction.

@@ -77,7 +77,8 @@ delta_both_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             named_bar_sync(1 + set, 128);  // the last chunk's operands are read
             prepare_chunk<DK, false>(mine, map_q, map_k, p, images + at * Layout<DK>::forward_bytes, now, bh, chunk, tid, warp & 3, tmem, turn,
                                      true, 1 + set, true, [&] { named_bar_sync(1 + set, 128); });
-            last = at;
+            // (a chunk whose own wait has run out is not published: its scan's wait runs out, too)
+            last = __any_sync(0xffffffffu, aborted(&mine.abort)) || i == p.drop ? -1 : at;
             publish();
         }
         tc_fence_before();

@@ -501,13 +501,13 @@ delta_prepare(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 }
 
 // Waits (with the limit of every wait) until another CTA of the launch has published a chunk's image.
-__device__ __forceinline__ bool wait_flag(const unsigned *flag, int *abort_flag)
+__device__ __forceinline__ bool wait_flag(const unsigned *flag, int *abort_flag, uint64_t limit_ns)
 {
     const uint64_t t0 = globaltimer_ns();
     bool there;
     while (!(there = __all_sync(0xffffffffu, ld_acquire_gpu(flag) != 0))) {
         if (__any_sync(0xffffffffu, aborted(abort_flag))) return false;
-        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) {
+        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) {
             *(volatile int *)abort_flag = 1;
             atomicOr(&g_delta_status, kStatusTimeout);
             return false;
@@ -619,7 +619,7 @@ __device__ __forceinline__ void scan_body(const CUtensorMap &map_q, const CUtens
             // V and the matrices of chunk c - 2 end with its E; where states are kept, the warps of E's rows tell when they have
             // read them, too, and (rows staged over W) when the rows' store has
             if (c >= 2 && !(ok = wait(kKeep ? &sm.rows_read[st] : &sm.e_full[st], (uint32_t)((c >> 1) - 1) & 1u))) break;
-            if (ready && !(ok = wait_flag(ready + (size_t)bh * chunks + x, abort_flag))) break;
+            if (ready && !(ok = wait_flag(ready + (size_t)bh * chunks + x, abort_flag, p.wait_ns))) break;
             if (__any_sync(0xffffffffu, aborted(abort_flag))) break;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&sm.full[st], DV / 64 * kSq + Sm::kMats + (kKeep ? kScanScalars : 0));

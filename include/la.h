@@ -695,7 +695,8 @@ la_status la_get_device_status(la_stream_t stream);
  * They act on the causal forward for bf16 with dk = dv = 64 (elu + 1 with the
  * normaliser, no decay): its chunk-parallel kernel (N > 2048 and 16 or more heads
  * in total), whose work items publish per-chunk states that later items wait
- * for, and -- the wait limit only -- its cluster kernel (N <= 2048).  Both
+ * for, and -- the wait limit only -- its cluster kernel (N <= 2048); and on the bf16 forward of the delta rule where one launch
+ * prepares chunks and scans them (its waits for a prepared chunk, and tickets in the same order).  Both
  * settings are process-wide and apply to launches made after the call.
  *
  * la_test_set_wait_limit_ns(ns): every bounded wait of those kernels gives up after

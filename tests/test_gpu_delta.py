@@ -452,3 +452,30 @@ def test_workspaces_of_growing_calls():
     gc.collect(), torch.cuda.synchronize(), torch.cuda.empty_cache()
     held = before - torch.cuda.mem_get_info()[0]
     assert held <= 1.25 * 8 * 370 * 0.297e6 + 64e6, held
+
+
+@pytest.mark.parametrize("ticket", [0, 100, 767])
+def test_a_lost_chunk_times_out_and_the_next_call_is_clean(ticket):
+    """48 heads of 16 chunks, prepared and scanned in one launch: a chunk (ticket / 48 of head ticket % 48) that is prepared but
+    never published makes its scan's wait run out, which the status word tells."""
+    lib = la.load_library()
+    s = on_gpu(delta_inputs(60, 1, 24, 48, 1009, 64, 64, torch.bfloat16))
+    want = forward(s)
+    torch.cuda.synchronize()
+    assert la.la_get_device_status() == 0
+    try:
+        lib.la_test_set_wait_limit_ns(50_000_000)
+        got = forward(s)  # a short limit alone does not fire
+        torch.cuda.synchronize()
+        assert la.la_get_device_status() == 0 and all(torch.equal(x, y) for x, y in zip(got, want))
+        lib.la_test_set_wait_limit_ns(2_000_000)
+        lib.la_test_drop_publication(ticket)
+        forward(s)
+        torch.cuda.synchronize()
+        assert la.la_get_device_status() == 5 and la.la_get_device_status() == 0
+    finally:
+        lib.la_test_drop_publication(-1)
+        lib.la_test_set_wait_limit_ns(0)
+    got = forward(s)
+    torch.cuda.synchronize()
+    assert la.la_get_device_status() == 0 and all(torch.equal(x, y) for x, y in zip(got, want))
