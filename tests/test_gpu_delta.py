@@ -479,3 +479,22 @@ def test_a_lost_chunk_times_out_and_the_next_call_is_clean(ticket):
     got = forward(s)
     torch.cuda.synchronize()
     assert la.la_get_device_status() == 0 and all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_steps_that_overwrite_one_key(dtype):
+    """beta = 1 and one unit key, again and again: what was stored is replaced, and read back with the key itself."""
+    t = TYPES[dtype]
+    s = delta_inputs(61, 2, 1, 2, 6, 64, 64, t)
+    s["k"] = s["k"][:, :, :1].expand(-1, -1, 6, -1).contiguous()
+    s["q"], s["beta"], s["g"] = s["k"].clone(), torch.ones_like(s["beta"]), torch.zeros_like(s["g"])
+    want = delta(s, 1.0, backward=False)
+    g = on_gpu(s)
+    S = g["S0"].clone()
+    for i in range(6):
+        o = la.la_delta_step(S, *[g[n][:, :, i].contiguous() for n in ("q", "k", "v", "g", "beta")], scale=1.0)
+        assert_near(o[:, :, None], want["o"][:, :, i:i + 1], delta_tolerance(t, t, False), "o")
+    assert_near(S, want["SN"], delta_tolerance(t, torch.float32, False), "S")
+    o, SN = forward(g, 1.0)
+    assert_near(o, want["o"], delta_tolerance(t, t, True), "o")
+    assert_near(SN, want["SN"], 4 * delta_tolerance(t, torch.float32, True), "SN")

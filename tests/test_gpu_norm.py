@@ -215,3 +215,21 @@ def test_an_outlier_over_positions(place, value, mean, spread, B, L, G, D, dtype
     eh = em * rstd + h.abs() * (er / rstd + 4 * U) + 2 * U * want.abs() * rstd
     ez = (eh * s["w"].double().abs().reshape(G, D)).reshape(B, L, G * D) + 4 * U * (z.abs() + s["b"].double().abs())
     assert_within(y, z, ez + half(TYPES[dtype]) * z.abs() + 1e-30, "y")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads_first", [False, True])
+@pytest.mark.parametrize("B,L,G,D", [(5, 1501, 16, 64), (3, 2003, 16, 40), (3, 2003, 16, 30), (5, 3001, 3, 509), (7, 2999, 5, 8)])
+def test_walks_over_many_tokens(B, L, G, D, heads_first, dtype):
+    """Six and more tokens to a slot, whose lengths divide neither the step nor one another, with entries to cross."""
+    s, dy = inputs(15, B, L, G, D, TYPES[dtype], heads_first, True, True)
+    check(s, dy, G, "silu", True, heads_first, not heads_first)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,L,G,D,gate", [(1, 4096, 1, 4096, True), (2, 1300, 2, 2049, False), (3, 2500, 1, 1030, True)])
+def test_wide_groups_of_many_tokens(B, L, G, D, gate, dtype):
+    """Tokens wider than the lanes' registers, more of them than one launch holds on chip."""
+    s, dy = inputs(16, B, L, G, D, TYPES[dtype], False, gate, True)
+    check(s, dy, G, "silu", True, False, True)
+    check(s, dy, G, "none", True, False, False)
