@@ -116,6 +116,14 @@ __device__ __forceinline__ float back(float h, float w, float b, float dy, float
     return dy * value;
 }
 
+// 1 / n of a count, within 2^-23 (it weighs corrections that are themselves of that accuracy).
+__device__ __forceinline__ float inverse(float n)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(n));
+    return r;
+}
+
 __device__ __forceinline__ float lanes_sum(float v, int lanes)
 {
 #pragma unroll
@@ -130,7 +138,7 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes)
 // registers, and walks over the tokens; the launch has a whole number of slots for each group.  The loads of the
 // next tokens are under way meanwhile: each thread copies its vectors asynchronously into a ring of its own in
 // shared memory, kRing tokens deep (held in registers, one token ahead, they were too few to keep HBM busy: 47 us
-// against 41 for 16384 tokens of 16 x 128 gated channels in bf16, 37 with today's grid: 5.4 TB/s; backward 70 us, 4.8
+// against 41 for 16384 tokens of 16 x 128 gated channels in bf16, 37 with today's grid: 5.4 TB/s; backward 64 us, 5.2
 // TB/s); channels by ones are loaded one token ahead.  What bounds them then is instructions: an issue slot is used in 3 of 4
 // cycles, by the exponentials, conversions and the sums over lanes.
 constexpr int kRing = 4;
@@ -371,7 +379,7 @@ template <typename T, int VEC> struct Moments {
     {
         if (center && n == 0) Pk::open(r[0], m);
         n += K;
-        const float part = __frcp_rn((float)n);
+        const float part = inverse((float)n);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             float s = 0.f;
@@ -396,8 +404,10 @@ __device__ __forceinline__ void join_moments(const float *m, const float *q, int
     const int base = n / ny, more = n % ny;
     const float ref = m[0];
     float s = 0.f, v = 0.f;
+#pragma unroll 4
     for (int k = 0; k < ny; ++k) s = fmaf((float)(base + (k < more)), m[k * step] - ref, s);
-    mean = n > 0 ? ref + s / n : 0.f;
+    mean = n > 0 ? fmaf(s, inverse((float)n), ref) : 0.f;
+#pragma unroll 4
     for (int k = 0; k < ny; ++k) {
         const float d = m[k * step] - mean;
         v += fmaf((float)(base + (k < more)) * d, d, q[k * step]);
@@ -550,19 +560,35 @@ __global__ void __launch_bounds__(kFinish) norm_statistics(Params p)
     sm100::griddep_wait();
     sm100::griddep_launch_dependents();
     const int bi = blockIdx.x / p.G, g = blockIdx.x % p.G, n = p.D * p.splits;
-    const float *part = p.part + (size_t)bi * p.splits * 2 * p.C + g * p.D, ref = part[0], inv = 1.f / p.D / p.L;
-    auto sum = [&](auto f) {
-        float s = 0.f;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < n; i += kFinish) {
-            const int split = i / p.D, c = i - split * p.D;
+    const float *part = p.part + (size_t)bi * p.splits * 2 * p.C + g * p.D, inv = 1.f / p.D / p.L;
+    float rows = 0.f, m = 0.f, q = 0.f;  // of the thread's share: channels' splits, four at a time
+    for (int i0 = threadIdx.x; i0 < n; i0 += 4 * kFinish) {
+        float r[4], mean[4], sq[4], s = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kFinish, split = i / p.D, c = i - split * p.D;
             const float *at = part + (size_t)split * 2 * p.C + c;
-            s += f((float)(min(p.L, (split + 1) * p.rows) - split * p.rows), at[0], at[p.C]);
+            r[u] = i < n ? (float)(min(p.L, (split + 1) * p.rows) - split * p.rows) : 0.f;
+            mean[u] = i < n ? at[0] : 0.f;
+            sq[u] = i < n ? at[p.C] : 0.f;
         }
-        return block_sum(s, tmp);
-    };
-    const float mean = ref + sum([&](float rows, float m, float) { return rows * (m - ref); }) * inv;
-    const float v = sum([&](float rows, float m, float q) { return fmaf(rows * (m - mean), m - mean, q); }) * inv;
+        if (i0 == (int)threadIdx.x) m = mean[0];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float d = i0 + u * kFinish < n ? mean[u] - m : 0.f;
+            s = fmaf(r[u], d, s);
+            rows += r[u];
+            q += fmaf(r[u] * d, d, sq[u]);
+        }
+        const float t = s * inverse(rows);
+        q = fmaf(-s, t, q);
+        m += t;
+    }
+    __shared__ float first;
+    if (threadIdx.x == 0) first = m;
+    __syncthreads();
+    const float mean = fmaf(block_sum(rows * (m - first), tmp), inv, first);
+    const float v = block_sum(fmaf(rows * (m - mean), m - mean, q), tmp) * inv;
     if (threadIdx.x == 0) {
         if (p.center) p.mean_out[blockIdx.x] = mean;
         p.rstd_out[blockIdx.x] = rsqrtf(v + p.eps);
@@ -696,13 +722,13 @@ __global__ void __launch_bounds__(256, apply_per_sm(kGate, kBack)) norm_apply(Pa
 // to a column of VEC channels, so that what it copies in (asynchronously) only it reads; the sums of a group go over threads,
 // then over the CTAs of the cluster, in a fixed order.
 constexpr int kFusedThreads = 256, kFusedMost = 8 /* CTAs of a cluster */, kFusedGroups = 64 /* of a slab */;
-constexpr int kFusedSmem = 200 << 10, kFusedShare = 72 << 10;  // of a CTA: at most, and if the cluster can be that large (three share an SM)
+constexpr int kFusedSmem = 200 << 10, kFusedShare = 72 << 10;  // of a CTA: at most, and if the cluster can be that large (two share an SM, three up to 70 KB)
 struct Slab {
     int groups, slabs, rows, cols;  // groups of a slab, slabs of an entry, positions a CTA, columns
 };
 
 template <typename T, int VEC, bool kGate, bool kBack, bool kAct>
-__global__ void __launch_bounds__(kFusedThreads) norm_fused(Params p, Slab q)
+__global__ void __launch_bounds__(kFusedThreads, kBack ? 1 : 4 /* 80 registers would leave room for three */) norm_fused(Params p, Slab q)
 {
     typedef Pack<T, VEC> Pk;
     typedef typename Pk::Raw Raw;
@@ -766,7 +792,12 @@ __global__ void __launch_bounds__(kFusedThreads) norm_fused(Params p, Slab q)
                 for (int u = 0; u < kRows; ++u) v[u] = sx[at0 + (i + u) * step];
                 so_far.template add<kRows>(v, p.center);
             }
-            for (; i < end; ++i) so_far.template add<1>(sx + at0 + i * step, p.center);
+            if (i + 2 <= end) {
+                const Raw v[2] = {sx[at0 + i * step], sx[at0 + (i + 1) * step]};
+                so_far.template add<2>(v, p.center);
+                i += 2;
+            }
+            if (i < end) so_far.template add<1>(sx + at0 + i * step, p.center);
         } else {
             for (; i < end; ++i) {
                 const int at = at0 + i * step;
@@ -813,7 +844,7 @@ __global__ void __launch_bounds__(kFusedThreads) norm_fused(Params p, Slab q)
             const float *m = sums + g * p.D, *sq = m + ny * wide;
             float s = 0.f, v = 0.f;
             for (int k = threadIdx.x & 31; k < p.D; k += 32) s += m[k] - m[0];
-            const float mean = m[0] + lanes_sum(s, 32) / p.D;
+            const float mean = fmaf(lanes_sum(s, 32), 1.f / p.D, m[0]);
             for (int k = threadIdx.x & 31; k < p.D; k += 32) v += fmaf((float)rows * (m[k] - mean), m[k] - mean, sq[k]);
             v = lanes_sum(v, 32);
             if ((threadIdx.x & 31) == 0) mine[0][g] = mean, mine[1][g] = v;
@@ -857,11 +888,18 @@ __global__ void __launch_bounds__(kFusedThreads) norm_fused(Params p, Slab q)
             done[0][i] = a0 * inv;
             done[1][i] = p.center ? a1 * inv : 0.f;
         } else {
-            auto share = [&](int k) { return (float)max(0, min(q.rows, p.L - k * q.rows)) / p.L; };  // of the positions
-            float d = 0.f, v = 0.f;
-            for (int k = 1; k < size; ++k) d = fmaf(share(k), one(k, 0) - one(0, 0), d);
-            const float m = one(0, 0) + d;
-            for (int k = 0; k < size; ++k) v += fmaf(share(k) * (one(k, 0) - m), one(k, 0) - m, one(k, 1) * inv);
+            const float inv_l = 1.f / p.L;
+            auto share = [&](int k) { return (float)max(0, min(q.rows, p.L - k * q.rows)) * inv_l; };  // of the positions
+            float mk[kFusedMost], d = 0.f, v = 0.f;
+#pragma unroll
+            for (int k = 0; k < kFusedMost; ++k) {
+                mk[k] = k < size ? one(k, 0) : 0.f;
+                v += k < size ? one(k, 1) * inv : 0.f;
+                d = k < size ? fmaf(share(k), mk[k] - mk[0], d) : d;
+            }
+            const float m = mk[0] + d;
+#pragma unroll
+            for (int k = 0; k < kFusedMost; ++k) v = k < size ? fmaf(share(k) * (mk[k] - m), mk[k] - m, v) : v;
             const float rs = rsqrtf(v + p.eps);
             done[0][i] = m, done[1][i] = rs;
             if (rank == 0) {
