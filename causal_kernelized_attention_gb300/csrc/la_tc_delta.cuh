@@ -25,9 +25,10 @@ using namespace tc;
 
 constexpr int kChunk = 64;
 constexpr uint32_t kSq = kChunk * 128;  // a [64 x 64] bf16 image, 128-byte swizzled: 8 KB
-// Gates that close what a token writes to exp(-64) by its chunk's end close it no further in S' (1.6e-28 of it is left): its
-// inverse, 6e27, leaves room for q.k up to 5e10.
-constexpr float kClosed = 64.f;
+// Gates that close what a token writes to exp(-48) by its chunk's end close it no further in S' (1.4e-21 of it is left, 1e-14
+// of what fp32 tells apart), so that its inverse, 7e20, leaves room for q.k up to 4e17, and a low part is a normal number for
+// errors down to 1e-14.
+constexpr float kClosed = 48.f;
 constexpr uint64_t kDrainNs = 100000000ull;
 
 // The scalars of a chunk, by token; a scan loads three of the first four.
@@ -93,7 +94,6 @@ __device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t 
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ uint32_t ld_shared32(const void *p) { return *reinterpret_cast<const uint32_t *>(p); }
 
 __device__ __forceinline__ float ex2(float x)
 {

@@ -613,8 +613,8 @@ la_status la_window_decode_step(void *kc, void *vc, const void *q, const void *k
  * Arithmetic: fp32 inputs in fp32 on the CUDA cores, 8 tokens at a time.  bf16 inputs on the tensor cores, 64 tokens at a
  * time: the states and all that feeds fp32 results (SN, dS0, dg, dbeta) multiply bf16 inputs with intermediate values in two
  * bf16 parts (within 2^-17 each; sums fp32), and so do the terms of o, dq and dk, the state's answer and that of the chunk's
- * own writes, which may be many times larger than what is left of them where keys overwrite one another.  A write that later gates of its 64 tokens close to less than exp(-64)
- * stays in the forward's state as exp(-64) of itself (1.6e-28).  The decode step is fp32 throughout.
+ * own writes, which may be many times larger than what is left of them where keys overwrite one another.  A write that later gates of its 64 tokens close to less than exp(-48)
+ * stays in the forward's state as exp(-48) of itself (1.4e-21).  The decode step is fp32 throughout.
  * Scratch, from the stream's workspace (kept for the stream's next calls: one buffer, at most a quarter larger than the largest
  * call's so far; growing it waits for the stream) or stream-ordered while the stream is being captured.  Forward (bf16): 34 KB and
  * 256 dk bytes a head and 64 tokens.  Backward: bf16 34 KB and 512 dk, 8 dk dv and 512 dv bytes a head and 64 tokens; fp32 the state before
@@ -656,7 +656,8 @@ la_status la_delta_step(float *S, const void *q, const void *k, const void *v, c
  * db need only their own 4-byte alignment.  Statistics and sums are fp32: an infinity or a NaN makes its group's rstd
  * NaN (an infinity without centring: 0), and values whose squares overflow make it 0.  Outputs overlap no input and no other output.
  * B, L or C = 0 is an empty problem (dw, db = 0).  Scratch (partial sums) from the stream's workspace, or
- * stream-ordered while the stream is being captured.
+ * stream-ordered while the stream is being captured: a few MB, but 8 bytes a value of x for per_token groups of more than 512
+ * channels, where the tensors exceed 16 MB together or a group 256 vectors of 16 bytes.
  */
 typedef enum { LA_ACT_NONE = 0, LA_ACT_SILU = 1 } la_act;
 
