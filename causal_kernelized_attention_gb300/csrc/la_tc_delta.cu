@@ -113,10 +113,10 @@ template <int DK, int DV> la_status forward_both(const DeltaProblem &p)
 
 // One launch clears its flags and fills its pipeline first (7 us), and hides the preparing kernel behind the scan: it pays from 5
 // chunks an SM, at 16 chunks a head and more (with fewer the scan is over before the rest is hidden), while half of the
-// SMs are left to prepare.  One launch against two, us, d 64 / d 128: 32 heads of 8 chunks 32 / 39 against 26 / 32, of 16
-// 42 / 53 against 40 / 50, of 24 52 / 69 against 56 / 72, of 64 108 / 133 against 129 / 165; 64 of 12 46 / 54 against
-// 40 / 52, of 16 52 / 62 against 51 / 63, of 64 142 / 168 against 163 / 206; 8 of 32 63 / 79 against 56 / 73, of
-// 64 102 / 133 against 101 / 133; 90 of 64 258 / 289 against 192 / 240.
+// SMs are left to prepare.  One launch against two, us, d 64 / d 128: 32 heads of 8 chunks 34 / 40 against 28 / 34, of 16
+// 45 / 55 against 46 / 54, of 24 57 / 73 against 60 / 77, of 64 114 / 150 against 152 / 177; 64 of 12 46 / 55 against
+// 44 / 55, of 16 53 / 64 against 55 / 67, of 64 146 / 170 against 184 / 218; 8 of 32 66 / 83 against 60 / 79, of
+// 64 110 / 144 against 125 / 144; 90 of 64 261 / 293 against 208 / 250.
 bool one_launch(const DeltaProblem &p)
 {
     const long long heads = (long long)p.B * p.H, chunks = ceil_div(p.N, kChunk);
