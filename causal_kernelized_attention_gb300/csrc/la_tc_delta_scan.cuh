@@ -536,8 +536,10 @@ template <int DK, int DV, int kMode> struct ScanSmem {
     // K (and in reverse Q) are needed late in a chunk: one stage where shared memory is short
     static constexpr int kKeyStages = kMode == kForward ? 2 : 1;
     static constexpr bool kOutOverW = kMode != kForward && DK >= DV;  // E's rows are staged where W was
-    // forward, d_k and d_v 128: no room to stage o (d 64 without a stage: 67.8 us of a call against 64)
-    static constexpr bool kStageO = kMode == kForward && DK + DV < 256;
+    // o is staged where its products have room for two chunks (d 64 without a stage: 67.8 us of a call against 64); with room for
+    // one, the next chunk's wait for its reading, which stores without a stage end sooner (d 128 x 64, 16381 tokens of one head:
+    // 556 us with a stage, 504 without), and at d_v 128 there is none
+    static constexpr bool kStageO = kMode == kForward && DK == 64;
     static constexpr uint32_t kMats = 2 * kSq + Layout<DK>::w_bytes;
     // forward, d_k 64: the products of o have room for two chunks, so that the chain does not wait for the warps of o
     static constexpr int kOuts = kMode == kForward && DK == 64 ? 2 : 1, kScalarRing = kOuts + 2;
