@@ -1015,8 +1015,8 @@ MapShape map_shape(const NormProblem &p, int per_sm)
 }
 
 // The slab and cluster of norm_fused; size 0 where the groups do not fit, or what would be held is so large that three
-// launches of many small blocks do better (device times in bf16, one launch against three: forward 2.1 M elements 7.8 / 12.0 us,
-// 8.4 M 14.9 / 18.7, 10.5 M 19.9 / 20.7 and gated 28.6 / 22.2; backward 2.1 M 12.4 / 15.1, 5.2 M 22.2 / 18.6, gated 31.5 / 19.7:
+// launches of many small blocks do better (device times in bf16, one launch against three: forward 2.1 M elements 8.2 / 12.0 us,
+// 8.4 M 15.9 / 18.7, 10.5 M 19.9 / 20.7 and gated 28.6 / 22.2; backward 2.1 M 12.4 / 15.1, 5.2 M 22.2 / 18.6, gated 31.5 / 19.7:
 // a CTA that holds its part of a group loads it, sums it and stores it one after another, with few of its kind beside it).
 struct FusedShape {
     int vec, size, smem;
